@@ -31,6 +31,7 @@ FSDP_LAYOUT_DIM0 = 1
 FSDP_LAYOUT_FLAT_PADDED = 2
 FSDP_DTYPE_F32 = 0
 FSDP_DTYPE_BF16 = 1
+FSDP_DTYPE_ACT8 = 2
 FSDP_GATHER_FROM_MASTER = 0
 FSDP_GATHER_FROM_SHADOW = 1
 
@@ -52,6 +53,13 @@ FSDP_KSTATUS_DRAIN_TIMEOUT = 2
 
 FSDP_NOALLOC_MAX_TILES = 32768
 
+FSDP_ACTIVATION_NONE = 0
+FSDP_ACTIVATION_RELU = 1
+FSDP_ACTIVATION_GELU_TANH = 2
+FSDP_ACTIVATION_GELU_ERF = 3
+FSDP_WEIGHT_IN_OUT = 0
+FSDP_WEIGHT_OUT_IN = 1
+
 LAYOUTS = {"flat": FSDP_LAYOUT_FLAT, "dim0": FSDP_LAYOUT_DIM0, "flat_padded": FSDP_LAYOUT_FLAT_PADDED}
 GRAD_DTYPES = {"f32": FSDP_DTYPE_F32, "bf16": FSDP_DTYPE_BF16}
 GATHER_SOURCES = {"master": FSDP_GATHER_FROM_MASTER, "shadow": FSDP_GATHER_FROM_SHADOW}
@@ -60,6 +68,9 @@ STATES = {"param": FSDP_STATE_PARAM, "grad": FSDP_STATE_GRAD, "exp_avg": FSDP_ST
 KERNELS = {"shard_in": FSDP_KERNEL_SHARD_IN, "gather": FSDP_KERNEL_GATHER,
            "reduce_scatter": FSDP_KERNEL_REDUCE_SCATTER, "adamw": FSDP_KERNEL_ADAMW,
            "reduce_adamw": FSDP_KERNEL_REDUCE_ADAMW}
+ACTIVATIONS = {"none": FSDP_ACTIVATION_NONE, "relu": FSDP_ACTIVATION_RELU,
+               "gelu_tanh": FSDP_ACTIVATION_GELU_TANH, "gelu_erf": FSDP_ACTIVATION_GELU_ERF}
+WEIGHT_LAYOUTS = {"in_out": FSDP_WEIGHT_IN_OUT, "out_in": FSDP_WEIGHT_OUT_IN}
 
 
 class Segment(ctypes.Structure):
@@ -93,6 +104,12 @@ class Allocator(ctypes.Structure):
     _fields_ = [("alloc", _ALLOC_FN), ("free", _FREE_FN), ("ctx", ctypes.c_void_p)]
 
 
+class Matrix(ctypes.Structure):
+    """fsdp_matrix: a view of a device matrix."""
+    _fields_ = [("data", ctypes.c_void_p), ("exps", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("ld", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
 class FsdpError(RuntimeError):
     def __init__(self, code: int, where: str, detail: str):
         super().__init__(f"{where}: {detail} (code {code})")
@@ -104,6 +121,8 @@ _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _PI64 = ctypes.POINTER(ctypes.c_int64)
 _PI = ctypes.POINTER(ctypes.c_int)
+_D = ctypes.c_double
+_PM = ctypes.POINTER(Matrix)
 
 _SIGNATURES = {
     "fsdp_plan_layout": (_I, [_I, _PI, _PI64, _I, _I, _PI64, _PI64, ctypes.POINTER(Segment), _I64]),
@@ -138,6 +157,20 @@ _SIGNATURES = {
     "fsdp_unit_set_wait_limit": (_I, [_P, ctypes.c_double, _I]),
     "fsdp_selftest_bounded_wait": (_I, [ctypes.c_double, ctypes.POINTER(ctypes.c_int32), _P]),
     "fsdp_host_device_pointer": (_I, [_P, ctypes.POINTER(_P)]),
+    "fsdp_compute_create": (_I, [_I64, ctypes.POINTER(Allocator), ctypes.POINTER(_P)]),
+    "fsdp_compute_destroy": (_I, [_P]),
+    "fsdp_compute_status": (_I, [_P, ctypes.POINTER(ctypes.c_int32), _P]),
+    "fsdp_compute_set_wait_limit": (_I, [_P, _D, _I]),
+    "fsdp_layer_norm_workspace_bytes": (_I, [_I64, _I64, _PI64]),
+    "fsdp_linear_workspace_bytes": (_I, [_I64, _I64, _I64, _I, _PI64]),
+    "fsdp_layer_norm_forward": (_I, [_P, _PM, _P, _P, _I, _D, _PM, _P, _P, _PM, _P]),
+    "fsdp_layer_norm_backward": (_I, [_P, _PM, _PM, _P, _I, _P, _P, _PM, _PM, _P, _P, _I, _I, _P]),
+    "fsdp_linear_forward": (_I, [_P, _PM, _PM, _I, _P, _I, _I, _PM, _PM, _PM, _P]),
+    "fsdp_linear_grad_input": (_I, [_P, _PM, _PM, _I, _I, _PM, _PM, _PM, _P]),
+    "fsdp_linear_grad_weight": (_I, [_P, _PM, _PM, _I, _PM, _P, _I, _P]),
+    "fsdp_act8_layout": (_I, [_I64, _I64, _PI64, _PI64]),
+    "fsdp_act8_pack": (_I, [_P, _PM, _PM, _P]),
+    "fsdp_act8_unpack": (_I, [_P, _PM, _I, _PM, _P]),
     "fsdp_strerror": (ctypes.c_char_p, [_I]),
     "fsdp_last_error": (ctypes.c_char_p, []),
 }
@@ -507,6 +540,211 @@ def fsdp_strerror(code: int) -> str:
 
 def fsdp_last_error() -> str:
     return lib().fsdp_last_error().decode()
+
+
+# ---- block operators -------------------------------------------------------
+
+_TORCH_DTYPES = {torch.float32: FSDP_DTYPE_F32, torch.bfloat16: FSDP_DTYPE_BF16}
+
+
+def fsdp_act8_layout(rows, cols):
+    """(row stride of the int8 payload, row stride of the exponents), in bytes."""
+    a, b = ctypes.c_int64(), ctypes.c_int64()
+    _check(lib().fsdp_act8_layout(int(rows), int(cols), ctypes.byref(a), ctypes.byref(b)), "fsdp_act8_layout")
+    return a.value, b.value
+
+
+class Act8:
+    """An 8-bit activation checkpoint of a rows x cols matrix: the int8 payload
+    ``q`` [rows, 32*ceil(cols/32)] and the exponent bytes ``exps``
+    [rows, ceil(cols/32)], allocated here unless given."""
+
+    def __init__(self, rows, cols, q=None, exps=None, device="cuda"):
+        self.rows, self.cols = int(rows), int(cols)
+        ld, eld = fsdp_act8_layout(self.rows, self.cols)
+        self.q = torch.empty((self.rows, ld), dtype=torch.int8, device=device) if q is None else q
+        self.exps = torch.empty((self.rows, eld), dtype=torch.uint8, device=device) if exps is None else exps
+        assert self.q.dtype == torch.int8 and tuple(self.q.shape) == (self.rows, ld) and self.q.is_contiguous()
+        assert self.exps.dtype == torch.uint8 and tuple(self.exps.shape) == (self.rows, eld) and self.exps.is_contiguous()
+        assert self.q.is_cuda and self.exps.is_cuda
+        self.matrix = Matrix(self.q.data_ptr(), self.exps.data_ptr(), self.rows, self.cols, ld, FSDP_DTYPE_ACT8)
+
+    @property
+    def nbytes(self) -> int:
+        return self.q.numel() + self.exps.numel()
+
+
+def _mat(t):
+    """fsdp_matrix of a 2-D CUDA tensor whose rows are contiguous, or of an Act8."""
+    if t is None:
+        return None
+    if isinstance(t, Act8):
+        return t.matrix
+    assert t.is_cuda and t.dim() == 2, "a matrix is a 2-D CUDA tensor"
+    rows, cols = t.shape
+    ld = t.stride(0) if rows > 1 else cols
+    assert cols <= 1 or t.stride(1) == 1, "a matrix's rows must be contiguous"
+    return Matrix(t.data_ptr(), None, rows, cols, ld, _TORCH_DTYPES[t.dtype])
+
+
+def _vec(t, n):
+    """(address, dtype) of a contiguous CUDA vector of n elements."""
+    assert t.is_cuda and t.is_contiguous() and t.numel() == n, f"a vector of {n} elements is expected"
+    return t.data_ptr(), _TORCH_DTYPES[t.dtype]
+
+
+def _stat(t, n):
+    assert t.is_cuda and t.is_contiguous() and t.numel() == n and t.dtype == torch.float32
+    return t.data_ptr()
+
+
+def fsdp_compute_create(workspace_bytes=0, allocator=None):
+    h = _P()
+    a = ctypes.byref(allocator) if allocator is not None else None
+    _check(lib().fsdp_compute_create(int(workspace_bytes), a, ctypes.byref(h)), "fsdp_compute_create")
+    return h
+
+
+def fsdp_compute_destroy(h) -> None:
+    _check(lib().fsdp_compute_destroy(h), "fsdp_compute_destroy")
+
+
+def fsdp_compute_status(h, stream=None) -> int:
+    """FSDP_KSTATUS_* bits raised since the last call (0: none); clears them."""
+    f = ctypes.c_int32()
+    _check(lib().fsdp_compute_status(h, ctypes.byref(f), _stream(stream)), "fsdp_compute_status")
+    return f.value
+
+
+def fsdp_compute_set_wait_limit(h, seconds=10.0, withhold_next=0) -> None:
+    _check(lib().fsdp_compute_set_wait_limit(h, float(seconds), int(withhold_next)), "fsdp_compute_set_wait_limit")
+
+
+def fsdp_layer_norm_workspace_bytes(rows, cols) -> int:
+    n = ctypes.c_int64()
+    _check(lib().fsdp_layer_norm_workspace_bytes(int(rows), int(cols), ctypes.byref(n)),
+           "fsdp_layer_norm_workspace_bytes")
+    return n.value
+
+
+def fsdp_linear_workspace_bytes(tokens, in_features, out_features, weight_aligned=None) -> int:
+    """``weight_aligned``: whether the weight's rows start on 16-byte
+    boundaries; None: true when both widths are multiples of 8 elements."""
+    if weight_aligned is None:
+        weight_aligned = in_features % 8 == 0 and out_features % 8 == 0
+    n = ctypes.c_int64()
+    _check(lib().fsdp_linear_workspace_bytes(int(tokens), int(in_features), int(out_features),
+                                             1 if weight_aligned else 0, ctypes.byref(n)),
+           "fsdp_linear_workspace_bytes")
+    return n.value
+
+
+def fsdp_layer_norm_forward(h, x, gamma, beta, eps, y, mean, rstd, ckpt=None, stream=None) -> None:
+    rows, cols = x.shape
+    g, dt = _vec(gamma, cols)
+    b, bt = _vec(beta, cols)
+    assert dt == bt, "gamma and beta have one dtype"
+    _check(lib().fsdp_layer_norm_forward(h, _mat(x), g, b, dt, float(eps), _mat(y), _stat(mean, rows),
+                                         _stat(rstd, rows), _mat(ckpt), _stream(stream)), "fsdp_layer_norm_forward")
+
+
+def fsdp_layer_norm_backward(h, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, add=None, accumulate=False,
+                             stream=None) -> None:
+    """``x``: the forward's input or its ``Act8`` checkpoint."""
+    rows, cols = dy.shape
+    g, dt = _vec(gamma, cols)
+    dg, gt = _vec(dgamma, cols)
+    db, bt = _vec(dbeta, cols)
+    assert gt == bt, "dgamma and dbeta have one dtype"
+    _check(lib().fsdp_layer_norm_backward(h, _mat(dy), _mat(x), g, dt, _stat(mean, rows), _stat(rstd, rows),
+                                          _mat(add), _mat(dx), dg, db, gt, 1 if accumulate else 0,
+                                          _stream(stream)), "fsdp_layer_norm_backward")
+
+
+def fsdp_linear_forward(h, x, w, y, bias=None, activation="none", residual=None, preact=None,
+                        weight_layout="in_out", stream=None) -> None:
+    """``preact``: None, or the tensor or ``Act8`` that receives x W + bias."""
+    b, bt = _vec(bias, y.shape[1]) if bias is not None else (None, FSDP_DTYPE_F32)
+    _check(lib().fsdp_linear_forward(h, _mat(x), _mat(w), WEIGHT_LAYOUTS.get(weight_layout, weight_layout), b, bt,
+                                     ACTIVATIONS.get(activation, activation), _mat(residual), _mat(preact), _mat(y),
+                                     _stream(stream)), "fsdp_linear_forward")
+
+
+def fsdp_linear_grad_input(h, dy, w, dx, activation="none", preact=None, add=None, weight_layout="in_out",
+                           stream=None) -> None:
+    _check(lib().fsdp_linear_grad_input(h, _mat(dy), _mat(w), WEIGHT_LAYOUTS.get(weight_layout, weight_layout),
+                                        ACTIVATIONS.get(activation, activation), _mat(preact), _mat(add), _mat(dx),
+                                        _stream(stream)), "fsdp_linear_grad_input")
+
+
+def fsdp_linear_grad_weight(h, x, dy, dw, dbias=None, weight_layout="in_out", accumulate=False, stream=None) -> None:
+    """``x``: the layer's input or its ``Act8`` checkpoint; ``dw`` is stored like the weight."""
+    db, bt = _vec(dbias, dy.shape[1]) if dbias is not None else (None, _TORCH_DTYPES[dw.dtype])
+    assert bt == _TORCH_DTYPES[dw.dtype], "dw and dbias have one dtype"
+    _check(lib().fsdp_linear_grad_weight(h, _mat(x), _mat(dy), WEIGHT_LAYOUTS.get(weight_layout, weight_layout),
+                                         _mat(dw), db, 1 if accumulate else 0, _stream(stream)),
+           "fsdp_linear_grad_weight")
+
+
+def fsdp_act8_pack(h, x, ckpt, stream=None) -> None:
+    _check(lib().fsdp_act8_pack(h, _mat(x), _mat(ckpt), _stream(stream)), "fsdp_act8_pack")
+
+
+def fsdp_act8_unpack(h, ckpt, out, activation="none", stream=None) -> None:
+    _check(lib().fsdp_act8_unpack(h, _mat(ckpt), ACTIVATIONS.get(activation, activation), _mat(out),
+                                  _stream(stream)), "fsdp_act8_unpack")
+
+
+class Compute:
+    """Owns one ``fsdp_compute`` handle; methods call the C entry points."""
+
+    def __init__(self, workspace_bytes=0, allocator=None):
+        """`allocator`: as for ``Unit``."""
+        self.handle = None
+        self.allocator = allocator
+        self.workspace_bytes = int(workspace_bytes)
+        self.handle = fsdp_compute_create(workspace_bytes, allocator.struct if allocator is not None else None)
+
+    def close(self):
+        if self.handle is not None:
+            fsdp_compute_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def status(self, stream=None) -> int:
+        return fsdp_compute_status(self.handle, stream)
+
+    def set_wait_limit(self, seconds=10.0, withhold_next=0) -> None:
+        fsdp_compute_set_wait_limit(self.handle, seconds, withhold_next)
+
+    def layer_norm_forward(self, x, gamma, beta, eps, y, mean, rstd, ckpt=None, stream=None):
+        fsdp_layer_norm_forward(self.handle, x, gamma, beta, eps, y, mean, rstd, ckpt, stream)
+
+    def layer_norm_backward(self, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, add=None, accumulate=False,
+                            stream=None):
+        fsdp_layer_norm_backward(self.handle, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, add, accumulate, stream)
+
+    def linear_forward(self, x, w, y, bias=None, activation="none", residual=None, preact=None,
+                       weight_layout="in_out", stream=None):
+        fsdp_linear_forward(self.handle, x, w, y, bias, activation, residual, preact, weight_layout, stream)
+
+    def linear_grad_input(self, dy, w, dx, activation="none", preact=None, add=None, weight_layout="in_out",
+                          stream=None):
+        fsdp_linear_grad_input(self.handle, dy, w, dx, activation, preact, add, weight_layout, stream)
+
+    def linear_grad_weight(self, x, dy, dw, dbias=None, weight_layout="in_out", accumulate=False, stream=None):
+        fsdp_linear_grad_weight(self.handle, x, dy, dw, dbias, weight_layout, accumulate, stream)
+
+    def act8_pack(self, x, ckpt, stream=None):
+        fsdp_act8_pack(self.handle, x, ckpt, stream)
+
+    def act8_unpack(self, ckpt, out, activation="none", stream=None):
+        fsdp_act8_unpack(self.handle, ckpt, out, activation, stream)
 
 
 # ---- a small owning wrapper ----------------------------------------------

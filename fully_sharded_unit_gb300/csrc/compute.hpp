@@ -1,0 +1,87 @@
+// Launchers of the block operators (layer norm, linear layer, 8-bit activation
+// checkpoints).  Every launcher enqueues on `st` only and returns the launch
+// status; arguments are checked by the C entry points in compute.cu.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace fsdp {
+
+// A matrix as the kernels see it: element (r, c) at p + (r*ld + c) elements.
+// ACT8: p is the int8 payload, e the exponent bytes, eld their row stride.
+struct Mat {
+    void* p;
+    uint8_t* e;
+    int64_t ld;
+    int64_t eld;
+    int dtype;   // FSDP_DTYPE_*
+};
+
+constexpr int kGroup = 32;   // elements that share an exponent in an ACT8 matrix
+
+inline int64_t act8_groups(int64_t cols) { return (cols + kGroup - 1) / kGroup; }
+
+// Rows of m start on 16-byte boundaries (vector accesses of 8 elements).
+inline bool rows_aligned(const Mat& m) {
+    const int64_t esz = m.dtype == 0 ? 4 : m.dtype == 1 ? 2 : 1;
+    return (reinterpret_cast<uintptr_t>(m.p) & 15u) == 0 && (m.ld * esz) % 16 == 0;
+}
+
+// ---- layer norm (norm.cu) ----
+struct NormForward {
+    int64_t rows, cols;
+    Mat x, y, ckpt;             // ckpt.p null: none
+    const void *gamma, *beta;
+    int param_dtype;
+    float eps;
+    float *mean, *rstd;
+};
+cudaError_t launch_norm_forward(const NormForward& a, int sms, cudaStream_t st);
+
+struct NormBackward {
+    int64_t rows, cols;
+    Mat dy, x, add, dx;         // add.p null: none
+    const void* gamma;
+    int param_dtype;
+    const float *mean, *rstd;
+    void *dgamma, *dbeta;
+    int grad_dtype, accumulate;
+    float* partials;            // workspace: norm_partials() x 2 x cols floats
+};
+int64_t norm_partials(int64_t rows, int64_t cols, int sms);
+cudaError_t launch_norm_backward(const NormBackward& a, int sms, cudaStream_t st);
+
+// out[c] (+)= sum over p of partials[p*stride + c], in the order of p.
+cudaError_t launch_sum_partials(const float* partials, int64_t count, int64_t stride, int64_t cols, void* out,
+                                int out_dtype, int accumulate, cudaStream_t st);
+
+// ---- 8-bit checkpoints (act8.cu) ----
+cudaError_t launch_act8_pack(int64_t rows, int64_t cols, const Mat& x, const Mat& q, int sms, cudaStream_t st);
+cudaError_t launch_act8_unpack(int64_t rows, int64_t cols, const Mat& q, int activation, const Mat& out, int sms,
+                               cudaStream_t st);
+
+// ---- linear layer (linear.cu) ----
+// C[m, n] = sum_k A(m, k) B(n, k) followed by, per element,
+//   v = c + bias[n];  forward (slope == 0): store v to pre, v = act(v)
+//                     slope == 1: v = c * act'(pre[m, n])
+//   v += add[m, n];  store v to out.
+struct Product {
+    int64_t M, N, K;
+    Mat a, b;                   // a: M x K (a_trans 0) or K x M (a_trans 1); b: N x K or K x N
+    int a_trans, b_trans;
+    const void* bias;
+    int bias_dtype;
+    int act, slope;
+    Mat pre, add, out;          // p null: none
+};
+cudaError_t launch_product(const Product& p, int sms, cudaStream_t st);
+
+// Column sums of dy (rows x cols, bf16) over its rows, through `partials`
+// (column_sum_partials() x cols floats).
+int64_t column_sum_partials(int64_t rows, int64_t cols, int sms);
+cudaError_t launch_column_sum(int64_t rows, int64_t cols, const Mat& dy, float* partials, void* out, int out_dtype,
+                              int accumulate, int sms, cudaStream_t st);
+
+}  // namespace fsdp

@@ -493,6 +493,163 @@ FSDP_API int fsdp_profile_reset(fsdp_unit* unit);
  * FSDP_E_INVALID_ARG if `host` is not pinned, mapped host memory. */
 FSDP_API int fsdp_host_device_pointer(const void* host, void** dev);
 
+/* ---- block operators --------------------------------------------------------- */
+/* What a unit computes between its gather and its reduce-scatter, for units
+ * that are transformer blocks: layer norm and linear layers on the gathered
+ * bf16 parameters, activation checkpoints in 8 bits, and the gradients of all
+ * of them, written where the reduce-scatter reads them.  (The pages shard such
+ * blocks and leave their arithmetic to the host framework; [FSDP] section 5
+ * trains with activation checkpointing.)
+ *
+ * Sums, statistics and products are held in fp32; every result is
+ * rounded once (to nearest even) to the type of its output.  Results do not
+ * depend on the stream, the device's load or earlier calls. */
+
+/* An 8-bit activation checkpoint: fsdp_matrix.dtype of matrices whose `data`
+ * holds int8 elements and whose `exps` holds one byte for each group of 32
+ * consecutive elements of a row (the last group of a row may be short).  With
+ * a = the group's largest magnitude:
+ *     E = floor(log2 a) clamped to [-120, 127] (-120 for a = 0); byte E + 127
+ *     q = x * 2^(6-E) rounded to nearest even, clamped to [-127, 127]
+ *     the element stands for q * 2^(E-6), which is a bf16 number exactly.
+ * A group that holds an infinity or a NaN gets byte 255 and stands for NaN in
+ * every place.  Rows of `data` are ld = 32*ceil(cols/32) bytes apart (the pad
+ * bytes are written as 0), rows of `exps` ceil(cols/32) bytes; `data` must be
+ * 16-byte aligned. */
+#define FSDP_DTYPE_ACT8 2
+
+/* activations of fsdp_linear_forward / _grad_input and fsdp_act8_unpack */
+#define FSDP_ACTIVATION_NONE      0
+#define FSDP_ACTIVATION_RELU      1   /* max(z, 0); slope 0 at z = 0; NaN stays NaN      */
+#define FSDP_ACTIVATION_GELU_TANH 2   /* z/2 * (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+#define FSDP_ACTIVATION_GELU_ERF  3   /* z/2 * (1 + erf(z / sqrt(2)))                    */
+
+/* how a weight matrix W (in_features x out_features in y = x W) is stored */
+#define FSDP_WEIGHT_IN_OUT 0   /* rows = in_features, cols = out_features (the GPT blocks)  */
+#define FSDP_WEIGHT_OUT_IN 1   /* rows = out_features, cols = in_features                   */
+
+/* A view of a caller's device matrix: element (r, c) is data[r*ld + c]; ld >= cols.
+ * `data` needs the alignment of its element type only; rows that start on
+ * 16-byte boundaries (data and ld) run fastest.  `exps` is used by
+ * FSDP_DTYPE_ACT8 alone. */
+typedef struct {
+    void* data;
+    uint8_t* exps;
+    int64_t rows, cols, ld;
+    int dtype;             /* FSDP_DTYPE_F32, _BF16 or _ACT8 */
+} fsdp_matrix;
+
+/* A compute handle: the device it was created on, a workspace of a fixed size
+ * and a kernel status word.  Calls allocate nothing and enqueue on `stream`
+ * only, so they can be captured into a CUDA graph.  Calls of one handle share
+ * its workspace: they must be ordered on the GPU (one stream, or streams
+ * ordered by events), and the handle is not thread-safe; distinct handles are
+ * independent.  A graph captured from a handle's calls uses its workspace at
+ * every replay. */
+typedef struct fsdp_compute fsdp_compute;
+
+/* Create a handle on the current device with `workspace_bytes` (>= 0) of
+ * workspace, from `alloc` (NULL: cudaMalloc; same rules as
+ * fsdp_unit_create_with_allocator).  Synchronous. */
+FSDP_API int fsdp_compute_create(int64_t workspace_bytes, const fsdp_allocator* alloc, fsdp_compute** out);
+
+/* Free what the handle owns.  Synchronises its device first.  NULL is accepted. */
+FSDP_API int fsdp_compute_destroy(fsdp_compute* c);
+
+/* The workspace that any call of the named operators needs at these sizes, in
+ * any type, layout and option, and with fewer rows or tokens.  weight_aligned:
+ * nonzero if W's rows start on 16-byte boundaries (data and ld); otherwise room
+ * for an aligned copy of W is counted.  Host only.  A call that needs more than
+ * its handle has returns FSDP_E_CAPACITY with the bytes in fsdp_last_error()
+ * and enqueues nothing. */
+FSDP_API int fsdp_layer_norm_workspace_bytes(int64_t rows, int64_t cols, int64_t* bytes);
+FSDP_API int fsdp_linear_workspace_bytes(int64_t tokens, int64_t in_features, int64_t out_features,
+                                         int weight_aligned, int64_t* bytes);
+
+/* Like fsdp_kernel_status, for the handle's kernels (the linear layer's
+ * products wait, with a bound, on their own copies and matrix instructions):
+ * synchronises `stream`, stores the FSDP_KSTATUS_* bits raised since the last
+ * call in *flags and clears them.  After a raised bit the outputs of the calls
+ * enqueued since the last read are incomplete; after
+ * FSDP_KSTATUS_DRAIN_TIMEOUT every later call but destroy returns
+ * FSDP_E_STATE. */
+FSDP_API int fsdp_compute_status(fsdp_compute* c, int32_t* flags, void* stream);
+
+/* Like fsdp_unit_set_wait_limit, for the handle: the bound of every wait, in
+ * seconds ([1e-6, 60]; 10 s until set).  withhold_next != 0 arms a one-shot
+ * test of the give-up path: in the handle's next matrix product that runs on
+ * staged tiles, the first block arms the barrier of its first stage but issues
+ * none of that stage's copies, so that the waits behind it run out and
+ * FSDP_KSTATUS_WAIT_TIMEOUT is raised; the launch reads and writes less than a
+ * normal one. */
+FSDP_API int fsdp_compute_set_wait_limit(fsdp_compute* c, double seconds, int withhold_next);
+
+/* Layer norm over each row of x (rows x cols, BF16 or F32; cols >= 1, rows >= 0):
+ *     mean = sum(x) / cols;  rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps)
+ *     y = (x - mean) * rstd * gamma + beta
+ * gamma, beta: cols elements of param_dtype (BF16, as gathered, or F32).
+ * y: BF16 or F32.  mean, rstd: `rows` floats each, for the backward pass.
+ * ckpt (optional): an ACT8 matrix of x's shape that receives x. */
+FSDP_API int fsdp_layer_norm_forward(fsdp_compute* c, const fsdp_matrix* x, const void* gamma, const void* beta,
+                                     int param_dtype, double eps, const fsdp_matrix* y, float* mean, float* rstd,
+                                     const fsdp_matrix* ckpt, void* stream);
+
+/* Its gradients.  x: the forward's input (BF16 or F32) or its ACT8 checkpoint;
+ * mean, rstd as the forward wrote them.  With xh = (x - mean) * rstd and
+ * g = dy * gamma:
+ *     dx = rstd * (g - mean_row(g) - xh * mean_row(g * xh)) [+ add]
+ *     dgamma = sum over rows of dy * xh;  dbeta = sum over rows of dy
+ * add (optional, BF16 or F32): another branch's gradient; may be dx itself.
+ * dgamma, dbeta: cols elements of grad_dtype, aligned to their element only
+ * (pieces of a rank's flat gradient); overwritten, or added to when
+ * `accumulate` is set.  The sums over rows have a fixed order.  rows = 0 gives
+ * zero (or unchanged) dgamma and dbeta. */
+FSDP_API int fsdp_layer_norm_backward(fsdp_compute* c, const fsdp_matrix* dy, const fsdp_matrix* x, const void* gamma,
+                                      int param_dtype, const float* mean, const float* rstd, const fsdp_matrix* add,
+                                      const fsdp_matrix* dx, void* dgamma, void* dbeta, int grad_dtype,
+                                      int accumulate, void* stream);
+
+/* A linear layer with its epilogue: z = x W + bias; y = activation(z) + residual.
+ * x: tokens x in_features, BF16.  W: BF16, stored per weight_layout.  bias
+ * (optional): out_features elements of bias_dtype (BF16 or F32).  residual
+ * (optional): tokens x out_features, BF16 or F32; may be y itself.  preact
+ * (optional): receives z, as BF16, F32 or ACT8.  y: BF16 or F32. */
+FSDP_API int fsdp_linear_forward(fsdp_compute* c, const fsdp_matrix* x, const fsdp_matrix* w, int weight_layout,
+                                 const void* bias, int bias_dtype, int activation, const fsdp_matrix* residual,
+                                 const fsdp_matrix* preact, const fsdp_matrix* y, void* stream);
+
+/* The input's gradient: dx = (dy W^T) * slope(preact) [+ add], where slope is
+ * the derivative of `activation` (FSDP_ACTIVATION_NONE: 1, preact unused) at
+ * the values that the layer below kept: with y1 = x W1, h = act(y1),
+ * y2 = h W2, one call on W2 with preact = y1 gives y1's gradient.
+ * dy: tokens x out_features, BF16.  preact: tokens x in_features, BF16, F32 or
+ * ACT8.  add (optional, BF16 or F32): another branch's gradient; may be dx
+ * itself.  dx: BF16 or F32. */
+FSDP_API int fsdp_linear_grad_input(fsdp_compute* c, const fsdp_matrix* dy, const fsdp_matrix* w, int weight_layout,
+                                    int activation, const fsdp_matrix* preact, const fsdp_matrix* add,
+                                    const fsdp_matrix* dx, void* stream);
+
+/* The weight's and the bias's gradients: dW = x^T dy, dbias = sum over tokens
+ * of dy.  x: BF16, or the ACT8 checkpoint of the layer's input.  dw: stored
+ * like W, F32 or BF16, aligned to its element only (a piece of a rank's flat
+ * gradient).  dbias (optional): out_features elements of dw's type.  Both are
+ * overwritten, or added to when `accumulate` is set; tokens = 0 gives zero
+ * (or unchanged) gradients. */
+FSDP_API int fsdp_linear_grad_weight(fsdp_compute* c, const fsdp_matrix* x, const fsdp_matrix* dy, int weight_layout,
+                                     const fsdp_matrix* dw, void* dbias, int accumulate, void* stream);
+
+/* The sizes of an ACT8 checkpoint of rows x cols: the row stride of `data` in
+ * bytes, the row stride of `exps` in bytes (rows times either is the size). */
+FSDP_API int fsdp_act8_layout(int64_t rows, int64_t cols, int64_t* data_ld, int64_t* exps_ld);
+
+/* Put x (BF16 or F32) into an ACT8 checkpoint of its shape, and read one back
+ * as activation(value) in BF16 or F32 (FSDP_ACTIVATION_NONE: the values
+ * themselves; with the forward's activation: that layer's output, recomputed
+ * from its kept pre-activation). */
+FSDP_API int fsdp_act8_pack(fsdp_compute* c, const fsdp_matrix* x, const fsdp_matrix* ckpt, void* stream);
+FSDP_API int fsdp_act8_unpack(fsdp_compute* c, const fsdp_matrix* ckpt, int activation, const fsdp_matrix* out,
+                              void* stream);
+
 /* ---- errors -------------------------------------------------------------- */
 /* Library infrastructure (the pages have no counterpart). */
 FSDP_API const char* fsdp_strerror(int code);
