@@ -17,18 +17,21 @@ namespace fsdp {
 int record_error(int code, const std::string& why);
 }  // namespace fsdp
 
+constexpr int64_t kHeader = 256 + (fsdp::kCounterBytes + 255) / 256 * 256;
+
 struct fsdp_compute {
     int device = 0;
     int sms = 0;
     fsdp_allocator allocator{nullptr, nullptr, nullptr};   // alloc == nullptr: cudaMalloc / cudaFree
-    char* block = nullptr;        // status word (256 bytes), then the workspace
+    char* block = nullptr;        // status word, counters of shared tiles, then the workspace
     int64_t workspace_bytes = 0;
     unsigned long long wait_ns = 10000000000ull;
     int withhold_next = 0;
     bool broken = false;          // a drain wait ran out: only destroy is accepted
 
     int32_t* status() const { return reinterpret_cast<int32_t*>(block); }
-    char* workspace() const { return block + 256; }
+    uint32_t* counters() const { return reinterpret_cast<uint32_t*>(block + 256); }
+    char* workspace() const { return block + kHeader; }
 };
 
 namespace {
@@ -157,6 +160,45 @@ int64_t norm_bytes(int64_t rows, int64_t cols) { return std::min<int64_t>(rows, 
 // column_sum_partials() * cols floats is no more than this.
 int64_t column_sum_bytes(int64_t cols) { return (int64_t(4) * kSms * 256 + cols + 256) * 4; }
 
+// Workspace of a weight gradient or a product: sums of shared tiles, column
+// sums, aligned copies of operands.
+int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
+
+int64_t copies_offset(int64_t out_features) { return fsdp::kPartialBytes + round256(column_sum_bytes(out_features)); }
+
+int64_t copy_bytes(int64_t rows, int64_t cols) { return round256(rows * ((cols + 7) / 8 * 8) * 2); }
+
+constexpr int64_t kMaxSide = (int64_t(1) << 31) - 512;   // tile coordinates are 32-bit
+
+int check_linear(int64_t T, int64_t I, int64_t O, int weight_layout) {
+    if (T < 0 || I < 1 || O < 1 || T > kMaxSide || I > kMaxSide || O > kMaxSide)
+        return fail(FSDP_E_INVALID_ARG, "linear: tokens must be >= 0 and features >= 1 (each below 2^31 - 512)");
+    if (weight_layout != FSDP_WEIGHT_IN_OUT && weight_layout != FSDP_WEIGHT_OUT_IN)
+        return fail(FSDP_E_INVALID_ARG, "unknown weight_layout");
+    return FSDP_OK;
+}
+
+// Checks the workspace for a product and takes its room from it.
+int take_room(fsdp_compute* c, const fsdp::Product& p, int64_t out_features, fsdp::ProductRoom* r) {
+    const int64_t copies = static_cast<int64_t>(
+        fsdp::product_copy_bytes(p.a, p.a_trans ? p.K : p.M, p.a_trans ? p.M : p.K) +
+        fsdp::product_copy_bytes(p.b, p.b_trans ? p.K : p.N, p.b_trans ? p.N : p.K));
+    TRY(check_workspace(c, copies_offset(out_features) + copies));
+    r->partials = reinterpret_cast<float*>(c->workspace());
+    r->counters = c->counters();
+    r->copies = c->workspace() + copies_offset(out_features);
+    r->status = c->status();
+    r->wait_ns = c->wait_ns;
+    r->withhold = c->withhold_next;
+    return FSDP_OK;
+}
+
+int run_product(fsdp_compute* c, const fsdp::Product& p, const fsdp::ProductRoom& r, cudaStream_t st, const char* what) {
+    if (p.M > 0 && p.K > 0) c->withhold_next = 0;
+    const cudaError_t e = fsdp::launch_product(p, r, c->sms, st);
+    return e == cudaSuccess ? FSDP_OK : cuda_fail(e, what);
+}
+
 }  // namespace
 
 extern "C" {
@@ -177,7 +219,7 @@ int fsdp_compute_create(int64_t workspace_bytes, const fsdp_allocator* alloc, fs
         c->device = device;
         c->sms = std::min(sms, kSms);
         c->workspace_bytes = workspace_bytes;
-        const size_t bytes = 256 + static_cast<size_t>(workspace_bytes);
+        const size_t bytes = kHeader + static_cast<size_t>(workspace_bytes);
         if (alloc != nullptr) {
             c->allocator = *alloc;
             void* p = alloc->alloc(bytes, alloc->ctx);
@@ -202,7 +244,7 @@ int fsdp_compute_create(int64_t workspace_bytes, const fsdp_allocator* alloc, fs
             }
             c->block = static_cast<char*>(p);
         }
-        e = cudaMemset(c->block, 0, 256);
+        e = cudaMemset(c->block, 0, kHeader);
         if (e == cudaSuccess) e = cudaDeviceSynchronize();
         if (e != cudaSuccess) {
             fsdp_compute_destroy(c);
@@ -241,6 +283,11 @@ int fsdp_compute_status(fsdp_compute* c, int32_t* flags, void* stream) {
         if (e != cudaSuccess) return cuda_fail(e, "reading the status word");
         *flags = v;
         if (v & FSDP_KSTATUS_DRAIN_TIMEOUT) c->broken = true;
+        if (v != 0) {   // a product that gave up leaves its counters as they were
+            e = cudaMemsetAsync(c->counters(), 0, fsdp::kCounterBytes, st);
+            if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+            if (e != cudaSuccess) return cuda_fail(e, "clearing the counters");
+        }
         return FSDP_OK;
     });
 }
@@ -269,10 +316,11 @@ int fsdp_linear_workspace_bytes(int64_t tokens, int64_t in_features, int64_t out
                                 int64_t* bytes) {
     return entry([&]() -> int {
         if (bytes == nullptr) return fail(FSDP_E_INVALID_ARG, "bytes is null");
-        TRY(check_shape(tokens, in_features, "linear"));
-        TRY(check_shape(tokens, out_features, "linear"));
-        (void)weight_aligned;
-        *bytes = column_sum_bytes(out_features);
+        TRY(check_linear(tokens, in_features, out_features, FSDP_WEIGHT_IN_OUT));
+        int64_t copies = copy_bytes(tokens, in_features) + copy_bytes(tokens, out_features);
+        if (!weight_aligned)
+            copies += std::max(copy_bytes(in_features, out_features), copy_bytes(out_features, in_features));
+        *bytes = copies_offset(std::max(in_features, out_features)) + copies;
         return FSDP_OK;
     });
 }
@@ -365,10 +413,7 @@ int fsdp_linear_forward(fsdp_compute* c, const fsdp_matrix* x, const fsdp_matrix
         TRY(check_handle(c));
         if (x == nullptr || y == nullptr) return fail(FSDP_E_INVALID_ARG, x == nullptr ? "x is null" : "y is null");
         const int64_t T = x->rows, I = x->cols, O = y->cols;
-        TRY(check_shape(T, I, "linear"));
-        TRY(check_shape(T, O, "linear"));
-        if (weight_layout != FSDP_WEIGHT_IN_OUT && weight_layout != FSDP_WEIGHT_OUT_IN)
-            return fail(FSDP_E_INVALID_ARG, "unknown weight_layout");
+        TRY(check_linear(T, I, O, weight_layout));
         const bool io = weight_layout == FSDP_WEIGHT_IN_OUT;
         fsdp::Product p{};
         p.M = T;
@@ -385,10 +430,11 @@ int fsdp_linear_forward(fsdp_compute* c, const fsdp_matrix* x, const fsdp_matrix
         p.bias = bias;
         p.bias_dtype = bias_dtype;
         p.act = activation;
+        fsdp::ProductRoom room{};
+        TRY(take_room(c, p, p.N, &room));
         OnDevice dev(c->device);
         if (!dev.ok()) return fail(FSDP_E_CUDA, "cannot select the handle's device");
-        const cudaError_t e = fsdp::launch_product(p, c->sms, static_cast<cudaStream_t>(stream));
-        return e == cudaSuccess ? FSDP_OK : cuda_fail(e, "linear forward launch");
+        return run_product(c, p, room, static_cast<cudaStream_t>(stream), "linear forward launch");
     });
 }
 
@@ -399,10 +445,7 @@ int fsdp_linear_grad_input(fsdp_compute* c, const fsdp_matrix* dy, const fsdp_ma
         TRY(check_handle(c));
         if (dy == nullptr || dx == nullptr) return fail(FSDP_E_INVALID_ARG, dy == nullptr ? "dy is null" : "dx is null");
         const int64_t T = dy->rows, O = dy->cols, I = dx->cols;
-        TRY(check_shape(T, I, "linear"));
-        TRY(check_shape(T, O, "linear"));
-        if (weight_layout != FSDP_WEIGHT_IN_OUT && weight_layout != FSDP_WEIGHT_OUT_IN)
-            return fail(FSDP_E_INVALID_ARG, "unknown weight_layout");
+        TRY(check_linear(T, I, O, weight_layout));
         const bool io = weight_layout == FSDP_WEIGHT_IN_OUT;
         fsdp::Product p{};
         p.M = T;
@@ -419,10 +462,11 @@ int fsdp_linear_grad_input(fsdp_compute* c, const fsdp_matrix* dy, const fsdp_ma
         }
         TRY(take_optional(add, "add", T, I, kFloats, &p.add));
         TRY(take(dx, "dx", T, I, kFloats, &p.out));
+        fsdp::ProductRoom room{};
+        TRY(take_room(c, p, p.N, &room));
         OnDevice dev(c->device);
         if (!dev.ok()) return fail(FSDP_E_CUDA, "cannot select the handle's device");
-        const cudaError_t e = fsdp::launch_product(p, c->sms, static_cast<cudaStream_t>(stream));
-        return e == cudaSuccess ? FSDP_OK : cuda_fail(e, "linear input-gradient launch");
+        return run_product(c, p, room, static_cast<cudaStream_t>(stream), "linear input-gradient launch");
     });
 }
 
@@ -433,10 +477,7 @@ int fsdp_linear_grad_weight(fsdp_compute* c, const fsdp_matrix* x, const fsdp_ma
         if (x == nullptr || dy == nullptr || dw == nullptr)
             return fail(FSDP_E_INVALID_ARG, x == nullptr ? "x is null" : dy == nullptr ? "dy is null" : "dw is null");
         const int64_t T = dy->rows, O = dy->cols, I = x->cols;
-        TRY(check_shape(T, I, "linear"));
-        TRY(check_shape(T, O, "linear"));
-        if (weight_layout != FSDP_WEIGHT_IN_OUT && weight_layout != FSDP_WEIGHT_OUT_IN)
-            return fail(FSDP_E_INVALID_ARG, "unknown weight_layout");
+        TRY(check_linear(T, I, O, weight_layout));
         const bool io = weight_layout == FSDP_WEIGHT_IN_OUT;
         fsdp::Product p{};
         Mat mx, mdy;
@@ -452,15 +493,16 @@ int fsdp_linear_grad_weight(fsdp_compute* c, const fsdp_matrix* x, const fsdp_ma
         if (accumulate) p.add = p.out;
         if (dbias != nullptr) {
             TRY(take_vector(dbias, "dbias", dw->dtype));
-            TRY(check_workspace(c, column_sum_bytes(O)));
         }
+        fsdp::ProductRoom room{};
+        TRY(take_room(c, p, O, &room));
         OnDevice dev(c->device);
         if (!dev.ok()) return fail(FSDP_E_CUDA, "cannot select the handle's device");
         cudaStream_t st = static_cast<cudaStream_t>(stream);
-        cudaError_t e = fsdp::launch_product(p, c->sms, st);
-        if (e != cudaSuccess) return cuda_fail(e, "linear weight-gradient launch");
+        TRY(run_product(c, p, room, st, "linear weight-gradient launch"));
         if (dbias != nullptr) {
-            e = fsdp::launch_column_sum(T, O, mdy, reinterpret_cast<float*>(c->workspace()), dbias, dw->dtype,
+            float* sums = reinterpret_cast<float*>(c->workspace() + fsdp::kPartialBytes);
+            const cudaError_t e = fsdp::launch_column_sum(T, O, mdy, sums, dbias, dw->dtype,
                                         accumulate != 0, c->sms, st);
             if (e != cudaSuccess) return cuda_fail(e, "bias-gradient launch");
         }

@@ -76,7 +76,24 @@ struct Product {
     int act, slope;
     Mat pre, add, out;          // p null: none
 };
-cudaError_t launch_product(const Product& p, int sms, cudaStream_t st);
+
+// What a product takes from the handle.
+constexpr int kMaxClusters = 76;                                  // pairs of SMs
+constexpr int64_t kPartialBytes = int64_t(kMaxClusters) * 256 * 256 * 4;
+constexpr int64_t kCounterBytes = kMaxClusters * 16 * 4;
+struct ProductRoom {
+    float* partials;            // kPartialBytes: sums of tiles that several clusters share
+    uint32_t* counters;         // kCounterBytes, zero between launches
+    char* copies;               // product_copy_bytes() of both operands
+    int32_t* status;            // FSDP_KSTATUS_* bits
+    unsigned long long wait_ns; // bound of every wait
+    int withhold;               // one-shot test of the give-up path
+};
+// Clusters of two CTAs that run at once (0: the kernel cannot run here).
+int product_clusters(int sms);
+// Bytes of the aligned bf16 copy that an operand needs (0: it is read in place).
+size_t product_copy_bytes(const Mat& m, int64_t rows, int64_t cols);
+cudaError_t launch_product(const Product& p, const ProductRoom& room, int sms, cudaStream_t st);
 
 // Column sums of dy (rows x cols, bf16) over its rows, through `partials`
 // (column_sum_partials() x cols floats).

@@ -1,5 +1,8 @@
 // The linear layer's products, and the column sums of its bias's gradient.
+#include <cuda.h>
+
 #include <algorithm>
+#include <mutex>
 
 #include "block_device.cuh"
 #include "compute.hpp"
@@ -7,88 +10,567 @@
 namespace fsdp {
 namespace {
 
-__device__ __forceinline__ float load_mat(const Mat& m, int64_t r, int64_t c) {
-    if (m.dtype == FSDP_DTYPE_ACT8) {
-        float v;
-        act8_readv<1>(static_cast<const uint8_t*>(m.p) + r * m.ld, m.e + r * m.eld, c, &v);
-        return v;
-    }
-    return load1(m.p, m.dtype, r * m.ld + c);
+// ---- the matrix product ------------------------------------------------------
+//
+// C[m, n] = sum_k A(m, k) B(n, k) on the 5th-generation tensor cores.  A pair
+// of CTAs (a cluster of two) computes one 256 x BN tile with
+// tcgen05.mma.cta_group::2: each CTA holds 128 rows of A and BN/2 rows of B in
+// shared memory, and 128 rows of the fp32 sums in its tensor memory.
+//
+//   warp 0   producer: TMA copies of 64-deep slices into a ring of stages
+//   warp 1   issues the pair's matrix instructions (first CTA only)
+//   warp 2   tensor memory allocation
+//   warps 4-11  epilogue: sums to registers, then bias, activation, residual,
+//            checkpoint, stores; while the next tile's products run into the
+//            other half of tensor memory
+//
+// Either operand may be contiguous along k or along its own rows (W is read
+// both ways, x and dy too): the copies take boxes of 64 elements along the
+// contiguous direction, and only the shared-memory descriptors differ.
+
+constexpr int kStages = 6;
+constexpr int kDepth = 64;                       // k per stage
+constexpr int kStageA = 128 * kDepth * 2;        // bytes of A in a stage, per CTA
+constexpr int kStageB = 128 * kDepth * 2;        // of B, at BN = 256
+constexpr int kEpiWarps = 8;
+constexpr int kEpiBytes = 32 * 32 * 4;           // a warp's transposing buffer
+constexpr int kThreads = 384;
+constexpr int kPiece = 32 * 128;                 // floats of a warp's part of a tile
+constexpr int kPieces = 2 * kEpiWarps;           // parts of a tile
+constexpr size_t kSmemBytes = 1024 + kStages * (kStageA + kStageB) + kEpiWarps * kEpiBytes + 256;
+
+struct Bars {
+    uint64_t full[kStages];      // first CTA's: both CTAs' copies of a stage have landed
+    uint64_t empty[kStages];     // the products that read a stage are done
+    uint64_t tmem_full[2];       // a tile's sums are complete
+    uint64_t tmem_empty[2];      // first CTA's: both CTAs' epilogues have read them
+    uint64_t drain;
+    uint32_t tmem_base;
+    uint32_t abort;              // a wait of this CTA ran out
+    uint32_t issued;             // stages the producer issued
+    uint32_t consumed;           // stages the matrix instructions read
+};
+static_assert(sizeof(Bars) <= 256, "the barriers' room");
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
 }
 
-// A 64 x 64 tile to a block, 4 x 4 products to a thread, fp32 multiply-adds.
-__global__ void __launch_bounds__(256) product_kernel(Product p) {
-    __shared__ float sa[16][65], sb[16][65], sz[64][65];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 64;
-    for (int64_t m0 = static_cast<int64_t>(blockIdx.y) * 64; m0 < p.M; m0 += static_cast<int64_t>(gridDim.y) * 64) {
-        float acc[4][4] = {};
-        for (int64_t k0 = 0; k0 < p.K; k0 += 16) {
-            for (int i = threadIdx.x; i < 1024; i += 256) {
-                const int ka = p.a_trans ? i >> 6 : i & 15, ma = p.a_trans ? i & 63 : i >> 4;
-                const int kb = p.b_trans ? i >> 6 : i & 15, nb = p.b_trans ? i & 63 : i >> 4;
-                const int64_t m = m0 + ma, n = n0 + nb;
-                float va = 0.0f, vb = 0.0f;
-                if (m < p.M && k0 + ka < p.K) va = p.a_trans ? load_mat(p.a, k0 + ka, m) : load_mat(p.a, m, k0 + ka);
-                if (n < p.N && k0 + kb < p.K) vb = p.b_trans ? load_mat(p.b, k0 + kb, n) : load_mat(p.b, n, k0 + kb);
-                sa[ka][ma] = va;
-                sb[kb][nb] = vb;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                float x[4], y[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[i] = sa[k][ty + 16 * i];
-                    y[i] = sb[k][tx + 16 * i];
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
-            }
-            __syncthreads();
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sz[ty + 16 * i][tx + 16 * j] = acc[i][j];
-        __syncthreads();
-        const int lane = threadIdx.x & 31;
-        for (int r = threadIdx.x >> 5; r < 64; r += 8) {
-            const int64_t m = m0 + r;
-            if (m >= p.M) break;   // the same for the whole warp
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t n = n0 + h * 32 + lane;
-                const bool on = n < p.N;
-                float v = on ? sz[r][h * 32 + lane] : 0.0f;
-                if (p.bias != nullptr && on) v += load1(p.bias, p.bias_dtype, n);
-                if (!p.slope) {
-                    if (p.pre.p != nullptr) {
-                        if (p.pre.dtype == FSDP_DTYPE_ACT8) {
-                            const uint32_t byte = act8_group_byte<1>(&v);
-                            if (n < p.pre.ld) {
-                                act8_writev<1>(static_cast<uint8_t*>(p.pre.p) + m * p.pre.ld, n, &v, byte);
-                                if (lane == 0) p.pre.e[m * p.pre.eld + (n >> 5)] = static_cast<uint8_t>(byte);
-                            }
-                        } else if (on) {
-                            store1(p.pre.p, p.pre.dtype, m * p.pre.ld + n, v);
-                        }
-                    }
-                    v = activate(v, p.act);
-                } else if (on) {
-                    v *= act_slope(load_mat(p.pre, m, n), p.act);
-                }
-                if (on) {
-                    if (p.add.p != nullptr) v += load1(p.add.p, p.add.dtype, m * p.add.ld + n);
-                    store1(p.out.p, p.out.dtype, m * p.out.ld + n, v);
-                }
-            }
-        }
-        __syncthreads();
+// The same shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t remote_addr(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+__device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void bar_arrive_remote(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void bar_expect_remote(uint32_t addr, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(addr), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ unsigned long long now_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+
+__device__ __forceinline__ bool bar_try(uint32_t addr, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        : "=r"(done)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// Wait for a phase; false if it has not completed within the limit, or if
+// another wait of this CTA has run out already.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns,
+                                         const volatile uint32_t* abort) {
+    const uint32_t addr = smem_addr(bar);
+    unsigned long long t0 = 0;
+    for (uint32_t i = 0;; ++i) {
+        if (bar_try(addr, parity)) return true;
+        if (i == 0) t0 = now_ns();
+        else if ((i & 63) == 0 && (*abort != 0 || now_ns() - t0 > limit_ns)) return false;
     }
+}
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+
+// Arrives on the barrier at this offset in both CTAs once the matrix
+// instructions issued so far are done.
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float* v) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Shared-memory descriptor of an operand slice, 128-byte swizzled.  Contiguous
+// along k: rows of 64 elements, 8-row groups 1024 bytes apart.  Contiguous
+// along its rows: blocks of 64 rows x 64 k, 8192 bytes apart, 8-k groups 1024
+// bytes apart.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool by_rows) {
+    const uint64_t lead = by_rows ? 8192 >> 4 : 1;
+    return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | lead << 16 | static_cast<uint64_t>(1024 >> 4) << 32 |
+           uint64_t(1) << 46 | uint64_t(2) << 61;
+}
+
+struct Plan {
+    int ks;                    // stages' worth of k
+    int bn;                    // columns of a tile: 32 .. 256 in steps of 32
+    int tiles_m, tiles_n;
+    int64_t whole;             // tiles done by one cluster each
+    int64_t units;             // whole + (tiles - whole) * parts
+    int parts;                 // clusters that share one of the remaining tiles, along k
+    int swapped;               // the tile's rows are C's columns (few tokens)
+    int vec;                   // every row of the epilogue's matrices on a 16-byte boundary, N % 8 == 0
+    float* partials;           // sums of the shared tiles: tile, part, piece, kPiece floats
+    uint32_t* counters;        // one to a shared tile's piece; zero between launches
+    int32_t* status;
+    unsigned long long wait_ns;
+    int withhold;
+};
+
+struct Unit {
+    int tm, tn, k0, k1, part;
+    int64_t shared;            // index among the shared tiles, or -1
+};
+
+__device__ __forceinline__ Unit unit_of(const Plan& p, int64_t u) {
+    Unit r;
+    int64_t t = u;
+    r.k0 = 0;
+    r.k1 = p.ks;
+    r.part = 0;
+    r.shared = -1;
+    if (u >= p.whole) {
+        const int64_t v = u - p.whole;
+        r.shared = v / p.parts;
+        r.part = static_cast<int>(v - r.shared * p.parts);
+        t = p.whole + r.shared;
+        r.k0 = static_cast<int>(static_cast<int64_t>(p.ks) * r.part / p.parts);
+        r.k1 = static_cast<int>(static_cast<int64_t>(p.ks) * (r.part + 1) / p.parts);
+    }
+    // bands of 8 tiles down, walked along n: a wave of clusters shares few
+    // slices of A and B in L2
+    const int64_t band = static_cast<int64_t>(8) * p.tiles_n;
+    const int64_t b = t / band;
+    const int in = static_cast<int>(t - b * band);
+    const int high = min(8, p.tiles_m - static_cast<int>(b) * 8);
+    r.tm = static_cast<int>(b) * 8 + in % high;
+    r.tn = in / high;
+    return r;
+}
+
+// One element of C: the tail of the epilogue where a lane holds one column.
+// All 32 lanes call it with consecutive columns n of one row m (a group of the
+// checkpoint when n0 is a multiple of 32).
+__device__ __forceinline__ void finish1(const Product& p, int64_t m, int64_t n, bool on, float v, int lane) {
+    if (p.bias != nullptr && on) v += load1(p.bias, p.bias_dtype, n);
+    if (!p.slope) {
+        if (p.pre.p != nullptr) {
+            if (p.pre.dtype == FSDP_DTYPE_ACT8) {
+                if (!on) v = 0.0f;
+                const uint32_t byte = act8_group_byte<1>(&v);
+                if (n < p.pre.ld) {
+                    act8_writev<1>(static_cast<uint8_t*>(p.pre.p) + m * p.pre.ld, n, &v, byte);
+                    if (lane == 0) p.pre.e[m * p.pre.eld + (n >> 5)] = static_cast<uint8_t>(byte);
+                }
+            } else if (on) {
+                store1(p.pre.p, p.pre.dtype, m * p.pre.ld + n, v);
+            }
+        }
+        v = activate(v, p.act);
+    } else if (on) {
+        float z;
+        if (p.pre.dtype == FSDP_DTYPE_ACT8)
+            act8_readv<1>(static_cast<const uint8_t*>(p.pre.p) + m * p.pre.ld, p.pre.e + m * p.pre.eld, n, &z);
+        else
+            z = load1(p.pre.p, p.pre.dtype, m * p.pre.ld + n);
+        v *= act_slope(z, p.act);
+    }
+    if (on) {
+        if (p.add.p != nullptr) v += load1(p.add.p, p.add.dtype, m * p.add.ld + n);
+        store1(p.out.p, p.out.dtype, m * p.out.ld + n, v);
+    }
+}
+
+// Eight consecutive columns from n (a multiple of 8, all inside the matrix
+// when `on`); four consecutive lanes hold a checkpoint's group.
+__device__ __forceinline__ void finish8(const Product& p, int64_t m, int64_t n, bool on, float* v, const float* bias,
+                                        int lane) {
+    if (p.bias != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += bias[j];
+    }
+    if (!p.slope) {
+        if (p.pre.p != nullptr) {
+            if (p.pre.dtype == FSDP_DTYPE_ACT8) {
+                if (!on) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+                }
+                const uint32_t byte = act8_group_byte<8>(v);
+                if (m < p.M && n < p.pre.ld) {
+                    act8_writev<8>(static_cast<uint8_t*>(p.pre.p) + m * p.pre.ld, n, v, byte);
+                    if ((lane & 3) == 0) p.pre.e[m * p.pre.eld + (n >> 5)] = static_cast<uint8_t>(byte);
+                }
+            } else if (on) {
+                store8(p.pre.p, p.pre.dtype, m * p.pre.ld + n, v);
+            }
+        }
+        if (p.act == FSDP_ACTIVATION_GELU_TANH) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = gelu_tanh(v[j]);
+        } else if (p.act != FSDP_ACTIVATION_NONE) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = activate(v[j], p.act);
+        }
+    } else if (on) {
+        float z[8];
+        if (p.pre.dtype == FSDP_DTYPE_ACT8)
+            act8_readv<8>(static_cast<const uint8_t*>(p.pre.p) + m * p.pre.ld, p.pre.e + m * p.pre.eld, n, z);
+        else
+            load8(p.pre.p, p.pre.dtype, m * p.pre.ld + n, z);
+        if (p.act == FSDP_ACTIVATION_GELU_TANH) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= gelu_tanh_slope(z[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= act_slope(z[j], p.act);
+        }
+    }
+    if (on) {
+        if (p.add.p != nullptr) {
+            float e[8];
+            load8(p.add.p, p.add.dtype, m * p.add.ld + n, e);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += e[j];
+        }
+        store8(p.out.p, p.out.dtype, m * p.out.ld + n, v);
+    }
+}
+
+// One 32 x 32 chunk whose rows lie one to a lane: v[j] is tile row `row0 +
+// lane`, tile column `col0 + j`.  buf: the warp's 4 KiB of shared memory, in
+// which 16-byte slot s of row r lies at s ^ (r & 7) (no bank conflicts either way).
+__device__ __forceinline__ void finish_chunk(const Product& p, const Plan& pl, int64_t row0, int64_t col0, float* v,
+                                             float4* buf, int lane) {
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+        buf[lane * 8 + (s ^ (lane & 7))] = make_float4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]);
+    __syncwarp();
+    if (pl.vec) {
+        const int64_t n = col0 + (lane & 3) * 8;
+        float bias[8];
+        if (p.bias != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) bias[j] = n < p.N ? load1(p.bias, p.bias_dtype, n + j) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2);
+            const float4 a = buf[r * 8 + (((lane & 3) * 2) ^ (r & 7))];
+            const float4 b = buf[r * 8 + (((lane & 3) * 2 + 1) ^ (r & 7))];
+            float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            const int64_t m = row0 + r;
+            finish8(p, m, n, m < p.M && n < p.N, w, bias, lane);
+        }
+    } else {
+        // one column of C to a lane; swapped, a lane's tile row is that column
+        const float* f = reinterpret_cast<const float*>(buf);
+        const int64_t m0 = pl.swapped ? col0 : row0, n = (pl.swapped ? row0 : col0) + lane;
+        const int count = static_cast<int>(min(static_cast<int64_t>(32), p.M - m0));
+        for (int i = 0; i < count; ++i) {
+            const int r = pl.swapped ? lane : i, c = pl.swapped ? i : lane;
+            finish1(p, m0 + i, n, n < p.N, f[r * 32 + (((c >> 2) ^ (r & 7)) << 2) + (c & 3)], lane);
+        }
+    }
+    __syncwarp();
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                   const __grid_constant__ Product p, const __grid_constant__ Plan pl) {
+    extern __shared__ uint8_t smem_raw[];
+    // the swizzle pattern repeats every 1024 bytes of the shared address; both
+    // CTAs of the pair compute the same offset
+    uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint8_t* stage_a = smem;
+    uint8_t* stage_b = smem + kStages * kStageA;
+    float4* epi = reinterpret_cast<float4*>(smem + kStages * (kStageA + kStageB));
+    Bars* bars = reinterpret_cast<Bars*>(smem + kStages * (kStageA + kStageB) + kEpiWarps * kEpiBytes);
+    volatile uint32_t* abort = &bars->abort;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int64_t cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            bar_init(&bars->full[i], 2);
+            bar_init(&bars->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&bars->tmem_full[i], 1);
+            bar_init(&bars->tmem_empty[i], 2 * kEpiWarps);
+        }
+        bar_init(&bars->drain, 1);
+        bars->abort = bars->issued = bars->consumed = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_b) : "memory");
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&bars->tmem_base)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    __syncthreads();
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = bars->tmem_base;
+
+    if (warp == 0 && lane == 0) {
+        // ---- producer ----
+        const uint32_t bytes = kStageA + pl.bn / 2 * kDepth * 2;
+        uint32_t q = 0;
+        bool ok = true;
+        for (int64_t u = cluster; u < pl.units && ok; u += clusters) {
+            const Unit un = unit_of(pl, u);
+            const int row = un.tm * 256 + static_cast<int>(rank) * 128;
+            const int col = un.tn * pl.bn + static_cast<int>(rank) * (pl.bn / 2);
+            for (int k = un.k0; k < un.k1; ++k, ++q) {
+                const uint32_t s = q % kStages;
+                if (q >= kStages && !bar_wait(&bars->empty[s], (q / kStages - 1) & 1u, pl.wait_ns, abort)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t full = remote_addr(smem_addr(&bars->full[s]), 0);
+                bar_expect_remote(full, bytes);
+                const uint32_t a = smem_addr(stage_a + s * kStageA), b = smem_addr(stage_b + s * kStageB);
+                if (!(pl.withhold && blockIdx.x < 2 && q == 0)) {
+                    if (!p.a_trans) {
+                        tma_load(a, &map_a, k * kDepth, row, full);
+                    } else {
+                        tma_load(a, &map_a, row, k * kDepth, full);
+                        tma_load(a + 8192, &map_a, row + 64, k * kDepth, full);
+                    }
+                    if (!p.b_trans) {
+                        tma_load(b, &map_b, k * kDepth, col, full);
+                    } else {
+                        tma_load(b, &map_b, col, k * kDepth, full);
+                        if (pl.bn == 256) tma_load(b + 8192, &map_b, col + 64, k * kDepth, full);
+                    }
+                }
+                bars->issued = q + 1;
+            }
+        }
+        // the stages still being read: their commits arrive here before this CTA leaves
+        for (uint32_t i = q > kStages ? q - kStages : 0; ok && i < q; ++i)
+            ok = bar_wait(&bars->empty[i % kStages], (i / kStages) & 1u, pl.wait_ns, abort);
+        if (!ok) {
+            atomicOr(pl.status, FSDP_KSTATUS_WAIT_TIMEOUT);
+            *abort = 1;
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ---- matrix instructions ----
+        const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | static_cast<uint32_t>(p.a_trans) << 15 |
+                               static_cast<uint32_t>(p.b_trans) << 16 | static_cast<uint32_t>(pl.bn >> 3) << 17 | 16u << 24;
+        const uint32_t step_a = p.a_trans ? 2048 >> 4 : 32 >> 4, step_b = p.b_trans ? 2048 >> 4 : 32 >> 4;
+        uint32_t q = 0, tile = 0;
+        bool ok = true;
+        for (int64_t u = cluster; u < pl.units && ok; u += clusters, ++tile) {
+            const Unit un = unit_of(pl, u);
+            const uint32_t buf = tile & 1u;
+            if (tile >= 2 && !bar_wait(&bars->tmem_empty[buf], (tile / 2 - 1) & 1u, pl.wait_ns, abort)) {
+                ok = false;
+                break;
+            }
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            for (int k = un.k0; k < un.k1; ++k, ++q) {
+                const uint32_t s = q % kStages;
+                if (!bar_wait(&bars->full[s], (q / kStages) & 1u, pl.wait_ns, abort)) {
+                    ok = false;
+                    break;
+                }
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint64_t da = smem_desc(smem_addr(stage_a + s * kStageA), p.a_trans);
+                const uint64_t db = smem_desc(smem_addr(stage_b + s * kStageB), p.b_trans);
+#pragma unroll
+                for (int i = 0; i < kDepth / 16; ++i)
+                    mma(tmem + buf * 256, da + i * step_a, db + i * step_b, idesc, (k > un.k0 || i > 0) ? 1u : 0u);
+                mma_commit(&bars->empty[s]);
+                bars->consumed = q + 1;
+            }
+            if (ok) mma_commit(&bars->tmem_full[buf]);
+        }
+        if (!ok) {
+            // give up: report, then wait for the matrix instructions in flight
+            atomicOr(pl.status, FSDP_KSTATUS_WAIT_TIMEOUT);
+            *abort = 1;
+            mma_commit(&bars->drain);
+            const volatile uint32_t never = 0;
+            if (!bar_wait(&bars->drain, 0, pl.wait_ns, &never)) atomicOr(pl.status, FSDP_KSTATUS_DRAIN_TIMEOUT);
+        }
+    } else if (warp >= 4) {
+        // ---- epilogue ----
+        const int w = warp - 4, quad = warp & 3, half = w >> 2;
+        float4* buf4 = epi + w * (kEpiBytes / 16);
+        const int chunks = pl.bn / 32;
+        uint32_t tile = 0;
+        for (int64_t u = cluster; u < pl.units; u += clusters, ++tile) {
+            const Unit un = unit_of(pl, u);
+            const uint32_t buf = tile & 1u;
+            // the whole warp goes on or none of it
+            if (!__all_sync(0xffffffffu, bar_wait(&bars->tmem_full[buf], (tile / 2) & 1u, pl.wait_ns, abort))) {
+                if (lane == 0) atomicOr(pl.status, FSDP_KSTATUS_WAIT_TIMEOUT);
+                *abort = 1;
+                break;
+            }
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const int64_t row0 = static_cast<int64_t>(un.tm) * 256 + rank * 128 + quad * 32;
+            const int64_t col0 = static_cast<int64_t>(un.tn) * pl.bn;
+            const uint32_t src = tmem + buf * 256 + (static_cast<uint32_t>(quad * 32) << 16);
+            if (un.shared < 0) {
+                for (int c = half; c < chunks; c += 2) {
+                    float v[32];
+                    tmem_load32(src + c * 32, v);
+                    if (c + 2 >= chunks) {
+                        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) bar_arrive_remote(remote_addr(smem_addr(&bars->tmem_empty[buf]), 0));
+                    }
+                    finish_chunk(p, pl, row0, col0 + c * 32, v, buf4, lane);
+                }
+                if (half >= chunks && lane == 0) bar_arrive_remote(remote_addr(smem_addr(&bars->tmem_empty[buf]), 0));
+            } else {
+                // a tile shared along k: leave this part's sums in the workspace;
+                // whichever warp comes last for this piece adds them up, in the
+                // order of the parts, and finishes
+                const int piece = static_cast<int>(rank) * kEpiWarps + w;
+                float4* tile_sums = reinterpret_cast<float4*>(pl.partials) +
+                                    (un.shared * pl.parts * kPieces + piece) * static_cast<int64_t>(kPiece / 4);
+                const int64_t part_stride = static_cast<int64_t>(kPieces) * (kPiece / 4);
+                for (int c = half; c < chunks; c += 2) {
+                    float v[32];
+                    tmem_load32(src + c * 32, v);
+                    float4* dst = tile_sums + un.part * part_stride + (c >> 1) * 256 + lane;
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+                        __stcg(dst + s * 32, make_float4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]));
+                }
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __threadfence();
+                __syncwarp();
+                uint32_t last = 0;
+                if (lane == 0) {
+                    bar_arrive_remote(remote_addr(smem_addr(&bars->tmem_empty[buf]), 0));
+                    uint32_t* counter = pl.counters + un.shared * kPieces + piece;
+                    last = atomicAdd(counter, 1u) == static_cast<uint32_t>(pl.parts - 1);
+                    if (last) *counter = 0;
+                    __threadfence();
+                }
+                last = __shfl_sync(0xffffffffu, last, 0);
+                __syncwarp();
+                if (last) {
+                    for (int c = half; c < chunks; c += 2) {
+                        float v[32];
+                        const float4* q = tile_sums + (c >> 1) * 256 + lane;
+#pragma unroll
+                        for (int s = 0; s < 8; ++s) {
+                            const float4 f = __ldcg(q + s * 32);
+                            v[4 * s] = f.x; v[4 * s + 1] = f.y; v[4 * s + 2] = f.z; v[4 * s + 3] = f.w;
+                        }
+                        for (int j = 1; j < pl.parts; ++j) {
+#pragma unroll
+                            for (int s = 0; s < 8; ++s) {
+                                const float4 f = __ldcg(q + j * part_stride + s * 32);
+                                v[4 * s] += f.x; v[4 * s + 1] += f.y; v[4 * s + 2] += f.z; v[4 * s + 3] += f.w;
+                            }
+                        }
+                        finish_chunk(p, pl, row0, col0 + c * 32, v, buf4, lane);
+                    }
+                }
+            }
+        }
+    }
+
+    __syncthreads();
+    // no CTA leaves while its pair may still read its shared memory or arrive on its barriers
+    cluster_sync();
+    if (rank == 0 && threadIdx.x == 0) {
+        const uint32_t peer = remote_addr(smem_addr(&bars->issued), 1);
+        uint32_t theirs;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(theirs) : "r"(peer) : "memory");
+        const uint32_t ours = bars->issued;
+        // after a give-up: copies in flight still land before either CTA leaves.
+        // Each stage that one side alone issued gets the other's arrival here.
+        const volatile uint32_t never = 0;
+        for (uint32_t q = bars->consumed; q < max(ours, theirs); ++q) {
+            const uint32_t bar = remote_addr(smem_addr(&bars->full[q % kStages]), 0);
+            if (pl.withhold && blockIdx.x < 2 && q == 0) continue;   // armed, but no copy was issued
+            if (q >= ours) bar_arrive_remote(bar);
+            if (q >= theirs) bar_arrive_remote(bar);
+            if (!bar_wait(&bars->full[q % kStages], (q / kStages) & 1u, pl.wait_ns, &never))
+                atomicOr(pl.status, FSDP_KSTATUS_DRAIN_TIMEOUT);
+        }
+    }
+    cluster_sync();
+    if (warp == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
 // 256 columns and one slice of the rows to a block.
@@ -100,13 +582,183 @@ __global__ void __launch_bounds__(256) column_sum_kernel(int64_t rows, int64_t c
     partials[static_cast<int64_t>(blockIdx.y) * cols + c] = s;
 }
 
+// Rows of a bf16 matrix that do not start on 16-byte boundaries, copied to
+// ones that do (dst.ld a multiple of 8).
+__global__ void __launch_bounds__(256) align_rows_kernel(int64_t rows, int64_t cols, Mat src, Mat dst) {
+    const int64_t chunks = (cols + 7) / 8;
+    for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+        const uint16_t* s = static_cast<const uint16_t*>(src.p) + row * src.ld;
+        uint16_t* d = static_cast<uint16_t*>(dst.p) + row * dst.ld;
+        for (int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; c < chunks;
+             c += static_cast<int64_t>(gridDim.x) * 256) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t i = c * 8 + 2 * j;
+                const uint32_t lo = i < cols ? s[i] : 0, hi = i + 1 < cols ? s[i + 1] : 0;
+                w[j] = lo | hi << 16;
+            }
+            *reinterpret_cast<uint4*>(d + c * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+bool tma_ready(const Mat& m) { return m.dtype == FSDP_DTYPE_BF16 && rows_aligned(m); }
+
+// The driver's tensor-map encoder, looked up once (no link against libcuda).
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+Encode encoder() {
+    static std::once_flag once;
+    static Encode fn = nullptr;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) == cudaSuccess &&
+            found == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<Encode>(p);
+    });
+    return fn;
+}
+
+// rows x cols of bf16, copied in boxes of box_rows x 64 columns.
+cudaError_t make_map(CUtensorMap* map, const Mat& m, int64_t rows, int64_t cols, int box_rows) {
+    const Encode fn = encoder();
+    if (fn == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(m.ld) * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t steps[2] = {1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, m.p, dims, strides, box, steps,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Tiles, and how the last ones are shared: the clusters take whole tiles in
+// turn; what is left over after the last full round is cut along k so that
+// every cluster has a part.  The width is the one with the least estimated
+// time; a stage of 64 k takes 2 cycles a column on the tensor cores, and the
+// copies 16 KiB + 64 bytes a column at about 56 bytes a cycle.
+Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, int clusters) {
+    Plan best{};
+    double least = 0;
+    for (int bn = 256; bn >= 32; bn -= 32) {
+        if (b_by_rows && bn != 256 && bn != 128) continue;
+        if (bn < 256 && bn >= 2 * cols && bn > 32) continue;
+        Plan p{};
+        p.ks = static_cast<int>((k + kDepth - 1) / kDepth);
+        p.bn = bn;
+        p.tiles_m = static_cast<int>((rows + 255) / 256);
+        p.tiles_n = static_cast<int>((cols + bn - 1) / bn);
+        const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+        const int64_t left = tiles % clusters;
+        p.parts = left == 0 ? 1 : static_cast<int>(std::min<int64_t>(clusters / left, std::max(1, p.ks / 4)));
+        p.whole = p.parts > 1 ? tiles - left : tiles;
+        p.units = p.whole + (tiles - p.whole) * p.parts;
+        const double stage = std::max(2.0 * bn, (16384.0 + 64.0 * bn) / 56.0);
+        const double rounds = static_cast<double>((p.whole + clusters - 1) / clusters);
+        double t = rounds * (p.ks * stage + 300.0) + 3.0 * bn + 2000.0;
+        if (p.parts > 1) t += (p.ks / p.parts + 1) * stage + 2500.0 + 60.0 * p.parts * bn / 32;
+        if (least == 0 || t < least) {
+            least = t;
+            best = p;
+        }
+    }
+    return best;
+}
+
 }  // namespace
 
-cudaError_t launch_product(const Product& p, int sms, cudaStream_t st) {
-    (void)sms;
+int product_clusters(int sms) {
+    static std::once_flag once;
+    static int most = 0;
+    std::call_once(once, [] {
+        if (cudaFuncSetAttribute(product_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) return;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(2 * kMaxClusters);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmemBytes;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, product_kernel, &cfg) == cudaSuccess) most = n;
+    });
+    return std::min(std::min(most, sms / 2), kMaxClusters);
+}
+
+size_t product_copy_bytes(const Mat& m, int64_t rows, int64_t cols) {
+    return tma_ready(m) ? 0 : static_cast<size_t>(round_up(rows * round_up(cols, 8) * 2, 256));
+}
+
+namespace {
+
+// An operand as the copies need it: itself, or an aligned bf16 copy in *room.
+cudaError_t settle(Mat* m, int64_t rows, int64_t cols, char** room, int sms, cudaStream_t st) {
+    if (tma_ready(*m)) return cudaSuccess;
+    Mat d{};
+    d.p = *room;
+    d.ld = round_up(cols, 8);
+    d.dtype = FSDP_DTYPE_BF16;
+    *room += product_copy_bytes(*m, rows, cols);
+    cudaError_t e;
+    if (m->dtype == FSDP_DTYPE_ACT8) {
+        // the checkpoint's pad elements are zeros: whole vectors can be read
+        e = launch_act8_unpack(rows, d.ld, *m, FSDP_ACTIVATION_NONE, d, sms, st);
+    } else {
+        const dim3 grid(static_cast<unsigned>(std::min<int64_t>((d.ld / 8 + 255) / 256, 1024)),
+                        static_cast<unsigned>(std::min<int64_t>(rows, 65535)));
+        align_rows_kernel<<<grid, 256, 0, st>>>(rows, cols, *m, d);
+        e = cudaGetLastError();
+    }
+    *m = d;
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_product(const Product& given, const ProductRoom& room, int sms, cudaStream_t st) {
+    Product p = given;
     if (p.M == 0 || p.N == 0) return cudaSuccess;
-    const dim3 grid(static_cast<unsigned>((p.N + 63) / 64), static_cast<unsigned>(std::min<int64_t>((p.M + 63) / 64, 65535)));
-    product_kernel<<<grid, 256, 0, st>>>(p);
+    if (p.K == 0) {   // an empty sum
+        if (p.add.p == p.out.p) return cudaSuccess;
+        const size_t esz = p.out.dtype == FSDP_DTYPE_F32 ? 4 : 2;
+        return cudaMemset2DAsync(p.out.p, p.out.ld * esz, 0, p.N * esz, p.M, st);
+    }
+    const int clusters = product_clusters(sms);
+    if (clusters < 1) return cudaErrorNotSupported;
+    char* copies = room.copies;
+    cudaError_t e = settle(&p.a, p.a_trans ? p.K : p.M, p.a_trans ? p.M : p.K, &copies, sms, st);
+    if (e == cudaSuccess) e = settle(&p.b, p.b_trans ? p.K : p.N, p.b_trans ? p.N : p.K, &copies, sms, st);
+    if (e != cudaSuccess) return e;
+
+    const bool vec = p.N % 8 == 0 && rows_aligned(p.out) && (p.add.p == nullptr || rows_aligned(p.add)) &&
+                     (p.pre.p == nullptr || rows_aligned(p.pre));
+    // Few rows: they become the tile's columns, so that a tile of 256 is not
+    // filled with rows that do not exist.
+    int64_t rows = p.M, cols = p.N;
+    const bool swap = p.M <= 256 && p.N > p.M && !p.a_trans;
+    if (swap) {
+        std::swap(p.a, p.b);
+        std::swap(p.a_trans, p.b_trans);
+        std::swap(rows, cols);
+    }
+    Plan pl = plan_product(rows, cols, p.K, p.b_trans, clusters);
+    pl.swapped = swap;
+    pl.vec = vec && !swap;
+    pl.partials = room.partials;
+    pl.counters = room.counters;
+    pl.status = room.status;
+    pl.wait_ns = room.wait_ns;
+    pl.withhold = room.withhold;
+    CUtensorMap map_a, map_b;
+    e = p.a_trans ? make_map(&map_a, p.a, p.K, rows, 64) : make_map(&map_a, p.a, rows, p.K, 128);
+    if (e == cudaSuccess) e = p.b_trans ? make_map(&map_b, p.b, p.K, cols, 64) : make_map(&map_b, p.b, cols, p.K, pl.bn / 2);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(pl.units, clusters));
+    product_kernel<<<grid, kThreads, kSmemBytes, st>>>(map_a, map_b, p, pl);
     return cudaGetLastError();
 }
 

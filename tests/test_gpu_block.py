@@ -468,3 +468,21 @@ def test_refusals_change_nothing(handle):
     assert lib.fsdp_linear_forward(handle.handle, ok, B._mat(w), 0, None, 0, 0, None, None, None, None) == bad
     torch.cuda.synchronize()
     assert bool((y == 9).all()) and bool((s == 9).all()) and bool((dw == 9).all()) and bool((g == 1).all())
+
+
+def test_a_copy_that_never_arrives_is_reported():
+    """The give-up path: the first stage's copies are withheld, the waits behind
+    them run out, and the handle works again after its status has been read."""
+    c = B.Compute(B.fsdp_linear_workspace_bytes(512, 256, 512))
+    x, w = _normal(1, (512, 256), 1.0, BF), _normal(2, (256, 512), 0.1, BF)
+    y, again = (torch.empty((512, 512), dtype=BF, device="cuda") for _ in range(2))
+    c.linear_forward(x, w, y)
+    assert c.status() == 0
+    c.set_wait_limit(0.02, withhold_next=1)
+    c.linear_forward(x, w, again)
+    assert c.status() == B.FSDP_KSTATUS_WAIT_TIMEOUT
+    assert c.status() == 0
+    c.set_wait_limit()
+    c.linear_forward(x, w, again)
+    assert c.status() == 0 and torch.equal(y, again)
+    c.close()
