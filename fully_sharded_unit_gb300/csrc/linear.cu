@@ -76,39 +76,34 @@ __device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
 }
 
 __device__ __forceinline__ void bar_arrive_remote(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
 __device__ __forceinline__ void bar_expect_remote(uint32_t addr, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(addr), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ unsigned long long now_ns() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(addr), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ bool bar_try(uint32_t addr, uint32_t parity) {
     uint32_t done;
     asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
         : "=r"(done)
         : "r"(addr), "r"(parity)
         : "memory");
     return done != 0;
 }
 
-// Wait for a phase; false if it has not completed within the limit, or if
-// another wait of this CTA has run out already.
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns,
-                                         const volatile uint32_t* abort) {
+// Wait for a phase; false if it has not completed within the limit (in clock
+// cycles), or if another wait of this CTA has run out already.  The clock is
+// read from the 16th try on: most waits end before, and reading the global
+// timer in each of them cost more than half of the products' rate.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, long long limit, const volatile uint32_t* abort) {
     const uint32_t addr = smem_addr(bar);
-    unsigned long long t0 = 0;
+    long long t0 = 0;
     for (uint32_t i = 0;; ++i) {
         if (bar_try(addr, parity)) return true;
-        if (i == 0) t0 = now_ns();
-        else if ((i & 63) == 0 && (*abort != 0 || now_ns() - t0 > limit_ns)) return false;
+        if (i == 16) t0 = clock64();
+        else if (i > 16 && (i & 15) == 0 && (*abort != 0 || clock64() - t0 > limit)) return false;
     }
 }
 
@@ -177,7 +172,7 @@ struct Plan {
     float* partials;           // sums of the shared tiles: tile, part, piece, kPiece floats
     uint32_t* counters;        // one to a shared tile's piece; zero between launches
     int32_t* status;
-    unsigned long long wait_ns;
+    long long wait_cycles;      // bound of every wait
     int withhold;
 };
 
@@ -394,7 +389,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int col = un.tn * pl.bn + static_cast<int>(rank) * (pl.bn / 2);
             for (int k = un.k0; k < un.k1; ++k, ++q) {
                 const uint32_t s = q % kStages;
-                if (q >= kStages && !bar_wait(&bars->empty[s], (q / kStages - 1) & 1u, pl.wait_ns, abort)) {
+                if (q >= kStages && !bar_wait(&bars->empty[s], (q / kStages - 1) & 1u, pl.wait_cycles, abort)) {
                     ok = false;
                     break;
                 }
@@ -420,7 +415,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // the stages still being read: their commits arrive here before this CTA leaves
         for (uint32_t i = q > kStages ? q - kStages : 0; ok && i < q; ++i)
-            ok = bar_wait(&bars->empty[i % kStages], (i / kStages) & 1u, pl.wait_ns, abort);
+            ok = bar_wait(&bars->empty[i % kStages], (i / kStages) & 1u, pl.wait_cycles, abort);
         if (!ok) {
             atomicOr(pl.status, FSDP_KSTATUS_WAIT_TIMEOUT);
             *abort = 1;
@@ -435,14 +430,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int64_t u = cluster; u < pl.units && ok; u += clusters, ++tile) {
             const Unit un = unit_of(pl, u);
             const uint32_t buf = tile & 1u;
-            if (tile >= 2 && !bar_wait(&bars->tmem_empty[buf], (tile / 2 - 1) & 1u, pl.wait_ns, abort)) {
+            if (tile >= 2 && !bar_wait(&bars->tmem_empty[buf], (tile / 2 - 1) & 1u, pl.wait_cycles, abort)) {
                 ok = false;
                 break;
             }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             for (int k = un.k0; k < un.k1; ++k, ++q) {
                 const uint32_t s = q % kStages;
-                if (!bar_wait(&bars->full[s], (q / kStages) & 1u, pl.wait_ns, abort)) {
+                if (!bar_wait(&bars->full[s], (q / kStages) & 1u, pl.wait_cycles, abort)) {
                     ok = false;
                     break;
                 }
@@ -463,7 +458,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             *abort = 1;
             mma_commit(&bars->drain);
             const volatile uint32_t never = 0;
-            if (!bar_wait(&bars->drain, 0, pl.wait_ns, &never)) atomicOr(pl.status, FSDP_KSTATUS_DRAIN_TIMEOUT);
+            if (!bar_wait(&bars->drain, 0, pl.wait_cycles, &never)) atomicOr(pl.status, FSDP_KSTATUS_DRAIN_TIMEOUT);
         }
     } else if (warp >= 4) {
         // ---- epilogue ----
@@ -475,7 +470,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const Unit un = unit_of(pl, u);
             const uint32_t buf = tile & 1u;
             // the whole warp goes on or none of it
-            if (!__all_sync(0xffffffffu, bar_wait(&bars->tmem_full[buf], (tile / 2) & 1u, pl.wait_ns, abort))) {
+            if (!__all_sync(0xffffffffu, bar_wait(&bars->tmem_full[buf], (tile / 2) & 1u, pl.wait_cycles, abort))) {
                 if (lane == 0) atomicOr(pl.status, FSDP_KSTATUS_WAIT_TIMEOUT);
                 *abort = 1;
                 break;
@@ -564,7 +559,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (pl.withhold && blockIdx.x < 2 && q == 0) continue;   // armed, but no copy was issued
             if (q >= ours) bar_arrive_remote(bar);
             if (q >= theirs) bar_arrive_remote(bar);
-            if (!bar_wait(&bars->full[q % kStages], (q / kStages) & 1u, pl.wait_ns, &never))
+            if (!bar_wait(&bars->full[q % kStages], (q / kStages) & 1u, pl.wait_cycles, &never))
                 atomicOr(pl.status, FSDP_KSTATUS_DRAIN_TIMEOUT);
         }
     }
@@ -751,7 +746,7 @@ cudaError_t launch_product(const Product& given, const ProductRoom& room, int sm
     pl.partials = room.partials;
     pl.counters = room.counters;
     pl.status = room.status;
-    pl.wait_ns = room.wait_ns;
+    pl.wait_cycles = static_cast<long long>(room.wait_ns) * 2;   // the SM clock is at most 2.07 GHz
     pl.withhold = room.withhold;
     CUtensorMap map_a, map_b;
     e = p.a_trans ? make_map(&map_a, p.a, p.K, rows, 64) : make_map(&map_a, p.a, rows, p.K, 128);
