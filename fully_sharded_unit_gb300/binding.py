@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Sequence
 
 import torch
@@ -122,7 +123,7 @@ _I64 = ctypes.c_int64
 _PI64 = ctypes.POINTER(ctypes.c_int64)
 _PI = ctypes.POINTER(ctypes.c_int)
 _D = ctypes.c_double
-_PM = ctypes.POINTER(Matrix)
+_PM = _P        # fsdp_matrix: its bytes, or ctypes.byref of a Matrix
 
 _SIGNATURES = {
     "fsdp_plan_layout": (_I, [_I, _PI, _PI64, _I, _I, _PI64, _PI64, ctypes.POINTER(Segment), _I64]),
@@ -567,35 +568,54 @@ class Act8:
         assert self.q.dtype == torch.int8 and tuple(self.q.shape) == (self.rows, ld) and self.q.is_contiguous()
         assert self.exps.dtype == torch.uint8 and tuple(self.exps.shape) == (self.rows, eld) and self.exps.is_contiguous()
         assert self.q.is_cuda and self.exps.is_cuda
-        self.matrix = Matrix(self.q.data_ptr(), self.exps.data_ptr(), self.rows, self.cols, ld, FSDP_DTYPE_ACT8)
+        self.matrix = _pack_matrix(self.q.data_ptr(), self.exps.data_ptr(), self.rows, self.cols, ld, FSDP_DTYPE_ACT8)
 
     @property
     def nbytes(self) -> int:
         return self.q.numel() + self.exps.numel()
 
 
+# The block operators are called several times a layer on small inputs too, so
+# their arguments are marshalled with as few Python operations as carry them: a
+# matrix is packed into bytes laid out as fsdp_matrix (the C side only reads it).
+_pack_matrix = struct.Struct("PPqqqi4x").pack
+assert struct.calcsize("PPqqqi4x") == ctypes.sizeof(Matrix)
+
+
 def _mat(t):
     """fsdp_matrix of a 2-D CUDA tensor whose rows are contiguous, or of an Act8."""
     if t is None:
         return None
-    if isinstance(t, Act8):
+    if t.__class__ is Act8:
         return t.matrix
-    assert t.is_cuda and t.dim() == 2, "a matrix is a 2-D CUDA tensor"
-    rows, cols = t.shape
-    ld = t.stride(0) if rows > 1 else cols
-    assert cols <= 1 or t.stride(1) == 1, "a matrix's rows must be contiguous"
-    return Matrix(t.data_ptr(), None, rows, cols, ld, _TORCH_DTYPES[t.dtype])
+    (rows, cols), (ld, one) = t.shape, t.stride()
+    if rows <= 1:
+        ld = cols
+    assert t.is_cuda and (one == 1 or cols <= 1), "a matrix is a CUDA tensor whose rows are contiguous"
+    return _pack_matrix(t.data_ptr(), 0, rows, cols, ld, _TORCH_DTYPES[t.dtype])
 
 
 def _vec(t, n):
     """(address, dtype) of a contiguous CUDA vector of n elements."""
-    assert t.is_cuda and t.is_contiguous() and t.numel() == n, f"a vector of {n} elements is expected"
+    assert t.is_cuda and t.shape == (n,) and (n <= 1 or t.stride(0) == 1), f"a vector of {n} elements is expected"
     return t.data_ptr(), _TORCH_DTYPES[t.dtype]
 
 
 def _stat(t, n):
-    assert t.is_cuda and t.is_contiguous() and t.numel() == n and t.dtype == torch.float32
-    return t.data_ptr()
+    address, dtype = _vec(t, n)
+    assert dtype == FSDP_DTYPE_F32, "row statistics are float32"
+    return address
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _current(stream):
+    """The stream's address; None: torch's current stream of the current device."""
+    if stream is None and _raw_stream is not None and _device is not None:
+        return _raw_stream(_device())
+    return _stream(stream)
 
 
 def fsdp_compute_create(workspace_bytes=0, allocator=None):
@@ -645,7 +665,7 @@ def fsdp_layer_norm_forward(h, x, gamma, beta, eps, y, mean, rstd, ckpt=None, st
     b, bt = _vec(beta, cols)
     assert dt == bt, "gamma and beta have one dtype"
     _check(lib().fsdp_layer_norm_forward(h, _mat(x), g, b, dt, float(eps), _mat(y), _stat(mean, rows),
-                                         _stat(rstd, rows), _mat(ckpt), _stream(stream)), "fsdp_layer_norm_forward")
+                                         _stat(rstd, rows), _mat(ckpt), _current(stream)), "fsdp_layer_norm_forward")
 
 
 def fsdp_layer_norm_backward(h, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, add=None, accumulate=False,
@@ -658,7 +678,7 @@ def fsdp_layer_norm_backward(h, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, add
     assert gt == bt, "dgamma and dbeta have one dtype"
     _check(lib().fsdp_layer_norm_backward(h, _mat(dy), _mat(x), g, dt, _stat(mean, rows), _stat(rstd, rows),
                                           _mat(add), _mat(dx), dg, db, gt, 1 if accumulate else 0,
-                                          _stream(stream)), "fsdp_layer_norm_backward")
+                                          _current(stream)), "fsdp_layer_norm_backward")
 
 
 def fsdp_linear_forward(h, x, w, y, bias=None, activation="none", residual=None, preact=None,
@@ -667,14 +687,14 @@ def fsdp_linear_forward(h, x, w, y, bias=None, activation="none", residual=None,
     b, bt = _vec(bias, y.shape[1]) if bias is not None else (None, FSDP_DTYPE_F32)
     _check(lib().fsdp_linear_forward(h, _mat(x), _mat(w), WEIGHT_LAYOUTS.get(weight_layout, weight_layout), b, bt,
                                      ACTIVATIONS.get(activation, activation), _mat(residual), _mat(preact), _mat(y),
-                                     _stream(stream)), "fsdp_linear_forward")
+                                     _current(stream)), "fsdp_linear_forward")
 
 
 def fsdp_linear_grad_input(h, dy, w, dx, activation="none", preact=None, add=None, weight_layout="in_out",
                            stream=None) -> None:
     _check(lib().fsdp_linear_grad_input(h, _mat(dy), _mat(w), WEIGHT_LAYOUTS.get(weight_layout, weight_layout),
                                         ACTIVATIONS.get(activation, activation), _mat(preact), _mat(add), _mat(dx),
-                                        _stream(stream)), "fsdp_linear_grad_input")
+                                        _current(stream)), "fsdp_linear_grad_input")
 
 
 def fsdp_linear_grad_weight(h, x, dy, dw, dbias=None, weight_layout="in_out", accumulate=False, stream=None) -> None:
@@ -682,17 +702,17 @@ def fsdp_linear_grad_weight(h, x, dy, dw, dbias=None, weight_layout="in_out", ac
     db, bt = _vec(dbias, dy.shape[1]) if dbias is not None else (None, _TORCH_DTYPES[dw.dtype])
     assert bt == _TORCH_DTYPES[dw.dtype], "dw and dbias have one dtype"
     _check(lib().fsdp_linear_grad_weight(h, _mat(x), _mat(dy), WEIGHT_LAYOUTS.get(weight_layout, weight_layout),
-                                         _mat(dw), db, 1 if accumulate else 0, _stream(stream)),
+                                         _mat(dw), db, 1 if accumulate else 0, _current(stream)),
            "fsdp_linear_grad_weight")
 
 
 def fsdp_act8_pack(h, x, ckpt, stream=None) -> None:
-    _check(lib().fsdp_act8_pack(h, _mat(x), _mat(ckpt), _stream(stream)), "fsdp_act8_pack")
+    _check(lib().fsdp_act8_pack(h, _mat(x), _mat(ckpt), _current(stream)), "fsdp_act8_pack")
 
 
 def fsdp_act8_unpack(h, ckpt, out, activation="none", stream=None) -> None:
     _check(lib().fsdp_act8_unpack(h, _mat(ckpt), ACTIVATIONS.get(activation, activation), _mat(out),
-                                  _stream(stream)), "fsdp_act8_unpack")
+                                  _current(stream)), "fsdp_act8_unpack")
 
 
 class Compute:

@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libfsdp_unit.so")
-SOURCES = ["plan.cpp", "kernels.cu", "api.cu", "noalloc.cu", "compute.cu", "norm.cu", "act8.cu", "linear.cu"]
+SOURCES = ["plan.cpp", "kernels.cu", "api.cu", "noalloc.cu", "compute.cu", "norm.cu", "act8.cu", "linear.cu",
+           "few.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",

@@ -69,6 +69,53 @@ __device__ __forceinline__ void storev(void* p, int dtype, int64_t i, const floa
     else store1(p, dtype, i, v[0]);
 }
 
+// ---- pairs of floats in one 64-bit register (one instruction for both) ----
+
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(f32x2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {   // 2^x, relative error about 2^-22
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {   // 1/x to an ulp; 1/inf = 0
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// 32 bytes from a 32-byte boundary.
+__device__ __forceinline__ void load32b(const void* p, uint32_t* w) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+}
+__device__ __forceinline__ void store32b(void* p, const uint32_t* w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 // ---- ACT8 ----
 
 // The magnitude bits of a float compare like the magnitudes; an infinity or a
@@ -140,8 +187,12 @@ __device__ __forceinline__ uint32_t act8_group_byte(const float* v) {
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < V; ++j) top = max(top, mag_bits(v[j]));
+    if constexpr (V == 1) {
+        top = __reduce_max_sync(0xffffffffu, top);
+    } else {
 #pragma unroll
-    for (int d = 1; d < 32 / V; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        for (int d = 1; d < 32 / V; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+    }
     return act8_byte(top);
 }
 
@@ -171,22 +222,49 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 constexpr float kGeluK2 = 1.5957691216057308f;    // 2 sqrt(2/pi)
 constexpr float kGeluC = 0.044715f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 // z/2 (1 + tanh(u)) = z / (1 + exp(-2u)), u = sqrt(2/pi) (z + 0.044715 z^3):
-// no cancellation for negative z, and exp's overflow gives the limit 0.
-__device__ __forceinline__ float gelu_tanh(float z) {
-    const float u2 = z * fmaf(kGeluK2 * kGeluC * z, z, kGeluK2);
-    return __fdividef(z, 1.0f + __expf(-u2));
+// no cancellation for negative z, and exp's overflow gives the limit 0.  Two
+// elements at a time: five packed instructions and four on the special-function
+// units, which bound it (16 lanes a cycle an SM).
+__device__ __forceinline__ void gelu_tanh2(float& z0, float& z1) {
+    const f32x2 z = pair(z0, z1);
+    const f32x2 t = fma2(mul2(z, z), pair(-kLog2e * kGeluK2 * kGeluC, -kLog2e * kGeluK2 * kGeluC),
+                         pair(-kLog2e * kGeluK2, -kLog2e * kGeluK2));
+    float a, b;
+    unpair(mul2(z, t), a, b);
+    unpair(add2(pair(exp2_fast(a), exp2_fast(b)), pair(1.0f, 1.0f)), a, b);
+    unpair(mul2(z, pair(rcp_fast(a), rcp_fast(b))), z0, z1);
 }
 
-// s + z s (1 - s) (2u)', s = 1 / (1 + exp(-2u)).  Past +-30 the slope is 1 or
-// 0 exactly; the clamp keeps z^2 finite.
+// s + z (s - s^2) (2u)', s = 1 / (1 + exp(-2u)).  z^2 is held at 900 so that it
+// stays finite: past |z| = 30, s is 0 or 1 exactly.
+__device__ __forceinline__ void gelu_tanh_slope2(float z0, float z1, float& d0, float& d1) {
+    const f32x2 z = pair(z0, z1);
+    float a, b;
+    unpair(mul2(z, z), a, b);
+    const f32x2 zz = pair(min_nan(a, 900.0f), min_nan(b, 900.0f));
+    const f32x2 t = fma2(zz, pair(-kLog2e * kGeluK2 * kGeluC, -kLog2e * kGeluK2 * kGeluC),
+                         pair(-kLog2e * kGeluK2, -kLog2e * kGeluK2));
+    unpair(mul2(z, t), a, b);
+    unpair(add2(pair(exp2_fast(a), exp2_fast(b)), pair(1.0f, 1.0f)), a, b);
+    const f32x2 s = pair(rcp_fast(a), rcp_fast(b));
+    const f32x2 rise = fma2(zz, pair(3.0f * kGeluK2 * kGeluC, 3.0f * kGeluK2 * kGeluC), pair(kGeluK2, kGeluK2));
+    const f32x2 fall = fma2(mul2(s, pair(-1.0f, -1.0f)), s, s);
+    unpair(fma2(mul2(z, rise), fall, s), d0, d1);
+}
+
+__device__ __forceinline__ float gelu_tanh(float z) {
+    float other = 0.0f;
+    gelu_tanh2(z, other);
+    return z;
+}
+
 __device__ __forceinline__ float gelu_tanh_slope(float z) {
-    z = min_nan(max_nan(z, -30.0f), 30.0f);
-    const float zz = z * z;
-    const float u2 = z * fmaf(kGeluK2 * kGeluC, zz, kGeluK2);
-    const float s = __fdividef(1.0f, 1.0f + __expf(-u2));
-    return fmaf(z * fmaf(3.0f * kGeluK2 * kGeluC, zz, kGeluK2), s - s * s, s);
+    float d, other;
+    gelu_tanh_slope2(z, 0.0f, d, other);
+    return d;
 }
 
 __device__ __forceinline__ float gelu_erf(float z) { return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f)); }
@@ -205,12 +283,53 @@ __device__ __forceinline__ float activate(float z, int act) {
     }
 }
 
+// N elements in place; the kind is looked at once.
+template <int N>
+__device__ __forceinline__ void activate_n(float* v, int act) {
+    if (act == FSDP_ACTIVATION_GELU_TANH) {
+        if constexpr (N % 2 == 0) {
+#pragma unroll
+            for (int j = 0; j < N; j += 2) gelu_tanh2(v[j], v[j + 1]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = gelu_tanh(v[j]);
+        }
+    } else if (act == FSDP_ACTIVATION_GELU_ERF) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = gelu_erf(v[j]);
+    } else if (act == FSDP_ACTIVATION_RELU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = max_nan(v[j], 0.0f);
+    }
+}
+
 __device__ __forceinline__ float act_slope(float z, int act) {
     switch (act) {
         case FSDP_ACTIVATION_RELU: return z > 0.0f ? 1.0f : 0.0f;
         case FSDP_ACTIVATION_GELU_TANH: return gelu_tanh_slope(z);
         case FSDP_ACTIVATION_GELU_ERF: return gelu_erf_slope(z);
         default: return 1.0f;
+    }
+}
+
+// v *= slope(z), N elements.
+template <int N>
+__device__ __forceinline__ void slope_n(float* v, const float* z, int act) {
+    if (act == FSDP_ACTIVATION_GELU_TANH) {
+        if constexpr (N % 2 != 0) v[N - 1] *= gelu_tanh_slope(z[N - 1]);
+#pragma unroll
+        for (int j = 0; j + 1 < N; j += 2) {
+            float a, b;
+            gelu_tanh_slope2(z[j], z[j + 1], a, b);
+            v[j] *= a;
+            v[j + 1] *= b;
+        }
+    } else if (act == FSDP_ACTIVATION_GELU_ERF) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] *= gelu_erf_slope(z[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = z[j] > 0.0f ? v[j] : v[j] * 0.0f;
     }
 }
 

@@ -17,20 +17,19 @@ namespace fsdp {
 int record_error(int code, const std::string& why);
 }  // namespace fsdp
 
-constexpr int64_t kHeader = 256 + (fsdp::kCounterBytes + 255) / 256 * 256;
+constexpr int64_t kHeader = 256;
 
 struct fsdp_compute {
     int device = 0;
     int sms = 0;
     fsdp_allocator allocator{nullptr, nullptr, nullptr};   // alloc == nullptr: cudaMalloc / cudaFree
-    char* block = nullptr;        // status word, counters of shared tiles, then the workspace
+    char* block = nullptr;        // status word, then the workspace
     int64_t workspace_bytes = 0;
     unsigned long long wait_ns = 10000000000ull;
     int withhold_next = 0;
     bool broken = false;          // a drain wait ran out: only destroy is accepted
 
     int32_t* status() const { return reinterpret_cast<int32_t*>(block); }
-    uint32_t* counters() const { return reinterpret_cast<uint32_t*>(block + 256); }
     char* workspace() const { return block + kHeader; }
 };
 
@@ -185,7 +184,6 @@ int take_room(fsdp_compute* c, const fsdp::Product& p, int64_t out_features, fsd
         fsdp::product_copy_bytes(p.b, p.b_trans ? p.K : p.N, p.b_trans ? p.N : p.K));
     TRY(check_workspace(c, copies_offset(out_features) + copies));
     r->partials = reinterpret_cast<float*>(c->workspace());
-    r->counters = c->counters();
     r->copies = c->workspace() + copies_offset(out_features);
     r->status = c->status();
     r->wait_ns = c->wait_ns;
@@ -283,11 +281,6 @@ int fsdp_compute_status(fsdp_compute* c, int32_t* flags, void* stream) {
         if (e != cudaSuccess) return cuda_fail(e, "reading the status word");
         *flags = v;
         if (v & FSDP_KSTATUS_DRAIN_TIMEOUT) c->broken = true;
-        if (v != 0) {   // a product that gave up leaves its counters as they were
-            e = cudaMemsetAsync(c->counters(), 0, fsdp::kCounterBytes, st);
-            if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-            if (e != cudaSuccess) return cuda_fail(e, "clearing the counters");
-        }
         return FSDP_OK;
     });
 }

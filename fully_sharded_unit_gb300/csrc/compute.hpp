@@ -23,10 +23,10 @@ constexpr int kGroup = 32;   // elements that share an exponent in an ACT8 matri
 
 inline int64_t act8_groups(int64_t cols) { return (cols + kGroup - 1) / kGroup; }
 
-// Rows of m start on 16-byte boundaries (vector accesses of 8 elements).
-inline bool rows_aligned(const Mat& m) {
-    const int64_t esz = m.dtype == 0 ? 4 : m.dtype == 1 ? 2 : 1;
-    return (reinterpret_cast<uintptr_t>(m.p) & 15u) == 0 && (m.ld * esz) % 16 == 0;
+// Rows of m start on boundaries of `to` bytes (16: vector accesses of 8 elements).
+inline bool rows_aligned(const Mat& m, uintptr_t to = 16) {
+    const uintptr_t esz = m.dtype == 0 ? 4 : m.dtype == 1 ? 2 : 1;
+    return ((reinterpret_cast<uintptr_t>(m.p) | static_cast<uintptr_t>(m.ld) * esz) & (to - 1)) == 0;
 }
 
 // ---- layer norm (norm.cu) ----
@@ -80,7 +80,6 @@ struct Product {
 // What a product takes from the handle.
 constexpr int kMaxClusters = 76;                                  // pairs of SMs
 constexpr int64_t kPartialBytes = int64_t(kMaxClusters) * 256 * 256 * 4;
-constexpr int64_t kCounterBytes = kMaxClusters * 16 * 4;
 struct ProductRoom {
     float* partials;            // kPartialBytes: sums of tiles that several clusters share
     uint32_t* counters;         // kCounterBytes, zero between launches
@@ -94,6 +93,14 @@ int product_clusters(int sms);
 // Bytes of the aligned bf16 copy that an operand needs (0: it is read in place).
 size_t product_copy_bytes(const Mat& m, int64_t rows, int64_t cols);
 cudaError_t launch_product(const Product& p, const ProductRoom& room, int sms, cudaStream_t st);
+
+// Products of at most kFewRows rows (few.cu): bound by reading B, which passes
+// once through registers; no workspace, any alignment.
+constexpr int kFewRows = 8;
+inline bool few_rows(const Product& p) {
+    return p.M <= kFewRows && !p.a_trans && p.a.dtype == 1 && p.b.dtype == 1;   // both BF16
+}
+cudaError_t launch_few_rows(const Product& p, int sms, cudaStream_t st);
 
 // Column sums of dy (rows x cols, bf16) over its rows, through `partials`
 // (column_sum_partials() x cols floats).

@@ -1,0 +1,206 @@
+// The linear layer's epilogue (see Product in compute.hpp): bias, kept
+// pre-activation, activation or its slope, added matrix, store.
+#pragma once
+
+#include "block_device.cuh"
+#include "compute.hpp"
+
+namespace fsdp {
+
+// 32 consecutive columns of one row, from column n (a multiple of 32); `left`
+// of them are inside the matrix (a multiple of 8, of 16 where WIDE).
+template <bool WIDE>
+__device__ __forceinline__ void load_row32(const Mat& x, int64_t m, int64_t n, int left, float* v) {
+    if (x.dtype == FSDP_DTYPE_F32) {
+        const float* src = static_cast<const float*>(x.p) + m * x.ld + n;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            if (s * 8 < left) {
+                if (WIDE) {
+                    uint32_t w[8];
+                    load32b(src + s * 8, w);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[s * 8 + j] = __uint_as_float(w[j]);
+                } else {
+                    load8(src, FSDP_DTYPE_F32, s * 8, v + s * 8);
+                }
+            }
+        }
+    } else if (x.dtype == FSDP_DTYPE_BF16) {
+        const uint16_t* src = static_cast<const uint16_t*>(x.p) + m * x.ld + n;
+        if (WIDE) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (s * 16 < left) {
+                    uint32_t w[8];
+                    load32b(src + s * 16, w);
+                    unpack8(make_uint4(w[0], w[1], w[2], w[3]), v + s * 16);
+                    unpack8(make_uint4(w[4], w[5], w[6], w[7]), v + s * 16 + 8);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                if (s * 8 < left) load8(src, FSDP_DTYPE_BF16, s * 8, v + s * 8);
+        }
+    } else {   // a whole group: the pads are there
+        const uint8_t* src = static_cast<const uint8_t*>(x.p) + m * x.ld + n;
+        const float step = act8_step(x.e[m * x.eld + (n >> 5)]);
+        uint32_t w[8];
+        if (WIDE) {
+            load32b(src, w);
+        } else {
+            const uint4 a = reinterpret_cast<const uint4*>(src)[0], b = reinterpret_cast<const uint4*>(src)[1];
+            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+            w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+        }
+#pragma unroll
+        for (int s = 0; s < 8; ++s) act8_read4(w[s], step, v + s * 4);
+    }
+}
+
+template <bool WIDE>
+__device__ __forceinline__ void store_row32(const Mat& x, int64_t m, int64_t n, int left, const float* v) {
+    if (x.dtype == FSDP_DTYPE_F32) {
+        float* dst = static_cast<float*>(x.p) + m * x.ld + n;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            if (s * 8 < left) {
+                if (WIDE) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[s * 8 + j]);
+                    store32b(dst + s * 8, w);
+                } else {
+                    store8(dst, FSDP_DTYPE_F32, s * 8, v + s * 8);
+                }
+            }
+        }
+    } else if (x.dtype == FSDP_DTYPE_BF16) {
+        uint16_t* dst = static_cast<uint16_t*>(x.p) + m * x.ld + n;
+        if (WIDE) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (s * 16 < left) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) w[j] = to_bf16x2(v[s * 16 + 2 * j], v[s * 16 + 2 * j + 1]);
+                    store32b(dst + s * 16, w);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                if (s * 8 < left) store8(dst, FSDP_DTYPE_BF16, s * 8, v + s * 8);
+        }
+    } else {   // a checkpoint's group, in one lane
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) top = max(top, j < left ? mag_bits(v[j]) : 0u);
+        const uint32_t byte = act8_byte(top);
+        const float scale = act8_scale(byte);
+        uint32_t w[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            // a group that is not finite, and the pad of a short one, are zeros
+            w[s] = byte == 255u || s * 4 >= left
+                       ? 0u
+                       : pack4(act8_quant(v[4 * s], scale), act8_quant(v[4 * s + 1], scale),
+                               act8_quant(v[4 * s + 2], scale), act8_quant(v[4 * s + 3], scale));
+        }
+        uint8_t* dst = static_cast<uint8_t*>(x.p) + m * x.ld + n;
+        if (WIDE) {
+            store32b(dst, w);
+        } else {
+            reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+        x.e[m * x.eld + (n >> 5)] = static_cast<uint8_t>(byte);
+    }
+}
+
+// The epilogue of 32 columns of one row: everything a lane needs is in its own
+// registers (a checkpoint's group too), so 32 independent elements hide each
+// other's latency, and every access is a whole 32-byte sector.
+template <bool WIDE, bool SLOPE>
+__device__ __forceinline__ void finish_row(const Product& p, int64_t m, int64_t n, const float4* bias, float* v) {
+    const int left = static_cast<int>(min(static_cast<int64_t>(32), p.N - n));
+    if (p.bias != nullptr) {
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const float4 t = bias[s];
+            v[4 * s] += t.x; v[4 * s + 1] += t.y; v[4 * s + 2] += t.z; v[4 * s + 3] += t.w;
+        }
+    }
+    if (SLOPE) {
+        float z[32];
+        load_row32<WIDE>(p.pre, m, n, left, z);
+        slope_n<32>(v, z, p.act);
+    } else {
+        if (p.pre.p != nullptr) store_row32<WIDE>(p.pre, m, n, left, v);
+        activate_n<32>(v, p.act);
+    }
+    if (p.add.p != nullptr) {
+        float e[32];
+        load_row32<WIDE>(p.add, m, n, left, e);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += e[j];
+    }
+    store_row32<WIDE>(p.out, m, n, left, v);
+}
+
+// The epilogue where a lane holds one column n of R consecutive rows from m
+// (`count` of them inside the matrix): matrices whose rows start anywhere, and
+// tiles whose rows are C's columns.  n - lane is a multiple of 32.
+template <int R, bool SLOPE>
+__device__ __forceinline__ void finish_column(const Product& p, int64_t m, int count, int64_t n, float bias, float* v, int lane) {
+    const bool on = n < p.N;
+#pragma unroll
+    for (int i = 0; i < R; ++i) v[i] += bias;
+    if (SLOPE) {
+        float z[R];
+        if (p.pre.dtype == FSDP_DTYPE_ACT8) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                z[i] = 0.0f;
+                if (on && i < count)
+                    act8_readv<1>(static_cast<const uint8_t*>(p.pre.p) + (m + i) * p.pre.ld, p.pre.e + (m + i) * p.pre.eld, n, z + i);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; ++i) z[i] = on && i < count ? load1(p.pre.p, p.pre.dtype, (m + i) * p.pre.ld + n) : 0.0f;
+        }
+        slope_n<R>(v, z, p.act);
+    } else {
+        if (p.pre.p != nullptr) {
+            if (p.pre.dtype == FSDP_DTYPE_ACT8) {
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const float x = on ? v[i] : 0.0f;
+                    const uint32_t byte = act8_group_byte<1>(&x);
+                    if (i < count && n < p.pre.ld) {
+                        act8_writev<1>(static_cast<uint8_t*>(p.pre.p) + (m + i) * p.pre.ld, n, &x, byte);
+                        if (lane == 0) p.pre.e[(m + i) * p.pre.eld + (n >> 5)] = static_cast<uint8_t>(byte);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    if (on && i < count) store1(p.pre.p, p.pre.dtype, (m + i) * p.pre.ld + n, v[i]);
+            }
+        }
+        activate_n<R>(v, p.act);
+    }
+    if (p.add.p != nullptr) {
+        float e[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) e[i] = on && i < count ? load1(p.add.p, p.add.dtype, (m + i) * p.add.ld + n) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < R; ++i) v[i] += e[i];
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (on && i < count) store1(p.out.p, p.out.dtype, (m + i) * p.out.ld + n, v[i]);
+}
+
+}  // namespace fsdp

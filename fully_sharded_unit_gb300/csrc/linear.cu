@@ -6,6 +6,7 @@
 
 #include "block_device.cuh"
 #include "compute.hpp"
+#include "epilogue.cuh"
 
 namespace fsdp {
 namespace {
@@ -168,18 +169,34 @@ struct Plan {
     int64_t units;             // whole + (tiles - whole) * parts
     int parts;                 // clusters that share one of the remaining tiles, along k
     int swapped;               // the tile's rows are C's columns (few tokens)
-    int vec;                   // every row of the epilogue's matrices on a 16-byte boundary, N % 8 == 0
+    int vec;                   // 1: every row of the epilogue's matrices starts on a 16-byte boundary and N % 8 == 0;
+                               // 2: on a 32-byte boundary and N % 16 == 0; 0: neither, or swapped
     float* partials;           // sums of the shared tiles: tile, part, piece, kPiece floats
-    uint32_t* counters;        // one to a shared tile's piece; zero between launches
     int32_t* status;
     long long wait_cycles;      // bound of every wait
     int withhold;
+
+    // One warp's part of a shared tile: chunk i of it at 256 * i, 16 bytes to a lane, eight times.
+    __device__ float4* sums(int64_t shared, int part, int piece) const {
+        return reinterpret_cast<float4*>(partials) + ((shared * parts + part) * kPieces + piece) * static_cast<int64_t>(kPiece / 4);
+    }
 };
 
 struct Unit {
     int tm, tn, k0, k1, part;
     int64_t shared;            // index among the shared tiles, or -1
 };
+
+// Bands of 8 tiles down, walked along n: a wave of clusters shares few slices
+// of A and B in L2.
+__device__ __forceinline__ void place_tile(const Plan& p, int64_t t, int* tm, int* tn) {
+    const int64_t band = static_cast<int64_t>(8) * p.tiles_n;
+    const int64_t b = t / band;
+    const int in = static_cast<int>(t - b * band);
+    const int high = min(8, p.tiles_m - static_cast<int>(b) * 8);
+    *tm = static_cast<int>(b) * 8 + in % high;
+    *tn = in / high;
+}
 
 __device__ __forceinline__ Unit unit_of(const Plan& p, int64_t u) {
     Unit r;
@@ -196,144 +213,53 @@ __device__ __forceinline__ Unit unit_of(const Plan& p, int64_t u) {
         r.k0 = static_cast<int>(static_cast<int64_t>(p.ks) * r.part / p.parts);
         r.k1 = static_cast<int>(static_cast<int64_t>(p.ks) * (r.part + 1) / p.parts);
     }
-    // bands of 8 tiles down, walked along n: a wave of clusters shares few
-    // slices of A and B in L2
-    const int64_t band = static_cast<int64_t>(8) * p.tiles_n;
-    const int64_t b = t / band;
-    const int in = static_cast<int>(t - b * band);
-    const int high = min(8, p.tiles_m - static_cast<int>(b) * 8);
-    r.tm = static_cast<int>(b) * 8 + in % high;
-    r.tn = in / high;
+    place_tile(p, t, &r.tm, &r.tn);
     return r;
-}
-
-// One element of C: the tail of the epilogue where a lane holds one column.
-// All 32 lanes call it with consecutive columns n of one row m (a group of the
-// checkpoint when n0 is a multiple of 32).
-__device__ __forceinline__ void finish1(const Product& p, int64_t m, int64_t n, bool on, float v, int lane) {
-    if (p.bias != nullptr && on) v += load1(p.bias, p.bias_dtype, n);
-    if (!p.slope) {
-        if (p.pre.p != nullptr) {
-            if (p.pre.dtype == FSDP_DTYPE_ACT8) {
-                if (!on) v = 0.0f;
-                const uint32_t byte = act8_group_byte<1>(&v);
-                if (n < p.pre.ld) {
-                    act8_writev<1>(static_cast<uint8_t*>(p.pre.p) + m * p.pre.ld, n, &v, byte);
-                    if (lane == 0) p.pre.e[m * p.pre.eld + (n >> 5)] = static_cast<uint8_t>(byte);
-                }
-            } else if (on) {
-                store1(p.pre.p, p.pre.dtype, m * p.pre.ld + n, v);
-            }
-        }
-        v = activate(v, p.act);
-    } else if (on) {
-        float z;
-        if (p.pre.dtype == FSDP_DTYPE_ACT8)
-            act8_readv<1>(static_cast<const uint8_t*>(p.pre.p) + m * p.pre.ld, p.pre.e + m * p.pre.eld, n, &z);
-        else
-            z = load1(p.pre.p, p.pre.dtype, m * p.pre.ld + n);
-        v *= act_slope(z, p.act);
-    }
-    if (on) {
-        if (p.add.p != nullptr) v += load1(p.add.p, p.add.dtype, m * p.add.ld + n);
-        store1(p.out.p, p.out.dtype, m * p.out.ld + n, v);
-    }
-}
-
-// Eight consecutive columns from n (a multiple of 8, all inside the matrix
-// when `on`); four consecutive lanes hold a checkpoint's group.
-__device__ __forceinline__ void finish8(const Product& p, int64_t m, int64_t n, bool on, float* v, const float* bias,
-                                        int lane) {
-    if (p.bias != nullptr) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += bias[j];
-    }
-    if (!p.slope) {
-        if (p.pre.p != nullptr) {
-            if (p.pre.dtype == FSDP_DTYPE_ACT8) {
-                if (!on) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-                }
-                const uint32_t byte = act8_group_byte<8>(v);
-                if (m < p.M && n < p.pre.ld) {
-                    act8_writev<8>(static_cast<uint8_t*>(p.pre.p) + m * p.pre.ld, n, v, byte);
-                    if ((lane & 3) == 0) p.pre.e[m * p.pre.eld + (n >> 5)] = static_cast<uint8_t>(byte);
-                }
-            } else if (on) {
-                store8(p.pre.p, p.pre.dtype, m * p.pre.ld + n, v);
-            }
-        }
-        if (p.act == FSDP_ACTIVATION_GELU_TANH) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = gelu_tanh(v[j]);
-        } else if (p.act != FSDP_ACTIVATION_NONE) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = activate(v[j], p.act);
-        }
-    } else if (on) {
-        float z[8];
-        if (p.pre.dtype == FSDP_DTYPE_ACT8)
-            act8_readv<8>(static_cast<const uint8_t*>(p.pre.p) + m * p.pre.ld, p.pre.e + m * p.pre.eld, n, z);
-        else
-            load8(p.pre.p, p.pre.dtype, m * p.pre.ld + n, z);
-        if (p.act == FSDP_ACTIVATION_GELU_TANH) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= gelu_tanh_slope(z[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= act_slope(z[j], p.act);
-        }
-    }
-    if (on) {
-        if (p.add.p != nullptr) {
-            float e[8];
-            load8(p.add.p, p.add.dtype, m * p.add.ld + n, e);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += e[j];
-        }
-        store8(p.out.p, p.out.dtype, m * p.out.ld + n, v);
-    }
 }
 
 // One 32 x 32 chunk whose rows lie one to a lane: v[j] is tile row `row0 +
 // lane`, tile column `col0 + j`.  buf: the warp's 4 KiB of shared memory, in
-// which 16-byte slot s of row r lies at s ^ (r & 7) (no bank conflicts either way).
+// which 16-byte slot s of row r lies at s ^ (r & 7) (no bank conflicts writing,
+// and none reading along a row).
+template <int VEC, bool SLOPE>
 __device__ __forceinline__ void finish_chunk(const Product& p, const Plan& pl, int64_t row0, int64_t col0, float* v,
                                              float4* buf, int lane) {
-#pragma unroll
-    for (int s = 0; s < 8; ++s)
-        buf[lane * 8 + (s ^ (lane & 7))] = make_float4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]);
-    __syncwarp();
-    if (pl.vec) {
-        const int64_t n = col0 + (lane & 3) * 8;
-        float bias[8];
+    if constexpr (VEC > 0) {
+        if (col0 >= p.N) return;
         if (p.bias != nullptr) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) bias[j] = n < p.N ? load1(p.bias, p.bias_dtype, n + j) : 0.0f;
+            __syncwarp();
+            reinterpret_cast<float*>(buf)[lane] = col0 + lane < p.N ? load1(p.bias, p.bias_dtype, col0 + lane) : 0.0f;
+            __syncwarp();
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = i * 8 + (lane >> 2);
-            const float4 a = buf[r * 8 + (((lane & 3) * 2) ^ (r & 7))];
-            const float4 b = buf[r * 8 + (((lane & 3) * 2 + 1) ^ (r & 7))];
-            float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            const int64_t m = row0 + r;
-            finish8(p, m, n, m < p.M && n < p.N, w, bias, lane);
-        }
+        if (row0 + lane < p.M) finish_row<VEC == 2, SLOPE>(p, row0 + lane, col0, buf, v);
     } else {
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            buf[lane * 8 + (s ^ (lane & 7))] = make_float4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]);
+        __syncwarp();
         // one column of C to a lane; swapped, a lane's tile row is that column
         const float* f = reinterpret_cast<const float*>(buf);
         const int64_t m0 = pl.swapped ? col0 : row0, n = (pl.swapped ? row0 : col0) + lane;
         const int count = static_cast<int>(min(static_cast<int64_t>(32), p.M - m0));
-        for (int i = 0; i < count; ++i) {
-            const int r = pl.swapped ? lane : i, c = pl.swapped ? i : lane;
-            finish1(p, m0 + i, n, n < p.N, f[r * 32 + (((c >> 2) ^ (r & 7)) << 2) + (c & 3)], lane);
+        const float bias = p.bias != nullptr && n < p.N ? load1(p.bias, p.bias_dtype, n) : 0.0f;
+        if (n - lane < p.N) {
+            for (int i = 0; i < count; i += 8) {
+                float w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int r = pl.swapped ? lane : i + j, c = pl.swapped ? i + j : lane;
+                    w[j] = f[r * 32 + (((c >> 2) ^ (r & 7)) << 2) + (c & 3)];
+                }
+                finish_column<8, SLOPE>(p, m0 + i, count - i, n, bias, w, lane);
+            }
         }
+        __syncwarp();
     }
-    __syncwarp();
 }
 
+// VEC: the alignment of the epilogue's matrices (Plan::vec).  SLOPE: the
+// epilogue multiplies by an activation's slope.
+template <int VEC, bool SLOPE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                    const __grid_constant__ Product p, const __grid_constant__ Plan pl) {
@@ -377,10 +303,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = bars->tmem_base;
-
     if (warp == 0 && lane == 0) {
         // ---- producer ----
-        const uint32_t bytes = kStageA + pl.bn / 2 * kDepth * 2;
+        const uint32_t bytes = kStageA + (p.b_trans ? (pl.bn > 128 ? 16384 : 8192) : pl.bn / 2 * kDepth * 2);
         uint32_t q = 0;
         bool ok = true;
         for (int64_t u = cluster; u < pl.units && ok; u += clusters) {
@@ -407,7 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tma_load(b, &map_b, k * kDepth, col, full);
                     } else {
                         tma_load(b, &map_b, col, k * kDepth, full);
-                        if (pl.bn == 256) tma_load(b + 8192, &map_b, col + 64, k * kDepth, full);
+                        if (pl.bn > 128) tma_load(b + 8192, &map_b, col + 64, k * kDepth, full);
                     }
                 }
                 bars->issued = q + 1;
@@ -479,67 +404,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int64_t row0 = static_cast<int64_t>(un.tm) * 256 + rank * 128 + quad * 32;
             const int64_t col0 = static_cast<int64_t>(un.tn) * pl.bn;
             const uint32_t src = tmem + buf * 256 + (static_cast<uint32_t>(quad * 32) << 16);
-            if (un.shared < 0) {
-                for (int c = half; c < chunks; c += 2) {
-                    float v[32];
-                    tmem_load32(src + c * 32, v);
-                    if (c + 2 >= chunks) {
-                        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) bar_arrive_remote(remote_addr(smem_addr(&bars->tmem_empty[buf]), 0));
-                    }
-                    finish_chunk(p, pl, row0, col0 + c * 32, v, buf4, lane);
+            // a tile shared along k leaves its sums in the workspace, for finish_kernel
+            float4* sums = un.shared < 0 ? nullptr : pl.sums(un.shared, un.part, static_cast<int>(rank) * kEpiWarps + w) + lane;
+            for (int c = half; c < chunks; c += 2) {
+                float v[32];
+                tmem_load32(src + c * 32, v);
+                if (c + 2 >= chunks) {
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) bar_arrive_remote(remote_addr(smem_addr(&bars->tmem_empty[buf]), 0));
                 }
-                if (half >= chunks && lane == 0) bar_arrive_remote(remote_addr(smem_addr(&bars->tmem_empty[buf]), 0));
-            } else {
-                // a tile shared along k: leave this part's sums in the workspace;
-                // whichever warp comes last for this piece adds them up, in the
-                // order of the parts, and finishes
-                const int piece = static_cast<int>(rank) * kEpiWarps + w;
-                float4* tile_sums = reinterpret_cast<float4*>(pl.partials) +
-                                    (un.shared * pl.parts * kPieces + piece) * static_cast<int64_t>(kPiece / 4);
-                const int64_t part_stride = static_cast<int64_t>(kPieces) * (kPiece / 4);
-                for (int c = half; c < chunks; c += 2) {
-                    float v[32];
-                    tmem_load32(src + c * 32, v);
-                    float4* dst = tile_sums + un.part * part_stride + (c >> 1) * 256 + lane;
+                if (sums != nullptr) {
 #pragma unroll
                     for (int s = 0; s < 8; ++s)
-                        __stcg(dst + s * 32, make_float4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]));
-                }
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                __threadfence();
-                __syncwarp();
-                uint32_t last = 0;
-                if (lane == 0) {
-                    bar_arrive_remote(remote_addr(smem_addr(&bars->tmem_empty[buf]), 0));
-                    uint32_t* counter = pl.counters + un.shared * kPieces + piece;
-                    last = atomicAdd(counter, 1u) == static_cast<uint32_t>(pl.parts - 1);
-                    if (last) *counter = 0;
-                    __threadfence();
-                }
-                last = __shfl_sync(0xffffffffu, last, 0);
-                __syncwarp();
-                if (last) {
-                    for (int c = half; c < chunks; c += 2) {
-                        float v[32];
-                        const float4* q = tile_sums + (c >> 1) * 256 + lane;
-#pragma unroll
-                        for (int s = 0; s < 8; ++s) {
-                            const float4 f = __ldcg(q + s * 32);
-                            v[4 * s] = f.x; v[4 * s + 1] = f.y; v[4 * s + 2] = f.z; v[4 * s + 3] = f.w;
-                        }
-                        for (int j = 1; j < pl.parts; ++j) {
-#pragma unroll
-                            for (int s = 0; s < 8; ++s) {
-                                const float4 f = __ldcg(q + j * part_stride + s * 32);
-                                v[4 * s] += f.x; v[4 * s + 1] += f.y; v[4 * s + 2] += f.z; v[4 * s + 3] += f.w;
-                            }
-                        }
-                        finish_chunk(p, pl, row0, col0 + c * 32, v, buf4, lane);
-                    }
+                        sums[(c >> 1) * 256 + s * 32] = make_float4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]);
+                } else {
+                    finish_chunk<VEC, SLOPE>(p, pl, row0, col0 + c * 32, v, buf4, lane);
                 }
             }
+            if (half >= chunks && lane == 0) bar_arrive_remote(remote_addr(smem_addr(&bars->tmem_empty[buf]), 0));
         }
     }
 
@@ -568,13 +451,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
-// 256 columns and one slice of the rows to a block.
+// Column sums of dy: V columns to a thread (8 from a 16-byte boundary, or 1),
+// 32 threads across and 8 slices of rows down to a block, which joins them and
+// leaves one row of sums.  Eight loads of a thread are in flight at a time.
+template <int V>
 __global__ void __launch_bounds__(256) column_sum_kernel(int64_t rows, int64_t cols, Mat dy, float* partials) {
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (c >= cols) return;
-    float s = 0.0f;
-    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) s += load1(dy.p, dy.dtype, r * dy.ld + c);
-    partials[static_cast<int64_t>(blockIdx.y) * cols + c] = s;
+    __shared__ float part[8][32 * V + 1];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + tx) * V;
+    float s[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[j] = 0.0f;
+    if (c < cols) {
+        const int64_t step = static_cast<int64_t>(gridDim.y) * 8;
+        int64_t r = static_cast<int64_t>(blockIdx.y) * 8 + ty;
+        for (; r + 7 * step < rows; r += 8 * step) {
+            float v[8][V];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) loadv<V>(dy.p, FSDP_DTYPE_BF16, (r + i * step) * dy.ld + c, v[i]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) s[j] += v[i][j];
+        }
+        for (; r < rows; r += step) {
+            float v[V];
+            loadv<V>(dy.p, FSDP_DTYPE_BF16, r * dy.ld + c, v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[j] += v[j];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) part[ty][j * 32 + tx] = s[j];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * V; i += 256) {
+        float t = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t += part[k][i];
+        const int64_t col = (static_cast<int64_t>(blockIdx.x) * 32 + (i & 31)) * V + (i >> 5);
+        if (col < cols) partials[static_cast<int64_t>(blockIdx.y) * cols + col] = t;
+    }
+}
+
+// The shared tiles: the parts' sums in the order of the parts, then the same
+// epilogue; a 32 x 32 chunk to a warp, so that all SMs take part.  (Done by the
+// last cluster to reach a tile instead, the sums of 19 parts took 60 us of its
+// two SMs' time.)
+template <int VEC, bool SLOPE>
+__global__ void __launch_bounds__(128) finish_kernel(const __grid_constant__ Product p, const __grid_constant__ Plan pl) {
+    __shared__ float4 buf[4][256];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, chunks = pl.bn / 32;
+    const int64_t job = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    const int64_t shared = job / (8 * chunks);
+    const int in = static_cast<int>(job - shared * 8 * chunks), c = in >> 3, rank = in >> 2 & 1, quad = in & 3;
+    if (pl.whole + shared >= static_cast<int64_t>(pl.tiles_m) * pl.tiles_n) return;
+    int tm, tn;
+    place_tile(pl, pl.whole + shared, &tm, &tn);
+    const float4* q = pl.sums(shared, 0, rank * kEpiWarps + (c & 1) * 4 + quad) + (c >> 1) * 256 + lane;
+    const int64_t next = static_cast<int64_t>(kPieces) * (kPiece / 4);
+    float v[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+#pragma unroll 2
+    for (int j = 0; j < pl.parts; ++j) {
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const float4 f = __ldcg(q + j * next + s * 32);
+            v[4 * s] += f.x; v[4 * s + 1] += f.y; v[4 * s + 2] += f.z; v[4 * s + 3] += f.w;
+        }
+    }
+    finish_chunk<VEC, SLOPE>(p, pl, static_cast<int64_t>(tm) * 256 + rank * 128 + quad * 32,
+                             static_cast<int64_t>(tn) * pl.bn + c * 32, v, buf[threadIdx.x >> 5], lane);
 }
 
 // Rows of a bf16 matrix that do not start on 16-byte boundaries, copied to
@@ -635,15 +583,16 @@ cudaError_t make_map(CUtensorMap* map, const Mat& m, int64_t rows, int64_t cols,
 }
 
 // Tiles, and how the last ones are shared: the clusters take whole tiles in
-// turn; what is left over after the last full round is cut along k so that
-// every cluster has a part.  The width is the one with the least estimated
-// time; a stage of 64 k takes 2 cycles a column on the tensor cores, and the
-// copies 16 KiB + 64 bytes a column at about 56 bytes a cycle.
+// turn; what is left over after the last full round may be cut along k so that
+// every cluster has a part.  The width and the choice are those of the least
+// estimated time, in cycles: a stage of 64 k takes 2 a column on the tensor
+// cores, and its copies' bytes at kCopyRate a cycle.
+constexpr double kCopyRate = 60.0;
+
 Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, int clusters) {
     Plan best{};
     double least = 0;
     for (int bn = 256; bn >= 32; bn -= 32) {
-        if (b_by_rows && bn != 256 && bn != 128) continue;
         if (bn < 256 && bn >= 2 * cols && bn > 32) continue;
         Plan p{};
         p.ks = static_cast<int>((k + kDepth - 1) / kDepth);
@@ -651,21 +600,35 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, int clu
         p.tiles_m = static_cast<int>((rows + 255) / 256);
         p.tiles_n = static_cast<int>((cols + bn - 1) / bn);
         const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-        const int64_t left = tiles % clusters;
-        p.parts = left == 0 ? 1 : static_cast<int>(std::min<int64_t>(clusters / left, std::max(1, p.ks / 4)));
-        p.whole = p.parts > 1 ? tiles - left : tiles;
-        p.units = p.whole + (tiles - p.whole) * p.parts;
-        const double stage = std::max(2.0 * bn, (16384.0 + 64.0 * bn) / 56.0);
-        const double rounds = static_cast<double>((p.whole + clusters - 1) / clusters);
-        double t = rounds * (p.ks * stage + 300.0) + 3.0 * bn + 2000.0;
-        if (p.parts > 1) t += (p.ks / p.parts + 1) * stage + 2500.0 + 60.0 * p.parts * bn / 32;
-        if (least == 0 || t < least) {
-            least = t;
-            best = p;
+        const double copied = 16384.0 + (b_by_rows ? (bn > 128 ? 16384.0 : 8192.0) : 64.0 * bn);
+        const double stage = std::max(2.0 * bn, copied / kCopyRate);
+        const double tail = 8.0 * bn + 1500.0;   // the last tile's epilogue, and the kernel's start and end
+        for (int share = 0; share < 2; ++share) {
+            const int64_t left = tiles % clusters;
+            p.parts = share == 0 || left == 0 ? 1 : static_cast<int>(std::min<int64_t>(clusters / left, std::max(1, p.ks / 4)));
+            if (share == 1 && p.parts == 1) continue;
+            p.whole = p.parts > 1 ? tiles - left : tiles;
+            p.units = p.whole + (tiles - p.whole) * p.parts;
+            const double rounds = static_cast<double>((p.whole + clusters - 1) / clusters);
+            double t = rounds * std::max(p.ks * stage, 24.0 * bn) + tail;
+            if (p.parts > 1) t += (p.ks / p.parts + 1) * stage + 6500.0 + 150.0 * p.parts;
+            if (least == 0 || t < least) {
+                least = t;
+                best = p;
+            }
         }
     }
     return best;
 }
+
+using FinishKernel = void (*)(Product, Plan);
+const FinishKernel kFinishKernels[2][3] = {
+    {finish_kernel<0, false>, finish_kernel<1, false>, finish_kernel<2, false>},
+    {finish_kernel<0, true>, finish_kernel<1, true>, finish_kernel<2, true>}};
+using ProductKernel = void (*)(CUtensorMap, CUtensorMap, Product, Plan);
+const ProductKernel kProductKernels[2][3] = {
+    {product_kernel<0, false>, product_kernel<1, false>, product_kernel<2, false>},
+    {product_kernel<0, true>, product_kernel<1, true>, product_kernel<2, true>}};
 
 }  // namespace
 
@@ -673,13 +636,15 @@ int product_clusters(int sms) {
     static std::once_flag once;
     static int most = 0;
     std::call_once(once, [] {
-        if (cudaFuncSetAttribute(product_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) return;
+        for (const ProductKernel* row : kProductKernels)
+            for (int i = 0; i < 3; ++i)
+                if (cudaFuncSetAttribute(row[i], cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) return;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(2 * kMaxClusters);
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = kSmemBytes;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, product_kernel, &cfg) == cudaSuccess) most = n;
+        if (cudaOccupancyMaxActiveClusters(&n, kProductKernels[0][0], &cfg) == cudaSuccess) most = n;
     });
     return std::min(std::min(most, sms / 2), kMaxClusters);
 }
@@ -722,6 +687,7 @@ cudaError_t launch_product(const Product& given, const ProductRoom& room, int sm
         const size_t esz = p.out.dtype == FSDP_DTYPE_F32 ? 4 : 2;
         return cudaMemset2DAsync(p.out.p, p.out.ld * esz, 0, p.N * esz, p.M, st);
     }
+    if (few_rows(p)) return launch_few_rows(p, sms, st);
     const int clusters = product_clusters(sms);
     if (clusters < 1) return cudaErrorNotSupported;
     char* copies = room.copies;
@@ -729,8 +695,12 @@ cudaError_t launch_product(const Product& given, const ProductRoom& room, int sm
     if (e == cudaSuccess) e = settle(&p.b, p.b_trans ? p.K : p.N, p.b_trans ? p.N : p.K, &copies, sms, st);
     if (e != cudaSuccess) return e;
 
-    const bool vec = p.N % 8 == 0 && rows_aligned(p.out) && (p.add.p == nullptr || rows_aligned(p.add)) &&
-                     (p.pre.p == nullptr || rows_aligned(p.pre));
+    const auto all_aligned = [&](uintptr_t to) {
+        for (const Mat* m : {&p.out, &p.add, &p.pre})
+            if (m->p != nullptr && !rows_aligned(*m, to)) return false;
+        return p.N % static_cast<int64_t>(to / 2) == 0;
+    };
+    const int vec = all_aligned(32) && (reinterpret_cast<uintptr_t>(p.bias) & 15u) == 0 ? 2 : all_aligned(16) ? 1 : 0;
     // Few rows: they become the tile's columns, so that a tile of 256 is not
     // filled with rows that do not exist.
     int64_t rows = p.M, cols = p.N;
@@ -742,9 +712,8 @@ cudaError_t launch_product(const Product& given, const ProductRoom& room, int sm
     }
     Plan pl = plan_product(rows, cols, p.K, p.b_trans, clusters);
     pl.swapped = swap;
-    pl.vec = vec && !swap;
+    pl.vec = swap ? 0 : vec;
     pl.partials = room.partials;
-    pl.counters = room.counters;
     pl.status = room.status;
     pl.wait_cycles = static_cast<long long>(room.wait_ns) * 2;   // the SM clock is at most 2.07 GHz
     pl.withhold = room.withhold;
@@ -753,13 +722,26 @@ cudaError_t launch_product(const Product& given, const ProductRoom& room, int sm
     if (e == cudaSuccess) e = p.b_trans ? make_map(&map_b, p.b, p.K, cols, 64) : make_map(&map_b, p.b, cols, p.K, pl.bn / 2);
     if (e != cudaSuccess) return e;
     const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(pl.units, clusters));
-    product_kernel<<<grid, kThreads, kSmemBytes, st>>>(map_a, map_b, p, pl);
-    return cudaGetLastError();
+    kProductKernels[p.slope][pl.vec]<<<grid, kThreads, kSmemBytes, st>>>(map_a, map_b, p, pl);
+    e = cudaGetLastError();
+    const int64_t shared = static_cast<int64_t>(pl.tiles_m) * pl.tiles_n - pl.whole;
+    if (e != cudaSuccess || shared == 0) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>((shared * 8 * (pl.bn / 32) + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cudaLaunchAttribute early{};   // its launch overlaps the product's end; it waits for all of it before it reads
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kFinishKernels[p.slope][pl.vec], p, pl);
 }
 
 int64_t column_sum_partials(int64_t rows, int64_t cols, int sms) {
+    // about two blocks to an SM, of at least 32 rows each
     const int64_t blocks = (cols + 255) / 256;
-    return std::max<int64_t>(1, std::min<int64_t>(rows, std::min<int64_t>(256, (4 * sms + blocks - 1) / blocks)));
+    return std::max<int64_t>(1, std::min<int64_t>((rows + 31) / 32, (2 * sms + blocks - 1) / blocks));
 }
 
 cudaError_t launch_column_sum(int64_t rows, int64_t cols, const Mat& dy, float* partials, void* out, int out_dtype,
@@ -767,8 +749,12 @@ cudaError_t launch_column_sum(int64_t rows, int64_t cols, const Mat& dy, float* 
     int64_t count = 0;
     if (rows > 0) {
         count = column_sum_partials(rows, cols, sms);
-        const dim3 grid(static_cast<unsigned>((cols + 255) / 256), static_cast<unsigned>(count));
-        column_sum_kernel<<<grid, 256, 0, st>>>(rows, cols, dy, partials);
+        if (rows_aligned(dy) && cols % 8 == 0)
+            column_sum_kernel<8><<<dim3(static_cast<unsigned>((cols + 255) / 256), static_cast<unsigned>(count)), 256, 0, st>>>(
+                rows, cols, dy, partials);
+        else
+            column_sum_kernel<1><<<dim3(static_cast<unsigned>((cols + 31) / 32), static_cast<unsigned>(count)), 256, 0, st>>>(
+                rows, cols, dy, partials);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }

@@ -456,8 +456,14 @@ def test_refusals_change_nothing(handle):
     small.close()
     # raw views: null data, short ld, misaligned data, an ACT8 ld that is not the format's
     lib, ok = B.lib(), B._mat(x)
-    m = lambda t, **k: B.Matrix(*[k.get(f, getattr(B._mat(t), f)) for f, _ in B.Matrix._fields_])  # noqa: E731
-    out = B._mat(y)
+
+    def m(t, **changes):
+        v = B.Matrix.from_buffer_copy(B._mat(t))
+        for field, value in changes.items():
+            setattr(v, field, value)
+        return bytes(v)
+
+    out = m(y)
     call = lambda a, b: lib.fsdp_act8_unpack(handle.handle, a, 0, b, None)  # noqa: E731
     k = B.Act8(4, 64)
     assert call(m(k, data=None), out) == bad and call(m(k, exps=None), out) == bad
