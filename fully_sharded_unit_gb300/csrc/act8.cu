@@ -1,132 +1,107 @@
 // 8-bit activation checkpoints: pack (quantise) and unpack.  Streaming passes,
 // bound by DRAM: pack reads 2 or 4 bytes and writes 33/32 byte an element,
 // unpack the reverse.
+#include <algorithm>
+
 #include "block_device.cuh"
 #include "compute.hpp"
+#include "epilogue.cuh"
 
 namespace fsdp {
 namespace {
 
-// Work is cut into items of 32*V consecutive columns of one row, one item to a
-// warp at a time.  A warp walks items w, w + W, w + 2W, ... and keeps its row
-// and segment by adding (W / segs, W % segs), so no division runs in the loop.
-struct Items {
-    int64_t count;      // rows * segs
-    int64_t segs;       // items in a row
-    int64_t step_row;   // W / segs
-    int64_t step_seg;   // W % segs
-};
-
-template <int V, int U>
-__global__ void __launch_bounds__(256) act8_pack_kernel(int64_t cols, Mat x, Mat q, Items it) {
-    const int lane = threadIdx.x & 31;
-    const int64_t W = static_cast<int64_t>(gridDim.x) * 8;
-    int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    int64_t row = i / it.segs, seg = i % it.segs;
-    while (i < it.count) {
-        float v[U][V];
-        int64_t rows[U], c[U];
-        bool on[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            rows[u] = row;
-            c[u] = (seg * 32 + lane) * V;
-            on[u] = i < it.count;
-            // cols is a multiple of 8 where V = 8
-            if (on[u] && c[u] < cols) {
-                loadv<V>(x.p, x.dtype, row * x.ld + c[u], v[u]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[u][j] = 0.0f;
-            }
-            i += W;
-            row += it.step_row;
-            seg += it.step_seg;
-            if (seg >= it.segs) { seg -= it.segs; ++row; }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t byte = act8_group_byte<V>(v[u]);
-            if (on[u] && c[u] < q.ld) {
-                act8_writev<V>(static_cast<uint8_t*>(q.p) + rows[u] * q.ld, c[u], v[u], byte);
-                if ((lane & (32 / V - 1)) == 0) q.e[rows[u] * q.eld + (c[u] >> 5)] = static_cast<uint8_t>(byte);
-            }
+// A whole group to a lane: 32 elements hide each other's latency, the largest
+// magnitude needs no exchange between lanes, and loads, payload and exponents
+// are whole sectors.  The payload's rows and the exponents' are contiguous
+// (their strides are the format's), so a group's place in them is its index.
+template <bool WIDE, bool PACK>
+__global__ void __launch_bounds__(256) act8_groups_kernel(int64_t cols, Mat q, int act, Mat x, int64_t count, uint32_t groups) {
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
+    for (int64_t g = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; g < count; g += stride) {
+        // a 32-bit division where the index allows it
+        const int64_t row = g <= 0xffffffffll ? static_cast<uint32_t>(g) / groups : g / groups;
+        const int64_t n = (g - row * groups) * kGroup;
+        const int left = static_cast<int>(min(static_cast<int64_t>(kGroup), cols - n));
+        float v[32];
+        if (PACK) {
+            load_row32<WIDE>(x, row, n, left, v);
+            store_row32<WIDE>(q, row, n, left, v);
+        } else {
+            load_row32<WIDE>(q, row, n, left, v);
+            activate_n<32>(v, act);
+            store_row32<WIDE>(x, row, n, left, v);
         }
     }
 }
 
-template <int V, int U>
-__global__ void __launch_bounds__(256) act8_unpack_kernel(int64_t cols, Mat q, int act, Mat out, Items it) {
+// Rows that start anywhere: a group to a warp, an element to a lane, U groups
+// in flight.
+template <bool PACK>
+__global__ void __launch_bounds__(256) act8_elements_kernel(int64_t cols, Mat q, int act, Mat x, int64_t count, uint32_t groups) {
+    constexpr int U = 4;
     const int lane = threadIdx.x & 31;
-    const int64_t W = static_cast<int64_t>(gridDim.x) * 8;
-    int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    int64_t row = i / it.segs, seg = i % it.segs;
-    while (i < it.count) {
-        float v[U][V];
-        int64_t rows[U], c[U];
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * 8;
+    for (int64_t g0 = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); g0 < count; g0 += stride * U) {
+        float v[U];
+        int64_t row[U], n[U];
         bool on[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            rows[u] = row;
-            c[u] = (seg * 32 + lane) * V;
-            on[u] = i < it.count && c[u] < cols;
-            if (on[u])
-                act8_readv<V>(static_cast<const uint8_t*>(q.p) + row * q.ld, q.e + row * q.eld, c[u], v[u]);
-            i += W;
-            row += it.step_row;
-            seg += it.step_seg;
-            if (seg >= it.segs) { seg -= it.segs; ++row; }
+            const int64_t g = g0 + u * stride;
+            row[u] = g <= 0xffffffffll ? static_cast<uint32_t>(g) / groups : g / groups;
+            n[u] = (g - row[u] * groups) * kGroup + lane;
+            on[u] = g < count && n[u] < cols;
+            v[u] = 0.0f;
+            if (on[u]) {
+                if (PACK) v[u] = load1(x.p, x.dtype, row[u] * x.ld + n[u]);
+                else act8_readv<1>(static_cast<const uint8_t*>(q.p) + row[u] * q.ld, q.e + row[u] * q.eld, n[u], &v[u]);
+            }
         }
+        if (PACK) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (!on[u]) continue;
+            for (int u = 0; u < U; ++u) {
+                const uint32_t top = act8_group_top<1>(&v[u]);
+                if (g0 + u * stride < count) {
+                    act8_writev<1>(static_cast<uint8_t*>(q.p) + row[u] * q.ld, n[u], &v[u], top);
+                    if (lane == 0) q.e[row[u] * q.eld + (n[u] >> 5)] = static_cast<uint8_t>(act8_byte(top));
+                }
+            }
+        } else {
+            activate_n<U>(v, act);
 #pragma unroll
-            for (int j = 0; j < V; ++j) v[u][j] = activate(v[u][j], act);
-            storev<V>(out.p, out.dtype, rows[u] * out.ld + c[u], v[u]);
+            for (int u = 0; u < U; ++u)
+                if (on[u]) store1(x.p, x.dtype, row[u] * x.ld + n[u], v[u]);
         }
     }
 }
 
-Items plan_items(int64_t rows, int64_t cols, int per_warp, int sms, int U, int* blocks) {
-    Items it;
-    it.segs = (cols + per_warp - 1) / per_warp;
-    it.count = rows * it.segs;
-    const int64_t want = (it.count + 8 * U - 1) / (8 * U);
-    const int64_t most = static_cast<int64_t>(sms) * 8;
-    *blocks = static_cast<int>(want < most ? want : most);
-    const int64_t W = static_cast<int64_t>(*blocks) * 8;
-    it.step_row = W / it.segs;
-    it.step_seg = W % it.segs;
-    return it;
+template <bool PACK>
+cudaError_t launch(int64_t rows, int64_t cols, const Mat& q, int act, const Mat& x, int sms, cudaStream_t st) {
+    if (rows == 0) return cudaSuccess;
+    const int64_t groups = act8_groups(cols), count = rows * groups;
+    if (groups > 0xffffffffll) return cudaErrorInvalidValue;
+    const auto blocks = [&](int64_t per_block) {
+        return static_cast<unsigned>(std::min((count + per_block - 1) / per_block, static_cast<int64_t>(sms) * 24));
+    };
+    const uint32_t gr = static_cast<uint32_t>(groups);
+    if (rows_aligned(x, 32) && rows_aligned(q, 32) && cols % 16 == 0)
+        act8_groups_kernel<true, PACK><<<blocks(256), 256, 0, st>>>(cols, q, act, x, count, gr);
+    else if (rows_aligned(x) && cols % 8 == 0)
+        act8_groups_kernel<false, PACK><<<blocks(256), 256, 0, st>>>(cols, q, act, x, count, gr);
+    else
+        act8_elements_kernel<PACK><<<blocks(32), 256, 0, st>>>(cols, q, act, x, count, gr);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_act8_pack(int64_t rows, int64_t cols, const Mat& x, const Mat& q, int sms, cudaStream_t st) {
-    if (rows == 0) return cudaSuccess;
-    int blocks = 0;
-    if (rows_aligned(x) && cols % 8 == 0) {
-        const Items it = plan_items(rows, cols, 256, sms, 4, &blocks);
-        act8_pack_kernel<8, 4><<<blocks, 256, 0, st>>>(cols, x, q, it);
-    } else {
-        const Items it = plan_items(rows, cols, 32, sms, 8, &blocks);
-        act8_pack_kernel<1, 8><<<blocks, 256, 0, st>>>(cols, x, q, it);
-    }
-    return cudaGetLastError();
+    return launch<true>(rows, cols, q, 0, x, sms, st);
 }
 
 cudaError_t launch_act8_unpack(int64_t rows, int64_t cols, const Mat& q, int activation, const Mat& out, int sms,
                                cudaStream_t st) {
-    if (rows == 0) return cudaSuccess;
-    int blocks = 0;
-    if (rows_aligned(out) && cols % 8 == 0) {
-        const Items it = plan_items(rows, cols, 256, sms, 4, &blocks);
-        act8_unpack_kernel<8, 4><<<blocks, 256, 0, st>>>(cols, q, activation, out, it);
-    } else {
-        const Items it = plan_items(rows, cols, 32, sms, 8, &blocks);
-        act8_unpack_kernel<1, 8><<<blocks, 256, 0, st>>>(cols, q, activation, out, it);
-    }
-    return cudaGetLastError();
+    return launch<false>(rows, cols, q, activation, out, sms, st);
 }
 
 }  // namespace fsdp

@@ -118,9 +118,13 @@ __device__ __forceinline__ void store32b(void* p, const uint32_t* w) {
 
 // ---- ACT8 ----
 
-// The magnitude bits of a float compare like the magnitudes; an infinity or a
-// NaN compares above every finite value.
-__device__ __forceinline__ uint32_t mag_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// Larger magnitude of the two, as a non-negative float; NaN if either is.  Its
+// bits order like the magnitudes, an infinity's and a NaN's above all others.
+__device__ __forceinline__ float larger(float top, float x) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(top), "f"(fabsf(x)));
+    return r;
+}
 
 // The exponent byte of a group from its largest magnitude's bits: the biased
 // exponent itself, at least 7 (so that 2^(6-E) and 2^(E-6) are normal floats).
@@ -137,24 +141,39 @@ __device__ __forceinline__ float act8_step(uint32_t byte) {
     return __uint_as_float(byte == 255u ? 0x7fc00000u : (max(byte, 7u) - 6u) << 23);
 }
 
-// x * 2^(6-E) rounded to nearest even and clamped to +-127, as the low byte of
-// the result.  The product is exact (a power of two), so adding 1.5 * 2^23 in
-// the same fma rounds it once, at the integers.
+// x * 2^(6-E) rounded to nearest even (and clamped to +-127), as the low byte
+// of the result.  The product is exact (a power of two), so adding 1.5 * 2^23
+// in the same fma rounds it once, at the integers.
+constexpr float kMagic = 12582912.0f;
 __device__ __forceinline__ uint32_t act8_quant(float x, float scale) {
-    const float magic = 12582912.0f;
-    const float t = fminf(fmaxf(fmaf(x, scale, magic), magic - 127.0f), magic + 127.0f);
-    return __float_as_uint(t);
+    return __float_as_uint(fminf(fmaxf(fmaf(x, scale, kMagic), kMagic - 127.0f), kMagic + 127.0f));
 }
 
 __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-__device__ __forceinline__ uint2 act8_quant8(const float* v, float scale) {
-    uint32_t q[8];
+// N/4 words of N values whose largest magnitude has the bits `top`.  Only a
+// group whose largest value rounds to 128 steps needs the clamp (one in a few
+// hundred), so the others leave its two instructions an element out.
+template <int N>
+__device__ __forceinline__ void act8_quant_n(const float* v, uint32_t top, float scale, uint32_t* w) {
+    if (__uint_as_float(top) * scale < 127.5f) {
+        const f32x2 s = pair(scale, scale), m = pair(kMagic, kMagic);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = act8_quant(v[j], scale);
-    return make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+        for (int i = 0; i < N / 4; ++i) {
+            float a, b, c, d;
+            unpair(fma2(pair(v[4 * i], v[4 * i + 1]), s, m), a, b);
+            unpair(fma2(pair(v[4 * i + 2], v[4 * i + 3]), s, m), c, d);
+            w[i] = pack4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+        }
+    } else {   // also a group that is not finite: its scale is 0 and its words become 0
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i)
+            w[i] = scale == 0.0f ? 0u
+                                 : pack4(act8_quant(v[4 * i], scale), act8_quant(v[4 * i + 1], scale),
+                                         act8_quant(v[4 * i + 2], scale), act8_quant(v[4 * i + 3], scale));
+    }
 }
 
 // Four int8 values of a word times `step`: the byte plus 128 goes into the
@@ -179,31 +198,34 @@ __device__ __forceinline__ void act8_readv(const uint8_t* q, const uint8_t* e, i
     }
 }
 
-// Quantise V consecutive elements per lane; the 32/V lanes that hold a group
-// are consecutive and all take part (elements past the row's end are 0).
-// Returns the group's exponent byte.
+// The bits of the largest magnitude of a group whose V consecutive elements lie
+// in each of 32/V consecutive lanes, which all take part (elements past the
+// row's end are 0).
 template <int V>
-__device__ __forceinline__ uint32_t act8_group_byte(const float* v) {
-    uint32_t top = 0;
+__device__ __forceinline__ uint32_t act8_group_top(const float* v) {
+    float most = 0.0f;
 #pragma unroll
-    for (int j = 0; j < V; ++j) top = max(top, mag_bits(v[j]));
+    for (int j = 0; j < V; ++j) most = larger(most, v[j]);
+    uint32_t top = __float_as_uint(most);
     if constexpr (V == 1) {
         top = __reduce_max_sync(0xffffffffu, top);
     } else {
 #pragma unroll
         for (int d = 1; d < 32 / V; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
     }
-    return act8_byte(top);
+    return top;
 }
 
+// V elements into the payload, at column c of the row at q.
 template <int V>
-__device__ __forceinline__ void act8_writev(uint8_t* q, int64_t c, const float* v, uint32_t byte) {
-    const float scale = act8_scale(byte);
+__device__ __forceinline__ void act8_writev(uint8_t* q, int64_t c, const float* v, uint32_t top) {
+    const float scale = act8_scale(act8_byte(top));
     if constexpr (V == 8) {
-        const uint2 w = act8_quant8(v, scale);
-        *reinterpret_cast<uint2*>(q + c) = byte == 255u ? make_uint2(0, 0) : w;
+        uint32_t w[2];
+        act8_quant_n<8>(v, top, scale, w);
+        *reinterpret_cast<uint2*>(q + c) = make_uint2(w[0], w[1]);
     } else {
-        q[c] = byte == 255u ? 0 : static_cast<uint8_t>(act8_quant(v[0], scale));
+        q[c] = scale == 0.0f ? 0 : static_cast<uint8_t>(act8_quant(v[0], scale));
     }
 }
 

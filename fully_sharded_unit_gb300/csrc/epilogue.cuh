@@ -94,19 +94,16 @@ __device__ __forceinline__ void store_row32(const Mat& x, int64_t m, int64_t n, 
                 if (s * 8 < left) store8(dst, FSDP_DTYPE_BF16, s * 8, v + s * 8);
         }
     } else {   // a checkpoint's group, in one lane
-        uint32_t top = 0;
+        float most = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) top = max(top, j < left ? mag_bits(v[j]) : 0u);
-        const uint32_t byte = act8_byte(top);
-        const float scale = act8_scale(byte);
+        for (int j = 0; j < 32; ++j) most = j < left ? larger(most, v[j]) : most;
+        const uint32_t top = __float_as_uint(most);
         uint32_t w[8];
+        act8_quant_n<32>(v, top, act8_scale(act8_byte(top)), w);
+        if (left < 32) {   // the pad of a short group is zeros
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            // a group that is not finite, and the pad of a short one, are zeros
-            w[s] = byte == 255u || s * 4 >= left
-                       ? 0u
-                       : pack4(act8_quant(v[4 * s], scale), act8_quant(v[4 * s + 1], scale),
-                               act8_quant(v[4 * s + 2], scale), act8_quant(v[4 * s + 3], scale));
+            for (int s = 0; s < 8; ++s)
+                if (s * 4 >= left) w[s] = 0u;
         }
         uint8_t* dst = static_cast<uint8_t*>(x.p) + m * x.ld + n;
         if (WIDE) {
@@ -115,7 +112,7 @@ __device__ __forceinline__ void store_row32(const Mat& x, int64_t m, int64_t n, 
             reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
             reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
-        x.e[m * x.eld + (n >> 5)] = static_cast<uint8_t>(byte);
+        x.e[m * x.eld + (n >> 5)] = static_cast<uint8_t>(act8_byte(top));
     }
 }
 
@@ -177,10 +174,10 @@ __device__ __forceinline__ void finish_column(const Product& p, int64_t m, int c
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
                     const float x = on ? v[i] : 0.0f;
-                    const uint32_t byte = act8_group_byte<1>(&x);
+                    const uint32_t top = act8_group_top<1>(&x);
                     if (i < count && n < p.pre.ld) {
-                        act8_writev<1>(static_cast<uint8_t*>(p.pre.p) + (m + i) * p.pre.ld, n, &x, byte);
-                        if (lane == 0) p.pre.e[(m + i) * p.pre.eld + (n >> 5)] = static_cast<uint8_t>(byte);
+                        act8_writev<1>(static_cast<uint8_t*>(p.pre.p) + (m + i) * p.pre.ld, n, &x, top);
+                        if (lane == 0) p.pre.e[(m + i) * p.pre.eld + (n >> 5)] = static_cast<uint8_t>(act8_byte(top));
                     }
                 }
             } else {

@@ -18,7 +18,19 @@ namespace cg = cooperative_groups;
 namespace fsdp {
 namespace {
 
+// One row by columns keeps more of W in flight with 16 warps; by rows, 8 warps
+// of 4 columns make up a block's 32.
+__host__ __device__ constexpr int few_threads(int T, bool by_columns) { return T == 1 && by_columns ? 512 : 256; }
+
 __device__ __forceinline__ float bf(uint16_t w) { return __uint_as_float(static_cast<uint32_t>(w) << 16); }
+
+// The first `left` (0 or fewer: none) of eight elements, the others 0.
+__device__ __forceinline__ uint4 load_end(const uint16_t* src, int64_t left) {
+    uint32_t w[4] = {0, 0, 0, 0};
+    for (int i = 0; i < 8; ++i)
+        if (i < left) w[i >> 1] |= static_cast<uint32_t>(src[i]) << (16 * (i & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
 // W contiguous along the columns (p.b_trans): V columns and 8 rows of W to a
 // thread at a time.
@@ -35,7 +47,7 @@ __device__ __forceinline__ void sums_by_columns(const Product& p, int64_t n0, in
     for (int t = 0; t < T; ++t)
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[t][j] = 0.0f;
-    for (int64_t k = k0 + (warp * kDown + lane / kAcross) * 8; k < k1; k += 8 * kDown * 8) {
+    for (int64_t k = k0 + (warp * kDown + lane / kAcross) * 8; k < k1; k += (blockDim.x >> 5) * kDown * 8) {
         uint4 w8[8];
         uint16_t w1[8];
 #pragma unroll
@@ -89,35 +101,51 @@ __device__ __forceinline__ void sums_by_rows(const Product& p, int64_t n0, int64
     for (int t = 0; t < T; ++t)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[t][j] = 0.0f;
-#pragma unroll 2
-    for (int64_t k = k0 + lane * V; k < k1; k += 32 * V) {
-        float w[4][V];
-        const bool whole = V == 1 || k + V <= k1;
+    if constexpr (V == 8) {
+        // two steps of k at a time: eight loads of W in flight to a lane
+        for (int64_t k = k0 + lane * 8; k < k1; k += 512) {
+            uint4 w[2][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + warp * 4 + j;
-            const uint16_t* src = W + n * p.b.ld + k;
-            if (n < p.N && whole && V == 8) {
-                unpack8(__ldg(reinterpret_cast<const uint4*>(src)), w[j]);
-            } else {
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int i = 0; i < V; ++i) w[j][i] = n < p.N && k + i < k1 ? bf(__ldg(src + i)) : 0.0f;
-            }
+                for (int j = 0; j < 4; ++j) {
+                    const int64_t n = n0 + warp * 4 + j, kk = k + u * 256;
+                    w[u][j] = n < p.N && kk + 8 <= k1 ? __ldg(reinterpret_cast<const uint4*>(W + n * p.b.ld + kk))
+                                                      : load_end(W + n * p.b.ld + kk, n < p.N ? k1 - kk : 0);
+                }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int t = 0; t < T; ++t) {
+                    const int64_t kk = k + u * 256;
+                    const uint16_t* src = X + t * p.a.ld + kk;
+                    float x[8];
+                    unpack8(t < p.M && kk + 8 <= k1 ? __ldg(reinterpret_cast<const uint4*>(src))
+                                                    : load_end(src, t < p.M ? k1 - kk : 0), x);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float v[8];
+                        unpack8(w[u][j], v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) acc[t][j] = fmaf(x[i], v[i], acc[t][j]);
+                    }
+                }
         }
+    } else {
+#pragma unroll 4
+        for (int64_t k = k0 + lane; k < k1; k += 32) {
+            float w[4];
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
-            float x[V];
-            const uint16_t* src = X + t * p.a.ld + k;
-            if (t < p.M && whole && V == 8) {
-                unpack8(__ldg(reinterpret_cast<const uint4*>(src)), x);
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) x[i] = t < p.M && k + i < k1 ? bf(__ldg(src + i)) : 0.0f;
+            for (int j = 0; j < 4; ++j) {
+                const int64_t n = n0 + warp * 4 + j;
+                w[j] = n < p.N ? bf(__ldg(W + n * p.b.ld + k)) : 0.0f;
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int t = 0; t < T; ++t) {
+                const float x = t < p.M ? bf(__ldg(X + t * p.a.ld + k)) : 0.0f;
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[t][j] = fmaf(x[i], w[j][i], acc[t][j]);
+                for (int j = 0; j < 4; ++j) acc[t][j] = fmaf(x, w[j], acc[t][j]);
+            }
         }
     }
 #pragma unroll
@@ -132,8 +160,9 @@ __device__ __forceinline__ void sums_by_rows(const Product& p, int64_t n0, int64
 }
 
 template <int V, int T, bool BY_COLUMNS>
-__global__ void __launch_bounds__(256) few_rows_kernel(const __grid_constant__ Product p) {
-    __shared__ float part[8][T][33];
+__global__ void __launch_bounds__(few_threads(T, BY_COLUMNS)) few_rows_kernel(const __grid_constant__ Product p) {
+    constexpr int kWarps = few_threads(T, BY_COLUMNS) / 32;
+    __shared__ float part[kWarps][T][33];
     __shared__ float total[T][33];
     cg::cluster_group cluster = cg::this_cluster();
     const int parts = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
@@ -144,12 +173,12 @@ __global__ void __launch_bounds__(256) few_rows_kernel(const __grid_constant__ P
     if constexpr (BY_COLUMNS) sums_by_columns<V, T>(p, n0, k0, k1, part);
     else sums_by_rows<V, T>(p, n0, k0, k1, part);
     __syncthreads();
-    for (int i = threadIdx.x; i < T * 32; i += 256) {
+    for (int i = threadIdx.x; i < T * 32; i += kWarps * 32) {
         const int t = i >> 5, c = i & 31;
         float s = part[0][t][c];
         if constexpr (BY_COLUMNS) {
 #pragma unroll
-            for (int w = 1; w < 8; ++w) s += part[w][t][c];
+            for (int w = 1; w < kWarps; ++w) s += part[w][t][c];
         }
         total[t][c] = s;
     }
@@ -174,7 +203,8 @@ __global__ void __launch_bounds__(256) few_rows_kernel(const __grid_constant__ P
 }
 
 template <int V, int T>
-cudaError_t run(const Product& p, const cudaLaunchConfig_t& cfg) {
+cudaError_t run(const Product& p, cudaLaunchConfig_t& cfg) {
+    cfg.blockDim = dim3(few_threads(T, p.b_trans != 0));
     return p.b_trans ? cudaLaunchKernelEx(&cfg, few_rows_kernel<V, T, true>, p)
                      : cudaLaunchKernelEx(&cfg, few_rows_kernel<V, T, false>, p);
 }
@@ -192,7 +222,6 @@ cudaError_t launch_few_rows(const Product& p, int sms, cudaStream_t st) {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks * parts));
-    cfg.blockDim = dim3(256);
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;

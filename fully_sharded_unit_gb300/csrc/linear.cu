@@ -610,7 +610,7 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, int clu
             p.whole = p.parts > 1 ? tiles - left : tiles;
             p.units = p.whole + (tiles - p.whole) * p.parts;
             const double rounds = static_cast<double>((p.whole + clusters - 1) / clusters);
-            double t = rounds * std::max(p.ks * stage, 24.0 * bn) + tail;
+            double t = rounds * std::max(p.ks * stage, 2500.0 + 10.0 * bn) + tail;
             if (p.parts > 1) t += (p.ks / p.parts + 1) * stage + 6500.0 + 150.0 * p.parts;
             if (least == 0 || t < least) {
                 least = t;

@@ -75,10 +75,10 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_forward_kernel(NormFor
         for (int k = 0; k < NV; ++k) {
             const int64_t c = static_cast<int64_t>(t + k * threads) * V;
             if (a.ckpt.p != nullptr) {
-                const uint32_t byte = act8_group_byte<V>(v[k]);
+                const uint32_t top = act8_group_top<V>(v[k]);
                 if (c < a.ckpt.ld) {
-                    act8_writev<V>(static_cast<uint8_t*>(a.ckpt.p) + row * a.ckpt.ld, c, v[k], byte);
-                    if ((t & (32 / V - 1)) == 0) a.ckpt.e[row * a.ckpt.eld + (c >> 5)] = static_cast<uint8_t>(byte);
+                    act8_writev<V>(static_cast<uint8_t*>(a.ckpt.p) + row * a.ckpt.ld, c, v[k], top);
+                    if ((t & (32 / V - 1)) == 0) a.ckpt.e[row * a.ckpt.eld + (c >> 5)] = static_cast<uint8_t>(act8_byte(top));
                 }
             }
             if (c < a.cols) {
@@ -117,9 +117,9 @@ __global__ void __launch_bounds__(1024) norm_forward_wide_kernel(NormForward a) 
             const bool on = c < a.cols;
             const float x = on ? load1(a.x.p, a.x.dtype, row * a.x.ld + c) : 0.0f;
             if (a.ckpt.p != nullptr) {   // ceil32 and the block are multiples of 32: whole warps
-                const uint32_t byte = act8_group_byte<1>(&x);
-                act8_writev<1>(static_cast<uint8_t*>(a.ckpt.p) + row * a.ckpt.ld, c, &x, byte);
-                if ((threadIdx.x & 31) == 0) a.ckpt.e[row * a.ckpt.eld + (c >> 5)] = static_cast<uint8_t>(byte);
+                const uint32_t top = act8_group_top<1>(&x);
+                act8_writev<1>(static_cast<uint8_t*>(a.ckpt.p) + row * a.ckpt.ld, c, &x, top);
+                if ((threadIdx.x & 31) == 0) a.ckpt.e[row * a.ckpt.eld + (c >> 5)] = static_cast<uint8_t>(act8_byte(top));
             }
             if (on)
                 store1(a.y.p, a.y.dtype, row * a.y.ld + c,
@@ -137,123 +137,514 @@ __device__ __forceinline__ void load_x(const Mat& x, int64_t row, int64_t c, flo
         loadv<V>(x.p, x.dtype, row * x.ld + c, v);
 }
 
-// A block holds G groups of `gt` threads (a multiple of 32); a group walks the
-// rows group, group + groups, ...  Thread t of a group owns the columns of
-// chunks t + k*gt, k < NV.
-template <int V, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_backward_kernel(NormBackward a, int gt) {
-    extern __shared__ float comb[];          // 2 * cols floats where the block has several groups
-    __shared__ float2 red[2][THREADS / 32];
-    const int g = threadIdx.x / gt, t = threadIdx.x % gt, G = blockDim.x / gt;
-    const int w0 = g * (gt >> 5), nw = gt >> 5;
+// ---- rows staged through shared memory ----
+//
+// A block walks rows with a fixed stride; the rows ahead are copied into a ring
+// of shared memory with cp.async.  Every thread copies exactly the chunks (8
+// columns) that it will read itself, so no barrier and no wait on another
+// thread is needed: only its own cp.async groups.
+//
+// A row belongs to a group of GT threads; thread t owns chunks t + k*GT, k < NV,
+// and a block holds several groups.  NV and GT are constants, so that the
+// addresses of a row's chunks differ by constants, and only the last chunk can
+// lie past the row's end.  FAST: every matrix and vector is BF16 (x may be
+// ACT8); otherwise types are looked at with every chunk.  The arithmetic runs
+// on pairs of columns.
+
+constexpr int kRing = 4;   // rows in the ring, at most
+
+__device__ __forceinline__ uint32_t shared_at(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// All but the newest `pending` groups have landed.
+__device__ __forceinline__ void copies_wait(int pending) {
+    switch (pending) {
+        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    }
+}
+
+// Bytes of eight elements.
+__host__ __device__ __forceinline__ int chunk_bytes(int dtype) {
+    return dtype == FSDP_DTYPE_F32 ? 32 : dtype == FSDP_DTYPE_BF16 ? 16 : 8;
+}
+
+// One matrix's rows as a thread sees them: its first chunk's address in global
+// memory for row 0, and its slots.  Slot (place, k) of a group starts at
+// (place * NV + k) * GT chunks; an F32 chunk is two halves GT * 16 bytes apart
+// (16-byte accesses of neighbouring threads are neighbours).
+template <int NV, int GT, bool FAST>
+struct Rows {
+    const uint8_t* first;
+    int64_t pitch;          // bytes between rows
+    uint8_t* slots;
+    int cb;                 // chunk_bytes
+    int place;              // bytes between places
+
+    __device__ Rows(const Mat& m, uint8_t* at, int group, int groups, int t) {
+        cb = chunk_bytes(m.dtype);
+        place = groups * NV * GT * cb;
+        slots = at + group * NV * GT * cb + t * (cb == 8 ? 8 : 16);
+        first = static_cast<const uint8_t*>(m.p) + t * cb;
+        pitch = m.ld * (cb >> 3);
+    }
+    __device__ void copy(int64_t row, int s, bool end) const {
+        const uint8_t* src = first + row * pitch;
+        const uint32_t dst = shared_at(slots + s * place);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (k + 1 < NV || end) {
+                if (cb == 8) {
+                    copy8(dst + k * GT * 8, src + k * GT * 8);
+                } else if (FAST || cb == 16) {
+                    copy16(dst + k * GT * 16, src + k * GT * 16);
+                } else {
+                    copy16(dst + k * GT * 32, src + k * GT * 32);
+                    copy16(dst + k * GT * 32 + GT * 16, src + k * GT * 32 + 16);
+                }
+            }
+        }
+    }
+    __device__ void read(int s, int k, f32x2* v) const {
+        const uint8_t* p = slots + s * place;
+        if (FAST || cb == 16) {
+            const uint4 w = *reinterpret_cast<const uint4*>(p + k * GT * 16);
+            v[0] = pair(bf16_lo(w.x), bf16_hi(w.x));
+            v[1] = pair(bf16_lo(w.y), bf16_hi(w.y));
+            v[2] = pair(bf16_lo(w.z), bf16_hi(w.z));
+            v[3] = pair(bf16_lo(w.w), bf16_hi(w.w));
+        } else {
+            const float4 a = *reinterpret_cast<const float4*>(p + k * GT * 32);
+            const float4 b = *reinterpret_cast<const float4*>(p + k * GT * 32 + GT * 16);
+            v[0] = pair(a.x, a.y);
+            v[1] = pair(a.z, a.w);
+            v[2] = pair(b.x, b.y);
+            v[3] = pair(b.z, b.w);
+        }
+    }
+    // The int8 values of an ACT8 chunk, as floats.
+    __device__ void read_ints(int s, int k, f32x2* v) const {
+        const uint2 w = *reinterpret_cast<const uint2*>(slots + s * place + k * GT * 8);
+        const f32x2 off = pair(-8388736.0f, -8388736.0f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t x = (h ? w.y : w.x) ^ 0x80808080u;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                v[2 * h + j] = add2(pair(__uint_as_float(__byte_perm(x, 0x4b000000u, 0x7440 + 2 * j)),
+                                         __uint_as_float(__byte_perm(x, 0x4b000000u, 0x7441 + 2 * j))), off);
+        }
+    }
+};
+
+// Where a thread's chunks of an output row go.
+template <int GT, bool FAST>
+struct Out {
+    uint8_t* first;
+    int64_t pitch;
+    int dtype;
+    __device__ Out(const Mat& m, int t) {
+        dtype = m.dtype;
+        first = static_cast<uint8_t*>(m.p) + t * chunk_bytes(m.dtype);
+        pitch = m.ld * (chunk_bytes(m.dtype) >> 3);
+    }
+    __device__ void store(uint8_t* row, int k, const f32x2* v) const {
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) unpair(v[j], o[2 * j], o[2 * j + 1]);
+        if (FAST) store8(row + k * GT * 16, FSDP_DTYPE_BF16, 0, o);
+        else store8(row + k * GT * chunk_bytes(dtype), dtype, 0, o);
+    }
+};
+
+// gamma or beta as a matrix of one row (all groups own the same columns and
+// share its slots).  Read from L1 or L2 with every row instead, they doubled
+// the time: the ring leaves L1 no room for them.
+__device__ __forceinline__ Mat vector_row(const void* p, int dtype) { return Mat{const_cast<void*>(p), nullptr, 0, 0, dtype}; }
+
+__device__ __forceinline__ float both(f32x2 v) {
+    float a, b;
+    unpair(v, a, b);
+    return a + b;
+}
+
+// Sums over a group of NW warps, for all of its threads.  Each warp leaves its
+// own; `red` is one of two buffers used in turn: a thread that writes one again
+// has passed the barrier behind which every thread had read it.
+template <int NW>
+__device__ __forceinline__ float group_sum(float a, float* red, int group) {
+    a = warp_sum(a);
+    if constexpr (NW == 1) return a;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(NW * 32) : "memory");
+    a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NW; i += 4) {
+        const float4 r = *reinterpret_cast<const float4*>(red + group * NW + i);
+        a += NW == 2 ? r.x + r.y : (r.x + r.y) + (r.z + r.w);
+    }
+    return a;
+}
+
+template <int NW>
+__device__ __forceinline__ float2 group_sum2(float a, float b, float2* red, int group) {
+    a = warp_sum(a);
+    b = warp_sum(b);
+    if constexpr (NW == 1) return make_float2(a, b);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(NW * 32) : "memory");
+    a = b = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NW; i += 2) {
+        const float4 r = *reinterpret_cast<const float4*>(red + group * NW + i);
+        a += r.x + r.z;
+        b += r.y + r.w;
+    }
+    return make_float2(a, b);
+}
+
+template <int NV, int GT, int THREADS, bool FAST>
+__global__ void __launch_bounds__(THREADS) norm_forward_ring_kernel(const __grid_constant__ NormForward a, int places) {
+    extern __shared__ __align__(16) uint8_t ring_bytes[];
+    __shared__ __align__(16) float red[2][32];
+    const int g = threadIdx.x / GT, t = threadIdx.x % GT, G = blockDim.x / GT;
+    const bool end = (t + (NV - 1) * GT) * 8 < a.cols;
+    const Rows<NV, GT, FAST> gammas(vector_row(a.gamma, a.param_dtype), ring_bytes, 0, 1, t);
+    const Rows<NV, GT, FAST> betas(vector_row(a.beta, a.param_dtype), ring_bytes + gammas.place, 0, 1, t);
+    const Rows<NV, GT, FAST> xs(a.x, ring_bytes + 2 * gammas.place, g, G, t);
+    const Out<GT, FAST> ys(a.y, t);
+    if (g == 0) {
+        gammas.copy(0, 0, end);
+        betas.copy(0, 0, end);
+        copies_end();
+        copies_wait(0);
+    }
+    __syncthreads();
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * G, first = static_cast<int64_t>(blockIdx.x) * G + g;
+    const float n = static_cast<float>(a.cols);
+    for (int s = 0; s + 1 < places; ++s) {
+        if (first + s * stride < a.rows) xs.copy(first + s * stride, s, end);
+        copies_end();
+    }
+    int place = 0;
+    for (int64_t row = first; row < a.rows; row += stride) {
+        const int64_t ahead = row + (places - 1) * stride;
+        if (ahead < a.rows) xs.copy(ahead, place == 0 ? places - 1 : place - 1, end);
+        copies_end();
+        copies_wait(places - 1);
+        f32x2 v[NV][4];
+        f32x2 s = pair(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (k + 1 < NV || end) {
+                xs.read(place, k, v[k]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[k][j] = pair(0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s = add2(s, v[k][j]);
+        }
+        place = place + 1 == places ? 0 : place + 1;
+        const float mean = group_sum<GT / 32>(both(s), red[0], g) / n;
+        const f32x2 less = pair(-mean, -mean);
+        f32x2 ss = pair(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (k + 1 < NV || end) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const f32x2 d = add2(v[k][j], less);
+                    ss = fma2(d, d, ss);
+                }
+            }
+        }
+        const float rstd = 1.0f / sqrtf(group_sum<GT / 32>(both(ss), red[1], g) / n + a.eps);
+        if (t == 0) {
+            a.mean[row] = mean;
+            a.rstd[row] = rstd;
+        }
+        if (a.ckpt.p != nullptr) {
+            uint8_t* q = static_cast<uint8_t*>(a.ckpt.p) + row * a.ckpt.ld;
+            uint8_t* e = a.ckpt.e + row * a.ckpt.eld;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) unpair(v[k][j], x[2 * j], x[2 * j + 1]);
+                const uint32_t top = act8_group_top<8>(x);
+                const int c = (t + k * GT) * 8;
+                if (k + 1 < NV || c < a.ckpt.ld) {   // the pads of a short last group are zeros
+                    act8_writev<8>(q, c, x, top);
+                    if ((t & 3) == 0) e[c >> 5] = static_cast<uint8_t>(act8_byte(top));
+                }
+            }
+        }
+        const f32x2 r2 = pair(rstd, rstd);
+        uint8_t* y = ys.first + row * ys.pitch;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (k + 1 < NV || end) {
+                f32x2 gm[4], bt[4];
+                gammas.read(0, k, gm);
+                betas.read(0, k, bt);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[k][j] = fma2(mul2(add2(v[k][j], less), r2), gm[j], bt[j]);
+                ys.store(y, k, v[k]);
+            }
+        }
+    }
+}
+
+template <int NV, int GT, int THREADS, bool FAST>
+__global__ void __launch_bounds__(THREADS) norm_backward_ring_kernel(const __grid_constant__ NormBackward a, int places) {
+    extern __shared__ __align__(16) uint8_t ring_bytes[];
+    __shared__ __align__(16) float2 red[2][32];
+    const int g = threadIdx.x / GT, t = threadIdx.x % GT, G = blockDim.x / GT;
+    const bool end = (t + (NV - 1) * GT) * 8 < a.cols;
+    uint8_t* at = ring_bytes;
+    const Rows<NV, GT, FAST> gammas(vector_row(a.gamma, a.param_dtype), at, 0, 1, t);
+    at += gammas.place;
+    const Rows<NV, GT, FAST> dys(a.dy, at, g, G, t);
+    at += places * dys.place;
+    const Rows<NV, GT, FAST> xs(a.x, at, g, G, t);
+    at += places * xs.place;
+    const Rows<NV, GT, FAST> adds(a.add, at, g, G, t);
+    const Out<GT, FAST> dxs(a.dx, t);
+    const bool added = a.add.p != nullptr, kept = a.x.dtype == FSDP_DTYPE_ACT8;
+    if (g == 0) {
+        gammas.copy(0, 0, end);
+        copies_end();
+        copies_wait(0);
+    }
+    __syncthreads();
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * G, first = static_cast<int64_t>(blockIdx.x) * G + g;
     const float inv_n = 1.0f / static_cast<float>(a.cols);
-    float dg[NV][V], db[NV][V];
+    const auto issue = [&](int64_t row, int s) {
+        if (row < a.rows) {
+            dys.copy(row, s, end);
+            xs.copy(row, s, end);
+            if (added) adds.copy(row, s, end);
+        }
+        copies_end();
+    };
+    // the row's scalars are a row ahead, in registers
+    float mean = 0.0f, rstd = 0.0f;
+    uint32_t byte[NV];
+    const auto scalars = [&](int64_t row) {
+        if (row < a.rows) {
+            mean = a.mean[row];
+            rstd = a.rstd[row];
+            if (kept) {
+                const uint8_t* e = a.x.e + row * a.x.eld + (t >> 2);
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    if (k + 1 < NV || end) byte[k] = e[k * (GT / 4)];
+            }
+        }
+    };
+    for (int s = 0; s + 1 < places; ++s) issue(first + s * stride, s);
+    scalars(first);
+    f32x2 dg[NV][4], db[NV][4];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int j = 0; j < V; ++j) dg[k][j] = db[k][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) dg[k][j] = db[k][j] = pair(0.0f, 0.0f);
+    int place = 0, flip = 0;
+    for (int64_t row = first; row < a.rows; row += stride) {
+        issue(row + (places - 1) * stride, place == 0 ? places - 1 : place - 1);
+        copies_wait(places - 1);
+        f32x2 xh[NV][4], gr[NV][4];
+        f32x2 s1 = pair(0.0f, 0.0f), s2 = pair(0.0f, 0.0f);
+        const float r = rstd;
+        const f32x2 shift = pair(-mean * r, -mean * r);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (k + 1 < NV || end) {
+                f32x2 gm[4], dy[4];
+                gammas.read(0, k, gm);
+                dys.read(place, k, dy);
+                // x rstd - mean rstd; a checkpoint's step (a power of two) goes into the factor
+                float scale = r;
+                if (kept) {
+                    xs.read_ints(place, k, xh[k]);
+                    scale = r * act8_step(byte[k]);
+                } else {
+                    xs.read(place, k, xh[k]);
+                }
+                const f32x2 scale2 = pair(scale, scale);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    xh[k][j] = fma2(xh[k][j], scale2, shift);
+                    db[k][j] = add2(db[k][j], dy[j]);
+                    dg[k][j] = fma2(dy[j], xh[k][j], dg[k][j]);
+                    gr[k][j] = mul2(dy[j], gm[j]);
+                    s1 = add2(s1, gr[k][j]);
+                    s2 = fma2(gr[k][j], xh[k][j], s2);
+                }
+            }
+        }
+        scalars(row + stride);
+        const float2 sum = group_sum2<GT / 32>(both(s1), both(s2), red[flip], g);
+        flip ^= 1;
+        // dx = dy gamma rstd - xh c2 - c1 [+ add]
+        const float c1 = -sum.x * inv_n * r, c2 = -sum.y * inv_n * r;
+        const f32x2 r2 = pair(r, r), m1 = pair(c1, c1), m2 = pair(c2, c2);
+        uint8_t* dx = dxs.first + row * dxs.pitch;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (k + 1 < NV || end) {
+                f32x2 o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[j] = fma2(r2, gr[k][j], fma2(xh[k][j], m2, m1));
+                if (added) {
+                    f32x2 e[4];
+                    adds.read(place, k, e);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[j] = add2(o[j], e[j]);
+                }
+                dxs.store(dx, k, o);
+            }
+        }
+        place = place + 1 == places ? 0 : place + 1;
+    }
+    // the groups' column sums meet in shared memory (element j of chunk i at
+    // j * slots + i: neighbouring threads on neighbouring banks)
+    float* part = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+    constexpr int kSlots = NV * GT;
+    if (G > 1) {
+        float* comb = reinterpret_cast<float*>(ring_bytes);
+        copies_wait(0);
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float* to = comb + (g * 16 + 2 * j) * kSlots + t + k * GT;
+                unpair(dg[k][j], to[0], to[kSlots]);
+                unpair(db[k][j], to[8 * kSlots], to[9 * kSlots]);
+            }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 16 * kSlots; i += blockDim.x) {
+            float s = 0.0f;
+            for (int h = 0; h < G; ++h) s += comb[h * 16 * kSlots + i];
+            const int j = i / kSlots, c = (i - j * kSlots) * 8 + (j & 7);
+            if (c < a.cols) part[(j >> 3) * a.cols + c] = s;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (k + 1 < NV || end) {
+                f32x2* p = reinterpret_cast<f32x2*>(part + (t + k * GT) * 8);
+                f32x2* q = reinterpret_cast<f32x2*>(part + a.cols + (t + k * GT) * 8);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    p[j] = dg[k][j];
+                    q[j] = db[k][j];
+                }
+            }
+        }
+    }
+}
+
+// ---- other rows ----
+
+// Rows that start anywhere: one column to a thread at a time, straight from
+// global memory.
+__device__ __forceinline__ float2 group_sum2(float a, float b, float2* red, int group, int gt) {
+    a = warp_sum(a);
+    b = warp_sum(b);
+    const int nw = gt >> 5;
+    if (nw == 1) return make_float2(a, b);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(gt) : "memory");
+    a = b = 0.0f;
+    for (int i = 0; i < nw; ++i) {
+        a += red[group * nw + i].x;
+        b += red[group * nw + i].y;
+    }
+    return make_float2(a, b);
+}
+
+template <int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_backward_kernel(NormBackward a, int gt) {
+    extern __shared__ __align__(16) uint8_t ring_bytes[];
+    __shared__ float2 red[2][THREADS / 32];
+    const int g = threadIdx.x / gt, t = threadIdx.x % gt, G = blockDim.x / gt;
+    const float inv_n = 1.0f / static_cast<float>(a.cols);
+    float dg[NV], db[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) dg[k] = db[k] = 0.0f;
     int flip = 0;
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * G + g; row < a.rows; row += static_cast<int64_t>(gridDim.x) * G) {
-        float xh[NV][V], dy[NV][V];
+        float xh[NV], dy[NV];
         const float mean = a.mean[row], rstd = a.rstd[row];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int64_t c = static_cast<int64_t>(t + k * gt) * V;
-            if (c < a.cols) {
-                loadv<V>(a.dy.p, a.dy.dtype, row * a.dy.ld + c, dy[k]);
-                load_x<V>(a.x, row, c, xh[k]);
-            } else {
+            const int64_t c = t + k * gt;
+            dy[k] = c < a.cols ? load1(a.dy.p, a.dy.dtype, row * a.dy.ld + c) : 0.0f;
+        }
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    dy[k][j] = 0.0f;
-                    xh[k][j] = mean;
-                }
-            }
+        for (int k = 0; k < NV; ++k) {
+            const int64_t c = t + k * gt;
+            xh[k] = mean;
+            if (c < a.cols) load_x<1>(a.x, row, c, &xh[k]);
         }
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int64_t c = static_cast<int64_t>(t + k * gt) * V;
-            float gm[V];
-            if (c < a.cols) {
-                loadv<V>(a.gamma, a.param_dtype, c, gm);
-            } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j) gm[j] = 0.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                xh[k][j] = (xh[k][j] - mean) * rstd;
-                db[k][j] += dy[k][j];
-                dg[k][j] = fmaf(dy[k][j], xh[k][j], dg[k][j]);
-                dy[k][j] *= gm[j];
-                s1 += dy[k][j];
-                s2 = fmaf(dy[k][j], xh[k][j], s2);
-            }
+            const int64_t c = t + k * gt;
+            xh[k] = (xh[k] - mean) * rstd;
+            db[k] += dy[k];
+            dg[k] = fmaf(dy[k], xh[k], dg[k]);
+            dy[k] *= c < a.cols ? load1(a.gamma, a.param_dtype, c) : 0.0f;
+            s1 += dy[k];
+            s2 = fmaf(dy[k], xh[k], s2);
         }
-        s1 = warp_sum(s1);
-        s2 = warp_sum(s2);
-        if (nw > 1) {
-            // two buffers in turn: a thread that writes one again has passed the
-            // barrier behind which every thread had read it
-            if ((t & 31) == 0) red[flip][threadIdx.x >> 5] = make_float2(s1, s2);
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "r"(gt) : "memory");
-            s1 = s2 = 0.0f;
-            for (int i = 0; i < nw; ++i) {
-                const float2 r = red[flip][w0 + i];
-                s1 += r.x;
-                s2 += r.y;
-            }
-            flip ^= 1;
-        }
-        const float c1 = s1 * inv_n, c2 = s2 * inv_n;
+        const float2 sum = group_sum2(s1, s2, red[flip], g, gt);
+        flip ^= 1;
+        const float c1 = sum.x * inv_n, c2 = sum.y * inv_n;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int64_t c = static_cast<int64_t>(t + k * gt) * V;
+            const int64_t c = t + k * gt;
             if (c < a.cols) {
-                float o[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) o[j] = rstd * (dy[k][j] - c1 - xh[k][j] * c2);
-                if (a.add.p != nullptr) {
-                    float e[V];
-                    loadv<V>(a.add.p, a.add.dtype, row * a.add.ld + c, e);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) o[j] += e[j];
-                }
-                storev<V>(a.dx.p, a.dx.dtype, row * a.dx.ld + c, o);
+                float o = rstd * (dy[k] - c1 - xh[k] * c2);
+                if (a.add.p != nullptr) o += load1(a.add.p, a.add.dtype, row * a.add.ld + c);
+                store1(a.dx.p, a.dx.dtype, row * a.dx.ld + c, o);
             }
         }
     }
     float* part = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+    const int slots = NV * gt;
+    float* comb = reinterpret_cast<float*>(ring_bytes);
     if (G > 1) {
-        for (int i = 0; i < G; ++i) {
-            if (g == i) {
 #pragma unroll
-                for (int k = 0; k < NV; ++k) {
-                    const int64_t c = static_cast<int64_t>(t + k * gt) * V;
-                    if (c < a.cols) {
-#pragma unroll
-                        for (int j = 0; j < V; ++j) {
-                            float* p = comb + c + j;
-                            p[0] = (i ? p[0] : 0.0f) + dg[k][j];
-                            p[a.cols] = (i ? p[a.cols] : 0.0f) + db[k][j];
-                        }
-                    }
-                }
-            }
-            __syncthreads();
+        for (int k = 0; k < NV; ++k) {
+            comb[2 * g * slots + t + k * gt] = dg[k];
+            comb[(2 * g + 1) * slots + t + k * gt] = db[k];
         }
-        for (int64_t i = threadIdx.x; i < 2 * a.cols; i += blockDim.x) part[i] = comb[i];
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * slots; i += blockDim.x) {
+            float s = 0.0f;
+            for (int h = 0; h < G; ++h) s += comb[2 * h * slots + i];
+            const int64_t c = i < slots ? i : i - slots;
+            if (c < a.cols) part[(i < slots ? 0 : a.cols) + c] = s;
+        }
     } else {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int64_t c = static_cast<int64_t>(t + k * gt) * V;
+            const int64_t c = t + k * gt;
             if (c < a.cols) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    part[c + j] = dg[k][j];
-                    part[a.cols + c + j] = db[k][j];
-                }
+                part[c] = dg[k];
+                part[a.cols + c] = db[k];
             }
         }
     }
@@ -303,36 +694,59 @@ __global__ void __launch_bounds__(256) norm_backward_wide_sums_kernel(NormBackwa
     part[a.cols + c] = db;
 }
 
-// out0 from partials[p*stride + c], out1 (blockIdx.y == 1) from columns
-// further on by `second`: 32 columns and 32 slices of p to a block, the slices
-// joined in order.
-__global__ void __launch_bounds__(1024) sum_partials_kernel(const float* partials, int64_t count, int64_t stride,
-                                                            int64_t second, int64_t cols, void* out0, void* out1,
-                                                            int dtype, int accumulate) {
-    __shared__ float part[32][33];
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + tx;
-    void* out = blockIdx.y ? out1 : out0;
+// out0 from partials[p*stride + c], out1 (blockIdx.y == 1) from `second` floats
+// further on: 16 threads of V columns across and 16 slices of p down to a
+// block, the slices joined in order.
+template <int V>
+__global__ void __launch_bounds__(256) sum_partials_kernel(const float* partials, int64_t count, int64_t stride, int64_t second,
+                                                           int64_t cols, void* out0, void* out1, int dtype, int accumulate) {
+    __shared__ float part[16][16 * V];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int64_t c = (static_cast<int64_t>(blockIdx.x) * 16 + tx) * V;
     const float* p = partials + (blockIdx.y ? second : 0) + c;
-    float s = 0.0f;
-    if (c < cols)
-        for (int64_t i = ty; i < count; i += 32) s += p[i * stride];
-    part[ty][tx] = s;
-    __syncthreads();
-    if (ty == 0 && c < cols) {
-        s = 0.0f;
+    float s[V];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s += part[i][tx];
-        if (accumulate) s += load1(out, dtype, c);
-        store1(out, dtype, c, s);
+    for (int j = 0; j < V; ++j) s[j] = 0.0f;
+    if (c < cols) {
+#pragma unroll 10
+        for (int64_t i = ty; i < count; i += 16) {
+            if constexpr (V == 4) {
+                const float4 f = __ldcg(reinterpret_cast<const float4*>(p + i * stride));
+                s[0] += f.x; s[1] += f.y; s[2] += f.z; s[3] += f.w;
+            } else {
+                s[0] += __ldcg(p + i * stride);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) part[ty][tx * V + j] = s[j];
+    __syncthreads();
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 16 * V + threadIdx.x;
+    if (threadIdx.x < 16 * V && col < cols) {
+        void* out = blockIdx.y ? out1 : out0;
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t += part[i][threadIdx.x];
+        if (accumulate) t += load1(out, dtype, col);
+        store1(out, dtype, col, t);
     }
 }
 
 cudaError_t sum_partials(const float* partials, int64_t count, int64_t stride, int64_t second, int64_t cols,
                          void* out0, void* out1, int dtype, int accumulate, cudaStream_t st) {
-    const dim3 grid(static_cast<unsigned>((cols + 31) / 32), out1 != nullptr ? 2 : 1);
-    sum_partials_kernel<<<grid, 1024, 0, st>>>(partials, count, stride, second, cols, out0, out1, dtype, accumulate);
-    return cudaGetLastError();
+    const bool vec = cols % 4 == 0;   // the workspace is aligned
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(vec ? (cols + 63) / 64 : (cols + 15) / 16), out1 != nullptr ? 2 : 1);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute early{};   // its launch overlaps the kernel before it; it waits for all of that before it reads
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, vec ? sum_partials_kernel<4> : sum_partials_kernel<1>, partials, count, stride, second,
+                              cols, out0, out1, dtype, accumulate);
 }
 
 int round32(int64_t n) { return static_cast<int>((n + 31) / 32 * 32); }
@@ -349,41 +763,90 @@ cudaError_t run_forward(const NormForward& a, int64_t chunks, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-// The backward's split: vector chunks or single columns, threads to a row,
-// rows to a block.
-struct BackwardPlan {
-    int V, NV, gt, groups;   // NV 0: rows too long for registers
-    int64_t blocks;
+// How a row is split: threads to it, chunks (or columns) to a thread, rows to a
+// block.
+struct Split {
+    int NV = 0, gt = 0, groups = 0;   // NV 0: rows too long for registers
+    int threads() const { return gt * groups; }
 };
 
-BackwardPlan backward_plan(int64_t rows, int64_t cols, bool vec, int sms) {
-    BackwardPlan p{};
-    p.V = vec ? 8 : 1;
-    const int64_t chunks = (cols + p.V - 1) / p.V;
-    if (vec) p.NV = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : chunks <= 1536 ? 3 : 0;
-    else p.NV = chunks <= 4096 ? 8 : chunks <= 12288 ? 24 : 0;
-    if (p.NV == 0) {
-        p.blocks = std::max<int64_t>(1, std::min<int64_t>(rows, 16));
-        return p;
+// The constants' combination that covers the row's chunks with the fewest
+// slots; of equals, the one with fewer threads, whose sums cost less.
+Split split_row(int64_t rows, int64_t chunks, const int (*options)[2], int count, int block_threads) {
+    Split p;
+    for (int i = 0; i < count; ++i) {
+        const int nv = options[i][0], gt = options[i][1];
+        if (nv * gt < chunks || (nv - 1) * gt >= chunks) continue;
+        if (p.NV != 0 && nv * gt >= p.NV * p.gt) continue;
+        p.NV = nv;
+        p.gt = gt;
     }
-    p.gt = round32((chunks + p.NV - 1) / p.NV);
-    const int most = p.NV == 1 || p.NV == 8 ? 1024 : 512;
-    // a named barrier to a group: 15 at most
-    p.groups = std::max(1, std::min(std::min(most / p.gt, 15), static_cast<int>(std::min<int64_t>(rows, 15))));
-    p.blocks = std::max<int64_t>(1, std::min<int64_t>((rows + p.groups - 1) / p.groups, sms));
+    if (p.NV != 0)   // a named barrier to a group: 15 at most
+        p.groups = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(block_threads / p.gt, 15), rows)));
     return p;
+}
+constexpr int kForward[][2] = {{1, 32}, {2, 32}, {3, 32}, {4, 32}, {5, 32}, {6, 32}, {2, 128}, {3, 128}, {4, 128}, {5, 128}, {6, 128}, {4, 256}, {5, 256}, {6, 256}, {4, 512}};
+constexpr int kBackward[][2] = {{1, 32}, {2, 32}, {3, 32}, {2, 64}, {3, 64}, {2, 128}, {3, 128}, {1, 512}, {2, 512}, {3, 512}};
+
+int64_t walkers(const Split& p, int64_t rows, int64_t most) {
+    return std::max<int64_t>(1, std::min((rows + p.groups - 1) / p.groups, most));
+}
+
+constexpr int kWideSlices = 64;   // row slices of the column sums where rows are too long
+
+Split backward_split(int64_t rows, int64_t cols, bool vec) {
+    if (vec) return split_row(rows, cols / 8, kBackward, 10, 512);
+    Split p;
+    if (cols <= 8192) {
+        p.NV = 8;
+        p.gt = round32((cols + 7) / 8);
+        p.groups = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(1024 / p.gt, 15), rows)));
+    }
+    return p;
+}
+
+int64_t backward_blocks(int64_t rows, int64_t cols, bool vec, int sms) {
+    const Split p = backward_split(rows, cols, vec);
+    if (p.NV == 0) return std::max<int64_t>(1, std::min<int64_t>(rows, kWideSlices));
+    return walkers(p, rows, sms);
+}
+
+// Launches with `bytes` of dynamic shared memory, allowed once per kernel.
+constexpr int kSharedMost = 222 * 1024;
+template <auto kernel, typename... Args>
+cudaError_t launch_shared(unsigned blocks, int threads, int bytes, cudaStream_t st, const Args&... args) {
+    static const cudaError_t allowed = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedMost);
+    if (allowed != cudaSuccess) return allowed;
+    kernel<<<blocks, threads, bytes, st>>>(args...);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_norm_forward(const NormForward& a, int sms, cudaStream_t st) {
-    (void)sms;
     if (a.rows == 0) return cudaSuccess;
     const bool vec = rows_aligned(a.x) && rows_aligned(a.y) && a.cols % 8 == 0 &&
                      ((reinterpret_cast<uintptr_t>(a.gamma) | reinterpret_cast<uintptr_t>(a.beta)) & 15u) == 0;
     if (vec) {
+        const Split p = split_row(a.rows, a.cols / 8, kForward, 15, 512);
+        const int keep = p.NV * p.gt * 2 * chunk_bytes(a.param_dtype), row_bytes = p.threads() * p.NV * chunk_bytes(a.x.dtype);
+        const int places = p.NV == 0 ? 0 : std::min(kRing, (kSharedMost - keep) / row_bytes);
+        // rows enough for every group to walk two
+        if (places > 0 && a.rows >= 2 * static_cast<int64_t>(sms) * p.groups) {
+            const unsigned blocks = static_cast<unsigned>(walkers(p, a.rows, sms));
+            const int bytes = keep + places * row_bytes;
+            const bool fast = a.x.dtype == FSDP_DTYPE_BF16 && a.y.dtype == FSDP_DTYPE_BF16 && a.param_dtype == FSDP_DTYPE_BF16;
+#define RING(nv, gt_)                                                                                             \
+    if (p.NV == nv && p.gt == gt_)                                                                                \
+        return fast ? launch_shared<norm_forward_ring_kernel<nv, gt_, 512, true>>(blocks, p.threads(), bytes, st, a, places) \
+                    : launch_shared<norm_forward_ring_kernel<nv, gt_, 512, false>>(blocks, p.threads(), bytes, st, a, places);
+            RING(1, 32) RING(2, 32) RING(3, 32) RING(4, 32) RING(5, 32) RING(6, 32)
+            RING(2, 128) RING(3, 128) RING(4, 128) RING(5, 128) RING(6, 128)
+            RING(4, 256) RING(5, 256) RING(6, 256) RING(4, 512)
+#undef RING
+        }
         const int64_t chunks = a.cols / 8;
-        if (chunks <= 512) return run_forward<8, 2>(a, chunks, st);
+        if (chunks <= 512) return run_forward<8, 1>(a, chunks, st);
         if (chunks <= 4096) return run_forward<8, 4>(a, chunks, st);
     } else {
         if (a.cols <= 4096) return run_forward<1, 8>(a, a.cols, st);
@@ -394,44 +857,45 @@ cudaError_t launch_norm_forward(const NormForward& a, int sms, cudaStream_t st) 
 }
 
 int64_t norm_partials(int64_t rows, int64_t cols, int sms) {
-    return std::max(backward_plan(rows, cols, true, sms).blocks, backward_plan(rows, cols, false, sms).blocks);
+    return std::max(cols % 8 == 0 ? backward_blocks(rows, cols, true, sms) : 0, backward_blocks(rows, cols, false, sms));
 }
 
 cudaError_t launch_norm_backward(const NormBackward& a, int sms, cudaStream_t st) {
     const bool vec = rows_aligned(a.dy) && rows_aligned(a.x) && rows_aligned(a.dx) &&
                      (a.add.p == nullptr || rows_aligned(a.add)) && a.cols % 8 == 0 &&
                      (reinterpret_cast<uintptr_t>(a.gamma) & 15u) == 0;
-    const BackwardPlan p = backward_plan(a.rows, a.cols, vec, sms);
+    const Split p = backward_split(a.rows, a.cols, vec);
     cudaError_t e = cudaSuccess;
-    int64_t count = p.blocks;
+    int64_t count = backward_blocks(a.rows, a.cols, vec, sms);
+    const unsigned blocks = static_cast<unsigned>(count);
     if (a.rows == 0) {
         count = 0;
     } else if (p.NV == 0) {
         norm_backward_wide_dx_kernel<<<static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t(1) << 30)), 1024, 0, st>>>(a);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        const dim3 grid(static_cast<unsigned>((a.cols + 255) / 256), static_cast<unsigned>(p.blocks));
+        const dim3 grid(static_cast<unsigned>((a.cols + 255) / 256), blocks);
         norm_backward_wide_sums_kernel<<<grid, 256, 0, st>>>(a);
         e = cudaGetLastError();
+    } else if (vec) {
+        const int row_bytes = p.threads() * p.NV *
+                              (chunk_bytes(a.dy.dtype) + chunk_bytes(a.x.dtype) + (a.add.p != nullptr ? chunk_bytes(a.add.dtype) : 0));
+        const int keep = p.NV * p.gt * chunk_bytes(a.param_dtype);
+        const int places = std::max(1, std::min(kRing, (kSharedMost - keep) / row_bytes));
+        const int comb = p.groups > 1 ? p.threads() * p.NV * 16 * 4 : 0;
+        const int bytes = std::max(keep + places * row_bytes, comb);
+        const bool fast = a.dy.dtype == FSDP_DTYPE_BF16 && a.dx.dtype == FSDP_DTYPE_BF16 && a.param_dtype == FSDP_DTYPE_BF16 &&
+                          a.x.dtype != FSDP_DTYPE_F32 && (a.add.p == nullptr || a.add.dtype == FSDP_DTYPE_BF16);
+        e = cudaErrorInvalidConfiguration;
+#define RING(nv, gt_)                                                                                              \
+    if (p.NV == nv && p.gt == gt_)                                                                                 \
+        e = fast ? launch_shared<norm_backward_ring_kernel<nv, gt_, 512, true>>(blocks, p.threads(), bytes, st, a, places) \
+                 : launch_shared<norm_backward_ring_kernel<nv, gt_, 512, false>>(blocks, p.threads(), bytes, st, a, places);
+        RING(1, 32) RING(2, 32) RING(3, 32) RING(2, 64) RING(3, 64) RING(2, 128) RING(3, 128) RING(1, 512) RING(2, 512) RING(3, 512)
+#undef RING
     } else {
-        const int threads = p.gt * p.groups;
-        const size_t smem = p.groups > 1 ? static_cast<size_t>(2 * a.cols) * sizeof(float) : 0;
-        auto go = [&](auto kernel) {
-            if (smem > 40 * 1024)
-                e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-            if (e == cudaSuccess) {
-                kernel<<<static_cast<unsigned>(p.blocks), threads, smem, st>>>(a, p.gt);
-                e = cudaGetLastError();
-            }
-        };
-        if (p.V == 8) {
-            if (p.NV == 1) go(norm_backward_kernel<8, 1, 1024>);
-            else if (p.NV == 2) go(norm_backward_kernel<8, 2, 512>);
-            else go(norm_backward_kernel<8, 3, 512>);
-        } else {
-            if (p.NV == 8) go(norm_backward_kernel<1, 8, 1024>);
-            else go(norm_backward_kernel<1, 24, 512>);
-        }
+        const int comb = p.groups > 1 ? p.threads() * p.NV * 2 * 4 : 0;
+        e = launch_shared<norm_backward_kernel<8, 1024>>(blocks, p.threads(), comb, st, a, p.gt);
     }
     if (e != cudaSuccess) return e;
     return sum_partials(a.partials, count, 2 * a.cols, a.cols, a.cols, a.dgamma, a.dbeta, a.grad_dtype, a.accumulate, st);

@@ -492,3 +492,24 @@ def test_a_copy_that_never_arrives_is_reported():
     c.linear_forward(x, w, again)
     assert c.status() == 0 and torch.equal(y, again)
     c.close()
+
+
+@pytest.mark.parametrize("rows,cols", [(1300, 520), (700, 4104), (1400, 1280)])
+def test_layer_norm_many_rows(handle, rows, cols):
+    """Enough rows for a block to walk several of them."""
+    x = _normal(cols, (rows, cols), 2.0, BF, 0.7)
+    gamma, beta = _normal(1, cols, 0.3, BF, 1.0), _normal(2, cols, 0.3, BF)
+    y, mean, rstd = torch.empty_like(x), torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    k = B.Act8(rows, cols)
+    handle.layer_norm_forward(x, gamma, beta, 1e-5, y, mean, rstd, ckpt=k)
+    X, G, Bt = np64(x), np64(gamma), np64(beta)
+    Y, M, R = O.layer_norm(X, G, Bt, 1e-5)
+    em, er, ey = _norm_bounds(X, G, Bt, Y, M, R, BF)
+    inside(mean, M, em, "mean")
+    inside(rstd, R, er, "rstd")
+    inside(y, Y, ey, "y")
+    other = B.Act8(rows, cols)
+    handle.act8_pack(x, other)
+    assert torch.equal(k.q, other.q) and torch.equal(k.exps, other.exps)
+    for ckpt, add in ((False, "other"), (True, None)):
+        _norm_grad_case(handle, rows, cols, 0, 0, BF, BF, BF, F32, ckpt, add, False)
