@@ -18,7 +18,8 @@ namespace {
 // tcgen05.mma.cta_group::2: each CTA holds 128 rows of A and BN/2 rows of B in
 // shared memory, and 128 rows of the fp32 sums in its tensor memory.
 //
-//   warp 0   producer: TMA copies of 64-deep slices into a ring of stages
+//   warps 0 and 3  producers: TMA copies of 64-deep slices of A and of B into a
+//            ring of stages (one warp for both took 250 cycles to issue a stage)
 //   warp 1   issues the pair's matrix instructions (first CTA only)
 //   warp 2   tensor memory allocation
 //   warps 4-11  epilogue: sums to registers, then bias, activation, residual,
@@ -30,9 +31,11 @@ namespace {
 // contiguous direction, and only the shared-memory descriptors differ.
 
 constexpr int kStages = 6;
-constexpr int kDepth = 64;                       // k per stage
+constexpr int kDepth = 64;                       // k per stage (3 stages of 128 were 4 % slower at 8192^3)
+constexpr int kBlock = 64 * kDepth * 2;          // a box of an operand that is contiguous along its rows: 64 rows
 constexpr int kStageA = 128 * kDepth * 2;        // bytes of A in a stage, per CTA
 constexpr int kStageB = 128 * kDepth * 2;        // of B, at BN = 256
+static_assert(kStageA == kStageB, "one stride for both operands' stages");
 constexpr int kEpiWarps = 8;
 constexpr int kEpiBytes = 32 * 32 * 4;           // a warp's transposing buffer
 constexpr int kThreads = 384;
@@ -41,14 +44,14 @@ constexpr int kPieces = 2 * kEpiWarps;           // parts of a tile
 constexpr size_t kSmemBytes = 1024 + kStages * (kStageA + kStageB) + kEpiWarps * kEpiBytes + 256;
 
 struct Bars {
-    uint64_t full[kStages];      // first CTA's: both CTAs' copies of a stage have landed
+    uint64_t full[kStages];      // first CTA's: both CTAs' copies of a stage, A's and B's, have landed
     uint64_t empty[kStages];     // the products that read a stage are done
     uint64_t tmem_full[2];       // a tile's sums are complete
     uint64_t tmem_empty[2];      // first CTA's: both CTAs' epilogues have read them
     uint64_t drain;
     uint32_t tmem_base;
     uint32_t abort;              // a wait of this CTA ran out
-    uint32_t issued;             // stages the producer issued
+    uint32_t issued[2];          // stages the producers issued: of A, of B
     uint32_t consumed;           // stages the matrix instructions read
 };
 static_assert(sizeof(Bars) <= 256, "the barriers' room");
@@ -124,6 +127,13 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
         : "memory");
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
+}
+
 // Arrives on the barrier at this offset in both CTAs once the matrix
 // instructions issued so far are done.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
@@ -153,10 +163,10 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float* v) {
 
 // Shared-memory descriptor of an operand slice, 128-byte swizzled.  Contiguous
 // along k: rows of 64 elements, 8-row groups 1024 bytes apart.  Contiguous
-// along its rows: blocks of 64 rows x 64 k, 8192 bytes apart, 8-k groups 1024
+// along its rows: blocks of 64 rows x 64 k, kBlock apart, 8-k groups 1024
 // bytes apart.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool by_rows) {
-    const uint64_t lead = by_rows ? 8192 >> 4 : 1;
+    const uint64_t lead = by_rows ? kBlock >> 4 : 1;
     return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | lead << 16 | static_cast<uint64_t>(1024 >> 4) << 32 |
            uint64_t(1) << 46 | uint64_t(2) << 61;
 }
@@ -279,7 +289,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            bar_init(&bars->full[i], 2);
+            bar_init(&bars->full[i], 4);
             bar_init(&bars->empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -287,7 +297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bar_init(&bars->tmem_empty[i], 2 * kEpiWarps);
         }
         bar_init(&bars->drain, 1);
-        bars->abort = bars->issued = bars->consumed = 0;
+        bars->abort = bars->issued[0] = bars->issued[1] = bars->consumed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_b) : "memory");
@@ -303,81 +313,102 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = bars->tmem_base;
-    if (warp == 0 && lane == 0) {
-        // ---- producer ----
-        const uint32_t bytes = kStageA + (p.b_trans ? (pl.bn > 128 ? 16384 : 8192) : pl.bn / 2 * kDepth * 2);
-        uint32_t q = 0;
+    // The producer's and the matrix warp's loops run in whole warps, with one
+    // lane elected to issue: their counters and descriptors are then uniform.
+    // (In a branch of one lane, each matrix instruction took 65 cycles to issue
+    // and a stage 520, whatever the tile's width.)
+    if (warp == 0 || warp == 3) {
+        // ---- producers: A's, and B's ----
+        const bool is_a = warp == 0;
+        const CUtensorMap* map = is_a ? &map_a : &map_b;
+        const bool by_rows = is_a ? p.a_trans : p.b_trans;
+        const int extent = is_a ? 128 : pl.bn / 2;                     // rows of the operand in a stage, per CTA
+        const bool second = by_rows && extent > 64;                    // a box holds 64 of them
+        const uint32_t bytes = by_rows ? (second ? 2 * kBlock : kBlock) : extent * kDepth * 2;
+        const uint32_t full0 = remote_addr(smem_addr(&bars->full[0]), 0);
+        const uint32_t stage0 = smem_addr(is_a ? stage_a : stage_b);
+        const bool withheld = pl.withhold && blockIdx.x < 2;
+        uint32_t* issued = &bars->issued[is_a ? 0 : 1];
+        uint32_t q = 0, s = 0, use = 0;   // stages issued, the next one's place and how often the ring went round (parity)
         bool ok = true;
         for (int64_t u = cluster; u < pl.units && ok; u += clusters) {
             const Unit un = unit_of(pl, u);
-            const int row = un.tm * 256 + static_cast<int>(rank) * 128;
-            const int col = un.tn * pl.bn + static_cast<int>(rank) * (pl.bn / 2);
-            for (int k = un.k0; k < un.k1; ++k, ++q) {
-                const uint32_t s = q % kStages;
-                if (q >= kStages && !bar_wait(&bars->empty[s], (q / kStages - 1) & 1u, pl.wait_cycles, abort)) {
+            const int at = (is_a ? un.tm * 256 : un.tn * pl.bn) + static_cast<int>(rank) * extent;
+            for (int k = un.k0; k < un.k1; ++k) {
+                if (q >= kStages && !__all_sync(0xffffffffu, bar_wait(&bars->empty[s], use ^ 1u, pl.wait_cycles, abort))) {
                     ok = false;
                     break;
                 }
-                const uint32_t full = remote_addr(smem_addr(&bars->full[s]), 0);
-                bar_expect_remote(full, bytes);
-                const uint32_t a = smem_addr(stage_a + s * kStageA), b = smem_addr(stage_b + s * kStageB);
-                if (!(pl.withhold && blockIdx.x < 2 && q == 0)) {
-                    if (!p.a_trans) {
-                        tma_load(a, &map_a, k * kDepth, row, full);
-                    } else {
-                        tma_load(a, &map_a, row, k * kDepth, full);
-                        tma_load(a + 8192, &map_a, row + 64, k * kDepth, full);
+                if (elect_one()) {
+                    const uint32_t full = full0 + s * 8, dst = stage0 + s * kStageA;
+                    bar_expect_remote(full, bytes);
+                    if (!(withheld && q == 0)) {
+                        if (!by_rows) {
+                            tma_load(dst, map, k * kDepth, at, full);
+                        } else {
+                            tma_load(dst, map, at, k * kDepth, full);
+                            if (second) tma_load(dst + kBlock, map, at + 64, k * kDepth, full);
+                        }
                     }
-                    if (!p.b_trans) {
-                        tma_load(b, &map_b, k * kDepth, col, full);
-                    } else {
-                        tma_load(b, &map_b, col, k * kDepth, full);
-                        if (pl.bn > 128) tma_load(b + 8192, &map_b, col + 64, k * kDepth, full);
-                    }
+                    *issued = q + 1;
                 }
-                bars->issued = q + 1;
+                ++q;
+                if (++s == kStages) {
+                    s = 0;
+                    use ^= 1u;
+                }
             }
         }
         // the stages still being read: their commits arrive here before this CTA leaves
         for (uint32_t i = q > kStages ? q - kStages : 0; ok && i < q; ++i)
-            ok = bar_wait(&bars->empty[i % kStages], (i / kStages) & 1u, pl.wait_cycles, abort);
-        if (!ok) {
+            ok = __all_sync(0xffffffffu, bar_wait(&bars->empty[i % kStages], (i / kStages) & 1u, pl.wait_cycles, abort));
+        if (!ok && lane == 0) {
             atomicOr(pl.status, FSDP_KSTATUS_WAIT_TIMEOUT);
             *abort = 1;
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
         // ---- matrix instructions ----
         const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | static_cast<uint32_t>(p.a_trans) << 15 |
                                static_cast<uint32_t>(p.b_trans) << 16 | static_cast<uint32_t>(pl.bn >> 3) << 17 | 16u << 24;
-        const uint32_t step_a = p.a_trans ? 2048 >> 4 : 32 >> 4, step_b = p.b_trans ? 2048 >> 4 : 32 >> 4;
-        uint32_t q = 0, tile = 0;
+        const uint32_t step_a = p.a_trans ? 2048 >> 4 : 32 >> 4, step_b = p.b_trans ? 2048 >> 4 : 32 >> 4;   // to the next 16 k
+        const int last = static_cast<int>((p.K - static_cast<int64_t>(pl.ks - 1) * kDepth + 15) / 16);   // products of the last stage
+        const uint64_t da0 = smem_desc(smem_addr(stage_a), p.a_trans), db0 = smem_desc(smem_addr(stage_b), p.b_trans);
+        uint32_t q = 0, s = 0, use = 0, tile = 0;
         bool ok = true;
         for (int64_t u = cluster; u < pl.units && ok; u += clusters, ++tile) {
             const Unit un = unit_of(pl, u);
-            const uint32_t buf = tile & 1u;
-            if (tile >= 2 && !bar_wait(&bars->tmem_empty[buf], (tile / 2 - 1) & 1u, pl.wait_cycles, abort)) {
+            const uint32_t buf = tile & 1u, d = tmem + buf * 256;
+            if (tile >= 2 &&
+                !__all_sync(0xffffffffu, bar_wait(&bars->tmem_empty[buf], (tile / 2 - 1) & 1u, pl.wait_cycles, abort))) {
                 ok = false;
                 break;
             }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            for (int k = un.k0; k < un.k1; ++k, ++q) {
-                const uint32_t s = q % kStages;
-                if (!bar_wait(&bars->full[s], (q / kStages) & 1u, pl.wait_cycles, abort)) {
+            for (int k = un.k0; k < un.k1; ++k) {
+                if (!__all_sync(0xffffffffu, bar_wait(&bars->full[s], use, pl.wait_cycles, abort))) {
                     ok = false;
                     break;
                 }
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint64_t da = smem_desc(smem_addr(stage_a + s * kStageA), p.a_trans);
-                const uint64_t db = smem_desc(smem_addr(stage_b + s * kStageB), p.b_trans);
+                if (elect_one()) {
+                    const uint64_t da = da0 + s * (kStageA >> 4), db = db0 + s * (kStageB >> 4);
+                    const int count = k + 1 == pl.ks ? last : kDepth / 16;
 #pragma unroll
-                for (int i = 0; i < kDepth / 16; ++i)
-                    mma(tmem + buf * 256, da + i * step_a, db + i * step_b, idesc, (k > un.k0 || i > 0) ? 1u : 0u);
-                mma_commit(&bars->empty[s]);
-                bars->consumed = q + 1;
+                    for (int i = 0; i < kDepth / 16; ++i)
+                        if (i < count)
+                            mma(d, da + i * step_a, db + i * step_b, idesc, i > 0 ? 1u : static_cast<uint32_t>(k > un.k0));
+                    mma_commit(&bars->empty[s]);
+                    if (k + 1 == un.k1) mma_commit(&bars->tmem_full[buf]);
+                    bars->consumed = q + 1;
+                }
+                ++q;
+                if (++s == kStages) {
+                    s = 0;
+                    use ^= 1u;
+                }
             }
-            if (ok) mma_commit(&bars->tmem_full[buf]);
         }
-        if (!ok) {
+        if (!ok && elect_one()) {
             // give up: report, then wait for the matrix instructions in flight
             atomicOr(pl.status, FSDP_KSTATUS_WAIT_TIMEOUT);
             *abort = 1;
@@ -430,18 +461,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // no CTA leaves while its pair may still read its shared memory or arrive on its barriers
     cluster_sync();
     if (rank == 0 && threadIdx.x == 0) {
-        const uint32_t peer = remote_addr(smem_addr(&bars->issued), 1);
-        uint32_t theirs;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(theirs) : "r"(peer) : "memory");
-        const uint32_t ours = bars->issued;
+        uint32_t issued[4] = {bars->issued[0], bars->issued[1], 0, 0}, most = 0;
+        for (int i = 0; i < 2; ++i)
+            asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                         : "=r"(issued[2 + i])
+                         : "r"(remote_addr(smem_addr(&bars->issued[i]), 1))
+                         : "memory");
+        for (int i = 0; i < 4; ++i) most = max(most, issued[i]);
         // after a give-up: copies in flight still land before either CTA leaves.
-        // Each stage that one side alone issued gets the other's arrival here.
+        // A stage that only some of the four producers issued gets the others'
+        // arrivals here.
         const volatile uint32_t never = 0;
-        for (uint32_t q = bars->consumed; q < max(ours, theirs); ++q) {
+        for (uint32_t q = bars->consumed; q < most; ++q) {
             const uint32_t bar = remote_addr(smem_addr(&bars->full[q % kStages]), 0);
             if (pl.withhold && blockIdx.x < 2 && q == 0) continue;   // armed, but no copy was issued
-            if (q >= ours) bar_arrive_remote(bar);
-            if (q >= theirs) bar_arrive_remote(bar);
+            for (int i = 0; i < 4; ++i)
+                if (q >= issued[i]) bar_arrive_remote(bar);
             if (!bar_wait(&bars->full[q % kStages], (q / kStages) & 1u, pl.wait_cycles, &never))
                 atomicOr(pl.status, FSDP_KSTATUS_DRAIN_TIMEOUT);
         }
@@ -585,10 +620,10 @@ cudaError_t make_map(CUtensorMap* map, const Mat& m, int64_t rows, int64_t cols,
 // Tiles, and how the last ones are shared: the clusters take whole tiles in
 // turn; what is left over after the last full round may be cut along k so that
 // every cluster has a part.  The width and the choice are those of the least
-// estimated time, in cycles: a stage of 64 k takes 2 a column on the tensor
-// cores, and its copies' bytes at kCopyRate a cycle.
-constexpr double kCopyRate = 60.0;
-
+// estimated time, in cycles.  Measured with whole rounds of tiles: a stage takes
+// 2.34 cycles a column where the products bound it (256: 600, 192: 455), and
+// otherwise what its copies take (20 KiB an SM: 382, 24 KiB: 410, 32 KiB: 500),
+// which is the rate at which an SM takes data from L2, about 60 bytes a cycle.
 Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, int clusters) {
     Plan best{};
     double least = 0;
@@ -600,9 +635,9 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, int clu
         p.tiles_m = static_cast<int>((rows + 255) / 256);
         p.tiles_n = static_cast<int>((cols + bn - 1) / bn);
         const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-        const double copied = 16384.0 + (b_by_rows ? (bn > 128 ? 16384.0 : 8192.0) : 64.0 * bn);
-        const double stage = std::max(2.0 * bn, copied / kCopyRate);
-        const double tail = 8.0 * bn + 1500.0;   // the last tile's epilogue, and the kernel's start and end
+        const double steps = static_cast<double>((k + 15) / 16) / (kDepth / 16);   // stages, the last one in part
+        const double copied = kStageA + (b_by_rows ? (bn > 128 ? 2.0 : 1.0) * kBlock : 64.0 * bn);
+        const double stage = std::max(2.34 * bn, 382.0 + 0.0095 * (copied - 20480.0));
         for (int share = 0; share < 2; ++share) {
             const int64_t left = tiles % clusters;
             p.parts = share == 0 || left == 0 ? 1 : static_cast<int>(std::min<int64_t>(clusters / left, std::max(1, p.ks / 4)));
@@ -610,8 +645,8 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, int clu
             p.whole = p.parts > 1 ? tiles - left : tiles;
             p.units = p.whole + (tiles - p.whole) * p.parts;
             const double rounds = static_cast<double>((p.whole + clusters - 1) / clusters);
-            double t = rounds * std::max(p.ks * stage, 2500.0 + 10.0 * bn) + tail;
-            if (p.parts > 1) t += (p.ks / p.parts + 1) * stage + 6500.0 + 150.0 * p.parts;
+            double t = rounds * (std::max(steps * stage, 2500.0 + 10.0 * bn) + 300.0) + 10.0 * bn;
+            if (p.parts > 1) t += (p.ks + p.parts - 1) / p.parts * stage + 11000.0 + 150.0 * p.parts;
             if (least == 0 || t < least) {
                 least = t;
                 best = p;
@@ -718,8 +753,8 @@ cudaError_t launch_product(const Product& given, const ProductRoom& room, int sm
     pl.wait_cycles = static_cast<long long>(room.wait_ns) * 2;   // the SM clock is at most 2.07 GHz
     pl.withhold = room.withhold;
     CUtensorMap map_a, map_b;
-    e = p.a_trans ? make_map(&map_a, p.a, p.K, rows, 64) : make_map(&map_a, p.a, rows, p.K, 128);
-    if (e == cudaSuccess) e = p.b_trans ? make_map(&map_b, p.b, p.K, cols, 64) : make_map(&map_b, p.b, cols, p.K, pl.bn / 2);
+    e = p.a_trans ? make_map(&map_a, p.a, p.K, rows, kDepth) : make_map(&map_a, p.a, rows, p.K, 128);
+    if (e == cudaSuccess) e = p.b_trans ? make_map(&map_b, p.b, p.K, cols, kDepth) : make_map(&map_b, p.b, cols, p.K, pl.bn / 2);
     if (e != cudaSuccess) return e;
     const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(pl.units, clusters));
     kProductKernels[p.slope][pl.vec]<<<grid, kThreads, kSmemBytes, st>>>(map_a, map_b, p, pl);
