@@ -16,6 +16,8 @@ namespace {
 // (their strides are the format's), so a group's place in them is its index.
 template <bool WIDE, bool PACK>
 __global__ void __launch_bounds__(256) act8_groups_kernel(int64_t cols, Mat q, int act, Mat x, int64_t count, uint32_t groups) {
+    starts_early();
+    after_previous();
     const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
     for (int64_t g = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; g < count; g += stride) {
         // a 32-bit division where the index allows it
@@ -38,6 +40,8 @@ __global__ void __launch_bounds__(256) act8_groups_kernel(int64_t cols, Mat q, i
 // in flight.
 template <bool PACK>
 __global__ void __launch_bounds__(256) act8_elements_kernel(int64_t cols, Mat q, int act, Mat x, int64_t count, uint32_t groups) {
+    starts_early();
+    after_previous();
     constexpr int U = 4;
     const int lane = threadIdx.x & 31;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * 8;
@@ -84,13 +88,12 @@ cudaError_t launch(int64_t rows, int64_t cols, const Mat& q, int act, const Mat&
         return static_cast<unsigned>(std::min((count + per_block - 1) / per_block, static_cast<int64_t>(sms) * 24));
     };
     const uint32_t gr = static_cast<uint32_t>(groups);
-    if (rows_aligned(x, 32) && rows_aligned(q, 32) && cols % 16 == 0)
-        act8_groups_kernel<true, PACK><<<blocks(256), 256, 0, st>>>(cols, q, act, x, count, gr);
-    else if (rows_aligned(x) && cols % 8 == 0)
-        act8_groups_kernel<false, PACK><<<blocks(256), 256, 0, st>>>(cols, q, act, x, count, gr);
-    else
-        act8_elements_kernel<PACK><<<blocks(32), 256, 0, st>>>(cols, q, act, x, count, gr);
-    return cudaGetLastError();
+    if (rows_aligned(x) && cols % 8 == 0) {
+        const bool wide = rows_aligned(x, 32) && rows_aligned(q, 32) && cols % 16 == 0;
+        return launch_early(wide ? act8_groups_kernel<true, PACK> : act8_groups_kernel<false, PACK>, dim3(blocks(256)), 256, 0, st,
+                            cols, q, act, x, count, gr);
+    }
+    return launch_early(act8_elements_kernel<PACK>, dim3(blocks(32)), 256, 0, st, cols, q, act, x, count, gr);
 }
 
 }  // namespace

@@ -19,6 +19,25 @@ struct Mat {
     int dtype;   // FSDP_DTYPE_*
 };
 
+// Every kernel of the block operators is launched so that its start may overlap
+// the end of the kernel before it (programmatic stream serialization): it lets
+// the kernel after it start early (starts_early), and touches memory only
+// after everything before it in the stream is complete (after_previous).
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t shared, cudaStream_t st, const Args&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = shared;
+    cfg.stream = st;
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
 constexpr int kGroup = 32;   // elements that share an exponent in an ACT8 matrix
 
 inline int64_t act8_groups(int64_t cols) { return (cols + kGroup - 1) / kGroup; }

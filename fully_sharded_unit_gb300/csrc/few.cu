@@ -164,6 +164,8 @@ __global__ void __launch_bounds__(few_threads(T, BY_COLUMNS)) few_rows_kernel(co
     constexpr int kWarps = few_threads(T, BY_COLUMNS) / 32;
     __shared__ float part[kWarps][T][33];
     __shared__ float total[T][33];
+    starts_early();
+    after_previous();
     cg::cluster_group cluster = cg::this_cluster();
     const int parts = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int64_t n0 = static_cast<int64_t>(blockIdx.x / parts) * 32;
@@ -216,15 +218,17 @@ cudaError_t launch_few_rows(const Product& p, int sms, cudaStream_t st) {
     // parts of k, of at least 256 each, until every SM has a block
     int parts = 1;
     while (parts < 8 && blocks * parts < sms && p.K >= 512 * parts) parts *= 2;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = static_cast<unsigned>(parts);
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(parts);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks * parts));
     cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = parts > 1 ? 2 : 1;
     const bool vec = rows_aligned(p.a) && rows_aligned(p.b) && (!p.b_trans || p.N % 8 == 0);
     if (p.M == 1) return vec ? run<8, 1>(p, cfg) : run<1, 1>(p, cfg);
     if (p.M <= 4) return vec ? run<8, 4>(p, cfg) : run<1, 4>(p, cfg);

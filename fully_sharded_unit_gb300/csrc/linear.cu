@@ -30,31 +30,31 @@ namespace {
 // both ways, x and dy too): the copies take boxes of 64 elements along the
 // contiguous direction, and only the shared-memory descriptors differ.
 
-constexpr int kStages = 6;
+constexpr int kStagesMost = 10;
 constexpr int kDepth = 64;                       // k per stage (3 stages of 128 were 4 % slower at 8192^3)
 constexpr int kBlock = 64 * kDepth * 2;          // a box of an operand that is contiguous along its rows: 64 rows
 constexpr int kStageA = 128 * kDepth * 2;        // bytes of A in a stage, per CTA
-constexpr int kStageB = 128 * kDepth * 2;        // of B, at BN = 256
-static_assert(kStageA == kStageB, "one stride for both operands' stages");
 constexpr int kEpiWarps = 8;
 constexpr int kEpiBytes = 32 * 32 * 4;           // a warp's transposing buffer
 constexpr int kThreads = 384;
 constexpr int kPiece = 32 * 128;                 // floats of a warp's part of a tile
 constexpr int kPieces = 2 * kEpiWarps;           // parts of a tile
-constexpr size_t kSmemBytes = 1024 + kStages * (kStageA + kStageB) + kEpiWarps * kEpiBytes + 256;
+constexpr int kRingBytes = 6 * (128 + 128) * 64 * 2;   // 6 stages at BN = 256, more of narrower tiles
+constexpr size_t kSmemBytes = 1024 + kRingBytes + kEpiWarps * kEpiBytes + 320;
 
 struct Bars {
-    uint64_t full[kStages];      // first CTA's: both CTAs' copies of a stage, A's and B's, have landed
-    uint64_t empty[kStages];     // the products that read a stage are done
+    uint64_t full[kStagesMost];      // first CTA's: both CTAs' copies of a stage, A's and B's, have landed
+    uint64_t empty[kStagesMost];     // the products that read a stage are done
     uint64_t tmem_full[2];       // a tile's sums are complete
     uint64_t tmem_empty[2];      // first CTA's: both CTAs' epilogues have read them
     uint64_t drain;
     uint32_t tmem_base;
     uint32_t abort;              // a wait of this CTA ran out
+    uint32_t pair_abort;         // one of the other CTA did
     uint32_t issued[2];          // stages the producers issued: of A, of B
     uint32_t consumed;           // stages the matrix instructions read
 };
-static_assert(sizeof(Bars) <= 256, "the barriers' room");
+static_assert(sizeof(Bars) <= 320, "the barriers' room");
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -174,6 +174,7 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool by_rows) {
 struct Plan {
     int ks;                    // stages' worth of k
     int bn;                    // columns of a tile: 32 .. 256 in steps of 32
+    int stages, stage_b;       // stages in the ring, and B's bytes in one, per CTA
     int tiles_m, tiles_n;
     int64_t whole;             // tiles done by one cluster each
     int64_t units;             // whole + (tiles - whole) * parts
@@ -243,27 +244,22 @@ __device__ __forceinline__ void finish_chunk(const Product& p, const Plan& pl, i
         }
         if (row0 + lane < p.M) finish_row<VEC == 2, SLOPE>(p, row0 + lane, col0, buf, v);
     } else {
-#pragma unroll
-        for (int s = 0; s < 8; ++s)
-            buf[lane * 8 + (s ^ (lane & 7))] = make_float4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]);
-        __syncwarp();
-        // one column of C to a lane; swapped, a lane's tile row is that column
-        const float* f = reinterpret_cast<const float*>(buf);
+        // one column of C to a lane
         const int64_t m0 = pl.swapped ? col0 : row0, n = (pl.swapped ? row0 : col0) + lane;
         const int count = static_cast<int>(min(static_cast<int64_t>(32), p.M - m0));
+        if (count <= 0 || n - lane >= p.N) return;   // the same for the whole warp
         const float bias = p.bias != nullptr && n < p.N ? load1(p.bias, p.bias_dtype, n) : 0.0f;
-        if (n - lane < p.N) {
-            for (int i = 0; i < count; i += 8) {
-                float w[8];
+        if (!pl.swapped) {   // swapped, the lane's tile row is that column already
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int r = pl.swapped ? lane : i + j, c = pl.swapped ? i + j : lane;
-                    w[j] = f[r * 32 + (((c >> 2) ^ (r & 7)) << 2) + (c & 3)];
-                }
-                finish_column<8, SLOPE>(p, m0 + i, count - i, n, bias, w, lane);
-            }
+            for (int s = 0; s < 8; ++s)
+                buf[lane * 8 + (s ^ (lane & 7))] = make_float4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]);
+            __syncwarp();
+            const float* f = reinterpret_cast<const float*>(buf);
+#pragma unroll
+            for (int r = 0; r < 32; ++r) v[r] = f[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)];
+            __syncwarp();
         }
-        __syncwarp();
+        finish_column<32, SLOPE>(p, m0, count, n, bias, v, lane);
     }
 }
 
@@ -278,17 +274,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // CTAs of the pair compute the same offset
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t* stage_a = smem;
-    uint8_t* stage_b = smem + kStages * kStageA;
-    float4* epi = reinterpret_cast<float4*>(smem + kStages * (kStageA + kStageB));
-    Bars* bars = reinterpret_cast<Bars*>(smem + kStages * (kStageA + kStageB) + kEpiWarps * kEpiBytes);
+    uint8_t* stage_b = smem + pl.stages * kStageA;
+    float4* epi = reinterpret_cast<float4*>(smem + kRingBytes);
+    Bars* bars = reinterpret_cast<Bars*>(smem + kRingBytes + kEpiWarps * kEpiBytes);
     volatile uint32_t* abort = &bars->abort;
+    const uint32_t stages = pl.stages;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int64_t cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < pl.stages; ++i) {
             bar_init(&bars->full[i], 4);
             bar_init(&bars->empty[i], 1);
         }
@@ -297,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bar_init(&bars->tmem_empty[i], 2 * kEpiWarps);
         }
         bar_init(&bars->drain, 1);
-        bars->abort = bars->issued[0] = bars->issued[1] = bars->consumed = 0;
+        bars->abort = bars->pair_abort = bars->issued[0] = bars->issued[1] = bars->consumed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_b) : "memory");
@@ -313,6 +310,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = bars->tmem_base;
+    starts_early();
+    after_previous();
     // The producer's and the matrix warp's loops run in whole warps, with one
     // lane elected to issue: their counters and descriptors are then uniform.
     // (In a branch of one lane, each matrix instruction took 65 cycles to issue
@@ -324,9 +323,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool by_rows = is_a ? p.a_trans : p.b_trans;
         const int extent = is_a ? 128 : pl.bn / 2;                     // rows of the operand in a stage, per CTA
         const bool second = by_rows && extent > 64;                    // a box holds 64 of them
-        const uint32_t bytes = by_rows ? (second ? 2 * kBlock : kBlock) : extent * kDepth * 2;
+        const uint32_t bytes = is_a ? kStageA : pl.stage_b;
         const uint32_t full0 = remote_addr(smem_addr(&bars->full[0]), 0);
-        const uint32_t stage0 = smem_addr(is_a ? stage_a : stage_b);
+        const uint32_t stage0 = smem_addr(is_a ? stage_a : stage_b), stride = is_a ? kStageA : pl.stage_b;
         const bool withheld = pl.withhold && blockIdx.x < 2;
         uint32_t* issued = &bars->issued[is_a ? 0 : 1];
         uint32_t q = 0, s = 0, use = 0;   // stages issued, the next one's place and how often the ring went round (parity)
@@ -335,12 +334,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const Unit un = unit_of(pl, u);
             const int at = (is_a ? un.tm * 256 : un.tn * pl.bn) + static_cast<int>(rank) * extent;
             for (int k = un.k0; k < un.k1; ++k) {
-                if (q >= kStages && !__all_sync(0xffffffffu, bar_wait(&bars->empty[s], use ^ 1u, pl.wait_cycles, abort))) {
+                if (q >= stages && !__all_sync(0xffffffffu, bar_wait(&bars->empty[s], use ^ 1u, pl.wait_cycles, abort))) {
                     ok = false;
                     break;
                 }
                 if (elect_one()) {
-                    const uint32_t full = full0 + s * 8, dst = stage0 + s * kStageA;
+                    const uint32_t full = full0 + s * 8, dst = stage0 + s * stride;
                     bar_expect_remote(full, bytes);
                     if (!(withheld && q == 0)) {
                         if (!by_rows) {
@@ -353,15 +352,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     *issued = q + 1;
                 }
                 ++q;
-                if (++s == kStages) {
+                if (++s == stages) {
                     s = 0;
                     use ^= 1u;
                 }
             }
         }
         // the stages still being read: their commits arrive here before this CTA leaves
-        for (uint32_t i = q > kStages ? q - kStages : 0; ok && i < q; ++i)
-            ok = __all_sync(0xffffffffu, bar_wait(&bars->empty[i % kStages], (i / kStages) & 1u, pl.wait_cycles, abort));
+        for (uint32_t i = q > stages ? q - stages : 0; ok && i < q; ++i)
+            ok = __all_sync(0xffffffffu, bar_wait(&bars->empty[i % stages], (i / stages) & 1u, pl.wait_cycles, abort));
         if (!ok && lane == 0) {
             atomicOr(pl.status, FSDP_KSTATUS_WAIT_TIMEOUT);
             *abort = 1;
@@ -391,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 if (elect_one()) {
-                    const uint64_t da = da0 + s * (kStageA >> 4), db = db0 + s * (kStageB >> 4);
+                    const uint64_t da = da0 + s * (kStageA >> 4), db = db0 + s * (pl.stage_b >> 4);
                     const int count = k + 1 == pl.ks ? last : kDepth / 16;
 #pragma unroll
                     for (int i = 0; i < kDepth / 16; ++i)
@@ -402,7 +401,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     bars->consumed = q + 1;
                 }
                 ++q;
-                if (++s == kStages) {
+                if (++s == stages) {
                     s = 0;
                     use ^= 1u;
                 }
@@ -458,30 +457,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 
     __syncthreads();
+    if (threadIdx.x == 0 && *abort != 0)   // the pair gives up together
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote_addr(smem_addr(&bars->pair_abort), rank ^ 1u)), "r"(1) : "memory");
     // no CTA leaves while its pair may still read its shared memory or arrive on its barriers
     cluster_sync();
-    if (rank == 0 && threadIdx.x == 0) {
-        uint32_t issued[4] = {bars->issued[0], bars->issued[1], 0, 0}, most = 0;
-        for (int i = 0; i < 2; ++i)
-            asm volatile("ld.shared::cluster.u32 %0, [%1];"
-                         : "=r"(issued[2 + i])
-                         : "r"(remote_addr(smem_addr(&bars->issued[i]), 1))
-                         : "memory");
-        for (int i = 0; i < 4; ++i) most = max(most, issued[i]);
-        // after a give-up: copies in flight still land before either CTA leaves.
-        // A stage that only some of the four producers issued gets the others'
-        // arrivals here.
-        const volatile uint32_t never = 0;
-        for (uint32_t q = bars->consumed; q < most; ++q) {
-            const uint32_t bar = remote_addr(smem_addr(&bars->full[q % kStages]), 0);
-            if (pl.withhold && blockIdx.x < 2 && q == 0) continue;   // armed, but no copy was issued
-            for (int i = 0; i < 4; ++i)
-                if (q >= issued[i]) bar_arrive_remote(bar);
-            if (!bar_wait(&bars->full[q % kStages], (q / kStages) & 1u, pl.wait_cycles, &never))
-                atomicOr(pl.status, FSDP_KSTATUS_DRAIN_TIMEOUT);
+    if (*abort != 0 || *static_cast<volatile uint32_t*>(&bars->pair_abort) != 0) {
+        if (rank == 0 && threadIdx.x == 0) {
+            uint32_t issued[4] = {bars->issued[0], bars->issued[1], 0, 0}, most = 0;
+            for (int i = 0; i < 2; ++i)
+                asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                             : "=r"(issued[2 + i])
+                             : "r"(remote_addr(smem_addr(&bars->issued[i]), 1))
+                             : "memory");
+            for (int i = 0; i < 4; ++i) most = max(most, issued[i]);
+            // after a give-up: copies in flight still land before either CTA leaves.
+            // A stage that only some of the four producers issued gets the others'
+            // arrivals here.
+            const volatile uint32_t never = 0;
+            for (uint32_t q = bars->consumed; q < most; ++q) {
+                const uint32_t bar = remote_addr(smem_addr(&bars->full[q % stages]), 0);
+                if (pl.withhold && blockIdx.x < 2 && q == 0) continue;   // armed, but no copy was issued
+                for (int i = 0; i < 4; ++i)
+                    if (q >= issued[i]) bar_arrive_remote(bar);
+                if (!bar_wait(&bars->full[q % stages], (q / stages) & 1u, pl.wait_cycles, &never))
+                    atomicOr(pl.status, FSDP_KSTATUS_DRAIN_TIMEOUT);
+            }
         }
+        cluster_sync();
     }
-    cluster_sync();
     if (warp == 2)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
@@ -492,6 +495,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 template <int V>
 __global__ void __launch_bounds__(256) column_sum_kernel(int64_t rows, int64_t cols, Mat dy, float* partials) {
     __shared__ float part[8][32 * V + 1];
+    starts_early();
+    after_previous();
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + tx) * V;
     float s[V];
@@ -535,7 +540,8 @@ __global__ void __launch_bounds__(256) column_sum_kernel(int64_t rows, int64_t c
 template <int VEC, bool SLOPE>
 __global__ void __launch_bounds__(128) finish_kernel(const __grid_constant__ Product p, const __grid_constant__ Plan pl) {
     __shared__ float4 buf[4][256];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    starts_early();
+    after_previous();
     const int lane = threadIdx.x & 31, chunks = pl.bn / 32;
     const int64_t job = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     const int64_t shared = job / (8 * chunks);
@@ -563,6 +569,8 @@ __global__ void __launch_bounds__(128) finish_kernel(const __grid_constant__ Pro
 // Rows of a bf16 matrix that do not start on 16-byte boundaries, copied to
 // ones that do (dst.ld a multiple of 8).
 __global__ void __launch_bounds__(256) align_rows_kernel(int64_t rows, int64_t cols, Mat src, Mat dst) {
+    starts_early();
+    after_previous();
     const int64_t chunks = (cols + 7) / 8;
     for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
         const uint16_t* s = static_cast<const uint16_t*>(src.p) + row * src.ld;
@@ -636,7 +644,9 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, int clu
         p.tiles_n = static_cast<int>((cols + bn - 1) / bn);
         const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
         const double steps = static_cast<double>((k + 15) / 16) / (kDepth / 16);   // stages, the last one in part
-        const double copied = kStageA + (b_by_rows ? (bn > 128 ? 2.0 : 1.0) * kBlock : 64.0 * bn);
+        p.stage_b = b_by_rows ? (bn > 128 ? 2 : 1) * kBlock : bn / 2 * kDepth * 2;   // a multiple of 1024
+        p.stages = std::min(kStagesMost, kRingBytes / (kStageA + p.stage_b));
+        const double copied = kStageA + p.stage_b;
         const double stage = std::max(2.34 * bn, 382.0 + 0.0095 * (copied - 20480.0));
         for (int share = 0; share < 2; ++share) {
             const int64_t left = tiles % clusters;
@@ -705,8 +715,7 @@ cudaError_t settle(Mat* m, int64_t rows, int64_t cols, char** room, int sms, cud
     } else {
         const dim3 grid(static_cast<unsigned>(std::min<int64_t>((d.ld / 8 + 255) / 256, 1024)),
                         static_cast<unsigned>(std::min<int64_t>(rows, 65535)));
-        align_rows_kernel<<<grid, 256, 0, st>>>(rows, cols, *m, d);
-        e = cudaGetLastError();
+        e = launch_early(align_rows_kernel, grid, 256, 0, st, rows, cols, *m, d);
     }
     *m = d;
     return e;
@@ -757,20 +766,11 @@ cudaError_t launch_product(const Product& given, const ProductRoom& room, int sm
     if (e == cudaSuccess) e = p.b_trans ? make_map(&map_b, p.b, p.K, cols, kDepth) : make_map(&map_b, p.b, cols, p.K, pl.bn / 2);
     if (e != cudaSuccess) return e;
     const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(pl.units, clusters));
-    kProductKernels[p.slope][pl.vec]<<<grid, kThreads, kSmemBytes, st>>>(map_a, map_b, p, pl);
-    e = cudaGetLastError();
+    e = launch_early(kProductKernels[p.slope][pl.vec], dim3(grid), kThreads, kSmemBytes, st, map_a, map_b, p, pl);
     const int64_t shared = static_cast<int64_t>(pl.tiles_m) * pl.tiles_n - pl.whole;
     if (e != cudaSuccess || shared == 0) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>((shared * 8 * (pl.bn / 32) + 3) / 4));
-    cfg.blockDim = dim3(128);
-    cfg.stream = st;
-    cudaLaunchAttribute early{};   // its launch overlaps the product's end; it waits for all of it before it reads
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kFinishKernels[p.slope][pl.vec], p, pl);
+    return launch_early(kFinishKernels[p.slope][pl.vec], dim3(static_cast<unsigned>((shared * 8 * (pl.bn / 32) + 3) / 4)), 128, 0,
+                        st, p, pl);
 }
 
 int64_t column_sum_partials(int64_t rows, int64_t cols, int sms) {
@@ -784,13 +784,9 @@ cudaError_t launch_column_sum(int64_t rows, int64_t cols, const Mat& dy, float* 
     int64_t count = 0;
     if (rows > 0) {
         count = column_sum_partials(rows, cols, sms);
-        if (rows_aligned(dy) && cols % 8 == 0)
-            column_sum_kernel<8><<<dim3(static_cast<unsigned>((cols + 255) / 256), static_cast<unsigned>(count)), 256, 0, st>>>(
-                rows, cols, dy, partials);
-        else
-            column_sum_kernel<1><<<dim3(static_cast<unsigned>((cols + 31) / 32), static_cast<unsigned>(count)), 256, 0, st>>>(
-                rows, cols, dy, partials);
-        const cudaError_t e = cudaGetLastError();
+        const bool vec = rows_aligned(dy) && cols % 8 == 0;
+        const dim3 grid(static_cast<unsigned>(vec ? (cols + 255) / 256 : (cols + 31) / 32), static_cast<unsigned>(count));
+        const cudaError_t e = launch_early(vec ? column_sum_kernel<8> : column_sum_kernel<1>, grid, 256, 0, st, rows, cols, dy, partials);
         if (e != cudaSuccess) return e;
     }
     return launch_sum_partials(partials, count, cols, cols, out, out_dtype, accumulate, st);

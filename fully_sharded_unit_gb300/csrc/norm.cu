@@ -34,6 +34,8 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 template <int V, int NV, bool WARP>
 __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_forward_kernel(NormForward a) {
     __shared__ float red[2][32];
+    starts_early();
+    after_previous();
     const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
     const int threads = WARP ? 32 : blockDim.x;
     const int64_t first = WARP ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;
@@ -97,6 +99,8 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_forward_kernel(NormFor
 // Rows too long for registers: three passes, the later ones from L2.
 __global__ void __launch_bounds__(1024) norm_forward_wide_kernel(NormForward a) {
     __shared__ float red[2][32];
+    starts_early();
+    after_previous();
     const float n = static_cast<float>(a.cols);
     const int64_t ceil32 = (a.cols + 31) / 32 * 32;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -315,6 +319,8 @@ template <int NV, int GT, int THREADS, bool FAST>
 __global__ void __launch_bounds__(THREADS) norm_forward_ring_kernel(const __grid_constant__ NormForward a, int places) {
     extern __shared__ __align__(16) uint8_t ring_bytes[];
     __shared__ __align__(16) float red[2][32];
+    starts_early();
+    after_previous();
     const int g = threadIdx.x / GT, t = threadIdx.x % GT, G = blockDim.x / GT;
     const bool end = (t + (NV - 1) * GT) * 8 < a.cols;
     const Rows<NV, GT, FAST> gammas(vector_row(a.gamma, a.param_dtype), ring_bytes, 0, 1, t);
@@ -408,6 +414,8 @@ template <int NV, int GT, int THREADS, bool FAST>
 __global__ void __launch_bounds__(THREADS) norm_backward_ring_kernel(const __grid_constant__ NormBackward a, int places) {
     extern __shared__ __align__(16) uint8_t ring_bytes[];
     __shared__ __align__(16) float2 red[2][32];
+    starts_early();
+    after_previous();
     const int g = threadIdx.x / GT, t = threadIdx.x % GT, G = blockDim.x / GT;
     const bool end = (t + (NV - 1) * GT) * 8 < a.cols;
     uint8_t* at = ring_bytes;
@@ -578,6 +586,8 @@ template <int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_backward_kernel(NormBackward a, int gt) {
     extern __shared__ __align__(16) uint8_t ring_bytes[];
     __shared__ float2 red[2][THREADS / 32];
+    starts_early();
+    after_previous();
     const int g = threadIdx.x / gt, t = threadIdx.x % gt, G = blockDim.x / gt;
     const float inv_n = 1.0f / static_cast<float>(a.cols);
     float dg[NV], db[NV];
@@ -654,6 +664,8 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(NormBackward a, 
 // column sums from dy and x once more.
 __global__ void __launch_bounds__(1024) norm_backward_wide_dx_kernel(NormBackward a) {
     __shared__ float red[2][32];
+    starts_early();
+    after_previous();
     const float inv_n = 1.0f / static_cast<float>(a.cols);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const float mean = a.mean[row], rstd = a.rstd[row];
@@ -679,6 +691,8 @@ __global__ void __launch_bounds__(1024) norm_backward_wide_dx_kernel(NormBackwar
 }
 
 __global__ void __launch_bounds__(256) norm_backward_wide_sums_kernel(NormBackward a) {
+    starts_early();
+    after_previous();
     const int64_t c = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (c >= a.cols) return;
     float dg = 0.0f, db = 0.0f;
@@ -701,7 +715,8 @@ template <int V>
 __global__ void __launch_bounds__(256) sum_partials_kernel(const float* partials, int64_t count, int64_t stride, int64_t second,
                                                            int64_t cols, void* out0, void* out1, int dtype, int accumulate) {
     __shared__ float part[16][16 * V];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    starts_early();
+    after_previous();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int64_t c = (static_cast<int64_t>(blockIdx.x) * 16 + tx) * V;
     const float* p = partials + (blockIdx.y ? second : 0) + c;
@@ -736,17 +751,9 @@ __global__ void __launch_bounds__(256) sum_partials_kernel(const float* partials
 cudaError_t sum_partials(const float* partials, int64_t count, int64_t stride, int64_t second, int64_t cols,
                          void* out0, void* out1, int dtype, int accumulate, cudaStream_t st) {
     const bool vec = cols % 4 == 0;   // the workspace is aligned
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(vec ? (cols + 63) / 64 : (cols + 15) / 16), out1 != nullptr ? 2 : 1);
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cudaLaunchAttribute early{};   // its launch overlaps the kernel before it; it waits for all of that before it reads
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, vec ? sum_partials_kernel<4> : sum_partials_kernel<1>, partials, count, stride, second,
-                              cols, out0, out1, dtype, accumulate);
+    const dim3 grid(static_cast<unsigned>(vec ? (cols + 63) / 64 : (cols + 15) / 16), out1 != nullptr ? 2 : 1);
+    return launch_early(vec ? sum_partials_kernel<4> : sum_partials_kernel<1>, grid, 256, 0, st, partials, count, stride, second,
+                        cols, out0, out1, dtype, accumulate);
 }
 
 int round32(int64_t n) { return static_cast<int>((n + 31) / 32 * 32); }
@@ -754,13 +761,10 @@ int round32(int64_t n) { return static_cast<int>((n + 31) / 32 * 32); }
 template <int V, int NV>
 cudaError_t run_forward(const NormForward& a, int64_t chunks, cudaStream_t st) {
     const int64_t cap = int64_t(1) << 30;
-    if (chunks <= 32 * NV) {
-        norm_forward_kernel<V, NV, true><<<static_cast<unsigned>(std::min((a.rows + 3) / 4, cap)), 128, 0, st>>>(a);
-    } else {
-        norm_forward_kernel<V, NV, false><<<static_cast<unsigned>(std::min(a.rows, cap)),
-                                            round32((chunks + NV - 1) / NV), 0, st>>>(a);
-    }
-    return cudaGetLastError();
+    if (chunks <= 32 * NV)
+        return launch_early(norm_forward_kernel<V, NV, true>, dim3(static_cast<unsigned>(std::min((a.rows + 3) / 4, cap))), 128, 0, st, a);
+    return launch_early(norm_forward_kernel<V, NV, false>, dim3(static_cast<unsigned>(std::min(a.rows, cap))),
+                        round32((chunks + NV - 1) / NV), 0, st, a);
 }
 
 // How a row is split: threads to it, chunks (or columns) to a thread, rows to a
@@ -817,8 +821,7 @@ template <auto kernel, typename... Args>
 cudaError_t launch_shared(unsigned blocks, int threads, int bytes, cudaStream_t st, const Args&... args) {
     static const cudaError_t allowed = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedMost);
     if (allowed != cudaSuccess) return allowed;
-    kernel<<<blocks, threads, bytes, st>>>(args...);
-    return cudaGetLastError();
+    return launch_early(kernel, dim3(blocks), threads, static_cast<size_t>(bytes), st, args...);
 }
 
 }  // namespace
@@ -852,8 +855,7 @@ cudaError_t launch_norm_forward(const NormForward& a, int sms, cudaStream_t st) 
         if (a.cols <= 4096) return run_forward<1, 8>(a, a.cols, st);
         if (a.cols <= 16384) return run_forward<1, 16>(a, a.cols, st);
     }
-    norm_forward_wide_kernel<<<static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t(1) << 30)), 1024, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(norm_forward_wide_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t(1) << 30))), 1024, 0, st, a);
 }
 
 int64_t norm_partials(int64_t rows, int64_t cols, int sms) {
@@ -871,12 +873,10 @@ cudaError_t launch_norm_backward(const NormBackward& a, int sms, cudaStream_t st
     if (a.rows == 0) {
         count = 0;
     } else if (p.NV == 0) {
-        norm_backward_wide_dx_kernel<<<static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t(1) << 30)), 1024, 0, st>>>(a);
-        e = cudaGetLastError();
+        e = launch_early(norm_backward_wide_dx_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t(1) << 30))), 1024, 0, st, a);
         if (e != cudaSuccess) return e;
         const dim3 grid(static_cast<unsigned>((a.cols + 255) / 256), blocks);
-        norm_backward_wide_sums_kernel<<<grid, 256, 0, st>>>(a);
-        e = cudaGetLastError();
+        e = launch_early(norm_backward_wide_sums_kernel, grid, 256, 0, st, a);
     } else if (vec) {
         const int row_bytes = p.threads() * p.NV *
                               (chunk_bytes(a.dy.dtype) + chunk_bytes(a.x.dtype) + (a.add.p != nullptr ? chunk_bytes(a.add.dtype) : 0));
