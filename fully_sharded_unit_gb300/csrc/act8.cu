@@ -56,10 +56,25 @@ __global__ void __launch_bounds__(256) act8_elements_kernel(int64_t cols, Mat q,
             n[u] = (g - row[u] * groups) * kGroup + lane;
             on[u] = g < count && n[u] < cols;
             v[u] = 0.0f;
-            if (on[u]) {
-                if (PACK) v[u] = load1(x.p, x.dtype, row[u] * x.ld + n[u]);
-                else act8_readv<1>(static_cast<const uint8_t*>(q.p) + row[u] * q.ld, q.e + row[u] * q.eld, n[u], &v[u]);
+        }
+        if (PACK && x.dtype == FSDP_DTYPE_F32) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (on[u]) v[u] = static_cast<const float*>(x.p)[row[u] * x.ld + n[u]];
+        } else if (PACK) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (on[u]) v[u] = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(x.p)[row[u] * x.ld + n[u]]) << 16);
+        } else {
+            int w[U];
+            uint32_t byte[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                w[u] = on[u] ? static_cast<const int8_t*>(q.p)[row[u] * q.ld + n[u]] : 0;
+                byte[u] = on[u] ? q.e[row[u] * q.eld + (n[u] >> 5)] : 127u;
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = static_cast<float>(w[u]) * act8_step(byte[u]);
         }
         if (PACK) {
 #pragma unroll

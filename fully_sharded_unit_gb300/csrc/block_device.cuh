@@ -73,6 +73,65 @@ __device__ __forceinline__ void storev(void* p, int dtype, int64_t i, const floa
     else store1(p, dtype, i, v[0]);
 }
 
+// N elements `stride` apart, or 0 where on(i) is false.  The type is looked at
+// once, outside the loop: with a branch in it, each load would wait for the one
+// before.
+template <int N, typename On>
+__device__ __forceinline__ void load_strided(const void* p, int dtype, int64_t i, int64_t stride, On on, float* v) {
+    if (dtype == FSDP_DTYPE_F32) {
+        const float* s = static_cast<const float*>(p) + i;
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = on(j) ? s[j * stride] : 0.0f;
+    } else {
+        const uint16_t* s = static_cast<const uint16_t*>(p) + i;
+        uint32_t w[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) w[j] = on(j) ? s[j * stride] : 0u;
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = __uint_as_float(w[j] << 16);
+    }
+}
+
+template <int N, typename On>
+__device__ __forceinline__ void store_strided(void* p, int dtype, int64_t i, int64_t stride, On on, const float* v) {
+    if (dtype == FSDP_DTYPE_F32) {
+        float* s = static_cast<float*>(p) + i;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (on(j)) s[j * stride] = v[j];
+    } else {
+        __nv_bfloat16* s = static_cast<__nv_bfloat16*>(p) + i;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (on(j)) s[j * stride] = __float2bfloat16_rn(v[j]);
+    }
+}
+
+// Chunks of eight, `stride` elements apart, from 16-byte boundaries.
+template <int N, typename On>
+__device__ __forceinline__ void load_chunks(const void* p, int dtype, int64_t i, int64_t stride, On on, float (*v)[8]) {
+    if (dtype == FSDP_DTYPE_F32) {
+        const float* s = static_cast<const float*>(p) + i;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            float4 a = make_float4(0, 0, 0, 0), b = a;
+            if (on(j)) {
+                a = reinterpret_cast<const float4*>(s + j * stride)[0];
+                b = reinterpret_cast<const float4*>(s + j * stride)[1];
+            }
+            v[j][0] = a.x; v[j][1] = a.y; v[j][2] = a.z; v[j][3] = a.w;
+            v[j][4] = b.x; v[j][5] = b.y; v[j][6] = b.z; v[j][7] = b.w;
+        }
+    } else {
+        const uint16_t* s = static_cast<const uint16_t*>(p) + i;
+        uint4 w[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) w[j] = on(j) ? *reinterpret_cast<const uint4*>(s + j * stride) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < N; ++j) unpack8(w[j], v[j]);
+    }
+}
+
 // ---- pairs of floats in one 64-bit register (one instruction for both) ----
 
 using f32x2 = unsigned long long;

@@ -151,21 +151,28 @@ __device__ __forceinline__ void finish_row(const Product& p, int64_t m, int64_t 
 // tiles whose rows are C's columns.  n - lane is a multiple of 32.
 template <int R, bool SLOPE>
 __device__ __forceinline__ void finish_column(const Product& p, int64_t m, int count, int64_t n, float bias, float* v, int lane) {
-    const bool on = n < p.N;
+    const bool in = n < p.N;
+    const auto on = [&](int i) { return in && i < count; };
 #pragma unroll
     for (int i = 0; i < R; ++i) v[i] += bias;
+    float e[R];
+    if (p.add.p != nullptr) load_strided<R>(p.add.p, p.add.dtype, m * p.add.ld + n, p.add.ld, on, e);
     if (SLOPE) {
         float z[R];
         if (p.pre.dtype == FSDP_DTYPE_ACT8) {
+            const int8_t* q = static_cast<const int8_t*>(p.pre.p) + m * p.pre.ld + n;
+            const uint8_t* x = p.pre.e + m * p.pre.eld + (n >> 5);
+            int w[R];
+            uint32_t byte[R];
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                z[i] = 0.0f;
-                if (on && i < count)
-                    act8_readv<1>(static_cast<const uint8_t*>(p.pre.p) + (m + i) * p.pre.ld, p.pre.e + (m + i) * p.pre.eld, n, z + i);
+                w[i] = on(i) ? q[i * p.pre.ld] : 0;
+                byte[i] = on(i) ? x[i * p.pre.eld] : 127u;
             }
-        } else {
 #pragma unroll
-            for (int i = 0; i < R; ++i) z[i] = on && i < count ? load1(p.pre.p, p.pre.dtype, (m + i) * p.pre.ld + n) : 0.0f;
+            for (int i = 0; i < R; ++i) z[i] = static_cast<float>(w[i]) * act8_step(byte[i]);
+        } else {
+            load_strided<R>(p.pre.p, p.pre.dtype, m * p.pre.ld + n, p.pre.ld, on, z);
         }
         slope_n<R>(v, z, p.act);
     } else {
@@ -173,7 +180,7 @@ __device__ __forceinline__ void finish_column(const Product& p, int64_t m, int c
             if (p.pre.dtype == FSDP_DTYPE_ACT8) {
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
-                    const float x = on ? v[i] : 0.0f;
+                    const float x = in ? v[i] : 0.0f;
                     const uint32_t top = act8_group_top<1>(&x);
                     if (i < count && n < p.pre.ld) {
                         act8_writev<1>(static_cast<uint8_t*>(p.pre.p) + (m + i) * p.pre.ld, n, &x, top);
@@ -181,23 +188,16 @@ __device__ __forceinline__ void finish_column(const Product& p, int64_t m, int c
                     }
                 }
             } else {
-#pragma unroll
-                for (int i = 0; i < R; ++i)
-                    if (on && i < count) store1(p.pre.p, p.pre.dtype, (m + i) * p.pre.ld + n, v[i]);
+                store_strided<R>(p.pre.p, p.pre.dtype, m * p.pre.ld + n, p.pre.ld, on, v);
             }
         }
         activate_n<R>(v, p.act);
     }
     if (p.add.p != nullptr) {
-        float e[R];
-#pragma unroll
-        for (int i = 0; i < R; ++i) e[i] = on && i < count ? load1(p.add.p, p.add.dtype, (m + i) * p.add.ld + n) : 0.0f;
 #pragma unroll
         for (int i = 0; i < R; ++i) v[i] += e[i];
     }
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-        if (on && i < count) store1(p.out.p, p.out.dtype, (m + i) * p.out.ld + n, v[i]);
+    store_strided<R>(p.out.p, p.out.dtype, m * p.out.ld + n, p.out.ld, on, v);
 }
 
 }  // namespace fsdp

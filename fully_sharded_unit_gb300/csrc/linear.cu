@@ -176,8 +176,8 @@ struct Plan {
     int bn;                    // columns of a tile: 32 .. 256 in steps of 32
     int stages, stage_b;       // stages in the ring, and B's bytes in one, per CTA
     int tiles_m, tiles_n;
-    int64_t whole;             // tiles done by one cluster each
-    int64_t units;             // whole + (tiles - whole) * parts
+    uint32_t whole;            // tiles done by one cluster each
+    uint32_t units;            // whole + (tiles - whole) * parts
     int parts;                 // clusters that share one of the remaining tiles, along k
     int swapped;               // the tile's rows are C's columns (few tokens)
     int vec;                   // 1: every row of the epilogue's matrices starts on a 16-byte boundary and N % 8 == 0;
@@ -195,30 +195,29 @@ struct Plan {
 
 struct Unit {
     int tm, tn, k0, k1, part;
-    int64_t shared;            // index among the shared tiles, or -1
+    int shared;                // index among the shared tiles, or -1
 };
 
 // Bands of 8 tiles down, walked along n: a wave of clusters shares few slices
 // of A and B in L2.
-__device__ __forceinline__ void place_tile(const Plan& p, int64_t t, int* tm, int* tn) {
-    const int64_t band = static_cast<int64_t>(8) * p.tiles_n;
-    const int64_t b = t / band;
-    const int in = static_cast<int>(t - b * band);
-    const int high = min(8, p.tiles_m - static_cast<int>(b) * 8);
-    *tm = static_cast<int>(b) * 8 + in % high;
-    *tn = in / high;
+__device__ __forceinline__ void place_tile(const Plan& p, uint32_t t, int* tm, int* tn) {
+    const uint32_t band = 8u * p.tiles_n;
+    const uint32_t b = t / band, in = t - b * band;
+    const uint32_t high = min(8u, p.tiles_m - b * 8);
+    *tm = static_cast<int>(b * 8 + in % high);
+    *tn = static_cast<int>(in / high);
 }
 
-__device__ __forceinline__ Unit unit_of(const Plan& p, int64_t u) {
+__device__ __forceinline__ Unit unit_of(const Plan& p, uint32_t u) {
     Unit r;
-    int64_t t = u;
+    uint32_t t = u;
     r.k0 = 0;
     r.k1 = p.ks;
     r.part = 0;
     r.shared = -1;
     if (u >= p.whole) {
-        const int64_t v = u - p.whole;
-        r.shared = v / p.parts;
+        const uint32_t v = u - p.whole;
+        r.shared = static_cast<int>(v / p.parts);
         r.part = static_cast<int>(v - r.shared * p.parts);
         t = p.whole + r.shared;
         r.k0 = static_cast<int>(static_cast<int64_t>(p.ks) * r.part / p.parts);
@@ -282,7 +281,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    const int64_t cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+    const uint32_t cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < pl.stages; ++i) {
@@ -330,7 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t* issued = &bars->issued[is_a ? 0 : 1];
         uint32_t q = 0, s = 0, use = 0;   // stages issued, the next one's place and how often the ring went round (parity)
         bool ok = true;
-        for (int64_t u = cluster; u < pl.units && ok; u += clusters) {
+        for (uint32_t u = cluster; u < pl.units && ok; u += clusters) {
             const Unit un = unit_of(pl, u);
             const int at = (is_a ? un.tm * 256 : un.tn * pl.bn) + static_cast<int>(rank) * extent;
             for (int k = un.k0; k < un.k1; ++k) {
@@ -374,7 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t da0 = smem_desc(smem_addr(stage_a), p.a_trans), db0 = smem_desc(smem_addr(stage_b), p.b_trans);
         uint32_t q = 0, s = 0, use = 0, tile = 0;
         bool ok = true;
-        for (int64_t u = cluster; u < pl.units && ok; u += clusters, ++tile) {
+        for (uint32_t u = cluster; u < pl.units && ok; u += clusters, ++tile) {
             const Unit un = unit_of(pl, u);
             const uint32_t buf = tile & 1u, d = tmem + buf * 256;
             if (tile >= 2 &&
@@ -421,7 +420,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float4* buf4 = epi + w * (kEpiBytes / 16);
         const int chunks = pl.bn / 32;
         uint32_t tile = 0;
-        for (int64_t u = cluster; u < pl.units; u += clusters, ++tile) {
+        for (uint32_t u = cluster; u < pl.units; u += clusters, ++tile) {
             const Unit un = unit_of(pl, u);
             const uint32_t buf = tile & 1u;
             // the whole warp goes on or none of it
@@ -533,37 +532,50 @@ __global__ void __launch_bounds__(256) column_sum_kernel(int64_t rows, int64_t c
     }
 }
 
-// The shared tiles: the parts' sums in the order of the parts, then the same
-// epilogue; a 32 x 32 chunk to a warp, so that all SMs take part.  (Done by the
-// last cluster to reach a tile instead, the sums of 19 parts took 60 us of its
-// two SMs' time.)
+// The shared tiles: the parts' sums, then the same epilogue.  A block finishes
+// one 32 x 32 chunk: each of its warps adds up a quarter of the parts, in their
+// order, and the first warp adds the four.  (Done by the last cluster to reach
+// a tile instead, the sums of 19 parts took 60 us of its two SMs' time; by one
+// warp a chunk, 15 us.)
 template <int VEC, bool SLOPE>
 __global__ void __launch_bounds__(128) finish_kernel(const __grid_constant__ Product p, const __grid_constant__ Plan pl) {
     __shared__ float4 buf[4][256];
     starts_early();
     after_previous();
-    const int lane = threadIdx.x & 31, chunks = pl.bn / 32;
-    const int64_t job = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int64_t shared = job / (8 * chunks);
-    const int in = static_cast<int>(job - shared * 8 * chunks), c = in >> 3, rank = in >> 2 & 1, quad = in & 3;
-    if (pl.whole + shared >= static_cast<int64_t>(pl.tiles_m) * pl.tiles_n) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per_tile = pl.bn / 4;   // chunks of a tile: 8 x bn/32
+    const uint32_t shared = blockIdx.x / per_tile;
+    const int in = static_cast<int>(blockIdx.x - shared * per_tile), c = in >> 3, rank = in >> 2 & 1, quad = in & 3;
     int tm, tn;
-    place_tile(pl, pl.whole + shared, &tm, &tn);
-    const float4* q = pl.sums(shared, 0, rank * kEpiWarps + (c & 1) * 4 + quad) + (c >> 1) * 256 + lane;
+    place_tile(pl, static_cast<uint32_t>(pl.whole) + shared, &tm, &tn);
+    const int j0 = pl.parts * warp / 4, j1 = pl.parts * (warp + 1) / 4;
+    const float4* q = pl.sums(shared, j0, rank * kEpiWarps + (c & 1) * 4 + quad) + (c >> 1) * 256 + lane;
     const int64_t next = static_cast<int64_t>(kPieces) * (kPiece / 4);
     float v[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = 0.0f;
 #pragma unroll 2
-    for (int j = 0; j < pl.parts; ++j) {
+    for (int j = j0; j < j1; ++j, q += next) {
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
-            const float4 f = __ldcg(q + j * next + s * 32);
+            const float4 f = __ldcg(q + s * 32);
+            v[4 * s] += f.x; v[4 * s + 1] += f.y; v[4 * s + 2] += f.z; v[4 * s + 3] += f.w;
+        }
+    }
+    if (warp > 0) {
+#pragma unroll
+        for (int s = 0; s < 8; ++s) buf[warp][s * 32 + lane] = make_float4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]);
+    }
+    __syncthreads();
+    if (warp > 0) return;
+    for (int w = 1; w < 4; ++w) {
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const float4 f = buf[w][s * 32 + lane];
             v[4 * s] += f.x; v[4 * s + 1] += f.y; v[4 * s + 2] += f.z; v[4 * s + 3] += f.w;
         }
     }
     finish_chunk<VEC, SLOPE>(p, pl, static_cast<int64_t>(tm) * 256 + rank * 128 + quad * 32,
-                             static_cast<int64_t>(tn) * pl.bn + c * 32, v, buf[threadIdx.x >> 5], lane);
+                             static_cast<int64_t>(tn) * pl.bn + c * 32, v, buf[0], lane);
 }
 
 // Rows of a bf16 matrix that do not start on 16-byte boundaries, copied to
@@ -652,11 +664,11 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, int clu
             const int64_t left = tiles % clusters;
             p.parts = share == 0 || left == 0 ? 1 : static_cast<int>(std::min<int64_t>(clusters / left, std::max(1, p.ks / 4)));
             if (share == 1 && p.parts == 1) continue;
-            p.whole = p.parts > 1 ? tiles - left : tiles;
-            p.units = p.whole + (tiles - p.whole) * p.parts;
+            p.whole = static_cast<uint32_t>(p.parts > 1 ? tiles - left : tiles);
+            p.units = static_cast<uint32_t>(p.whole + (tiles - p.whole) * p.parts);
             const double rounds = static_cast<double>((p.whole + clusters - 1) / clusters);
             double t = rounds * (std::max(steps * stage, 2500.0 + 10.0 * bn) + 300.0) + 10.0 * bn;
-            if (p.parts > 1) t += (p.ks + p.parts - 1) / p.parts * stage + 11000.0 + 150.0 * p.parts;
+            if (p.parts > 1) t += (p.ks + p.parts - 1) / p.parts * stage + 9000.0 + 60.0 * p.parts;
             if (least == 0 || t < least) {
                 least = t;
                 best = p;
@@ -765,11 +777,12 @@ cudaError_t launch_product(const Product& given, const ProductRoom& room, int sm
     e = p.a_trans ? make_map(&map_a, p.a, p.K, rows, kDepth) : make_map(&map_a, p.a, rows, p.K, 128);
     if (e == cudaSuccess) e = p.b_trans ? make_map(&map_b, p.b, p.K, cols, kDepth) : make_map(&map_b, p.b, cols, p.K, pl.bn / 2);
     if (e != cudaSuccess) return e;
+    if (static_cast<int64_t>(pl.tiles_m) * pl.tiles_n > 0x7fffffff) return cudaErrorInvalidValue;   // far beyond any memory
     const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(pl.units, clusters));
     e = launch_early(kProductKernels[p.slope][pl.vec], dim3(grid), kThreads, kSmemBytes, st, map_a, map_b, p, pl);
     const int64_t shared = static_cast<int64_t>(pl.tiles_m) * pl.tiles_n - pl.whole;
     if (e != cudaSuccess || shared == 0) return e;
-    return launch_early(kFinishKernels[p.slope][pl.vec], dim3(static_cast<unsigned>((shared * 8 * (pl.bn / 32) + 3) / 4)), 128, 0,
+    return launch_early(kFinishKernels[p.slope][pl.vec], dim3(static_cast<unsigned>(shared * (pl.bn / 4))), 128, 0,
                         st, p, pl);
 }
 

@@ -44,16 +44,9 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_forward_kernel(NormFor
     for (int64_t row = first; row < a.rows; row += stride) {
         float v[NV][V];
         float s = 0.0f;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int64_t c = static_cast<int64_t>(t + k * threads) * V;
-            if (c < a.cols) {
-                loadv<V>(a.x.p, a.x.dtype, row * a.x.ld + c, v[k]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[k][j] = 0.0f;
-            }
-        }
+        const auto on = [&](int k) { return static_cast<int64_t>(t + k * threads) * V < a.cols; };
+        if constexpr (V == 8) load_chunks<NV>(a.x.p, a.x.dtype, row * a.x.ld + t * 8, threads * 8, on, v);
+        else load_strided<NV>(a.x.p, a.x.dtype, row * a.x.ld + t, threads, on, &v[0][0]);
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
@@ -185,7 +178,7 @@ __host__ __device__ __forceinline__ int chunk_bytes(int dtype) {
 // memory for row 0, and its slots.  Slot (place, k) of a group starts at
 // (place * NV + k) * GT chunks; an F32 chunk is two halves GT * 16 bytes apart
 // (16-byte accesses of neighbouring threads are neighbours).
-template <int NV, int GT, bool FAST>
+template <int NV, int GT, bool FAST, bool INT8 = false>
 struct Rows {
     const uint8_t* first;
     int64_t pitch;          // bytes between rows
@@ -194,9 +187,9 @@ struct Rows {
     int place;              // bytes between places
 
     __device__ Rows(const Mat& m, uint8_t* at, int group, int groups, int t) {
-        cb = chunk_bytes(m.dtype);
+        cb = INT8 ? 8 : FAST ? 16 : chunk_bytes(m.dtype);
         place = groups * NV * GT * cb;
-        slots = at + group * NV * GT * cb + t * (cb == 8 ? 8 : 16);
+        slots = at + group * NV * GT * cb + t * (INT8 ? 8 : 16);
         first = static_cast<const uint8_t*>(m.p) + t * cb;
         pitch = m.ld * (cb >> 3);
     }
@@ -206,7 +199,7 @@ struct Rows {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (k + 1 < NV || end) {
-                if (cb == 8) {
+                if (INT8) {
                     copy8(dst + k * GT * 8, src + k * GT * 8);
                 } else if (FAST || cb == 16) {
                     copy16(dst + k * GT * 16, src + k * GT * 16);
@@ -410,7 +403,8 @@ __global__ void __launch_bounds__(THREADS) norm_forward_ring_kernel(const __grid
     }
 }
 
-template <int NV, int GT, int THREADS, bool FAST>
+// KEPT: x is an ACT8 checkpoint.
+template <int NV, int GT, int THREADS, bool FAST, bool KEPT>
 __global__ void __launch_bounds__(THREADS) norm_backward_ring_kernel(const __grid_constant__ NormBackward a, int places) {
     extern __shared__ __align__(16) uint8_t ring_bytes[];
     __shared__ __align__(16) float2 red[2][32];
@@ -423,11 +417,12 @@ __global__ void __launch_bounds__(THREADS) norm_backward_ring_kernel(const __gri
     at += gammas.place;
     const Rows<NV, GT, FAST> dys(a.dy, at, g, G, t);
     at += places * dys.place;
-    const Rows<NV, GT, FAST> xs(a.x, at, g, G, t);
+    const Rows<NV, GT, FAST, KEPT> xs(a.x, at, g, G, t);
     at += places * xs.place;
     const Rows<NV, GT, FAST> adds(a.add, at, g, G, t);
     const Out<GT, FAST> dxs(a.dx, t);
-    const bool added = a.add.p != nullptr, kept = a.x.dtype == FSDP_DTYPE_ACT8;
+    const bool added = a.add.p != nullptr;
+    constexpr bool kept = KEPT;
     if (g == 0) {
         gammas.copy(0, 0, end);
         copies_end();
@@ -524,43 +519,30 @@ __global__ void __launch_bounds__(THREADS) norm_backward_ring_kernel(const __gri
         }
         place = place + 1 == places ? 0 : place + 1;
     }
-    // the groups' column sums meet in shared memory (element j of chunk i at
-    // j * slots + i: neighbouring threads on neighbouring banks)
+    // the groups' column sums meet in shared memory: element j of chunk i at
+    // j * kSlots + i (no bank conflicts writing, nor reading the columns in order)
     float* part = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
-    constexpr int kSlots = NV * GT;
-    if (G > 1) {
-        float* comb = reinterpret_cast<float*>(ring_bytes);
-        copies_wait(0);
-        __syncthreads();
+    constexpr int kSlots = NV * GT + 4;
+    float* comb = reinterpret_cast<float*>(ring_bytes);
+    copies_wait(0);
+    __syncthreads();
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float* to = comb + (g * 16 + 2 * j) * kSlots + t + k * GT;
-                unpair(dg[k][j], to[0], to[kSlots]);
-                unpair(db[k][j], to[8 * kSlots], to[9 * kSlots]);
-            }
-        __syncthreads();
-        for (int i = threadIdx.x; i < 16 * kSlots; i += blockDim.x) {
-            float s = 0.0f;
-            for (int h = 0; h < G; ++h) s += comb[h * 16 * kSlots + i];
-            const int j = i / kSlots, c = (i - j * kSlots) * 8 + (j & 7);
-            if (c < a.cols) part[(j >> 3) * a.cols + c] = s;
+        for (int j = 0; j < 4; ++j) {
+            float* to = comb + (g * 16 + 2 * j) * kSlots + t + k * GT;
+            unpair(dg[k][j], to[0], to[kSlots]);
+            unpair(db[k][j], to[8 * kSlots], to[9 * kSlots]);
         }
-    } else {
+    __syncthreads();
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            if (k + 1 < NV || end) {
-                f32x2* p = reinterpret_cast<f32x2*>(part + (t + k * GT) * 8);
-                f32x2* q = reinterpret_cast<f32x2*>(part + a.cols + (t + k * GT) * 8);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    p[j] = dg[k][j];
-                    q[j] = db[k][j];
-                }
-            }
+    for (int o = 0; o < 2; ++o)
+        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+            const float* from = comb + (o * 8 + (c & 7)) * kSlots + (c >> 3);
+            float s = from[0];
+            for (int h = 1; h < G; ++h) s += from[h * 16 * kSlots];
+            part[o * a.cols + c] = s;
         }
-    }
 }
 
 // ---- other rows ----
@@ -597,25 +579,33 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(NormBackward a, 
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * G + g; row < a.rows; row += static_cast<int64_t>(gridDim.x) * G) {
         float xh[NV], dy[NV];
         const float mean = a.mean[row], rstd = a.rstd[row];
+        const auto on = [&](int k) { return t + k * gt < a.cols; };
+        load_strided<NV>(a.dy.p, a.dy.dtype, row * a.dy.ld + t, gt, on, dy);
+        if (a.x.dtype == FSDP_DTYPE_ACT8) {
+            const int8_t* q = static_cast<const int8_t*>(a.x.p) + row * a.x.ld + t;
+            const uint8_t* e = a.x.e + row * a.x.eld + (t >> 5);   // gt is a multiple of 32
+            int w[NV];
+            uint32_t byte[NV];
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int64_t c = t + k * gt;
-            dy[k] = c < a.cols ? load1(a.dy.p, a.dy.dtype, row * a.dy.ld + c) : 0.0f;
-        }
+            for (int k = 0; k < NV; ++k) {
+                w[k] = on(k) ? q[k * gt] : 0;
+                byte[k] = on(k) ? e[k * (gt >> 5)] : 127u;
+            }
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int64_t c = t + k * gt;
-            xh[k] = mean;
-            if (c < a.cols) load_x<1>(a.x, row, c, &xh[k]);
+            for (int k = 0; k < NV; ++k) xh[k] = static_cast<float>(w[k]) * act8_step(byte[k]);
+        } else {
+            load_strided<NV>(a.x.p, a.x.dtype, row * a.x.ld + t, gt, on, xh);
         }
+        float gm[NV], add[NV];
+        load_strided<NV>(a.gamma, a.param_dtype, t, gt, on, gm);
+        if (a.add.p != nullptr) load_strided<NV>(a.add.p, a.add.dtype, row * a.add.ld + t, gt, on, add);
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int64_t c = t + k * gt;
-            xh[k] = (xh[k] - mean) * rstd;
+            xh[k] = on(k) ? (xh[k] - mean) * rstd : 0.0f;
             db[k] += dy[k];
             dg[k] = fmaf(dy[k], xh[k], dg[k]);
-            dy[k] *= c < a.cols ? load1(a.gamma, a.param_dtype, c) : 0.0f;
+            dy[k] *= gm[k];
             s1 += dy[k];
             s2 = fmaf(dy[k], xh[k], s2);
         }
@@ -623,14 +613,8 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(NormBackward a, 
         flip ^= 1;
         const float c1 = sum.x * inv_n, c2 = sum.y * inv_n;
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int64_t c = t + k * gt;
-            if (c < a.cols) {
-                float o = rstd * (dy[k] - c1 - xh[k] * c2);
-                if (a.add.p != nullptr) o += load1(a.add.p, a.add.dtype, row * a.add.ld + c);
-                store1(a.dx.p, a.dx.dtype, row * a.dx.ld + c, o);
-            }
-        }
+        for (int k = 0; k < NV; ++k) dy[k] = rstd * (dy[k] - c1 - xh[k] * c2) + (a.add.p != nullptr ? add[k] : 0.0f);
+        store_strided<NV>(a.dx.p, a.dx.dtype, row * a.dx.ld + t, gt, on, dy);
     }
     float* part = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
     const int slots = NV * gt;
@@ -790,7 +774,7 @@ Split split_row(int64_t rows, int64_t chunks, const int (*options)[2], int count
     return p;
 }
 constexpr int kForward[][2] = {{1, 32}, {2, 32}, {3, 32}, {4, 32}, {5, 32}, {6, 32}, {2, 128}, {3, 128}, {4, 128}, {5, 128}, {6, 128}, {4, 256}, {5, 256}, {6, 256}, {4, 512}};
-constexpr int kBackward[][2] = {{1, 32}, {2, 32}, {3, 32}, {2, 64}, {3, 64}, {2, 128}, {3, 128}, {1, 512}, {2, 512}, {3, 512}};
+constexpr int kBackward[][2] = {{1, 32}, {2, 32}, {3, 32}, {4, 32}, {5, 32}, {2, 128}, {3, 128}, {1, 512}, {2, 512}, {3, 512}};
 
 int64_t walkers(const Split& p, int64_t rows, int64_t most) {
     return std::max<int64_t>(1, std::min((rows + p.groups - 1) / p.groups, most));
@@ -799,7 +783,11 @@ int64_t walkers(const Split& p, int64_t rows, int64_t most) {
 constexpr int kWideSlices = 64;   // row slices of the column sums where rows are too long
 
 Split backward_split(int64_t rows, int64_t cols, bool vec) {
-    if (vec) return split_row(rows, cols / 8, kBackward, 10, 512);
+    if (vec) {
+        Split p = split_row(rows, cols / 8, kBackward, 10, 512);
+        if (p.NV > 3) p.groups = std::min(p.groups, 8);   // 256 threads, which may have twice the registers
+        return p;
+    }
     Split p;
     if (cols <= 8192) {
         p.NV = 8;
@@ -882,17 +870,26 @@ cudaError_t launch_norm_backward(const NormBackward& a, int sms, cudaStream_t st
                               (chunk_bytes(a.dy.dtype) + chunk_bytes(a.x.dtype) + (a.add.p != nullptr ? chunk_bytes(a.add.dtype) : 0));
         const int keep = p.NV * p.gt * chunk_bytes(a.param_dtype);
         const int places = std::max(1, std::min(kRing, (kSharedMost - keep) / row_bytes));
-        const int comb = p.groups > 1 ? p.threads() * p.NV * 16 * 4 : 0;
+        const int comb = p.groups * 16 * (p.NV * p.gt + 4) * 4;
         const int bytes = std::max(keep + places * row_bytes, comb);
+        const bool kept = a.x.dtype == FSDP_DTYPE_ACT8;
         const bool fast = a.dy.dtype == FSDP_DTYPE_BF16 && a.dx.dtype == FSDP_DTYPE_BF16 && a.param_dtype == FSDP_DTYPE_BF16 &&
                           a.x.dtype != FSDP_DTYPE_F32 && (a.add.p == nullptr || a.add.dtype == FSDP_DTYPE_BF16);
         e = cudaErrorInvalidConfiguration;
-#define RING(nv, gt_)                                                                                              \
-    if (p.NV == nv && p.gt == gt_)                                                                                 \
-        e = fast ? launch_shared<norm_backward_ring_kernel<nv, gt_, 512, true>>(blocks, p.threads(), bytes, st, a, places) \
-                 : launch_shared<norm_backward_ring_kernel<nv, gt_, 512, false>>(blocks, p.threads(), bytes, st, a, places);
-        RING(1, 32) RING(2, 32) RING(3, 32) RING(2, 64) RING(3, 64) RING(2, 128) RING(3, 128) RING(1, 512) RING(2, 512) RING(3, 512)
+#define RING_(nv, gt_, f, k)                                                                                      \
+    if (fast == f && kept == k) e = launch_shared<norm_backward_ring_kernel<nv, gt_, nv <= 3 ? 512 : 256, f, k>>( \
+        blocks, p.threads(), bytes, st, a, places)
+#define RING(nv, gt_)                    \
+    if (p.NV == nv && p.gt == gt_) {     \
+        RING_(nv, gt_, true, true);      \
+        RING_(nv, gt_, true, false);     \
+        RING_(nv, gt_, false, true);     \
+        RING_(nv, gt_, false, false);    \
+    }
+        RING(1, 32) RING(2, 32) RING(3, 32) RING(4, 32) RING(5, 32)
+        RING(2, 128) RING(3, 128) RING(1, 512) RING(2, 512) RING(3, 512)
 #undef RING
+#undef RING_
     } else {
         const int comb = p.groups > 1 ? p.threads() * p.NV * 2 * 4 : 0;
         e = launch_shared<norm_backward_kernel<8, 1024>>(blocks, p.threads(), comb, st, a, p.gt);
