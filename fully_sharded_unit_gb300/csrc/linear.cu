@@ -111,6 +111,16 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, long lo
     }
 }
 
+// The same for a whole warp, which goes on or gives up together.
+__device__ __forceinline__ bool bar_wait_warp(uint32_t addr, uint32_t parity, long long limit, const volatile uint32_t* abort) {
+    long long t0 = 0;
+    for (uint32_t i = 0;; ++i) {
+        if (__all_sync(0xffffffffu, bar_try(addr, parity))) return true;
+        if (i == 16) t0 = clock64();
+        else if (i > 16 && (i & 15) == 0 && __any_sync(0xffffffffu, *abort != 0 || clock64() - t0 > limit)) return false;
+    }
+}
+
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
@@ -119,28 +129,31 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         : "memory");
 }
 
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+// One 16-deep product of the pair, d = a b (add == 0) or d += a b, issued by the
+// lane where `leader` is set.  The predicate is inside the statement: the code
+// around it stays that of a whole warp, and its operands uniform.
+__device__ __forceinline__ void mma(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
     asm volatile(
-        "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        "{ .reg .pred e, p; setp.ne.u32 e, %5, 0; setp.ne.u32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(leader)
         : "memory");
 }
 
-// True in one lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
+// 1 in one lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
     uint32_t r;
     asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
-    return r != 0;
+    return r;
 }
 
 // Arrives on the barrier at this offset in both CTAs once the matrix
 // instructions issued so far are done.
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+__device__ __forceinline__ void mma_commit(uint32_t leader, uint32_t bar) {
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_addr(bar)),
-        "h"(static_cast<uint16_t>(3))
+        "{ .reg .pred e; setp.ne.u32 e, %2, 0;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1; }" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3)), "r"(leader)
         : "memory");
 }
 
@@ -311,10 +324,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tmem = bars->tmem_base;
     starts_early();
     after_previous();
-    // The producer's and the matrix warp's loops run in whole warps, with one
-    // lane elected to issue: their counters and descriptors are then uniform.
-    // (In a branch of one lane, each matrix instruction took 65 cycles to issue
-    // and a stage 520, whatever the tile's width.)
+    // The producers' and the matrix warp's loops run in whole warps, one lane of
+    // which issues: their counters and descriptors are then uniform.  What the
+    // matrix warp does in a stage has to fit into the time of the stage's
+    // products (512 cycles at BN = 256): in a branch of one lane, with the clock
+    // or the progress written in every stage, it took 520 to 600.
     if (warp == 0 || warp == 3) {
         // ---- producers: A's, and B's ----
         const bool is_a = warp == 0;
@@ -323,24 +337,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int extent = is_a ? 128 : pl.bn / 2;                     // rows of the operand in a stage, per CTA
         const bool second = by_rows && extent > 64;                    // a box holds 64 of them
         const uint32_t bytes = is_a ? kStageA : pl.stage_b;
-        const uint32_t full0 = remote_addr(smem_addr(&bars->full[0]), 0);
+        const uint32_t full0 = remote_addr(smem_addr(&bars->full[0]), 0), empty0 = smem_addr(&bars->empty[0]);
         const uint32_t stage0 = smem_addr(is_a ? stage_a : stage_b), stride = is_a ? kStageA : pl.stage_b;
-        const bool withheld = pl.withhold && blockIdx.x < 2;
-        uint32_t* issued = &bars->issued[is_a ? 0 : 1];
+        const uint32_t leader = elect_one();
+        bool withhold = pl.withhold && blockIdx.x < 2;                 // the first stage's copies
         uint32_t q = 0, s = 0, use = 0;   // stages issued, the next one's place and how often the ring went round (parity)
         bool ok = true;
         for (uint32_t u = cluster; u < pl.units && ok; u += clusters) {
             const Unit un = unit_of(pl, u);
             const int at = (is_a ? un.tm * 256 : un.tn * pl.bn) + static_cast<int>(rank) * extent;
             for (int k = un.k0; k < un.k1; ++k) {
-                if (q >= stages && !__all_sync(0xffffffffu, bar_wait(&bars->empty[s], use ^ 1u, pl.wait_cycles, abort))) {
+                if (q >= stages && !bar_wait_warp(empty0 + s * 8, use ^ 1u, pl.wait_cycles, abort)) {
                     ok = false;
                     break;
                 }
-                if (elect_one()) {
+                if (leader) {
                     const uint32_t full = full0 + s * 8, dst = stage0 + s * stride;
                     bar_expect_remote(full, bytes);
-                    if (!(withheld && q == 0)) {
+                    if (!withhold) {
                         if (!by_rows) {
                             tma_load(dst, map, k * kDepth, at, full);
                         } else {
@@ -348,7 +362,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             if (second) tma_load(dst + kBlock, map, at + 64, k * kDepth, full);
                         }
                     }
-                    *issued = q + 1;
+                    withhold = false;
                 }
                 ++q;
                 if (++s == stages) {
@@ -359,60 +373,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // the stages still being read: their commits arrive here before this CTA leaves
         for (uint32_t i = q > stages ? q - stages : 0; ok && i < q; ++i)
-            ok = __all_sync(0xffffffffu, bar_wait(&bars->empty[i % stages], (i / stages) & 1u, pl.wait_cycles, abort));
-        if (!ok && lane == 0) {
-            atomicOr(pl.status, FSDP_KSTATUS_WAIT_TIMEOUT);
-            *abort = 1;
+            ok = bar_wait_warp(empty0 + (i % stages) * 8, (i / stages) & 1u, pl.wait_cycles, abort);
+        if (lane == 0) {
+            bars->issued[is_a ? 0 : 1] = q;
+            if (!ok) {
+                atomicOr(pl.status, FSDP_KSTATUS_WAIT_TIMEOUT);
+                *abort = 1;
+            }
         }
     } else if (warp == 1 && rank == 0) {
         // ---- matrix instructions ----
         const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | static_cast<uint32_t>(p.a_trans) << 15 |
                                static_cast<uint32_t>(p.b_trans) << 16 | static_cast<uint32_t>(pl.bn >> 3) << 17 | 16u << 24;
         const uint32_t step_a = p.a_trans ? 2048 >> 4 : 32 >> 4, step_b = p.b_trans ? 2048 >> 4 : 32 >> 4;   // to the next 16 k
+        const uint32_t next_b = pl.stage_b >> 4;
         const int last = static_cast<int>((p.K - static_cast<int64_t>(pl.ks - 1) * kDepth + 15) / 16);   // products of the last stage
         const uint64_t da0 = smem_desc(smem_addr(stage_a), p.a_trans), db0 = smem_desc(smem_addr(stage_b), p.b_trans);
+        const uint32_t full0 = smem_addr(&bars->full[0]), empty0 = smem_addr(&bars->empty[0]);
+        const uint32_t tmem_full0 = smem_addr(&bars->tmem_full[0]), tmem_empty0 = smem_addr(&bars->tmem_empty[0]);
+        const uint32_t leader = elect_one();
+        uint64_t da = da0, db = db0;
         uint32_t q = 0, s = 0, use = 0, tile = 0;
         bool ok = true;
         for (uint32_t u = cluster; u < pl.units && ok; u += clusters, ++tile) {
             const Unit un = unit_of(pl, u);
             const uint32_t buf = tile & 1u, d = tmem + buf * 256;
-            if (tile >= 2 &&
-                !__all_sync(0xffffffffu, bar_wait(&bars->tmem_empty[buf], (tile / 2 - 1) & 1u, pl.wait_cycles, abort))) {
+            if (tile >= 2 && !bar_wait_warp(tmem_empty0 + buf * 8, (tile / 2 - 1) & 1u, pl.wait_cycles, abort)) {
                 ok = false;
                 break;
             }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            uint32_t add = 0;
             for (int k = un.k0; k < un.k1; ++k) {
-                if (!__all_sync(0xffffffffu, bar_wait(&bars->full[s], use, pl.wait_cycles, abort))) {
+                if (!bar_wait_warp(full0 + s * 8, use, pl.wait_cycles, abort)) {
                     ok = false;
                     break;
                 }
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                if (elect_one()) {
-                    const uint64_t da = da0 + s * (kStageA >> 4), db = db0 + s * (pl.stage_b >> 4);
-                    const int count = k + 1 == pl.ks ? last : kDepth / 16;
-#pragma unroll
-                    for (int i = 0; i < kDepth / 16; ++i)
-                        if (i < count)
-                            mma(d, da + i * step_a, db + i * step_b, idesc, i > 0 ? 1u : static_cast<uint32_t>(k > un.k0));
-                    mma_commit(&bars->empty[s]);
-                    if (k + 1 == un.k1) mma_commit(&bars->tmem_full[buf]);
-                    bars->consumed = q + 1;
+                if (k + 1 < pl.ks || last == 4) {
+                    mma(leader, d, da, db, idesc, add);
+                    mma(leader, d, da + step_a, db + step_b, idesc, 1u);
+                    mma(leader, d, da + 2 * step_a, db + 2 * step_b, idesc, 1u);
+                    mma(leader, d, da + 3 * step_a, db + 3 * step_b, idesc, 1u);
+                } else {
+                    for (int i = 0; i < last; ++i) mma(leader, d, da + i * step_a, db + i * step_b, idesc, add | i);
                 }
+                add = 1;
+                mma_commit(leader, empty0 + s * 8);
                 ++q;
+                da += kStageA >> 4;
+                db += next_b;
                 if (++s == stages) {
                     s = 0;
                     use ^= 1u;
+                    da = da0;
+                    db = db0;
                 }
             }
+            if (ok) mma_commit(leader, tmem_full0 + buf * 8);
         }
-        if (!ok && elect_one()) {
+        if (lane == 0) bars->consumed = q;
+        if (!ok) {
             // give up: report, then wait for the matrix instructions in flight
-            atomicOr(pl.status, FSDP_KSTATUS_WAIT_TIMEOUT);
-            *abort = 1;
-            mma_commit(&bars->drain);
+            if (lane == 0) {
+                atomicOr(pl.status, FSDP_KSTATUS_WAIT_TIMEOUT);
+                *abort = 1;
+            }
+            mma_commit(leader, smem_addr(&bars->drain));
             const volatile uint32_t never = 0;
-            if (!bar_wait(&bars->drain, 0, pl.wait_cycles, &never)) atomicOr(pl.status, FSDP_KSTATUS_DRAIN_TIMEOUT);
+            if (!bar_wait_warp(smem_addr(&bars->drain), 0, pl.wait_cycles, &never) && lane == 0)
+                atomicOr(pl.status, FSDP_KSTATUS_DRAIN_TIMEOUT);
         }
     } else if (warp >= 4) {
         // ---- epilogue ----
@@ -424,7 +453,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const Unit un = unit_of(pl, u);
             const uint32_t buf = tile & 1u;
             // the whole warp goes on or none of it
-            if (!__all_sync(0xffffffffu, bar_wait(&bars->tmem_full[buf], (tile / 2) & 1u, pl.wait_cycles, abort))) {
+            if (!bar_wait_warp(smem_addr(&bars->tmem_full[buf]), (tile / 2) & 1u, pl.wait_cycles, abort)) {
                 if (lane == 0) atomicOr(pl.status, FSDP_KSTATUS_WAIT_TIMEOUT);
                 *abort = 1;
                 break;
