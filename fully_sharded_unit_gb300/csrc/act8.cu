@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(256) act8_groups_kernel(int64_t cols, Mat q, i
         float v[32];
         if (PACK) {
             load_row32<WIDE>(x, row, n, left, v);
-            store_row32<WIDE>(q, row, n, left, v);
+            q.e[g] = static_cast<uint8_t>(store_row32<WIDE>(q, row, n, left, v));
         } else {
             load_row32<WIDE>(q, row, n, left, v);
             activate_n<32>(v, act);

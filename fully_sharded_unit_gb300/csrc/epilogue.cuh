@@ -59,8 +59,9 @@ __device__ __forceinline__ void load_row32(const Mat& x, int64_t m, int64_t n, i
     }
 }
 
+// Returns the exponent byte of an ACT8 group, which is left to the caller.
 template <bool WIDE>
-__device__ __forceinline__ void store_row32(const Mat& x, int64_t m, int64_t n, int left, const float* v) {
+__device__ __forceinline__ uint32_t store_row32(const Mat& x, int64_t m, int64_t n, int left, const float* v) {
     if (x.dtype == FSDP_DTYPE_F32) {
         float* dst = static_cast<float*>(x.p) + m * x.ld + n;
 #pragma unroll
@@ -112,15 +113,18 @@ __device__ __forceinline__ void store_row32(const Mat& x, int64_t m, int64_t n, 
             reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
             reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
-        x.e[m * x.eld + (n >> 5)] = static_cast<uint8_t>(act8_byte(top));
+        return act8_byte(top);
     }
+    return 0;
 }
 
 // The epilogue of 32 columns of one row: everything a lane needs is in its own
 // registers (a checkpoint's group too), so 32 independent elements hide each
-// other's latency, and every access is a whole 32-byte sector.
+// other's latency, and every access is a whole 32-byte sector.  `byte`
+// takes the exponent byte of a checkpoint's group, which the caller stores.
 template <bool WIDE, bool SLOPE>
-__device__ __forceinline__ void finish_row(const Product& p, int64_t m, int64_t n, const float4* bias, float* v) {
+__device__ __forceinline__ void finish_row(const Product& p, int64_t m, int64_t n, const float4* bias, float* v,
+                                           uint32_t* byte) {
     const int left = static_cast<int>(min(static_cast<int64_t>(32), p.N - n));
     if (p.bias != nullptr) {
 #pragma unroll
@@ -134,7 +138,7 @@ __device__ __forceinline__ void finish_row(const Product& p, int64_t m, int64_t 
         load_row32<WIDE>(p.pre, m, n, left, z);
         slope_n<32>(v, z, p.act);
     } else {
-        if (p.pre.p != nullptr) store_row32<WIDE>(p.pre, m, n, left, v);
+        if (p.pre.p != nullptr) *byte = store_row32<WIDE>(p.pre, m, n, left, v);
         activate_n<32>(v, p.act);
     }
     if (p.add.p != nullptr) {

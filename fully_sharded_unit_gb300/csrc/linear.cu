@@ -242,19 +242,14 @@ __device__ __forceinline__ Unit unit_of(const Plan& p, uint32_t u) {
 
 // One 32 x 32 chunk whose rows lie one to a lane: v[j] is tile row `row0 +
 // lane`, tile column `col0 + j`.  buf: the warp's 4 KiB of shared memory, in
-// which 16-byte slot s of row r lies at s ^ (r & 7) (no bank conflicts writing,
-// and none reading along a row).
+// which 16-byte slot s of row r lies at s ^ (r & 7)
+// (no bank conflicts writing, and none reading along a row).  Where rows are
+// aligned, its first 32 floats are the chunk's bias.
 template <int VEC, bool SLOPE>
 __device__ __forceinline__ void finish_chunk(const Product& p, const Plan& pl, int64_t row0, int64_t col0, float* v,
-                                             float4* buf, int lane) {
+                                             float4* buf, int lane, uint32_t* byte) {
     if constexpr (VEC > 0) {
-        if (col0 >= p.N) return;
-        if (p.bias != nullptr) {
-            __syncwarp();
-            reinterpret_cast<float*>(buf)[lane] = col0 + lane < p.N ? load1(p.bias, p.bias_dtype, col0 + lane) : 0.0f;
-            __syncwarp();
-        }
-        if (row0 + lane < p.M) finish_row<VEC == 2, SLOPE>(p, row0 + lane, col0, buf, v);
+        if (col0 < p.N && row0 + lane < p.M) finish_row<VEC == 2, SLOPE>(p, row0 + lane, col0, buf, v, byte);
     } else {
         // one column of C to a lane
         const int64_t m0 = pl.swapped ? col0 : row0, n = (pl.swapped ? row0 : col0) + lane;
@@ -447,11 +442,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---- epilogue ----
         const int w = warp - 4, quad = warp & 3, half = w >> 2;
         float4* buf4 = epi + w * (kEpiBytes / 16);
-        const int chunks = pl.bn / 32;
+        // the warp's chunks of 32 columns: the first or the second half of the tile's
+        const int chunks = pl.bn / 32, c0 = half ? (chunks + 1) / 2 : 0, c1 = half ? chunks : (chunks + 1) / 2;
         uint32_t tile = 0;
         for (uint32_t u = cluster; u < pl.units; u += clusters, ++tile) {
             const Unit un = unit_of(pl, u);
             const uint32_t buf = tile & 1u;
+            const int64_t row0 = static_cast<int64_t>(un.tm) * 256 + rank * 128 + quad * 32;
+            const int64_t col0 = static_cast<int64_t>(un.tn) * pl.bn;
+            if (VEC > 0 && p.bias != nullptr) {   // of this warp's chunks, before their sums are there
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t n = col0 + (c0 + i) * 32 + lane;
+                    reinterpret_cast<float*>(buf4)[i * 32 + lane] = i < c1 - c0 && n < p.N ? load1(p.bias, p.bias_dtype, n) : 0.0f;
+                }
+                __syncwarp();
+            }
             // the whole warp goes on or none of it
             if (!bar_wait_warp(smem_addr(&bars->tmem_full[buf]), (tile / 2) & 1u, pl.wait_cycles, abort)) {
                 if (lane == 0) atomicOr(pl.status, FSDP_KSTATUS_WAIT_TIMEOUT);
@@ -459,15 +466,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 break;
             }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const int64_t row0 = static_cast<int64_t>(un.tm) * 256 + rank * 128 + quad * 32;
-            const int64_t col0 = static_cast<int64_t>(un.tn) * pl.bn;
             const uint32_t src = tmem + buf * 256 + (static_cast<uint32_t>(quad * 32) << 16);
             // a tile shared along k leaves its sums in the workspace, for finish_kernel
             float4* sums = un.shared < 0 ? nullptr : pl.sums(un.shared, un.part, static_cast<int>(rank) * kEpiWarps + w) + lane;
-            for (int c = half; c < chunks; c += 2) {
+            uint32_t bytes = 0;   // exponents of this warp's chunks of the lane's row
+            for (int c = c0; c < c1; ++c) {
                 float v[32];
                 tmem_load32(src + c * 32, v);
-                if (c + 2 >= chunks) {
+                if (c + 1 == c1) {
                     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) bar_arrive_remote(remote_addr(smem_addr(&bars->tmem_empty[buf]), 0));
@@ -475,12 +481,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (sums != nullptr) {
 #pragma unroll
                     for (int s = 0; s < 8; ++s)
-                        sums[(c >> 1) * 256 + s * 32] = make_float4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]);
+                        sums[(c - c0) * 256 + s * 32] = make_float4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]);
                 } else {
-                    finish_chunk<VEC, SLOPE>(p, pl, row0, col0 + c * 32, v, buf4, lane);
+                    uint32_t byte = 0;
+                    finish_chunk<VEC, SLOPE>(p, pl, row0, col0 + c * 32, v, VEC > 0 ? buf4 + (c - c0) * 8 : buf4, lane, &byte);
+                    bytes |= byte << (8 * (c - c0));
                 }
             }
-            if (half >= chunks && lane == 0) bar_arrive_remote(remote_addr(smem_addr(&bars->tmem_empty[buf]), 0));
+            if (VEC > 0 && !SLOPE && sums == nullptr && p.pre.p != nullptr && p.pre.dtype == FSDP_DTYPE_ACT8) {
+                // four neighbouring bytes of eight rows at a time: one byte of 32
+                // rows at a time is 32 partial sectors, which cost 6 us in 40
+                const int i = lane & 3;
+                const int64_t group = (col0 >> 5) + c0 + i;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = j * 8 + (lane >> 2);
+                    const uint32_t w = __shfl_sync(0xffffffffu, bytes, r);
+                    if (i < c1 - c0 && group < p.pre.eld && row0 + r < p.M)
+                        p.pre.e[(row0 + r) * p.pre.eld + group] = static_cast<uint8_t>(w >> (8 * i));
+                }
+            }
+            if (c0 >= c1 && lane == 0) bar_arrive_remote(remote_addr(smem_addr(&bars->tmem_empty[buf]), 0));
         }
     }
 
@@ -577,7 +598,8 @@ __global__ void __launch_bounds__(128) finish_kernel(const __grid_constant__ Pro
     int tm, tn;
     place_tile(pl, static_cast<uint32_t>(pl.whole) + shared, &tm, &tn);
     const int j0 = pl.parts * warp / 4, j1 = pl.parts * (warp + 1) / 4;
-    const float4* q = pl.sums(shared, j0, rank * kEpiWarps + (c & 1) * 4 + quad) + (c >> 1) * 256 + lane;
+    const int first = (pl.bn / 32 + 1) / 2, half = c >= first ? 1 : 0;   // as the product's epilogue divides a tile
+    const float4* q = pl.sums(shared, j0, rank * kEpiWarps + half * 4 + quad) + (c - half * first) * 256 + lane;
     const int64_t next = static_cast<int64_t>(kPieces) * (kPiece / 4);
     float v[32];
 #pragma unroll
@@ -603,8 +625,17 @@ __global__ void __launch_bounds__(128) finish_kernel(const __grid_constant__ Pro
             v[4 * s] += f.x; v[4 * s + 1] += f.y; v[4 * s + 2] += f.z; v[4 * s + 3] += f.w;
         }
     }
-    finish_chunk<VEC, SLOPE>(p, pl, static_cast<int64_t>(tm) * 256 + rank * 128 + quad * 32,
-                             static_cast<int64_t>(tn) * pl.bn + c * 32, v, buf[0], lane);
+    const int64_t col0 = static_cast<int64_t>(tn) * pl.bn + c * 32;
+    if (VEC > 0 && p.bias != nullptr) {
+        __syncwarp();
+        reinterpret_cast<float*>(buf[0])[lane] = col0 + lane < p.N ? load1(p.bias, p.bias_dtype, col0 + lane) : 0.0f;
+        __syncwarp();
+    }
+    const int64_t row0 = static_cast<int64_t>(tm) * 256 + rank * 128 + quad * 32;
+    uint32_t byte = 0;
+    finish_chunk<VEC, SLOPE>(p, pl, row0, col0, v, buf[0], lane, &byte);
+    if (VEC > 0 && !SLOPE && p.pre.dtype == FSDP_DTYPE_ACT8 && p.pre.p != nullptr && row0 + lane < p.M && col0 < p.N)
+        p.pre.e[(row0 + lane) * p.pre.eld + (col0 >> 5)] = static_cast<uint8_t>(byte);
 }
 
 // Rows of a bf16 matrix that do not start on 16-byte boundaries, copied to
