@@ -241,21 +241,20 @@ __device__ __forceinline__ Unit unit_of(const Plan& p, uint32_t u) {
 }
 
 // One 32 x 32 chunk whose rows lie one to a lane: v[j] is tile row `row0 +
-// lane`, tile column `col0 + j`.  buf: the warp's 4 KiB of shared memory, in
-// which 16-byte slot s of row r lies at s ^ (r & 7)
-// (no bank conflicts writing, and none reading along a row).  Where rows are
-// aligned, its first 32 floats are the chunk's bias.
+// lane`, tile column `col0 + j`.  buf: 4 KiB of shared memory for rows that are
+// not aligned, in which 16-byte slot s of row r lies at s ^ (r & 7) (no bank
+// conflicts writing, and none reading along a row).
 template <int VEC, bool SLOPE>
 __device__ __forceinline__ void finish_chunk(const Product& p, const Plan& pl, int64_t row0, int64_t col0, float* v,
-                                             float4* buf, int lane, uint32_t* byte) {
+                                             float4* buf, int lane, float bias, const Operands& from, uint32_t* byte) {
     if constexpr (VEC > 0) {
-        if (col0 < p.N && row0 + lane < p.M) finish_row<VEC == 2, SLOPE>(p, row0 + lane, col0, buf, v, byte);
+        if (col0 < p.N) finish_row<VEC == 2, SLOPE>(p, row0 + lane, col0, row0 + lane < p.M, bias, v, from, byte);
     } else {
         // one column of C to a lane
         const int64_t m0 = pl.swapped ? col0 : row0, n = (pl.swapped ? row0 : col0) + lane;
         const int count = static_cast<int>(min(static_cast<int64_t>(32), p.M - m0));
         if (count <= 0 || n - lane >= p.N) return;   // the same for the whole warp
-        const float bias = p.bias != nullptr && n < p.N ? load1(p.bias, p.bias_dtype, n) : 0.0f;
+        bias = p.bias != nullptr && n < p.N ? load1(p.bias, p.bias_dtype, n) : 0.0f;
         if (!pl.swapped) {   // swapped, the lane's tile row is that column already
 #pragma unroll
             for (int s = 0; s < 8; ++s)
@@ -287,7 +286,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     volatile uint32_t* abort = &bars->abort;
     const uint32_t stages = pl.stages;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // through a shuffle, which makes it uniform to the compiler: so are then the
+    // branches on it, and what the warps' roles compute in them
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const uint32_t cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
 
@@ -316,7 +317,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     cluster_sync();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    const uint32_t tmem = bars->tmem_base;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
     starts_early();
     after_previous();
     // The producers' and the matrix warp's loops run in whole warps, one lane of
@@ -444,20 +445,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float4* buf4 = epi + w * (kEpiBytes / 16);
         // the warp's chunks of 32 columns: the first or the second half of the tile's
         const int chunks = pl.bn / 32, c0 = half ? (chunks + 1) / 2 : 0, c1 = half ? chunks : (chunks + 1) / 2;
+        // chunks of what the epilogue reads that fit the warp's 4 KiB (256 pieces of 16 bytes)
+        const int pre_pieces = SLOPE ? staged_pieces(p.pre.dtype) : 0;
+        const int chunk_pieces = pre_pieces + (p.add.p != nullptr ? staged_pieces(p.add.dtype) : 0);
+        const int depth = chunk_pieces <= 2 ? 4 : chunk_pieces <= 4 ? 2 : 1;
         uint32_t tile = 0;
         for (uint32_t u = cluster; u < pl.units; u += clusters, ++tile) {
             const Unit un = unit_of(pl, u);
             const uint32_t buf = tile & 1u;
             const int64_t row0 = static_cast<int64_t>(un.tm) * 256 + rank * 128 + quad * 32;
             const int64_t col0 = static_cast<int64_t>(un.tn) * pl.bn;
-            if (VEC > 0 && p.bias != nullptr) {   // of this warp's chunks, before their sums are there
-                __syncwarp();
+            // What the epilogue reads is on its way before the tile's sums are
+            // there, a few chunks ahead: the operands' copies keep the SM's port
+            // from L2 busy, so that a load issued when it is needed waits for
+            // 2000 cycles and more behind them.
+            const bool staged = VEC > 0 && un.shared < 0 && chunk_pieces > 0 && chunk_pieces <= 8;
+            const bool row_on = row0 + lane < p.M;
+            const auto fetch = [&](int i) {
+                const int64_t n = col0 + (c0 + i) * 32;
+                if (i < c1 - c0 && row_on && n < p.N) {
+                    const int left = static_cast<int>(min(static_cast<int64_t>(32), p.N - n));
+                    float4* at = buf4 + (i % depth) * chunk_pieces * 32 + lane;
+                    if (SLOPE) stage_row32(p.pre, row0 + lane, n, left, at);
+                    if (p.add.p != nullptr) stage_row32(p.add, row0 + lane, n, left, at + pre_pieces * 32);
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            float bias[4] = {};
+            uint32_t pre_bytes = 0;
+            if (staged) {
+                for (int i = 0; i < depth; ++i) fetch(i);
+                if (SLOPE && p.pre.dtype == FSDP_DTYPE_ACT8 && row_on) {
+                    const uint8_t* e = p.pre.e + (row0 + lane) * p.pre.eld + (col0 >> 5) + c0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < c1 - c0 && col0 + (c0 + i) * 32 < p.N) pre_bytes |= static_cast<uint32_t>(e[i]) << (8 * i);
+                }
+            }
+            if (VEC > 0 && p.bias != nullptr) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int64_t n = col0 + (c0 + i) * 32 + lane;
-                    reinterpret_cast<float*>(buf4)[i * 32 + lane] = i < c1 - c0 && n < p.N ? load1(p.bias, p.bias_dtype, n) : 0.0f;
+                    if (i < c1 - c0 && n < p.N) bias[i] = load1(p.bias, p.bias_dtype, n);
                 }
-                __syncwarp();
             }
             // the whole warp goes on or none of it
             if (!bar_wait_warp(smem_addr(&bars->tmem_full[buf]), (tile / 2) & 1u, pl.wait_cycles, abort)) {
@@ -483,9 +513,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int s = 0; s < 8; ++s)
                         sums[(c - c0) * 256 + s * 32] = make_float4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]);
                 } else {
+                    const int i = c - c0;
+                    Operands from{};
+                    if (staged) {
+                        if (depth == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+                        else if (depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+                        else asm volatile("cp.async.wait_group 0;" ::: "memory");
+                        from.pre = buf4 + (i % depth) * chunk_pieces * 32 + lane;
+                        from.add = from.pre + pre_pieces * 32;
+                        from.byte = pre_bytes >> (8 * i) & 255u;
+                    }
                     uint32_t byte = 0;
-                    finish_chunk<VEC, SLOPE>(p, pl, row0, col0 + c * 32, v, VEC > 0 ? buf4 + (c - c0) * 8 : buf4, lane, &byte);
-                    bytes |= byte << (8 * (c - c0));
+                    finish_chunk<VEC, SLOPE>(p, pl, row0, col0 + c * 32, v, buf4, lane,
+                                             i == 0 ? bias[0] : i == 1 ? bias[1] : i == 2 ? bias[2] : bias[3], from, &byte);
+                    bytes |= byte << (8 * i);
+                    if (staged) fetch(i + depth);
                 }
             }
             if (VEC > 0 && !SLOPE && sums == nullptr && p.pre.p != nullptr && p.pre.dtype == FSDP_DTYPE_ACT8) {
@@ -626,14 +668,10 @@ __global__ void __launch_bounds__(128) finish_kernel(const __grid_constant__ Pro
         }
     }
     const int64_t col0 = static_cast<int64_t>(tn) * pl.bn + c * 32;
-    if (VEC > 0 && p.bias != nullptr) {
-        __syncwarp();
-        reinterpret_cast<float*>(buf[0])[lane] = col0 + lane < p.N ? load1(p.bias, p.bias_dtype, col0 + lane) : 0.0f;
-        __syncwarp();
-    }
     const int64_t row0 = static_cast<int64_t>(tm) * 256 + rank * 128 + quad * 32;
+    const float bias = VEC > 0 && p.bias != nullptr && col0 + lane < p.N ? load1(p.bias, p.bias_dtype, col0 + lane) : 0.0f;
     uint32_t byte = 0;
-    finish_chunk<VEC, SLOPE>(p, pl, row0, col0, v, buf[0], lane, &byte);
+    finish_chunk<VEC, SLOPE>(p, pl, row0, col0, v, buf[0], lane, bias, Operands{}, &byte);
     if (VEC > 0 && !SLOPE && p.pre.dtype == FSDP_DTYPE_ACT8 && p.pre.p != nullptr && row0 + lane < p.M && col0 < p.N)
         p.pre.e[(row0 + lane) * p.pre.eld + (col0 >> 5)] = static_cast<uint8_t>(byte);
 }
