@@ -739,9 +739,9 @@ cudaError_t make_map(CUtensorMap* map, const Mat& m, int64_t rows, int64_t cols,
 // turn; what is left over after the last full round may be cut along k so that
 // every cluster has a part.  The width and the choice are those of the least
 // estimated time, in cycles.  Measured with whole rounds of tiles: a stage takes
-// 2.34 cycles a column where the products bound it (256: 600, 192: 455), and
-// otherwise what its copies take (20 KiB an SM: 382, 24 KiB: 410, 32 KiB: 500),
-// which is the rate at which an SM takes data from L2, about 60 bytes a cycle.
+// 2.3 cycles a column where the products bound it (256: 580, 192: 453), what its
+// copies take at 75 bytes a cycle an SM (32 KiB: 442), and 275 at least; a
+// tile's epilogue 13 a column.
 Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, int clusters) {
     Plan best{};
     double least = 0;
@@ -757,7 +757,7 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, int clu
         p.stage_b = b_by_rows ? (bn > 128 ? 2 : 1) * kBlock : bn / 2 * kDepth * 2;   // a multiple of 1024
         p.stages = std::min(kStagesMost, kRingBytes / (kStageA + p.stage_b));
         const double copied = kStageA + p.stage_b;
-        const double stage = std::max(2.34 * bn, 382.0 + 0.0095 * (copied - 20480.0));
+        const double stage = std::max({2.3 * bn + 10.0, 275.0, copied / 75.0});
         for (int share = 0; share < 2; ++share) {
             const int64_t left = tiles % clusters;
             p.parts = share == 0 || left == 0 ? 1 : static_cast<int>(std::min<int64_t>(clusters / left, std::max(1, p.ks / 4)));
@@ -765,7 +765,7 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, int clu
             p.whole = static_cast<uint32_t>(p.parts > 1 ? tiles - left : tiles);
             p.units = static_cast<uint32_t>(p.whole + (tiles - p.whole) * p.parts);
             const double rounds = static_cast<double>((p.whole + clusters - 1) / clusters);
-            double t = rounds * (std::max(steps * stage, 2500.0 + 10.0 * bn) + 300.0) + 10.0 * bn;
+            double t = rounds * (std::max(steps * stage, 400.0 + 13.0 * bn) + 300.0) + 13.0 * bn;
             if (p.parts > 1) t += (p.ks + p.parts - 1) / p.parts * stage + 9000.0 + 60.0 * p.parts;
             if (least == 0 || t < least) {
                 least = t;
