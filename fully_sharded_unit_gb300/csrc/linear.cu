@@ -676,26 +676,44 @@ __global__ void __launch_bounds__(128) finish_kernel(const __grid_constant__ Pro
         p.pre.e[(row0 + lane) * p.pre.eld + (col0 >> 5)] = static_cast<uint8_t>(byte);
 }
 
-// Rows of a bf16 matrix that do not start on 16-byte boundaries, copied to
-// ones that do (dst.ld a multiple of 8).
-__global__ void __launch_bounds__(256) align_rows_kernel(int64_t rows, int64_t cols, Mat src, Mat dst) {
+// Rows of a bf16 matrix that do not start on 16-byte boundaries, copied to ones
+// that do (dst.ld a multiple of 8): eight elements to a thread, from the two
+// 16-byte words that hold them, moved together.  A word is read only if it holds
+// a byte between the matrix's first element and its last; what dst gets past a
+// row's end is not defined.
+__global__ void __launch_bounds__(256) align_rows_kernel(int64_t rows, int64_t cols, Mat src, Mat dst, uint32_t chunks) {
     starts_early();
     after_previous();
-    const int64_t chunks = (cols + 7) / 8;
-    for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
-        const uint16_t* s = static_cast<const uint16_t*>(src.p) + row * src.ld;
-        uint16_t* d = static_cast<uint16_t*>(dst.p) + row * dst.ld;
-        for (int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; c < chunks;
-             c += static_cast<int64_t>(gridDim.x) * 256) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t i = c * 8 + 2 * j;
-                const uint32_t lo = i < cols ? s[i] : 0, hi = i + 1 < cols ? s[i + 1] : 0;
-                w[j] = lo | hi << 16;
-            }
-            *reinterpret_cast<uint4*>(d + c * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+    const uintptr_t end = reinterpret_cast<uintptr_t>(src.p) + ((rows - 1) * src.ld + cols) * 2;
+    const int64_t count = rows * chunks, stride = static_cast<int64_t>(gridDim.x) * 256;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < count; i += stride) {
+        const int64_t row = i <= 0xffffffffll ? static_cast<uint32_t>(i) / chunks : i / chunks;
+        const int64_t c = (i - row * chunks) * 8;
+        const uintptr_t from = reinterpret_cast<uintptr_t>(src.p) + (row * src.ld + c) * 2;
+        const uintptr_t word = from & ~uintptr_t(15);
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(word));
+        uint4 b = make_uint4(0, 0, 0, 0);
+        if (from != word && word + 16 < end) b = __ldg(reinterpret_cast<const uint4*>(word + 16));
+        const uint32_t shift = static_cast<uint32_t>(from & 2) * 8;
+        uint4 o;
+        switch ((from >> 2) & 3) {
+            case 0:
+                o = make_uint4(__funnelshift_r(a.x, a.y, shift), __funnelshift_r(a.y, a.z, shift), __funnelshift_r(a.z, a.w, shift),
+                               __funnelshift_r(a.w, b.x, shift));
+                break;
+            case 1:
+                o = make_uint4(__funnelshift_r(a.y, a.z, shift), __funnelshift_r(a.z, a.w, shift), __funnelshift_r(a.w, b.x, shift),
+                               __funnelshift_r(b.x, b.y, shift));
+                break;
+            case 2:
+                o = make_uint4(__funnelshift_r(a.z, a.w, shift), __funnelshift_r(a.w, b.x, shift), __funnelshift_r(b.x, b.y, shift),
+                               __funnelshift_r(b.y, b.z, shift));
+                break;
+            default:
+                o = make_uint4(__funnelshift_r(a.w, b.x, shift), __funnelshift_r(b.x, b.y, shift), __funnelshift_r(b.y, b.z, shift),
+                               __funnelshift_r(b.z, b.w, shift));
         }
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst.p) + row * dst.ld + c) = o;
     }
 }
 
@@ -823,9 +841,9 @@ cudaError_t settle(Mat* m, int64_t rows, int64_t cols, char** room, int sms, cud
         // the checkpoint's pad elements are zeros: whole vectors can be read
         e = launch_act8_unpack(rows, d.ld, *m, FSDP_ACTIVATION_NONE, d, sms, st);
     } else {
-        const dim3 grid(static_cast<unsigned>(std::min<int64_t>((d.ld / 8 + 255) / 256, 1024)),
-                        static_cast<unsigned>(std::min<int64_t>(rows, 65535)));
-        e = launch_early(align_rows_kernel, grid, 256, 0, st, rows, cols, *m, d);
+        const int64_t count = rows * (d.ld / 8);
+        const dim3 grid(static_cast<unsigned>(std::min<int64_t>((count + 255) / 256, static_cast<int64_t>(sms) * 16)));
+        e = launch_early(align_rows_kernel, grid, 256, 0, st, rows, cols, *m, d, static_cast<uint32_t>(d.ld / 8));
     }
     *m = d;
     return e;

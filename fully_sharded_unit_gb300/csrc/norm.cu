@@ -877,7 +877,7 @@ cudaError_t launch_norm_backward(const NormBackward& a, int sms, cudaStream_t st
                           a.x.dtype != FSDP_DTYPE_F32 && (a.add.p == nullptr || a.add.dtype == FSDP_DTYPE_BF16);
         e = cudaErrorInvalidConfiguration;
 #define RING_(nv, gt_, f, k)                                                                                      \
-    if (fast == f && kept == k) e = launch_shared<norm_backward_ring_kernel<nv, gt_, nv <= 3 ? 512 : 256, f, k>>( \
+    if (fast == f && kept == k) e = launch_shared<norm_backward_ring_kernel<nv, gt_, (nv <= 3 ? 512 : 256), f, k>>( \
         blocks, p.threads(), bytes, st, a, places)
 #define RING(nv, gt_)                    \
     if (p.NV == nv && p.gt == gt_) {     \
