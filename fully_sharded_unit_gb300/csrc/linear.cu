@@ -174,6 +174,22 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float* v) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const float* v) {
+    uint32_t r[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
 // Shared-memory descriptor of an operand slice, 128-byte swizzled.  Contiguous
 // along k: rows of 64 elements, 8-row groups 1024 bytes apart.  Contiguous
 // along its rows: blocks of 64 rows x 64 k, kBlock apart, 8-k groups 1024
@@ -188,6 +204,8 @@ struct Plan {
     int ks;                    // stages' worth of k
     int bn;                    // columns of a tile: 32 .. 256 in steps of 32
     int stages, stage_b;       // stages in the ring, and B's bytes in one, per CTA
+    int slice;                 // stages after which the sums leave the tensor cores' accumulator
+    int buffer;                // columns of tensor memory between the two accumulators
     int tiles_m, tiles_n;
     uint32_t whole;            // tiles done by one cluster each
     uint32_t units;            // whole + (tiles - whole) * parts
@@ -391,41 +409,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint64_t da = da0, db = db0;
         uint32_t q = 0, s = 0, use = 0, tile = 0;
         bool ok = true;
-        for (uint32_t u = cluster; u < pl.units && ok; u += clusters, ++tile) {
+        for (uint32_t u = cluster; u < pl.units && ok; u += clusters) {
             const Unit un = unit_of(pl, u);
-            const uint32_t buf = tile & 1u, d = tmem + buf * 256;
-            if (tile >= 2 && !bar_wait_warp(tmem_empty0 + buf * 8, (tile / 2 - 1) & 1u, pl.wait_cycles, abort)) {
-                ok = false;
-                break;
-            }
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            uint32_t add = 0;
-            for (int k = un.k0; k < un.k1; ++k) {
-                if (!bar_wait_warp(full0 + s * 8, use, pl.wait_cycles, abort)) {
+            for (int first = un.k0; first < un.k1 && ok; first += pl.slice, ++tile) {
+                const int end = min(un.k1, first + pl.slice);
+                const uint32_t buf = tile & 1u, d = tmem + buf * pl.buffer;
+                if (tile >= 2 && !bar_wait_warp(tmem_empty0 + buf * 8, (tile / 2 - 1) & 1u, pl.wait_cycles, abort)) {
                     ok = false;
                     break;
                 }
-                if (k + 1 < pl.ks || last == 4) {
-                    mma(leader, d, da, db, idesc, add);
-                    mma(leader, d, da + step_a, db + step_b, idesc, 1u);
-                    mma(leader, d, da + 2 * step_a, db + 2 * step_b, idesc, 1u);
-                    mma(leader, d, da + 3 * step_a, db + 3 * step_b, idesc, 1u);
-                } else {
-                    for (int i = 0; i < last; ++i) mma(leader, d, da + i * step_a, db + i * step_b, idesc, add | i);
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                uint32_t add = 0;
+                for (int k = first; k < end; ++k) {
+                    if (!bar_wait_warp(full0 + s * 8, use, pl.wait_cycles, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    if (k + 1 < pl.ks || last == 4) {
+                        mma(leader, d, da, db, idesc, add);
+                        mma(leader, d, da + step_a, db + step_b, idesc, 1u);
+                        mma(leader, d, da + 2 * step_a, db + 2 * step_b, idesc, 1u);
+                        mma(leader, d, da + 3 * step_a, db + 3 * step_b, idesc, 1u);
+                    } else {
+                        for (int i = 0; i < last; ++i) mma(leader, d, da + i * step_a, db + i * step_b, idesc, add | i);
+                    }
+                    add = 1;
+                    mma_commit(leader, empty0 + s * 8);
+                    ++q;
+                    da += kStageA >> 4;
+                    db += next_b;
+                    if (++s == stages) {
+                        s = 0;
+                        use ^= 1u;
+                        da = da0;
+                        db = db0;
+                    }
                 }
-                add = 1;
-                mma_commit(leader, empty0 + s * 8);
-                ++q;
-                da += kStageA >> 4;
-                db += next_b;
-                if (++s == stages) {
-                    s = 0;
-                    use ^= 1u;
-                    da = da0;
-                    db = db0;
-                }
+                if (ok) mma_commit(leader, tmem_full0 + buf * 8);
             }
-            if (ok) mma_commit(leader, tmem_full0 + buf * 8);
         }
         if (lane == 0) bars->consumed = q;
         if (!ok) {
@@ -452,7 +473,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t tile = 0;
         for (uint32_t u = cluster; u < pl.units; u += clusters, ++tile) {
             const Unit un = unit_of(pl, u);
-            const uint32_t buf = tile & 1u;
             const int64_t row0 = static_cast<int64_t>(un.tm) * 256 + rank * 128 + quad * 32;
             const int64_t col0 = static_cast<int64_t>(un.tn) * pl.bn;
             // What the epilogue reads is on its way before the tile's sums are
@@ -489,20 +509,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (i < c1 - c0 && n < p.N) bias[i] = load1(p.bias, p.bias_dtype, n);
                 }
             }
+            // the slices of a long sum but the last are added up in tensor memory;
             // the whole warp goes on or none of it
-            if (!bar_wait_warp(smem_addr(&bars->tmem_full[buf]), (tile / 2) & 1u, pl.wait_cycles, abort)) {
+            const uint32_t sliced = tmem + 2 * pl.buffer + (static_cast<uint32_t>(quad * 32) << 16);
+            uint32_t buf = tile & 1u, src = 0;
+            bool given_up = false;
+            for (int first = un.k0;; first += pl.slice, ++tile) {
+                buf = tile & 1u;
+                src = tmem + buf * pl.buffer + (static_cast<uint32_t>(quad * 32) << 16);
+                given_up = !bar_wait_warp(smem_addr(&bars->tmem_full[buf]), (tile / 2) & 1u, pl.wait_cycles, abort);
+                if (given_up) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                if (first + pl.slice >= un.k1) break;
+                for (int c = c0; c < c1; ++c) {
+                    float v[32];
+                    tmem_load32(src + c * 32, v);
+                    if (first > un.k0) {
+                        float w[32];
+                        tmem_load32(sliced + c * 32, w);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] += w[j];
+                    }
+                    tmem_store32(sliced + c * 32, v);
+                }
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) bar_arrive_remote(remote_addr(smem_addr(&bars->tmem_empty[buf]), 0));
+            }
+            if (given_up) {
                 if (lane == 0) atomicOr(pl.status, FSDP_KSTATUS_WAIT_TIMEOUT);
                 *abort = 1;
                 break;
             }
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t src = tmem + buf * 256 + (static_cast<uint32_t>(quad * 32) << 16);
             // a tile shared along k leaves its sums in the workspace, for finish_kernel
             float4* sums = un.shared < 0 ? nullptr : pl.sums(un.shared, un.part, static_cast<int>(rank) * kEpiWarps + w) + lane;
             uint32_t bytes = 0;   // exponents of this warp's chunks of the lane's row
             for (int c = c0; c < c1; ++c) {
                 float v[32];
                 tmem_load32(src + c * 32, v);
+                if (un.k1 - un.k0 > pl.slice) {
+                    float w[32];
+                    tmem_load32(sliced + c * 32, w);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] += w[j];
+                }
                 if (c + 1 == c1) {
                     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                     __syncwarp();
@@ -760,14 +810,27 @@ cudaError_t make_map(CUtensorMap* map, const Mat& m, int64_t rows, int64_t cols,
 // 2.3 cycles a column where the products bound it (256: 580, 192: 453), what its
 // copies take at 75 bytes a cycle an SM (32 KiB: 442), and 275 at least; a
 // tile's epilogue 13 a column.
-Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, int clusters) {
+//
+// Long sums: the tensor cores cut an accumulator off to 24 bits with every 16
+// products (measured: a relative error of 1.1e-9 k for random signs, at k =
+// 16384 already 1.8e-5), which an F32 result would show.  So where one is
+// asked for and k is above kLongSum stages, the accumulator is emptied every
+// kSlice stages (k = 4096) and the slices are added in fp32, rounded to nearest;
+// the running sums need tensor memory, which leaves tiles of at most 160 columns.
+constexpr int kLongSum = 96, kSlice = 64;
+
+Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, bool exact_sums, int clusters) {
     Plan best{};
     double least = 0;
-    for (int bn = 256; bn >= 32; bn -= 32) {
-        if (bn < 256 && bn >= 2 * cols && bn > 32) continue;
+    const bool sliced = exact_sums && k > static_cast<int64_t>(kLongSum) * kDepth;
+    const int widest = sliced ? 160 : 256;
+    for (int bn = widest; bn >= 32; bn -= 32) {
+        if (bn < widest && bn >= 2 * cols && bn > 32) continue;
         Plan p{};
         p.ks = static_cast<int>((k + kDepth - 1) / kDepth);
         p.bn = bn;
+        p.slice = sliced ? kSlice : 0x40000000;
+        p.buffer = sliced ? bn : 256;
         p.tiles_m = static_cast<int>((rows + 255) / 256);
         p.tiles_n = static_cast<int>((cols + bn - 1) / bn);
         const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
@@ -882,7 +945,8 @@ cudaError_t launch_product(const Product& given, const ProductRoom& room, int sm
         std::swap(p.a_trans, p.b_trans);
         std::swap(rows, cols);
     }
-    Plan pl = plan_product(rows, cols, p.K, p.b_trans, clusters);
+    const bool f32 = p.out.dtype == FSDP_DTYPE_F32 || (!p.slope && p.pre.p != nullptr && p.pre.dtype == FSDP_DTYPE_F32);
+    Plan pl = plan_product(rows, cols, p.K, p.b_trans, f32, clusters);
     pl.swapped = swap;
     pl.vec = swap ? 0 : vec;
     pl.partials = room.partials;

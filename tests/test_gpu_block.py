@@ -513,3 +513,27 @@ def test_layer_norm_many_rows(handle, rows, cols):
     assert torch.equal(k.q, other.q) and torch.equal(k.exps, other.exps)
     for ckpt, add in ((False, "other"), (True, None)):
         _norm_grad_case(handle, rows, cols, 0, 0, BF, BF, BF, F32, ckpt, add, False)
+
+
+@pytest.mark.parametrize("T,I,O_,kind", [(300, 16384, 512, "fwd"), (20000, 264, 512, "dw"), (300, 40000, 8192, "fwd")])
+def test_long_fp32_sums_do_not_drift(handle, T, I, O_, kind):
+    """All products positive, so that an accumulator which cuts off instead of
+    rounding errs the same way in every step.  A slice of 4096 products is 256
+    steps, each off by at most a unit of 2^-23 of the sum; the slices' own
+    additions round to nearest."""
+    c = B.Compute(B.fsdp_linear_workspace_bytes(T, I, O_))
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(T)
+    x = torch.rand((T, I), device="cuda", generator=gen).to(BF)
+    if kind == "fwd":
+        w = torch.rand((I, O_), device="cuda", generator=gen).to(BF)
+        got, want, k = torch.empty((T, O_), device="cuda"), x.double() @ w.double(), I
+        c.linear_forward(x, w, got)
+    else:
+        dy = torch.rand((T, O_), device="cuda", generator=gen).to(BF)
+        got, want, k = torch.empty((I, O_), device="cuda"), x.double().t() @ dy.double(), T
+        c.linear_grad_weight(x, dy, got)
+    assert c.status() == 0
+    off = ((got.double() - want).abs() / want).max().item()
+    assert off <= 256 * 2.0 ** -23 + (k / 4096 + 20) * 2.0 ** -24, off
+    c.close()
