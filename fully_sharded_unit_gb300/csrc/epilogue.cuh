@@ -118,52 +118,6 @@ __device__ __forceinline__ uint32_t store_row32(const Mat& x, int64_t m, int64_t
     return 0;
 }
 
-// 32 columns of a lane's row on their way through shared memory: 16-byte piece
-// j of lane l at j*32 + l (neighbouring lanes on neighbouring banks).  A lane
-// copies and reads only its own pieces.
-__device__ __forceinline__ int staged_pieces(int dtype) { return dtype == FSDP_DTYPE_F32 ? 8 : dtype == FSDP_DTYPE_BF16 ? 4 : 2; }
-
-__device__ __forceinline__ void stage_row32(const Mat& x, int64_t m, int64_t n, int left, float4* to) {
-    const int esz = x.dtype == FSDP_DTYPE_F32 ? 4 : x.dtype == FSDP_DTYPE_BF16 ? 2 : 1;
-    const char* src = static_cast<const char*>(x.p) + (m * x.ld + n) * esz;
-    const int pieces = x.dtype == FSDP_DTYPE_ACT8 ? 2 : left * esz / 16;   // a checkpoint's group is whole
-    const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
-    for (int j = 0; j < pieces; ++j)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + j * 512), "l"(src + j * 16) : "memory");
-}
-
-// What stage_row32 copied; elements past `left` are not defined.
-__device__ __forceinline__ void unstage_row32(const float4* from, int dtype, uint32_t byte, float* v) {
-    if (dtype == FSDP_DTYPE_F32) {
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            const float4 f = from[s * 32];
-            v[4 * s] = f.x; v[4 * s + 1] = f.y; v[4 * s + 2] = f.z; v[4 * s + 3] = f.w;
-        }
-    } else if (dtype == FSDP_DTYPE_BF16) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) unpack8(*reinterpret_cast<const uint4*>(from + s * 32), v + 8 * s);
-    } else {
-        const float step = act8_step(byte);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const uint4 w = *reinterpret_cast<const uint4*>(from + s * 32);
-            act8_read4(w.x, step, v + 16 * s);
-            act8_read4(w.y, step, v + 16 * s + 4);
-            act8_read4(w.z, step, v + 16 * s + 8);
-            act8_read4(w.w, step, v + 16 * s + 12);
-        }
-    }
-}
-
-// Where a row's epilogue finds what it combines the sums with: staged pieces of
-// the kept pre-activation (and its exponent byte) and of the added matrix, or
-// null to read them from global memory.
-struct Operands {
-    const float4 *pre, *add;
-    uint32_t byte;
-};
-
 // The epilogue of 32 columns of one row: everything a lane needs is in its own
 // registers (a checkpoint's group too), so 32 independent elements hide each
 // other's latency, and every access is a whole 32-byte sector.  `bias` is the
@@ -172,7 +126,7 @@ struct Operands {
 // exists.
 template <bool WIDE, bool SLOPE>
 __device__ __forceinline__ void finish_row(const Product& p, int64_t m, int64_t n, bool on, float bias, float* v,
-                                           const Operands& from, uint32_t* byte) {
+                                           uint32_t* byte) {
     const int left = static_cast<int>(min(static_cast<int64_t>(32), p.N - n));
     if (p.bias != nullptr) {
 #pragma unroll
@@ -181,8 +135,7 @@ __device__ __forceinline__ void finish_row(const Product& p, int64_t m, int64_t 
     if (!on) return;
     if (SLOPE) {
         float z[32];
-        if (from.pre != nullptr) unstage_row32(from.pre, p.pre.dtype, from.byte, z);
-        else load_row32<WIDE>(p.pre, m, n, left, z);
+        load_row32<WIDE>(p.pre, m, n, left, z);
         slope_n<32>(v, z, p.act);
     } else {
         if (p.pre.p != nullptr) *byte = store_row32<WIDE>(p.pre, m, n, left, v);
@@ -190,8 +143,7 @@ __device__ __forceinline__ void finish_row(const Product& p, int64_t m, int64_t 
     }
     if (p.add.p != nullptr) {
         float e[32];
-        if (from.add != nullptr) unstage_row32(from.add, p.add.dtype, 0, e);
-        else load_row32<WIDE>(p.add, m, n, left, e);
+        load_row32<WIDE>(p.add, m, n, left, e);
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] += e[j];
     }

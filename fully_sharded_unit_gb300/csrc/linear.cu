@@ -264,9 +264,9 @@ __device__ __forceinline__ Unit unit_of(const Plan& p, uint32_t u) {
 // conflicts writing, and none reading along a row).
 template <int VEC, bool SLOPE>
 __device__ __forceinline__ void finish_chunk(const Product& p, const Plan& pl, int64_t row0, int64_t col0, float* v,
-                                             float4* buf, int lane, float bias, const Operands& from, uint32_t* byte) {
+                                             float4* buf, int lane, float bias, uint32_t* byte) {
     if constexpr (VEC > 0) {
-        if (col0 < p.N) finish_row<VEC == 2, SLOPE>(p, row0 + lane, col0, row0 + lane < p.M, bias, v, from, byte);
+        if (col0 < p.N) finish_row<VEC == 2, SLOPE>(p, row0 + lane, col0, row0 + lane < p.M, bias, v, byte);
     } else {
         // one column of C to a lane
         const int64_t m0 = pl.swapped ? col0 : row0, n = (pl.swapped ? row0 : col0) + lane;
@@ -466,42 +466,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float4* buf4 = epi + w * (kEpiBytes / 16);
         // the warp's chunks of 32 columns: the first or the second half of the tile's
         const int chunks = pl.bn / 32, c0 = half ? (chunks + 1) / 2 : 0, c1 = half ? chunks : (chunks + 1) / 2;
-        // chunks of what the epilogue reads that fit the warp's 4 KiB (256 pieces of 16 bytes)
-        const int pre_pieces = SLOPE ? staged_pieces(p.pre.dtype) : 0;
-        const int chunk_pieces = pre_pieces + (p.add.p != nullptr ? staged_pieces(p.add.dtype) : 0);
-        const int depth = chunk_pieces <= 2 ? 4 : chunk_pieces <= 4 ? 2 : 1;
         uint32_t tile = 0;
         for (uint32_t u = cluster; u < pl.units; u += clusters, ++tile) {
             const Unit un = unit_of(pl, u);
             const int64_t row0 = static_cast<int64_t>(un.tm) * 256 + rank * 128 + quad * 32;
             const int64_t col0 = static_cast<int64_t>(un.tn) * pl.bn;
-            // What the epilogue reads is on its way before the tile's sums are
-            // there, a few chunks ahead: the operands' copies keep the SM's port
-            // from L2 busy, so that a load issued when it is needed waits for
-            // 2000 cycles and more behind them.
-            const bool staged = VEC > 0 && un.shared < 0 && chunk_pieces > 0 && chunk_pieces <= 8;
-            const bool row_on = row0 + lane < p.M;
-            const auto fetch = [&](int i) {
-                const int64_t n = col0 + (c0 + i) * 32;
-                if (i < c1 - c0 && row_on && n < p.N) {
-                    const int left = static_cast<int>(min(static_cast<int64_t>(32), p.N - n));
-                    float4* at = buf4 + (i % depth) * chunk_pieces * 32 + lane;
-                    if (SLOPE) stage_row32(p.pre, row0 + lane, n, left, at);
-                    if (p.add.p != nullptr) stage_row32(p.add, row0 + lane, n, left, at + pre_pieces * 32);
-                }
-                asm volatile("cp.async.commit_group;" ::: "memory");
-            };
-            float bias[4] = {};
-            uint32_t pre_bytes = 0;
-            if (staged) {
-                for (int i = 0; i < depth; ++i) fetch(i);
-                if (SLOPE && p.pre.dtype == FSDP_DTYPE_ACT8 && row_on) {
-                    const uint8_t* e = p.pre.e + (row0 + lane) * p.pre.eld + (col0 >> 5) + c0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i < c1 - c0 && col0 + (c0 + i) * 32 < p.N) pre_bytes |= static_cast<uint32_t>(e[i]) << (8 * i);
-                }
-            }
+            float bias[4] = {};   // of the warp's chunks, read before their sums are there
             if (VEC > 0 && p.bias != nullptr) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -564,20 +534,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         sums[(c - c0) * 256 + s * 32] = make_float4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]);
                 } else {
                     const int i = c - c0;
-                    Operands from{};
-                    if (staged) {
-                        if (depth == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
-                        else if (depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-                        else asm volatile("cp.async.wait_group 0;" ::: "memory");
-                        from.pre = buf4 + (i % depth) * chunk_pieces * 32 + lane;
-                        from.add = from.pre + pre_pieces * 32;
-                        from.byte = pre_bytes >> (8 * i) & 255u;
-                    }
                     uint32_t byte = 0;
                     finish_chunk<VEC, SLOPE>(p, pl, row0, col0 + c * 32, v, buf4, lane,
-                                             i == 0 ? bias[0] : i == 1 ? bias[1] : i == 2 ? bias[2] : bias[3], from, &byte);
+                                             i == 0 ? bias[0] : i == 1 ? bias[1] : i == 2 ? bias[2] : bias[3], &byte);
                     bytes |= byte << (8 * i);
-                    if (staged) fetch(i + depth);
                 }
             }
             if (VEC > 0 && !SLOPE && sums == nullptr && p.pre.p != nullptr && p.pre.dtype == FSDP_DTYPE_ACT8) {
@@ -721,7 +681,7 @@ __global__ void __launch_bounds__(128) finish_kernel(const __grid_constant__ Pro
     const int64_t row0 = static_cast<int64_t>(tm) * 256 + rank * 128 + quad * 32;
     const float bias = VEC > 0 && p.bias != nullptr && col0 + lane < p.N ? load1(p.bias, p.bias_dtype, col0 + lane) : 0.0f;
     uint32_t byte = 0;
-    finish_chunk<VEC, SLOPE>(p, pl, row0, col0, v, buf[0], lane, bias, Operands{}, &byte);
+    finish_chunk<VEC, SLOPE>(p, pl, row0, col0, v, buf[0], lane, bias, &byte);
     if (VEC > 0 && !SLOPE && p.pre.dtype == FSDP_DTYPE_ACT8 && p.pre.p != nullptr && row0 + lane < p.M && col0 < p.N)
         p.pre.e[(row0 + lane) * p.pre.eld + (col0 >> 5)] = static_cast<uint8_t>(byte);
 }
