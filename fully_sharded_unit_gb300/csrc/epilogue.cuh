@@ -103,8 +103,7 @@ __device__ __forceinline__ uint32_t store_row32(const Mat& x, int64_t m, int64_t
         act8_quant_n<32>(v, top, act8_scale(act8_byte(top)), w);
         if (left < 32) {   // the pad of a short group is zeros
 #pragma unroll
-            for (int s = 0; s < 8; ++s)
-                if (s * 4 >= left) w[s] = 0u;
+            for (int s = 0; s < 8; ++s) w[s] = s * 4 >= left ? 0u : s * 4 + 4 <= left ? w[s] : w[s] & ((1u << 8 * (left - s * 4)) - 1u);
         }
         uint8_t* dst = static_cast<uint8_t*>(x.p) + m * x.ld + n;
         if (WIDE) {
@@ -116,6 +115,108 @@ __device__ __forceinline__ uint32_t store_row32(const Mat& x, int64_t m, int64_t
         return act8_byte(top);
     }
     return 0;
+}
+
+// The same from a row that starts anywhere (BF16 or F32): the 16-byte words that
+// hold the elements (each read only if it holds one), moved together by the
+// row's offset.  An element at a time, 32 loads of 64 bytes a warp, it took twice
+// the time of the whole product.
+template <int WORDS>
+__device__ __forceinline__ void load_window(uintptr_t from, int bytes, uint32_t* w) {
+    const uintptr_t word = from & ~uintptr_t(15), end = from + bytes;
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+        uint4 a = make_uint4(0, 0, 0, 0);
+        if (word + 16 * i < end) a = *reinterpret_cast<const uint4*>(word + 16 * i);
+        w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
+    }
+    if (from & 8) {
+#pragma unroll
+        for (int i = 0; i + 2 < 4 * WORDS; ++i) w[i] = w[i + 2];
+    }
+    if (from & 4) {
+#pragma unroll
+        for (int i = 0; i + 1 < 4 * WORDS; ++i) w[i] = w[i + 1];
+    }
+    if (from & 2) {
+#pragma unroll
+        for (int i = 0; i + 1 < 4 * WORDS; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+}
+
+__device__ __forceinline__ void load_row32_any(const Mat& x, int64_t m, int64_t n, int left, float* v) {
+    if (x.dtype == FSDP_DTYPE_ACT8) {
+        load_row32<false>(x, m, n, left, v);   // aligned by its format
+    } else if (x.dtype == FSDP_DTYPE_F32) {
+        uint32_t w[36];
+        load_window<9>(reinterpret_cast<uintptr_t>(static_cast<const float*>(x.p) + m * x.ld + n), left * 4, w);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]);
+    } else {
+        uint32_t w[20];
+        load_window<5>(reinterpret_cast<uintptr_t>(static_cast<const uint16_t*>(x.p) + m * x.ld + n), left * 2, w);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            v[2 * j] = bf16_lo(w[j]);
+            v[2 * j + 1] = bf16_hi(w[j]);
+        }
+    }
+}
+
+// A 32 x 32 chunk whose rows lie one to a lane, stored to rows that start
+// anywhere: turned in shared memory (buf: 4 KiB, 16-byte slot s of row r at
+// s ^ (r & 7): no bank conflicts either way), so that a store is a piece of one
+// row.  `count` rows from m, the lane's column n.
+__device__ __forceinline__ void store_rows_any(const Mat& x, int64_t m, int count, int64_t n, int64_t cols, const float* v,
+                                               float4* buf, int lane) {
+    float t[32];
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+        buf[lane * 8 + (s ^ (lane & 7))] = make_float4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]);
+    __syncwarp();
+    const float* f = reinterpret_cast<const float*>(buf);
+#pragma unroll
+    for (int r = 0; r < 32; ++r) t[r] = f[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)];
+    __syncwarp();
+    store_strided<32>(x.p, x.dtype, m * x.ld + n, x.ld, [&](int i) { return n < cols && i < count; }, t);
+}
+
+// The epilogue of a chunk whose matrices' rows start anywhere: as finish_row, a
+// row to a lane; only the stores go by columns.  All lanes take part.
+template <bool SLOPE>
+__device__ __forceinline__ void finish_rows_any(const Product& p, int64_t m0, int64_t n, int lane, float bias, float* v,
+                                                float4* buf) {
+    const int left = static_cast<int>(min(static_cast<int64_t>(32), p.N - n));
+    const int count = static_cast<int>(min(static_cast<int64_t>(32), p.M - m0));
+    const int64_t m = m0 + lane;
+    const bool on = lane < count;
+    if (p.bias != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, bias, j);
+    }
+    if (SLOPE) {
+        float z[32];
+        if (on) {
+            load_row32_any(p.pre, m, n, left, z);
+            slope_n<32>(v, z, p.act);
+        }
+    } else {
+        if (p.pre.p != nullptr) {
+            if (p.pre.dtype == FSDP_DTYPE_ACT8) {
+                if (on) p.pre.e[m * p.pre.eld + (n >> 5)] = static_cast<uint8_t>(store_row32<false>(p.pre, m, n, left, v));
+            } else {
+                store_rows_any(p.pre, m0, count, n + lane, p.N, v, buf, lane);
+            }
+        }
+        activate_n<32>(v, p.act);
+    }
+    if (p.add.p != nullptr && on) {
+        float e[32];
+        load_row32_any(p.add, m, n, left, e);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += e[j];
+    }
+    store_rows_any(p.out, m0, count, n + lane, p.N, v, buf, lane);
 }
 
 // The epilogue of 32 columns of one row: everything a lane needs is in its own
@@ -151,8 +252,8 @@ __device__ __forceinline__ void finish_row(const Product& p, int64_t m, int64_t 
 }
 
 // The epilogue where a lane holds one column n of R consecutive rows from m
-// (`count` of them inside the matrix): matrices whose rows start anywhere, and
-// tiles whose rows are C's columns.  n - lane is a multiple of 32.
+// (`count` of them inside the matrix): tiles whose rows are C's columns, and the
+// products of few rows.  n - lane is a multiple of 32.
 template <int R, bool SLOPE>
 __device__ __forceinline__ void finish_column(const Product& p, int64_t m, int count, int64_t n, float bias, float* v, int lane) {
     const bool in = n < p.N;

@@ -259,31 +259,22 @@ __device__ __forceinline__ Unit unit_of(const Plan& p, uint32_t u) {
 }
 
 // One 32 x 32 chunk whose rows lie one to a lane: v[j] is tile row `row0 +
-// lane`, tile column `col0 + j`.  buf: 4 KiB of shared memory for rows that are
-// not aligned, in which 16-byte slot s of row r lies at s ^ (r & 7) (no bank
-// conflicts writing, and none reading along a row).
+// lane`, tile column `col0 + j`; `bias` that of tile column `col0 + lane`.  buf:
+// 4 KiB of shared memory for rows that are not aligned.
 template <int VEC, bool SLOPE>
 __device__ __forceinline__ void finish_chunk(const Product& p, const Plan& pl, int64_t row0, int64_t col0, float* v,
                                              float4* buf, int lane, float bias, uint32_t* byte) {
     if constexpr (VEC > 0) {
         if (col0 < p.N) finish_row<VEC == 2, SLOPE>(p, row0 + lane, col0, row0 + lane < p.M, bias, v, byte);
+    } else if (!pl.swapped) {
+        if (col0 < p.N && row0 < p.M) finish_rows_any<SLOPE>(p, row0, col0, lane, bias, v, buf);
     } else {
-        // one column of C to a lane
-        const int64_t m0 = pl.swapped ? col0 : row0, n = (pl.swapped ? row0 : col0) + lane;
-        const int count = static_cast<int>(min(static_cast<int64_t>(32), p.M - m0));
-        if (count <= 0 || n - lane >= p.N) return;   // the same for the whole warp
+        // the lane's tile row is a column of C
+        const int64_t n = row0 + lane;
+        const int count = static_cast<int>(min(static_cast<int64_t>(32), p.M - col0));
+        if (count <= 0 || row0 >= p.N) return;   // the same for the whole warp
         bias = p.bias != nullptr && n < p.N ? load1(p.bias, p.bias_dtype, n) : 0.0f;
-        if (!pl.swapped) {   // swapped, the lane's tile row is that column already
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-                buf[lane * 8 + (s ^ (lane & 7))] = make_float4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]);
-            __syncwarp();
-            const float* f = reinterpret_cast<const float*>(buf);
-#pragma unroll
-            for (int r = 0; r < 32; ++r) v[r] = f[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)];
-            __syncwarp();
-        }
-        finish_column<32, SLOPE>(p, m0, count, n, bias, v, lane);
+        finish_column<32, SLOPE>(p, col0, count, n, bias, v, lane);
     }
 }
 
@@ -472,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int64_t row0 = static_cast<int64_t>(un.tm) * 256 + rank * 128 + quad * 32;
             const int64_t col0 = static_cast<int64_t>(un.tn) * pl.bn;
             float bias[4] = {};   // of the warp's chunks, read before their sums are there
-            if (VEC > 0 && p.bias != nullptr) {
+            if (p.bias != nullptr && !pl.swapped) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int64_t n = col0 + (c0 + i) * 32 + lane;
@@ -679,7 +670,7 @@ __global__ void __launch_bounds__(128) finish_kernel(const __grid_constant__ Pro
     }
     const int64_t col0 = static_cast<int64_t>(tn) * pl.bn + c * 32;
     const int64_t row0 = static_cast<int64_t>(tm) * 256 + rank * 128 + quad * 32;
-    const float bias = VEC > 0 && p.bias != nullptr && col0 + lane < p.N ? load1(p.bias, p.bias_dtype, col0 + lane) : 0.0f;
+    const float bias = p.bias != nullptr && !pl.swapped && col0 + lane < p.N ? load1(p.bias, p.bias_dtype, col0 + lane) : 0.0f;
     uint32_t byte = 0;
     finish_chunk<VEC, SLOPE>(p, pl, row0, col0, v, buf[0], lane, bias, &byte);
     if (VEC > 0 && !SLOPE && p.pre.dtype == FSDP_DTYPE_ACT8 && p.pre.p != nullptr && row0 + lane < p.M && col0 < p.N)
