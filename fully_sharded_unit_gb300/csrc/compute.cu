@@ -40,6 +40,7 @@ using fsdp::Mat;
 int fail(int code, const std::string& why) { return fsdp::record_error(code, why); }
 
 int cuda_fail(cudaError_t e, const char* what) {
+    cudaGetLastError();   // reported here, not to whoever asks next
     return fail(FSDP_E_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 

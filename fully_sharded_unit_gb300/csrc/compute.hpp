@@ -5,6 +5,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 namespace fsdp {
@@ -36,6 +37,22 @@ cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size
     cfg.attrs = &early;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
+// The value of f() for the current device, computed once for each device (a
+// kernel's attributes belong to a device).  Every call site's f is a type of its
+// own; two threads that come first together both compute the same value.
+template <typename F>
+int once_per_device(F f) {
+    static std::atomic<int> values[64] = {};   // value + 1
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= 64) return f();
+    int v = values[device].load(std::memory_order_acquire);
+    if (v == 0) {
+        v = f() + 1;
+        values[device].store(v, std::memory_order_release);
+    }
+    return v - 1;
 }
 
 constexpr int kGroup = 32;   // elements that share an exponent in an ACT8 matrix

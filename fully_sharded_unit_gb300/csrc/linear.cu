@@ -820,18 +820,16 @@ const ProductKernel kProductKernels[2][3] = {
 }  // namespace
 
 int product_clusters(int sms) {
-    static std::once_flag once;
-    static int most = 0;
-    std::call_once(once, [] {
+    const int most = once_per_device([] {
         for (const ProductKernel* row : kProductKernels)
             for (int i = 0; i < 3; ++i)
-                if (cudaFuncSetAttribute(row[i], cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) return;
+                if (cudaFuncSetAttribute(row[i], cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) return 0;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(2 * kMaxClusters);
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = kSmemBytes;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kProductKernels[0][0], &cfg) == cudaSuccess) most = n;
+        return cudaOccupancyMaxActiveClusters(&n, kProductKernels[0][0], &cfg) == cudaSuccess ? n : 0;
     });
     return std::min(std::min(most, sms / 2), kMaxClusters);
 }

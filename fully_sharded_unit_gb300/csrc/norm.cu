@@ -803,12 +803,14 @@ int64_t backward_blocks(int64_t rows, int64_t cols, bool vec, int sms) {
     return walkers(p, rows, sms);
 }
 
-// Launches with `bytes` of dynamic shared memory, allowed once per kernel.
+// Launches with `bytes` of dynamic shared memory.
 constexpr int kSharedMost = 222 * 1024;
 template <auto kernel, typename... Args>
 cudaError_t launch_shared(unsigned blocks, int threads, int bytes, cudaStream_t st, const Args&... args) {
-    static const cudaError_t allowed = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedMost);
-    if (allowed != cudaSuccess) return allowed;
+    const int allowed = once_per_device([] {
+        return static_cast<int>(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedMost));
+    });
+    if (allowed != cudaSuccess) return static_cast<cudaError_t>(allowed);
     return launch_early(kernel, dim3(blocks), threads, static_cast<size_t>(bytes), st, args...);
 }
 
