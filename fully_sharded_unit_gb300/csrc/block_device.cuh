@@ -359,15 +359,6 @@ __device__ __forceinline__ float gelu_erf_slope(float z) {
     return fmaf(z * 0.39894228040143268f, __expf(-0.5f * z * z), 0.5f * (1.0f + erff(z * 0.70710678118654752f)));
 }
 
-__device__ __forceinline__ float activate(float z, int act) {
-    switch (act) {
-        case FSDP_ACTIVATION_RELU: return max_nan(z, 0.0f);
-        case FSDP_ACTIVATION_GELU_TANH: return gelu_tanh(z);
-        case FSDP_ACTIVATION_GELU_ERF: return gelu_erf(z);
-        default: return z;
-    }
-}
-
 // N elements in place; the kind is looked at once.
 template <int N>
 __device__ __forceinline__ void activate_n(float* v, int act) {
@@ -385,15 +376,6 @@ __device__ __forceinline__ void activate_n(float* v, int act) {
     } else if (act == FSDP_ACTIVATION_RELU) {
 #pragma unroll
         for (int j = 0; j < N; ++j) v[j] = max_nan(v[j], 0.0f);
-    }
-}
-
-__device__ __forceinline__ float act_slope(float z, int act) {
-    switch (act) {
-        case FSDP_ACTIVATION_RELU: return z > 0.0f ? 1.0f : 0.0f;
-        case FSDP_ACTIVATION_GELU_TANH: return gelu_tanh_slope(z);
-        case FSDP_ACTIVATION_GELU_ERF: return gelu_erf_slope(z);
-        default: return 1.0f;
     }
 }
 

@@ -84,9 +84,8 @@ struct NormBackward {
     const float *mean, *rstd;
     void *dgamma, *dbeta;
     int grad_dtype, accumulate;
-    float* partials;            // workspace: norm_partials() x 2 x cols floats
+    float* partials;            // workspace: a row of 2 x cols floats for each of up to min(rows, sms) blocks
 };
-int64_t norm_partials(int64_t rows, int64_t cols, int sms);
 cudaError_t launch_norm_backward(const NormBackward& a, int sms, cudaStream_t st);
 
 // out[c] (+)= sum over p of partials[p*stride + c], in the order of p.
@@ -118,7 +117,6 @@ constexpr int kMaxClusters = 76;                                  // pairs of SM
 constexpr int64_t kPartialBytes = int64_t(kMaxClusters) * 256 * 256 * 4;
 struct ProductRoom {
     float* partials;            // kPartialBytes: sums of tiles that several clusters share
-    uint32_t* counters;         // kCounterBytes, zero between launches
     char* copies;               // product_copy_bytes() of both operands
     int32_t* status;            // FSDP_KSTATUS_* bits
     unsigned long long wait_ns; // bound of every wait

@@ -763,25 +763,25 @@ cudaError_t make_map(CUtensorMap* map, const Mat& m, int64_t rows, int64_t cols,
 // tile's epilogue 13 a column.
 //
 // Long sums: the tensor cores cut an accumulator off to 24 bits with every 16
-// products (measured: a relative error of 1.1e-9 k for random signs, at k =
-// 16384 already 1.8e-5), which an F32 result would show.  So where one is
-// asked for and k is above kLongSum stages, the accumulator is emptied every
-// kSlice stages (k = 4096) and the slices are added in fp32, rounded to nearest;
-// the running sums need tensor memory, which leaves tiles of at most 160 columns.
-constexpr int kLongSum = 96, kSlice = 64;
+// products (measured: a relative error of 1.1e-9 k for random signs, 4.4e-6 at
+// k = 4096), which an F32 result would show.  So where one is asked for and a
+// cluster's k is above kLongSum stages (2048), the accumulator is emptied every
+// kSlice stages (1024) and the slices are added in fp32, rounded to nearest: an
+// error of 1.0e-6 at any k.  The running sums need tensor memory, which leaves
+// tiles of at most 160 columns: 8192 x 4608 x 4608 at 1615 to 1635 TFLOP/s
+// against 1700 uncut, 1640 to 1670 with slices of 2048, 1570 with slices of 512.
+// At k up to 2048 the narrower tiles cost more than the bits are worth (1031 x
+// 5121 x 1283 in two parts: 42.0 us against 38.3, for 7e-7 against 1.0e-6).
+constexpr int kLongSum = 32, kSlice = 16;
 
 Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, bool exact_sums, int clusters) {
     Plan best{};
     double least = 0;
-    const bool sliced = exact_sums && k > static_cast<int64_t>(kLongSum) * kDepth;
-    const int widest = sliced ? 160 : 256;
-    for (int bn = widest; bn >= 32; bn -= 32) {
-        if (bn < widest && bn >= 2 * cols && bn > 32) continue;
+    for (int bn = 256; bn >= 32; bn -= 32) {
+        if (bn < 256 && bn >= 2 * cols && bn > 32) continue;
         Plan p{};
         p.ks = static_cast<int>((k + kDepth - 1) / kDepth);
         p.bn = bn;
-        p.slice = sliced ? kSlice : 0x40000000;
-        p.buffer = sliced ? bn : 256;
         p.tiles_m = static_cast<int>((rows + 255) / 256);
         p.tiles_n = static_cast<int>((cols + bn - 1) / bn);
         const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
@@ -796,6 +796,11 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, bool ex
             if (share == 1 && p.parts == 1) continue;
             p.whole = static_cast<uint32_t>(p.parts > 1 ? tiles - left : tiles);
             p.units = static_cast<uint32_t>(p.whole + (tiles - p.whole) * p.parts);
+            const int deepest = p.whole > 0 ? p.ks : (p.ks + p.parts - 1) / p.parts;
+            const bool sliced = exact_sums && deepest > kLongSum;
+            if (sliced && bn > 160) continue;
+            p.slice = sliced ? kSlice : 0x40000000;
+            p.buffer = sliced ? bn : 256;
             const double rounds = static_cast<double>((p.whole + clusters - 1) / clusters);
             double t = rounds * (std::max(steps * stage, 400.0 + 13.0 * bn) + 300.0) + 13.0 * bn;
             if (p.parts > 1) t += (p.ks + p.parts - 1) / p.parts * stage + 9000.0 + 60.0 * p.parts;

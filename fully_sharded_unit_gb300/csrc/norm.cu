@@ -403,8 +403,10 @@ __global__ void __launch_bounds__(THREADS) norm_forward_ring_kernel(const __grid
     }
 }
 
-// KEPT: x is an ACT8 checkpoint.
-template <int NV, int GT, int THREADS, bool FAST, bool KEPT>
+// KEPT: x is an ACT8 checkpoint.  AGAIN: a row's x-hat and dy gamma are computed
+// from shared memory once more for dx, not held in registers, which leaves those
+// to more columns' sums.
+template <int NV, int GT, int THREADS, bool FAST, bool KEPT, bool AGAIN>
 __global__ void __launch_bounds__(THREADS) norm_backward_ring_kernel(const __grid_constant__ NormBackward a, int places) {
     extern __shared__ __align__(16) uint8_t ring_bytes[];
     __shared__ __align__(16) float2 red[2][32];
@@ -419,10 +421,9 @@ __global__ void __launch_bounds__(THREADS) norm_backward_ring_kernel(const __gri
     at += places * dys.place;
     const Rows<NV, GT, FAST, KEPT> xs(a.x, at, g, G, t);
     at += places * xs.place;
-    const Rows<NV, GT, FAST> adds(a.add, at, g, G, t);
+    const Rows<NV, GT, FAST> adds(a.add, at, g, G, t);   // read only if there is one
     const Out<GT, FAST> dxs(a.dx, t);
     const bool added = a.add.p != nullptr;
-    constexpr bool kept = KEPT;
     if (g == 0) {
         gammas.copy(0, 0, end);
         copies_end();
@@ -439,14 +440,15 @@ __global__ void __launch_bounds__(THREADS) norm_backward_ring_kernel(const __gri
         }
         copies_end();
     };
-    // the row's scalars are a row ahead, in registers
+    // the row's scalars are a row ahead, in registers (copied into the ring, a
+    // word each, they cost more than they hid: 64 us against 51 at 4096 x 8192)
     float mean = 0.0f, rstd = 0.0f;
     uint32_t byte[NV];
     const auto scalars = [&](int64_t row) {
         if (row < a.rows) {
             mean = a.mean[row];
             rstd = a.rstd[row];
-            if (kept) {
+            if (KEPT) {
                 const uint8_t* e = a.x.e + row * a.x.eld + (t >> 2);
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
@@ -465,33 +467,45 @@ __global__ void __launch_bounds__(THREADS) norm_backward_ring_kernel(const __gri
     for (int64_t row = first; row < a.rows; row += stride) {
         issue(row + (places - 1) * stride, place == 0 ? places - 1 : place - 1);
         copies_wait(places - 1);
-        f32x2 xh[NV][4], gr[NV][4];
+        constexpr int kHeld = AGAIN ? 1 : NV;
+        f32x2 xh[kHeld][4], gr[kHeld][4];
         f32x2 s1 = pair(0.0f, 0.0f), s2 = pair(0.0f, 0.0f);
         const float r = rstd;
         const f32x2 shift = pair(-mean * r, -mean * r);
+        uint32_t now[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) now[k] = KEPT ? byte[k] : 0u;
+        // x rstd - mean rstd, and dy gamma; a checkpoint's step (a power of two) goes into the factor
+        const auto expand = [&](int k, f32x2* x, f32x2* dy, f32x2* g4) {
+            f32x2 gm[4];
+            gammas.read(0, k, gm);
+            dys.read(place, k, dy);
+            float scale = r;
+            if (KEPT) {
+                xs.read_ints(place, k, x);
+                scale = r * act8_step(now[k]);
+            } else {
+                xs.read(place, k, x);
+            }
+            const f32x2 scale2 = pair(scale, scale);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[j] = fma2(x[j], scale2, shift);
+                g4[j] = mul2(dy[j], gm[j]);
+            }
+        };
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (k + 1 < NV || end) {
-                f32x2 gm[4], dy[4];
-                gammas.read(0, k, gm);
-                dys.read(place, k, dy);
-                // x rstd - mean rstd; a checkpoint's step (a power of two) goes into the factor
-                float scale = r;
-                if (kept) {
-                    xs.read_ints(place, k, xh[k]);
-                    scale = r * act8_step(byte[k]);
-                } else {
-                    xs.read(place, k, xh[k]);
-                }
-                const f32x2 scale2 = pair(scale, scale);
+                const int h = AGAIN ? 0 : k;
+                f32x2 dy[4];
+                expand(k, xh[h], dy, gr[h]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    xh[k][j] = fma2(xh[k][j], scale2, shift);
                     db[k][j] = add2(db[k][j], dy[j]);
-                    dg[k][j] = fma2(dy[j], xh[k][j], dg[k][j]);
-                    gr[k][j] = mul2(dy[j], gm[j]);
-                    s1 = add2(s1, gr[k][j]);
-                    s2 = fma2(gr[k][j], xh[k][j], s2);
+                    dg[k][j] = fma2(dy[j], xh[h][j], dg[k][j]);
+                    s1 = add2(s1, gr[h][j]);
+                    s2 = fma2(gr[h][j], xh[h][j], s2);
                 }
             }
         }
@@ -505,9 +519,11 @@ __global__ void __launch_bounds__(THREADS) norm_backward_ring_kernel(const __gri
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (k + 1 < NV || end) {
+                const int h = AGAIN ? 0 : k;
                 f32x2 o[4];
+                if (AGAIN) expand(k, xh[h], o, gr[h]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[j] = fma2(r2, gr[k][j], fma2(xh[k][j], m2, m1));
+                for (int j = 0; j < 4; ++j) o[j] = fma2(r2, gr[h][j], fma2(xh[h][j], m2, m1));
                 if (added) {
                     f32x2 e[4];
                     adds.read(place, k, e);
@@ -742,14 +758,19 @@ cudaError_t sum_partials(const float* partials, int64_t count, int64_t stride, i
 
 int round32(int64_t n) { return static_cast<int>((n + 31) / 32 * 32); }
 
-template <int V, int NV>
+// A row to a block, or to a warp (SHORT) where its lanes hold it whole.
+template <int V, int NV, bool SHORT>
 cudaError_t run_forward(const NormForward& a, int64_t chunks, cudaStream_t st) {
     const int64_t cap = int64_t(1) << 30;
-    if (chunks <= 32 * NV)
-        return launch_early(norm_forward_kernel<V, NV, true>, dim3(static_cast<unsigned>(std::min((a.rows + 3) / 4, cap))), 128, 0, st, a);
+    if constexpr (SHORT) {
+        if (chunks <= 32 * NV)
+            return launch_early(norm_forward_kernel<V, NV, true>, dim3(static_cast<unsigned>(std::min((a.rows + 3) / 4, cap))), 128, 0, st, a);
+    }
     return launch_early(norm_forward_kernel<V, NV, false>, dim3(static_cast<unsigned>(std::min(a.rows, cap))),
                         round32((chunks + NV - 1) / NV), 0, st, a);
 }
+
+constexpr int kSharedMost = 222 * 1024;   // dynamic shared memory of a block
 
 // How a row is split: threads to it, chunks (or columns) to a thread, rows to a
 // block.
@@ -774,7 +795,7 @@ Split split_row(int64_t rows, int64_t chunks, const int (*options)[2], int count
     return p;
 }
 constexpr int kForward[][2] = {{1, 32}, {2, 32}, {3, 32}, {4, 32}, {5, 32}, {6, 32}, {2, 128}, {3, 128}, {4, 128}, {5, 128}, {6, 128}, {4, 256}, {5, 256}, {6, 256}, {4, 512}};
-constexpr int kBackward[][2] = {{1, 32}, {2, 32}, {3, 32}, {4, 32}, {5, 32}, {2, 128}, {3, 128}, {1, 512}, {2, 512}, {3, 512}};
+constexpr int kBackward[][2] = {{1, 32}, {2, 32}, {3, 32}, {4, 32}, {5, 32}, {2, 128}, {3, 128}, {4, 128}, {5, 128}, {3, 256}, {4, 256}, {3, 512}, {4, 512}, {5, 512}};
 
 int64_t walkers(const Split& p, int64_t rows, int64_t most) {
     return std::max<int64_t>(1, std::min((rows + p.groups - 1) / p.groups, most));
@@ -782,10 +803,27 @@ int64_t walkers(const Split& p, int64_t rows, int64_t most) {
 
 constexpr int kWideSlices = 64;   // row slices of the column sums where rows are too long
 
-Split backward_split(int64_t rows, int64_t cols, bool vec) {
+bool backward_aligned(const NormBackward& a) {
+    return rows_aligned(a.dy) && rows_aligned(a.x) && rows_aligned(a.dx) && (a.add.p == nullptr || rows_aligned(a.add)) &&
+           a.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(a.gamma) & 15u) == 0;
+}
+
+// Bytes of eight columns in the ring.
+int backward_chunk(const NormBackward& a) {
+    return chunk_bytes(a.dy.dtype) + chunk_bytes(a.x.dtype) + (a.add.p != nullptr ? chunk_bytes(a.add.dtype) : 0);
+}
+
+Split backward_split(const NormBackward& a, bool vec) {
+    const int64_t rows = a.rows, cols = a.cols;
     if (vec) {
-        Split p = split_row(rows, cols / 8, kBackward, 10, 512);
-        if (p.NV > 3) p.groups = std::min(p.groups, 8);   // 256 threads, which may have twice the registers
+        Split p = split_row(rows, cols / 8, kBackward, 14, 512);
+        if (p.gt == 32 && p.NV > 3) p.groups = std::min(p.groups, 8);   // 256 threads, which may have twice the registers
+        if (p.NV != 0) {
+            // two places in the ring for every group, or one for one
+            const int row = p.NV * p.gt * backward_chunk(a), room = kSharedMost - p.NV * p.gt * chunk_bytes(a.param_dtype);
+            if (row > room) p.NV = 0;
+            else p.groups = std::max(1, std::min(p.groups, room / (2 * row)));
+        }
         return p;
     }
     Split p;
@@ -797,14 +835,12 @@ Split backward_split(int64_t rows, int64_t cols, bool vec) {
     return p;
 }
 
-int64_t backward_blocks(int64_t rows, int64_t cols, bool vec, int sms) {
-    const Split p = backward_split(rows, cols, vec);
+int64_t backward_blocks(const Split& p, int64_t rows, int sms) {
     if (p.NV == 0) return std::max<int64_t>(1, std::min<int64_t>(rows, kWideSlices));
     return walkers(p, rows, sms);
 }
 
 // Launches with `bytes` of dynamic shared memory.
-constexpr int kSharedMost = 222 * 1024;
 template <auto kernel, typename... Args>
 cudaError_t launch_shared(unsigned blocks, int threads, int bytes, cudaStream_t st, const Args&... args) {
     const int allowed = once_per_device([] {
@@ -839,26 +875,20 @@ cudaError_t launch_norm_forward(const NormForward& a, int sms, cudaStream_t st) 
 #undef RING
         }
         const int64_t chunks = a.cols / 8;
-        if (chunks <= 512) return run_forward<8, 1>(a, chunks, st);
-        if (chunks <= 4096) return run_forward<8, 4>(a, chunks, st);
+        if (chunks <= 512) return run_forward<8, 1, true>(a, chunks, st);
+        if (chunks <= 4096) return run_forward<8, 4, false>(a, chunks, st);
     } else {
-        if (a.cols <= 4096) return run_forward<1, 8>(a, a.cols, st);
-        if (a.cols <= 16384) return run_forward<1, 16>(a, a.cols, st);
+        if (a.cols <= 4096) return run_forward<1, 8, true>(a, a.cols, st);
+        if (a.cols <= 16384) return run_forward<1, 16, false>(a, a.cols, st);
     }
     return launch_early(norm_forward_wide_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t(1) << 30))), 1024, 0, st, a);
 }
 
-int64_t norm_partials(int64_t rows, int64_t cols, int sms) {
-    return std::max(cols % 8 == 0 ? backward_blocks(rows, cols, true, sms) : 0, backward_blocks(rows, cols, false, sms));
-}
-
 cudaError_t launch_norm_backward(const NormBackward& a, int sms, cudaStream_t st) {
-    const bool vec = rows_aligned(a.dy) && rows_aligned(a.x) && rows_aligned(a.dx) &&
-                     (a.add.p == nullptr || rows_aligned(a.add)) && a.cols % 8 == 0 &&
-                     (reinterpret_cast<uintptr_t>(a.gamma) & 15u) == 0;
-    const Split p = backward_split(a.rows, a.cols, vec);
+    const bool vec = backward_aligned(a);
+    const Split p = backward_split(a, vec);
     cudaError_t e = cudaSuccess;
-    int64_t count = backward_blocks(a.rows, a.cols, vec, sms);
+    int64_t count = backward_blocks(p, a.rows, sms);
     const unsigned blocks = static_cast<unsigned>(count);
     if (a.rows == 0) {
         count = 0;
@@ -868,8 +898,7 @@ cudaError_t launch_norm_backward(const NormBackward& a, int sms, cudaStream_t st
         const dim3 grid(static_cast<unsigned>((a.cols + 255) / 256), blocks);
         e = launch_early(norm_backward_wide_sums_kernel, grid, 256, 0, st, a);
     } else if (vec) {
-        const int row_bytes = p.threads() * p.NV *
-                              (chunk_bytes(a.dy.dtype) + chunk_bytes(a.x.dtype) + (a.add.p != nullptr ? chunk_bytes(a.add.dtype) : 0));
+        const int row_bytes = p.threads() * p.NV * backward_chunk(a);
         const int keep = p.NV * p.gt * chunk_bytes(a.param_dtype);
         const int places = std::max(1, std::min(kRing, (kSharedMost - keep) / row_bytes));
         const int comb = p.groups * 16 * (p.NV * p.gt + 4) * 4;
@@ -878,18 +907,20 @@ cudaError_t launch_norm_backward(const NormBackward& a, int sms, cudaStream_t st
         const bool fast = a.dy.dtype == FSDP_DTYPE_BF16 && a.dx.dtype == FSDP_DTYPE_BF16 && a.param_dtype == FSDP_DTYPE_BF16 &&
                           a.x.dtype != FSDP_DTYPE_F32 && (a.add.p == nullptr || a.add.dtype == FSDP_DTYPE_BF16);
         e = cudaErrorInvalidConfiguration;
-#define RING_(nv, gt_, f, k)                                                                                      \
-    if (fast == f && kept == k) e = launch_shared<norm_backward_ring_kernel<nv, gt_, (nv <= 3 ? 512 : 256), f, k>>( \
-        blocks, p.threads(), bytes, st, a, places)
-#define RING(nv, gt_)                    \
-    if (p.NV == nv && p.gt == gt_) {     \
-        RING_(nv, gt_, true, true);      \
-        RING_(nv, gt_, true, false);     \
-        RING_(nv, gt_, false, true);     \
-        RING_(nv, gt_, false, false);    \
+#define RING_(nv, gt_, most, again, f, k)                                                                 \
+    if (fast == f && kept == k)                                                                           \
+        e = launch_shared<norm_backward_ring_kernel<nv, gt_, most, f, k, again>>(blocks, p.threads(), bytes, st, a, places)
+#define RING(nv, gt_, most, again)                    \
+    if (p.NV == nv && p.gt == gt_) {                  \
+        RING_(nv, gt_, most, again, true, true);     \
+        RING_(nv, gt_, most, again, true, false);     \
+        RING_(nv, gt_, most, again, false, true);     \
+        RING_(nv, gt_, most, again, false, false);     \
     }
-        RING(1, 32) RING(2, 32) RING(3, 32) RING(4, 32) RING(5, 32)
-        RING(2, 128) RING(3, 128) RING(1, 512) RING(2, 512) RING(3, 512)
+        RING(1, 32, 512, false) RING(2, 32, 512, false) RING(3, 32, 512, true) RING(4, 32, 256, false) RING(5, 32, 256, false)
+        RING(2, 128, 512, false) RING(3, 128, 512, true) RING(4, 128, 512, true) RING(5, 128, 512, true)
+        RING(3, 256, 512, true) RING(4, 256, 512, true)
+        RING(3, 512, 512, false) RING(4, 512, 512, true) RING(5, 512, 512, true)
 #undef RING
 #undef RING_
     } else {

@@ -494,7 +494,8 @@ def test_a_copy_that_never_arrives_is_reported():
     c.close()
 
 
-@pytest.mark.parametrize("rows,cols", [(1300, 520), (700, 4104), (1400, 1280)])
+@pytest.mark.parametrize("rows,cols", [(1300, 520), (700, 4104), (1400, 1280), (5000, 768), (1300, 2880), (1300, 4096), (1000, 5000),
+                                       (700, 6000), (700, 8192), (320, 16384), (320, 20480), (160, 20488)])
 def test_layer_norm_many_rows(handle, rows, cols):
     """Enough rows for a block to walk several of them."""
     x = _normal(cols, (rows, cols), 2.0, BF, 0.7)
