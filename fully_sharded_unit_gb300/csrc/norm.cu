@@ -157,6 +157,9 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void copy4(uint32_t dst, uintptr_t src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // All but the newest `pending` groups have landed.
@@ -405,7 +408,13 @@ __global__ void __launch_bounds__(THREADS) norm_forward_ring_kernel(const __grid
 
 // KEPT: x is an ACT8 checkpoint.  AGAIN: a row's x-hat and dy gamma are computed
 // from shared memory once more for dx, not held in registers, which leaves those
-// to more columns' sums.
+// to more columns' sums.  What bounds it below 4096 columns or so is the latency
+// of a row, from its sums to its last store, and the rows in flight on an SM:
+// the blocks hold as many groups as the registers and the ring allow.  Measured,
+// with an added branch, from BF16 and from 8 bits (bytes over time): 4096 x 12288
+// 74 us (5.4 TB/s) and 70 (5.0); 8192 x 6144 75 (5.3) and 74 (4.7); 8192 x 4096
+// 58 (4.6) and 54 (4.4), by one group of 512 threads a block 94 and 78; 8192 x
+// 1280 27 (3.1) and 27 (2.7).
 template <int NV, int GT, int THREADS, bool FAST, bool KEPT, bool AGAIN>
 __global__ void __launch_bounds__(THREADS) norm_backward_ring_kernel(const __grid_constant__ NormBackward a, int places) {
     extern __shared__ __align__(16) uint8_t ring_bytes[];
@@ -432,32 +441,32 @@ __global__ void __launch_bounds__(THREADS) norm_backward_ring_kernel(const __gri
     __syncthreads();
     const int64_t stride = static_cast<int64_t>(gridDim.x) * G, first = static_cast<int64_t>(blockIdx.x) * G + g;
     const float inv_n = 1.0f / static_cast<float>(a.cols);
+    // What a warp needs of a row besides comes with it in one copy instruction, 32
+    // words to a warp and place: the aligned words that hold the exponents of its
+    // chunks (8 bytes of each chunk's, in three words), mean and rstd.  (A row
+    // ahead in registers, the exponents came too late: 96 us against 70 at 4096 x
+    // 12288; a copy instruction for each of a thread's, 90.)
+    at += added ? places * adds.place : 0;
+    const int lane = threadIdx.x & 31;
+    uint32_t* const words = reinterpret_cast<uint32_t*>(at) + (threadIdx.x & ~31);
+    const uintptr_t exps = reinterpret_cast<uintptr_t>(a.x.e) + ((t & ~31) >> 2);   // of the warp's first chunk
     const auto issue = [&](int64_t row, int s) {
         if (row < a.rows) {
+            bool on = lane >= 30;
+            uintptr_t from = reinterpret_cast<uintptr_t>((lane == 30 ? a.mean : a.rstd) + row);
+            if (KEPT && lane < 3 * NV) {
+                const uintptr_t start = row * a.x.eld;
+                from = ((exps + start + lane / 3 * (GT / 4)) & ~uintptr_t(3)) + lane % 3 * 4;
+                on = from < reinterpret_cast<uintptr_t>(a.x.e) + start + a.x.eld;
+            }
+            if (on) copy4(shared_at(words + s * blockDim.x + lane), from);
             dys.copy(row, s, end);
             xs.copy(row, s, end);
             if (added) adds.copy(row, s, end);
         }
         copies_end();
     };
-    // the row's scalars are a row ahead, in registers (copied into the ring, a
-    // word each, they cost more than they hid: 64 us against 51 at 4096 x 8192)
-    float mean = 0.0f, rstd = 0.0f;
-    uint32_t byte[NV];
-    const auto scalars = [&](int64_t row) {
-        if (row < a.rows) {
-            mean = a.mean[row];
-            rstd = a.rstd[row];
-            if (KEPT) {
-                const uint8_t* e = a.x.e + row * a.x.eld + (t >> 2);
-#pragma unroll
-                for (int k = 0; k < NV; ++k)
-                    if (k + 1 < NV || end) byte[k] = e[k * (GT / 4)];
-            }
-        }
-    };
     for (int s = 0; s + 1 < places; ++s) issue(first + s * stride, s);
-    scalars(first);
     f32x2 dg[NV][4], db[NV][4];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
@@ -470,11 +479,11 @@ __global__ void __launch_bounds__(THREADS) norm_backward_ring_kernel(const __gri
         constexpr int kHeld = AGAIN ? 1 : NV;
         f32x2 xh[kHeld][4], gr[kHeld][4];
         f32x2 s1 = pair(0.0f, 0.0f), s2 = pair(0.0f, 0.0f);
-        const float r = rstd;
+        __syncwarp();   // the words are other lanes' copies
+        const uint32_t* w = words + place * blockDim.x;
+        const float mean = __uint_as_float(w[30]), r = __uint_as_float(w[31]);
         const f32x2 shift = pair(-mean * r, -mean * r);
-        uint32_t now[NV];
-#pragma unroll
-        for (int k = 0; k < NV; ++k) now[k] = KEPT ? byte[k] : 0u;
+        const uint8_t* byte = reinterpret_cast<const uint8_t*>(w) + ((exps + row * a.x.eld) & 3u) + (lane >> 2);
         // x rstd - mean rstd, and dy gamma; a checkpoint's step (a power of two) goes into the factor
         const auto expand = [&](int k, f32x2* x, f32x2* dy, f32x2* g4) {
             f32x2 gm[4];
@@ -483,7 +492,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_ring_kernel(const __gri
             float scale = r;
             if (KEPT) {
                 xs.read_ints(place, k, x);
-                scale = r * act8_step(now[k]);
+                scale = r * act8_step(byte[k * 12]);
             } else {
                 xs.read(place, k, x);
             }
@@ -509,7 +518,6 @@ __global__ void __launch_bounds__(THREADS) norm_backward_ring_kernel(const __gri
                 }
             }
         }
-        scalars(row + stride);
         const float2 sum = group_sum2<GT / 32>(both(s1), both(s2), red[flip], g);
         flip ^= 1;
         // dx = dy gamma rstd - xh c2 - c1 [+ add]
@@ -534,6 +542,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_ring_kernel(const __gri
             }
         }
         place = place + 1 == places ? 0 : place + 1;
+        __syncwarp();   // a place's words are read before they are copied anew
     }
     // the groups' column sums meet in shared memory: element j of chunk i at
     // j * kSlots + i (no bank conflicts writing, nor reading the columns in order)
@@ -795,7 +804,7 @@ Split split_row(int64_t rows, int64_t chunks, const int (*options)[2], int count
     return p;
 }
 constexpr int kForward[][2] = {{1, 32}, {2, 32}, {3, 32}, {4, 32}, {5, 32}, {6, 32}, {2, 128}, {3, 128}, {4, 128}, {5, 128}, {6, 128}, {4, 256}, {5, 256}, {6, 256}, {4, 512}};
-constexpr int kBackward[][2] = {{1, 32}, {2, 32}, {3, 32}, {4, 32}, {5, 32}, {2, 128}, {3, 128}, {4, 128}, {5, 128}, {3, 256}, {4, 256}, {3, 512}, {4, 512}, {5, 512}};
+constexpr int kBackward[][2] = {{1, 32}, {2, 32}, {3, 32}, {4, 32}, {5, 32}, {2, 128}, {3, 128}, {4, 128}, {3, 256}, {2, 512}, {3, 512}, {4, 512}, {5, 512}};
 
 int64_t walkers(const Split& p, int64_t rows, int64_t most) {
     return std::max<int64_t>(1, std::min((rows + p.groups - 1) / p.groups, most));
@@ -816,11 +825,11 @@ int backward_chunk(const NormBackward& a) {
 Split backward_split(const NormBackward& a, bool vec) {
     const int64_t rows = a.rows, cols = a.cols;
     if (vec) {
-        Split p = split_row(rows, cols / 8, kBackward, 14, 512);
+        Split p = split_row(rows, cols / 8, kBackward, 13, 512);
         if (p.gt == 32 && p.NV > 3) p.groups = std::min(p.groups, 8);   // 256 threads, which may have twice the registers
         if (p.NV != 0) {
             // two places in the ring for every group, or one for one
-            const int row = p.NV * p.gt * backward_chunk(a), room = kSharedMost - p.NV * p.gt * chunk_bytes(a.param_dtype);
+            const int row = p.NV * p.gt * backward_chunk(a) + p.gt * 4, room = kSharedMost - p.NV * p.gt * chunk_bytes(a.param_dtype);
             if (row > room) p.NV = 0;
             else p.groups = std::max(1, std::min(p.groups, room / (2 * row)));
         }
@@ -898,7 +907,7 @@ cudaError_t launch_norm_backward(const NormBackward& a, int sms, cudaStream_t st
         const dim3 grid(static_cast<unsigned>((a.cols + 255) / 256), blocks);
         e = launch_early(norm_backward_wide_sums_kernel, grid, 256, 0, st, a);
     } else if (vec) {
-        const int row_bytes = p.threads() * p.NV * backward_chunk(a);
+        const int row_bytes = p.threads() * (p.NV * backward_chunk(a) + 4);
         const int keep = p.NV * p.gt * chunk_bytes(a.param_dtype);
         const int places = std::max(1, std::min(kRing, (kSharedMost - keep) / row_bytes));
         const int comb = p.groups * 16 * (p.NV * p.gt + 4) * 4;
@@ -918,9 +927,8 @@ cudaError_t launch_norm_backward(const NormBackward& a, int sms, cudaStream_t st
         RING_(nv, gt_, most, again, false, false);     \
     }
         RING(1, 32, 512, false) RING(2, 32, 512, false) RING(3, 32, 512, true) RING(4, 32, 256, false) RING(5, 32, 256, false)
-        RING(2, 128, 512, false) RING(3, 128, 512, true) RING(4, 128, 512, true) RING(5, 128, 512, true)
-        RING(3, 256, 512, true) RING(4, 256, 512, true)
-        RING(3, 512, 512, false) RING(4, 512, 512, true) RING(5, 512, 512, true)
+        RING(2, 128, 512, false) RING(3, 128, 512, true) RING(4, 128, 512, true) RING(3, 256, 512, true)
+        RING(2, 512, 512, false) RING(3, 512, 512, false) RING(4, 512, 512, true) RING(5, 512, 512, true)
 #undef RING
 #undef RING_
     } else {
