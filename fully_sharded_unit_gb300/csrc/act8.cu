@@ -14,6 +14,8 @@ namespace {
 // magnitude needs no exchange between lanes, and loads, payload and exponents
 // are whole sectors.  The payload's rows and the exponents' are contiguous
 // (their strides are the format's), so a group's place in them is its index.
+// 8192 x 5120: pack 24.5 us (5.2 TB/s), unpack with GELU 28 (4.5; the special
+// functions take half of it); 4096 x 12288: unpack 27 (5.7).
 template <bool WIDE, bool PACK>
 __global__ void __launch_bounds__(256) act8_groups_kernel(int64_t cols, Mat q, int act, Mat x, int64_t count, uint32_t groups) {
     starts_early();
@@ -37,7 +39,8 @@ __global__ void __launch_bounds__(256) act8_groups_kernel(int64_t cols, Mat q, i
 }
 
 // Rows that start anywhere: a group to a warp, an element to a lane, U groups
-// in flight.
+// in flight.  Bound by loads and stores of two bytes a lane: pack of 4096 x 1281,
+// 27 us (an aligned 4096 x 1280 takes 6.4).
 template <bool PACK>
 __global__ void __launch_bounds__(256) act8_elements_kernel(int64_t cols, Mat q, int act, Mat x, int64_t count, uint32_t groups) {
     starts_early();

@@ -29,6 +29,17 @@ namespace {
 // Either operand may be contiguous along k or along its own rows (W is read
 // both ways, x and dy too): the copies take boxes of 64 elements along the
 // contiguous direction, and only the shared-memory descriptors differ.
+//
+// What bounds it: the tensor cores where k and the tiles are many (8192 x 8192 x
+// 8192 in BF16: 1980 TFLOP/s, the rate of the library's product there; for
+// seconds on end, the power limit: 1740), the SMs' ports from L2 where the
+// epilogue's traffic meets the copies (4096 x 1280 -> 5120: 32.5 us, 1650
+// TFLOP/s, plain; 40 with bias, GELU and an 8-bit checkpoint kept; 42.5 with a
+// residual; 46 for an input gradient with GELU's slope from a checkpoint), and
+// the latency of one tile where there are few (64 x 1280 -> 5120: 7.5 us).
+// Pairs of CTAs, since a pair halves B's copies; tiles as wide as tensor memory
+// holds twice, since a tile's copies for a product fall with its width; one
+// persistent pair to two SMs, so that an epilogue runs beside the next tile.
 
 constexpr int kStagesMost = 10;
 constexpr int kDepth = 64;                       // k per stage (3 stages of 128 were 4 % slower at 8192^3)
@@ -583,7 +594,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // Column sums of dy: V columns to a thread (8 from a 16-byte boundary, or 1),
 // 32 threads across and 8 slices of rows down to a block, which joins them and
-// leaves one row of sums.  Eight loads of a thread are in flight at a time.
+// leaves one row of sums, for sum_partials_kernel to add in order (atomics'
+// order would change results).  Bound by DRAM and, in short matrices, by the
+// latency of a thread's loads, of which eight are in flight: 2048 x 49152 in 43
+// us (4.7 TB/s), 4096 x 1280 in 6.
 template <int V>
 __global__ void __launch_bounds__(256) column_sum_kernel(int64_t rows, int64_t cols, Mat dy, float* partials) {
     __shared__ float part[8][32 * V + 1];
@@ -629,7 +643,7 @@ __global__ void __launch_bounds__(256) column_sum_kernel(int64_t rows, int64_t c
 // one 32 x 32 chunk: each of its warps adds up a quarter of the parts, in their
 // order, and the first warp adds the four.  (Done by the last cluster to reach
 // a tile instead, the sums of 19 parts took 60 us of its two SMs' time; by one
-// warp a chunk, 15 us.)
+// warp a chunk, 15 us.)  Bound by the latency of the parts' sums from L2.
 template <int VEC, bool SLOPE>
 __global__ void __launch_bounds__(128) finish_kernel(const __grid_constant__ Product p, const __grid_constant__ Plan pl) {
     __shared__ float4 buf[4][256];
@@ -681,7 +695,8 @@ __global__ void __launch_bounds__(128) finish_kernel(const __grid_constant__ Pro
 // that do (dst.ld a multiple of 8): eight elements to a thread, from the two
 // 16-byte words that hold them, moved together.  A word is read only if it holds
 // a byte between the matrix's first element and its last; what dst gets past a
-// row's end is not defined.
+// row's end is not defined.  Bound by latency at the sizes that come unaligned:
+// 5121 x 1283 in 6.0 us.
 __global__ void __launch_bounds__(256) align_rows_kernel(int64_t rows, int64_t cols, Mat src, Mat dst, uint32_t chunks) {
     starts_early();
     after_previous();
@@ -765,14 +780,13 @@ cudaError_t make_map(CUtensorMap* map, const Mat& m, int64_t rows, int64_t cols,
 // Long sums: the tensor cores cut an accumulator off to 24 bits with every 16
 // products (measured: a relative error of 1.1e-9 k for random signs, 4.4e-6 at
 // k = 4096), which an F32 result would show.  So where one is asked for and a
-// cluster's k is above kLongSum stages (2048), the accumulator is emptied every
-// kSlice stages (1024) and the slices are added in fp32, rounded to nearest: an
-// error of 1.0e-6 at any k.  The running sums need tensor memory, which leaves
-// tiles of at most 160 columns: 8192 x 4608 x 4608 at 1615 to 1635 TFLOP/s
-// against 1700 uncut, 1640 to 1670 with slices of 2048, 1570 with slices of 512.
-// At k up to 2048 the narrower tiles cost more than the bits are worth (1031 x
-// 5121 x 1283 in two parts: 42.0 us against 38.3, for 7e-7 against 1.0e-6).
-constexpr int kLongSum = 32, kSlice = 16;
+// cluster's k is above kSlice stages (768), the accumulator is emptied every
+// kSlice stages and the slices are added in fp32, rounded to nearest: an error of
+// 7.3e-7 at any k.  The running sums need tensor memory, which leaves tiles of at
+// most 160 columns: 8192 x 4608 x 4608 at 1610 TFLOP/s against 1700 uncut, 1630
+// with slices of 1024 (1.0e-6), 1655 with 2048 (2.1e-6), 1570 with 512 (4.7e-7);
+// 1031 x 1283 x 5121 in 42.2 us (5.0e-7) against 38.3 uncut (1.0e-6).
+constexpr int kSlice = 12;
 
 Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, bool exact_sums, int clusters) {
     Plan best{};
@@ -797,7 +811,7 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, bool ex
             p.whole = static_cast<uint32_t>(p.parts > 1 ? tiles - left : tiles);
             p.units = static_cast<uint32_t>(p.whole + (tiles - p.whole) * p.parts);
             const int deepest = p.whole > 0 ? p.ks : (p.ks + p.parts - 1) / p.parts;
-            const bool sliced = exact_sums && deepest > kLongSum;
+            const bool sliced = exact_sums && deepest > kSlice;
             if (sliced && bn > 160) continue;
             p.slice = sliced ? kSlice : 0x40000000;
             p.buffer = sliced ? bn : 256;
