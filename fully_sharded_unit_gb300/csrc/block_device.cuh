@@ -132,6 +132,130 @@ __device__ __forceinline__ void load_chunks(const void* p, int dtype, int64_t i,
     }
 }
 
+// ---- rows that start anywhere ----
+
+// `bytes` bytes from an address that is aligned to its elements only, as words: the
+// 16-byte words that hold them (each read only if it holds one), moved together by
+// the address's offset.  What lies past `bytes` in w is not defined.
+template <int WORDS>
+__device__ __forceinline__ void load_window(uintptr_t from, int bytes, uint32_t* w) {
+    const uintptr_t word = from & ~uintptr_t(15), end = bytes > 0 ? from + bytes : 0;
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+        uint4 a = make_uint4(0, 0, 0, 0);
+        if (word + 16 * i < end) a = *reinterpret_cast<const uint4*>(word + 16 * i);
+        w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
+    }
+    if (from & 8) {
+#pragma unroll
+        for (int i = 0; i + 2 < 4 * WORDS; ++i) w[i] = w[i + 2];
+    }
+    if (from & 4) {
+#pragma unroll
+        for (int i = 0; i + 1 < 4 * WORDS; ++i) w[i] = w[i + 1];
+    }
+    if (from & 2) {
+#pragma unroll
+        for (int i = 0; i + 1 < 4 * WORDS; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+}
+
+// The reverse: `bytes` (at most 16 N) of the words in v to an address that is
+// aligned to its elements only, in whole 16-byte words where the address allows
+// it.  `joined`: the lane before stores the 16 N bytes that end where this lane's
+// begin, so that this lane's first word takes their end along.  What is left at
+// the ends of such a run goes two bytes at a time.  All lanes take part.
+template <int N>
+__device__ __forceinline__ void store_window(uintptr_t to, int bytes, bool joined, const uint32_t* v) {
+    const bool next = __shfl_down_sync(0xffffffffu, static_cast<int>(joined), 1) != 0 && (threadIdx.x & 31) != 31;
+    uint32_t w[4 * N + 8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(0xffffffffu, v[4 * N - 4 + i], 1);
+#pragma unroll
+    for (int i = 0; i < 4 * N; ++i) w[4 + i] = v[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[4 * N + 4 + i] = 0;
+    // w holds the bytes from to - 16 on: brought to those from the word below `to`
+    const uint32_t shift = 16 - static_cast<uint32_t>(to & 15);
+    if (shift & 16) {
+#pragma unroll
+        for (int i = 0; i < 4 * N + 4; ++i) w[i] = w[i + 4];
+    }
+    if (shift & 8) {
+#pragma unroll
+        for (int i = 0; i < 4 * N + 4; ++i) w[i] = w[i + 2];
+    }
+    if (shift & 4) {
+#pragma unroll
+        for (int i = 0; i < 4 * N + 4; ++i) w[i] = w[i + 1];
+    }
+    if (shift & 2) {
+#pragma unroll
+        for (int i = 0; i < 4 * N + 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+    const uintptr_t base = to & ~uintptr_t(15), end = to + bytes, first = joined ? base : to;
+#pragma unroll
+    for (int i = 0; i <= N; ++i) {
+        const uintptr_t at = base + 16 * i;
+        if (at >= first && at + 16 <= end) {
+            *reinterpret_cast<uint4*>(at) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        } else if (at < end && !(next && at + 16 > end)) {
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+                const uintptr_t p = at + 2 * h;
+                if (p >= first && p < end) *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[4 * i + h / 2] >> (16 * (h & 1)));
+            }
+        }
+    }
+}
+
+// Eight elements of a row from column c on, `left` of them inside it (0 or fewer:
+// none); the others are 0.  N chunks `stride` columns apart.
+template <int N>
+__device__ __forceinline__ void load_chunks_any(const void* p, int dtype, int64_t i, int64_t left, int64_t stride, float (*v)[8]) {
+    if (dtype == FSDP_DTYPE_F32) {
+        uint32_t w[N][12];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int64_t n = max(static_cast<int64_t>(0), min(static_cast<int64_t>(8), left - k * stride));
+            load_window<3>(reinterpret_cast<uintptr_t>(static_cast<const float*>(p) + i + k * stride), static_cast<int>(n) * 4, w[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[k][j] = j < left - k * stride ? __uint_as_float(w[k][j]) : 0.0f;
+    } else {
+        uint32_t w[N][8];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int64_t n = max(static_cast<int64_t>(0), min(static_cast<int64_t>(8), left - k * stride));
+            load_window<2>(reinterpret_cast<uintptr_t>(static_cast<const uint16_t*>(p) + i + k * stride), static_cast<int>(n) * 2, w[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[k][j] = j < left - k * stride ? (j & 1 ? bf16_hi(w[k][j / 2]) : bf16_lo(w[k][j / 2])) : 0.0f;
+    }
+}
+
+// The reverse, one chunk; the lane before holds the chunk before.  All lanes take part.
+__device__ __forceinline__ void store_chunk_any(void* p, int dtype, int64_t i, int64_t left, const float* v) {
+    const int n = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(8), left)));
+    const bool joined = n > 0 && (threadIdx.x & 31) != 0;
+    if (dtype == FSDP_DTYPE_F32) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[j]);
+        store_window<2>(reinterpret_cast<uintptr_t>(static_cast<float*>(p) + i), n * 4, joined, w);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = to_bf16x2(v[2 * j], v[2 * j + 1]);
+        store_window<1>(reinterpret_cast<uintptr_t>(static_cast<uint16_t*>(p) + i), n * 2, joined, w);
+    }
+}
+
 // ---- pairs of floats in one 64-bit register (one instruction for both) ----
 
 using f32x2 = unsigned long long;

@@ -117,33 +117,8 @@ __device__ __forceinline__ uint32_t store_row32(const Mat& x, int64_t m, int64_t
     return 0;
 }
 
-// The same from a row that starts anywhere (BF16 or F32): the 16-byte words that
-// hold the elements (each read only if it holds one), moved together by the
-// row's offset.  An element at a time, 32 loads of 64 bytes a warp, it took twice
-// the time of the whole product.
-template <int WORDS>
-__device__ __forceinline__ void load_window(uintptr_t from, int bytes, uint32_t* w) {
-    const uintptr_t word = from & ~uintptr_t(15), end = from + bytes;
-#pragma unroll
-    for (int i = 0; i < WORDS; ++i) {
-        uint4 a = make_uint4(0, 0, 0, 0);
-        if (word + 16 * i < end) a = *reinterpret_cast<const uint4*>(word + 16 * i);
-        w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
-    }
-    if (from & 8) {
-#pragma unroll
-        for (int i = 0; i + 2 < 4 * WORDS; ++i) w[i] = w[i + 2];
-    }
-    if (from & 4) {
-#pragma unroll
-        for (int i = 0; i + 1 < 4 * WORDS; ++i) w[i] = w[i + 1];
-    }
-    if (from & 2) {
-#pragma unroll
-        for (int i = 0; i + 1 < 4 * WORDS; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-    }
-}
-
+// The same from a row that starts anywhere (BF16 or F32).  An element at a time,
+// 32 loads of 64 bytes a warp, it took twice the time of the whole product.
 __device__ __forceinline__ void load_row32_any(const Mat& x, int64_t m, int64_t n, int left, float* v) {
     if (x.dtype == FSDP_DTYPE_ACT8) {
         load_row32<false>(x, m, n, left, v);   // aligned by its format
@@ -160,6 +135,21 @@ __device__ __forceinline__ void load_row32_any(const Mat& x, int64_t m, int64_t 
             v[2 * j] = bf16_lo(w[j]);
             v[2 * j + 1] = bf16_hi(w[j]);
         }
+    }
+}
+
+// The reverse (see store_window); all lanes take part.
+__device__ __forceinline__ void store_row32_any(const Mat& x, int64_t m, int64_t n, int left, bool joined, const float* v) {
+    if (x.dtype == FSDP_DTYPE_F32) {
+        uint32_t w[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j]);
+        store_window<8>(reinterpret_cast<uintptr_t>(static_cast<float*>(x.p) + m * x.ld + n), left * 4, joined, w);
+    } else {
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) w[j] = to_bf16x2(v[2 * j], v[2 * j + 1]);
+        store_window<4>(reinterpret_cast<uintptr_t>(static_cast<uint16_t*>(x.p) + m * x.ld + n), left * 2, joined, w);
     }
 }
 

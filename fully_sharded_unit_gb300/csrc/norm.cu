@@ -29,12 +29,11 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
     return s;
 }
 
-// One row to a warp (WARP) or to a block; chunk k of a thread holds the V
-// columns from (t + k * threads) * V.  For rows that are too few to walk, or that
-// start anywhere: one row of 1280 takes the latency of a launch, a load and two
-// sums; 4096 rows of 1281 columns (V = 1) take 22 us,
-// which loads and stores of two bytes a lane bound.
-template <int V, int NV, bool WARP>
+// One row to a warp (WARP) or to a block; chunk k of a thread holds the eight
+// columns from (t + k * threads) * 8.  For rows that are too few to walk, or (ANY)
+// that start anywhere: one row of 1280 takes the latency of a launch, a load and
+// two sums; 4096 rows of 1281 columns, NORMU.
+template <int NV, bool WARP, bool ANY>
 __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_forward_kernel(NormForward a) {
     __shared__ float red[2][32];
     starts_early();
@@ -45,22 +44,24 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_forward_kernel(NormFor
     const int64_t stride = WARP ? static_cast<int64_t>(gridDim.x) * 4 : gridDim.x;
     const float n = static_cast<float>(a.cols);
     for (int64_t row = first; row < a.rows; row += stride) {
-        float v[NV][V];
+        float v[NV][8];
         float s = 0.0f;
-        const auto on = [&](int k) { return static_cast<int64_t>(t + k * threads) * V < a.cols; };
-        if constexpr (V == 8) load_chunks<NV>(a.x.p, a.x.dtype, row * a.x.ld + t * 8, threads * 8, on, v);
-        else load_strided<NV>(a.x.p, a.x.dtype, row * a.x.ld + t, threads, on, &v[0][0]);
+        const auto on = [&](int k) { return static_cast<int64_t>(t + k * threads) * 8 < a.cols; };
+        if constexpr (ANY) load_chunks_any<NV>(a.x.p, a.x.dtype, row * a.x.ld + t * 8, a.cols - t * 8, threads * 8, v);
+        else load_chunks<NV>(a.x.p, a.x.dtype, row * a.x.ld + t * 8, threads * 8, on, v);
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
-            for (int j = 0; j < V; ++j) s += v[k][j];
+            for (int j = 0; j < 8; ++j) s += v[k][j];
         const float mean = (WARP ? warp_sum(s) : block_sum(s, red[0])) / n;
         float ss = 0.0f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (static_cast<int64_t>(t + k * threads) * V < a.cols) {
+            const int64_t left = a.cols - static_cast<int64_t>(t + k * threads) * 8;
 #pragma unroll
-                for (int j = 0; j < V; ++j) ss = fmaf(v[k][j] - mean, v[k][j] - mean, ss);
+            for (int j = 0; j < 8; ++j) {
+                const float d = j < left || (!ANY && left > 0) ? v[k][j] - mean : 0.0f;
+                ss = fmaf(d, d, ss);
             }
         }
         const float var = (WARP ? warp_sum(ss) : block_sum(ss, red[1])) / n;
@@ -69,23 +70,31 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_forward_kernel(NormFor
             a.mean[row] = mean;
             a.rstd[row] = rstd;
         }
+        float g[ANY ? NV : 1][8], b[ANY ? NV : 1][8];
+        if constexpr (ANY) {
+            load_chunks_any<NV>(a.gamma, a.param_dtype, t * 8, a.cols - t * 8, threads * 8, g);
+            load_chunks_any<NV>(a.beta, a.param_dtype, t * 8, a.cols - t * 8, threads * 8, b);
+        }
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int64_t c = static_cast<int64_t>(t + k * threads) * V;
+            const int64_t c = static_cast<int64_t>(t + k * threads) * 8;
             if (a.ckpt.p != nullptr) {
-                const uint32_t top = act8_group_top<V>(v[k]);
+                const uint32_t top = act8_group_top<8>(v[k]);
                 if (c < a.ckpt.ld) {
-                    act8_writev<V>(static_cast<uint8_t*>(a.ckpt.p) + row * a.ckpt.ld, c, v[k], top);
-                    if ((t & (32 / V - 1)) == 0) a.ckpt.e[row * a.ckpt.eld + (c >> 5)] = static_cast<uint8_t>(act8_byte(top));
+                    act8_writev<8>(static_cast<uint8_t*>(a.ckpt.p) + row * a.ckpt.ld, c, v[k], top);
+                    if ((t & 3) == 0) a.ckpt.e[row * a.ckpt.eld + (c >> 5)] = static_cast<uint8_t>(act8_byte(top));
                 }
             }
-            if (c < a.cols) {
-                float g[V], b[V];
-                loadv<V>(a.gamma, a.param_dtype, c, g);
-                loadv<V>(a.beta, a.param_dtype, c, b);
+            if constexpr (ANY) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) v[k][j] = fmaf((v[k][j] - mean) * rstd, g[j], b[j]);
-                storev<V>(a.y.p, a.y.dtype, row * a.y.ld + c, v[k]);
+                for (int j = 0; j < 8; ++j) v[k][j] = fmaf((v[k][j] - mean) * rstd, g[k][j], b[k][j]);
+                store_chunk_any(a.y.p, a.y.dtype, row * a.y.ld + c, a.cols - c, v[k]);
+            } else if (c < a.cols) {
+                load8(a.gamma, a.param_dtype, c, g[0]);
+                load8(a.beta, a.param_dtype, c, b[0]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[k][j] = fmaf((v[k][j] - mean) * rstd, g[0][j], b[0][j]);
+                store8(a.y.p, a.y.dtype, row * a.y.ld + c, v[k]);
             }
         }
         if (!WARP) __syncthreads();
@@ -580,9 +589,6 @@ __global__ void __launch_bounds__(THREADS) norm_backward_ring_kernel(const __gri
 
 // ---- other rows ----
 
-// Rows that start anywhere: one column to a thread at a time, straight from
-// global memory.  Bound by the loads, of two bytes a lane: 4096 x 1281 in 63
-// us (0.5 TB/s).
 __device__ __forceinline__ float2 group_sum2(float a, float b, float2* red, int group, int gt) {
     a = warp_sum(a);
     b = warp_sum(b);
@@ -598,6 +604,9 @@ __device__ __forceinline__ float2 group_sum2(float a, float b, float2* red, int 
     return make_float2(a, b);
 }
 
+// Rows that start anywhere: chunks of eight columns straight from global memory,
+// as words that hold them.  Bound by a row's latency and the registers, which
+// allow few rows on an SM: 4096 x 1281, BWDU.
 template <int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_backward_kernel(NormBackward a, int gt) {
     extern __shared__ __align__(16) uint8_t ring_bytes[];
@@ -606,76 +615,87 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(NormBackward a, 
     after_previous();
     const int g = threadIdx.x / gt, t = threadIdx.x % gt, G = blockDim.x / gt;
     const float inv_n = 1.0f / static_cast<float>(a.cols);
-    float dg[NV], db[NV];
+    const int64_t left = a.cols - t * 8;
+    float dg[NV][8], db[NV][8], gm[NV][8];
+    load_chunks_any<NV>(a.gamma, a.param_dtype, t * 8, left, gt * 8, gm);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) dg[k] = db[k] = 0.0f;
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dg[k][j] = db[k][j] = 0.0f;
     int flip = 0;
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * G + g; row < a.rows; row += static_cast<int64_t>(gridDim.x) * G) {
-        float xh[NV], dy[NV];
+        float xh[NV][8], dy[NV][8];
         const float mean = a.mean[row], rstd = a.rstd[row];
-        const auto on = [&](int k) { return t + k * gt < a.cols; };
-        load_strided<NV>(a.dy.p, a.dy.dtype, row * a.dy.ld + t, gt, on, dy);
+        load_chunks_any<NV>(a.dy.p, a.dy.dtype, row * a.dy.ld + t * 8, left, gt * 8, dy);
         if (a.x.dtype == FSDP_DTYPE_ACT8) {
-            const int8_t* q = static_cast<const int8_t*>(a.x.p) + row * a.x.ld + t;
-            const uint8_t* e = a.x.e + row * a.x.eld + (t >> 5);   // gt is a multiple of 32
-            int w[NV];
-            uint32_t byte[NV];
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                w[k] = on(k) ? q[k * gt] : 0;
-                byte[k] = on(k) ? e[k * (gt >> 5)] : 127u;
-            }
+                const int64_t c = (t + k * gt) * 8;
+                if (c < a.cols) {
+                    act8_readv<8>(static_cast<const uint8_t*>(a.x.p) + row * a.x.ld, a.x.e + row * a.x.eld, c, xh[k]);
+                } else {
 #pragma unroll
-            for (int k = 0; k < NV; ++k) xh[k] = static_cast<float>(w[k]) * act8_step(byte[k]);
+                    for (int j = 0; j < 8; ++j) xh[k][j] = 0.0f;
+                }
+            }
         } else {
-            load_strided<NV>(a.x.p, a.x.dtype, row * a.x.ld + t, gt, on, xh);
+            load_chunks_any<NV>(a.x.p, a.x.dtype, row * a.x.ld + t * 8, left, gt * 8, xh);
         }
-        float gm[NV], add[NV];
-        load_strided<NV>(a.gamma, a.param_dtype, t, gt, on, gm);
-        if (a.add.p != nullptr) load_strided<NV>(a.add.p, a.add.dtype, row * a.add.ld + t, gt, on, add);
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            xh[k] = on(k) ? (xh[k] - mean) * rstd : 0.0f;
-            db[k] += dy[k];
-            dg[k] = fmaf(dy[k], xh[k], dg[k]);
-            dy[k] *= gm[k];
-            s1 += dy[k];
-            s2 = fmaf(dy[k], xh[k], s2);
-        }
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                // past the row's end dy and gamma are 0, and x-hat is held at 0
+                xh[k][j] = j < left - k * gt * 8 ? (xh[k][j] - mean) * rstd : 0.0f;
+                db[k][j] += dy[k][j];
+                dg[k][j] = fmaf(dy[k][j], xh[k][j], dg[k][j]);
+                dy[k][j] *= gm[k][j];
+                s1 += dy[k][j];
+                s2 = fmaf(dy[k][j], xh[k][j], s2);
+            }
         const float2 sum = group_sum2(s1, s2, red[flip], g, gt);
         flip ^= 1;
         const float c1 = sum.x * inv_n, c2 = sum.y * inv_n;
 #pragma unroll
-        for (int k = 0; k < NV; ++k) dy[k] = rstd * (dy[k] - c1 - xh[k] * c2) + (a.add.p != nullptr ? add[k] : 0.0f);
-        store_strided<NV>(a.dx.p, a.dx.dtype, row * a.dx.ld + t, gt, on, dy);
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dy[k][j] = rstd * (dy[k][j] - c1 - xh[k][j] * c2);
+        if (a.add.p != nullptr) {
+            load_chunks_any<NV>(a.add.p, a.add.dtype, row * a.add.ld + t * 8, left, gt * 8, xh);
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dy[k][j] += xh[k][j];
+            // add may be dx itself: the chunks' neighbours, of which the words above hold
+            // a part, are stored after every lane has read them
+            __syncwarp();
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int64_t c = (t + k * gt) * 8;
+            store_chunk_any(a.dx.p, a.dx.dtype, row * a.dx.ld + c, a.cols - c, dy[k]);
+        }
     }
+    // the groups' column sums meet in shared memory: element j of chunk i at j * slots + i
     float* part = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
-    const int slots = NV * gt;
+    const int slots = NV * gt + 4;
     float* comb = reinterpret_cast<float*>(ring_bytes);
-    if (G > 1) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            comb[2 * g * slots + t + k * gt] = dg[k];
-            comb[(2 * g + 1) * slots + t + k * gt] = db[k];
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < 2 * slots; i += blockDim.x) {
-            float s = 0.0f;
-            for (int h = 0; h < G; ++h) s += comb[2 * h * slots + i];
-            const int64_t c = i < slots ? i : i - slots;
-            if (c < a.cols) part[(i < slots ? 0 : a.cols) + c] = s;
-        }
-    } else {
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int64_t c = t + k * gt;
-            if (c < a.cols) {
-                part[c] = dg[k];
-                part[a.cols + c] = db[k];
-            }
+        for (int j = 0; j < 8; ++j) {
+            comb[(g * 16 + j) * slots + t + k * gt] = dg[k][j];
+            comb[(g * 16 + 8 + j) * slots + t + k * gt] = db[k][j];
         }
-    }
+    __syncthreads();
+    for (int o = 0; o < 2; ++o)
+        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+            const float* from = comb + (o * 8 + (c & 7)) * slots + (c >> 3);
+            float s = from[0];
+            for (int h = 1; h < G; ++h) s += from[h * 16 * slots];
+            part[o * a.cols + c] = s;
+        }
 }
 
 // Rows too long for registers: dx first (two passes over a row), then the
@@ -778,16 +798,14 @@ cudaError_t sum_partials(const float* partials, int64_t count, int64_t stride, i
 
 int round32(int64_t n) { return static_cast<int>((n + 31) / 32 * 32); }
 
-// A row to a block, or to a warp (SHORT) where its lanes hold it whole.
-template <int V, int NV, bool SHORT>
+// A row to a warp where its lanes hold it whole, or to a block.
+template <bool ANY>
 cudaError_t run_forward(const NormForward& a, int64_t chunks, cudaStream_t st) {
-    const int64_t cap = int64_t(1) << 30;
-    if constexpr (SHORT) {
-        if (chunks <= 32 * NV)
-            return launch_early(norm_forward_kernel<V, NV, true>, dim3(static_cast<unsigned>(std::min((a.rows + 3) / 4, cap))), 128, 0, st, a);
-    }
-    return launch_early(norm_forward_kernel<V, NV, false>, dim3(static_cast<unsigned>(std::min(a.rows, cap))),
-                        round32((chunks + NV - 1) / NV), 0, st, a);
+    const unsigned blocks = static_cast<unsigned>(std::min(chunks <= 32 ? (a.rows + 3) / 4 : a.rows, int64_t(1) << 30));
+    if (chunks <= 32) return launch_early(norm_forward_kernel<1, true, ANY>, dim3(blocks), 128, 0, st, a);
+    if (chunks <= 512) return launch_early(norm_forward_kernel<1, false, ANY>, dim3(blocks), round32(chunks), 0, st, a);
+    constexpr int kMost = ANY ? 2 : 4;   // unaligned rows need more registers for a chunk
+    return launch_early(norm_forward_kernel<kMost, false, ANY>, dim3(blocks), round32((chunks + kMost - 1) / kMost), 0, st, a);
 }
 
 constexpr int kSharedMost = 222 * 1024;   // dynamic shared memory of a block
@@ -847,10 +865,11 @@ Split backward_split(const NormBackward& a, bool vec) {
         return p;
     }
     Split p;
-    if (cols <= 8192) {
-        p.NV = 8;
-        p.gt = round32((cols + 7) / 8);
-        p.groups = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(1024 / p.gt, 15), rows)));
+    const int64_t chunks = (cols + 7) / 8;
+    if (chunks <= 1536) {
+        p.NV = chunks <= 768 ? 1 : 2;
+        p.gt = round32((chunks + p.NV - 1) / p.NV);
+        p.groups = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(768 / p.gt, 15), rows)));
     }
     return p;
 }
@@ -894,12 +913,9 @@ cudaError_t launch_norm_forward(const NormForward& a, int sms, cudaStream_t st) 
             RING(4, 256) RING(5, 256) RING(6, 256) RING(4, 512)
 #undef RING
         }
-        const int64_t chunks = a.cols / 8;
-        if (chunks <= 512) return run_forward<8, 1, true>(a, chunks, st);
-        if (chunks <= 4096) return run_forward<8, 4, false>(a, chunks, st);
-    } else {
-        if (a.cols <= 4096) return run_forward<1, 8, true>(a, a.cols, st);
-        if (a.cols <= 16384) return run_forward<1, 16, false>(a, a.cols, st);
+        if (a.cols <= 4096 * 8) return run_forward<false>(a, a.cols / 8, st);
+    } else if (a.cols <= 2048 * 8) {
+        return run_forward<true>(a, (a.cols + 7) / 8, st);
     }
     return launch_early(norm_forward_wide_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t(1) << 30))), 1024, 0, st, a);
 }
@@ -943,8 +959,9 @@ cudaError_t launch_norm_backward(const NormBackward& a, int sms, cudaStream_t st
 #undef RING
 #undef RING_
     } else {
-        const int comb = p.groups > 1 ? p.threads() * p.NV * 2 * 4 : 0;
-        e = launch_shared<norm_backward_kernel<8, 1024>>(blocks, p.threads(), comb, st, a, p.gt);
+        const int comb = p.groups * 16 * (p.NV * p.gt + 4) * 4;
+        e = p.NV == 1 ? launch_shared<norm_backward_kernel<1, 768>>(blocks, p.threads(), comb, st, a, p.gt)
+                      : launch_shared<norm_backward_kernel<2, 768>>(blocks, p.threads(), comb, st, a, p.gt);
     }
     if (e != cudaSuccess) return e;
     return sum_partials(a.partials, count, 2 * a.cols, a.cols, a.cols, a.dgamma, a.dbeta, a.grad_dtype, a.accumulate, st);

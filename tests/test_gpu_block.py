@@ -40,7 +40,8 @@ def _same_pack(x, k):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("rows,cols,pad,offset", [(1, 1, 0, 0), (3, 31, 0, 0), (2, 32, 8, 8), (5, 33, 3, 1), (7, 256, 0, 0),
-                                                  (4, 264, 8, 0), (3, 264, 5, 0), (2, 1283, 1, 3), (300, 40, 0, 0)])
+                                                  (4, 264, 8, 0), (3, 264, 5, 0), (2, 1283, 1, 3), (300, 40, 0, 0),
+                                                  (70, 1025, 2, 1), (9, 1056, 3, 2), (130, 37, 0, 0)])
 def test_act8_pack_and_unpack(handle, dtype, rows, cols, pad, offset):
     x = Guarded(rows, cols, dtype, pad, offset, _normal(rows + cols, (rows, cols), 3.0, dtype)).t
     k = B.Act8(rows, cols)
@@ -514,6 +515,15 @@ def test_layer_norm_many_rows(handle, rows, cols):
     assert torch.equal(k.q, other.q) and torch.equal(k.exps, other.exps)
     for ckpt, add in ((False, "other"), (True, None)):
         _norm_grad_case(handle, rows, cols, 0, 0, BF, BF, BF, F32, ckpt, add, False)
+
+
+@pytest.mark.parametrize("rows,cols,pad,offset", [(1000, 31, 3, 1), (1000, 257, 0, 0), (700, 1283, 3, 1), (400, 2050, 2, 6), (320, 4099, 0, 0),
+                                                  (320, 6151, 1, 0), (160, 12287, 3, 5), (40, 16383, 2, 1), (700, 1280, 3, 0)])
+def test_layer_norm_many_rows_anywhere(handle, rows, cols, pad, offset):
+    for xdt, ydt, pdt in ((BF, BF, BF), (F32, BF, F32)):
+        test_layer_norm_forward(handle, rows, cols, pad, offset, xdt, ydt, pdt)
+    for (xdt, ydt, pdt), ckpt, add in (((BF, BF, BF), False, "same"), ((BF, BF, F32), True, "other"), ((F32, F32, BF), False, "other")):
+        _norm_grad_case(handle, rows, cols, pad, offset, xdt, ydt, pdt, F32, ckpt, add, False)
 
 
 @pytest.mark.parametrize("T,I,O_,kind", [(300, 16384, 512, "fwd"), (20000, 264, 512, "dw"), (300, 40000, 8192, "fwd")])
