@@ -17,8 +17,7 @@ namespace {
 // 8192 x 5120: pack 24.5 us (5.2 TB/s), unpack with GELU 28 (4.5; the special
 // functions take half of it); 4096 x 12288: unpack 27 (5.7).
 // ANY: x's rows start anywhere and are read and stored as the 16-byte words that
-// hold them (4096 x 1281: pack PACKU us, unpack UNPACKU; an element to a lane
-// took 27).
+// hold them (4096 x 1281: pack 11 us, unpack 11; an element to a lane took 27).
 template <bool WIDE, bool ANY, bool PACK>
 __global__ void __launch_bounds__(256) act8_groups_kernel(int64_t cols, Mat q, int act, Mat x, int64_t count, uint32_t groups) {
     starts_early();

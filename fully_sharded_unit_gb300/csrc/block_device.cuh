@@ -67,11 +67,6 @@ __device__ __forceinline__ void loadv(const void* p, int dtype, int64_t i, float
     if constexpr (V == 8) load8(p, dtype, i, v);
     else v[0] = load1(p, dtype, i);
 }
-template <int V>
-__device__ __forceinline__ void storev(void* p, int dtype, int64_t i, const float* v) {
-    if constexpr (V == 8) store8(p, dtype, i, v);
-    else store1(p, dtype, i, v[0]);
-}
 
 // N elements `stride` apart, or 0 where on(i) is false.  The type is looked at
 // once, outside the loop: with a branch in it, each load would wait for the one
@@ -139,11 +134,12 @@ __device__ __forceinline__ void load_chunks(const void* p, int dtype, int64_t i,
 // the address's offset.  What lies past `bytes` in w is not defined.
 template <int WORDS>
 __device__ __forceinline__ void load_window(uintptr_t from, int bytes, uint32_t* w) {
-    const uintptr_t word = from & ~uintptr_t(15), end = bytes > 0 ? from + bytes : 0;
+    const uintptr_t word = from & ~uintptr_t(15);
+    const int end = bytes > 0 ? static_cast<int>(from & 15) + bytes : 0;
 #pragma unroll
     for (int i = 0; i < WORDS; ++i) {
         uint4 a = make_uint4(0, 0, 0, 0);
-        if (word + 16 * i < end) a = *reinterpret_cast<const uint4*>(word + 16 * i);
+        if (16 * i < end) a = *reinterpret_cast<const uint4*>(word + 16 * i);
         w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
     }
     if (from & 8) {
@@ -193,55 +189,53 @@ __device__ __forceinline__ void store_window(uintptr_t to, int bytes, bool joine
 #pragma unroll
         for (int i = 0; i < 4 * N + 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
     }
-    const uintptr_t base = to & ~uintptr_t(15), end = to + bytes, first = joined ? base : to;
+    uint8_t* const base = reinterpret_cast<uint8_t*>(to & ~uintptr_t(15));
+    const int skip = static_cast<int>(to & 15), end = skip + bytes, first = joined ? 0 : skip;
 #pragma unroll
     for (int i = 0; i <= N; ++i) {
-        const uintptr_t at = base + 16 * i;
-        if (at >= first && at + 16 <= end) {
-            *reinterpret_cast<uint4*>(at) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        } else if (at < end && !(next && at + 16 > end)) {
+        if (16 * i >= first && 16 * i + 16 <= end) {
+            reinterpret_cast<uint4*>(base)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        } else if (16 * i < end && bytes > 0 && !(next && 16 * i + 16 > end)) {
 #pragma unroll
-            for (int h = 0; h < 8; ++h) {
-                const uintptr_t p = at + 2 * h;
-                if (p >= first && p < end) *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[4 * i + h / 2] >> (16 * (h & 1)));
-            }
+            for (int h = 0; h < 8; ++h)
+                if (16 * i + 2 * h >= first && 16 * i + 2 * h < end)
+                    reinterpret_cast<uint16_t*>(base)[8 * i + h] = static_cast<uint16_t>(w[4 * i + h / 2] >> (16 * (h & 1)));
         }
     }
 }
 
-// Eight elements of a row from column c on, `left` of them inside it (0 or fewer:
-// none); the others are 0.  N chunks `stride` columns apart.
+// How many of the eight columns from c on are inside a row of `cols`.
+__device__ __forceinline__ int inside8(int64_t c, int64_t cols) {
+    return static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(8), cols - c)));
+}
+
+// Chunks of eight columns `stride` elements apart, n[k] of them inside the row
+// (see inside8); the others are 0.
 template <int N>
-__device__ __forceinline__ void load_chunks_any(const void* p, int dtype, int64_t i, int64_t left, int64_t stride, float (*v)[8]) {
+__device__ __forceinline__ void load_chunks_any(const void* p, int dtype, int64_t i, const int* n, int64_t stride, float (*v)[8]) {
     if (dtype == FSDP_DTYPE_F32) {
         uint32_t w[N][12];
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int64_t n = max(static_cast<int64_t>(0), min(static_cast<int64_t>(8), left - k * stride));
-            load_window<3>(reinterpret_cast<uintptr_t>(static_cast<const float*>(p) + i + k * stride), static_cast<int>(n) * 4, w[k]);
-        }
+        for (int k = 0; k < N; ++k)
+            load_window<3>(reinterpret_cast<uintptr_t>(static_cast<const float*>(p) + i + k * stride), n[k] * 4, w[k]);
 #pragma unroll
         for (int k = 0; k < N; ++k)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[k][j] = j < left - k * stride ? __uint_as_float(w[k][j]) : 0.0f;
+            for (int j = 0; j < 8; ++j) v[k][j] = j < n[k] ? __uint_as_float(w[k][j]) : 0.0f;
     } else {
         uint32_t w[N][8];
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int64_t n = max(static_cast<int64_t>(0), min(static_cast<int64_t>(8), left - k * stride));
-            load_window<2>(reinterpret_cast<uintptr_t>(static_cast<const uint16_t*>(p) + i + k * stride), static_cast<int>(n) * 2, w[k]);
-        }
+        for (int k = 0; k < N; ++k)
+            load_window<2>(reinterpret_cast<uintptr_t>(static_cast<const uint16_t*>(p) + i + k * stride), n[k] * 2, w[k]);
 #pragma unroll
         for (int k = 0; k < N; ++k)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[k][j] = j < left - k * stride ? (j & 1 ? bf16_hi(w[k][j / 2]) : bf16_lo(w[k][j / 2])) : 0.0f;
+            for (int j = 0; j < 8; ++j) v[k][j] = j < n[k] ? (j & 1 ? bf16_hi(w[k][j / 2]) : bf16_lo(w[k][j / 2])) : 0.0f;
     }
 }
 
 // The reverse, one chunk; the lane before holds the chunk before.  All lanes take part.
-__device__ __forceinline__ void store_chunk_any(void* p, int dtype, int64_t i, int64_t left, const float* v) {
-    const int n = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(8), left)));
+__device__ __forceinline__ void store_chunk_any(void* p, int dtype, int64_t i, int n, const float* v) {
     const bool joined = n > 0 && (threadIdx.x & 31) != 0;
     if (dtype == FSDP_DTYPE_F32) {
         uint32_t w[8];

@@ -32,7 +32,9 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 // One row to a warp (WARP) or to a block; chunk k of a thread holds the eight
 // columns from (t + k * threads) * 8.  For rows that are too few to walk, or (ANY)
 // that start anywhere: one row of 1280 takes the latency of a launch, a load and
-// two sums; 4096 rows of 1281 columns, NORMU.
+// two sums; 4096 rows of 1281 columns, 21 us (1.0 TB/s; an element to a lane, 27),
+// of 5121, 66 (1.3; 88), which the instructions that move the words bound with
+// the rows in flight.
 template <int NV, bool WARP, bool ANY>
 __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_forward_kernel(NormForward a) {
     __shared__ float red[2][32];
@@ -43,11 +45,19 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_forward_kernel(NormFor
     const int64_t first = WARP ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;
     const int64_t stride = WARP ? static_cast<int64_t>(gridDim.x) * 4 : gridDim.x;
     const float n = static_cast<float>(a.cols);
+    float g[NV][8], b[NV][8];
+    int in[NV];   // of a chunk's columns
+#pragma unroll
+    for (int k = 0; k < NV; ++k) in[k] = inside8(static_cast<int64_t>(t + k * threads) * 8, a.cols);
+    if constexpr (ANY) {   // the blocks walk rows
+        load_chunks_any<NV>(a.gamma, a.param_dtype, t * 8, in, threads * 8, g);
+        load_chunks_any<NV>(a.beta, a.param_dtype, t * 8, in, threads * 8, b);
+    }
     for (int64_t row = first; row < a.rows; row += stride) {
         float v[NV][8];
         float s = 0.0f;
         const auto on = [&](int k) { return static_cast<int64_t>(t + k * threads) * 8 < a.cols; };
-        if constexpr (ANY) load_chunks_any<NV>(a.x.p, a.x.dtype, row * a.x.ld + t * 8, a.cols - t * 8, threads * 8, v);
+        if constexpr (ANY) load_chunks_any<NV>(a.x.p, a.x.dtype, row * a.x.ld + t * 8, in, threads * 8, v);
         else load_chunks<NV>(a.x.p, a.x.dtype, row * a.x.ld + t * 8, threads * 8, on, v);
 #pragma unroll
         for (int k = 0; k < NV; ++k)
@@ -57,10 +67,9 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_forward_kernel(NormFor
         float ss = 0.0f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int64_t left = a.cols - static_cast<int64_t>(t + k * threads) * 8;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float d = j < left || (!ANY && left > 0) ? v[k][j] - mean : 0.0f;
+                const float d = (ANY ? j : 0) < in[k] ? v[k][j] - mean : 0.0f;
                 ss = fmaf(d, d, ss);
             }
         }
@@ -69,11 +78,6 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_forward_kernel(NormFor
         if (t == 0) {
             a.mean[row] = mean;
             a.rstd[row] = rstd;
-        }
-        float g[ANY ? NV : 1][8], b[ANY ? NV : 1][8];
-        if constexpr (ANY) {
-            load_chunks_any<NV>(a.gamma, a.param_dtype, t * 8, a.cols - t * 8, threads * 8, g);
-            load_chunks_any<NV>(a.beta, a.param_dtype, t * 8, a.cols - t * 8, threads * 8, b);
         }
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -88,7 +92,7 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_forward_kernel(NormFor
             if constexpr (ANY) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[k][j] = fmaf((v[k][j] - mean) * rstd, g[k][j], b[k][j]);
-                store_chunk_any(a.y.p, a.y.dtype, row * a.y.ld + c, a.cols - c, v[k]);
+                store_chunk_any(a.y.p, a.y.dtype, row * a.y.ld + c, in[k], v[k]);
             } else if (c < a.cols) {
                 load8(a.gamma, a.param_dtype, c, g[0]);
                 load8(a.beta, a.param_dtype, c, b[0]);
@@ -606,7 +610,8 @@ __device__ __forceinline__ float2 group_sum2(float a, float b, float2* red, int 
 
 // Rows that start anywhere: chunks of eight columns straight from global memory,
 // as words that hold them.  Bound by a row's latency and the registers, which
-// allow few rows on an SM: 4096 x 1281, BWDU.
+// allow few rows on an SM: 4096 x 1281 with an added branch 36 us (1.2 TB/s; an
+// element to a lane, 60), 4096 x 5121 109 (1.5; 361).
 template <int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_backward_kernel(NormBackward a, int gt) {
     extern __shared__ __align__(16) uint8_t ring_bytes[];
@@ -615,9 +620,11 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(NormBackward a, 
     after_previous();
     const int g = threadIdx.x / gt, t = threadIdx.x % gt, G = blockDim.x / gt;
     const float inv_n = 1.0f / static_cast<float>(a.cols);
-    const int64_t left = a.cols - t * 8;
+    int in[NV];   // of a chunk's columns
+#pragma unroll
+    for (int k = 0; k < NV; ++k) in[k] = inside8((t + k * gt) * 8, a.cols);
     float dg[NV][8], db[NV][8], gm[NV][8];
-    load_chunks_any<NV>(a.gamma, a.param_dtype, t * 8, left, gt * 8, gm);
+    load_chunks_any<NV>(a.gamma, a.param_dtype, t * 8, in, gt * 8, gm);
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
@@ -626,7 +633,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(NormBackward a, 
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * G + g; row < a.rows; row += static_cast<int64_t>(gridDim.x) * G) {
         float xh[NV][8], dy[NV][8];
         const float mean = a.mean[row], rstd = a.rstd[row];
-        load_chunks_any<NV>(a.dy.p, a.dy.dtype, row * a.dy.ld + t * 8, left, gt * 8, dy);
+        load_chunks_any<NV>(a.dy.p, a.dy.dtype, row * a.dy.ld + t * 8, in, gt * 8, dy);
         if (a.x.dtype == FSDP_DTYPE_ACT8) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
@@ -639,7 +646,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(NormBackward a, 
                 }
             }
         } else {
-            load_chunks_any<NV>(a.x.p, a.x.dtype, row * a.x.ld + t * 8, left, gt * 8, xh);
+            load_chunks_any<NV>(a.x.p, a.x.dtype, row * a.x.ld + t * 8, in, gt * 8, xh);
         }
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
@@ -647,7 +654,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(NormBackward a, 
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 // past the row's end dy and gamma are 0, and x-hat is held at 0
-                xh[k][j] = j < left - k * gt * 8 ? (xh[k][j] - mean) * rstd : 0.0f;
+                xh[k][j] = j < in[k] ? (xh[k][j] - mean) * rstd : 0.0f;
                 db[k][j] += dy[k][j];
                 dg[k][j] = fmaf(dy[k][j], xh[k][j], dg[k][j]);
                 dy[k][j] *= gm[k][j];
@@ -662,7 +669,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(NormBackward a, 
 #pragma unroll
             for (int j = 0; j < 8; ++j) dy[k][j] = rstd * (dy[k][j] - c1 - xh[k][j] * c2);
         if (a.add.p != nullptr) {
-            load_chunks_any<NV>(a.add.p, a.add.dtype, row * a.add.ld + t * 8, left, gt * 8, xh);
+            load_chunks_any<NV>(a.add.p, a.add.dtype, row * a.add.ld + t * 8, in, gt * 8, xh);
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
@@ -674,7 +681,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(NormBackward a, 
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int64_t c = (t + k * gt) * 8;
-            store_chunk_any(a.dx.p, a.dx.dtype, row * a.dx.ld + c, a.cols - c, dy[k]);
+            store_chunk_any(a.dx.p, a.dx.dtype, row * a.dx.ld + c, in[k], dy[k]);
         }
     }
     // the groups' column sums meet in shared memory: element j of chunk i at j * slots + i
@@ -798,14 +805,20 @@ cudaError_t sum_partials(const float* partials, int64_t count, int64_t stride, i
 
 int round32(int64_t n) { return static_cast<int>((n + 31) / 32 * 32); }
 
-// A row to a warp where its lanes hold it whole, or to a block.
+// A row to a warp where its lanes hold it whole, or to a block.  ANY: as many
+// blocks as run at once, which walk the rows.
 template <bool ANY>
-cudaError_t run_forward(const NormForward& a, int64_t chunks, cudaStream_t st) {
-    const unsigned blocks = static_cast<unsigned>(std::min(chunks <= 32 ? (a.rows + 3) / 4 : a.rows, int64_t(1) << 30));
-    if (chunks <= 32) return launch_early(norm_forward_kernel<1, true, ANY>, dim3(blocks), 128, 0, st, a);
-    if (chunks <= 512) return launch_early(norm_forward_kernel<1, false, ANY>, dim3(blocks), round32(chunks), 0, st, a);
-    constexpr int kMost = ANY ? 2 : 4;   // unaligned rows need more registers for a chunk
-    return launch_early(norm_forward_kernel<kMost, false, ANY>, dim3(blocks), round32((chunks + kMost - 1) / kMost), 0, st, a);
+cudaError_t run_forward(const NormForward& a, int64_t chunks, int sms, cudaStream_t st) {
+    const auto blocks = [&](int64_t rows, int threads) {
+        return dim3(static_cast<unsigned>(std::min(rows, ANY ? static_cast<int64_t>(sms) * (1024 / threads) : int64_t(1) << 30)));
+    };
+    if (chunks <= 32) return launch_early(norm_forward_kernel<1, true, ANY>, blocks((a.rows + 3) / 4, 128), 128, 0, st, a);
+    // two chunks to a thread leave room for more rows on an SM (4096 x 4097: 50 us,
+    // with one 76; 4096 x 3585: 48 against 52 at 512)
+    constexpr int kShort = ANY ? 256 : 512, kMost = ANY ? 2 : 4;
+    const int threads = round32(chunks <= kShort ? chunks : (chunks + kMost - 1) / kMost);
+    if (chunks <= kShort) return launch_early(norm_forward_kernel<1, false, ANY>, blocks(a.rows, threads), threads, 0, st, a);
+    return launch_early(norm_forward_kernel<kMost, false, ANY>, blocks(a.rows, threads), threads, 0, st, a);
 }
 
 constexpr int kSharedMost = 222 * 1024;   // dynamic shared memory of a block
@@ -913,9 +926,9 @@ cudaError_t launch_norm_forward(const NormForward& a, int sms, cudaStream_t st) 
             RING(4, 256) RING(5, 256) RING(6, 256) RING(4, 512)
 #undef RING
         }
-        if (a.cols <= 4096 * 8) return run_forward<false>(a, a.cols / 8, st);
+        if (a.cols <= 4096 * 8) return run_forward<false>(a, a.cols / 8, sms, st);
     } else if (a.cols <= 2048 * 8) {
-        return run_forward<true>(a, (a.cols + 7) / 8, st);
+        return run_forward<true>(a, (a.cols + 7) / 8, sms, st);
     }
     return launch_early(norm_forward_wide_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t(1) << 30))), 1024, 0, st, a);
 }
