@@ -23,7 +23,11 @@ struct Mat {
 // Every kernel of the block operators is launched so that its start may overlap
 // the end of the kernel before it (programmatic stream serialization): it lets
 // the kernel after it start early (starts_early), and touches memory only
-// after everything before it in the stream is complete (after_previous).
+// after everything before it in the stream is complete (after_previous).  Such a
+// kernel's lifetime covers the end of the kernel that writes its inputs, so its
+// loads are ordinary ones: the non-coherent path (__ldg, ld.global.nc, const
+// __restrict__ parameters) is for data that nobody writes while the kernel lives,
+// and a line it left in an SM's cache may be older than the wait.
 template <typename... Params, typename... Args>
 cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t shared, cudaStream_t st, const Args&... args) {
     cudaLaunchConfig_t cfg{};

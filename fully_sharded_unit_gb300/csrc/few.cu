@@ -55,18 +55,18 @@ __device__ __forceinline__ void sums_by_columns(const Product& p, int64_t n0, in
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if constexpr (V == 8)
-                w8[i] = k + i < k1 && n < p.N ? __ldg(reinterpret_cast<const uint4*>(W + (k + i) * p.b.ld + n)) : make_uint4(0, 0, 0, 0);
+                w8[i] = k + i < k1 && n < p.N ? *reinterpret_cast<const uint4*>(W + (k + i) * p.b.ld + n) : make_uint4(0, 0, 0, 0);
             else
-                w1[i] = k + i < k1 && n < p.N ? __ldg(W + (k + i) * p.b.ld + n) : uint16_t(0);
+                w1[i] = k + i < k1 && n < p.N ? W[(k + i) * p.b.ld + n] : uint16_t(0);
         }
 #pragma unroll
         for (int t = 0; t < T; ++t) {
             float x[8];
             if (t < p.M && V == 8 && k + 8 <= k1) {
-                unpack8(__ldg(reinterpret_cast<const uint4*>(X + t * p.a.ld + k)), x);
+                unpack8(*reinterpret_cast<const uint4*>(X + t * p.a.ld + k), x);
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = t < p.M && k + i < k1 ? bf(__ldg(X + t * p.a.ld + k + i)) : 0.0f;
+                for (int i = 0; i < 8; ++i) x[i] = t < p.M && k + i < k1 ? bf(X[t * p.a.ld + k + i]) : 0.0f;
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -112,7 +112,7 @@ __device__ __forceinline__ void sums_by_rows(const Product& p, int64_t n0, int64
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int64_t n = n0 + warp * 4 + j, kk = k + u * 256;
-                    w[u][j] = n < p.N && kk + 8 <= k1 ? __ldg(reinterpret_cast<const uint4*>(W + n * p.b.ld + kk))
+                    w[u][j] = n < p.N && kk + 8 <= k1 ? *reinterpret_cast<const uint4*>(W + n * p.b.ld + kk)
                                                       : load_end(W + n * p.b.ld + kk, n < p.N ? k1 - kk : 0);
                 }
 #pragma unroll
@@ -122,7 +122,7 @@ __device__ __forceinline__ void sums_by_rows(const Product& p, int64_t n0, int64
                     const int64_t kk = k + u * 256;
                     const uint16_t* src = X + t * p.a.ld + kk;
                     float x[8];
-                    unpack8(t < p.M && kk + 8 <= k1 ? __ldg(reinterpret_cast<const uint4*>(src))
+                    unpack8(t < p.M && kk + 8 <= k1 ? *reinterpret_cast<const uint4*>(src)
                                                     : load_end(src, t < p.M ? k1 - kk : 0), x);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -140,11 +140,11 @@ __device__ __forceinline__ void sums_by_rows(const Product& p, int64_t n0, int64
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int64_t n = n0 + warp * 4 + j;
-                w[j] = n < p.N ? bf(__ldg(W + n * p.b.ld + k)) : 0.0f;
+                w[j] = n < p.N ? bf(W[n * p.b.ld + k]) : 0.0f;
             }
 #pragma unroll
             for (int t = 0; t < T; ++t) {
-                const float x = t < p.M ? bf(__ldg(X + t * p.a.ld + k)) : 0.0f;
+                const float x = t < p.M ? bf(X[t * p.a.ld + k]) : 0.0f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[t][j] = fmaf(x, w[j], acc[t][j]);
             }

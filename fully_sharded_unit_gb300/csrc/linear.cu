@@ -707,9 +707,9 @@ __global__ void __launch_bounds__(256) align_rows_kernel(int64_t rows, int64_t c
         const int64_t c = (i - row * chunks) * 8;
         const uintptr_t from = reinterpret_cast<uintptr_t>(src.p) + (row * src.ld + c) * 2;
         const uintptr_t word = from & ~uintptr_t(15);
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(word));
+        const uint4 a = *reinterpret_cast<const uint4*>(word);
         uint4 b = make_uint4(0, 0, 0, 0);
-        if (from != word && word + 16 < end) b = __ldg(reinterpret_cast<const uint4*>(word + 16));
+        if (from != word && word + 16 < end) b = *reinterpret_cast<const uint4*>(word + 16);
         const uint32_t shift = static_cast<uint32_t>(from & 2) * 8;
         uint4 o;
         switch ((from >> 2) & 3) {
