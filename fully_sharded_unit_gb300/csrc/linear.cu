@@ -779,13 +779,14 @@ cudaError_t make_map(CUtensorMap* map, const Mat& m, int64_t rows, int64_t cols,
 //
 // Long sums: the tensor cores cut an accumulator off to 24 bits with every 16
 // products (measured: a relative error of 1.1e-9 k for random signs, 4.4e-6 at
-// k = 4096), which an F32 result would show.  So where one is asked for and a
-// cluster's k is above kSlice stages (768), the accumulator is emptied every
-// kSlice stages and the slices are added in fp32, rounded to nearest: an error of
-// 7.3e-7 at any k.  The running sums need tensor memory, which leaves tiles of at
-// most 160 columns: 8192 x 4608 x 4608 at 1610 TFLOP/s against 1700 uncut, 1630
-// with slices of 1024 (1.0e-6), 1655 with 2048 (2.1e-6), 1570 with 512 (4.7e-7);
-// 1031 x 1283 x 5121 in 42.2 us (5.0e-7) against 38.3 uncut (1.0e-6).
+// k = 4096), which an F32 result would show, and an 8-bit checkpoint by a whole
+// step.  So where one is asked for and a cluster's k is above kSlice stages (768),
+// it is taken in slices of equal length of at most as many, which are added in
+// fp32, rounded to nearest: an error of 7.3e-7 for random signs.  The running sums
+// need tensor memory, which leaves tiles of at most 160 columns: 8192 x 4608 x 4608
+// at 1610 TFLOP/s against 1700 uncut, 1630 with slices of 1024 (1.0e-6), 1655 with
+// 2048 (2.1e-6), 1570 with 512 (4.7e-7); 4096 x 1280 -> 5120 with GELU and
+// checkpoint in 46 us against 41 uncut.
 constexpr int kSlice = 12;
 
 Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, bool exact_sums, int clusters) {
@@ -811,10 +812,10 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, bool ex
             p.whole = static_cast<uint32_t>(p.parts > 1 ? tiles - left : tiles);
             p.units = static_cast<uint32_t>(p.whole + (tiles - p.whole) * p.parts);
             const int deepest = p.whole > 0 ? p.ks : (p.ks + p.parts - 1) / p.parts;
-            const bool sliced = exact_sums && deepest > kSlice;
-            if (sliced && bn > 160) continue;
-            p.slice = sliced ? kSlice : 0x40000000;
-            p.buffer = sliced ? bn : 256;
+            const int slices = exact_sums ? (deepest + kSlice - 1) / kSlice : 1;
+            if (slices > 1 && bn > 160) continue;
+            p.slice = slices > 1 ? (deepest + slices - 1) / slices : 0x40000000;   // of equal length
+            p.buffer = slices > 1 ? bn : 256;
             const double rounds = static_cast<double>((p.whole + clusters - 1) / clusters);
             double t = rounds * (std::max(steps * stage, 400.0 + 13.0 * bn) + 300.0) + 13.0 * bn;
             if (p.parts > 1) t += (p.ks + p.parts - 1) / p.parts * stage + 9000.0 + 60.0 * p.parts;
@@ -913,8 +914,9 @@ cudaError_t launch_product(const Product& given, const ProductRoom& room, int sm
         std::swap(p.a_trans, p.b_trans);
         std::swap(rows, cols);
     }
-    const bool f32 = p.out.dtype == FSDP_DTYPE_F32 || (!p.slope && p.pre.p != nullptr && p.pre.dtype == FSDP_DTYPE_F32);
-    Plan pl = plan_product(rows, cols, p.K, p.b_trans, f32, clusters);
+    // a kept checkpoint's values are rounded to 8 bits from the sums: those of an F32 result
+    const bool exact = p.out.dtype == FSDP_DTYPE_F32 || (!p.slope && p.pre.p != nullptr && p.pre.dtype != FSDP_DTYPE_BF16);
+    Plan pl = plan_product(rows, cols, p.K, p.b_trans, exact, clusters);
     pl.swapped = swap;
     pl.vec = swap ? 0 : vec;
     pl.partials = room.partials;

@@ -1,0 +1,51 @@
+"""How exactly the linear layer adds up: sums of one sign, in which an
+accumulator that cuts off instead of rounding errs the same way in every step."""
+import pytest
+import torch
+
+from fully_sharded_unit_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from conftest import library
+    library()
+
+
+def _positive(gen, rows, cols):
+    """Values in (0, 2), every row by a factor of its own in [1, 2), so that sums
+    of products lie anywhere between two powers of two."""
+    out = torch.empty((rows, cols), dtype=BF, device="cuda")
+    factor = 1 + torch.rand((rows, 1), device="cuda", generator=gen)
+    step = max(1, (1 << 27) // rows)
+    for c in range(0, cols, step):
+        part = out[:, c:c + step]
+        part.copy_(torch.rand(part.shape, device="cuda", generator=gen) * factor)
+    return out
+
+
+def test_a_kept_checkpoint_comes_from_sums_as_exact_as_fp32_results():
+    """z is known to ez, the error that an F32 result of these products may have
+    (slices of 768 products are 48 steps, each off by at most a unit of 2^-23; the
+    slices' additions round to nearest), so a kept element lies within half a step
+    and ez of the exact sum.  Cut off in each of 2500 steps without slices, the sums
+    put elements near a boundary beyond it."""
+    T, I, O_ = 300, 40000, 8192
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    x, w = _positive(gen, T, I), _positive(gen, O_, I)
+    c = B.Compute(B.fsdp_linear_workspace_bytes(T, I, O_))
+    k, y, v = B.Act8(T, O_), torch.empty((T, O_), dtype=BF, device="cuda"), torch.empty((T, O_), device="cuda")
+    c.linear_forward(x, w, y, preact=k, weight_layout="out_in")
+    c.act8_unpack(k, v)
+    assert c.status() == 0
+    c.close()
+    z = torch.cat([x.double() @ part.double().t() for part in w.split(1024)], dim=1)
+    ez = (48 * 2.0 ** -23 + (I / 768 + 20) * 2.0 ** -24) * z
+    step = torch.exp2(k.exps.double() - 133).repeat_interleave(32, dim=1)
+    off = (v.double() - z).abs()
+    allowed = torch.where(z + ez >= 127 * step, step, step / 2) + ez
+    assert bool((off <= allowed).all()), ((off - allowed) / step).max().item()
