@@ -216,7 +216,9 @@ struct Plan {
     int bn;                    // columns of a tile: 32 .. 256 in steps of 32
     int stages, stage_b;       // stages in the ring, and B's bytes in one, per CTA
     int slice;                 // stages after which the sums leave the tensor cores' accumulator
-    int buffer;                // columns of tensor memory between the two accumulators
+    int two;                   // 1: two accumulators in turn, so that an epilogue runs beside the next products; 0: one
+    int buffer;                // columns of tensor memory between the two
+    int running;               // the column where the running sums of slices start
     int tiles_m, tiles_n;
     uint32_t whole;            // tiles done by one cluster each
     uint32_t units;            // whole + (tiles - whole) * parts
@@ -415,8 +417,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const Unit un = unit_of(pl, u);
             for (int first = un.k0; first < un.k1 && ok; first += pl.slice, ++tile) {
                 const int end = min(un.k1, first + pl.slice);
-                const uint32_t buf = tile & 1u, d = tmem + buf * pl.buffer;
-                if (tile >= 2 && !bar_wait_warp(tmem_empty0 + buf * 8, (tile / 2 - 1) & 1u, pl.wait_cycles, abort)) {
+                const uint32_t buf = tile & pl.two, turn = tile >> pl.two, d = tmem + buf * pl.buffer;
+                if (turn > 0 && !bar_wait_warp(tmem_empty0 + buf * 8, (turn - 1) & 1u, pl.wait_cycles, abort)) {
                     ok = false;
                     break;
                 }
@@ -481,18 +483,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (i < c1 - c0 && n < p.N) bias[i] = load1(p.bias, p.bias_dtype, n);
                 }
             }
-            // the slices of a long sum but the last are added up in tensor memory;
-            // the whole warp goes on or none of it
-            const uint32_t sliced = tmem + 2 * pl.buffer + (static_cast<uint32_t>(quad * 32) << 16);
-            uint32_t buf = tile & 1u, src = 0;
+            // the slices of a long sum are added up in tensor memory, but the last one
+            // where there are two accumulators: where there is one, it has to be free
+            // before the epilogue's long part begins, which then reads the running
+            // sums.  The whole warp goes on or none of it.
+            const uint32_t sliced = tmem + pl.running + (static_cast<uint32_t>(quad * 32) << 16);
+            uint32_t buf = 0, src = 0;
             bool given_up = false;
             for (int first = un.k0;; first += pl.slice, ++tile) {
-                buf = tile & 1u;
+                buf = tile & pl.two;
                 src = tmem + buf * pl.buffer + (static_cast<uint32_t>(quad * 32) << 16);
-                given_up = !bar_wait_warp(smem_addr(&bars->tmem_full[buf]), (tile / 2) & 1u, pl.wait_cycles, abort);
+                given_up = !bar_wait_warp(smem_addr(&bars->tmem_full[buf]), (tile >> pl.two) & 1u, pl.wait_cycles, abort);
                 if (given_up) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                if (first + pl.slice >= un.k1) break;
+                const bool last = first + pl.slice >= un.k1;
+                if (last && pl.two) break;
                 for (int c = c0; c < c1; ++c) {
                     float v[32];
                     tmem_load32(src + c * 32, v);
@@ -507,6 +512,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) bar_arrive_remote(remote_addr(smem_addr(&bars->tmem_empty[buf]), 0));
+                if (last) break;
             }
             if (given_up) {
                 if (lane == 0) atomicOr(pl.status, FSDP_KSTATUS_WAIT_TIMEOUT);
@@ -515,17 +521,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             // a tile shared along k leaves its sums in the workspace, for finish_kernel
             float4* sums = un.shared < 0 ? nullptr : pl.sums(un.shared, un.part, static_cast<int>(rank) * kEpiWarps + w) + lane;
+            const bool joins = pl.two && un.k1 - un.k0 > pl.slice;
+            if (!pl.two) src = sliced;
             uint32_t bytes = 0;   // exponents of this warp's chunks of the lane's row
             for (int c = c0; c < c1; ++c) {
                 float v[32];
                 tmem_load32(src + c * 32, v);
-                if (un.k1 - un.k0 > pl.slice) {
+                if (joins) {
                     float w[32];
                     tmem_load32(sliced + c * 32, w);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] += w[j];
                 }
-                if (c + 1 == c1) {
+                if (c + 1 == c1 && pl.two) {
                     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) bar_arrive_remote(remote_addr(smem_addr(&bars->tmem_empty[buf]), 0));
@@ -555,7 +563,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         p.pre.e[(row0 + r) * p.pre.eld + group] = static_cast<uint8_t>(w >> (8 * i));
                 }
             }
-            if (c0 >= c1 && lane == 0) bar_arrive_remote(remote_addr(smem_addr(&bars->tmem_empty[buf]), 0));
+            if (c0 >= c1 && pl.two && lane == 0) bar_arrive_remote(remote_addr(smem_addr(&bars->tmem_empty[buf]), 0));
         }
     }
 
@@ -777,19 +785,33 @@ cudaError_t make_map(CUtensorMap* map, const Mat& m, int64_t rows, int64_t cols,
 // copies take at 75 bytes a cycle an SM (32 KiB: 442), and 275 at least; a
 // tile's epilogue 13 a column.
 //
-// Long sums: the tensor cores cut an accumulator off to 24 bits with every 16
-// products (measured: a relative error of 1.1e-9 k for random signs, 4.4e-6 at
-// k = 4096), which an F32 result would show, and an 8-bit checkpoint by a whole
-// step.  So where one is asked for and a cluster's k is above kSlice stages (768),
-// it is taken in slices of equal length of at most as many, which are added in
-// fp32, rounded to nearest: an error of 7.3e-7 for random signs.  The running sums
-// need tensor memory, which leaves tiles of at most 160 columns: 8192 x 4608 x 4608
-// at 1610 TFLOP/s against 1700 uncut, 1630 with slices of 1024 (1.0e-6), 1655 with
-// 2048 (2.1e-6), 1570 with 512 (4.7e-7); 4096 x 1280 -> 5120 with GELU and
-// checkpoint in 46 us against 41 uncut.
+// Long sums: in every step of 16 products the tensor cores cut what they add off
+// below the accumulator's last bits.  Measured, in units of 2^-23 of the running
+// sum a step: products of random signs err by 1.1e-9 k in all; products of one
+// sign and size by 0.2 units at k = 768 and 0.75 at 300000, all one way; small
+// products on one large sum by 2.3, at most 3.8.  So a cluster's k is taken in
+// slices of equal length, at whose ends the accumulator is emptied and added to
+// the running sums in fp32, rounded to nearest.
+//
+// F32 results, and 8-bit checkpoints, whose rounding shows an error of the sums
+// by a whole step: at most kSlice stages (768).  Random signs err by 7.3e-7 at any
+// k, products of one sign by 1.3e-6.  The running sums need tensor memory, which
+// leaves two accumulators of at most 160 columns: 8192 x 4608 x 4608 at 1610
+// TFLOP/s against 1700 uncut, 1630 with slices of 1024 (1.0e-6 for random signs),
+// 1655 with 2048 (2.1e-6), 1570 with 512 (4.7e-7); 4096 x 1280 -> 5120 with GELU
+// and checkpoint in 46 us against 41 uncut.
+//
+// BF16 results: at most kSliceBf16 stages (16384), so that a drift of one way stays
+// near 1e-4, where BF16's own rounding is up to 2^-8 (uncut, it reached 1.7e-3 at
+// k = 300000).  There a tile is as wide as it would be uncut, with one accumulator
+// beside its running sums: the products wait while a slice's sums are taken.  4096
+// x 49152 -> 12288: 2864 us against 2846 uncut; with two accumulators and tiles of
+// 160 columns, 3335.  Slices of 8192 cost 25 us more.
 constexpr int kSlice = 12;
+constexpr int kSliceBf16 = 256;
+constexpr int kSlicedTwice = 160;   // columns of tensor memory that hold two accumulators and the running sums
 
-Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, bool exact_sums, int clusters) {
+Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, int longest, int clusters) {
     Plan best{};
     double least = 0;
     for (int bn = 256; bn >= 32; bn -= 32) {
@@ -812,12 +834,15 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, bool ex
             p.whole = static_cast<uint32_t>(p.parts > 1 ? tiles - left : tiles);
             p.units = static_cast<uint32_t>(p.whole + (tiles - p.whole) * p.parts);
             const int deepest = p.whole > 0 ? p.ks : (p.ks + p.parts - 1) / p.parts;
-            const int slices = exact_sums ? (deepest + kSlice - 1) / kSlice : 1;
-            if (slices > 1 && bn > 160) continue;
+            const int slices = (deepest + longest - 1) / longest;
             p.slice = slices > 1 ? (deepest + slices - 1) / slices : 0x40000000;   // of equal length
-            p.buffer = slices > 1 ? bn : 256;
+            p.two = slices == 1 || bn <= kSlicedTwice;
+            if (!p.two && longest == kSlice) continue;
+            p.buffer = slices > 1 && p.two ? bn : 256;
+            p.running = p.two ? 2 * p.buffer : p.buffer;
             const double rounds = static_cast<double>((p.whole + clusters - 1) / clusters);
-            double t = rounds * (std::max(steps * stage, 400.0 + 13.0 * bn) + 300.0) + 13.0 * bn;
+            const double waits = p.two ? 0.0 : slices * 6.0 * bn;   // the products wait for a slice's sums to be taken
+            double t = rounds * (std::max(steps * stage, 400.0 + 13.0 * bn) + waits + 300.0) + 13.0 * bn;
             if (p.parts > 1) t += (p.ks + p.parts - 1) / p.parts * stage + 9000.0 + 60.0 * p.parts;
             if (least == 0 || t < least) {
                 least = t;
@@ -916,7 +941,7 @@ cudaError_t launch_product(const Product& given, const ProductRoom& room, int sm
     }
     // a kept checkpoint's values are rounded to 8 bits from the sums: those of an F32 result
     const bool exact = p.out.dtype == FSDP_DTYPE_F32 || (!p.slope && p.pre.p != nullptr && p.pre.dtype != FSDP_DTYPE_BF16);
-    Plan pl = plan_product(rows, cols, p.K, p.b_trans, exact, clusters);
+    Plan pl = plan_product(rows, cols, p.K, p.b_trans, exact ? kSlice : kSliceBf16, clusters);
     pl.swapped = swap;
     pl.vec = swap ? 0 : vec;
     pl.partials = room.partials;

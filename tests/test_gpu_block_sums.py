@@ -49,3 +49,31 @@ def test_a_kept_checkpoint_comes_from_sums_as_exact_as_fp32_results():
     off = (v.double() - z).abs()
     allowed = torch.where(z + ez >= 127 * step, step, step / 2) + ez
     assert bool((off <= allowed).all()), ((off - allowed) / step).max().item()
+
+
+@pytest.mark.parametrize("kind", ["forward", "grad_weight"])
+def test_long_bf16_sums_do_not_drift(kind):
+    """The drift may be 2^-13, a thirty-second of BF16's own rounding (up to 2^-8):
+    a unit of 2^-23 of the sum in each of 1024 steps of 16 products.  The rounding
+    is to nearest and the sums lie anywhere, so it averages out over the elements;
+    four deviations of its mean are added.  300000 products in one go are 18750 such
+    steps, and were off by up to 1.7e-3."""
+    T, I, O_ = 300, 300000, 8192
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(2)
+    x, w = _positive(gen, T, I), _positive(gen, O_, I)
+    got = torch.empty((T, O_), dtype=BF, device="cuda")
+    some = slice(0, O_, 32)
+    want = torch.cat([x.double() @ part.double().t() for part in w[some].split(64)], dim=1)
+    if kind == "forward":
+        c = B.Compute(B.fsdp_linear_workspace_bytes(T, I, O_))
+        c.linear_forward(x, w, got, weight_layout="out_in")
+    else:
+        c = B.Compute(B.fsdp_linear_workspace_bytes(I, T, O_))
+        c.linear_grad_weight(x.t().contiguous(), w.t().contiguous(), got)
+    assert c.status() == 0
+    c.close()
+    rel = (got[:, some].double() - want) / want
+    assert rel.abs().max().item() <= 2.0 ** -8 + 2.0 ** -13 + 2.0 ** -18
+    mean = rel.mean().abs().item()
+    assert mean <= 2.0 ** -13 + 4 * 2.0 ** -8 / 3 ** 0.5 / rel.numel() ** 0.5, mean
