@@ -503,24 +503,27 @@ __global__ void __launch_bounds__(THREADS) norm_backward_ring_kernel(const __gri
         __syncwarp();   // the words are other lanes' copies
         const uint32_t* w = words + place * blockDim.x;
         const float mean = __uint_as_float(w[30]), r = __uint_as_float(w[31]);
-        const f32x2 shift = pair(-mean * r, -mean * r);
+        const f32x2 less = pair(-mean, -mean), r2 = pair(r, r);
         const uint8_t* byte = reinterpret_cast<const uint8_t*>(w) + ((exps + row * a.x.eld) & 3u) + (lane >> 2);
-        // x rstd - mean rstd, and dy gamma; a checkpoint's step (a power of two) goes into the factor
+        // x-hat = (x - mean) rstd, and dy gamma.  The difference comes first and is
+        // rounded once (a checkpoint's value, its integer times a power of two, is exact):
+        // x rstd - (mean rstd) would be off by the rounding of mean rstd, which is
+        // thousands of x-hat's own where the mean is thousands of deviations.
         const auto expand = [&](int k, f32x2* x, f32x2* dy, f32x2* g4) {
             f32x2 gm[4];
             gammas.read(0, k, gm);
             dys.read(place, k, dy);
-            float scale = r;
+            f32x2 step2 = 0;
             if (KEPT) {
                 xs.read_ints(place, k, x);
-                scale = r * act8_step(byte[k * 12]);
+                const float step = act8_step(byte[k * 12]);
+                step2 = pair(step, step);
             } else {
                 xs.read(place, k, x);
             }
-            const f32x2 scale2 = pair(scale, scale);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                x[j] = fma2(x[j], scale2, shift);
+                x[j] = mul2(KEPT ? fma2(x[j], step2, less) : add2(x[j], less), r2);
                 g4[j] = mul2(dy[j], gm[j]);
             }
         };
@@ -543,7 +546,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_ring_kernel(const __gri
         flip ^= 1;
         // dx = dy gamma rstd - xh c2 - c1 [+ add]
         const float c1 = -sum.x * inv_n * r, c2 = -sum.y * inv_n * r;
-        const f32x2 r2 = pair(r, r), m1 = pair(c1, c1), m2 = pair(c2, c2);
+        const f32x2 m1 = pair(c1, c1), m2 = pair(c2, c2);
         uint8_t* dx = dxs.first + row * dxs.pitch;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
