@@ -193,9 +193,10 @@ int take_room(fsdp_compute* c, const fsdp::Product& p, int64_t out_features, fsd
 }
 
 int run_product(fsdp_compute* c, const fsdp::Product& p, const fsdp::ProductRoom& r, cudaStream_t st, const char* what) {
-    if (p.M > 0 && p.K > 0) c->withhold_next = 0;
     const cudaError_t e = fsdp::launch_product(p, r, c->sms, st);
-    return e == cudaSuccess ? FSDP_OK : cuda_fail(e, what);
+    if (e != cudaSuccess) return cuda_fail(e, what);
+    if (p.M > 0 && p.N > 0 && p.K > 0 && !fsdp::few_rows(p)) c->withhold_next = 0;   // it ran on staged tiles
+    return FSDP_OK;
 }
 
 }  // namespace
