@@ -178,8 +178,10 @@ int check_linear(int64_t T, int64_t I, int64_t O, int weight_layout) {
     return FSDP_OK;
 }
 
-// Checks the workspace for a product and takes its room from it.
+// Checks the workspace for a product and takes its room from it; products of a
+// few rows use none.
 int take_room(fsdp_compute* c, const fsdp::Product& p, int64_t out_features, fsdp::ProductRoom* r) {
+    if (fsdp::few_rows(p)) return FSDP_OK;
     const int64_t copies = static_cast<int64_t>(
         fsdp::product_copy_bytes(p.a, p.a_trans ? p.K : p.M, p.a_trans ? p.M : p.K) +
         fsdp::product_copy_bytes(p.b, p.b_trans ? p.K : p.N, p.b_trans ? p.N : p.K));

@@ -570,7 +570,8 @@ FSDP_API int fsdp_compute_destroy(fsdp_compute* c);
  * nonzero if W's rows start on 16-byte boundaries (data and ld); otherwise room
  * for an aligned copy of W is counted.  Host only.  A call that needs more than
  * its handle has returns FSDP_E_CAPACITY with the bytes in fsdp_last_error()
- * and enqueues nothing. */
+ * and enqueues nothing.  fsdp_linear_forward and _grad_input of at most 8 tokens
+ * and fsdp_layer_norm_forward need none. */
 FSDP_API int fsdp_layer_norm_workspace_bytes(int64_t rows, int64_t cols, int64_t* bytes);
 FSDP_API int fsdp_linear_workspace_bytes(int64_t tokens, int64_t in_features, int64_t out_features,
                                          int weight_aligned, int64_t* bytes);

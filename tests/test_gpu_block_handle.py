@@ -48,3 +48,26 @@ def test_a_withheld_copy_is_that_of_the_next_staged_product():
     c.linear_forward(x, w, again)
     assert c.status() == 0 and torch.equal(y, again)
     c.close()
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 8])
+@pytest.mark.parametrize("i,o", [(64, 128), (129, 40), (1280, 640)])
+@pytest.mark.parametrize("layout", ["in_out", "out_in"])
+def test_a_few_tokens_need_no_workspace(tokens, i, o, layout):
+    """Aligned or not: the same bits from a handle that has none as from one that
+    has more than enough."""
+    none, plenty = B.Compute(0), B.Compute(64 << 20)
+    x, dy = _normal(i, tokens, i), _normal(o, tokens, o)
+    w = _normal(7, i * o + 1)[1:].view((i, o) if layout == "in_out" else (o, i))
+    got = []
+    for c in (none, plenty):
+        y, dx = torch.empty_like(dy), torch.empty_like(x)
+        c.linear_forward(x, w, y, weight_layout=layout)
+        c.linear_grad_input(dy, w, dx, weight_layout=layout)
+        assert c.status() == 0
+        got.append((y, dx))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    more = _normal(8, 9, i)
+    assert _code(lambda: none.linear_forward(more, w, torch.empty((9, o), dtype=BF, device="cuda"), weight_layout=layout)) == B.FSDP_E_CAPACITY
+    none.close()
+    plenty.close()
