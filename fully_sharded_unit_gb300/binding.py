@@ -565,9 +565,13 @@ class Act8:
         ld, eld = fsdp_act8_layout(self.rows, self.cols)
         self.q = torch.empty((self.rows, ld), dtype=torch.int8, device=device) if q is None else q
         self.exps = torch.empty((self.rows, eld), dtype=torch.uint8, device=device) if exps is None else exps
-        assert self.q.dtype == torch.int8 and tuple(self.q.shape) == (self.rows, ld) and self.q.is_contiguous()
-        assert self.exps.dtype == torch.uint8 and tuple(self.exps.shape) == (self.rows, eld) and self.exps.is_contiguous()
-        assert self.q.is_cuda and self.exps.is_cuda
+        for t, name, dtype, width in ((self.q, "q", torch.int8, ld), (self.exps, "exps", torch.uint8, eld)):
+            if not (t.is_cuda and t.dtype == dtype and tuple(t.shape) == (self.rows, width) and t.is_contiguous()):
+                _refuse(f"{name} of a {self.rows} x {self.cols} checkpoint is a contiguous {dtype} CUDA tensor of "
+                        f"{self.rows} x {width}, not {_about(t)}")
+        self.device = self.q.get_device()
+        if self.exps.get_device() != self.device:
+            _refuse("q and exps of a checkpoint are on one device")
         self.matrix = _pack_matrix(self.q.data_ptr(), self.exps.data_ptr(), self.rows, self.cols, ld, FSDP_DTYPE_ACT8)
 
     @property
@@ -582,46 +586,91 @@ _pack_matrix = struct.Struct("PPqqqi4x").pack
 assert struct.calcsize("PPqqqi4x") == ctypes.sizeof(Matrix)
 
 
-def _mat(t):
-    """fsdp_matrix of a 2-D CUDA tensor whose rows are contiguous, or of an Act8."""
+def _refuse(why):
+    """Arguments that the C side cannot see are checked here, and refused in its way."""
+    raise FsdpError(FSDP_E_INVALID_ARG, "arguments", why)
+
+
+def _about(t):
+    return f"{t.dtype} of {tuple(t.shape)} (strides {tuple(t.stride())}) on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
+
+
+def _dtype(t):
+    dtype = _TORCH_DTYPES.get(t.dtype)
+    if dtype is None:
+        _refuse(f"float32 and bfloat16 are supported, not {t.dtype}")
+    return dtype
+
+
+def _mat(t, device=None):
+    """fsdp_matrix of a 2-D CUDA tensor whose rows are contiguous, or of an Act8;
+    on ``device`` where one is given."""
     if t is None:
         return None
     if t.__class__ is Act8:
+        if device is not None and t.device != device:
+            _refuse(f"a checkpoint on cuda:{t.device} with a handle of cuda:{device}")
         return t.matrix
-    (rows, cols), (ld, one) = t.shape, t.stride()
+    try:
+        (rows, cols), (ld, one) = t.shape, t.stride()
+    except (AttributeError, ValueError):
+        _refuse(f"a matrix is a 2-D tensor or an Act8, not {_about(t)}")
     if rows <= 1:
         ld = cols
-    assert t.is_cuda and (one == 1 or cols <= 1), "a matrix is a CUDA tensor whose rows are contiguous"
-    return _pack_matrix(t.data_ptr(), 0, rows, cols, ld, _TORCH_DTYPES[t.dtype])
+    at = t.get_device()
+    if at < 0 or (one != 1 and cols > 1):
+        _refuse(f"a matrix is a CUDA tensor whose rows are contiguous, not {_about(t)}")
+    if device is not None and at != device:
+        _refuse(f"a matrix on cuda:{at} with a handle of cuda:{device}")
+    return _pack_matrix(t.data_ptr(), 0, rows, cols, ld, _dtype(t))
 
 
-def _vec(t, n):
+def _vec(t, n, device=None):
     """(address, dtype) of a contiguous CUDA vector of n elements."""
-    assert t.is_cuda and t.shape == (n,) and (n <= 1 or t.stride(0) == 1), f"a vector of {n} elements is expected"
-    return t.data_ptr(), _TORCH_DTYPES[t.dtype]
+    at = t.get_device()
+    if at < 0 or t.shape != (n,) or (n > 1 and t.stride(0) != 1) or (device is not None and at != device):
+        _refuse(f"a contiguous vector of {n} elements on the handle's device is expected, not {_about(t)}")
+    return t.data_ptr(), _dtype(t)
 
 
-def _stat(t, n):
-    address, dtype = _vec(t, n)
-    assert dtype == FSDP_DTYPE_F32, "row statistics are float32"
+def _stat(t, n, device=None):
+    address, dtype = _vec(t, n, device)
+    if dtype != FSDP_DTYPE_F32:
+        _refuse("row statistics are float32")
     return address
+
+
+def _same(a, b, names):
+    if a != b:
+        _refuse(f"{names} have one dtype")
+
+
+class ComputeHandle(_P):
+    """An fsdp_compute*, and the device it was created on."""
+    device = None
+
+
+def _device_of(h):
+    """The handle's device; None for a bare pointer, whose device is not known."""
+    return h.device if h.__class__ is ComputeHandle else None
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-def _current(stream):
-    """The stream's address; None: torch's current stream of the current device."""
+def _current(stream, device=None):
+    """The stream's address; None: torch's current stream of the handle's device."""
     if stream is None and _raw_stream is not None and _device is not None:
-        return _raw_stream(_device())
+        return _raw_stream(_device() if device is None else device)
     return _stream(stream)
 
 
 def fsdp_compute_create(workspace_bytes=0, allocator=None):
-    h = _P()
+    h = ComputeHandle()
     a = ctypes.byref(allocator) if allocator is not None else None
     _check(lib().fsdp_compute_create(int(workspace_bytes), a, ctypes.byref(h)), "fsdp_compute_create")
+    h.device = torch.cuda.current_device()
     return h
 
 
@@ -660,59 +709,72 @@ def fsdp_linear_workspace_bytes(tokens, in_features, out_features, weight_aligne
 
 
 def fsdp_layer_norm_forward(h, x, gamma, beta, eps, y, mean, rstd, ckpt=None, stream=None) -> None:
+    d = _device_of(h)
+    xm = _mat(x, d)
     rows, cols = x.shape
-    g, dt = _vec(gamma, cols)
-    b, bt = _vec(beta, cols)
-    assert dt == bt, "gamma and beta have one dtype"
-    _check(lib().fsdp_layer_norm_forward(h, _mat(x), g, b, dt, float(eps), _mat(y), _stat(mean, rows),
-                                         _stat(rstd, rows), _mat(ckpt), _current(stream)), "fsdp_layer_norm_forward")
+    g, dt = _vec(gamma, cols, d)
+    b, bt = _vec(beta, cols, d)
+    _same(dt, bt, "gamma and beta")
+    _check(lib().fsdp_layer_norm_forward(h, xm, g, b, dt, float(eps), _mat(y, d), _stat(mean, rows, d),
+                                         _stat(rstd, rows, d), _mat(ckpt, d), _current(stream, d)), "fsdp_layer_norm_forward")
 
 
 def fsdp_layer_norm_backward(h, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, add=None, accumulate=False,
                              stream=None) -> None:
     """``x``: the forward's input or its ``Act8`` checkpoint."""
+    d = _device_of(h)
+    dym = _mat(dy, d)
     rows, cols = dy.shape
-    g, dt = _vec(gamma, cols)
-    dg, gt = _vec(dgamma, cols)
-    db, bt = _vec(dbeta, cols)
-    assert gt == bt, "dgamma and dbeta have one dtype"
-    _check(lib().fsdp_layer_norm_backward(h, _mat(dy), _mat(x), g, dt, _stat(mean, rows), _stat(rstd, rows),
-                                          _mat(add), _mat(dx), dg, db, gt, 1 if accumulate else 0,
-                                          _current(stream)), "fsdp_layer_norm_backward")
+    g, dt = _vec(gamma, cols, d)
+    dg, gt = _vec(dgamma, cols, d)
+    db, bt = _vec(dbeta, cols, d)
+    _same(gt, bt, "dgamma and dbeta")
+    _check(lib().fsdp_layer_norm_backward(h, dym, _mat(x, d), g, dt, _stat(mean, rows, d), _stat(rstd, rows, d),
+                                          _mat(add, d), _mat(dx, d), dg, db, gt, 1 if accumulate else 0,
+                                          _current(stream, d)), "fsdp_layer_norm_backward")
 
 
 def fsdp_linear_forward(h, x, w, y, bias=None, activation="none", residual=None, preact=None,
                         weight_layout="in_out", stream=None) -> None:
     """``preact``: None, or the tensor or ``Act8`` that receives x W + bias."""
-    b, bt = _vec(bias, y.shape[1]) if bias is not None else (None, FSDP_DTYPE_F32)
-    _check(lib().fsdp_linear_forward(h, _mat(x), _mat(w), WEIGHT_LAYOUTS.get(weight_layout, weight_layout), b, bt,
-                                     ACTIVATIONS.get(activation, activation), _mat(residual), _mat(preact), _mat(y),
-                                     _current(stream)), "fsdp_linear_forward")
+    d = _device_of(h)
+    ym = _mat(y, d)
+    b, bt = _vec(bias, y.shape[1], d) if bias is not None else (None, FSDP_DTYPE_F32)
+    _check(lib().fsdp_linear_forward(h, _mat(x, d), _mat(w, d), WEIGHT_LAYOUTS.get(weight_layout, weight_layout), b, bt,
+                                     ACTIVATIONS.get(activation, activation), _mat(residual, d), _mat(preact, d), ym,
+                                     _current(stream, d)), "fsdp_linear_forward")
 
 
 def fsdp_linear_grad_input(h, dy, w, dx, activation="none", preact=None, add=None, weight_layout="in_out",
                            stream=None) -> None:
-    _check(lib().fsdp_linear_grad_input(h, _mat(dy), _mat(w), WEIGHT_LAYOUTS.get(weight_layout, weight_layout),
-                                        ACTIVATIONS.get(activation, activation), _mat(preact), _mat(add), _mat(dx),
-                                        _current(stream)), "fsdp_linear_grad_input")
+    d = _device_of(h)
+    _check(lib().fsdp_linear_grad_input(h, _mat(dy, d), _mat(w, d), WEIGHT_LAYOUTS.get(weight_layout, weight_layout),
+                                        ACTIVATIONS.get(activation, activation), _mat(preact, d), _mat(add, d), _mat(dx, d),
+                                        _current(stream, d)), "fsdp_linear_grad_input")
 
 
 def fsdp_linear_grad_weight(h, x, dy, dw, dbias=None, weight_layout="in_out", accumulate=False, stream=None) -> None:
     """``x``: the layer's input or its ``Act8`` checkpoint; ``dw`` is stored like the weight."""
-    db, bt = _vec(dbias, dy.shape[1]) if dbias is not None else (None, _TORCH_DTYPES[dw.dtype])
-    assert bt == _TORCH_DTYPES[dw.dtype], "dw and dbias have one dtype"
-    _check(lib().fsdp_linear_grad_weight(h, _mat(x), _mat(dy), WEIGHT_LAYOUTS.get(weight_layout, weight_layout),
-                                         _mat(dw), db, 1 if accumulate else 0, _current(stream)),
+    d = _device_of(h)
+    dym, dwm = _mat(dy, d), _mat(dw, d)
+    db = None
+    if dbias is not None:
+        db, bt = _vec(dbias, dy.shape[1], d)
+        _same(bt, _dtype(dw), "dw and dbias")
+    _check(lib().fsdp_linear_grad_weight(h, _mat(x, d), dym, WEIGHT_LAYOUTS.get(weight_layout, weight_layout),
+                                         dwm, db, 1 if accumulate else 0, _current(stream, d)),
            "fsdp_linear_grad_weight")
 
 
 def fsdp_act8_pack(h, x, ckpt, stream=None) -> None:
-    _check(lib().fsdp_act8_pack(h, _mat(x), _mat(ckpt), _current(stream)), "fsdp_act8_pack")
+    d = _device_of(h)
+    _check(lib().fsdp_act8_pack(h, _mat(x, d), _mat(ckpt, d), _current(stream, d)), "fsdp_act8_pack")
 
 
 def fsdp_act8_unpack(h, ckpt, out, activation="none", stream=None) -> None:
-    _check(lib().fsdp_act8_unpack(h, _mat(ckpt), ACTIVATIONS.get(activation, activation), _mat(out),
-                                  _current(stream)), "fsdp_act8_unpack")
+    d = _device_of(h)
+    _check(lib().fsdp_act8_unpack(h, _mat(ckpt, d), ACTIVATIONS.get(activation, activation), _mat(out, d),
+                                  _current(stream, d)), "fsdp_act8_unpack")
 
 
 class Compute:
