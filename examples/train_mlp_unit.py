@@ -42,14 +42,15 @@ class MlpUnit:
                      torch.empty((d, ffn), device="cuda").normal_(0, std, generator=gen), torch.zeros(ffn, device="cuda"),
                      torch.empty((ffn, d), device="cuda").normal_(0, std, generator=gen), torch.zeros(d, device="cuda")]
         self.unit.load(self.init)
-        # one compute handle for every operator: the larger workspace of the two kinds
-        self.compute = B.Compute(max(B.fsdp_linear_workspace_bytes(tokens, d, ffn),
-                                     B.fsdp_layer_norm_workspace_bytes(tokens, d)))
         bf = torch.bfloat16
         self.gathered = torch.empty(self.unit.numel, dtype=bf, device="cuda")
         gdt = bf if grad_dtype == "bf16" else torch.float32
         self.grads = [torch.empty(self.unit.numel, dtype=gdt, device="cuda") for _ in range(ranks)]
         self.params = self._views(self.gathered)
+        # one compute handle for every operator: the larger workspace of the two kinds
+        weights = (self.params[2], self.params[4])   # pieces of the gathered buffer: they begin where it has them
+        self.compute = B.Compute(max(B.fsdp_linear_workspace_bytes(tokens, d, ffn, weight_aligned=weights),
+                                     B.fsdp_layer_norm_workspace_bytes(tokens, d)))
         self.mean, self.rstd = torch.empty(tokens, device="cuda"), torch.empty(tokens, device="cuda")
         self.wide, self.narrow = (torch.empty((tokens, n), dtype=bf, device="cuda") for n in (ffn, d))
         self.y, self.dx = (torch.empty((tokens, d), dtype=bf, device="cuda") for _ in range(2))

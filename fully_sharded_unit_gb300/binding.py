@@ -696,11 +696,24 @@ def fsdp_layer_norm_workspace_bytes(rows, cols) -> int:
     return n.value
 
 
+def _rows_aligned(t):
+    """Whether the rows of a matrix start on 16-byte boundaries."""
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return (t.data_ptr() | ld * t.element_size()) % 16 == 0
+
+
 def fsdp_linear_workspace_bytes(tokens, in_features, out_features, weight_aligned=None) -> int:
-    """``weight_aligned``: whether the weight's rows start on 16-byte
-    boundaries; None: true when both widths are multiples of 8 elements."""
+    """``weight_aligned``: whether the weight's rows start on 16-byte boundaries;
+    the weight itself (or several, as a list or tuple) may be given instead, which
+    is then looked at.  None goes by the widths: true when both are multiples of 8
+    elements, which says nothing of where a weight begins, so give the weight where
+    it is a piece of a longer buffer."""
     if weight_aligned is None:
         weight_aligned = in_features % 8 == 0 and out_features % 8 == 0
+    elif isinstance(weight_aligned, torch.Tensor):
+        weight_aligned = _rows_aligned(weight_aligned)
+    elif isinstance(weight_aligned, (list, tuple)):
+        weight_aligned = all(_rows_aligned(w) for w in weight_aligned)
     n = ctypes.c_int64()
     _check(lib().fsdp_linear_workspace_bytes(int(tokens), int(in_features), int(out_features),
                                              1 if weight_aligned else 0, ctypes.byref(n)),
