@@ -430,7 +430,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 // z/2 (1 + tanh(u)) = z / (1 + exp(-2u)), u = sqrt(2/pi) (z + 0.044715 z^3):
 // no cancellation for negative z, and exp's overflow gives the limit 0.  Two
 // elements at a time: five packed instructions and four on the special-function
-// units, which bound it (16 lanes a cycle an SM).
+// units, which bound it (16 lanes a cycle an SM).  Rounding: with s = 1 / (1 + e) an
+// error d of e's exponent moves s by s (1 - s) d, at most d/4; exp2's own (2^-22) and
+// that of its argument (2^-24 of it) give 2^-23, the reciprocal's ulp 2^-23 and the
+// last product 2^-24: below 2^-21 |z| together, also where the result is F32.
 __device__ __forceinline__ void gelu_tanh2(float& z0, float& z1) {
     const f32x2 z = pair(z0, z1);
     const f32x2 t = fma2(mul2(z, z), pair(-kLog2e * kGeluK2 * kGeluC, -kLog2e * kGeluK2 * kGeluC),
@@ -441,7 +444,9 @@ __device__ __forceinline__ void gelu_tanh2(float& z0, float& z1) {
     unpair(mul2(z, pair(rcp_fast(a), rcp_fast(b))), z0, z1);
 }
 
-// s + z (s - s^2) (2u)', s = 1 / (1 + exp(-2u)).  z^2 is held at 900 so that it
+// s + z (s - s^2) (2u)', s = 1 / (1 + exp(-2u)).  Where s is an ulp (2^-24) off 1,
+// at |z| up to 5.2, s - s^2 is off by as much and its factor is up to 38: an error
+// of up to 2^-18 there, as in any fp32 form that has s or tanh.  z^2 is held at 900 so that it
 // stays finite: past |z| = 30, s is 0 or 1 exactly.
 __device__ __forceinline__ void gelu_tanh_slope2(float z0, float z1, float& d0, float& d1) {
     const f32x2 z = pair(z0, z1);
@@ -472,6 +477,7 @@ __device__ __forceinline__ float gelu_tanh_slope(float z) {
 
 __device__ __forceinline__ float gelu_erf(float z) { return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f)); }
 
+// __expf: its error, 2^-22 and 2^-23 |z^2/2| of the result, is below 2^-22 of the slope's size.
 __device__ __forceinline__ float gelu_erf_slope(float z) {
     z = min_nan(max_nan(z, -30.0f), 30.0f);
     return fmaf(z * 0.39894228040143268f, __expf(-0.5f * z * z), 0.5f * (1.0f + erff(z * 0.70710678118654752f)));

@@ -527,7 +527,10 @@ FSDP_API int fsdp_host_device_pointer(const void* host, void** dev);
  * 16-byte aligned. */
 #define FSDP_DTYPE_ACT8 2
 
-/* activations of fsdp_linear_forward / _grad_input and fsdp_act8_unpack */
+/* activations of fsdp_linear_forward / _grad_input and fsdp_act8_unpack.  GELU is
+ * evaluated in fp32 (the tanh form with the special-function units' exponential and
+ * reciprocal, subnormal ones taken as 0), for F32 results too: within 2^-21 |z|;
+ * its slope within 2^-17 (measured: 1.4e-7 |z|, and 2e-6). */
 #define FSDP_ACTIVATION_NONE      0
 #define FSDP_ACTIVATION_RELU      1   /* max(z, 0); slope 0 at z = 0; NaN stays NaN      */
 #define FSDP_ACTIVATION_GELU_TANH 2   /* z/2 * (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
