@@ -848,9 +848,10 @@ cudaError_t launch_product(const Product& given, const ProductRoom& room, int sm
         std::swap(p.a_trans, p.b_trans);
         std::swap(rows, cols);
     }
-    // a kept checkpoint's values are rounded to 8 bits from the sums: those of an F32 result
-    const bool exact = p.out.dtype == FSDP_DTYPE_F32 || (!p.slope && p.pre.p != nullptr && p.pre.dtype != FSDP_DTYPE_BF16);
-    Plan pl{plan_product(rows, cols, p.K, p.b_trans, exact, clusters)};
+    const bool keeps = !p.slope && p.pre.p != nullptr;
+    const Sums sums = keeps && p.pre.dtype == FSDP_DTYPE_ACT8 ? Sums::kKept
+                      : p.out.dtype == FSDP_DTYPE_F32 || (keeps && p.pre.dtype == FSDP_DTYPE_F32) ? Sums::kExact : Sums::kRounded;
+    Plan pl{plan_product(rows, cols, p.K, p.b_trans, sums, clusters)};
     pl.swapped = swap;
     pl.vec = swap ? 0 : vec;
     pl.partials = room.partials;

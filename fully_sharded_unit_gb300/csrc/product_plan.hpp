@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 namespace fsdp {
@@ -27,6 +28,9 @@ struct Tiling {
     int parts;                 // clusters that share one of the remaining tiles, along k
 };
 
+// What a product's sums are for: a BF16 result, an F32 one, or an 8-bit checkpoint.
+enum class Sums { kRounded, kExact, kKept };
+
 // Few rows become the tile's columns, so that a tile of 256 is not filled with rows
 // that do not exist.
 inline bool swaps(int64_t M, int64_t N, bool a_trans) { return M <= 256 && N > M && !a_trans; }
@@ -47,13 +51,19 @@ inline bool swaps(int64_t M, int64_t N, bool a_trans) { return M <= 256 && N > M
 // slices of equal length, at whose ends the accumulator is emptied and added to
 // the running sums in fp32, rounded to nearest.
 //
-// F32 results, and 8-bit checkpoints, whose rounding shows an error of the sums
-// by a whole step: at most kSlice stages (768).  Random signs err by 7.3e-7 at any
-// k, products of one sign by 1.3e-6.  The running sums need tensor memory, which
+// F32 results: at most kSlice stages (768).  Random signs err by 7.3e-7 at any k,
+// products of one sign by 1.3e-6.  The running sums need tensor memory, which
 // leaves two accumulators of at most 160 columns: 8192 x 4608 x 4608 at 1610
 // TFLOP/s against 1700 uncut, 1630 with slices of 1024 (1.0e-6 for random signs),
-// 1655 with 2048 (2.1e-6), 1570 with 512 (4.7e-7); 4096 x 1280 -> 5120 with GELU
-// and checkpoint in 46 us against 41 uncut.
+// 1655 with 2048 (2.1e-6), 1570 with 512 (4.7e-7).
+//
+// 8-bit checkpoints: their rounding shows an error of the sums by a whole step, so
+// that twice the error doubles the elements which land on the wrong side.  A slice
+// is also at most 16 sqrt(k) products long (256 at least), which keeps the sums'
+// error within about twice that of fp32 sums in order, 8e-9 sqrt(k) measured.  4096
+// x 1280 -> 5120 with GELU and checkpoint, and its unpacking: 65.4 us with slices of
+// 448, 61.0 with 640, 54.7 uncut; the kept values' error, as a norm, is 1.2, 1.5 and
+// 1.9 times that from fp32 sums.
 //
 // BF16 results: at most kSliceBf16 stages (16384), so that a drift of one way stays
 // near 1e-4, where BF16's own rounding is up to 2^-8 (uncut, it reached 1.7e-3 at
@@ -65,8 +75,15 @@ constexpr int kSlice = 12;
 constexpr int kSliceBf16 = 256;
 constexpr int kSlicedTwice = 160;   // columns of tensor memory that hold two accumulators and the running sums
 
-inline Tiling plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, bool exact, int clusters) {
-    const int longest = exact ? kSlice : kSliceBf16;
+// Stages of a slice, at most.
+inline int longest_slice(int64_t k, Sums sums) {
+    if (sums == Sums::kRounded) return kSliceBf16;
+    if (sums == Sums::kExact) return kSlice;
+    return std::min(kSlice, std::max(4, static_cast<int>(std::sqrt(static_cast<double>(k)) * 16 / kDepth)));
+}
+
+inline Tiling plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows, Sums sums, int clusters) {
+    const int longest = longest_slice(k, sums);
     Tiling best{};
     double least = 0;
     for (int bn = 256; bn >= 32; bn -= 32) {
@@ -92,11 +109,13 @@ inline Tiling plan_product(int64_t rows, int64_t cols, int64_t k, bool b_by_rows
             const int slices = (deepest + longest - 1) / longest;
             p.slice = slices > 1 ? (deepest + slices - 1) / slices : 0x40000000;   // of equal length
             p.two = slices == 1 || bn <= kSlicedTwice;
-            if (!p.two && longest == kSlice) continue;
+            if (!p.two && sums != Sums::kRounded) continue;
             p.buffer = slices > 1 && p.two ? bn : 256;
             p.running = p.two ? 2 * p.buffer : p.buffer;
             const double rounds = static_cast<double>((p.whole + clusters - 1) / clusters);
-            const double waits = p.two ? 0.0 : slices * 6.0 * bn;   // the products wait for a slice's sums to be taken
+            // a slice's sums: the products wait while they are taken where there is one
+            // accumulator, and for an epilogue that has a checkpoint to keep besides
+            const double waits = !p.two ? slices * 6.0 * bn : sums == Sums::kKept ? (slices - 1) * 1000.0 : 0.0;
             double t = rounds * (std::max(steps * stage, 400.0 + 13.0 * bn) + waits + 300.0) + 13.0 * bn;
             if (p.parts > 1) t += (p.ks + p.parts - 1) / p.parts * stage + 9000.0 + 60.0 * p.parts;
             if (least == 0 || t < least) {

@@ -507,11 +507,12 @@ FSDP_API int fsdp_host_device_pointer(const void* host, void** dev);
  * in steps of 16 products: measured, up to 4 units of 2^-23 of it a step where
  * small products meet a large sum, 1 where they are of one size, and 1.1e-9 of
  * the result for each product of random signs.  So sums are taken in slices, which
- * are added with rounding: at most 768 products where the result is F32 or kept as
- * ACT8, 16384 where it is BF16.  An F32 result's error, of the sum of the products'
- * magnitudes, is then within 48 steps' cuts and 2^-24 * (k/768 + 20) for the
- * slices; measured at k = 768 to 7680: 7e-7 of the result for random signs,
- * 1.3e-6 for one sign, 1.3e-5 with one product far larger than the rest.)
+ * are added with rounding: at most 768 products where the result is F32, 768 and
+ * 16 sqrt(k) where it is kept as ACT8, 16384 where it is BF16.  An F32 result's
+ * error, of the sum of the products' magnitudes, is then within 48 steps' cuts and
+ * 2^-24 * (k/768 + 20) for the slices; measured at k = 768 to 7680: 7e-7 of the
+ * result for random signs, 1.3e-6 for one sign, 1.3e-5 with one product far larger
+ * than the rest.)
  * Results do not depend on the stream, the device's load or earlier calls. */
 
 /* An 8-bit activation checkpoint: fsdp_matrix.dtype of matrices whose `data`

@@ -42,17 +42,18 @@ class Plan(dict):
 
 
 def plans(products, clusters=CLUSTERS):
-    """``products``: (M, N, K, a_trans, b_trans, exact)."""
+    """``products``: (M, N, K, a_trans, b_trans, sums), sums 0 for a BF16 result, 1
+    for an F32 one, 2 for an 8-bit checkpoint."""
     text = "".join("%d %d %d %d %d %d %d\n" % (*(int(v) for v in p), clusters) for p in products)
     out = subprocess.run([_program()], input=text, capture_output=True, text=True, check=True).stdout
     return [Plan((k, int(v)) for k, v in (f.split("=") for f in line.split())) for line in out.splitlines()]
 
 
-def of(kind, T, I, O, layout, exact):
+def of(kind, T, I, O, layout, sums):
     """The plan of one of the linear layer's products."""
     io = layout == "in_out"
-    p = {"forward": (T, O, I, 0, io, exact), "grad_input": (T, I, O, 0, not io, exact),
-         "grad_weight": ((I, O) if io else (O, I)) + (T, 1, 1, exact)}[kind]
+    p = {"forward": (T, O, I, 0, io, sums), "grad_input": (T, I, O, 0, not io, sums),
+         "grad_weight": ((I, O) if io else (O, I)) + (T, 1, 1, sums)}[kind]
     return plans([p])[0]
 
 

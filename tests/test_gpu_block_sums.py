@@ -103,3 +103,33 @@ def test_fp32_sums_are_as_exact_as_the_header_states(data, stated, k):
     want = x.double() @ w.double().t()
     off = ((y.double() - want).norm() / want.norm()).item()
     assert off <= 2 * stated, off
+
+
+@pytest.mark.parametrize("k", [256, 512, 768, 1280, 3000])
+def test_a_kept_checkpoint_of_random_signs(k):
+    """Elements land on the wrong side of a rounding boundary in proportion to the
+    sums' error, which slices keep within about twice that of fp32 sums (measured
+    ones: 8e-9 sqrt(k) of the result).  As a norm, where each of these is one step
+    off, the kept values' error is then within sqrt(2), and 1.5 with what the
+    sample of a few thousand of them adds, of that from fp32 sums."""
+    T, O_ = 4096, 2560
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    x, w = (torch.empty((n, k), device="cuda").normal_(generator=gen).to(BF) for n in (T, O_))
+    c = B.Compute(B.fsdp_linear_workspace_bytes(T, k, O_))
+    kept, y, v = B.Act8(T, O_), torch.empty((T, O_), dtype=BF, device="cuda"), torch.empty((T, O_), device="cuda")
+    c.linear_forward(x, w, y, preact=kept, weight_layout="out_in")
+    c.act8_unpack(kept, v)
+    assert c.status() == 0
+    c.close()
+
+    def quantised(z):
+        top = z.unflatten(1, (-1, 32)).abs().amax(dim=2, keepdim=True)
+        step = torch.exp2(torch.floor(torch.log2(top)) - 6)
+        return ((z.unflatten(1, (-1, 32)) / step).round().clamp(-127, 127) * step).flatten(1)
+
+    z = x.double() @ w.double().t()
+    exact = quantised(z)
+    noise = 8e-9 * k ** 0.5 * z.square().mean().sqrt() * torch.empty_like(z).normal_(generator=gen)
+    off = lambda a: ((a - exact).norm() / exact.norm()).item()  # noqa: E731
+    assert off(v.double()) <= 1.5 * off(quantised(z + noise)), (off(v.double()), off(quantised(z + noise)))

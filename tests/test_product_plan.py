@@ -21,7 +21,7 @@ def _sound(q, p, clusters):
     assert p.two in (0, 1) and p.buffer >= p.bn
     assert (p.running + p.bn if sliced or not p.two else (p.two * p.buffer + p.bn)) <= 512
     assert p.running >= p.buffer * (1 + p.two)
-    longest = 12 if q[5] else 256
+    longest = (256, 12, max(4, min(12, int(K ** 0.5 / 4))))[q[5]]
     assert p.deepest <= longest and p.slice == UNCUT or p.slice <= longest and p.slices == -(-p.deepest // longest)
     assert p.two or not q[5]
 
@@ -29,8 +29,8 @@ def _sound(q, p, clusters):
 def test_any_plan_is_sound():
     rng = random.Random(1)
     size = lambda hi: int(2 ** rng.uniform(0, hi))  # noqa: E731
-    asked = [(size(15), size(15), size(19), rng.random() < 0.3, rng.random() < 0.5, rng.random() < 0.5) for _ in range(4000)]
-    asked += [(*p, a, b, e) for p in PRODUCTS for a, b in ((0, 0), (0, 1), (1, 1)) for e in (0, 1)]
+    asked = [(size(15), size(15), size(19), rng.random() < 0.3, rng.random() < 0.5, rng.randrange(3)) for _ in range(4000)]
+    asked += [(*p, a, b, e) for p in PRODUCTS for a, b in ((0, 0), (0, 1), (1, 1)) for e in (0, 1, 2)]
     for clusters in (CLUSTERS, 70, 1):
         for q, p in zip(asked, plans(asked, clusters)):
             _sound(q, p, clusters)
@@ -39,7 +39,7 @@ def test_any_plan_is_sound():
 def test_the_shapes_of_the_gpu_tests_reach_every_path():
     """forward and grad_input call both orders of B's memory, with every type of
     result; what each of them has to have met."""
-    asked = [(*p, 0, b, e) for p in PRODUCTS for b in (0, 1) for e in (0, 1)]
+    asked = [(*p, 0, b, e) for p in PRODUCTS for b in (0, 1) for e in (0, 1, 2)]
     met = list(zip(asked, plans(asked)))
     have = lambda f: [q for q, p in met if f(q, p)]  # noqa: E731
     alignment = lambda q: 0 if q[1] % 8 else 2 if q[1] % 16 == 0 else 1  # noqa: E731
