@@ -1,6 +1,5 @@
-// 8-bit activation checkpoints: pack (quantise) and unpack.  Streaming passes,
-// bound by DRAM: pack reads 2 or 4 bytes and writes 33/32 byte an element,
-// unpack the reverse.
+// 8-bit activation checkpoints: pack (quantise) and unpack.  Streaming passes:
+// pack reads 2 or 4 bytes and writes 33/32 byte an element, unpack the reverse.
 #include <algorithm>
 
 #include "block_device.cuh"
@@ -15,7 +14,8 @@ namespace {
 // are whole sectors.  The payload's rows and the exponents' are contiguous
 // (their strides are the format's), so a group's place in them is its index.
 // 8192 x 5120: pack 24.5 us (5.2 TB/s), unpack with GELU 28 (4.5; the special
-// functions take half of it); 4096 x 12288: unpack 27 (5.7).
+// functions take half of it); 4096 x 12288: unpack 27 (5.7).  DRAM is half busy, by
+// ncu, with 31 % of the warps that an SM can hold: what is in flight bounds them.
 // ANY: x's rows start anywhere and are read and stored as the 16-byte words that
 // hold them (4096 x 1281: pack 11 us, unpack 11; an element to a lane took 27).
 template <bool WIDE, bool ANY, bool PACK>

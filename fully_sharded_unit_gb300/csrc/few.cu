@@ -1,8 +1,9 @@
 // Products of a few rows: y = x W for one to eight tokens, and the same for an
-// input gradient.  W is read once, so DRAM bounds them; no tile of the tensor
-// cores could be filled.  One token, 1280 -> 5120 (13 MB of W, from DRAM):
-// 10.3 us alone and cold, 6.7 a call in a stream of them, which the launching host
-// bounds; by the tensor cores, 64 tokens take 7.5.
+// input gradient.  W is read once; no tile of the tensor cores could be filled.
+// One token, 1280 -> 5120: 10.3 us alone and cold, where 13 MB of W from DRAM take
+// 1.9 and a launch two more: two dependent steps of loads bound it, the second a
+// quarter full.  7.0 a call in a stream of them that finds W in L2, which the
+// launching host bounds; by the tensor cores, 64 tokens take 7.5.
 //
 // A block computes 32 columns (a checkpoint's group), a cluster of up to 8
 // blocks splits k where the columns alone would leave SMs idle, and the first

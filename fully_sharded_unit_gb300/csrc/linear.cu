@@ -33,11 +33,11 @@ namespace {
 //
 // What bounds it: the tensor cores where k and the tiles are many (8192 x 8192 x
 // 8192 in BF16: 1980 TFLOP/s, the rate of the library's product there; for
-// seconds on end, the power limit: 1740), the SMs' ports from L2 where the
-// epilogue's traffic meets the copies (4096 x 1280 -> 5120: 32.5 us, 1650
-// TFLOP/s, plain; 40 with bias, GELU and an 8-bit checkpoint kept; 42.5 with a
-// residual; 46 for an input gradient with GELU's slope from a checkpoint), and
-// the latency of one tile where there are few (64 x 1280 -> 5120: 7.5 us).
+// seconds on end, the power limit: 1740), an epilogue that takes as long as a
+// tile's products where k is short (4096 x 1280 -> 5120: 32.5 us, 1650 TFLOP/s,
+// plain; 49 with bias, GELU and an 8-bit checkpoint kept, whose sums are cut three
+// times; 42.5 with a residual; 46 for an input gradient with GELU's slope from a
+// checkpoint; by ncu its latencies, with no unit over 60 % busy), and the latency of one tile where there are few (64 x 1280 -> 5120: 7.5 us).
 // Pairs of CTAs, since a pair halves B's copies; tiles as wide as tensor memory
 // holds twice, since a tile's copies for a product fall with its width; one
 // persistent pair to two SMs, so that an epilogue runs beside the next tile.
@@ -588,9 +588,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // Column sums of dy: V columns to a thread (8 from a 16-byte boundary, or 1),
 // 32 threads across and 8 slices of rows down to a block, which joins them and
 // leaves one row of sums, for sum_partials_kernel to add in order (atomics'
-// order would change results).  Bound by DRAM and, in short matrices, by the
-// latency of a thread's loads, of which eight are in flight: 2048 x 49152 in 43
-// us (4.7 TB/s), 4096 x 1280 in 6.
+// order would change results).  Bound by the latency of a thread's loads, of which
+// eight are in flight: 2048 x 49152 in 43 us (4.7 TB/s), 4096 x 5120 in 13 (3.2),
+// 4096 x 1280 in 6.
 template <int V>
 __global__ void __launch_bounds__(256) column_sum_kernel(int64_t rows, int64_t cols, Mat dy, float* partials) {
     __shared__ float part[8][32 * V + 1];

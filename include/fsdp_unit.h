@@ -513,7 +513,9 @@ FSDP_API int fsdp_host_device_pointer(const void* host, void** dev);
  * 2^-24 * (k/768 + 20) for the slices; measured at k = 768 to 7680: 7e-7 of the
  * result for random signs, 1.3e-6 for one sign, 1.3e-5 with one product far larger
  * than the rest.)
- * Results do not depend on the stream, the device's load or earlier calls. */
+ * Results do not depend on the stream, the device's load or earlier calls.
+ * Except where a call says otherwise, what it writes shares no memory with what it
+ * reads. */
 
 /* An 8-bit activation checkpoint: fsdp_matrix.dtype of matrices whose `data`
  * holds int8 elements and whose `exps` holds one byte for each group of 32
@@ -585,7 +587,7 @@ FSDP_API int fsdp_linear_workspace_bytes(int64_t tokens, int64_t in_features, in
  * synchronises `stream`, stores the FSDP_KSTATUS_* bits raised since the last
  * call in *flags and clears them.  After a raised bit the outputs of the calls
  * enqueued since the last read are incomplete; after
- * FSDP_KSTATUS_DRAIN_TIMEOUT every later call but destroy returns
+ * FSDP_KSTATUS_DRAIN_TIMEOUT every later call but this one and destroy returns
  * FSDP_E_STATE. */
 FSDP_API int fsdp_compute_status(fsdp_compute* c, int32_t* flags, void* stream);
 
