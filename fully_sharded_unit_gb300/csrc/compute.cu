@@ -173,6 +173,8 @@ constexpr int64_t kMaxSide = (int64_t(1) << 31) - 512;   // tile coordinates are
 int check_linear(int64_t T, int64_t I, int64_t O, int weight_layout) {
     if (T < 0 || I < 1 || O < 1 || T > kMaxSide || I > kMaxSide || O > kMaxSide)
         return fail(FSDP_E_INVALID_ARG, "linear: tokens must be >= 0 and features >= 1 (each below 2^31 - 512)");
+    if (std::max(T, std::min(I, O)) > (int64_t(1) << 60) / std::max(I, O))   // the largest of the three matrices
+        return fail(FSDP_E_INVALID_ARG, "linear: a matrix of more than 2^60 elements");
     if (weight_layout != FSDP_WEIGHT_IN_OUT && weight_layout != FSDP_WEIGHT_OUT_IN)
         return fail(FSDP_E_INVALID_ARG, "unknown weight_layout");
     return FSDP_OK;

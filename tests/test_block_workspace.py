@@ -48,3 +48,16 @@ def test_a_handle_sized_by_the_weight_serves_it(offset):
     c.close()
     for got, want in ((y, x.double() @ w.double()), (dx, dy.double() @ w.double().t())):
         assert (got.double() - want).norm() <= 2.0 ** -8 * want.norm()
+
+
+def test_sizes_whose_bytes_do_not_fit_are_refused():
+    """Each width is below 2^31 - 512, but a matrix of two of them has more bytes
+    than 63 bits hold; a workspace of a negative or a wrapped size helps nobody."""
+    top = (1 << 31) - 513
+    for sizes in ((top, top, 8), (top, 8, top), (8, top, top), (top, top, top)):
+        for aligned in (True, False):
+            with pytest.raises(B.FsdpError) as e:
+                B.fsdp_linear_workspace_bytes(*sizes, weight_aligned=aligned)
+            assert e.value.code == B.FSDP_E_INVALID_ARG
+    most = B.fsdp_linear_workspace_bytes(1 << 28, 1 << 30, 1 << 30, weight_aligned=False)
+    assert most > (1 << 59) + (1 << 59) + (1 << 61)
