@@ -51,6 +51,7 @@ FSDP_KERNEL_COUNT = 5
 
 FSDP_KSTATUS_WAIT_TIMEOUT = 1
 FSDP_KSTATUS_DRAIN_TIMEOUT = 2
+FSDP_KSTATUS_BAD_TOKEN = 4
 
 FSDP_NOALLOC_MAX_TILES = 32768
 
@@ -60,6 +61,10 @@ FSDP_ACTIVATION_GELU_TANH = 2
 FSDP_ACTIVATION_GELU_ERF = 3
 FSDP_WEIGHT_IN_OUT = 0
 FSDP_WEIGHT_OUT_IN = 1
+FSDP_STATE8_SIGNED = 0
+FSDP_STATE8_UNSIGNED = 1
+FSDP_MOMENTS_F32 = 0
+FSDP_MOMENTS_8BIT = 1
 
 LAYOUTS = {"flat": FSDP_LAYOUT_FLAT, "dim0": FSDP_LAYOUT_DIM0, "flat_padded": FSDP_LAYOUT_FLAT_PADDED}
 GRAD_DTYPES = {"f32": FSDP_DTYPE_F32, "bf16": FSDP_DTYPE_BF16}
@@ -109,6 +114,14 @@ class Matrix(ctypes.Structure):
     """fsdp_matrix: a view of a device matrix."""
     _fields_ = [("data", ctypes.c_void_p), ("exps", ctypes.c_void_p), ("rows", ctypes.c_int64),
                 ("cols", ctypes.c_int64), ("ld", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
+class AdamWTensor(ctypes.Structure):
+    """fsdp_adamw_tensor: one tensor of a step over many."""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+                ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_exps", ctypes.c_void_p), ("exp_avg_sq_exps", ctypes.c_void_p),
+                ("copy_bf16", ctypes.c_void_p), ("numel", ctypes.c_int64), ("lr_scale", ctypes.c_double),
+                ("decay_scale", ctypes.c_double), ("grad_dtype", ctypes.c_int), ("moments", ctypes.c_int)]
 
 
 class FsdpError(RuntimeError):
@@ -174,6 +187,15 @@ _SIGNATURES = {
     "fsdp_act8_unpack": (_I, [_P, _PM, _I, _PM, _P]),
     "fsdp_strerror": (ctypes.c_char_p, [_I]),
     "fsdp_last_error": (ctypes.c_char_p, []),
+    "fsdp_token_logprobs_forward": (_I, [_P, _PM, _P, _D, _P, _P, _P, _I, _P, _P, _P]),
+    "fsdp_token_logprobs_backward": (_I, [_P, _PM, _P, _D, _P, _P, _P, _P, _PM, _P]),
+    "fsdp_token_logprobs_loss": (_I, [_P, _PM, _P, _D, _P, _P, _P, _P, _P, _PM, _P]),
+    "fsdp_residual_norm_workspace_bytes": (_I, [_I64, _I64, _PI64]),
+    "fsdp_residual_norm_forward": (_I, [_P, _PM, _PM, _P, _P, _P, _I, _D, _D, _PM, _PM, _P, _P, _P]),
+    "fsdp_residual_norm_backward": (_I, [_P, _PM, _PM, _PM, _PM, _P, _P, _P, _I, _D, _P, _P, _PM, _PM, _P, _P, _P, _I, _I, _P]),
+    "fsdp_state8_pack": (_I, [_P, _I, _P, _I64, _P, _P, _P]),
+    "fsdp_state8_unpack": (_I, [_P, _I, _P, _P, _I64, _P, _I, _P]),
+    "fsdp_adamw_tensors": (_I, [_P, ctypes.POINTER(AdamWTensor), _I64, ctypes.POINTER(AdamWHp), _I64, ctypes.c_uint64, _P, _P, _P]),
 }
 
 _lib = None
@@ -790,6 +812,220 @@ def fsdp_act8_unpack(h, ckpt, out, activation="none", stream=None) -> None:
                                   _current(stream, d)), "fsdp_act8_unpack")
 
 
+# ---- a training step's ends --------------------------------------------------
+
+def _array(t, shape, dtype, device=None):
+    """The address of a contiguous CUDA tensor of this shape and dtype; None for None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0 or t.dtype != dtype or t.shape != shape or not t.is_contiguous() \
+            or (device is not None and t.get_device() != device):
+        _refuse(f"a contiguous {dtype} CUDA tensor of {tuple(shape)} on the handle's device is expected, not {_about(t)}")
+    return t.data_ptr()
+
+
+def _shaped(t, name, device):
+    """fsdp_matrix of a tensor whose shape says that of the others."""
+    m = _mat(t, device)
+    if m is None or t.__class__ is Act8:
+        _refuse(f"{name} is a 2-D tensor")
+    return m
+
+
+def fsdp_token_logprobs_forward(h, logits, tokens, logprob, entropy=None, stats=None, top_tokens=None, top_logprobs=None,
+                                scale=1.0, stream=None) -> None:
+    """``tokens`` int64 [rows] with ``logprob`` float32 [rows], or both None; ``stats`` float32 [rows, 2];
+    ``top_tokens`` int64 and ``top_logprobs`` float32 [rows, k], k at most 32."""
+    d = _device_of(h)
+    zm = _shaped(logits, "logits", d)
+    rows = logits.shape[0]
+    top = 0
+    if top_tokens is not None or top_logprobs is not None:
+        if top_tokens is None or top_logprobs is None or top_tokens.dim() != 2:
+            _refuse("top_tokens and top_logprobs are two matrices of rows x k")
+        top = top_tokens.shape[1]
+        if top < 1:
+            _refuse("top_tokens has at least one column")
+    f32 = torch.float32
+    _check(lib().fsdp_token_logprobs_forward(h, zm, _array(tokens, (rows,), torch.int64, d), float(scale), _array(logprob, (rows,), f32, d),
+                                             _array(entropy, (rows,), f32, d), _array(stats, (rows, 2), f32, d), top,
+                                             _array(top_tokens, (rows, top), torch.int64, d), _array(top_logprobs, (rows, top), f32, d),
+                                             _current(stream, d)), "fsdp_token_logprobs_forward")
+
+
+def fsdp_token_logprobs_backward(h, logits, tokens, stats, dlogits, dlogprob=None, entropy=None, dentropy=None, scale=1.0,
+                                 stream=None) -> None:
+    """``dlogits`` may be ``logits`` itself."""
+    d = _device_of(h)
+    zm = _shaped(logits, "logits", d)
+    rows = logits.shape[0]
+    f32 = torch.float32
+    _check(lib().fsdp_token_logprobs_backward(h, zm, _array(tokens, (rows,), torch.int64, d), float(scale), _array(stats, (rows, 2), f32, d),
+                                              _array(entropy, (rows,), f32, d), _array(dlogprob, (rows,), f32, d),
+                                              _array(dentropy, (rows,), f32, d), _mat(dlogits, d), _current(stream, d)),
+           "fsdp_token_logprobs_backward")
+
+
+def fsdp_token_logprobs_loss(h, logits, tokens, logprob, dlogits, dlogprob=None, dentropy=None, entropy=None, stats=None, scale=1.0,
+                             stream=None) -> None:
+    """Forward and backward pass in one call; ``dlogits`` may be ``logits`` itself."""
+    d = _device_of(h)
+    zm = _shaped(logits, "logits", d)
+    rows = logits.shape[0]
+    f32 = torch.float32
+    _check(lib().fsdp_token_logprobs_loss(h, zm, _array(tokens, (rows,), torch.int64, d), float(scale), _array(dlogprob, (rows,), f32, d),
+                                          _array(dentropy, (rows,), f32, d), _array(logprob, (rows,), f32, d),
+                                          _array(entropy, (rows,), f32, d), _array(stats, (rows, 2), f32, d), _mat(dlogits, d),
+                                          _current(stream, d)), "fsdp_token_logprobs_loss")
+
+
+def fsdp_residual_norm_workspace_bytes(rows, cols) -> int:
+    n = ctypes.c_int64()
+    _check(lib().fsdp_residual_norm_workspace_bytes(int(rows), int(cols), ctypes.byref(n)), "fsdp_residual_norm_workspace_bytes")
+    return n.value
+
+
+def _vecs(named, n, device):
+    """Addresses of vectors of one dtype (None stays None), and that dtype."""
+    out, kind = [], None
+    for name, t in named:
+        if t is None:
+            out.append(None)
+            continue
+        p, dt = _vec(t, n, device)
+        if kind is not None:
+            _same(kind, dt, ", ".join(k for k, v in named if v is not None))
+        kind = dt
+        out.append(p)
+    return out, FSDP_DTYPE_F32 if kind is None else kind
+
+
+def fsdp_residual_norm_forward(h, residual, out, block=None, post_gamma=None, gate=None, residual_scale=1.0, y=None, gamma=None,
+                               eps=1e-6, rstd=None, post_rstd=None, stream=None) -> None:
+    d = _device_of(h)
+    hm = _shaped(residual, "residual", d)
+    rows, cols = residual.shape
+    (p, g, w), dt = _vecs((("post_gamma", post_gamma), ("gate", gate), ("gamma", gamma)), cols, d)
+    f32 = torch.float32
+    _check(lib().fsdp_residual_norm_forward(h, hm, _mat(block, d), p, g, w, dt, float(residual_scale), float(eps), _mat(out, d), _mat(y, d),
+                                            _array(post_rstd, (rows,), f32, d), _array(rstd, (rows,), f32, d), _current(stream, d)),
+           "fsdp_residual_norm_forward")
+
+
+def fsdp_residual_norm_backward(h, dy, dout, out, block, dresidual, dblock, gamma=None, rstd=None, dgamma=None, post_gamma=None,
+                                post_rstd=None, dpost_gamma=None, gate=None, dgate=None, residual_scale=1.0, accumulate=False,
+                                stream=None) -> None:
+    d = _device_of(h)
+    dm = _shaped(dresidual, "dresidual", d)
+    rows, cols = dresidual.shape
+    (p, g, w), dt = _vecs((("post_gamma", post_gamma), ("gate", gate), ("gamma", gamma)), cols, d)
+    (dp, dg, dw), gt = _vecs((("dpost_gamma", dpost_gamma), ("dgate", dgate), ("dgamma", dgamma)), cols, d)
+    f32 = torch.float32
+    _check(lib().fsdp_residual_norm_backward(h, _mat(dy, d), _mat(dout, d), _mat(out, d), _mat(block, d), p, g, w, dt, float(residual_scale),
+                                             _array(post_rstd, (rows,), f32, d), _array(rstd, (rows,), f32, d), dm, _mat(dblock, d), dw, dp, dg,
+                                             gt, 1 if accumulate else 0, _current(stream, d)), "fsdp_residual_norm_backward")
+
+
+class State8:
+    """8-bit moments of ``numel`` elements: ``codes`` uint8 [numel] and ``exps`` uint8
+    [ceil(numel/32)], zeros unless given.  ``signed``: exp_avg; else exp_avg_sq."""
+
+    def __init__(self, numel, signed, codes=None, exps=None, device="cuda"):
+        self.numel, self.signed = int(numel), bool(signed)
+        groups = (self.numel + 31) // 32
+        self.codes = torch.zeros(self.numel, dtype=torch.uint8, device=device) if codes is None else codes
+        self.exps = torch.zeros(groups, dtype=torch.uint8, device=device) if exps is None else exps
+        for t, n in ((self.codes, self.numel), (self.exps, groups)):
+            _array(t, (n,), torch.uint8)
+        self.device = self.codes.get_device()
+        if self.exps.get_device() != self.device:
+            _refuse("codes and exps of 8-bit moments are on one device")
+
+    @property
+    def kind(self):
+        return FSDP_STATE8_SIGNED if self.signed else FSDP_STATE8_UNSIGNED
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.exps.numel()
+
+    def piece(self, begin, numel):
+        """A view of the elements from ``begin`` (a multiple of 32) on; a piece that ends inside a group
+        leaves the rest of that group to nobody else."""
+        if begin % 32 or begin < 0 or numel < 0 or begin + numel > self.numel:
+            _refuse("a piece of 8-bit moments begins at a multiple of 32 and ends inside them")
+        return State8(numel, self.signed, self.codes[begin:begin + numel], self.exps[begin // 32:begin // 32 + (numel + 31) // 32])
+
+
+def fsdp_state8_pack(h, x, state, stream=None) -> None:
+    """Floats into 8-bit moments, to nearest."""
+    d = _device_of(h)
+    if state.__class__ is not State8 or (d is not None and state.device != d):
+        _refuse("8-bit moments on the handle's device are expected")
+    _check(lib().fsdp_state8_pack(h, state.kind, _array(x, (state.numel,), torch.float32, d), state.numel, state.codes.data_ptr(),
+                                  state.exps.data_ptr(), _current(stream, d)), "fsdp_state8_pack")
+
+
+def fsdp_state8_unpack(h, state, out, stream=None) -> None:
+    """The values that 8-bit moments stand for, as float32 or bfloat16."""
+    d = _device_of(h)
+    if state.__class__ is not State8 or (d is not None and state.device != d):
+        _refuse("8-bit moments on the handle's device are expected")
+    o, dt = _vec(out, state.numel, d)
+    _check(lib().fsdp_state8_unpack(h, state.kind, state.codes.data_ptr(), state.exps.data_ptr(), state.numel, o, dt,
+                                    _current(stream, d)), "fsdp_state8_unpack")
+
+
+class AdamWTensors:
+    """The tensors of an AdamW step, as the library takes them; made once and used every step.
+
+    ``params``: float32; ``grads``: float32 or bfloat16; ``exp_avg``, ``exp_avg_sq``: float32, or both ``State8``;
+    ``copies``: bfloat16 that receive the rounded parameters, or None; all contiguous, of the parameters' sizes,
+    on one device.  ``lr_scale``, ``decay_scale``: a number for each tensor (1 unless given)."""
+
+    def __init__(self, params, grads, exp_avg, exp_avg_sq, copies=None, lr_scale=None, decay_scale=None):
+        n = len(params)
+        copies = [None] * n if copies is None else copies
+        lr_scale, decay_scale = ([1.0] * n if s is None else s for s in (lr_scale, decay_scale))
+        if any(len(v) != n for v in (grads, exp_avg, exp_avg_sq, copies, lr_scale, decay_scale)):
+            _refuse("the lists of an AdamW step are of one length")
+        self.count, self.device = n, params[0].get_device() if n else None
+        self.array = (AdamWTensor * max(1, n))()
+        self.kept = (list(params), list(grads), list(exp_avg), list(exp_avg_sq), list(copies))
+        for e, p, g, m, v, c, ls, ds in zip(self.array, params, grads, exp_avg, exp_avg_sq, copies, lr_scale, decay_scale):
+            shape = p.shape
+            e.numel = p.numel()
+            e.param = _array(p, shape, torch.float32, self.device)
+            e.grad = _array(g, shape, g.dtype, self.device)
+            e.grad_dtype = _dtype(g)
+            e.copy_bf16 = _array(c, shape, torch.bfloat16, self.device)
+            e.lr_scale, e.decay_scale = float(ls), float(ds)
+            if m.__class__ is State8 and v.__class__ is State8:
+                if not m.signed or v.signed or m.numel != e.numel or v.numel != e.numel or m.device != self.device or v.device != self.device:
+                    _refuse(f"exp_avg (signed) and exp_avg_sq (unsigned) of {e.numel} elements on the parameters' device are expected")
+                e.moments = FSDP_MOMENTS_8BIT
+                e.exp_avg, e.exp_avg_exps = m.codes.data_ptr(), m.exps.data_ptr()
+                e.exp_avg_sq, e.exp_avg_sq_exps = v.codes.data_ptr(), v.exps.data_ptr()
+            else:
+                e.moments = FSDP_MOMENTS_F32
+                e.exp_avg = _array(m, shape, torch.float32, self.device)
+                e.exp_avg_sq = _array(v, shape, torch.float32, self.device)
+
+
+def fsdp_adamw_tensors(h, tensors, hp, step, seed=0, grad_scale=None, skip=None, stream=None) -> None:
+    """``tensors``: an ``AdamWTensors``; ``step``: 1 at the first; ``seed``: another every step where moments have 8 bits;
+    ``grad_scale``: None or a float32 tensor of one element; ``skip``: None or an int32 tensor of one element."""
+    d = _device_of(h)
+    if tensors.__class__ is not AdamWTensors or (d is not None and tensors.count and tensors.device != d):
+        _refuse("an AdamWTensors on the handle's device is expected")
+    for t, dtype in ((grad_scale, torch.float32), (skip, torch.int32)):
+        if t is not None and (t.numel() != 1 or t.dtype != dtype or t.get_device() < 0 or (d is not None and t.get_device() != d)):
+            _refuse(f"one {dtype} element on the handle's device is expected, not {_about(t)}")
+    _check(lib().fsdp_adamw_tensors(h, tensors.array, tensors.count, ctypes.byref(_hp(hp)), int(step), int(seed) & (2 ** 64 - 1),
+                                    None if grad_scale is None else grad_scale.data_ptr(), None if skip is None else skip.data_ptr(),
+                                    _current(stream, d)), "fsdp_adamw_tensors")
+
+
 class Compute:
     """Owns one ``fsdp_compute`` handle; methods call the C entry points."""
 
@@ -840,6 +1076,38 @@ class Compute:
 
     def act8_unpack(self, ckpt, out, activation="none", stream=None):
         fsdp_act8_unpack(self.handle, ckpt, out, activation, stream)
+
+    def token_logprobs_forward(self, logits, tokens, logprob, entropy=None, stats=None, top_tokens=None, top_logprobs=None,
+                               scale=1.0, stream=None):
+        fsdp_token_logprobs_forward(self.handle, logits, tokens, logprob, entropy, stats, top_tokens, top_logprobs, scale, stream)
+
+    def token_logprobs_backward(self, logits, tokens, stats, dlogits, dlogprob=None, entropy=None, dentropy=None, scale=1.0,
+                                stream=None):
+        fsdp_token_logprobs_backward(self.handle, logits, tokens, stats, dlogits, dlogprob, entropy, dentropy, scale, stream)
+
+    def token_logprobs_loss(self, logits, tokens, logprob, dlogits, dlogprob=None, dentropy=None, entropy=None, stats=None,
+                            scale=1.0, stream=None):
+        fsdp_token_logprobs_loss(self.handle, logits, tokens, logprob, dlogits, dlogprob, dentropy, entropy, stats, scale, stream)
+
+    def residual_norm_forward(self, residual, out, block=None, post_gamma=None, gate=None, residual_scale=1.0, y=None, gamma=None,
+                              eps=1e-6, rstd=None, post_rstd=None, stream=None):
+        fsdp_residual_norm_forward(self.handle, residual, out, block, post_gamma, gate, residual_scale, y, gamma, eps, rstd,
+                                   post_rstd, stream)
+
+    def residual_norm_backward(self, dy, dout, out, block, dresidual, dblock, gamma=None, rstd=None, dgamma=None, post_gamma=None,
+                               post_rstd=None, dpost_gamma=None, gate=None, dgate=None, residual_scale=1.0, accumulate=False,
+                               stream=None):
+        fsdp_residual_norm_backward(self.handle, dy, dout, out, block, dresidual, dblock, gamma, rstd, dgamma, post_gamma, post_rstd,
+                                    dpost_gamma, gate, dgate, residual_scale, accumulate, stream)
+
+    def state8_pack(self, x, state, stream=None):
+        fsdp_state8_pack(self.handle, x, state, stream)
+
+    def state8_unpack(self, state, out, stream=None):
+        fsdp_state8_unpack(self.handle, state, out, stream)
+
+    def adamw_tensors(self, tensors, hp, step, seed=0, grad_scale=None, skip=None, stream=None):
+        fsdp_adamw_tensors(self.handle, tensors, hp, step, seed, grad_scale, skip, stream)
 
 
 # ---- a small owning wrapper ----------------------------------------------

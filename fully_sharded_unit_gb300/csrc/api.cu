@@ -28,6 +28,9 @@ using fsdp::Tile;
 
 namespace {
 
+using fsdp::adamw_consts;
+using fsdp::check_hp;
+
 thread_local std::string g_last_error;
 
 int fail(int code, const std::string& why) {
@@ -226,18 +229,6 @@ int check_unit(const fsdp_unit* u, bool need_loaded) {
     return FSDP_OK;
 }
 
-int check_hp(const fsdp_adamw_hp* hp) {
-    if (hp == nullptr) return fail(FSDP_E_INVALID_ARG, "hp is null");
-    auto fin = [](double x) { return std::isfinite(x); };
-    if (!fin(hp->lr) || !fin(hp->beta1) || !fin(hp->beta2) || !fin(hp->eps) || !fin(hp->weight_decay))
-        return fail(FSDP_E_INVALID_ARG, "AdamW hyper-parameters must be finite");
-    if (hp->lr < 0 || hp->eps < 0 || hp->weight_decay < 0)
-        return fail(FSDP_E_INVALID_ARG, "lr, eps and weight_decay must be >= 0");
-    if (!(hp->beta1 >= 0 && hp->beta1 < 1) || !(hp->beta2 >= 0 && hp->beta2 < 1))
-        return fail(FSDP_E_INVALID_ARG, "betas must be in [0, 1)");
-    return FSDP_OK;
-}
-
 // Gradient buffers must be 16-byte aligned; *narrow is set when one of them
 // is not 32-byte aligned (the kernels then use 16-byte loads).
 int check_grads(const fsdp_unit* u, const void* const* grads, int* narrow) {
@@ -274,21 +265,6 @@ void wait_args(fsdp_unit* u, fsdp::ReduceArgs* a) {
     a->wait_ns = u->wait_ns;
     a->withhold = u->withhold_next;
     u->withhold_next = 0;
-}
-
-fsdp::AdamWConsts adamw_consts(const fsdp_adamw_hp* hp, int64_t t) {
-    const double bc1 = 1.0 - std::pow(hp->beta1, static_cast<double>(t));
-    const double bc2 = 1.0 - std::pow(hp->beta2, static_cast<double>(t));
-    fsdp::AdamWConsts c;
-    c.decay = static_cast<float>(1.0 - hp->lr * hp->weight_decay);
-    c.b1 = static_cast<float>(hp->beta1);
-    c.c1 = static_cast<float>(1.0 - hp->beta1);
-    c.b2 = static_cast<float>(hp->beta2);
-    c.c2 = static_cast<float>(1.0 - hp->beta2);
-    c.bc2 = static_cast<float>(bc2);
-    c.step = static_cast<float>(hp->lr / bc1);
-    c.eps = static_cast<float>(hp->eps);
-    return c;
 }
 
 // Recompute the whole shadow slab from the master if AdamW left it stale.

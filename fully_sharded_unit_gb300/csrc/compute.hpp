@@ -8,6 +8,8 @@
 #include <atomic>
 #include <cstdint>
 
+#include "fsdp_unit.h"
+
 namespace fsdp {
 
 // A matrix as the kernels see it: element (r, c) at p + (r*ld + c) elements.
@@ -145,5 +147,58 @@ cudaError_t launch_few_rows(const Product& p, int sms, cudaStream_t st);
 int64_t column_sum_partials(int64_t rows, int64_t cols, int sms);
 cudaError_t launch_column_sum(int64_t rows, int64_t cols, const Mat& dy, float* partials, void* out, int out_dtype,
                               int accumulate, int sms, cudaStream_t st);
+
+// ---- log probabilities of tokens (logprobs.cu) ----
+constexpr int kMostTop = 32;   // alternatives of a row
+struct TokenLogprobs {
+    int64_t rows, vocab;
+    Mat z;
+    const int64_t* tokens;          // null: none given
+    float scale;
+    float *logprob, *entropy, *stats;   // null: not wanted (backward: stats and entropy are read)
+    int top;
+    int64_t* top_tokens;
+    float* top_logprobs;
+    Mat dz;                         // p null: no gradient
+    const float *dlogprob, *dentropy;   // null: zeros
+    int32_t* status;                // FSDP_KSTATUS_* bits
+};
+// Everything but the gradient; with dz, the gradient behind it.
+cudaError_t launch_token_logprobs(const TokenLogprobs& a, int sms, cudaStream_t st);
+// The gradient alone, from stats (and entropy).
+cudaError_t launch_token_logprobs_backward(const TokenLogprobs& a, int sms, cudaStream_t st);
+
+// ---- residual norm (residual_norm.cu) ----
+struct ResidualNorm {
+    int64_t rows, cols;
+    Mat h, o, out, y;               // o.p, y.p null: none
+    const void *post, *gate, *gamma;
+    int param_dtype;
+    float alpha, eps;
+    float *post_rstd, *rstd;
+};
+cudaError_t launch_residual_norm_forward(const ResidualNorm& a, int sms, cudaStream_t st);
+
+struct ResidualNormGrad {
+    int64_t rows, cols;
+    Mat dy, dout, out, o, dh, dblock;   // dy.p, dout.p, o.p null: none
+    const void *post, *gate, *gamma;
+    int param_dtype;
+    float alpha;
+    const float *post_rstd, *rstd;
+    void *dgamma, *dpost, *dgate;
+    int grad_dtype, accumulate;
+    float* partials;                // workspace: a row of 2 x cols floats a block
+};
+// Blocks that sums over rows are split over, at most (the workspace's rows).
+int64_t residual_norm_blocks(int64_t rows, int64_t cols);
+cudaError_t launch_residual_norm_backward(const ResidualNormGrad& a, int sms, cudaStream_t st);
+
+// ---- AdamW over many tensors, 8-bit moments (adamw_tensors.cu) ----
+cudaError_t launch_state8_pack(int kind, const float* x, int64_t n, uint8_t* codes, uint8_t* exps, int sms, cudaStream_t st);
+cudaError_t launch_state8_unpack(int kind, const uint8_t* codes, const uint8_t* exps, int64_t n, void* out, int out_dtype,
+                                 int sms, cudaStream_t st);
+cudaError_t launch_adamw_tensors(const fsdp_adamw_tensor* tensors, int64_t count, const fsdp_adamw_hp& hp, int64_t step,
+                                 uint64_t seed, const float* grad_scale, const int32_t* skip, int sms, cudaStream_t st);
 
 }  // namespace fsdp

@@ -645,15 +645,6 @@ __global__ void __launch_bounds__(kBlock) reduce_scatter_kernel(const Tile* __re
 
 // ---------------------------------------------------------------- AdamW
 
-__device__ __forceinline__ void adamw_elem(float& p, float g, float& m, float& v,
-                                           const AdamWConsts& c) {
-    const float pd = __fmul_rn(p, c.decay);
-    m = __fadd_rn(__fmul_rn(c.b1, m), __fmul_rn(c.c1, g));
-    v = __fadd_rn(__fmul_rn(c.b2, v), __fmul_rn(c.c2, __fmul_rn(g, g)));
-    const float denom = __fadd_rn(__fsqrt_rn(__fdiv_rn(v, c.bc2)), c.eps);
-    p = __fsub_rn(pd, __fmul_rn(c.step, __fdiv_rn(m, denom)));
-}
-
 // This step's constants.  Device-step mode reads entry *counter of the table
 // (the counter only changes in launch_advance_step, which runs after this
 // kernel on the same stream); a used-up table skips the update and raises

@@ -6,19 +6,10 @@
 
 #include <cstdint>
 
+#include "adamw.hpp"
 #include "plan.hpp"
 
 namespace fsdp {
-
-// fp32 constants of one AdamW step, formed on the host.
-struct AdamWConsts {
-    float decay;   // 1 - lr*wd
-    float b1, c1;  // beta1, 1 - beta1
-    float b2, c2;  // beta2, 1 - beta2
-    float bc2;     // 1 - beta2^t
-    float step;    // lr / (1 - beta1^t)
-    float eps;
-};
 
 // Where AdamW takes one step's constants from: the host-formed `c`, or (for
 // CUDA-graph replay) entry *counter of a device table of consecutive steps.

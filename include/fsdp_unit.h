@@ -107,6 +107,9 @@ extern "C" {
                                           the kernel ended, so nothing computed around that
                                           launch can be trusted                             */
 
+#define FSDP_KSTATUS_BAD_TOKEN     4   /* a compute handle's kernel met a token >= vocab (see
+                                          fsdp_token_logprobs_forward)                      */
+
 /* ---- plain structs ------------------------------------------------------ */
 typedef struct fsdp_unit fsdp_unit;   /* opaque; one FlatParamHandle ([FSDP] section 4.2) */
 
@@ -665,6 +668,153 @@ FSDP_API int fsdp_act8_layout(int64_t rows, int64_t cols, int64_t* data_ld, int6
 FSDP_API int fsdp_act8_pack(fsdp_compute* c, const fsdp_matrix* x, const fsdp_matrix* ckpt, void* stream);
 FSDP_API int fsdp_act8_unpack(fsdp_compute* c, const fsdp_matrix* ckpt, int activation, const fsdp_matrix* out,
                               void* stream);
+
+/* ---- a training step's ends -------------------------------------------------- */
+/* What a language model has around its units: the log probabilities that its loss
+ * is made of, with the logits' gradient; the norms before and after a block
+ * with its gate and residual scale; AdamW over tensors that no unit shards, or that
+ * want their moments in 8 bits.  Handles, streams and roundings are those of the
+ * block operators; results do not depend on the order in which blocks run. */
+
+/* Log probabilities of given tokens.  logits: rows x vocab, BF16 or F32 (vocab <=
+ * 2^30).  With z a row, d_i = scale (z_i - max z) and S = sum exp(d_i), in natural
+ * logarithms:
+ *     logprob[row] = d_t - ln S                       t = tokens[row]
+ *     entropy[row] = ln S - sum exp(d_i) d_i / S      (terms with exp(d_i) = 0 are 0)
+ *     stats[2 row], stats[2 row + 1] = max z, ln S    for the backward pass
+ *     top_tokens, top_logprobs [row*top + j]: the j-th largest logit's index and
+ *     log probability, the lowest index first among equal logits
+ * tokens, logprob: both or neither; the other outputs may be NULL (both top_*
+ * with top = 0).  top: 0 .. 32, at most vocab.  scale (1 / temperature): finite, > 0.
+ *  - tokens[row] < 0 gives none: logprob 0, and no gradient through it.
+ *  - tokens[row] >= vocab: logprob (and in the gradient's calls the whole row of
+ *    dlogits) is NaN and FSDP_KSTATUS_BAD_TOKEN is raised; nothing is read there.
+ *  - A logit of -inf is masked: probability 0, gradient 0.  A row of nothing else
+ *    has log probabilities of -inf, entropy 0 and gradient 0.
+ *  - A row that holds +inf or NaN has NaN results, and top_tokens of -1. */
+FSDP_API int fsdp_token_logprobs_forward(fsdp_compute* c, const fsdp_matrix* logits, const int64_t* tokens, double scale,
+                                         float* logprob, float* entropy, float* stats, int top, int64_t* top_tokens,
+                                         float* top_logprobs, void* stream);
+
+/* The logits' gradient of a loss L, given a = dL/dlogprob and b = dL/dentropy
+ * (floats, one a row; either may be NULL for zeros, not both):
+ *     dlogits_i = scale (a ([i = t] - p_i) - b p_i (ln p_i + entropy)),  p_i = exp(d_i) / S
+ * stats and, with dentropy, entropy as the forward wrote them.  tokens may be NULL
+ * where dlogprob is.  dlogits: BF16 or F32, may be logits itself.  A row whose a and b
+ * are 0 (a without a token counts as 0) gets zeros, whatever its logits. */
+FSDP_API int fsdp_token_logprobs_backward(fsdp_compute* c, const fsdp_matrix* logits, const int64_t* tokens, double scale,
+                                          const float* stats, const float* entropy, const float* dlogprob,
+                                          const float* dentropy, const fsdp_matrix* dlogits, void* stream);
+
+/* Both in one call, where a and b are known before the log probabilities (a loss that is
+ * a weighted sum of them): the logits are read from memory once.  logprob is
+ * required; entropy and stats may be NULL. */
+FSDP_API int fsdp_token_logprobs_loss(fsdp_compute* c, const fsdp_matrix* logits, const int64_t* tokens, double scale,
+                                      const float* dlogprob, const float* dentropy, float* logprob, float* entropy,
+                                      float* stats, const fsdp_matrix* dlogits, void* stream);
+
+/* The norms before and after a block (root mean square, without mean), with its gate
+ * and residual scale.  With h the residual stream and o the block's result, in each
+ * row of cols elements:
+ *     post_rstd = 1 / sqrt(sum(o^2) / cols + eps)
+ *     out = residual_scale * h + gate * (o * post_rstd * post_gamma)
+ *     rstd = 1 / sqrt(sum(out^2) / cols + eps)
+ *     y = out * rstd * gamma                     from out before its rounding
+ * post_gamma NULL: no norm after the block (o itself).  gate NULL: 1.  block NULL (with
+ * post_gamma and gate): out = residual_scale * h.  gamma NULL (with y and rstd): no norm
+ * before the next block.  post_gamma, gate, gamma: cols elements of param_dtype (BF16
+ * or F32).  residual, block, out, y: rows x cols, BF16 or F32 each.  rstd,
+ * post_rstd: `rows` floats each, for the backward pass.  eps: finite, >= 0. */
+FSDP_API int fsdp_residual_norm_forward(fsdp_compute* c, const fsdp_matrix* residual, const fsdp_matrix* block,
+                                        const void* post_gamma, const void* gate, const void* gamma, int param_dtype,
+                                        double residual_scale, double eps, const fsdp_matrix* out, const fsdp_matrix* y,
+                                        float* post_rstd, float* rstd, void* stream);
+
+/* Its gradients.  dy: y's gradient (NULL with gamma, rstd and dgamma); dout: out's
+ * from the residual stream (NULL: none; not both).  out, block, rstd and
+ * post_rstd as in the forward pass.  With u = o * post_rstd (o without that norm),
+ * xh = out * rstd and g = dy * gamma:
+ *     t = dout + rstd * (g - xh * mean_row(g * xh))
+ *     dresidual = residual_scale * t
+ *     e = t * gate * post_gamma;  dblock = post_rstd * (e - u * mean_row(e * u))   (e without that norm)
+ *     dgamma = sum over rows of dy * xh
+ *     dpost_gamma = gate * sum over rows of t * u;  dgate = post_gamma * the same sum
+ * dresidual and dblock: BF16 or F32; block NULL: no dblock.  dgamma, dpost_gamma, dgate:
+ * cols elements of grad_dtype, one for each vector that is given (NULL where that is),
+ * aligned to their element only; overwritten, or added to when `accumulate` is set.
+ * The sums over rows have a fixed order. */
+FSDP_API int fsdp_residual_norm_backward(fsdp_compute* c, const fsdp_matrix* dy, const fsdp_matrix* dout,
+                                         const fsdp_matrix* out, const fsdp_matrix* block, const void* post_gamma,
+                                         const void* gate, const void* gamma, int param_dtype, double residual_scale,
+                                         const float* post_rstd, const float* rstd, const fsdp_matrix* dresidual,
+                                         const fsdp_matrix* dblock, void* dgamma, void* dpost_gamma, void* dgate,
+                                         int grad_dtype, int accumulate, void* stream);
+
+/* The workspace that fsdp_residual_norm_backward needs at these sizes, in any type and
+ * option, and with fewer rows (the forward needs none).  Host only. */
+FSDP_API int fsdp_residual_norm_workspace_bytes(int64_t rows, int64_t cols, int64_t* bytes);
+
+/* 8-bit moments of an optimizer.  A tensor's elements, in order, form groups of 32 (the last
+ * may be short) that share one exponent byte; `codes` holds a byte an element, `exps`
+ * ceil(numel/32) bytes; neither needs an alignment.  An element of a group with exponent
+ * byte B stands for f * 2^(B-127), 1 <= B <= 253, where f < 2 is a small float:
+ *   SIGNED (exp_avg):      sign, 4 bits of exponent e, 3 of mantissa k: (8 + k) * 2^(e-18), k * 2^-17 for e = 0
+ *   UNSIGNED (exp_avg_sq):       5 bits of exponent e, 3 of mantissa k: (8 + k) * 2^(e-34), k * 2^-33 for e = 0
+ * B is the smallest for which every magnitude is at most 1.875 * 2^(B-127).  A group with
+ * an infinity or a NaN gets byte 255 and stands for NaN.  Bytes of zeros stand for
+ * zeros.  An UNSIGNED element that is not 0 is not rounded to 0 (the update divides by
+ * its root); a negative one counts as 0. */
+#define FSDP_STATE8_SIGNED   0
+#define FSDP_STATE8_UNSIGNED 1
+
+/* Put numel floats into 8 bits (rounded to nearest even), and read them back, as F32 or
+ * BF16 (both hold every value that an element can stand for, above 2^-126). */
+FSDP_API int fsdp_state8_pack(fsdp_compute* c, int kind, const float* x, int64_t numel, uint8_t* codes, uint8_t* exps,
+                              void* stream);
+FSDP_API int fsdp_state8_unpack(fsdp_compute* c, int kind, const uint8_t* codes, const uint8_t* exps, int64_t numel,
+                                void* out, int out_dtype, void* stream);
+
+/* One tensor of fsdp_adamw_tensors.  All pointers need the alignment of their element
+ * only; tensors whose pointers are all 16-byte aligned run fastest. */
+#define FSDP_MOMENTS_F32  0
+#define FSDP_MOMENTS_8BIT 1
+typedef struct {
+    float* param;             /* updated                                                       */
+    const void* grad;         /* numel elements of grad_dtype                                  */
+    void* exp_avg;            /* numel floats, or SIGNED codes                                 */
+    void* exp_avg_sq;         /* numel floats, or UNSIGNED codes                               */
+    uint8_t* exp_avg_exps;    /* 8-bit moments: their exponent bytes                           */
+    uint8_t* exp_avg_sq_exps;
+    uint16_t* copy_bf16;      /* optional: receives RNE_bf16(param)                            */
+    int64_t numel;            /* >= 0, at most 2^40                                            */
+    double lr_scale;          /* times hp->lr                                                  */
+    double decay_scale;       /* times hp->weight_decay (0: a bias or a norm's weight)         */
+    int grad_dtype;           /* FSDP_DTYPE_F32 or _BF16                                       */
+    int moments;              /* FSDP_MOMENTS_*                                                */
+} fsdp_adamw_tensor;
+
+/* AdamW on `count` tensors (a HOST array) in one launch for every few hundred: the formula of
+ * fsdp_adamw_step at step number `step` (>= 1), element by element in fp32, with lr and
+ * weight decay scaled as the tensor says, so F32 moments and gradients give the bits
+ * of fsdp_adamw_step.
+ *  - grad_scale_dev (optional device float): every gradient is multiplied by it first (loss-scale
+ *    removal, clipping).
+ *  - skip_dev (optional device int32, e.g. fsdp_rs_options.found_nonfinite_dev): if it is not 0
+ *    when the kernel runs, nothing is changed.
+ *  - 8-bit moments are decoded, updated and used in fp32, and then rounded up or down at
+ *    random, in proportion: to nearest, a moving average whose change a step is below half a
+ *    step of the 8 bits would stand still.  The 16 random bits r of element i of tensor number
+ *    j (of `count`) come from `seed`, which a training run changes every step: with mod 2^32
+ *        x = low32(i) ^ key ^ high32(i) * 0x85157AF5,
+ *        key = high32(seed * 0x9E3779B97F4A7C15 + (j + 1) * 0xD1B54A32D192ED03 mod 2^64)
+ *        x ^= x >> 16; x *= 0xD36F86A9; x ^= x >> 15; x *= 0xC242E759; x ^= x >> 16
+ *    r = the low half of x for exp_avg, the high half for exp_avg_sq; the magnitude is rounded
+ *    to 20 bits below the code's last (to nearest) and goes up if those plus 16 r reach 2^20.
+ * The constants are formed from hp and `step` at the call: a captured call replays them.  No
+ * two tensors share what is written. */
+FSDP_API int fsdp_adamw_tensors(fsdp_compute* c, const fsdp_adamw_tensor* tensors, int64_t count, const fsdp_adamw_hp* hp,
+                                int64_t step, uint64_t seed, const float* grad_scale_dev, const int32_t* skip_dev,
+                                void* stream);
 
 /* ---- errors -------------------------------------------------------------- */
 /* Library infrastructure (the pages have no counterpart). */
