@@ -71,12 +71,21 @@ __global__ void __launch_bounds__(256) state8_pack_kernel(const float* x, int64_
 }
 
 template <bool SIGNED>
-__global__ void __launch_bounds__(256) state8_unpack_kernel(const uint8_t* codes, const uint8_t* exps, int64_t n, void* out, int dtype) {
+__global__ void __launch_bounds__(256) state8_unpack_kernel(const uint8_t* codes, const uint8_t* exps, int64_t n, void* out, int dtype,
+                                                            bool vector) {
     starts_early();
     after_previous();
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += stride)
-        store1(out, dtype, i, state8_value<SIGNED>(codes[i], state8_unit(exps[i >> 5])));
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * 256, first = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t eights = vector ? n / 8 : 0;
+    for (int64_t q = first; q < eights; q += stride) {
+        const uint2 w = *reinterpret_cast<const uint2*>(codes + q * 8);
+        const float unit = state8_unit(exps[q >> 2]);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = state8_value<SIGNED>(((j < 4 ? w.x : w.y) >> (8 * (j & 3))) & 0xffu, unit);
+        store8(out, dtype, q * 8, v);
+    }
+    for (int64_t i = eights * 8 + first; i < n; i += stride) store1(out, dtype, i, state8_value<SIGNED>(codes[i], state8_unit(exps[i >> 5])));
 }
 
 // ---- AdamW ----
@@ -95,9 +104,10 @@ struct Tensor {
     uint32_t first;      // tile
     int grad_dtype;
     int moments8;
+    int vector;
 };
 
-constexpr int kTile = 2048;      // elements of a tile
+constexpr int kTile = 4096;      // elements of a tile
 constexpr int kTensors = 256;    // of one launch, in the kernel's parameters
 
 struct Tensors {
@@ -117,62 +127,192 @@ __device__ __forceinline__ uint32_t random_bits(int64_t i, uint32_t key) {
     return x ^ (x >> 16);
 }
 
-// A group of 32 elements to a warp.
+// The last tensor whose first tile is at or before `tile`.
+__device__ __forceinline__ uint32_t tensor_of(const Tensors& a, uint32_t tile) {
+    uint32_t lo = 0, hi = a.count;
+    while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (a.t[mid].first <= tile) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Eight elements of a tensor whose pointers allow vector accesses; the four threads
+// beside one another that have a group of 32 take part together (`n` of a thread's elements are
+// the tensor's, and may be none).
+template <bool EIGHT>
+__device__ __forceinline__ void step8(const Tensor& t, const AdamWConsts& c, bool scaled, float scale, int64_t i, int n) {
+    float p[8], g[8], m[8], v[8];
+    uint2 cm = make_uint2(0, 0), cv = cm;
+    uint32_t em = 0, ev = 0;
+    if (n == 8) {
+        load8(t.p, FSDP_DTYPE_F32, i, p);
+        load8(t.g, t.grad_dtype, i, g);
+        if (EIGHT) {
+            cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i);
+            cv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + i);
+        } else {
+            load8(t.m, FSDP_DTYPE_F32, i, m);
+            load8(t.v, FSDP_DTYPE_F32, i, v);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool on = j < n;
+            p[j] = on ? t.p[i + j] : 0.0f;
+            g[j] = on ? load1(t.g, t.grad_dtype, i + j) : 0.0f;
+            if (EIGHT) {
+                uint32_t& wm = j < 4 ? cm.x : cm.y;
+                uint32_t& wv = j < 4 ? cv.x : cv.y;
+                wm |= on ? static_cast<uint32_t>(static_cast<const uint8_t*>(t.m)[i + j]) << (8 * (j & 3)) : 0u;
+                wv |= on ? static_cast<uint32_t>(static_cast<const uint8_t*>(t.v)[i + j]) << (8 * (j & 3)) : 0u;
+            } else {
+                m[j] = on ? static_cast<const float*>(t.m)[i + j] : 0.0f;
+                v[j] = on ? static_cast<const float*>(t.v)[i + j] : 0.0f;
+            }
+        }
+    }
+    if (EIGHT) {
+        if (n > 0) {
+            em = t.me[i >> 5];
+            ev = t.ve[i >> 5];
+        }
+        const float um = state8_unit(em), uv = state8_unit(ev);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            m[j] = state8_value<true>(((j < 4 ? cm.x : cm.y) >> (8 * (j & 3))) & 0xffu, um);
+            v[j] = state8_value<false>(((j < 4 ? cv.x : cv.y) >> (8 * (j & 3))) & 0xffu, uv);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (scaled) g[j] = __fmul_rn(g[j], scale);
+        adamw_elem(p[j], g[j], m[j], v[j], c);
+    }
+    if (EIGHT) {
+        float mt = 0.0f, vt = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            mt = j < n ? larger(mt, m[j]) : mt;
+            vt = j < n ? larger(vt, v[j]) : vt;
+        }
+        uint32_t mb = __float_as_uint(mt), vb = __float_as_uint(vt);
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+            mb = max(mb, __shfl_xor_sync(kAll, mb, d));
+            vb = max(vb, __shfl_xor_sync(kAll, vb, d));
+        }
+        mb = state8_byte(mb);
+        vb = state8_byte(vb);
+        cm = cv = make_uint2(0, 0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t r = random_bits(i + j, t.key);
+            (j < 4 ? cm.x : cm.y) |= state8_code<true>(m[j], mb, (r & 0xffffu) << 4) << (8 * (j & 3));
+            (j < 4 ? cv.x : cv.y) |= state8_code<false>(v[j], vb, (r >> 16) << 4) << (8 * (j & 3));
+        }
+        if (n > 0 && (i & 31) == 0) {
+            t.me[i >> 5] = static_cast<uint8_t>(mb);
+            t.ve[i >> 5] = static_cast<uint8_t>(vb);
+        }
+    }
+    if (n == 8) {
+        store8(t.p, FSDP_DTYPE_F32, i, p);
+        if (t.copy != nullptr) store8(t.copy, FSDP_DTYPE_BF16, i, p);
+        if (EIGHT) {
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + i) = cm;
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i) = cv;
+        } else {
+            store8(t.m, FSDP_DTYPE_F32, i, m);
+            store8(t.v, FSDP_DTYPE_F32, i, v);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j >= n) continue;
+            t.p[i + j] = p[j];
+            if (t.copy != nullptr) store1(t.copy, FSDP_DTYPE_BF16, i + j, p[j]);
+            if (EIGHT) {
+                static_cast<uint8_t*>(t.m)[i + j] = static_cast<uint8_t>((j < 4 ? cm.x : cm.y) >> (8 * (j & 3)));
+                static_cast<uint8_t*>(t.v)[i + j] = static_cast<uint8_t>((j < 4 ? cv.x : cv.y) >> (8 * (j & 3)));
+            } else {
+                static_cast<float*>(t.m)[i + j] = m[j];
+                static_cast<float*>(t.v)[i + j] = v[j];
+            }
+        }
+    }
+}
+
+// The same for tensors that begin anywhere: a group of 32 to a warp, an element to a lane.
+__device__ __forceinline__ void step1(const Tensor& t, const AdamWConsts& c, bool scaled, float scale, int64_t i, bool on) {
+    float p = on ? t.p[i] : 0.0f, g = on ? load1(t.g, t.grad_dtype, i) : 0.0f, m = 0.0f, v = 0.0f;
+    if (scaled) g = __fmul_rn(g, scale);
+    if (on) {
+        if (t.moments8) {
+            m = state8_value<true>(static_cast<uint8_t*>(t.m)[i], state8_unit(t.me[i >> 5]));
+            v = state8_value<false>(static_cast<uint8_t*>(t.v)[i], state8_unit(t.ve[i >> 5]));
+        } else {
+            m = static_cast<float*>(t.m)[i];
+            v = static_cast<float*>(t.v)[i];
+        }
+    }
+    adamw_elem(p, g, m, v, c);
+    if (on) {
+        t.p[i] = p;
+        if (t.copy != nullptr) store1(t.copy, FSDP_DTYPE_BF16, i, p);
+    }
+    if (t.moments8) {
+        const uint32_t r = random_bits(i, t.key);
+        const uint32_t mb = state8_byte(__reduce_max_sync(kAll, on ? __float_as_uint(larger(0.0f, m)) : 0u));
+        const uint32_t vb = state8_byte(__reduce_max_sync(kAll, on ? __float_as_uint(larger(0.0f, v)) : 0u));
+        if (on) {
+            static_cast<uint8_t*>(t.m)[i] = static_cast<uint8_t>(state8_code<true>(m, mb, (r & 0xffffu) << 4));
+            static_cast<uint8_t*>(t.v)[i] = static_cast<uint8_t>(state8_code<false>(v, vb, (r >> 16) << 4));
+        }
+        if ((i & 31) == 0) {
+            t.me[i >> 5] = static_cast<uint8_t>(mb);
+            t.ve[i >> 5] = static_cast<uint8_t>(vb);
+        }
+    } else if (on) {
+        static_cast<float*>(t.m)[i] = m;
+        static_cast<float*>(t.v)[i] = v;
+    }
+}
+
 __global__ void __launch_bounds__(256) adamw_tensors_kernel(const __grid_constant__ Tensors a) {
     starts_early();
     after_previous();
     if (a.skip != nullptr && *a.skip != 0) return;
-    const float scale = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
-    const int lane = threadIdx.x & 31;
+    const bool scaled = a.grad_scale != nullptr;
+    const float scale = scaled ? *a.grad_scale : 1.0f;
     for (uint32_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
-        uint32_t lo = 0, hi = a.count;   // the last tensor whose first tile is at or before this one
-        while (hi - lo > 1) {
-            const uint32_t mid = (lo + hi) / 2;
-            if (a.t[mid].first <= tile) lo = mid;
-            else hi = mid;
-        }
-        const Tensor& t = a.t[lo];
+        const Tensor& t = a.t[tensor_of(a, tile)];
         AdamWConsts c = a.c;
         c.decay = t.decay;
         c.step = t.step;
         const int64_t begin = static_cast<int64_t>(tile - t.first) * kTile, end = min(begin + kTile, t.n);
-        for (int64_t at = begin + (threadIdx.x & ~31); at < end; at += 256) {
-            const int64_t i = at + lane;
-            const bool on = i < end;
-            float p = on ? t.p[i] : 0.0f, g = on ? load1(t.g, t.grad_dtype, i) : 0.0f, m = 0.0f, v = 0.0f;
-            if (a.grad_scale != nullptr) g = __fmul_rn(g, scale);
-            if (t.moments8) {
-                if (on) {
-                    m = state8_value<true>(static_cast<uint8_t*>(t.m)[i], state8_unit(t.me[i >> 5]));
-                    v = state8_value<false>(static_cast<uint8_t*>(t.v)[i], state8_unit(t.ve[i >> 5]));
-                }
-            } else if (on) {
-                m = static_cast<float*>(t.m)[i];
-                v = static_cast<float*>(t.v)[i];
+        if (t.vector) {   // whole warps: a group's threads take part together
+            for (int64_t at = begin + (threadIdx.x & ~31) * 8; at < end; at += 256 * 8) {
+                const int64_t i = at + (threadIdx.x & 31) * 8;
+                const int n = inside8(i, end);
+                if (t.moments8) step8<true>(t, c, scaled, scale, i, n);
+                else step8<false>(t, c, scaled, scale, i, n);
             }
-            adamw_elem(p, g, m, v, c);
-            if (on) {
-                t.p[i] = p;
-                if (t.copy != nullptr) reinterpret_cast<__nv_bfloat16*>(t.copy)[i] = __float2bfloat16_rn(p);
-            }
-            if (t.moments8) {
-                const uint32_t r = random_bits(i, t.key);
-                const uint32_t mb = state8_byte(__reduce_max_sync(kAll, on ? __float_as_uint(larger(0.0f, m)) : 0u));
-                const uint32_t vb = state8_byte(__reduce_max_sync(kAll, on ? __float_as_uint(larger(0.0f, v)) : 0u));
-                if (on) {
-                    static_cast<uint8_t*>(t.m)[i] = static_cast<uint8_t>(state8_code<true>(m, mb, (r & 0xffffu) << 4));
-                    static_cast<uint8_t*>(t.v)[i] = static_cast<uint8_t>(state8_code<false>(v, vb, (r >> 16) << 4));
-                }
-                if (lane == 0) {
-                    t.me[i >> 5] = static_cast<uint8_t>(mb);
-                    t.ve[i >> 5] = static_cast<uint8_t>(vb);
-                }
-            } else if (on) {
-                static_cast<float*>(t.m)[i] = m;
-                static_cast<float*>(t.v)[i] = v;
+        } else {
+            for (int64_t at = begin + (threadIdx.x & ~31); at < end; at += 256) {
+                const int64_t i = at + (threadIdx.x & 31);
+                step1(t, c, scaled, scale, i, i < end);
             }
         }
     }
+}
+
+// Whether step8 may have the tensor.
+bool vector_accesses(const fsdp_adamw_tensor& t) {
+    const auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
+    const uintptr_t moments = at(t.exp_avg) | at(t.exp_avg_sq);
+    return ((at(t.param) | at(t.grad) | at(t.copy_bf16)) & 15) == 0 && (moments & (t.moments == FSDP_MOMENTS_8BIT ? 7 : 15)) == 0;
 }
 
 unsigned blocks_for(int64_t items, int64_t each, int64_t most) { return static_cast<unsigned>(std::min((items + each - 1) / each, most)); }
@@ -188,8 +328,9 @@ cudaError_t launch_state8_pack(int kind, const float* x, int64_t n, uint8_t* cod
 cudaError_t launch_state8_unpack(int kind, const uint8_t* codes, const uint8_t* exps, int64_t n, void* out, int out_dtype,
                                  int sms, cudaStream_t st) {
     if (n == 0) return cudaSuccess;
+    const bool vector = (reinterpret_cast<uintptr_t>(codes) & 7) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
     return launch_early(kind == FSDP_STATE8_SIGNED ? state8_unpack_kernel<true> : state8_unpack_kernel<false>,
-                        dim3(blocks_for(n, 256, sms * 32)), 256, 0, st, codes, exps, n, out, out_dtype);
+                        dim3(blocks_for(n, vector ? 2048 : 256, sms * 16)), 256, 0, st, codes, exps, n, out, out_dtype, vector);
 }
 
 cudaError_t launch_adamw_tensors(const fsdp_adamw_tensor* tensors, int64_t count, const fsdp_adamw_hp& hp, int64_t step,
@@ -211,7 +352,7 @@ cudaError_t launch_adamw_tensors(const fsdp_adamw_tensor* tensors, int64_t count
             const AdamWConsts c = adamw_consts(&own, step);
             const uint64_t key = seed * 0x9E3779B97F4A7C15ull + (static_cast<uint64_t>(j) + 1) * 0xD1B54A32D192ED03ull;
             a.t[a.count++] = Tensor{s.param, s.grad, s.exp_avg, s.exp_avg_sq, s.exp_avg_exps, s.exp_avg_sq_exps, s.copy_bf16, s.numel,
-                                    c.decay, c.step, static_cast<uint32_t>(key >> 32), a.tiles, s.grad_dtype, s.moments == FSDP_MOMENTS_8BIT};
+                                    c.decay, c.step, static_cast<uint32_t>(key >> 32), a.tiles, s.grad_dtype, s.moments == FSDP_MOMENTS_8BIT, vector_accesses(s)};
             a.tiles += static_cast<uint32_t>(tiles);
         }
         if (a.count == 0) continue;

@@ -7,15 +7,10 @@
 
 #include "block_device.cuh"
 #include "compute.hpp"
+#include "rows.cuh"
 
 namespace fsdp {
 namespace {
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    return v;
-}
 
 // Sum over the block; every thread gets it.  `red` holds 32 floats and is free
 // again after the next barrier.
@@ -168,28 +163,6 @@ __device__ __forceinline__ void load_x(const Mat& x, int64_t row, int64_t c, flo
 
 constexpr int kRing = 4;   // rows in the ring, at most
 
-__device__ __forceinline__ uint32_t shared_at(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, uintptr_t src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-// All but the newest `pending` groups have landed.
-__device__ __forceinline__ void copies_wait(int pending) {
-    switch (pending) {
-        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-        default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    }
-}
-
 // Bytes of eight elements.
 __host__ __device__ __forceinline__ int chunk_bytes(int dtype) {
     return dtype == FSDP_DTYPE_F32 ? 32 : dtype == FSDP_DTYPE_BF16 ? 16 : 8;
@@ -287,12 +260,6 @@ struct Out {
 // share its slots).  Read from L1 or L2 with every row instead, they doubled
 // the time: the ring leaves L1 no room for them.
 __device__ __forceinline__ Mat vector_row(const void* p, int dtype) { return Mat{const_cast<void*>(p), nullptr, 0, 0, dtype}; }
-
-__device__ __forceinline__ float both(f32x2 v) {
-    float a, b;
-    unpair(v, a, b);
-    return a + b;
-}
 
 // Sums over a group of NW warps, for all of its threads.  Each warp leaves its
 // own; `red` is one of two buffers used in turn: a thread that writes one again
@@ -826,8 +793,6 @@ cudaError_t run_forward(const NormForward& a, int64_t chunks, int sms, cudaStrea
     return launch_early(norm_forward_kernel<kMost, false, ANY>, blocks(a.rows, threads), threads, 0, st, a);
 }
 
-constexpr int kSharedMost = 222 * 1024;   // dynamic shared memory of a block
-
 // How a row is split: threads to it, chunks (or columns) to a thread, rows to a
 // block.
 struct Split {
@@ -895,16 +860,6 @@ Split backward_split(const NormBackward& a, bool vec) {
 int64_t backward_blocks(const Split& p, int64_t rows, int sms) {
     if (p.NV == 0) return std::max<int64_t>(1, std::min<int64_t>(rows, kWideSlices));
     return walkers(p, rows, sms);
-}
-
-// Launches with `bytes` of dynamic shared memory.
-template <auto kernel, typename... Args>
-cudaError_t launch_shared(unsigned blocks, int threads, int bytes, cudaStream_t st, const Args&... args) {
-    const int allowed = once_per_device([] {
-        return static_cast<int>(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedMost));
-    });
-    if (allowed != cudaSuccess) return static_cast<cudaError_t>(allowed);
-    return launch_early(kernel, dim3(blocks), threads, static_cast<size_t>(bytes), st, args...);
 }
 
 }  // namespace

@@ -4,17 +4,10 @@
 
 #include "block_device.cuh"
 #include "compute.hpp"
+#include "rows.cuh"
 
 namespace fsdp {
 namespace {
-
-constexpr unsigned kAll = 0xffffffffu;
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
-    return v;
-}
 
 // Sums over the block, for every thread.  `red` is free again after the next barrier.
 template <int N>
@@ -182,32 +175,529 @@ __global__ void __launch_bounds__(512) residual_norm_any_backward_kernel(const R
     }
 }
 
+// ---- a chunk to a thread ----
+//
+// Rows of any type and alignment in registers: a row to a block, or to a cluster of blocks
+// that join their sums through one another's shared memory.
+
+constexpr int kMostThreads = 768;   // of a block, which leaves a thread the 80 registers that the backward pass takes
+
+// Sums over the cluster's blocks, for every thread.  `mine` of each block is free again after
+// the cluster's next barrier but one.
+template <int N>
+__device__ __forceinline__ void cluster_sums(float (&v)[N], float (*mine)[4], int cluster) {
+    if (cluster == 1) return;
+    const uint32_t rank = cluster_rank();
+    if (threadIdx.x < static_cast<unsigned>(cluster)) {
+        const uint32_t to = remote_addr(shared_at(mine[rank]), threadIdx.x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4 * i), "f"(v[i]) : "memory");
+    }
+    cluster_sync();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v[i] = 0.0f;
+        for (int j = 0; j < cluster; ++j) v[i] += mine[j][i];
+    }
+}
+
+// load_any, or from 16-byte boundaries.
+template <bool ANY>
+__device__ __forceinline__ void load_part(const void* p, int dtype, int64_t at, int in, float otherwise, float* v) {
+    if (!ANY && p != nullptr) {
+        if (in > 0) {
+            load8(p, dtype, at, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        }
+    } else {
+        load_any(p, dtype, at, in, otherwise, v);
+    }
+}
+template <bool ANY>
+__device__ __forceinline__ void store_part(const Mat& m, int64_t at, int in, const float* v) {
+    if (ANY) store_chunk_any(m.p, m.dtype, at, in, v);
+    else if (in > 0) store8(m.p, m.dtype, at, v);
+}
+
+template <bool ANY>
+__global__ void __launch_bounds__(kMostThreads) residual_norm_kernel(const ResidualNorm a, int cluster) {
+    __shared__ float red[2][1][32];
+    __shared__ float joined[2][8][4];
+    starts_early();
+    after_previous();
+    if (cluster > 1) cluster_sync();   // the others' shared memory is there
+    const float n = static_cast<float>(a.cols);
+    const int64_t c = (static_cast<int64_t>(cluster > 1 ? cluster_rank() : 0) * blockDim.x + threadIdx.x) * 8;
+    const int in = inside8(c, a.cols);
+    for (int64_t row = blockIdx.x / cluster; row < a.rows; row += gridDim.x / cluster) {
+        float s[8], o[8], p[8], g[8], w[8];
+        load_part<ANY>(a.o.p, a.o.dtype, row * a.o.ld + c, in, 0.0f, o);
+        load_part<ANY>(a.h.p, a.h.dtype, row * a.h.ld + c, in, 0.0f, s);
+        load_part<ANY>(a.post, a.param_dtype, c, in, 1.0f, p);
+        load_part<ANY>(a.gate, a.param_dtype, c, in, 1.0f, g);
+        load_part<ANY>(a.gamma, a.param_dtype, c, in, 1.0f, w);
+        float post_rstd = 1.0f;
+        if (a.post != nullptr) {
+            float ss[1] = {0.0f};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss[0] = fmaf(o[j], o[j], ss[0]);
+            block_sums(ss, red[0]);
+            cluster_sums(ss, joined[0], cluster);
+            post_rstd = 1.0f / sqrtf(ss[0] / n + a.eps);
+            if (c == 0) a.post_rstd[row] = post_rstd;
+        }
+        float ss[1] = {0.0f};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            s[j] = fmaf(a.alpha, s[j], o[j] * post_rstd * p[j] * g[j]);
+            if (j < in) ss[0] = fmaf(s[j], s[j], ss[0]);
+        }
+        store_part<ANY>(a.out, row * a.out.ld + c, in, s);
+        if (a.y.p != nullptr) {
+            block_sums(ss, red[1]);
+            cluster_sums(ss, joined[1], cluster);
+            const float rstd = 1.0f / sqrtf(ss[0] / n + a.eps);
+            if (c == 0) a.rstd[row] = rstd;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] = s[j] * rstd * w[j];
+            store_part<ANY>(a.y, row * a.y.ld + c, in, s);
+        }
+        if (a.post == nullptr || a.y.p == nullptr) {   // one barrier a row does not keep the rows' sums apart
+            if (cluster > 1) cluster_sync();
+            else __syncthreads();
+        }
+    }
+}
+
+template <bool ANY>
+__global__ void __launch_bounds__(kMostThreads) residual_norm_backward_kernel(const ResidualNormGrad a, int cluster) {
+    __shared__ float red[2][3][32];
+    __shared__ float joined[2][8][4];
+    starts_early();
+    after_previous();
+    if (cluster > 1) cluster_sync();   // the others' shared memory is there
+    const float inv_n = 1.0f / static_cast<float>(a.cols);
+    const int64_t c = (static_cast<int64_t>(cluster > 1 ? cluster_rank() : 0) * blockDim.x + threadIdx.x) * 8;
+    const int in = inside8(c, a.cols);
+    float dg[8], du[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[j] = du[j] = 0.0f;
+    int flip = 0;
+    for (int64_t row = blockIdx.x / cluster; row < a.rows; row += gridDim.x / cluster) {
+        const float rstd = a.dy.p != nullptr ? a.rstd[row] : 0.0f, post_rstd = a.post != nullptr ? a.post_rstd[row] : 1.0f;
+        float t[8], xh[8], u[8], k[8], w[8], g[8];
+        load_part<ANY>(a.dy.p, a.dy.dtype, row * a.dy.ld + c, in, 0.0f, g);
+        load_part<ANY>(a.dy.p != nullptr ? a.out.p : nullptr, a.out.dtype, row * a.out.ld + c, in, 0.0f, xh);
+        load_part<ANY>(a.dout.p, a.dout.dtype, row * a.dout.ld + c, in, 0.0f, t);
+        load_part<ANY>(a.o.p, a.o.dtype, row * a.o.ld + c, in, 0.0f, u);
+        load_part<ANY>(a.gamma, a.param_dtype, c, in, 1.0f, w);
+        float s[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            xh[j] *= rstd;
+            dg[j] = fmaf(g[j], xh[j], dg[j]);
+            g[j] *= w[j];
+            s[0] = fmaf(g[j], xh[j], s[0]);
+            t[j] = fmaf(rstd, g[j], t[j]);
+        }
+        load_part<ANY>(a.post, a.param_dtype, c, in, 1.0f, k);
+        load_part<ANY>(a.gate, a.param_dtype, c, in, 1.0f, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            k[j] *= w[j];
+            u[j] *= post_rstd;
+            s[1] = fmaf(k[j] * u[j], t[j], s[1]);
+            s[2] = fmaf(k[j] * u[j], xh[j], s[2]);
+        }
+        block_sums(s, red[flip]);
+        cluster_sums(s, joined[flip], cluster);
+        flip ^= 1;
+        // with e = t k and t = dout + rstd (g - xh c1), sum(e u) is linear in c1
+        const float c1 = s[0] * inv_n, c2 = a.post != nullptr ? (s[1] - rstd * c1 * s[2]) * inv_n : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            t[j] = fmaf(-rstd * c1, xh[j], t[j]);
+            du[j] = fmaf(t[j], u[j], du[j]);
+            u[j] = post_rstd * fmaf(-u[j], c2, t[j] * k[j]);
+            t[j] *= a.alpha;
+        }
+        store_part<ANY>(a.dh, row * a.dh.ld + c, in, t);
+        if (a.dblock.p != nullptr) store_part<ANY>(a.dblock, row * a.dblock.ld + c, in, u);
+    }
+    float* part = a.partials + static_cast<int64_t>(blockIdx.x / cluster) * 2 * a.cols + c;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (j < in) {
+            part[j] = dg[j];
+            part[a.cols + j] = du[j];
+        }
+    }
+}
+
+// ---- rows staged through shared memory ----
+//
+// BF16 rows on 16-byte boundaries, as they come in training.  A block holds G groups of
+// GT threads, each with a row; thread t of a group owns its chunks t + k GT, k < NV, and
+// copies the ones of the rows ahead into a ring of shared memory (cp.async), so that
+// it waits for its own copies alone.
+
+constexpr int kMostPlaces = 4;      // rows of a group in the ring
+constexpr int kRingThreads = 512;
+
+struct RingShape {
+    int gt, groups, places;
+};
+
+template <int NV, int M>
+struct Ring {
+    uint8_t* base;
+    int gt, groups, g, t;
+    __device__ uint8_t* slot(int place, int m, int k) const {
+        return base + (((place * M + m) * groups + g) * NV * gt + k * gt + t) * 16;
+    }
+    __device__ void copy(const Mat& x, int64_t row, int place, int m, bool end) const {
+        const uint8_t* from = static_cast<const uint8_t*>(x.p) + (row * x.ld + t * 8) * 2;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (k + 1 < NV || end) copy16(shared_at(slot(place, m, k)), from + k * gt * 16);
+    }
+    __device__ uint4 read(int place, int m, int k) const { return *reinterpret_cast<const uint4*>(slot(place, m, k)); }
+};
+
+__device__ __forceinline__ void pairs(uint4 w, f32x2* v) {
+    v[0] = pair(bf16_lo(w.x), bf16_hi(w.x));
+    v[1] = pair(bf16_lo(w.y), bf16_hi(w.y));
+    v[2] = pair(bf16_lo(w.z), bf16_hi(w.z));
+    v[3] = pair(bf16_lo(w.w), bf16_hi(w.w));
+}
+__device__ __forceinline__ uint4 rounded(const f32x2* v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float a, b;
+        unpair(v[j], a, b);
+        w[j] = to_bf16x2(a, b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ f32x2 twice(float v) { return pair(v, v); }
+
+// The vectors of cols elements, which all groups share: ones where there is none.  Floats
+// lie in two halves of 16 bytes a chunk, so that neighbouring threads' accesses are neighbours.
+template <int NV, bool FLOATS>
+struct Vectors {
+    uint8_t* base;
+    int gt, t;
+    static constexpr int kChunk = FLOATS ? 32 : 16;
+    __device__ uint8_t* slot(int v, int k) const { return base + (v * NV + k) * gt * kChunk + t * 16; }
+    __device__ void fill(const void* p, int v, bool end) const {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (k + 1 < NV || end) {
+                const uint8_t* from = static_cast<const uint8_t*>(p) + (t + k * gt) * kChunk;
+                uint8_t* to = slot(v, k);
+                if (p != nullptr) {
+                    copy16(shared_at(to), from);
+                    if (FLOATS) copy16(shared_at(to + gt * 16), from + 16);
+                } else {
+                    const uint32_t one = FLOATS ? 0x3f800000u : 0x3f803f80u;
+                    *reinterpret_cast<uint4*>(to) = make_uint4(one, one, one, one);
+                    if (FLOATS) *reinterpret_cast<uint4*>(to + gt * 16) = make_uint4(one, one, one, one);
+                }
+            }
+        }
+    }
+    __device__ void read(int v, int k, f32x2* x) const {
+        if (FLOATS) {
+            const float4 a = *reinterpret_cast<const float4*>(slot(v, k)), b = *reinterpret_cast<const float4*>(slot(v, k) + gt * 16);
+            x[0] = pair(a.x, a.y);
+            x[1] = pair(a.z, a.w);
+            x[2] = pair(b.x, b.y);
+            x[3] = pair(b.z, b.w);
+        } else {
+            pairs(*reinterpret_cast<const uint4*>(slot(v, k)), x);
+        }
+    }
+};
+
+// Sums over a group, for all of its threads.  `red` is one of two buffers used in turn: a thread
+// that writes one again has passed the barrier behind which every thread had read it.
+template <int N>
+__device__ __forceinline__ void group_sums(float (&v)[N], float4* red, int group, int gt) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+    const int warps = gt >> 5;
+    if (warps == 1) return;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float4(v[0], N > 1 ? v[N > 1] : 0.0f, N > 2 ? v[N > 2 ? 2 : 0] : 0.0f, 0.0f);
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(gt) : "memory");
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = 0; i < warps; ++i) {
+        const float4 r = red[group * warps + i];
+        s.x += r.x;
+        s.y += r.y;
+        s.z += r.z;
+    }
+    v[0] = s.x;
+    if (N > 1) v[N > 1] = s.y;
+    if (N > 2) v[N > 2 ? 2 : 0] = s.z;
+}
+
+template <int NV, bool FLOATS>
+__global__ void __launch_bounds__(kRingThreads) residual_norm_ring_kernel(const __grid_constant__ ResidualNorm a, const RingShape shape) {
+    extern __shared__ __align__(16) uint8_t ring_bytes[];
+    __shared__ float4 red[2][kRingThreads / 32];
+    starts_early();
+    after_previous();
+    const int gt = shape.gt, places = shape.places, g = threadIdx.x / gt, t = threadIdx.x % gt;
+    const bool end = (t + (NV - 1) * gt) * 8 < a.cols;
+    const Vectors<NV, FLOATS> vec{ring_bytes, gt, t};
+    const Ring<NV, 2> ring{ring_bytes + 3 * NV * gt * vec.kChunk, gt, shape.groups, g, t};
+    if (g == 0) {
+        vec.fill(a.post, 0, end);
+        vec.fill(a.gate, 1, end);
+        vec.fill(a.gamma, 2, end);
+        copies_end();
+        copies_wait(0);
+    }
+    __syncthreads();
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * shape.groups, first = static_cast<int64_t>(blockIdx.x) * shape.groups + g;
+    const float n = static_cast<float>(a.cols);
+    const auto issue = [&](int64_t row, int place) {
+        if (row < a.rows) {
+            ring.copy(a.o, row, place, 0, end);
+            ring.copy(a.h, row, place, 1, end);
+        }
+        copies_end();
+    };
+    for (int s = 0; s + 1 < places; ++s) issue(first + s * stride, s);
+    int place = 0;
+    for (int64_t row = first; row < a.rows; row += stride) {
+        issue(row + (places - 1) * stride, place == 0 ? places - 1 : place - 1);
+        copies_wait(places - 1);
+        f32x2 o[NV][4], s[NV][4];
+        f32x2 ss = 0;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const bool on = k + 1 < NV || end;
+            pairs(on ? ring.read(place, 0, k) : make_uint4(0, 0, 0, 0), o[k]);
+            pairs(on ? ring.read(place, 1, k) : make_uint4(0, 0, 0, 0), s[k]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ss = fma2(o[k][j], o[k][j], ss);
+        }
+        place = place + 1 == places ? 0 : place + 1;
+        float post_rstd = 1.0f;
+        if (a.post != nullptr) {
+            float sum[1] = {both(ss)};
+            group_sums(sum, red[0], g, gt);
+            post_rstd = 1.0f / sqrtf(sum[0] / n + a.eps);
+            if (t == 0) a.post_rstd[row] = post_rstd;
+        }
+        ss = 0;
+        uint8_t* out = static_cast<uint8_t*>(a.out.p) + (row * a.out.ld + t * 8) * 2;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (k + 1 < NV || end) {
+                f32x2 p[4], w[4];
+                vec.read(0, k, p);
+                vec.read(1, k, w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const f32x2 b = mul2(mul2(mul2(o[k][j], twice(post_rstd)), p[j]), w[j]);
+                    s[k][j] = fma2(s[k][j], twice(a.alpha), b);
+                    ss = fma2(s[k][j], s[k][j], ss);
+                }
+                *reinterpret_cast<uint4*>(out + k * gt * 16) = rounded(s[k]);
+            }
+        }
+        float sum[1] = {both(ss)};
+        group_sums(sum, red[1], g, gt);
+        const float rstd = 1.0f / sqrtf(sum[0] / n + a.eps);
+        if (t == 0) a.rstd[row] = rstd;
+        uint8_t* y = static_cast<uint8_t*>(a.y.p) + (row * a.y.ld + t * 8) * 2;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (k + 1 < NV || end) {
+                f32x2 w[4];
+                vec.read(2, k, w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[k][j] = mul2(mul2(s[k][j], twice(rstd)), w[j]);
+                *reinterpret_cast<uint4*>(y + k * gt * 16) = rounded(s[k]);
+            }
+        }
+        if (a.post == nullptr) asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "r"(gt) : "memory");   // keeps the rows' sums apart
+    }
+}
+
+template <int NV, bool FLOATS>
+__global__ void __launch_bounds__(kRingThreads) residual_norm_backward_ring_kernel(const __grid_constant__ ResidualNormGrad a,
+                                                                                   const RingShape shape) {
+    extern __shared__ __align__(16) uint8_t ring_bytes[];
+    __shared__ float4 red[2][kRingThreads / 32];
+    starts_early();
+    after_previous();
+    const int gt = shape.gt, places = shape.places, g = threadIdx.x / gt, t = threadIdx.x % gt;
+    const bool end = (t + (NV - 1) * gt) * 8 < a.cols;
+    const Vectors<NV, FLOATS> vec{ring_bytes, gt, t};
+    const Ring<NV, 4> ring{ring_bytes + 3 * NV * gt * vec.kChunk, gt, shape.groups, g, t};
+    if (g == 0) {
+        vec.fill(a.post, 0, end);
+        vec.fill(a.gate, 1, end);
+        vec.fill(a.gamma, 2, end);
+        copies_end();
+        copies_wait(0);
+    }
+    __syncthreads();
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * shape.groups, first = static_cast<int64_t>(blockIdx.x) * shape.groups + g;
+    const float inv_n = 1.0f / static_cast<float>(a.cols);
+    const auto issue = [&](int64_t row, int place) {
+        if (row < a.rows) {
+            ring.copy(a.dy, row, place, 0, end);
+            ring.copy(a.dout, row, place, 1, end);
+            ring.copy(a.out, row, place, 2, end);
+            ring.copy(a.o, row, place, 3, end);
+        }
+        copies_end();
+    };
+    for (int s = 0; s < places; ++s) issue(first + s * stride, s);
+    f32x2 dg[NV][4], du[NV][4];
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dg[k][j] = du[k][j] = 0;
+    int place = 0, flip = 0;
+    for (int64_t row = first; row < a.rows; row += stride) {
+        const float r1 = a.rstd[row], r2 = a.post != nullptr ? a.post_rstd[row] : 1.0f;
+        const f32x2 rstd = twice(r1), post_rstd = twice(r2);
+        copies_wait(places - 1);
+        // the row's words stay in registers, and their places take the rows ahead at once
+        uint4 raw[NV][4];
+        f32x2 s1 = 0, s2 = 0, s3 = 0;
+        const auto expand = [&](const uint4* w, int k, f32x2* xh, f32x2* tt, f32x2* u, f32x2* gr, f32x2* dy) {
+            pairs(w[0], dy);
+            pairs(w[1], tt);
+            pairs(w[2], xh);
+            pairs(w[3], u);
+            vec.read(2, k, gr);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                xh[j] = mul2(xh[j], rstd);
+                gr[j] = mul2(dy[j], gr[j]);
+                tt[j] = fma2(rstd, gr[j], tt[j]);
+                u[j] = mul2(u[j], post_rstd);
+            }
+        };
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) raw[k][m] = k + 1 < NV || end ? ring.read(place, m, k) : make_uint4(0, 0, 0, 0);
+            if (k + 1 < NV || end) {
+                f32x2 xh[4], tt[4], u[4], x[4], dy[4], p[4], w[4];
+                expand(raw[k], k, xh, tt, u, x, dy);
+                vec.read(0, k, p);
+                vec.read(1, k, w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    dg[k][j] = fma2(dy[j], xh[j], dg[k][j]);
+                    s1 = fma2(x[j], xh[j], s1);
+                    const f32x2 ku = mul2(mul2(p[j], w[j]), u[j]);
+                    s2 = fma2(ku, tt[j], s2);
+                    s3 = fma2(ku, xh[j], s3);
+                }
+            }
+        }
+        issue(row + places * stride, place);
+        place = place + 1 == places ? 0 : place + 1;
+        float sum[3] = {both(s1), both(s2), both(s3)};
+        group_sums(sum, red[flip], g, gt);
+        flip ^= 1;
+        const float c1 = sum[0] * inv_n, c2 = a.post != nullptr ? (sum[1] - r1 * c1 * sum[2]) * inv_n : 0.0f;
+        const f32x2 less1 = twice(-r1 * c1), less2 = twice(-c2), alpha = twice(a.alpha);
+        uint8_t* dh = static_cast<uint8_t*>(a.dh.p) + (row * a.dh.ld + t * 8) * 2;
+        uint8_t* db = static_cast<uint8_t*>(a.dblock.p) + (row * a.dblock.ld + t * 8) * 2;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (k + 1 < NV || end) {
+                f32x2 xh[4], tt[4], u[4], x[4], dy[4], p[4], w[4];
+                expand(raw[k], k, xh, tt, u, x, dy);
+                vec.read(0, k, p);
+                vec.read(1, k, w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    tt[j] = fma2(less1, xh[j], tt[j]);
+                    du[k][j] = fma2(tt[j], u[j], du[k][j]);
+                    u[j] = mul2(post_rstd, fma2(u[j], less2, mul2(tt[j], mul2(p[j], w[j]))));
+                    tt[j] = mul2(tt[j], alpha);
+                }
+                *reinterpret_cast<uint4*>(dh + k * gt * 16) = rounded(tt);
+                *reinterpret_cast<uint4*>(db + k * gt * 16) = rounded(u);
+            }
+        }
+    }
+    // the groups' column sums meet in shared memory: element j of chunk i at j * slots + i
+    copies_wait(0);
+    __syncthreads();
+    const int slots = NV * gt + 4;
+    float* comb = reinterpret_cast<float*>(ring_bytes);
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float* to = comb + (g * 16 + 2 * j) * slots + t + k * gt;
+            unpair(dg[k][j], to[0], to[slots]);
+            unpair(du[k][j], to[8 * slots], to[9 * slots]);
+        }
+    __syncthreads();
+    float* part = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+            const float* from = comb + (o * 8 + (c & 7)) * slots + (c >> 3);
+            float s = from[0];
+            for (int h = 1; h < shape.groups; ++h) s += from[h * 16 * slots];
+            part[o * a.cols + c] = s;
+        }
+}
+
 // The columns' sums over the blocks, in their order: dgamma from the first half of the
-// partial rows, dpost_gamma and dgate from the second.  16 columns across and 16
-// slices of the blocks down.
+// partial rows, dpost_gamma and dgate from the second.  16 threads of V columns across and
+// 16 slices of the blocks down.
+template <int V>
 __global__ void __launch_bounds__(256) residual_norm_sums_kernel(const ResidualNormGrad a, int64_t count) {
-    __shared__ float part[16][17];
+    __shared__ float part[16][16 * V];
     starts_early();
     after_previous();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 16 + tx;
+    const int64_t c = (static_cast<int64_t>(blockIdx.x) * 16 + tx) * V;
     const float* p = a.partials + blockIdx.y * a.cols + c;
-    float s = 0.0f;
+    float s[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[j] = 0.0f;
     if (c < a.cols) {
 #pragma unroll 10
-        for (int64_t i = ty; i < count; i += 16) s += __ldcg(p + i * 2 * a.cols);
+        for (int64_t i = ty; i < count; i += 16) {
+            if constexpr (V == 4) {
+                const float4 f = __ldcg(reinterpret_cast<const float4*>(p + i * 2 * a.cols));
+                s[0] += f.x; s[1] += f.y; s[2] += f.z; s[3] += f.w;
+            } else {
+                s[0] += __ldcg(p + i * 2 * a.cols);
+            }
+        }
     }
-    part[ty][tx] = s;
-    __syncthreads();
-    if (ty != 0 || c >= a.cols) return;
-    s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s += part[i][tx];
+    for (int j = 0; j < V; ++j) part[ty][tx * V + j] = s[j];
+    __syncthreads();
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 16 * V + threadIdx.x;
+    if (threadIdx.x >= 16 * V || col >= a.cols) return;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum += part[i][threadIdx.x];
     const auto put = [&](void* out, const void* by) {
         if (out == nullptr) return;
-        float v = by != nullptr ? s * load1(by, a.param_dtype, c) : s;
-        if (a.accumulate) v += load1(out, a.grad_dtype, c);
-        store1(out, a.grad_dtype, c, v);
+        float v = by != nullptr ? sum * load1(by, a.param_dtype, col) : sum;
+        if (a.accumulate) v += load1(out, a.grad_dtype, col);
+        store1(out, a.grad_dtype, col, v);
     };
     if (blockIdx.y == 0) {
         put(a.dgamma, nullptr);
@@ -219,24 +709,111 @@ __global__ void __launch_bounds__(256) residual_norm_sums_kernel(const ResidualN
 
 constexpr int kSms = 152;
 
+int round32(int64_t n) { return static_cast<int>((n + 31) / 32 * 32); }
+
+// How a chunk to a thread is laid out: 0 threads where eight blocks do not hold a row.
+struct Spread {
+    int threads = 0, cluster = 1, blocks = 1;   // blocks (or clusters) that run at once on an SM (or its share of SMs)
+};
+Spread spread(int64_t cols) {
+    const int64_t chunks = (cols + 7) / 8;
+    Spread s;
+    while (s.cluster <= 8 && chunks > static_cast<int64_t>(s.cluster) * kMostThreads) s.cluster *= 2;
+    if (s.cluster > 8) return s;
+    s.threads = round32((chunks + s.cluster - 1) / s.cluster);
+    s.blocks = std::min(8, kMostThreads / s.threads);
+    return s;
+}
+
+bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool aligned_or_none(const Mat& m) { return m.p == nullptr || rows_aligned(m); }
+
+// Groups and places of the ring for `matrices` rows of BF16; NV 0 where they do not fit.
+int ring_shape(int64_t rows, int64_t cols, int matrices, int param_dtype, int places, RingShape* s, int* bytes) {
+    const int64_t chunks = cols / 8;
+    const int nv = static_cast<int>((chunks + kRingThreads - 1) / kRingThreads);
+    if (nv > 3) return 0;
+    s->gt = round32((chunks + nv - 1) / nv);
+    if (static_cast<int64_t>(nv - 1) * s->gt >= chunks) return 0;
+    s->groups = static_cast<int>(std::min<int64_t>(std::min(kRingThreads / s->gt, 15), rows));
+    const int keep = 3 * nv * s->gt * (param_dtype == FSDP_DTYPE_F32 ? 32 : 16), row = matrices * nv * s->gt * 16;
+    s->places = std::min(kMostPlaces, (kSharedMost - keep) / (row * s->groups));
+    *bytes = keep + s->places * s->groups * row;
+    return s->places >= places ? nv : 0;
+}
+
 }  // namespace
 
-int64_t residual_norm_blocks(int64_t rows, int64_t) { return std::min<int64_t>(rows, 2 * kSms); }
+int64_t residual_norm_blocks(int64_t rows, int64_t cols) { return std::min<int64_t>(rows, kSms * spread(cols).blocks); }
 
 cudaError_t launch_residual_norm_forward(const ResidualNorm& a, int sms, cudaStream_t st) {
     if (a.rows == 0) return cudaSuccess;
+    const bool aligned = a.cols % 8 == 0 && rows_aligned(a.h) && aligned_or_none(a.o) && rows_aligned(a.out) && aligned_or_none(a.y) &&
+                         on16(a.post) && on16(a.gate) && on16(a.gamma);
+    const bool fast = aligned && a.o.p != nullptr && a.y.p != nullptr && a.h.dtype == FSDP_DTYPE_BF16 && a.o.dtype == FSDP_DTYPE_BF16 &&
+                      a.out.dtype == FSDP_DTYPE_BF16 && a.y.dtype == FSDP_DTYPE_BF16;
+    RingShape shape;
+    int bytes = 0;
+    const int nv = fast ? ring_shape(a.rows, a.cols, 2, a.param_dtype, 2, &shape, &bytes) : 0;
+    if (nv != 0 && a.rows >= 2 * static_cast<int64_t>(sms) * shape.groups) {   // rows enough for every group to walk two
+        const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((a.rows + shape.groups - 1) / shape.groups, sms));
+        const int threads = shape.gt * shape.groups;
+        const bool floats = a.param_dtype == FSDP_DTYPE_F32;
+#define RING(nv_)                                                                                                             \
+    if (nv == nv_)                                                                                                            \
+        return floats ? launch_shared<residual_norm_ring_kernel<nv_, true>>(blocks, threads, bytes, st, a, shape)            \
+                      : launch_shared<residual_norm_ring_kernel<nv_, false>>(blocks, threads, bytes, st, a, shape);
+        RING(1) RING(2) RING(3)
+#undef RING
+    }
+    const Spread s = spread(a.cols);
+    if (s.threads != 0) {
+        const int64_t most = std::max<int64_t>(1, static_cast<int64_t>(sms) * std::min(16, 2048 / s.threads) / s.cluster);
+        const dim3 grid(static_cast<unsigned>(std::min(a.rows, most) * s.cluster));
+        return launch_early_clusters(aligned ? residual_norm_kernel<false> : residual_norm_kernel<true>, grid, s.threads, 0, s.cluster, st, a, s.cluster);
+    }
     return launch_early(residual_norm_any_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t(1) << 30))), 512, 0, st, a);
 }
 
 cudaError_t launch_residual_norm_backward(const ResidualNormGrad& a, int sms, cudaStream_t st) {
-    const int64_t blocks = residual_norm_blocks(a.rows, a.cols);
+    const bool aligned = a.cols % 8 == 0 && aligned_or_none(a.dy) && aligned_or_none(a.dout) && aligned_or_none(a.out) && aligned_or_none(a.o) &&
+                         rows_aligned(a.dh) && aligned_or_none(a.dblock) && on16(a.post) && on16(a.gate) && on16(a.gamma);
+    const bool fast = aligned && a.dy.p != nullptr && a.dout.p != nullptr && a.o.p != nullptr && a.dy.dtype == FSDP_DTYPE_BF16 &&
+                      a.dout.dtype == FSDP_DTYPE_BF16 && a.out.dtype == FSDP_DTYPE_BF16 && a.o.dtype == FSDP_DTYPE_BF16 &&
+                      a.dh.dtype == FSDP_DTYPE_BF16 && a.dblock.dtype == FSDP_DTYPE_BF16;
+    int64_t count = 0;   // of partial rows
+    cudaError_t e = cudaSuccess;
     if (a.rows > 0) {
-        const cudaError_t e = launch_early(residual_norm_any_backward_kernel, dim3(static_cast<unsigned>(blocks)), 512, 0, st, a);
-        if (e != cudaSuccess) return e;
+        RingShape shape;
+        int bytes = 0;
+        const int nv = fast ? ring_shape(a.rows, a.cols, 4, a.param_dtype, 1, &shape, &bytes) : 0;
+        const Spread s = spread(a.cols);
+        if (nv != 0) {
+            count = std::min<int64_t>((a.rows + shape.groups - 1) / shape.groups, sms);
+            const unsigned blocks = static_cast<unsigned>(count);
+            const int threads = shape.gt * shape.groups;
+            bytes = std::max(bytes, shape.groups * 16 * (nv * shape.gt + 4) * 4);
+            const bool floats = a.param_dtype == FSDP_DTYPE_F32;
+            e = cudaErrorInvalidConfiguration;
+#define RING(nv_)                                                                                                          \
+    if (nv == nv_)                                                                                                         \
+        e = floats ? launch_shared<residual_norm_backward_ring_kernel<nv_, true>>(blocks, threads, bytes, st, a, shape)    \
+                   : launch_shared<residual_norm_backward_ring_kernel<nv_, false>>(blocks, threads, bytes, st, a, shape);
+            RING(1) RING(2) RING(3)
+#undef RING
+        } else if (s.threads != 0) {
+            count = std::min(a.rows, std::max<int64_t>(1, static_cast<int64_t>(sms) * s.blocks / s.cluster));
+            e = launch_early_clusters(aligned ? residual_norm_backward_kernel<false> : residual_norm_backward_kernel<true>,
+                                      dim3(static_cast<unsigned>(count * s.cluster)), s.threads, 0, s.cluster, st, a, s.cluster);
+        } else {
+            count = std::min<int64_t>(a.rows, sms);
+            e = launch_early(residual_norm_any_backward_kernel, dim3(static_cast<unsigned>(count)), 512, 0, st, a);
+        }
     }
-    if (a.dgamma == nullptr && a.dpost == nullptr && a.dgate == nullptr) return cudaSuccess;
-    const dim3 grid(static_cast<unsigned>((a.cols + 15) / 16), 2);
-    return launch_early(residual_norm_sums_kernel, grid, 256, 0, st, a, blocks);
+    if (e != cudaSuccess || (a.dgamma == nullptr && a.dpost == nullptr && a.dgate == nullptr)) return e;
+    const bool vec = a.cols % 4 == 0;   // the workspace is aligned
+    const dim3 grid(static_cast<unsigned>(vec ? (a.cols + 63) / 64 : (a.cols + 15) / 16), 2);
+    return launch_early(vec ? residual_norm_sums_kernel<4> : residual_norm_sums_kernel<1>, grid, 256, 0, st, a, count);
 }
 
 }  // namespace fsdp
