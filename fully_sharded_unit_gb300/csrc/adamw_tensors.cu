@@ -53,6 +53,78 @@ __device__ __forceinline__ float state8_value(uint32_t code, float unit) {
     return SIGNED && (code & 0x80u) ? -f : f;
 }
 
+// Eight codes of one group.  Up to an exponent byte of kPlain the two scalings of a value are one
+// multiplication by a normal or subnormal power of two, and no code needs its limit; larger
+// groups (magnitudes from 2^15) take the steps one by one.
+constexpr uint32_t kPlain = 142;
+
+template <bool SIGNED>
+__device__ __forceinline__ void state8_values(uint2 w, uint32_t byte, float* v) {
+    if (byte <= kPlain) {
+        const float by = byte == 0 ? 0.0f : __uint_as_float((byte + (SIGNED ? 112u : 96u)) << 23);
+        const f32x2 by2 = pair(by, by);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            uint32_t b[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {   // the code as the float's top byte, then where it belongs
+                const uint32_t top = __byte_perm(j < 4 ? w.x : w.y, 0, (((j + h) & 3) << 12) | 0x0444);
+                b[h] = SIGNED ? static_cast<uint32_t>(static_cast<int32_t>(top) >> 4) & 0x87ffffffu : top >> 4;
+            }
+            unpair(mul2(pair(__uint_as_float(b[0]), __uint_as_float(b[1])), by2), v[j], v[j + 1]);
+        }
+    } else {
+        const float unit = state8_unit(byte);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = state8_value<SIGNED>(((j < 4 ? w.x : w.y) >> (8 * (j & 3))) & 0xffu, unit);
+    }
+}
+
+// Four words' top bytes.
+__device__ __forceinline__ uint32_t top_bytes(const uint32_t* t) {
+    return __byte_perm(__byte_perm(t[0], t[1], 0x0073), __byte_perm(t[2], t[3], 0x0073), 0x5410);
+}
+
+// `random`: what is added below each code, 20 bits.
+template <bool SIGNED>
+__device__ __forceinline__ uint2 state8_codes(const float* x, uint32_t byte, const uint32_t* random) {
+    uint32_t w[2] = {0, 0};
+    if (byte <= kPlain) {
+        // 2^(15-B) or 2^(31-B): 2^-127 at the least, a subnormal number
+        const int e = (SIGNED ? 142 : 158) - static_cast<int>(byte);
+        const float by = __uint_as_float(e > 0 ? static_cast<uint32_t>(e) << 23 : 0x400000u);
+        const f32x2 by2 = pair(by, by);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint32_t t[4];
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+                const int i = 4 * q + j;
+                float a, b;
+                unpair(mul2(pair(x[i], x[i + 1]), by2), a, b);
+                if (SIGNED) {
+                    t[j] = ((__float_as_uint(a) & 0x7fffffffu) + random[i]) << 4;
+                    t[j + 1] = ((__float_as_uint(b) & 0x7fffffffu) + random[i + 1]) << 4;
+                } else {   // an element that is not 0 is at least the first code
+                    t[j] = max(__float_as_uint(a) + random[i], x[i] > 0.0f ? 0x100000u : 0u) << 4;
+                    t[j + 1] = max(__float_as_uint(b) + random[i + 1], x[i + 1] > 0.0f ? 0x100000u : 0u) << 4;
+                }
+            }
+            w[q] = top_bytes(t);
+            if (SIGNED) {   // the sign, of codes that are not 0
+                uint32_t b[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(x[4 * q + j]);
+                w[q] |= top_bytes(b) & (w[q] + 0x7f7f7f7fu) & 0x80808080u;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j >> 2] |= state8_code<SIGNED>(x[j], byte, random[j]) << (8 * (j & 3));
+    }
+    return make_uint2(w[0], w[1]);
+}
+
 __device__ __forceinline__ float magnitude(float x, bool is_signed) { return is_signed ? x : max_nan(x, 0.0f); }
 
 template <bool SIGNED>
@@ -79,10 +151,8 @@ __global__ void __launch_bounds__(256) state8_unpack_kernel(const uint8_t* codes
     const int64_t eights = vector ? n / 8 : 0;
     for (int64_t q = first; q < eights; q += stride) {
         const uint2 w = *reinterpret_cast<const uint2*>(codes + q * 8);
-        const float unit = state8_unit(exps[q >> 2]);
         float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = state8_value<SIGNED>(((j < 4 ? w.x : w.y) >> (8 * (j & 3))) & 0xffu, unit);
+        state8_values<SIGNED>(w, exps[q >> 2], v);
         store8(out, dtype, q * 8, v);
     }
     for (int64_t i = eights * 8 + first; i < n; i += stride) store1(out, dtype, i, state8_value<SIGNED>(codes[i], state8_unit(exps[i >> 5])));
@@ -119,12 +189,34 @@ struct Tensors {
 };
 
 __device__ __forceinline__ uint32_t random_bits(int64_t i, uint32_t key) {
-    uint32_t x = static_cast<uint32_t>(i) ^ key ^ static_cast<uint32_t>(i >> 32) * 0x85157AF5u;
+    uint32_t x = static_cast<uint32_t>(i) ^ (key ^ static_cast<uint32_t>(i >> 32) * 0x85157AF5u);
     x ^= x >> 16;
     x *= 0xD36F86A9u;
     x ^= x >> 15;
     x *= 0xC242E759u;
     return x ^ (x >> 16);
+}
+
+// adamw_elem for two elements beside one another: the same operations, each rounded by itself, the
+// products in one instruction for both.  The sums are scalar: the compiler joins an add2 with
+// the mul2 before it into one rounding.
+__device__ __forceinline__ void adamw_pair(float* p, const float* g, float* m, float* v, const AdamWConsts& c) {
+    const f32x2 g2 = pair(g[0], g[1]);
+    float pd[2], om[2], gm[2], ov[2], gv[2], q[2];
+    unpair(mul2(pair(p[0], p[1]), pair(c.decay, c.decay)), pd[0], pd[1]);
+    unpair(mul2(pair(m[0], m[1]), pair(c.b1, c.b1)), om[0], om[1]);
+    unpair(mul2(g2, pair(c.c1, c.c1)), gm[0], gm[1]);
+    unpair(mul2(pair(v[0], v[1]), pair(c.b2, c.b2)), ov[0], ov[1]);
+    unpair(mul2(mul2(g2, g2), pair(c.c2, c.c2)), gv[0], gv[1]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        m[j] = __fadd_rn(om[j], gm[j]);
+        v[j] = __fadd_rn(ov[j], gv[j]);
+        q[j] = __fdiv_rn(m[j], __fadd_rn(__fsqrt_rn(__fdiv_rn(v[j], c.bc2)), c.eps));
+    }
+    unpair(mul2(pair(q[0], q[1]), pair(c.step, c.step)), q[0], q[1]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) p[j] = __fsub_rn(pd[j], q[j]);
 }
 
 // The last tensor whose first tile is at or before `tile`.
@@ -178,18 +270,15 @@ __device__ __forceinline__ void step8(const Tensor& t, const AdamWConsts& c, boo
             em = t.me[i >> 5];
             ev = t.ve[i >> 5];
         }
-        const float um = state8_unit(em), uv = state8_unit(ev);
+        state8_values<true>(cm, em, m);
+        state8_values<false>(cv, ev, v);
+    }
+    if (scaled) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            m[j] = state8_value<true>(((j < 4 ? cm.x : cm.y) >> (8 * (j & 3))) & 0xffu, um);
-            v[j] = state8_value<false>(((j < 4 ? cv.x : cv.y) >> (8 * (j & 3))) & 0xffu, uv);
-        }
+        for (int j = 0; j < 8; ++j) g[j] = __fmul_rn(g[j], scale);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (scaled) g[j] = __fmul_rn(g[j], scale);
-        adamw_elem(p[j], g[j], m[j], v[j], c);
-    }
+    for (int j = 0; j < 8; j += 2) adamw_pair(p + j, g + j, m + j, v + j, c);
     if (EIGHT) {
         float mt = 0.0f, vt = 0.0f;
 #pragma unroll
@@ -205,13 +294,15 @@ __device__ __forceinline__ void step8(const Tensor& t, const AdamWConsts& c, boo
         }
         mb = state8_byte(mb);
         vb = state8_byte(vb);
-        cm = cv = make_uint2(0, 0);
+        uint32_t rm[8], rv[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const uint32_t r = random_bits(i + j, t.key);
-            (j < 4 ? cm.x : cm.y) |= state8_code<true>(m[j], mb, (r & 0xffffu) << 4) << (8 * (j & 3));
-            (j < 4 ? cv.x : cv.y) |= state8_code<false>(v[j], vb, (r >> 16) << 4) << (8 * (j & 3));
+            rm[j] = r << 4 & 0xffff0u;
+            rv[j] = r >> 12 & 0xffff0u;
         }
+        cm = state8_codes<true>(m, mb, rm);
+        cv = state8_codes<false>(v, vb, rv);
         if (n > 0 && (i & 31) == 0) {
             t.me[i >> 5] = static_cast<uint8_t>(mb);
             t.ve[i >> 5] = static_cast<uint8_t>(vb);
@@ -280,7 +371,7 @@ __device__ __forceinline__ void step1(const Tensor& t, const AdamWConsts& c, boo
     }
 }
 
-__global__ void __launch_bounds__(256) adamw_tensors_kernel(const __grid_constant__ Tensors a) {
+__global__ void __launch_bounds__(256, 4) adamw_tensors_kernel(const __grid_constant__ Tensors a) {
     starts_early();
     after_previous();
     if (a.skip != nullptr && *a.skip != 0) return;

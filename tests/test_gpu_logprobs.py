@@ -3,8 +3,8 @@ definitions in 64 bits.
 
 Bounds.  With d2 = (z - max) scale log2 e, a term 2^d2 is off by 2^-22 (the exponential) and
 2^-23 |d2| ln 2 (two roundings of its argument); weighted by the terms the second is below 2^-23 (H + ln S).
-A thread adds n terms (2^-24 each) and rescales its sums at most once a group of 16 or 32 and 21 times
-on the way to the block's (2^-22 each, and as much again for the distance moved).  `_eps` adds
+A row has 128 threads at least.  A thread adds n terms (2^-24 each) and rescales its sums at most once a
+group of 16 or 32 and 21 times on the way to the block's (2^-22 each, and as much again for the distance moved).  `_eps` adds
 these up; ln S is off by that and by its own roundings."""
 import math
 
@@ -64,7 +64,7 @@ def _reference(z, t, scale):
 
 
 def _eps(vocab, h, ln_s):
-    n = -(-vocab // 512) + 8
+    n = -(-vocab // 128) + 8
     return 2.0 ** -22 * (1 + h + np.abs(ln_s) + 2 * (n / 16 + 22)) + 2.0 ** -24 * (n + 40)
 
 
@@ -124,7 +124,7 @@ def _wanted_grad(z, t, scale, a, b, h=None):
 
 CASES = [(1, 1, BF, 0, 1.0, 1), (3, 2, F32, 0, 1.0, 2), (5, 40, BF, 3, 0.7, 32), (2, 257, F32, 1, 1.5, 5), (7, 1283, BF, 0, 1.0, 20),
          (4, 4096, BF, 8, 1.0, 1), (3, 4099, F32, 0, 2.0, 32), (9, 50257, BF, 0, 1.0, 20), (3, 50257, F32, 47, 1.25, 7),
-         (2, 70001, BF, 5, 0.25, 3)]
+         (2, 70001, BF, 5, 0.25, 3), (1300, 4099, BF, 0, 1.0, 20), (600, 2053, F32, 3, 1.0, 32)]
 
 
 @pytest.mark.parametrize("rows,vocab,dtype,pad,scale,top", CASES)
@@ -235,7 +235,7 @@ def test_a_token_outside_the_vocabulary(c):
 def test_alternatives_that_one_list_holds(c, dtype, each):
     """Logits placed so that the largest ones all belong to a few threads: more candidates than
     there is room for, in rising, falling and equal order."""
-    vocab = 400000
+    vocab = 4000000
     i = torch.arange(vocab, device="cuda")
     mine = (i // each) % 512 < 3
     z = torch.zeros((3, vocab), device="cuda")
@@ -264,13 +264,16 @@ def test_no_rows_and_no_tokens(c):
 
 
 def test_many_rows(c):
-    """More rows than blocks run at once; every row is as if it were alone."""
+    """More rows than blocks run at once.  A row alone is split over more threads: both are within eps."""
     z, t = _logits(3001, 300, BF, seed=4)
     lp, _, h = _check_forward(c, z, t, 1.0, 5)
     one = torch.empty(1, device="cuda")
     for r in (0, 1500, 3000):
         c.token_logprobs_forward(z[r:r + 1], t[r:r + 1], one)
-        assert torch.equal(one, lp[r:r + 1])
+        if torch.isfinite(lp[r]):
+            assert abs(one.item() - lp[r].item()) <= 2 * _eps(300, 6.0, 6.0) + 2.0 ** -22 * (abs(lp[r].item()) + 6)
+        else:
+            assert one.item() == lp[r].item()
 
 
 def test_offsets_beyond_32_bits(c):
