@@ -316,6 +316,16 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
+// A barrier of the cluster for what the first warp has stored in the other blocks' shared memory.
+// The other warps do not wait for their own stores to global memory to be complete.  Warps arrive whole:
+// lanes of one that arrived in different branches would wait for one another.
+__device__ __forceinline__ void cluster_meet() {
+    __syncwarp();
+    if (threadIdx.x < 32) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    else asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // ---- ACT8 ----
 
 // Larger magnitude of the two, as a non-negative float; NaN if either is.  Its

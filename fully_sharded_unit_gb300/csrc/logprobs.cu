@@ -5,12 +5,16 @@
 
 #include "block_device.cuh"
 #include "compute.hpp"
+#include "rows.cuh"
 
 namespace fsdp {
 namespace {
 
-constexpr int kMostThreads = 512;
-constexpr int kWords = 4;            // 16-byte words of a thread in a group
+constexpr int kThreads = 128;         // of a block; each of them costs a row some work of its own
+constexpr int kWords = 8;            // 16-byte words of a thread in a group
+constexpr int kPlaces = 2;           // groups of a thread in shared memory
+constexpr int kBlocks = 5;           // on an SM
+constexpr int kRingBytes = kPlaces * kWords * kThreads * 16;
 constexpr int kMostCluster = 8;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kNone = -200.0f;     // 2^kNone is 0 in fp32
@@ -39,11 +43,8 @@ struct RowWords {
         const uint32_t x = BF16 ? 0xff80ff80u : 0xff800000u;
         return make_uint4(x, x, x, x);
     }
-    // The first or last word, or one behind it.
-    __device__ uint4 edge(int w) const {
-        uint4 v = none();
-        if (w >= count) return v;
-        v = words[w];
+    // Word w, whose bits are v, without what is not the row's.
+    __device__ uint4 masked(uint4 v, int w) const {
         uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int j = 0; j < E; ++j) {
@@ -54,7 +55,7 @@ struct RowWords {
         return make_uint4(x[0], x[1], x[2], x[3]);
     }
     __device__ uint4 load(int w) const {
-        return w > 0 && w < count - 1 ? words[w] : edge(w);
+        return w > 0 && w < count - 1 ? words[w] : masked(words[w], w);
     }
     __device__ static void floats(uint4 v, float* f) {
         if constexpr (BF16) {
@@ -157,20 +158,32 @@ __device__ __forceinline__ Key key_of(float z, int64_t i) {
     return (static_cast<Key>(order(z)) << 32) | (0xffffffffu - static_cast<uint32_t>(i));
 }
 
-constexpr int kLists = 64;      // of as many neighbouring threads each
-constexpr int kRoom = 2048;     // candidates
+constexpr int kLists = 32;      // of neighbouring threads' logits: a lane's each when the floor is found
+constexpr int kRoom = 1024;     // candidates
 
 struct TopShared {
-    Key best[kLists];
+    uint32_t lists[kLists];     // order() of their largest logits
+    uint8_t who[kThreads];      // threads that hold candidates
     Key found[kRoom];
     Key got[kMostTop];
-    Key floor;
-    int count;
+    int asked, count;
 };
+static_assert(kThreads % kLists == 0 && kThreads <= 256);
+
+// Before the block's next barrier: the lists' maxima.  `mine`: order() of the thread's largest
+// logit, 0 if it has none.
+__device__ __forceinline__ void top_lists(uint32_t mine, TopShared& s) {
+    constexpr int width = kThreads / kLists;
+#pragma unroll
+    for (int d = 1; d < width; d <<= 1) mine = max(mine, __shfl_xor_sync(kAll, mine, d));
+    if (threadIdx.x % width == 0) s.lists[threadIdx.x / width] = mine;
+    if (threadIdx.x < kMostTop) s.got[threadIdx.x] = 0;
+    if (threadIdx.x == 0) s.asked = s.count = 0;
+}
 
 // Puts the `top` largest of `count` keys into `to`, in order.
 __device__ __forceinline__ void rank_keys(const Key* keys, int count, int top, Key* to) {
-    for (int i = threadIdx.x; i < count; i += blockDim.x) {
+    for (int i = threadIdx.x; i < count; i += kThreads) {
         const Key k = keys[i];
         int above = 0;
         for (int j = 0; j < count; ++j) above += keys[j] > k;
@@ -178,62 +191,61 @@ __device__ __forceinline__ void rank_keys(const Key* keys, int count, int top, K
     }
 }
 
-// The `top` largest keys of the words [first, end), in order, into s.got (0 where the words
-// hold fewer).  Every one of them is at least the top-th largest of the lists' maxima; a
-// warp looks through the elements of each of its threads whose largest key (`mine`) reaches that.
+// Behind that barrier: the `top` largest keys of the words [first, end), in order, into s.got (0
+// where the words hold fewer).  Every one of them is at least the top-th largest of the lists'
+// maxima, and the words of the few threads whose own largest logit reaches that are read again,
+// by the whole block.
 template <bool BF16>
-__device__ void top_keys(const RowWords<BF16>& r, int first, int end, int top, Key mine, TopShared& s) {
+__device__ void top_keys(const RowWords<BF16>& r, int first, int end, int top, uint32_t mine, TopShared& s) {
     constexpr int E = RowWords<BF16>::E;
-    const int t = threadIdx.x, lane = t & 31, threads = blockDim.x, width = threads / kLists;
-    Key list = mine;
-    for (int d = 1; d < width; d <<= 1) list = max(list, __shfl_xor_sync(kAll, list, d));
-    if ((t & (width - 1)) == 0) s.best[t / width] = list;
-    if (t < kMostTop) s.got[t] = 0;
-    if (t == 0) {
-        s.count = 0;
-        s.floor = 0;
-    }
-    __syncthreads();
-    if (t < kLists) {
-        const Key k = s.best[t];
-        int above = 0;
-        for (int i = 0; i < kLists; ++i) above += s.best[i] > k;
-        if (above == top - 1 && k != 0) s.floor = k;   // one list's, or none if fewer than `top` hold any
-    }
-    __syncthreads();
-    const Key floor = s.floor;
-    const auto each = [&](int from, int step, auto f) {
-        for (int w = from; w < end; w += step) {
-            float z[8];
-            RowWords<BF16>::floats(r.load(w), z);
+    const int t = threadIdx.x, lane = t & 31;
+    const uint32_t list = s.lists[lane];
+    int above = 0;
 #pragma unroll
-            for (int j = 0; j < E; ++j)
-                if (r.inside(r.column(w, j))) f(key_of(z[j], r.column(w, j)));
-        }
-    };
-    for (unsigned who = __ballot_sync(kAll, mine >= floor && mine != 0); who != 0; who &= who - 1) {
-        const int thread = (t & ~31) + __ffs(who) - 1;
-        each(first + thread + lane * threads, 32 * threads, [&](Key k) {
-            if (k >= floor) {
+    for (int i = 0; i < kLists; ++i) above += __shfl_sync(kAll, list, i) > list;
+    const bool enough = __popc(__ballot_sync(kAll, list != 0)) >= top;
+    const uint32_t floor = enough ? __reduce_min_sync(kAll, above < top ? list : 0xffffffffu) : 1u;
+    if (mine >= floor) s.who[atomicAdd(&s.asked, 1)] = static_cast<uint8_t>(t);
+    __syncthreads();
+    const unsigned each = static_cast<unsigned>((end - first + kThreads - 1) / kThreads), items = each * static_cast<unsigned>(s.asked);
+    const float least = unorder(floor);
+    for (unsigned i = t; i < items; i += kThreads) {
+        const int w = first + s.who[i / each] + static_cast<int>(i % each) * kThreads;
+        if (w >= end) continue;
+        const uint4 v = r.load(w);
+        if (largest<BF16, 1>(&v) < least) continue;   // (not so where the floor is no number)
+        float z[8];
+        RowWords<BF16>::floats(v, z);
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            if (order(z[j]) >= floor && r.inside(r.column(w, j))) {
                 const int at = atomicAdd(&s.count, 1);
-                if (at < kRoom) s.found[at] = k;
+                if (at < kRoom) s.found[at] = key_of(z[j], r.column(w, j));
             }
-        });
+        }
     }
     __syncthreads();
     const int count = s.count;
     if (count <= kRoom) {
         rank_keys(s.found, count, top, s.got);
-    } else {   // more than there is room for: one after the other
+    } else {   // more than there is room for (many equal logits): one after the other
         Key last = ~Key(0);
         for (int n = 0; n < top; ++n) {
             Key k = 0;
-            each(first + t, threads, [&](Key x) { k = x < last ? max(k, x) : k; });
+            for (int w = first + t; w < end; w += kThreads) {
+                float z[8];
+                RowWords<BF16>::floats(r.load(w), z);
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    const Key x = key_of(z[j], r.column(w, j));
+                    if (r.inside(r.column(w, j)) && x < last) k = max(k, x);
+                }
+            }
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) k = max(k, __shfl_xor_sync(kAll, k, d));
-            if (lane == 0) s.best[t >> 5] = k;
+            if (lane == 0) s.found[t >> 5] = k;
             __syncthreads();
-            for (int i = 0; i < threads / 32; ++i) k = max(k, s.best[i]);
+            for (int i = 0; i < kThreads / 32; ++i) k = max(k, s.found[i]);
             last = k;
             if (t == 0) s.got[n] = k;
             __syncthreads();
@@ -252,13 +264,14 @@ struct RowGrad {
     bool zero;        // the whole row
 };
 
-// p (-(a + b h) - b ln p) of eight logits; and a at the token.
+// p (-(a + b h) - b ln p) of N logits; and a at the token.
+template <int N = 8>
 __device__ __forceinline__ void logit_grads(float* v, float c, const RowGrad& g) {
     const f32x2 less = pair(-g.m, -g.m), c2 = pair(c, c), l = pair(-g.ln2s, -g.ln2s);
     const float a1 = -fmaf(g.b, g.h, g.a), b1 = -g.b * kLn2;
     const f32x2 a2 = pair(a1, a1), b2 = pair(b1, b1);
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
+    for (int j = 0; j < N; j += 2) {
         float x0, x1;
         unpair(fma2(add2(pair(v[j], v[j + 1]), less), c2, l), x0, x1);
         if (b1 != 0.0f) {
@@ -288,7 +301,8 @@ __device__ __forceinline__ void row_gradient(const TokenLogprobs& a, int64_t row
     constexpr int kZ = ZHALF ? FSDP_DTYPE_BF16 : FSDP_DTYPE_F32, kD = DHALF ? FSDP_DTYPE_BF16 : FSDP_DTYPE_F32;
     constexpr int N = ZHALF ? 4 : 2, W = ZHALF ? 1 : 2;   // chunks in flight; words of a chunk
     const float c = a.scale * kLog2e;
-    const int lead = grad_lead(a, row), vocab = static_cast<int>(a.vocab), t = threadIdx.x, threads = blockDim.x;
+    const int lead = grad_lead(a, row), vocab = static_cast<int>(a.vocab), t = threadIdx.x;
+    constexpr int threads = kThreads;
     const int64_t zrow = row * a.z.ld, drow = row * a.dz.ld;
     // a row's ends, an element to a thread
     const int last = (lead + vocab - 1) / 8;
@@ -356,11 +370,19 @@ __device__ __forceinline__ void row_gradient(const TokenLogprobs& a, int64_t row
     else row_gradient<ZHALF, false>(a, row, g, begin, end);
 }
 
-__device__ RowGrad row_grad(const TokenLogprobs& a, int64_t row, float m, float ln_s, float h) {
+// What the caller gives for a row, and the gradient's constants made of it.
+struct RowGiven {
+    int64_t token;
+    float a, b;
+    __device__ RowGiven(const TokenLogprobs& x, int64_t row)
+        : token(x.tokens != nullptr ? x.tokens[row] : -1), a(x.dlogprob != nullptr ? x.dlogprob[row] : 0.0f),
+          b(x.dentropy != nullptr ? x.dentropy[row] : 0.0f) {}
+};
+__device__ __forceinline__ RowGrad row_grad(const TokenLogprobs& a, const RowGiven& given, float m, float ln_s, float h) {
     RowGrad g;
-    g.token = a.dlogprob != nullptr ? a.tokens[row] : -1;
-    g.a = g.token >= 0 ? a.dlogprob[row] * a.scale : 0.0f;
-    g.b = a.dentropy != nullptr ? a.dentropy[row] * a.scale : 0.0f;
+    g.token = a.dlogprob != nullptr ? given.token : -1;
+    g.a = g.token >= 0 ? given.a * a.scale : 0.0f;
+    g.b = given.b * a.scale;
     // a masked row's S is 0; a token that does not exist leaves nothing to say
     g.zero = (g.a == 0.0f && g.b == 0.0f) || ln_s == -kInf;
     if (g.token >= a.vocab) {
@@ -375,39 +397,136 @@ __device__ RowGrad row_grad(const TokenLogprobs& a, int64_t row, float m, float 
 
 // ---- kernels ----
 
-// A row to a block, or to a cluster of blocks that have a run of its words each.
+// A block's share of a row's words: all of them, or a run of them in a cluster of blocks.
+struct Share {
+    int first, end;
+    __device__ Share(int count, int rank, int cluster)
+        : first(static_cast<int>(static_cast<int64_t>(count) * rank / cluster)),
+          end(static_cast<int>(static_cast<int64_t>(count) * (rank + 1) / cluster)) {}
+};
+
+// The threads' sums joined over a block's WARPS warps, and over the cluster: for every thread.
+template <int WARPS>
+__device__ __forceinline__ Soft join_all(Soft s, float c, Soft* softs, Soft* joined, int rank, int cluster) {
+    const int t = threadIdx.x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1)
+        s = join(s, Soft{__shfl_xor_sync(kAll, s.m, d), __shfl_xor_sync(kAll, s.S, d), __shfl_xor_sync(kAll, s.Q, d)}, c);
+    if ((t & 31) == 0) softs[t >> 5] = s;
+    __syncthreads();
+    s = softs[0];
+    for (int i = 1; i < WARPS; ++i) s = join(s, softs[i], c);
+    if (cluster > 1) {
+        if (t < cluster) {
+            const uint32_t to = remote_addr(shared_at(&joined[rank]), t);
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(s.m) : "memory");
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4), "f"(s.S) : "memory");
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 8), "f"(s.Q) : "memory");
+        }
+        cluster_meet();
+        s = joined[0];
+        for (int i = 1; i < cluster; ++i) s = join(s, joined[i], c);
+    }
+    return s;
+}
+
+// A row's results, by one thread.  z: the token's logit.
+template <bool ENTROPY>
+__device__ __forceinline__ void row_results(const TokenLogprobs& a, int64_t row, const Soft& s, float ln_s, float h, int64_t token, float z) {
+    if (a.tokens != nullptr) {
+        float lp = 0.0f;
+        if (token >= a.vocab) {
+            lp = __uint_as_float(0x7fc00000u);
+            atomicOr(a.status, FSDP_KSTATUS_BAD_TOKEN);
+        } else if (token >= 0) {
+            lp = s.S == 0.0f ? -kInf : fmaf(z - s.m, a.scale, -ln_s);
+        }
+        a.logprob[row] = lp;
+    }
+    if (ENTROPY && a.entropy != nullptr) a.entropy[row] = h;
+    if (a.stats != nullptr) {
+        a.stats[2 * row] = s.m;
+        a.stats[2 * row + 1] = ln_s;
+    }
+}
+
+__device__ __forceinline__ float token_logit(const TokenLogprobs& a, int64_t row, int64_t token) {
+    return token >= 0 && token < a.vocab ? load1(a.z.p, a.z.dtype, row * a.z.ld + token) : 0.0f;
+}
+
+// Rows to blocks, or to clusters of blocks.  A thread copies the words that it will look at itself,
+// in groups and row after row, into its own places in shared memory (cp.async), so
+// that while the block joins a row's sums and looks for its alternatives the next row's
+// words are under way.
 template <bool BF16, bool ENTROPY, bool GRAD>
-__global__ void __launch_bounds__(kMostThreads, 2) token_logprobs_kernel(const TokenLogprobs a, int cluster) {
-    constexpr int E = RowWords<BF16>::E;
+__global__ void __launch_bounds__(kThreads, kBlocks) token_logprobs_kernel(const __grid_constant__ TokenLogprobs a, int cluster) {
+    constexpr int threads = kThreads;
+    extern __shared__ __align__(16) uint4 ring[];
     __shared__ TopShared tops;
-    __shared__ Soft softs[kMostThreads / 32], joined[kMostCluster];
+    __shared__ Soft softs[kThreads / 32], joined[kMostCluster];
     starts_early();
     after_previous();
     if (cluster > 1) cluster_sync();   // the others' shared memory is there
-    const int t = threadIdx.x, lane = t & 31, threads = blockDim.x;
+    const int t = threadIdx.x;
     const int rank = cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
     const float c = a.scale * kLog2e;
-    for (int64_t row = blockIdx.x / cluster; row < a.rows; row += gridDim.x / cluster) {
-        const RowWords<BF16> r(a.z, row, a.vocab);
-        const int first = static_cast<int>(static_cast<int64_t>(r.count) * rank / cluster);
-        const int end = static_cast<int>(static_cast<int64_t>(r.count) * (rank + 1) / cluster);
-        Soft s{-kInf, 0.0f, 0.0f};
-        int best = first + t;   // the first word of the group that holds the largest logit
-        const auto load = [&](int w) { return w < end ? r.load(w) : r.none(); };
-        uint4 next[kWords];
+    const int64_t stride = gridDim.x / cluster;
+    const uint32_t slots = shared_at(ring + t);
+    // the group to copy next: its row, that row's words, its first word and the share's end
+    int64_t ahead = blockIdx.x / cluster;
+    const uint4* words = nullptr;
+    int w_ahead = 0, end_ahead = 0;
+    const auto look_ahead = [&] {   // to a row of which the thread has words
+        for (; ahead < a.rows; ahead += stride) {
+            const RowWords<BF16> r(a.z, ahead, a.vocab);
+            const Share share(r.count, rank, cluster);
+            words = r.words;
+            w_ahead = share.first + t;
+            end_ahead = share.end;
+            if (w_ahead < end_ahead) return;
+        }
+    };
+    const auto copy_ahead = [&](int place) {
+        if (ahead < a.rows) {
 #pragma unroll
-        for (int k = 0; k < kWords; ++k) next[k] = load(first + t + k * threads);
+            for (int k = 0; k < kWords; ++k)
+                if (w_ahead + k * threads < end_ahead)
+                    copy16(slots + (place * kWords + k) * threads * 16, words + w_ahead + k * threads);
+            w_ahead += kWords * threads;
+            if (w_ahead >= end_ahead) {
+                ahead += stride;
+                look_ahead();
+            }
+        }
+        copies_end();
+    };
+    look_ahead();
+    for (int i = 0; i < kPlaces; ++i) copy_ahead(i);
+    int place = 0;
+    for (int64_t row = blockIdx.x / cluster; row < a.rows; row += stride) {
+        const RowWords<BF16> r(a.z, row, a.vocab);
+        const Share share(r.count, rank, cluster);
+        const int first = share.first, end = share.end;
+        const int64_t token = t == 0 && a.tokens != nullptr ? a.tokens[row] : -1;
+        const float z_token = token_logit(a, row, token);
+        Soft s{-kInf, 0.0f, 0.0f};
         for (int w = first + t; w < end; w += kWords * threads) {
+            copies_wait(kPlaces - 1);
             uint4 v[kWords];
 #pragma unroll
-            for (int k = 0; k < kWords; ++k) v[k] = next[k];
+            for (int k = 0; k < kWords; ++k) v[k] = ring[(place * kWords + k) * threads + t];
+            if (w == 0 || w + (kWords - 1) * threads >= min(end, r.count - 1)) {   // a row's ends
 #pragma unroll
-            for (int k = 0; k < kWords; ++k) next[k] = load(w + (kWords + k) * threads);
-            const float top = largest<BF16, kWords>(v);
-            if (top > s.m) {
-                rescale(s, top, c);
-                best = w;
+                for (int k = 0; k < kWords; ++k) {
+                    const int i = w + k * threads;
+                    if (i >= end) v[k] = r.none();
+                    else if (i == 0 || i == r.count - 1) v[k] = r.masked(v[k], i);
+                }
             }
+            const float top = largest<BF16, kWords>(v);
+            if (top > s.m) rescale(s, top, c);
+            copy_ahead(place);   // the words are in registers
+            place = place + 1 == kPlaces ? 0 : place + 1;
             const float ref = s.m == -kInf ? 0.0f : s.m;
             f32x2 S2 = pair(s.S, 0.0f), Q2 = pair(s.Q, 0.0f);
             if (fabsf(s.m) < 0x1p99f && c < 0x1p20f) {
@@ -423,58 +542,13 @@ __global__ void __launch_bounds__(kMostThreads, 2) token_logprobs_kernel(const T
             unpair(Q2, x, y);
             s.Q = x + y;
         }
-        // the thread's largest logit's key: the first of its group that equals it
-        Key mine = 0;
-        if (a.top > 0) {
-            for (int k = 0; k < kWords; ++k) {
-                const int w = best + k * threads;
-                if (w >= end) break;
-                float z[8];
-                RowWords<BF16>::floats(r.load(w), z);
-#pragma unroll
-                for (int j = 0; j < E; ++j)
-                    if (mine == 0 && z[j] == s.m && r.inside(r.column(w, j))) mine = key_of(z[j], r.column(w, j));
-            }
-        }
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1)
-            s = join(s, Soft{__shfl_xor_sync(kAll, s.m, d), __shfl_xor_sync(kAll, s.S, d), __shfl_xor_sync(kAll, s.Q, d)}, c);
-        if (lane == 0) softs[t >> 5] = s;
-        __syncthreads();
-        s = softs[0];
-        for (int i = 1; i < threads / 32; ++i) s = join(s, softs[i], c);
-        if (cluster > 1) {
-            if (t < cluster) {
-                const uint32_t to = remote_addr(static_cast<uint32_t>(__cvta_generic_to_shared(&joined[rank])), t);
-                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(s.m) : "memory");
-                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4), "f"(s.S) : "memory");
-                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 8), "f"(s.Q) : "memory");
-            }
-            cluster_sync();
-            s = joined[0];
-            for (int i = 1; i < cluster; ++i) s = join(s, joined[i], c);
-        }
+        const uint32_t mine = first + t < end ? order(s.m) : 0;
+        if (a.top > 0) top_lists(mine, tops);
+        s = join_all<kThreads / 32>(s, c, softs, joined, rank, cluster);
         const bool bad = !(s.S == s.S);
         const float ln_s = logf(s.S);
         const float h = s.S == 0.0f ? 0.0f : fmaf(-kLn2, s.Q / s.S, ln_s);
-        if (t == 0 && rank == 0) {
-            if (a.tokens != nullptr) {
-                const int64_t token = a.tokens[row];
-                float lp = 0.0f;
-                if (token >= a.vocab) {
-                    lp = __uint_as_float(0x7fc00000u);
-                    atomicOr(a.status, FSDP_KSTATUS_BAD_TOKEN);
-                } else if (token >= 0) {
-                    lp = s.S == 0.0f ? -kInf : fmaf(load1(a.z.p, a.z.dtype, row * a.z.ld + token) - s.m, a.scale, -ln_s);
-                }
-                a.logprob[row] = lp;
-            }
-            if (ENTROPY && a.entropy != nullptr) a.entropy[row] = h;
-            if (a.stats != nullptr) {
-                a.stats[2 * row] = s.m;
-                a.stats[2 * row + 1] = ln_s;
-            }
-        }
+        if (t == 0 && rank == 0) row_results<ENTROPY>(a, row, s, ln_s, h, token, z_token);
         if (a.top > 0) {
             if (!bad) top_keys<BF16>(r, first, end, a.top, mine, tops);
             if (cluster > 1) {   // the blocks' lists meet in the first one's candidates
@@ -498,21 +572,128 @@ __global__ void __launch_bounds__(kMostThreads, 2) token_logprobs_kernel(const T
         else __syncthreads();
         if constexpr (GRAD) {
             const int chunks = grad_chunks(a, row);
-            row_gradient<BF16>(a, row, row_grad(a, row, s.m, ln_s, h), static_cast<int>(static_cast<int64_t>(chunks) * rank / cluster),
-                               static_cast<int>(static_cast<int64_t>(chunks) * (rank + 1) / cluster));
+            const Share part(chunks, rank, cluster);
+            row_gradient<BF16>(a, row, row_grad(a, RowGiven(a, row), s.m, ln_s, h), part.first, part.end);
         }
+    }
+}
+
+// Forward and backward with the row's words held in shared memory in between: kMostSlots words
+// to a thread, copied by itself.  Where a word has given its gradient, the next row's
+// takes its place, so a block's loads run on under its second pass.  dz lies on its words as z does.
+constexpr int kMostSlots = 13;      // of 512 threads: 104 KB, two blocks on an SM
+
+template <bool BF16, bool ENTROPY, int T>
+__global__ void __launch_bounds__(T, 1024 / T) token_loss_kernel(const __grid_constant__ TokenLogprobs a, int cluster, int slots) {
+    constexpr int E = RowWords<BF16>::E, G = 4;   // words of a group
+    extern __shared__ __align__(16) uint4 held[];
+    __shared__ Soft softs[2][T / 32], joined[2][kMostCluster];   // used in turn: there is one barrier a row
+    starts_early();
+    after_previous();
+    if (cluster > 1) cluster_sync();   // the others' shared memory is there
+    const int t = threadIdx.x;
+    const int rank = cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const float c = a.scale * kLog2e;
+    const int64_t stride = gridDim.x / cluster;
+    const uint32_t mine = shared_at(held + t);
+    int64_t row = blockIdx.x / cluster;
+    if (row < a.rows) {
+        const RowWords<BF16> r(a.z, row, a.vocab);
+        const Share share(r.count, rank, cluster);
+        for (int k = 0; k < slots; ++k)
+            if (share.first + t + k * T < share.end) copy16(mine + k * T * 16, r.words + share.first + t + k * T);
+        copies_end();
+    }
+    int flip = 0;
+    for (; row < a.rows; row += stride) {
+        const RowWords<BF16> r(a.z, row, a.vocab);
+        const Share share(r.count, rank, cluster);
+        const RowGiven given(a, row);
+        const float z_token = t == 0 && rank == 0 ? token_logit(a, row, given.token) : 0.0f;
+        copies_wait(0);
+        Soft s{-kInf, 0.0f, 0.0f};
+        for (int k0 = 0; share.first + t + k0 * T < share.end; k0 += G) {
+            uint4 v[G];
+            const int w = share.first + t + k0 * T;
+#pragma unroll
+            for (int k = 0; k < G; ++k) v[k] = k0 + k < slots ? held[(k0 + k) * T + t] : r.none();
+            if (w == 0 || w + (G - 1) * T >= min(share.end, r.count - 1)) {   // a row's ends
+#pragma unroll
+                for (int k = 0; k < G; ++k) {
+                    const int i = w + k * T;
+                    if (i >= share.end) v[k] = r.none();
+                    else if (i == 0 || i == r.count - 1) v[k] = r.masked(v[k], i);
+                }
+            }
+            const float top = largest<BF16, G>(v);
+            if (top > s.m) rescale(s, top, c);
+            const float ref = s.m == -kInf ? 0.0f : s.m;
+            f32x2 S2 = pair(s.S, 0.0f), Q2 = pair(s.Q, 0.0f);
+            if (fabsf(s.m) < 0x1p99f && c < 0x1p20f) {
+#pragma unroll
+                for (int k = 0; k < G; ++k) add_word<BF16, ENTROPY>(s, S2, Q2, v[k], ref, c, true);
+            } else {
+#pragma unroll
+                for (int k = 0; k < G; ++k) add_word<BF16, ENTROPY>(s, S2, Q2, v[k], ref, c, false);
+            }
+            float x, y;
+            unpair(S2, x, y);
+            s.S = x + y;
+            unpair(Q2, x, y);
+            s.Q = x + y;
+        }
+        s = join_all<T / 32>(s, c, softs[flip], joined[flip], rank, cluster);
+        flip ^= 1;
+        const float ln_s = logf(s.S);
+        const float h = s.S == 0.0f ? 0.0f : fmaf(-kLn2, s.Q / s.S, ln_s);
+        if (t == 0 && rank == 0) row_results<ENTROPY>(a, row, s, ln_s, h, given.token, z_token);
+        const RowGrad g = row_grad(a, given, s.m, ln_s, h);
+        const int hit = g.token >= 0 && g.token < a.vocab ? (static_cast<int>(g.token) + r.lead) / E : -1;   // the token's word
+        uint4* out = reinterpret_cast<uint4*>((reinterpret_cast<uintptr_t>(a.dz.p) + static_cast<uintptr_t>(row * a.dz.ld) * (16 / E)) & ~uintptr_t(15));
+        const bool more = row + stride < a.rows;
+        const RowWords<BF16> next(a.z, more ? row + stride : row, a.vocab);
+        const Share ahead(next.count, rank, cluster);
+        for (int k = 0; k < slots; ++k) {
+            const int w = share.first + t + k * T;
+            if (w < share.end) {
+                float v[8];
+                RowWords<BF16>::floats(held[k * T + t], v);
+                if (g.zero) {
+#pragma unroll
+                    for (int j = 0; j < E; ++j) v[j] = 0.0f;
+                } else {
+                    logit_grads<E>(v, c, g);
+                    if (w == hit) {
+#pragma unroll
+                        for (int j = 0; j < E; ++j)
+                            if (r.column(w, j) == static_cast<int>(g.token)) v[j] += g.a;
+                    }
+                }
+                if (w > 0 && w < r.count - 1) {
+                    out[w] = BF16 ? make_uint4(to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]), to_bf16x2(v[E - 4], v[E - 3]), to_bf16x2(v[E - 2], v[E - 1]))
+                                  : make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+                } else {   // a row's ends
+#pragma unroll
+                    for (int j = 0; j < E; ++j)
+                        if (r.inside(r.column(w, j))) store1(a.dz.p, a.dz.dtype, row * a.dz.ld + r.column(w, j), v[j]);
+                }
+            }
+            const int i = ahead.first + t + k * T;
+            if (more && i < ahead.end) copy16(mine + k * T * 16, next.words + i);
+        }
+        copies_end();
     }
 }
 
 // `parts` blocks to a row, which have a run of its chunks each.
 template <bool BF16>
-__global__ void __launch_bounds__(256) token_logprobs_backward_kernel(const TokenLogprobs a, int parts) {
+__global__ void __launch_bounds__(kThreads) token_logprobs_backward_kernel(const TokenLogprobs a, int parts) {
     starts_early();
     after_previous();
     const int part = blockIdx.x % parts;
     for (int64_t row = blockIdx.x / parts; row < a.rows; row += gridDim.x / parts) {
         const float m = a.stats[2 * row], ln_s = a.stats[2 * row + 1];
-        const RowGrad g = row_grad(a, row, m, ln_s, a.entropy != nullptr ? a.entropy[row] : 0.0f);
+        const RowGrad g = row_grad(a, RowGiven(a, row), m, ln_s, a.entropy != nullptr ? a.entropy[row] : 0.0f);
         if (threadIdx.x == 0 && part == 0 && g.token >= a.vocab) atomicOr(a.status, FSDP_KSTATUS_BAD_TOKEN);
         const int chunks = grad_chunks(a, row);
         row_gradient<BF16>(a, row, g, static_cast<int>(static_cast<int64_t>(chunks) * part / parts),
@@ -526,15 +707,35 @@ cudaError_t launch_token_logprobs(const TokenLogprobs& a, int sms, cudaStream_t 
     if (a.rows == 0) return cudaSuccess;
     const bool half = a.z.dtype == FSDP_DTYPE_BF16, grad = a.dz.p != nullptr;
     const bool entropy = a.entropy != nullptr || a.dentropy != nullptr;
-    // threads to a row: as many as fill the SMs, in blocks of 128 to 512 and clusters of up to
-    // eight, but two words at least to each
-    const int64_t words = a.vocab * (half ? 2 : 4) / 16 + 1;
-    const int64_t wanted = std::min<int64_t>(static_cast<int64_t>(sms) * 1024 / a.rows, words / 2);
-    int threads = 128, cluster = 1;
-    while (threads < kMostThreads && threads < wanted) threads *= 2;
-    while (cluster < kMostCluster && threads * cluster < wanted) cluster *= 2;
-    const int64_t rows = std::min<int64_t>(a.rows, int64_t(1) << 27);
-#define RUN(h, e, g) return launch_early_clusters(token_logprobs_kernel<h, e, g>, dim3(static_cast<unsigned>(rows * cluster)), threads, 0, cluster, st, a, cluster)
+    // blocks to a row: as many as fill the SMs, but two words at least to a thread
+    const int64_t words = a.vocab * (half ? 2 : 4) / 16 + 2;   // and where a row begins inside one
+    // dz on its words as z is on its own, row by row
+    const int64_t size = half ? 2 : 4;
+    if (grad && a.dz.dtype == a.z.dtype && (((reinterpret_cast<uintptr_t>(a.z.p) ^ reinterpret_cast<uintptr_t>(a.dz.p)) | static_cast<uintptr_t>((a.z.ld - a.dz.ld) * size)) & 15) == 0) {
+        // blocks to a row: what holds it in shared memory, and as many as fill the SMs
+        int parts = 1;
+        while (parts < kMostCluster && (words > static_cast<int64_t>(parts) * 1024 * kMostSlots ||
+                                        (a.rows * parts * 2 <= 2 * sms && words >= static_cast<int64_t>(parts) * 2 * 512 * 2))) parts *= 2;
+        const int64_t share = (words + parts - 1) / parts + 1;
+        const int threads = share <= 512 * kMostSlots ? 512 : 1024;
+        const int slots = static_cast<int>((share + threads - 1) / threads);
+        if (slots <= kMostSlots) {
+            const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(a.rows, std::max(1, sms * (1024 / threads) / parts)) * parts);
+#define RUN(h, e, t) return launch_shared_clusters<token_loss_kernel<h, e, t>>(blocks, threads, slots * threads * 16, parts, st, a, parts, slots)
+#define RUN_(h, e) do { if (threads == 512) RUN(h, e, 512); RUN(h, e, 1024); } while (0)
+            if (half && entropy) RUN_(true, true);
+            if (half) RUN_(true, false);
+            if (entropy) RUN_(false, true);
+            RUN_(false, false);
+#undef RUN_
+#undef RUN
+        }
+    }
+    const int64_t most = static_cast<int64_t>(sms) * kBlocks;
+    int cluster = 1;
+    while (cluster < kMostCluster && a.rows * cluster * 2 <= most && words >= static_cast<int64_t>(cluster) * 2 * kThreads * 2) cluster *= 2;
+    const int64_t rows = std::min(a.rows, std::max<int64_t>(1, most / cluster));
+#define RUN(h, e, g) return launch_shared_clusters<token_logprobs_kernel<h, e, g>, kRingBytes>(static_cast<unsigned>(rows * cluster), kThreads, kRingBytes, cluster, st, a, cluster)
     if (half) {
         if (entropy) { if (grad) RUN(true, true, true); RUN(true, true, false); }
         if (grad) RUN(true, false, true);
@@ -549,11 +750,11 @@ cudaError_t launch_token_logprobs(const TokenLogprobs& a, int sms, cudaStream_t 
 cudaError_t launch_token_logprobs_backward(const TokenLogprobs& a, int sms, cudaStream_t st) {
     if (a.rows == 0) return cudaSuccess;
     // few rows are shared by blocks, down to a group of chunks to a thread
-    const int64_t most = a.vocab / (8 * 4 * 256) + 1;
+    const int64_t most = a.vocab / (8 * 4 * kThreads) + 1;
     const int64_t parts = std::max<int64_t>(1, std::min(most, static_cast<int64_t>(sms) * 8 / a.rows));
     const int64_t rows = std::min(a.rows, (int64_t(1) << 30) / parts);
     return launch_early(a.z.dtype == FSDP_DTYPE_BF16 ? token_logprobs_backward_kernel<true> : token_logprobs_backward_kernel<false>,
-                        dim3(static_cast<unsigned>(rows * parts)), 256, 0, st, a, static_cast<int>(parts));
+                        dim3(static_cast<unsigned>(rows * parts)), kThreads, 0, st, a, static_cast<int>(parts));
 }
 
 }  // namespace fsdp

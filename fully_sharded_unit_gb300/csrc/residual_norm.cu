@@ -193,7 +193,7 @@ __device__ __forceinline__ void cluster_sums(float (&v)[N], float (*mine)[4], in
 #pragma unroll
         for (int i = 0; i < N; ++i) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4 * i), "f"(v[i]) : "memory");
     }
-    cluster_sync();
+    cluster_meet();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         v[i] = 0.0f;
@@ -338,32 +338,83 @@ __global__ void __launch_bounds__(kMostThreads) residual_norm_backward_kernel(co
 
 // ---- rows staged through shared memory ----
 //
-// BF16 rows on 16-byte boundaries, as they come in training.  A block holds G groups of
-// GT threads, each with a row; thread t of a group owns its chunks t + k GT, k < NV, and
-// copies the ones of the rows ahead into a ring of shared memory (cp.async), so that
-// it waits for its own copies alone.
+// BF16 rows, as they come in training.  A block holds G groups of GT threads, each with a
+// row (or, in a cluster, a run of its columns); thread t of a group owns its chunks of eight
+// columns t + k GT, k < NV, and copies the ones of the rows ahead into a ring of shared
+// memory (cp.async), so that it waits for its own copies alone.  ANY: rows start anywhere;
+// a chunk is then the two 16-byte words that hold it, moved together when it is read.
 
 constexpr int kMostPlaces = 4;      // rows of a group in the ring
 constexpr int kRingThreads = 512;
 
 struct RingShape {
-    int gt, groups, places;
+    int gt, groups, places, cluster;
+    int chunks;                     // of a block's share of a row, but for the last one's
 };
 
-template <int NV, int M>
+// A thread's place: its group, its number there, its block's first chunk.  Only a thread's last
+// chunk can be short or lie past the share's end (ring_shape has the shares so).
+template <int NV>
+struct Place {
+    int gt, groups, g, t;
+    int64_t first;
+    int last;                       // columns of the last chunk
+    __device__ Place(const RingShape& s, int64_t cols) : gt(s.gt), groups(s.groups), g(threadIdx.x / s.gt), t(threadIdx.x % s.gt) {
+        first = static_cast<int64_t>(s.cluster > 1 ? cluster_rank() : 0) * s.chunks;
+        last = t + (NV - 1) * gt < s.chunks ? inside8(column(NV - 1), cols) : 0;
+    }
+    __device__ int64_t column(int k) const { return (first + t + k * gt) * 8; }
+    __device__ int in(int k) const { return k + 1 < NV ? 8 : last; }
+};
+
+template <int NV, int M, bool ANY>
 struct Ring {
     uint8_t* base;
-    int gt, groups, g, t;
-    __device__ uint8_t* slot(int place, int m, int k) const {
-        return base + (((place * M + m) * groups + g) * NV * gt + k * gt + t) * 16;
+    static constexpr int kHalves = ANY ? 2 : 1;
+    __device__ uint8_t* slot(const Place<NV>& at, int place, int m, int k) const {
+        return base + ((((place * M + m) * at.groups + at.g) * NV + k) * kHalves * at.gt + at.t) * 16;
     }
-    __device__ void copy(const Mat& x, int64_t row, int place, int m, bool end) const {
-        const uint8_t* from = static_cast<const uint8_t*>(x.p) + (row * x.ld + t * 8) * 2;
+    __device__ void copy(const Place<NV>& at, const Mat& x, int64_t row, int place, int m) const {
+        const uint8_t* from = static_cast<const uint8_t*>(x.p) + (row * x.ld + (at.first + at.t) * 8) * 2;
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (k + 1 < NV || end) copy16(shared_at(slot(place, m, k)), from + k * gt * 16);
+        for (int k = 0; k < NV; ++k) {
+            if (at.in(k) == 0) continue;
+            const uint32_t to = shared_at(slot(at, place, m, k));
+            if (ANY) {
+                const uintptr_t chunk = reinterpret_cast<uintptr_t>(from + k * at.gt * 16), word = chunk & ~uintptr_t(15);
+                copy16(to, reinterpret_cast<const void*>(word));
+                if (static_cast<int>(chunk & 15) + 2 * at.in(k) > 16) copy16(to + at.gt * 16, reinterpret_cast<const void*>(word + 16));
+            } else {
+                copy16(to, from + k * at.gt * 16);
+            }
+        }
     }
-    __device__ uint4 read(int place, int m, int k) const { return *reinterpret_cast<const uint4*>(slot(place, m, k)); }
+    // The chunk; zeros past the row's end.  (What no copy has written is read too, and dropped: a
+    // branch here would keep the reads behind one another, 78 us against 66.)
+    __device__ uint4 read(const Place<NV>& at, const Mat& x, int64_t row, int place, int m, int k) const {
+        const uint4 lo = *reinterpret_cast<const uint4*>(slot(at, place, m, k));
+        if (!ANY) return k + 1 < NV || at.last != 0 ? lo : make_uint4(0, 0, 0, 0);
+        const uint4 hi = *reinterpret_cast<const uint4*>(slot(at, place, m, k) + at.gt * 16);
+        uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(x.p) + static_cast<uintptr_t>(row * x.ld) * 2) & 15u;
+        if (off & 8) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+        }
+        if (off & 4) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+        }
+        if (off & 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+        }
+        if (k + 1 == NV) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] &= 2 * i + 1 < at.last ? 0xffffffffu : 2 * i < at.last ? 0xffffu : 0u;
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
 };
 
 __device__ __forceinline__ void pairs(uint4 w, f32x2* v) {
@@ -372,52 +423,49 @@ __device__ __forceinline__ void pairs(uint4 w, f32x2* v) {
     v[2] = pair(bf16_lo(w.z), bf16_hi(w.z));
     v[3] = pair(bf16_lo(w.w), bf16_hi(w.w));
 }
-__device__ __forceinline__ uint4 rounded(const f32x2* v) {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float a, b;
-        unpair(v[j], a, b);
-        w[j] = to_bf16x2(a, b);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
 __device__ __forceinline__ f32x2 twice(float v) { return pair(v, v); }
 
-// The vectors of cols elements, which all groups share: ones where there is none.  Floats
-// lie in two halves of 16 bytes a chunk, so that neighbouring threads' accesses are neighbours.
+// A chunk of an output row; whole warps take part.
+template <int NV, bool ANY>
+__device__ __forceinline__ void put(const Place<NV>& at, const Mat& m, int64_t row, int k, const f32x2* v) {
+    float o[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) unpair(v[j], o[2 * j], o[2 * j + 1]);
+    if (ANY) store_chunk_any(m.p, FSDP_DTYPE_BF16, row * m.ld + at.column(k), at.in(k), o);
+    else if (at.in(k) != 0) store8(m.p, FSDP_DTYPE_BF16, row * m.ld + at.column(k), o);
+}
+
+// The vectors, which all groups share: ones where there is none.  Floats lie in two
+// halves of 16 bytes a chunk, so that neighbouring threads' accesses are neighbours.
 template <int NV, bool FLOATS>
 struct Vectors {
     uint8_t* base;
-    int gt, t;
     static constexpr int kChunk = FLOATS ? 32 : 16;
-    __device__ uint8_t* slot(int v, int k) const { return base + (v * NV + k) * gt * kChunk + t * 16; }
-    __device__ void fill(const void* p, int v, bool end) const {
+    __device__ uint8_t* slot(const Place<NV>& at, int v, int k) const { return base + (v * NV + k) * at.gt * kChunk + at.t * 16; }
+    __device__ void fill(const Place<NV>& at, const void* p, int dtype, int v) const {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (k + 1 < NV || end) {
-                const uint8_t* from = static_cast<const uint8_t*>(p) + (t + k * gt) * kChunk;
-                uint8_t* to = slot(v, k);
-                if (p != nullptr) {
-                    copy16(shared_at(to), from);
-                    if (FLOATS) copy16(shared_at(to + gt * 16), from + 16);
-                } else {
-                    const uint32_t one = FLOATS ? 0x3f800000u : 0x3f803f80u;
-                    *reinterpret_cast<uint4*>(to) = make_uint4(one, one, one, one);
-                    if (FLOATS) *reinterpret_cast<uint4*>(to + gt * 16) = make_uint4(one, one, one, one);
-                }
+            float x[8];
+            load_any(p, dtype, at.column(k), at.in(k), 1.0f, x);
+            uint4* to = reinterpret_cast<uint4*>(slot(at, v, k));
+            if (FLOATS) {
+                *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<float4*>(to + at.gt) = make_float4(x[4], x[5], x[6], x[7]);
+            } else {
+                *to = make_uint4(to_bf16x2(x[0], x[1]), to_bf16x2(x[2], x[3]), to_bf16x2(x[4], x[5]), to_bf16x2(x[6], x[7]));
             }
         }
     }
-    __device__ void read(int v, int k, f32x2* x) const {
+    __device__ void read(const Place<NV>& at, int v, int k, f32x2* x) const {
+        const uint8_t* from = slot(at, v, k);
         if (FLOATS) {
-            const float4 a = *reinterpret_cast<const float4*>(slot(v, k)), b = *reinterpret_cast<const float4*>(slot(v, k) + gt * 16);
+            const float4 a = *reinterpret_cast<const float4*>(from), b = *reinterpret_cast<const float4*>(from + at.gt * 16);
             x[0] = pair(a.x, a.y);
             x[1] = pair(a.z, a.w);
             x[2] = pair(b.x, b.y);
             x[3] = pair(b.z, b.w);
         } else {
-            pairs(*reinterpret_cast<const uint4*>(slot(v, k)), x);
+            pairs(*reinterpret_cast<const uint4*>(from), x);
         }
     }
 };
@@ -444,34 +492,35 @@ __device__ __forceinline__ void group_sums(float (&v)[N], float4* red, int group
     if (N > 2) v[N > 2 ? 2 : 0] = s.z;
 }
 
-template <int NV, bool FLOATS>
+template <int NV, bool FLOATS, bool ANY>
 __global__ void __launch_bounds__(kRingThreads) residual_norm_ring_kernel(const __grid_constant__ ResidualNorm a, const RingShape shape) {
     extern __shared__ __align__(16) uint8_t ring_bytes[];
     __shared__ float4 red[2][kRingThreads / 32];
+    __shared__ float joined[2][8][4];
     starts_early();
     after_previous();
-    const int gt = shape.gt, places = shape.places, g = threadIdx.x / gt, t = threadIdx.x % gt;
-    const bool end = (t + (NV - 1) * gt) * 8 < a.cols;
-    const Vectors<NV, FLOATS> vec{ring_bytes, gt, t};
-    const Ring<NV, 2> ring{ring_bytes + 3 * NV * gt * vec.kChunk, gt, shape.groups, g, t};
-    if (g == 0) {
-        vec.fill(a.post, 0, end);
-        vec.fill(a.gate, 1, end);
-        vec.fill(a.gamma, 2, end);
-        copies_end();
-        copies_wait(0);
-    }
-    __syncthreads();
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * shape.groups, first = static_cast<int64_t>(blockIdx.x) * shape.groups + g;
-    const float n = static_cast<float>(a.cols);
+    const int places = shape.places, cluster = shape.cluster;
+    if (cluster > 1) cluster_sync();   // the others' shared memory is there
+    const Place<NV> at(shape, a.cols);
+    const Vectors<NV, FLOATS> vec{ring_bytes};
+    const Ring<NV, 2, ANY> ring{ring_bytes + 3 * NV * at.gt * vec.kChunk};
+    const int64_t stride = static_cast<int64_t>(gridDim.x / cluster) * at.groups, first = static_cast<int64_t>(blockIdx.x / cluster) * at.groups + at.g;
     const auto issue = [&](int64_t row, int place) {
         if (row < a.rows) {
-            ring.copy(a.o, row, place, 0, end);
-            ring.copy(a.h, row, place, 1, end);
+            ring.copy(at, a.o, row, place, 0);
+            ring.copy(at, a.h, row, place, 1);
         }
         copies_end();
     };
     for (int s = 0; s + 1 < places; ++s) issue(first + s * stride, s);
+    if (at.g == 0) {
+        vec.fill(at, a.post, a.param_dtype, 0);
+        vec.fill(at, a.gate, a.param_dtype, 1);
+        vec.fill(at, a.gamma, a.param_dtype, 2);
+    }
+    __syncthreads();
+    const float n = static_cast<float>(a.cols);
+    const bool tells = at.t == 0 && at.first == 0;   // the statistics
     int place = 0;
     for (int64_t row = first; row < a.rows; row += stride) {
         issue(row + (places - 1) * stride, place == 0 ? places - 1 : place - 1);
@@ -480,9 +529,8 @@ __global__ void __launch_bounds__(kRingThreads) residual_norm_ring_kernel(const 
         f32x2 ss = 0;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const bool on = k + 1 < NV || end;
-            pairs(on ? ring.read(place, 0, k) : make_uint4(0, 0, 0, 0), o[k]);
-            pairs(on ? ring.read(place, 1, k) : make_uint4(0, 0, 0, 0), s[k]);
+            pairs(ring.read(at, a.o, row, place, 0, k), o[k]);
+            pairs(ring.read(at, a.h, row, place, 1, k), s[k]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) ss = fma2(o[k][j], o[k][j], ss);
         }
@@ -490,85 +538,93 @@ __global__ void __launch_bounds__(kRingThreads) residual_norm_ring_kernel(const 
         float post_rstd = 1.0f;
         if (a.post != nullptr) {
             float sum[1] = {both(ss)};
-            group_sums(sum, red[0], g, gt);
+            group_sums(sum, red[0], at.g, at.gt);
+            cluster_sums(sum, joined[0], cluster);
             post_rstd = 1.0f / sqrtf(sum[0] / n + a.eps);
-            if (t == 0) a.post_rstd[row] = post_rstd;
+            if (tells) a.post_rstd[row] = post_rstd;
         }
         ss = 0;
-        uint8_t* out = static_cast<uint8_t*>(a.out.p) + (row * a.out.ld + t * 8) * 2;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (k + 1 < NV || end) {
-                f32x2 p[4], w[4];
-                vec.read(0, k, p);
-                vec.read(1, k, w);
+            f32x2 p[4], w[4];
+            vec.read(at, 0, k, p);
+            vec.read(at, 1, k, w);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const f32x2 b = mul2(mul2(mul2(o[k][j], twice(post_rstd)), p[j]), w[j]);
-                    s[k][j] = fma2(s[k][j], twice(a.alpha), b);
-                    ss = fma2(s[k][j], s[k][j], ss);
-                }
-                *reinterpret_cast<uint4*>(out + k * gt * 16) = rounded(s[k]);
+            for (int j = 0; j < 4; ++j) {
+                const f32x2 b = mul2(mul2(mul2(o[k][j], twice(post_rstd)), p[j]), w[j]);
+                s[k][j] = fma2(s[k][j], twice(a.alpha), b);
+                ss = fma2(s[k][j], s[k][j], ss);   // 0 past the row's end
             }
+            put<NV, ANY>(at, a.out, row, k, s[k]);
         }
         float sum[1] = {both(ss)};
-        group_sums(sum, red[1], g, gt);
+        group_sums(sum, red[1], at.g, at.gt);
+        cluster_sums(sum, joined[1], cluster);
         const float rstd = 1.0f / sqrtf(sum[0] / n + a.eps);
-        if (t == 0) a.rstd[row] = rstd;
-        uint8_t* y = static_cast<uint8_t*>(a.y.p) + (row * a.y.ld + t * 8) * 2;
+        if (tells) a.rstd[row] = rstd;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (k + 1 < NV || end) {
-                f32x2 w[4];
-                vec.read(2, k, w);
+            f32x2 w[4];
+            vec.read(at, 2, k, w);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[k][j] = mul2(mul2(s[k][j], twice(rstd)), w[j]);
-                *reinterpret_cast<uint4*>(y + k * gt * 16) = rounded(s[k]);
-            }
+            for (int j = 0; j < 4; ++j) s[k][j] = mul2(mul2(s[k][j], twice(rstd)), w[j]);
+            put<NV, ANY>(at, a.y, row, k, s[k]);
         }
-        if (a.post == nullptr) asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "r"(gt) : "memory");   // keeps the rows' sums apart
+        if (a.post == nullptr) {   // one barrier a row does not keep the rows' sums apart
+            if (cluster > 1) cluster_sync();
+            else asm volatile("bar.sync %0, %1;" ::"r"(1 + at.g), "r"(at.gt) : "memory");
+        }
     }
 }
 
-template <int NV, bool FLOATS>
+template <int NV, bool FLOATS, bool ANY>
 __global__ void __launch_bounds__(kRingThreads) residual_norm_backward_ring_kernel(const __grid_constant__ ResidualNormGrad a,
                                                                                    const RingShape shape) {
     extern __shared__ __align__(16) uint8_t ring_bytes[];
     __shared__ float4 red[2][kRingThreads / 32];
+    __shared__ float joined[2][8][4];
     starts_early();
     after_previous();
-    const int gt = shape.gt, places = shape.places, g = threadIdx.x / gt, t = threadIdx.x % gt;
-    const bool end = (t + (NV - 1) * gt) * 8 < a.cols;
-    const Vectors<NV, FLOATS> vec{ring_bytes, gt, t};
-    const Ring<NV, 4> ring{ring_bytes + 3 * NV * gt * vec.kChunk, gt, shape.groups, g, t};
-    if (g == 0) {
-        vec.fill(a.post, 0, end);
-        vec.fill(a.gate, 1, end);
-        vec.fill(a.gamma, 2, end);
-        copies_end();
-        copies_wait(0);
-    }
-    __syncthreads();
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * shape.groups, first = static_cast<int64_t>(blockIdx.x) * shape.groups + g;
-    const float inv_n = 1.0f / static_cast<float>(a.cols);
+    const int places = shape.places, cluster = shape.cluster;
+    if (cluster > 1) cluster_sync();   // the others' shared memory is there
+    const Place<NV> at(shape, a.cols);
+    const Vectors<NV, FLOATS> vec{ring_bytes};
+    const Ring<NV, 4, ANY> ring{ring_bytes + 3 * NV * at.gt * vec.kChunk};
+    const int64_t stride = static_cast<int64_t>(gridDim.x / cluster) * at.groups, first = static_cast<int64_t>(blockIdx.x / cluster) * at.groups + at.g;
     const auto issue = [&](int64_t row, int place) {
         if (row < a.rows) {
-            ring.copy(a.dy, row, place, 0, end);
-            ring.copy(a.dout, row, place, 1, end);
-            ring.copy(a.out, row, place, 2, end);
-            ring.copy(a.o, row, place, 3, end);
+            ring.copy(at, a.dy, row, place, 0);
+            ring.copy(at, a.dout, row, place, 1);
+            ring.copy(at, a.out, row, place, 2);
+            ring.copy(at, a.o, row, place, 3);
         }
         copies_end();
     };
     for (int s = 0; s < places; ++s) issue(first + s * stride, s);
+    if (at.g == 0) {
+        vec.fill(at, a.post, a.param_dtype, 0);
+        vec.fill(at, a.gate, a.param_dtype, 1);
+        vec.fill(at, a.gamma, a.param_dtype, 2);
+    }
+    __syncthreads();
+    const float inv_n = 1.0f / static_cast<float>(a.cols);
     f32x2 dg[NV][4], du[NV][4];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) dg[k][j] = du[k][j] = 0;
     int place = 0, flip = 0;
+    float next1 = 1.0f, next2 = 1.0f;   // the next row's statistics
+    const auto statistics = [&](int64_t row) {
+        if (row < a.rows) {
+            next1 = a.rstd[row];
+            if (a.post != nullptr) next2 = a.post_rstd[row];
+        }
+    };
+    statistics(first);
     for (int64_t row = first; row < a.rows; row += stride) {
-        const float r1 = a.rstd[row], r2 = a.post != nullptr ? a.post_rstd[row] : 1.0f;
+        const float r1 = next1, r2 = next2;
+        statistics(row + stride);
         const f32x2 rstd = twice(r1), post_rstd = twice(r2);
         copies_wait(places - 1);
         // the row's words stay in registers, and their places take the rows ahead at once
@@ -579,7 +635,7 @@ __global__ void __launch_bounds__(kRingThreads) residual_norm_backward_ring_kern
             pairs(w[1], tt);
             pairs(w[2], xh);
             pairs(w[3], u);
-            vec.read(2, k, gr);
+            vec.read(at, 2, k, gr);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 xh[j] = mul2(xh[j], rstd);
@@ -590,72 +646,70 @@ __global__ void __launch_bounds__(kRingThreads) residual_norm_backward_ring_kern
         };
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
+            raw[k][0] = ring.read(at, a.dy, row, place, 0, k);
+            raw[k][1] = ring.read(at, a.dout, row, place, 1, k);
+            raw[k][2] = ring.read(at, a.out, row, place, 2, k);
+            raw[k][3] = ring.read(at, a.o, row, place, 3, k);
+            f32x2 xh[4], tt[4], u[4], gr[4], dy[4], p[4], w[4];
+            expand(raw[k], k, xh, tt, u, gr, dy);
+            vec.read(at, 0, k, p);
+            vec.read(at, 1, k, w);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) raw[k][m] = k + 1 < NV || end ? ring.read(place, m, k) : make_uint4(0, 0, 0, 0);
-            if (k + 1 < NV || end) {
-                f32x2 xh[4], tt[4], u[4], x[4], dy[4], p[4], w[4];
-                expand(raw[k], k, xh, tt, u, x, dy);
-                vec.read(0, k, p);
-                vec.read(1, k, w);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    dg[k][j] = fma2(dy[j], xh[j], dg[k][j]);
-                    s1 = fma2(x[j], xh[j], s1);
-                    const f32x2 ku = mul2(mul2(p[j], w[j]), u[j]);
-                    s2 = fma2(ku, tt[j], s2);
-                    s3 = fma2(ku, xh[j], s3);
-                }
+            for (int j = 0; j < 4; ++j) {
+                dg[k][j] = fma2(dy[j], xh[j], dg[k][j]);
+                s1 = fma2(gr[j], xh[j], s1);
+                const f32x2 ku = mul2(mul2(p[j], w[j]), u[j]);
+                s2 = fma2(ku, tt[j], s2);
+                s3 = fma2(ku, xh[j], s3);
             }
         }
         issue(row + places * stride, place);
         place = place + 1 == places ? 0 : place + 1;
         float sum[3] = {both(s1), both(s2), both(s3)};
-        group_sums(sum, red[flip], g, gt);
+        group_sums(sum, red[flip], at.g, at.gt);
+        cluster_sums(sum, joined[flip], cluster);
         flip ^= 1;
         const float c1 = sum[0] * inv_n, c2 = a.post != nullptr ? (sum[1] - r1 * c1 * sum[2]) * inv_n : 0.0f;
         const f32x2 less1 = twice(-r1 * c1), less2 = twice(-c2), alpha = twice(a.alpha);
-        uint8_t* dh = static_cast<uint8_t*>(a.dh.p) + (row * a.dh.ld + t * 8) * 2;
-        uint8_t* db = static_cast<uint8_t*>(a.dblock.p) + (row * a.dblock.ld + t * 8) * 2;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (k + 1 < NV || end) {
-                f32x2 xh[4], tt[4], u[4], x[4], dy[4], p[4], w[4];
-                expand(raw[k], k, xh, tt, u, x, dy);
-                vec.read(0, k, p);
-                vec.read(1, k, w);
+            f32x2 xh[4], tt[4], u[4], gr[4], dy[4], p[4], w[4];
+            expand(raw[k], k, xh, tt, u, gr, dy);
+            vec.read(at, 0, k, p);
+            vec.read(at, 1, k, w);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    tt[j] = fma2(less1, xh[j], tt[j]);
-                    du[k][j] = fma2(tt[j], u[j], du[k][j]);
-                    u[j] = mul2(post_rstd, fma2(u[j], less2, mul2(tt[j], mul2(p[j], w[j]))));
-                    tt[j] = mul2(tt[j], alpha);
-                }
-                *reinterpret_cast<uint4*>(dh + k * gt * 16) = rounded(tt);
-                *reinterpret_cast<uint4*>(db + k * gt * 16) = rounded(u);
+            for (int j = 0; j < 4; ++j) {
+                tt[j] = fma2(less1, xh[j], tt[j]);
+                du[k][j] = fma2(tt[j], u[j], du[k][j]);
+                u[j] = mul2(post_rstd, fma2(u[j], less2, mul2(tt[j], mul2(p[j], w[j]))));
+                tt[j] = mul2(tt[j], alpha);
             }
+            put<NV, ANY>(at, a.dh, row, k, tt);
+            put<NV, ANY>(at, a.dblock, row, k, u);
         }
     }
     // the groups' column sums meet in shared memory: element j of chunk i at j * slots + i
     copies_wait(0);
     __syncthreads();
-    const int slots = NV * gt + 4;
+    const int slots = NV * at.gt + 4;
     float* comb = reinterpret_cast<float*>(ring_bytes);
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float* to = comb + (g * 16 + 2 * j) * slots + t + k * gt;
+            float* to = comb + (at.g * 16 + 2 * j) * slots + at.t + k * at.gt;
             unpair(dg[k][j], to[0], to[slots]);
             unpair(du[k][j], to[8 * slots], to[9 * slots]);
         }
     __syncthreads();
-    float* part = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+    float* part = a.partials + static_cast<int64_t>(blockIdx.x / cluster) * 2 * a.cols + at.first * 8;
+    const int columns = static_cast<int>(max(int64_t(0), min(a.cols - at.first * 8, static_cast<int64_t>(shape.chunks) * 8)));
 #pragma unroll
     for (int o = 0; o < 2; ++o)
-        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+        for (int c = threadIdx.x; c < columns; c += blockDim.x) {
             const float* from = comb + (o * 8 + (c & 7)) * slots + (c >> 3);
             float s = from[0];
-            for (int h = 1; h < shape.groups; ++h) s += from[h * 16 * slots];
+            for (int h = 1; h < at.groups; ++h) s += from[h * 16 * slots];
             part[o * a.cols + c] = s;
         }
 }
@@ -728,18 +782,26 @@ Spread spread(int64_t cols) {
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool aligned_or_none(const Mat& m) { return m.p == nullptr || rows_aligned(m); }
 
-// Groups and places of the ring for `matrices` rows of BF16; NV 0 where they do not fit.
-int ring_shape(int64_t rows, int64_t cols, int matrices, int param_dtype, int places, RingShape* s, int* bytes) {
-    const int64_t chunks = cols / 8;
-    const int nv = static_cast<int>((chunks + kRingThreads - 1) / kRingThreads);
-    if (nv > 3) return 0;
-    s->gt = round32((chunks + nv - 1) / nv);
-    if (static_cast<int64_t>(nv - 1) * s->gt >= chunks) return 0;
-    s->groups = static_cast<int>(std::min<int64_t>(std::min(kRingThreads / s->gt, 15), rows));
-    const int keep = 3 * nv * s->gt * (param_dtype == FSDP_DTYPE_F32 ? 32 : 16), row = matrices * nv * s->gt * 16;
-    s->places = std::min(kMostPlaces, (kSharedMost - keep) / (row * s->groups));
-    *bytes = keep + s->places * s->groups * row;
-    return s->places >= places ? nv : 0;
+// How the ring takes `matrices` rows of BF16: chunks to a thread (0: it does not), threads, groups,
+// clusters and places, with `most` chunks to a thread at most.
+int ring_shape(int64_t rows, int64_t cols, int matrices, bool floats, bool any, int most, int least_places, RingShape* s, int* bytes) {
+    const int64_t chunks = (cols + 7) / 8;
+    for (s->cluster = 1; s->cluster <= 8; s->cluster *= 2) {
+        const int64_t share = (chunks + s->cluster - 1) / s->cluster;
+        const int nv = static_cast<int>((share + kRingThreads - 1) / kRingThreads);
+        if (nv > most) continue;
+        s->chunks = static_cast<int>(share);
+        s->gt = round32((share + nv - 1) / nv);
+        s->groups = s->cluster > 1 ? 1 : static_cast<int>(std::min<int64_t>(std::min(kRingThreads / s->gt, 15), rows));
+        const int keep = 3 * nv * s->gt * (floats ? 32 : 16), row = matrices * nv * s->gt * (any ? 32 : 16);
+        while (s->groups > 1 && keep + least_places * s->groups * row > kSharedMost) --s->groups;
+        s->places = std::min(kMostPlaces, (kSharedMost - keep) / (row * s->groups));
+        // only a thread's last chunk may lie past the end of a share, the last and smallest one too
+        if (s->places < least_places || static_cast<int64_t>(nv - 1) * s->gt > chunks - (s->cluster - 1) * share) continue;
+        *bytes = keep + s->places * s->groups * row;
+        return nv;
+    }
+    return 0;
 }
 
 }  // namespace
@@ -750,21 +812,22 @@ cudaError_t launch_residual_norm_forward(const ResidualNorm& a, int sms, cudaStr
     if (a.rows == 0) return cudaSuccess;
     const bool aligned = a.cols % 8 == 0 && rows_aligned(a.h) && aligned_or_none(a.o) && rows_aligned(a.out) && aligned_or_none(a.y) &&
                          on16(a.post) && on16(a.gate) && on16(a.gamma);
-    const bool fast = aligned && a.o.p != nullptr && a.y.p != nullptr && a.h.dtype == FSDP_DTYPE_BF16 && a.o.dtype == FSDP_DTYPE_BF16 &&
+    const bool half = a.o.p != nullptr && a.y.p != nullptr && a.h.dtype == FSDP_DTYPE_BF16 && a.o.dtype == FSDP_DTYPE_BF16 &&
                       a.out.dtype == FSDP_DTYPE_BF16 && a.y.dtype == FSDP_DTYPE_BF16;
+    const bool floats = !aligned || a.param_dtype == FSDP_DTYPE_F32;
     RingShape shape;
     int bytes = 0;
-    const int nv = fast ? ring_shape(a.rows, a.cols, 2, a.param_dtype, 2, &shape, &bytes) : 0;
-    if (nv != 0 && a.rows >= 2 * static_cast<int64_t>(sms) * shape.groups) {   // rows enough for every group to walk two
-        const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((a.rows + shape.groups - 1) / shape.groups, sms));
+    const int nv = half ? ring_shape(a.rows, a.cols, 2, floats, !aligned, 3, 2, &shape, &bytes) : 0;
+    if (nv != 0 && a.rows * shape.cluster >= 2 * static_cast<int64_t>(sms) * shape.groups) {   // rows enough for every group to walk two
+        const unsigned clusters = static_cast<unsigned>(std::min<int64_t>((a.rows + shape.groups - 1) / shape.groups, sms / shape.cluster));
         const int threads = shape.gt * shape.groups;
-        const bool floats = a.param_dtype == FSDP_DTYPE_F32;
-#define RING(nv_)                                                                                                             \
-    if (nv == nv_)                                                                                                            \
-        return floats ? launch_shared<residual_norm_ring_kernel<nv_, true>>(blocks, threads, bytes, st, a, shape)            \
-                      : launch_shared<residual_norm_ring_kernel<nv_, false>>(blocks, threads, bytes, st, a, shape);
+#define RING_(nv_, f, any)                                                                                                       \
+    if (nv == nv_ && floats == f && aligned != any)                                                                              \
+        return launch_shared_clusters<residual_norm_ring_kernel<nv_, f, any>>(clusters * shape.cluster, threads, bytes, shape.cluster, st, a, shape);
+#define RING(nv_) RING_(nv_, false, false) RING_(nv_, true, false) RING_(nv_, true, true)
         RING(1) RING(2) RING(3)
 #undef RING
+#undef RING_
     }
     const Spread s = spread(a.cols);
     if (s.threads != 0) {
@@ -778,29 +841,30 @@ cudaError_t launch_residual_norm_forward(const ResidualNorm& a, int sms, cudaStr
 cudaError_t launch_residual_norm_backward(const ResidualNormGrad& a, int sms, cudaStream_t st) {
     const bool aligned = a.cols % 8 == 0 && aligned_or_none(a.dy) && aligned_or_none(a.dout) && aligned_or_none(a.out) && aligned_or_none(a.o) &&
                          rows_aligned(a.dh) && aligned_or_none(a.dblock) && on16(a.post) && on16(a.gate) && on16(a.gamma);
-    const bool fast = aligned && a.dy.p != nullptr && a.dout.p != nullptr && a.o.p != nullptr && a.dy.dtype == FSDP_DTYPE_BF16 &&
+    const bool half = a.dy.p != nullptr && a.dout.p != nullptr && a.o.p != nullptr && a.dy.dtype == FSDP_DTYPE_BF16 &&
                       a.dout.dtype == FSDP_DTYPE_BF16 && a.out.dtype == FSDP_DTYPE_BF16 && a.o.dtype == FSDP_DTYPE_BF16 &&
                       a.dh.dtype == FSDP_DTYPE_BF16 && a.dblock.dtype == FSDP_DTYPE_BF16;
+    const bool floats = !aligned || a.param_dtype == FSDP_DTYPE_F32;
     int64_t count = 0;   // of partial rows
     cudaError_t e = cudaSuccess;
     if (a.rows > 0) {
         RingShape shape;
         int bytes = 0;
-        const int nv = fast ? ring_shape(a.rows, a.cols, 4, a.param_dtype, 1, &shape, &bytes) : 0;
+        const int nv = half ? ring_shape(a.rows, a.cols, 4, floats, !aligned, 2, 1, &shape, &bytes) : 0;
         const Spread s = spread(a.cols);
         if (nv != 0) {
-            count = std::min<int64_t>((a.rows + shape.groups - 1) / shape.groups, sms);
-            const unsigned blocks = static_cast<unsigned>(count);
+            count = std::min<int64_t>((a.rows + shape.groups - 1) / shape.groups, sms / shape.cluster);
+            const unsigned blocks = static_cast<unsigned>(count * shape.cluster);
             const int threads = shape.gt * shape.groups;
             bytes = std::max(bytes, shape.groups * 16 * (nv * shape.gt + 4) * 4);
-            const bool floats = a.param_dtype == FSDP_DTYPE_F32;
             e = cudaErrorInvalidConfiguration;
-#define RING(nv_)                                                                                                          \
-    if (nv == nv_)                                                                                                         \
-        e = floats ? launch_shared<residual_norm_backward_ring_kernel<nv_, true>>(blocks, threads, bytes, st, a, shape)    \
-                   : launch_shared<residual_norm_backward_ring_kernel<nv_, false>>(blocks, threads, bytes, st, a, shape);
-            RING(1) RING(2) RING(3)
+#define RING_(nv_, f, any)                                                                                                       \
+    if (nv == nv_ && floats == f && aligned != any)                                                                              \
+        e = launch_shared_clusters<residual_norm_backward_ring_kernel<nv_, f, any>>(blocks, threads, bytes, shape.cluster, st, a, shape);
+#define RING(nv_) RING_(nv_, false, false) RING_(nv_, true, false) RING_(nv_, true, true)
+            RING(1) RING(2)
 #undef RING
+#undef RING_
         } else if (s.threads != 0) {
             count = std::min(a.rows, std::max<int64_t>(1, static_cast<int64_t>(sms) * s.blocks / s.cluster));
             e = launch_early_clusters(aligned ? residual_norm_backward_kernel<false> : residual_norm_backward_kernel<true>,

@@ -45,14 +45,18 @@ __device__ __forceinline__ float both(f32x2 v) {
 
 constexpr int kSharedMost = 222 * 1024;   // dynamic shared memory of a block
 
-// Launches with `bytes` of dynamic shared memory.
-template <auto kernel, typename... Args>
-cudaError_t launch_shared(unsigned blocks, int threads, int bytes, cudaStream_t st, const Args&... args) {
+// Launches with `bytes` of dynamic shared memory, at most MOST, in clusters of `cluster` blocks.
+template <auto kernel, int MOST = kSharedMost, typename... Args>
+cudaError_t launch_shared_clusters(unsigned blocks, int threads, int bytes, int cluster, cudaStream_t st, const Args&... args) {
     const int allowed = once_per_device([] {
-        return static_cast<int>(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedMost));
+        return static_cast<int>(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST));
     });
     if (allowed != cudaSuccess) return static_cast<cudaError_t>(allowed);
-    return launch_early(kernel, dim3(blocks), threads, static_cast<size_t>(bytes), st, args...);
+    return launch_early_clusters(kernel, dim3(blocks), threads, static_cast<size_t>(bytes), cluster, st, args...);
+}
+template <auto kernel, typename... Args>
+cudaError_t launch_shared(unsigned blocks, int threads, int bytes, cudaStream_t st, const Args&... args) {
+    return launch_shared_clusters<kernel>(blocks, threads, bytes, 1, st, args...);
 }
 
 }  // namespace fsdp
