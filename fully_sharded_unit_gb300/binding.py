@@ -818,10 +818,13 @@ def _array(t, shape, dtype, device=None):
     """The address of a contiguous CUDA tensor of this shape and dtype; None for None."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.get_device() < 0 or t.dtype != dtype or t.shape != shape or not t.is_contiguous() \
-            or (device is not None and t.get_device() != device):
-        _refuse(f"a contiguous {dtype} CUDA tensor of {tuple(shape)} on the handle's device is expected, not {_about(t)}")
-    return t.data_ptr()
+    try:
+        at = t.get_device()
+        if (at == device or (device is None and at >= 0)) and t.dtype is dtype and t.shape == shape and t.is_contiguous() and at >= 0:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(f"a contiguous {dtype} CUDA tensor of {tuple(shape)} on the handle's device is expected, not {_about(t)}")
 
 
 def _shaped(t, name, device):
@@ -893,7 +896,7 @@ def _vecs(named, n, device):
             out.append(None)
             continue
         p, dt = _vec(t, n, device)
-        if kind is not None:
+        if kind is not None and dt != kind:
             _same(kind, dt, ", ".join(k for k, v in named if v is not None))
         kind = dt
         out.append(p)

@@ -442,19 +442,65 @@ struct Vectors {
     uint8_t* base;
     static constexpr int kChunk = FLOATS ? 32 : 16;
     __device__ uint8_t* slot(const Place<NV>& at, int v, int k) const { return base + (v * NV + k) * at.gt * kChunk + at.t * 16; }
-    __device__ void fill(const Place<NV>& at, const void* p, int dtype, int v) const {
+    // From 16-byte boundaries, of the slots' type: asynchronous.
+    __device__ void copy(const Place<NV>& at, const void* p, int v) const {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            float x[8];
-            load_any(p, dtype, at.column(k), at.in(k), 1.0f, x);
-            uint4* to = reinterpret_cast<uint4*>(slot(at, v, k));
-            if (FLOATS) {
-                *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
-                *reinterpret_cast<float4*>(to + at.gt) = make_float4(x[4], x[5], x[6], x[7]);
+            if (at.in(k) == 0) continue;
+            uint8_t* to = slot(at, v, k);
+            if (p != nullptr) {
+                const uint8_t* from = static_cast<const uint8_t*>(p) + at.column(k) / 8 * kChunk;
+                copy16(shared_at(to), from);
+                if (FLOATS) copy16(shared_at(to + at.gt * 16), from + 16);
             } else {
-                *to = make_uint4(to_bf16x2(x[0], x[1]), to_bf16x2(x[2], x[3]), to_bf16x2(x[4], x[5]), to_bf16x2(x[6], x[7]));
+                const uint32_t one = FLOATS ? 0x3f800000u : 0x3f803f80u;
+                *reinterpret_cast<uint4*>(to) = make_uint4(one, one, one, one);
+                if (FLOATS) *reinterpret_cast<uint4*>(to + at.gt * 16) = make_uint4(one, one, one, one);
             }
         }
+    }
+    // From anywhere, of either type, to floats.
+    __device__ void load(const Place<NV>& at, const void* p, int dtype, int v) const {
+        float x[NV][8];
+        int in[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            in[k] = at.in(k);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[k][j] = 1.0f;
+        }
+        if (p != nullptr) load_chunks_any<NV>(p, dtype, at.column(0), in, at.gt * 8, x);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float4* to = reinterpret_cast<float4*>(slot(at, v, k));
+            to[0] = make_float4(x[k][0], x[k][1], x[k][2], x[k][3]);
+            to[at.gt] = make_float4(x[k][4], x[k][5], x[k][6], x[k][7]);
+        }
+    }
+    // All three; `ahead` issues the ring's first copies, of `groups` groups.
+    template <bool ANY, typename Ahead>
+    __device__ void fill(const Place<NV>& at, const void* v0, const void* v1, const void* v2, int dtype, int groups, Ahead ahead) const {
+        if (!ANY) {
+            if (at.g == 0) {
+                copy(at, v0, 0);
+                copy(at, v1, 1);
+                copy(at, v2, 2);
+            }
+            copies_end();
+        }
+        ahead();
+        if (ANY) {
+            if constexpr (FLOATS) {
+                if (at.g == 0) {
+                    load(at, v0, dtype, 0);
+                    load(at, v1, dtype, 1);
+                    load(at, v2, dtype, 2);
+                }
+            }
+        } else {
+            copies_wait(groups);
+        }
+        __syncthreads();
     }
     __device__ void read(const Place<NV>& at, int v, int k, f32x2* x) const {
         const uint8_t* from = slot(at, v, k);
@@ -512,13 +558,9 @@ __global__ void __launch_bounds__(kRingThreads) residual_norm_ring_kernel(const 
         }
         copies_end();
     };
-    for (int s = 0; s + 1 < places; ++s) issue(first + s * stride, s);
-    if (at.g == 0) {
-        vec.fill(at, a.post, a.param_dtype, 0);
-        vec.fill(at, a.gate, a.param_dtype, 1);
-        vec.fill(at, a.gamma, a.param_dtype, 2);
-    }
-    __syncthreads();
+    vec.template fill<ANY>(at, a.post, a.gate, a.gamma, a.param_dtype, places - 1, [&] {
+        for (int s = 0; s + 1 < places; ++s) issue(first + s * stride, s);
+    });
     const float n = static_cast<float>(a.cols);
     const bool tells = at.t == 0 && at.first == 0;   // the statistics
     int place = 0;
@@ -600,13 +642,9 @@ __global__ void __launch_bounds__(kRingThreads) residual_norm_backward_ring_kern
         }
         copies_end();
     };
-    for (int s = 0; s < places; ++s) issue(first + s * stride, s);
-    if (at.g == 0) {
-        vec.fill(at, a.post, a.param_dtype, 0);
-        vec.fill(at, a.gate, a.param_dtype, 1);
-        vec.fill(at, a.gamma, a.param_dtype, 2);
-    }
-    __syncthreads();
+    vec.template fill<ANY>(at, a.post, a.gate, a.gamma, a.param_dtype, places, [&] {
+        for (int s = 0; s < places; ++s) issue(first + s * stride, s);
+    });
     const float inv_n = 1.0f / static_cast<float>(a.cols);
     f32x2 dg[NV][4], du[NV][4];
 #pragma unroll
@@ -712,6 +750,163 @@ __global__ void __launch_bounds__(kRingThreads) residual_norm_backward_ring_kern
             for (int h = 1; h < at.groups; ++h) s += from[h * 16 * slots];
             part[o * a.cols + c] = s;
         }
+}
+
+// The same for rows of 8200 to 12288 columns on 16-byte boundaries, a row to a block: the vectors lie
+// in registers, as BF16, and two whole rows in the ring, from which both passes over a
+// row read.  (With the vectors in shared memory there is room for one row; and a thread's three
+// chunks, with their columns' sums, leave no registers to hold a row in between, 187 us at 4096 x 12288.)
+constexpr int kKeepChunks = 3;
+template <bool GATE>
+__global__ void __launch_bounds__(kRingThreads) residual_norm_backward_keep_kernel(const __grid_constant__ ResidualNormGrad a, const RingShape shape) {
+    constexpr int NV = kKeepChunks;
+    extern __shared__ __align__(16) uint8_t ring_bytes[];
+    __shared__ float4 red[2][kRingThreads / 32];
+    starts_early();
+    after_previous();
+    const Place<NV> at(shape, a.cols);
+    const Ring<NV, 4, false> ring{ring_bytes};
+    const int64_t stride = gridDim.x;
+    const auto issue = [&](int64_t row, int place) {
+        if (row < a.rows) {
+            ring.copy(at, a.dy, row, place, 0);
+            ring.copy(at, a.out, row, place, 2);
+            ring.copy(at, a.dout, row, place, 1);
+            ring.copy(at, a.o, row, place, 3);
+        }
+        copies_end();
+    };
+    issue(blockIdx.x, 0);
+    uint4 gammas[NV], posts[NV], gates[NV];
+    const auto vector = [&](const void* p, uint4* v) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            v[k] = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+            if (p != nullptr && at.in(k) != 0) v[k] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + at.column(k) * 2);
+        }
+    };
+    vector(a.gamma, gammas);
+    vector(a.post, posts);
+    if (GATE) vector(a.gate, gates);
+    const float inv_n = 1.0f / static_cast<float>(a.cols);
+    f32x2 dg[NV][4], du[NV][4];
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dg[k][j] = du[k][j] = 0;
+    int place = 0;
+    float next1 = 1.0f, next2 = 1.0f;   // the next row's statistics
+    const auto statistics = [&](int64_t row) {
+        if (row < a.rows) {
+            next1 = a.rstd[row];
+            if (a.post != nullptr) next2 = a.post_rstd[row];
+        }
+    };
+    statistics(blockIdx.x);
+    for (int64_t row = blockIdx.x; row < a.rows; row += stride) {
+        const float r1 = next1, r2 = next2;
+        statistics(row + stride);
+        issue(row + stride, place ^ 1);
+        copies_wait(1);
+        const f32x2 rstd = twice(r1), post_rstd = twice(r2);
+        // half a chunk at a time, which keeps what is expanded in the registers that are left
+        const auto words = [](uint4 w, int half, f32x2* v) {
+            const uint32_t x = half ? w.z : w.x, y = half ? w.w : w.y;
+            v[0] = pair(bf16_lo(x), bf16_hi(x));
+            v[1] = pair(bf16_lo(y), bf16_hi(y));
+        };
+        const auto read = [&](int k, uint4* raw) {
+            raw[0] = ring.read(at, a.dy, row, place, 0, k);
+            raw[1] = ring.read(at, a.dout, row, place, 1, k);
+            raw[2] = ring.read(at, a.out, row, place, 2, k);
+            raw[3] = ring.read(at, a.o, row, place, 3, k);
+        };
+        const auto expand = [&](const uint4* raw, int k, int half, f32x2* xh, f32x2* tt, f32x2* u, f32x2* gr, f32x2* dy, f32x2* kk) {
+            words(raw[0], half, dy);
+            words(raw[1], half, tt);
+            words(raw[2], half, xh);
+            words(raw[3], half, u);
+            words(gammas[k], half, gr);
+            words(posts[k], half, kk);
+            f32x2 w[2];
+            if (GATE) words(gates[k], half, w);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                xh[j] = mul2(xh[j], rstd);
+                gr[j] = mul2(dy[j], gr[j]);
+                tt[j] = fma2(rstd, gr[j], tt[j]);
+                u[j] = mul2(u[j], post_rstd);
+                if (GATE) kk[j] = mul2(kk[j], w[j]);
+            }
+        };
+        f32x2 s1 = 0, s2 = 0, s3 = 0;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            uint4 raw[4];
+            read(k, raw);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                f32x2 xh[2], tt[2], u[2], gr[2], dy[2], kk[2];
+                expand(raw, k, half, xh, tt, u, gr, dy, kk);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    dg[k][2 * half + j] = fma2(dy[j], xh[j], dg[k][2 * half + j]);
+                    s1 = fma2(gr[j], xh[j], s1);
+                    const f32x2 ku = mul2(kk[j], u[j]);
+                    s2 = fma2(ku, tt[j], s2);
+                    s3 = fma2(ku, xh[j], s3);
+                }
+            }
+        }
+        float sum[3] = {both(s1), both(s2), both(s3)};
+        group_sums(sum, red[place], 0, at.gt);
+        const float c1 = sum[0] * inv_n, c2 = a.post != nullptr ? (sum[1] - r1 * c1 * sum[2]) * inv_n : 0.0f;
+        const f32x2 less1 = twice(-r1 * c1), less2 = twice(-c2), alpha = twice(a.alpha);
+        uint8_t* dh = static_cast<uint8_t*>(a.dh.p) + (row * a.dh.ld + at.t * 8) * 2;
+        uint8_t* db = static_cast<uint8_t*>(a.dblock.p) + (row * a.dblock.ld + at.t * 8) * 2;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            uint32_t h[4], b[4];
+            uint4 raw[4];
+            read(k, raw);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                f32x2 xh[2], tt[2], u[2], gr[2], dy[2], kk[2];
+                expand(raw, k, half, xh, tt, u, gr, dy, kk);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    tt[j] = fma2(less1, xh[j], tt[j]);
+                    du[k][2 * half + j] = fma2(tt[j], u[j], du[k][2 * half + j]);
+                    u[j] = mul2(post_rstd, fma2(u[j], less2, mul2(tt[j], kk[j])));
+                    tt[j] = mul2(tt[j], alpha);
+                    float x, y;
+                    unpair(tt[j], x, y);
+                    h[2 * half + j] = to_bf16x2(x, y);
+                    unpair(u[j], x, y);
+                    b[2 * half + j] = to_bf16x2(x, y);
+                }
+            }
+            if (k + 1 < NV || at.last != 0) {
+                *reinterpret_cast<uint4*>(dh + k * at.gt * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(db + k * at.gt * 16) = make_uint4(b[0], b[1], b[2], b[3]);
+            }
+        }
+        place ^= 1;
+    }
+    float* part = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        if (k + 1 < NV || at.last != 0) {
+            float x[8], y[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                unpair(dg[k][j], x[2 * j], x[2 * j + 1]);
+                unpair(du[k][j], y[2 * j], y[2 * j + 1]);
+            }
+            store8(part, FSDP_DTYPE_F32, at.column(k), x);
+            store8(part + a.cols, FSDP_DTYPE_F32, at.column(k), y);
+        }
+    }
 }
 
 // The columns' sums over the blocks, in their order: dgamma from the first half of the
@@ -852,7 +1047,17 @@ cudaError_t launch_residual_norm_backward(const ResidualNormGrad& a, int sms, cu
         int bytes = 0;
         const int nv = half ? ring_shape(a.rows, a.cols, 4, floats, !aligned, 2, 1, &shape, &bytes) : 0;
         const Spread s = spread(a.cols);
-        if (nv != 0) {
+        const int64_t chunks = a.cols / 8;
+        if (half && !floats && chunks > 2 * kRingThreads && chunks <= kKeepChunks * kRingThreads) {
+            shape.cluster = shape.groups = 1;
+            shape.places = 2;
+            shape.chunks = static_cast<int>(chunks);
+            shape.gt = round32((chunks + kKeepChunks - 1) / kKeepChunks);
+            count = std::min<int64_t>(a.rows, sms);
+            bytes = 2 * 4 * kKeepChunks * shape.gt * 16;
+            e = a.gate != nullptr ? launch_shared<residual_norm_backward_keep_kernel<true>>(static_cast<unsigned>(count), shape.gt, bytes, st, a, shape)
+                                  : launch_shared<residual_norm_backward_keep_kernel<false>>(static_cast<unsigned>(count), shape.gt, bytes, st, a, shape);
+        } else if (nv != 0) {
             count = std::min<int64_t>((a.rows + shape.groups - 1) / shape.groups, sms / shape.cluster);
             const unsigned blocks = static_cast<unsigned>(count * shape.cluster);
             const int threads = shape.gt * shape.groups;
