@@ -94,13 +94,21 @@ __device__ __forceinline__ float largest(const uint4* v) {
     }
 }
 
-// The running maximum m of some logits, S = sum 2^((z - m) c) and Q = sum of
-// 2^((z - m) c) (z - m) c, c = scale log2(e).
+// The running maximum m of some logits, S = sum of 2^d and Q = sum of 2^d d over them, where
+// d = z c - mc, c = scale log2(e) and mc = m c as fp32 has it: one rounding a term, and
+// what mc is off by is the same for all of a row's terms and is put right in ln S at the end.
+// (A running maximum too large for that, |mc| from 2^100, has d = (z - m) c instead.)
 struct Soft {
     float m, S, Q;
 };
 
-__device__ __forceinline__ float grown(float from, float to, float c) { return fmaxf((from - to) * c, kNone); }
+__device__ __forceinline__ bool plain(float mc) { return fabsf(mc) < 0x1p100f; }
+
+// d of the old maximum under the new one; at kNone what is behind it vanishes.
+__device__ __forceinline__ float grown(float from, float to, float c) {
+    const float a = __fmul_rn(from, c), b = __fmul_rn(to, c);
+    return fmaxf(plain(a) && plain(b) ? a - b : (from - to) * c, kNone);
+}
 
 __device__ __forceinline__ void rescale(Soft& s, float to, float c) {
     const float d = grown(s.m, to, c), f = exp2_fast(d);
@@ -116,32 +124,58 @@ __device__ __forceinline__ Soft join(Soft a, Soft b, float c) {
     return Soft{m, a.S + b.S, a.Q + b.Q};
 }
 
-// Adds a word's elements to s, whose m is at least as large as they are.
-// Q's terms must not have d = -inf.  A bf16 logit is held at -2^100 first, two at a time, which
-// is as good as masked while m is below 2^99 in magnitude and c is small enough for d to stay finite
-// (`plain`); otherwise d itself is held.
-template <bool BF16, bool ENTROPY>
-__device__ __forceinline__ void add_word(Soft& s, f32x2& S2, f32x2& Q2, uint4 v, float ref, float c, bool plain) {
+// What mc is off by, in natural logarithms.
+__device__ __forceinline__ float anchor_error(float m, float mc, float c) { return plain(mc) ? kLn2 * fmaf(-m, c, mc) : 0.0f; }
+
+// Adds N words' elements to s, whose m is at least as large as they are.  Q's terms must not have
+// d = -inf: a bf16 logit is held at -2^100 first, two at a time, which is as good as masked
+// where d is a plain one and c small enough for it to stay finite; otherwise d itself is held.
+template <bool BF16, bool ENTROPY, bool PLAIN, int N>
+__device__ __forceinline__ void add_words(Soft& s, const uint4* words, float c) {
     constexpr int E = RowWords<BF16>::E;
-    float z[8];
-    if (BF16 && ENTROPY && plain) {
-        constexpr uint32_t kFloor = 0xf180f180u;   // -2^100
-        v = make_uint4(max_nan_bf16x2(v.x, kFloor), max_nan_bf16x2(v.y, kFloor), max_nan_bf16x2(v.z, kFloor), max_nan_bf16x2(v.w, kFloor));
-    }
-    RowWords<BF16>::floats(v, z);
-    const f32x2 less = pair(-ref, -ref), c2 = pair(c, c);
+    const f32x2 c2 = pair(c, c);
+    const float m = s.m == -kInf ? 0.0f : s.m;   // nothing but masked logits so far
+    const float mc = __fmul_rn(m, c);
+    const f32x2 less = PLAIN ? pair(-mc, -mc) : pair(-m, -m);
+    f32x2 S2 = pair(s.S, 0.0f), Q2 = pair(s.Q, 0.0f);
 #pragma unroll
-    for (int j = 0; j < E; j += 2) {
-        float d0, d1;
-        unpair(mul2(add2(pair(z[j], z[j + 1]), less), c2), d0, d1);
-        if (ENTROPY && !(BF16 && plain)) {
-            d0 = max_nan(d0, kNone);
-            d1 = max_nan(d1, kNone);
+    for (int k = 0; k < N; ++k) {
+        uint4 v = words[k];
+        float z[8];
+        if (BF16 && ENTROPY && PLAIN) {
+            constexpr uint32_t kFloor = 0xf180f180u;   // -2^100
+            v = make_uint4(max_nan_bf16x2(v.x, kFloor), max_nan_bf16x2(v.y, kFloor), max_nan_bf16x2(v.z, kFloor), max_nan_bf16x2(v.w, kFloor));
         }
-        const f32x2 e = pair(exp2_fast(d0), exp2_fast(d1));
-        S2 = add2(S2, e);
-        if (ENTROPY) Q2 = fma2(e, pair(d0, d1), Q2);
+        RowWords<BF16>::floats(v, z);
+#pragma unroll
+        for (int j = 0; j < E; j += 2) {
+            f32x2 d = pair(z[j], z[j + 1]);
+            d = PLAIN ? fma2(d, c2, less) : mul2(add2(d, less), c2);
+            float d0, d1;
+            unpair(d, d0, d1);
+            if (ENTROPY && !(BF16 && PLAIN)) {
+                d0 = max_nan(d0, kNone);
+                d1 = max_nan(d1, kNone);
+            }
+            const f32x2 e = pair(exp2_fast(d0), exp2_fast(d1));
+            S2 = add2(S2, e);
+            if (ENTROPY) Q2 = fma2(e, pair(d0, d1), Q2);
+        }
     }
+    float x, y;
+    unpair(S2, x, y);
+    s.S = x + y;
+    unpair(Q2, x, y);
+    s.Q = x + y;
+}
+
+// The same with s.m brought up to them.
+template <bool BF16, bool ENTROPY, int N>
+__device__ __forceinline__ void take_words(Soft& s, const uint4* words, float c) {
+    const float top = largest<BF16, N>(words);
+    if (top > s.m) rescale(s, top, c);
+    if (plain(s.m * c) && c < 0x1p20f) add_words<BF16, ENTROPY, true, N>(s, words, c);
+    else add_words<BF16, ENTROPY, false, N>(s, words, c);
 }
 
 // Orders like the logits, -0 like 0.
@@ -256,32 +290,37 @@ __device__ void top_keys(const RowWords<BF16>& r, int first, int end, int top, u
 
 // ---- gradient ----
 
+// dz = 2^d (A + B d), and a at the token; d as above.  With p = 2^d / S and ln p = d ln 2 - ln S, these
+// are A = -(a + b (h - ln S)) / S and B = -b ln 2 / S.
 struct RowGrad {
-    float a, b;       // scale a (0 without a token), scale b
-    float m, ln2s;    // max z, log2 S
-    float h;          // entropy
+    float a, A, B;
+    float m, mc;
     int64_t token;    // -1: none
     bool zero;        // the whole row
 };
 
-// p (-(a + b h) - b ln p) of N logits; and a at the token.
-template <int N = 8>
+template <int N, bool ENTROPY, bool PLAIN>
 __device__ __forceinline__ void logit_grads(float* v, float c, const RowGrad& g) {
-    const f32x2 less = pair(-g.m, -g.m), c2 = pair(c, c), l = pair(-g.ln2s, -g.ln2s);
-    const float a1 = -fmaf(g.b, g.h, g.a), b1 = -g.b * kLn2;
-    const f32x2 a2 = pair(a1, a1), b2 = pair(b1, b1);
+    const f32x2 c2 = pair(c, c), less = PLAIN ? pair(-g.mc, -g.mc) : pair(-g.m, -g.m), A2 = pair(g.A, g.A), B2 = pair(g.B, g.B);
 #pragma unroll
     for (int j = 0; j < N; j += 2) {
-        float x0, x1;
-        unpair(fma2(add2(pair(v[j], v[j + 1]), less), c2, l), x0, x1);
-        if (b1 != 0.0f) {
-            x0 = max_nan(x0, kNone);
-            x1 = max_nan(x1, kNone);
-            unpair(mul2(pair(exp2_fast(x0), exp2_fast(x1)), fma2(pair(x0, x1), b2, a2)), v[j], v[j + 1]);
-        } else {
-            unpair(mul2(pair(exp2_fast(x0), exp2_fast(x1)), a2), v[j], v[j + 1]);
+        f32x2 d = pair(v[j], v[j + 1]);
+        d = PLAIN ? fma2(d, c2, less) : mul2(add2(d, less), c2);
+        float d0, d1;
+        unpair(d, d0, d1);
+        if (ENTROPY) {
+            d0 = max_nan(d0, kNone);
+            d1 = max_nan(d1, kNone);
         }
+        const f32x2 e = pair(exp2_fast(d0), exp2_fast(d1));
+        unpair(mul2(e, ENTROPY ? fma2(pair(d0, d1), B2, A2) : A2), v[j], v[j + 1]);
     }
+}
+template <int N = 8>
+__device__ __forceinline__ void logit_grads(float* v, float c, const RowGrad& g) {
+    if (!plain(g.mc)) logit_grads<N, true, false>(v, c, g);
+    else if (g.B != 0.0f) logit_grads<N, true, true>(v, c, g);
+    else logit_grads<N, false, true>(v, c, g);
 }
 
 __device__ __forceinline__ int grad_lead(const TokenLogprobs& a, int64_t row) {
@@ -370,7 +409,7 @@ __device__ __forceinline__ void row_gradient(const TokenLogprobs& a, int64_t row
     else row_gradient<ZHALF, false>(a, row, g, begin, end);
 }
 
-// What the caller gives for a row, and the gradient's constants made of it.
+// What the caller gives for a row, and the gradient's constants made of it: ln S and 1 / S are those of this d.
 struct RowGiven {
     int64_t token;
     float a, b;
@@ -378,20 +417,21 @@ struct RowGiven {
         : token(x.tokens != nullptr ? x.tokens[row] : -1), a(x.dlogprob != nullptr ? x.dlogprob[row] : 0.0f),
           b(x.dentropy != nullptr ? x.dentropy[row] : 0.0f) {}
 };
-__device__ __forceinline__ RowGrad row_grad(const TokenLogprobs& a, const RowGiven& given, float m, float ln_s, float h) {
+__device__ __forceinline__ RowGrad row_grad(const TokenLogprobs& x, const RowGiven& given, float m, float ln, float inv, float h) {
     RowGrad g;
-    g.token = a.dlogprob != nullptr ? given.token : -1;
-    g.a = g.token >= 0 ? given.a * a.scale : 0.0f;
-    g.b = given.b * a.scale;
+    const float c = x.scale * kLog2e, b = given.b * x.scale;
+    g.token = x.dlogprob != nullptr ? given.token : -1;
+    g.a = g.token >= 0 ? given.a * x.scale : 0.0f;
     // a masked row's S is 0; a token that does not exist leaves nothing to say
-    g.zero = (g.a == 0.0f && g.b == 0.0f) || ln_s == -kInf;
-    if (g.token >= a.vocab) {
+    g.zero = (g.a == 0.0f && b == 0.0f) || ln == -kInf;
+    if (g.token >= x.vocab) {
         g.a = __uint_as_float(0x7fc00000u);
         g.zero = false;
     }
     g.m = m;
-    g.ln2s = ln_s * kLog2e;
-    g.h = g.b != 0.0f ? h : 0.0f;
+    g.mc = __fmul_rn(m, c);
+    g.A = -inv * (b != 0.0f ? fmaf(b, h - ln, g.a) : g.a);
+    g.B = -inv * b * kLn2;
     return g;
 }
 
@@ -523,31 +563,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks) token_logprobs_kernel(const
                     else if (i == 0 || i == r.count - 1) v[k] = r.masked(v[k], i);
                 }
             }
-            const float top = largest<BF16, kWords>(v);
-            if (top > s.m) rescale(s, top, c);
+            take_words<BF16, ENTROPY, kWords>(s, v, c);
             copy_ahead(place);   // the words are in registers
             place = place + 1 == kPlaces ? 0 : place + 1;
-            const float ref = s.m == -kInf ? 0.0f : s.m;
-            f32x2 S2 = pair(s.S, 0.0f), Q2 = pair(s.Q, 0.0f);
-            if (fabsf(s.m) < 0x1p99f && c < 0x1p20f) {
-#pragma unroll
-                for (int k = 0; k < kWords; ++k) add_word<BF16, ENTROPY>(s, S2, Q2, v[k], ref, c, true);
-            } else {
-#pragma unroll
-                for (int k = 0; k < kWords; ++k) add_word<BF16, ENTROPY>(s, S2, Q2, v[k], ref, c, false);
-            }
-            float x, y;
-            unpair(S2, x, y);
-            s.S = x + y;
-            unpair(Q2, x, y);
-            s.Q = x + y;
         }
         const uint32_t mine = first + t < end ? order(s.m) : 0;
         if (a.top > 0) top_lists(mine, tops);
         s = join_all<kThreads / 32>(s, c, softs, joined, rank, cluster);
         const bool bad = !(s.S == s.S);
-        const float ln_s = logf(s.S);
-        const float h = s.S == 0.0f ? 0.0f : fmaf(-kLn2, s.Q / s.S, ln_s);
+        const float ln = logf(s.S), ln_s = ln + anchor_error(s.m, __fmul_rn(s.m, c), c);
+        const float h = s.S == 0.0f ? 0.0f : fmaf(-kLn2, s.Q / s.S, ln);
         if (t == 0 && rank == 0) row_results<ENTROPY>(a, row, s, ln_s, h, token, z_token);
         if (a.top > 0) {
             if (!bad) top_keys<BF16>(r, first, end, a.top, mine, tops);
@@ -573,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) token_logprobs_kernel(const
         if constexpr (GRAD) {
             const int chunks = grad_chunks(a, row);
             const Share part(chunks, rank, cluster);
-            row_gradient<BF16>(a, row, row_grad(a, RowGiven(a, row), s.m, ln_s, h), part.first, part.end);
+            row_gradient<BF16>(a, row, row_grad(a, RowGiven(a, row), s.m, ln, 1.0f / s.S, h), part.first, part.end);
         }
     }
 }
@@ -625,62 +650,52 @@ __global__ void __launch_bounds__(T, 1024 / T) token_loss_kernel(const __grid_co
                     else if (i == 0 || i == r.count - 1) v[k] = r.masked(v[k], i);
                 }
             }
-            const float top = largest<BF16, G>(v);
-            if (top > s.m) rescale(s, top, c);
-            const float ref = s.m == -kInf ? 0.0f : s.m;
-            f32x2 S2 = pair(s.S, 0.0f), Q2 = pair(s.Q, 0.0f);
-            if (fabsf(s.m) < 0x1p99f && c < 0x1p20f) {
-#pragma unroll
-                for (int k = 0; k < G; ++k) add_word<BF16, ENTROPY>(s, S2, Q2, v[k], ref, c, true);
-            } else {
-#pragma unroll
-                for (int k = 0; k < G; ++k) add_word<BF16, ENTROPY>(s, S2, Q2, v[k], ref, c, false);
-            }
-            float x, y;
-            unpair(S2, x, y);
-            s.S = x + y;
-            unpair(Q2, x, y);
-            s.Q = x + y;
+            take_words<BF16, ENTROPY, G>(s, v, c);
         }
         s = join_all<T / 32>(s, c, softs[flip], joined[flip], rank, cluster);
         flip ^= 1;
-        const float ln_s = logf(s.S);
-        const float h = s.S == 0.0f ? 0.0f : fmaf(-kLn2, s.Q / s.S, ln_s);
+        const float ln = logf(s.S), ln_s = ln + anchor_error(s.m, __fmul_rn(s.m, c), c);
+        const float h = s.S == 0.0f ? 0.0f : fmaf(-kLn2, s.Q / s.S, ln);
         if (t == 0 && rank == 0) row_results<ENTROPY>(a, row, s, ln_s, h, given.token, z_token);
-        const RowGrad g = row_grad(a, given, s.m, ln_s, h);
-        const int hit = g.token >= 0 && g.token < a.vocab ? (static_cast<int>(g.token) + r.lead) / E : -1;   // the token's word
+        const RowGrad g = row_grad(a, given, s.m, ln, 1.0f / s.S, h);
+        const int hit = !g.zero && g.token >= 0 && g.token < a.vocab ? (static_cast<int>(g.token) + r.lead) / E : -1;   // the token's word
         uint4* out = reinterpret_cast<uint4*>((reinterpret_cast<uintptr_t>(a.dz.p) + static_cast<uintptr_t>(row * a.dz.ld) * (16 / E)) & ~uintptr_t(15));
         const bool more = row + stride < a.rows;
         const RowWords<BF16> next(a.z, more ? row + stride : row, a.vocab);
         const Share ahead(next.count, rank, cluster);
-        for (int k = 0; k < slots; ++k) {
-            const int w = share.first + t + k * T;
-            if (w < share.end) {
-                float v[8];
-                RowWords<BF16>::floats(held[k * T + t], v);
-                if (g.zero) {
-#pragma unroll
-                    for (int j = 0; j < E; ++j) v[j] = 0.0f;
-                } else {
-                    logit_grads<E>(v, c, g);
+        const uint4* from = next.words + ahead.first + t;
+        const int left = more ? ahead.end - ahead.first - t : 0;   // of the next row's words, from this thread's first
+        const auto second_pass = [&](auto grads) {
+#pragma unroll 2
+            for (int k = 0; k < slots; ++k) {
+                const int w = share.first + t + k * T;
+                if (w < share.end) {
+                    float v[8];
+                    RowWords<BF16>::floats(held[k * T + t], v);
+                    grads(v);
                     if (w == hit) {
 #pragma unroll
                         for (int j = 0; j < E; ++j)
                             if (r.column(w, j) == static_cast<int>(g.token)) v[j] += g.a;
                     }
-                }
-                if (w > 0 && w < r.count - 1) {
-                    out[w] = BF16 ? make_uint4(to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]), to_bf16x2(v[E - 4], v[E - 3]), to_bf16x2(v[E - 2], v[E - 1]))
-                                  : make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-                } else {   // a row's ends
+                    if (static_cast<unsigned>(w - 1) < static_cast<unsigned>(r.count - 2)) {
+                        out[w] = BF16 ? make_uint4(to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]), to_bf16x2(v[E - 4], v[E - 3]), to_bf16x2(v[E - 2], v[E - 1]))
+                                      : make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+                    } else {   // a row's ends
 #pragma unroll
-                    for (int j = 0; j < E; ++j)
-                        if (r.inside(r.column(w, j))) store1(a.dz.p, a.dz.dtype, row * a.dz.ld + r.column(w, j), v[j]);
+                        for (int j = 0; j < E; ++j)
+                            if (r.inside(r.column(w, j))) store1(a.dz.p, a.dz.dtype, row * a.dz.ld + r.column(w, j), v[j]);
+                    }
                 }
+                if (k * T < left) copy16(mine + k * T * 16, from + k * T);
             }
-            const int i = ahead.first + t + k * T;
-            if (more && i < ahead.end) copy16(mine + k * T * 16, next.words + i);
-        }
+        };
+        if (!g.zero && plain(g.mc)) second_pass([&](float* v) { logit_grads<E, ENTROPY, true>(v, c, g); });
+        else second_pass([&](float* v) {
+            logit_grads<E, true, false>(v, c, g);
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] = g.zero ? 0.0f : v[j];
+        });
         copies_end();
     }
 }
@@ -693,7 +708,8 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_backward_kernel(const
     const int part = blockIdx.x % parts;
     for (int64_t row = blockIdx.x / parts; row < a.rows; row += gridDim.x / parts) {
         const float m = a.stats[2 * row], ln_s = a.stats[2 * row + 1];
-        const RowGrad g = row_grad(a, RowGiven(a, row), m, ln_s, a.entropy != nullptr ? a.entropy[row] : 0.0f);
+        const float c = a.scale * kLog2e, ln = ln_s - anchor_error(m, __fmul_rn(m, c), c);
+        const RowGrad g = row_grad(a, RowGiven(a, row), m, ln, expf(-ln), a.entropy != nullptr ? a.entropy[row] : 0.0f);
         if (threadIdx.x == 0 && part == 0 && g.token >= a.vocab) atomicOr(a.status, FSDP_KSTATUS_BAD_TOKEN);
         const int chunks = grad_chunks(a, row);
         row_gradient<BF16>(a, row, g, static_cast<int>(static_cast<int64_t>(chunks) * part / parts),
