@@ -1,6 +1,7 @@
 // AdamW over many tensors in one launch, with moments in 32 or 8 bits, and 8-bit moments
 // from and to floats.
 #include <algorithm>
+#include <cmath>
 
 #include "adamw.hpp"
 #include "block_device.cuh"
@@ -85,7 +86,10 @@ __device__ __forceinline__ uint32_t top_bytes(const uint32_t* t) {
     return __byte_perm(__byte_perm(t[0], t[1], 0x0073), __byte_perm(t[2], t[3], 0x0073), 0x5410);
 }
 
-// `random`: what is added below each code, 20 bits.
+// What is added below a code, of its 32 random bits: 16 of 20.
+template <bool SIGNED>
+__device__ __forceinline__ uint32_t below(uint32_t r) { return (SIGNED ? r << 4 : r >> 12) & 0xffff0u; }
+
 template <bool SIGNED>
 __device__ __forceinline__ uint2 state8_codes(const float* x, uint32_t byte, const uint32_t* random) {
     uint32_t w[2] = {0, 0};
@@ -103,11 +107,11 @@ __device__ __forceinline__ uint2 state8_codes(const float* x, uint32_t byte, con
                 float a, b;
                 unpair(mul2(pair(x[i], x[i + 1]), by2), a, b);
                 if (SIGNED) {
-                    t[j] = ((__float_as_uint(a) & 0x7fffffffu) + random[i]) << 4;
-                    t[j + 1] = ((__float_as_uint(b) & 0x7fffffffu) + random[i + 1]) << 4;
+                    t[j] = ((__float_as_uint(a) & 0x7fffffffu) + below<SIGNED>(random[i])) << 4;
+                    t[j + 1] = ((__float_as_uint(b) & 0x7fffffffu) + below<SIGNED>(random[i + 1])) << 4;
                 } else {   // an element that is not 0 is at least the first code
-                    t[j] = max(__float_as_uint(a) + random[i], x[i] > 0.0f ? 0x100000u : 0u) << 4;
-                    t[j + 1] = max(__float_as_uint(b) + random[i + 1], x[i + 1] > 0.0f ? 0x100000u : 0u) << 4;
+                    t[j] = max(__float_as_uint(a) + below<SIGNED>(random[i]), x[i] > 0.0f ? 0x100000u : 0u) << 4;
+                    t[j + 1] = max(__float_as_uint(b) + below<SIGNED>(random[i + 1]), x[i + 1] > 0.0f ? 0x100000u : 0u) << 4;
                 }
             }
             w[q] = top_bytes(t);
@@ -120,7 +124,7 @@ __device__ __forceinline__ uint2 state8_codes(const float* x, uint32_t byte, con
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j >> 2] |= state8_code<SIGNED>(x[j], byte, random[j]) << (8 * (j & 3));
+        for (int j = 0; j < 8; ++j) w[j >> 2] |= state8_code<SIGNED>(x[j], byte, below<SIGNED>(random[j])) << (8 * (j & 3));
     }
     return make_uint2(w[0], w[1]);
 }
@@ -173,23 +177,29 @@ struct Tensor {
     uint32_t key;
     uint32_t first;      // tile
     int grad_dtype;
-    int moments8;
     int vector;
 };
 
-constexpr int kTile = 4096;      // elements of a tile
-constexpr int kTensors = 256;    // of one launch, in the kernel's parameters
+// Elements of a tile, which a block takes at a time: few for little work, so that it spreads (its latency
+// is that of a thread's passes over the tile), many for a lot, so that finding a tile's tensor counts little.
+constexpr int kLeastTile = 256, kMostTile32 = 2048, kMostTile8 = 16384;
+constexpr int kFew = 16, kTensors = 256;   // tensors of one launch, in the kernel's parameters
 
+template <int MOST>
 struct Tensors {
     AdamWConsts c;               // decay and step: the tensor's
     const float* grad_scale;
     const int32_t* skip;
     uint32_t count, tiles;
-    Tensor t[kTensors];
+    int tile;                    // elements of one
+    Tensor t[MOST];
 };
 
-__device__ __forceinline__ uint32_t random_bits(int64_t i, uint32_t key) {
-    uint32_t x = static_cast<uint32_t>(i) ^ (key ^ static_cast<uint32_t>(i >> 32) * 0x85157AF5u);
+// i's part of what is hashed; of i + j, j < 8 with i a multiple of 8, it is that ^ j.
+__device__ __forceinline__ uint32_t random_input(int64_t i, uint32_t key) {
+    return static_cast<uint32_t>(i) ^ key ^ static_cast<uint32_t>(i >> 32) * 0x85157AF5u;
+}
+__device__ __forceinline__ uint32_t random_bits(uint32_t x) {
     x ^= x >> 16;
     x *= 0xD36F86A9u;
     x ^= x >> 15;
@@ -220,7 +230,8 @@ __device__ __forceinline__ void adamw_pair(float* p, const float* g, float* m, f
 }
 
 // The last tensor whose first tile is at or before `tile`.
-__device__ __forceinline__ uint32_t tensor_of(const Tensors& a, uint32_t tile) {
+template <int MOST>
+__device__ __forceinline__ uint32_t tensor_of(const Tensors<MOST>& a, uint32_t tile) {
     uint32_t lo = 0, hi = a.count;
     while (hi - lo > 1) {
         const uint32_t mid = (lo + hi) / 2;
@@ -280,11 +291,16 @@ __device__ __forceinline__ void step8(const Tensor& t, const AdamWConsts& c, boo
 #pragma unroll
     for (int j = 0; j < 8; j += 2) adamw_pair(p + j, g + j, m + j, v + j, c);
     if (EIGHT) {
+        if (n < 8) {   // what is not the tensor's stays out of the groups' largest
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j >= n) m[j] = v[j] = 0.0f;
+        }
         float mt = 0.0f, vt = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            mt = j < n ? larger(mt, m[j]) : mt;
-            vt = j < n ? larger(vt, v[j]) : vt;
+            mt = larger(mt, m[j]);
+            vt = larger(vt, v[j]);
         }
         uint32_t mb = __float_as_uint(mt), vb = __float_as_uint(vt);
 #pragma unroll
@@ -294,15 +310,12 @@ __device__ __forceinline__ void step8(const Tensor& t, const AdamWConsts& c, boo
         }
         mb = state8_byte(mb);
         vb = state8_byte(vb);
-        uint32_t rm[8], rv[8];
+        const uint32_t input = random_input(i, t.key);
+        uint32_t r[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t r = random_bits(i + j, t.key);
-            rm[j] = r << 4 & 0xffff0u;
-            rv[j] = r >> 12 & 0xffff0u;
-        }
-        cm = state8_codes<true>(m, mb, rm);
-        cv = state8_codes<false>(v, vb, rv);
+        for (int j = 0; j < 8; ++j) r[j] = random_bits(input ^ j);
+        cm = state8_codes<true>(m, mb, r);
+        cv = state8_codes<false>(v, vb, r);
         if (n > 0 && (i & 31) == 0) {
             t.me[i >> 5] = static_cast<uint8_t>(mb);
             t.ve[i >> 5] = static_cast<uint8_t>(vb);
@@ -336,11 +349,12 @@ __device__ __forceinline__ void step8(const Tensor& t, const AdamWConsts& c, boo
 }
 
 // The same for tensors that begin anywhere: a group of 32 to a warp, an element to a lane.
+template <bool EIGHT>
 __device__ __forceinline__ void step1(const Tensor& t, const AdamWConsts& c, bool scaled, float scale, int64_t i, bool on) {
     float p = on ? t.p[i] : 0.0f, g = on ? load1(t.g, t.grad_dtype, i) : 0.0f, m = 0.0f, v = 0.0f;
     if (scaled) g = __fmul_rn(g, scale);
     if (on) {
-        if (t.moments8) {
+        if (EIGHT) {
             m = state8_value<true>(static_cast<uint8_t*>(t.m)[i], state8_unit(t.me[i >> 5]));
             v = state8_value<false>(static_cast<uint8_t*>(t.v)[i], state8_unit(t.ve[i >> 5]));
         } else {
@@ -353,13 +367,13 @@ __device__ __forceinline__ void step1(const Tensor& t, const AdamWConsts& c, boo
         t.p[i] = p;
         if (t.copy != nullptr) store1(t.copy, FSDP_DTYPE_BF16, i, p);
     }
-    if (t.moments8) {
-        const uint32_t r = random_bits(i, t.key);
+    if (EIGHT) {
+        const uint32_t r = random_bits(random_input(i, t.key));
         const uint32_t mb = state8_byte(__reduce_max_sync(kAll, on ? __float_as_uint(larger(0.0f, m)) : 0u));
         const uint32_t vb = state8_byte(__reduce_max_sync(kAll, on ? __float_as_uint(larger(0.0f, v)) : 0u));
         if (on) {
-            static_cast<uint8_t*>(t.m)[i] = static_cast<uint8_t>(state8_code<true>(m, mb, (r & 0xffffu) << 4));
-            static_cast<uint8_t*>(t.v)[i] = static_cast<uint8_t>(state8_code<false>(v, vb, (r >> 16) << 4));
+            static_cast<uint8_t*>(t.m)[i] = static_cast<uint8_t>(state8_code<true>(m, mb, below<true>(r)));
+            static_cast<uint8_t*>(t.v)[i] = static_cast<uint8_t>(state8_code<false>(v, vb, below<false>(r)));
         }
         if ((i & 31) == 0) {
             t.me[i >> 5] = static_cast<uint8_t>(mb);
@@ -371,7 +385,9 @@ __device__ __forceinline__ void step1(const Tensor& t, const AdamWConsts& c, boo
     }
 }
 
-__global__ void __launch_bounds__(256, 4) adamw_tensors_kernel(const __grid_constant__ Tensors a) {
+// EIGHT: moments in 8 bits.
+template <bool EIGHT, int MOST>
+__global__ void __launch_bounds__(256, 4) adamw_tensors_kernel(const __grid_constant__ Tensors<MOST> a) {
     starts_early();
     after_previous();
     if (a.skip != nullptr && *a.skip != 0) return;
@@ -382,18 +398,17 @@ __global__ void __launch_bounds__(256, 4) adamw_tensors_kernel(const __grid_cons
         AdamWConsts c = a.c;
         c.decay = t.decay;
         c.step = t.step;
-        const int64_t begin = static_cast<int64_t>(tile - t.first) * kTile, end = min(begin + kTile, t.n);
+        const int64_t begin = static_cast<int64_t>(tile - t.first) * a.tile, end = min(begin + a.tile, t.n);
         if (t.vector) {   // whole warps: a group's threads take part together
             for (int64_t at = begin + (threadIdx.x & ~31) * 8; at < end; at += 256 * 8) {
                 const int64_t i = at + (threadIdx.x & 31) * 8;
                 const int n = inside8(i, end);
-                if (t.moments8) step8<true>(t, c, scaled, scale, i, n);
-                else step8<false>(t, c, scaled, scale, i, n);
+                step8<EIGHT>(t, c, scaled, scale, i, n);
             }
         } else {
             for (int64_t at = begin + (threadIdx.x & ~31); at < end; at += 256) {
                 const int64_t i = at + (threadIdx.x & 31);
-                step1(t, c, scaled, scale, i, i < end);
+                step1<EIGHT>(t, c, scaled, scale, i, i < end);
             }
         }
     }
@@ -424,33 +439,52 @@ cudaError_t launch_state8_unpack(int kind, const uint8_t* codes, const uint8_t* 
                         dim3(blocks_for(n, vector ? 2048 : 256, sms * 16)), 256, 0, st, codes, exps, n, out, out_dtype, vector);
 }
 
-cudaError_t launch_adamw_tensors(const fsdp_adamw_tensor* tensors, int64_t count, const fsdp_adamw_hp& hp, int64_t step,
-                                 uint64_t seed, const float* grad_scale, const int32_t* skip, int sms, cudaStream_t st) {
-    Tensors a;
+namespace {
+
+template <int MOST>
+cudaError_t launch_tensors(const fsdp_adamw_tensor* tensors, int64_t count, const fsdp_adamw_hp& hp, int64_t step, uint64_t seed,
+                           const float* grad_scale, const int32_t* skip, int sms, cudaStream_t st) {
+    Tensors<MOST> a;
     a.c = adamw_consts(&hp, step);
+    const double bc1 = 1.0 - std::pow(hp.beta1, static_cast<double>(step));
     a.grad_scale = grad_scale;
     a.skip = skip;
-    for (int64_t j = 0; j < count;) {
-        a.count = a.tiles = 0;
-        for (; j < count && a.count < kTensors; ++j) {
-            const fsdp_adamw_tensor& s = tensors[j];
-            if (s.numel == 0) continue;
-            const int64_t tiles = (s.numel + kTile - 1) / kTile;
-            if (a.tiles + tiles > 0x7fffffff) break;   // a tensor has at most 2^29 tiles
-            fsdp_adamw_hp own = hp;
-            own.lr *= s.lr_scale;
-            own.weight_decay *= s.decay_scale;
-            const AdamWConsts c = adamw_consts(&own, step);
-            const uint64_t key = seed * 0x9E3779B97F4A7C15ull + (static_cast<uint64_t>(j) + 1) * 0xD1B54A32D192ED03ull;
-            a.t[a.count++] = Tensor{s.param, s.grad, s.exp_avg, s.exp_avg_sq, s.exp_avg_exps, s.exp_avg_sq_exps, s.copy_bf16, s.numel,
-                                    c.decay, c.step, static_cast<uint32_t>(key >> 32), a.tiles, s.grad_dtype, s.moments == FSDP_MOMENTS_8BIT, vector_accesses(s)};
-            a.tiles += static_cast<uint32_t>(tiles);
+    for (const int moments : {FSDP_MOMENTS_F32, FSDP_MOMENTS_8BIT}) {   // a kernel for each kind
+        const bool eight = moments == FSDP_MOMENTS_8BIT;
+        int64_t total = 0;
+        for (int64_t j = 0; j < count; ++j) total += tensors[j].moments == moments ? tensors[j].numel : 0;
+        a.tile = static_cast<int>(std::min<int64_t>(eight ? kMostTile8 : kMostTile32,
+                                                    std::max<int64_t>(1, total / (static_cast<int64_t>(sms) * 8 * kLeastTile)) * kLeastTile));
+        for (int64_t j = 0; j < count;) {
+            a.count = a.tiles = 0;
+            for (; j < count && a.count < MOST; ++j) {
+                const fsdp_adamw_tensor& s = tensors[j];
+                if (s.numel == 0 || s.moments != moments) continue;
+                const int64_t tiles = (s.numel + a.tile - 1) / a.tile;
+                if (a.tiles + tiles > 0x7fffffff) break;   // 2^40 elements are at most 2^29 tiles of the largest size
+                const double lr = hp.lr * s.lr_scale;      // decay and step as adamw_consts forms them
+                const float decay = static_cast<float>(1.0 - lr * (hp.weight_decay * s.decay_scale)), size = static_cast<float>(lr / bc1);
+                const uint64_t key = seed * 0x9E3779B97F4A7C15ull + (static_cast<uint64_t>(j) + 1) * 0xD1B54A32D192ED03ull;
+                a.t[a.count++] = Tensor{s.param, s.grad, s.exp_avg, s.exp_avg_sq, s.exp_avg_exps, s.exp_avg_sq_exps, s.copy_bf16, s.numel,
+                                        decay, size, static_cast<uint32_t>(key >> 32), a.tiles, s.grad_dtype, vector_accesses(s)};
+                a.tiles += static_cast<uint32_t>(tiles);
+            }
+            if (a.count == 0) continue;
+            const cudaError_t e = launch_early(eight ? adamw_tensors_kernel<true, MOST> : adamw_tensors_kernel<false, MOST>,
+                                               dim3(std::min<uint32_t>(a.tiles, static_cast<uint32_t>(sms) * 8)), 256, 0, st, a);
+            if (e != cudaSuccess) return e;
         }
-        if (a.count == 0) continue;
-        const cudaError_t e = launch_early(adamw_tensors_kernel, dim3(std::min<uint32_t>(a.tiles, static_cast<uint32_t>(sms) * 8)), 256, 0, st, a);
-        if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_adamw_tensors(const fsdp_adamw_tensor* tensors, int64_t count, const fsdp_adamw_hp& hp, int64_t step,
+                                 uint64_t seed, const float* grad_scale, const int32_t* skip, int sms, cudaStream_t st) {
+    // a few tensors: kilobytes of parameters instead of tens of them for a launch to carry
+    return count <= kFew ? launch_tensors<kFew>(tensors, count, hp, step, seed, grad_scale, skip, sms, st)
+                         : launch_tensors<kTensors>(tensors, count, hp, step, seed, grad_scale, skip, sms, st);
 }
 
 }  // namespace fsdp

@@ -117,11 +117,18 @@ __device__ __forceinline__ void rescale(Soft& s, float to, float c) {
     s.m = to;
 }
 
-__device__ __forceinline__ Soft join(Soft a, Soft b, float c) {
-    const float m = fmaxf(a.m, b.m);
-    rescale(a, m, c);
-    rescale(b, m, c);
-    return Soft{m, a.S + b.S, a.Q + b.Q};
+// Joined over a warp's lanes, for each of them: all brought to the largest maximum, then added.
+__device__ __forceinline__ Soft join_lanes(Soft s, float c) {
+    float m = s.m;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, d));
+    rescale(s, m, c);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        s.S += __shfl_xor_sync(kAll, s.S, d);
+        s.Q += __shfl_xor_sync(kAll, s.Q, d);
+    }
+    return s;
 }
 
 // What mc is off by, in natural logarithms.
@@ -437,25 +444,27 @@ __device__ __forceinline__ RowGrad row_grad(const TokenLogprobs& x, const RowGiv
 
 // ---- kernels ----
 
-// A block's share of a row's words: all of them, or a run of them in a cluster of blocks.
+// A block's share of a row's words: all of them, or a run of them in a cluster of blocks, of
+// which there are a power of two (a division here, for every thread and row, took a tenth of
+// the forward pass's instructions and a fifth of the loss's).
 struct Share {
     int first, end;
-    __device__ Share(int count, int rank, int cluster)
-        : first(static_cast<int>(static_cast<int64_t>(count) * rank / cluster)),
-          end(static_cast<int>(static_cast<int64_t>(count) * (rank + 1) / cluster)) {}
+    __device__ Share(int count, int rank, int cluster) {
+        const int shift = 31 - __clz(cluster);
+        first = static_cast<int>((static_cast<int64_t>(count) * rank) >> shift);
+        end = static_cast<int>((static_cast<int64_t>(count) * (rank + 1)) >> shift);
+    }
 };
 
 // The threads' sums joined over a block's WARPS warps, and over the cluster: for every thread.
 template <int WARPS>
 __device__ __forceinline__ Soft join_all(Soft s, float c, Soft* softs, Soft* joined, int rank, int cluster) {
-    const int t = threadIdx.x;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1)
-        s = join(s, Soft{__shfl_xor_sync(kAll, s.m, d), __shfl_xor_sync(kAll, s.S, d), __shfl_xor_sync(kAll, s.Q, d)}, c);
-    if ((t & 31) == 0) softs[t >> 5] = s;
+    const int t = threadIdx.x, lane = t & 31;
+    const Soft none{-kInf, 0.0f, 0.0f};
+    s = join_lanes(s, c);
+    if (lane == 0) softs[t >> 5] = s;
     __syncthreads();
-    s = softs[0];
-    for (int i = 1; i < WARPS; ++i) s = join(s, softs[i], c);
+    s = join_lanes(lane < WARPS ? softs[lane] : none, c);
     if (cluster > 1) {
         if (t < cluster) {
             const uint32_t to = remote_addr(shared_at(&joined[rank]), t);
@@ -464,8 +473,7 @@ __device__ __forceinline__ Soft join_all(Soft s, float c, Soft* softs, Soft* joi
             asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 8), "f"(s.Q) : "memory");
         }
         cluster_meet();
-        s = joined[0];
-        for (int i = 1; i < cluster; ++i) s = join(s, joined[i], c);
+        s = join_lanes(lane < cluster ? joined[lane] : none, c);
     }
     return s;
 }

@@ -345,10 +345,16 @@ __global__ void __launch_bounds__(kMostThreads) residual_norm_backward_kernel(co
 // a chunk is then the two 16-byte words that hold it, moved together when it is read.
 
 constexpr int kMostPlaces = 4;      // rows of a group in the ring
-constexpr int kRingThreads = 512;
+// Threads of a block by the chunks of one.  The backward pass holds a row's words and its columns' sums:
+// 128 registers, or 168 for two chunks (with the 96 and 128 that more threads leave, what is
+// spilled goes to L2, for the ring takes L1's room: 4096 x 1280 27 us against 23).
+constexpr int forward_threads(int nv) { return nv == 1 ? 768 : 512; }
+constexpr int backward_threads(int nv) { return nv == 1 ? 512 : 384; }
+constexpr int keep_threads = 512;
+constexpr int kRingWarps = 24;
 
 struct RingShape {
-    int gt, groups, places, cluster;
+    int gt, groups, places, cluster;   // clusters have two chunks to a thread
     int chunks;                     // of a block's share of a row, but for the last one's
 };
 
@@ -360,7 +366,7 @@ struct Place {
     int64_t first;
     int last;                       // columns of the last chunk
     __device__ Place(const RingShape& s, int64_t cols) : gt(s.gt), groups(s.groups), g(threadIdx.x / s.gt), t(threadIdx.x % s.gt) {
-        first = static_cast<int64_t>(s.cluster > 1 ? cluster_rank() : 0) * s.chunks;
+        first = NV == 2 && s.cluster > 1 ? static_cast<int64_t>(cluster_rank()) * s.chunks : 0;
         last = t + (NV - 1) * gt < s.chunks ? inside8(column(NV - 1), cols) : 0;
     }
     __device__ int64_t column(int k) const { return (first + t + k * gt) * 8; }
@@ -422,6 +428,11 @@ __device__ __forceinline__ void pairs(uint4 w, f32x2* v) {
     v[1] = pair(bf16_lo(w.y), bf16_hi(w.y));
     v[2] = pair(bf16_lo(w.z), bf16_hi(w.z));
     v[3] = pair(bf16_lo(w.w), bf16_hi(w.w));
+}
+__device__ __forceinline__ void half_pairs(uint4 w, int h, f32x2* v) {
+    const uint32_t x = h ? w.z : w.x, y = h ? w.w : w.y;
+    v[0] = pair(bf16_lo(x), bf16_hi(x));
+    v[1] = pair(bf16_lo(y), bf16_hi(y));
 }
 __device__ __forceinline__ f32x2 twice(float v) { return pair(v, v); }
 
@@ -502,6 +513,19 @@ struct Vectors {
         }
         __syncthreads();
     }
+    // Half a chunk: of floats, a place of its own; of BF16, a half of `whole`.
+    __device__ uint4 whole(const Place<NV>& at, int v, int k) const {
+        return FLOATS ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(slot(at, v, k));
+    }
+    __device__ void half(const Place<NV>& at, int v, int k, int h, uint4 w, f32x2* x) const {
+        if (FLOATS) {
+            const float4 a = *reinterpret_cast<const float4*>(slot(at, v, k) + h * at.gt * 16);
+            x[0] = pair(a.x, a.y);
+            x[1] = pair(a.z, a.w);
+        } else {
+            half_pairs(w, h, x);
+        }
+    }
     __device__ void read(const Place<NV>& at, int v, int k, f32x2* x) const {
         const uint8_t* from = slot(at, v, k);
         if (FLOATS) {
@@ -539,13 +563,13 @@ __device__ __forceinline__ void group_sums(float (&v)[N], float4* red, int group
 }
 
 template <int NV, bool FLOATS, bool ANY>
-__global__ void __launch_bounds__(kRingThreads) residual_norm_ring_kernel(const __grid_constant__ ResidualNorm a, const RingShape shape) {
+__global__ void __launch_bounds__(forward_threads(NV)) residual_norm_ring_kernel(const __grid_constant__ ResidualNorm a, const RingShape shape) {
     extern __shared__ __align__(16) uint8_t ring_bytes[];
-    __shared__ float4 red[2][kRingThreads / 32];
+    __shared__ float4 red[2][kRingWarps];
     __shared__ float joined[2][8][4];
     starts_early();
     after_previous();
-    const int places = shape.places, cluster = shape.cluster;
+    const int places = shape.places, cluster = NV == 2 ? shape.cluster : 1;
     if (cluster > 1) cluster_sync();   // the others' shared memory is there
     const Place<NV> at(shape, a.cols);
     const Vectors<NV, FLOATS> vec{ring_bytes};
@@ -620,14 +644,14 @@ __global__ void __launch_bounds__(kRingThreads) residual_norm_ring_kernel(const 
 }
 
 template <int NV, bool FLOATS, bool ANY>
-__global__ void __launch_bounds__(kRingThreads) residual_norm_backward_ring_kernel(const __grid_constant__ ResidualNormGrad a,
+__global__ void __launch_bounds__(backward_threads(NV)) residual_norm_backward_ring_kernel(const __grid_constant__ ResidualNormGrad a,
                                                                                    const RingShape shape) {
     extern __shared__ __align__(16) uint8_t ring_bytes[];
-    __shared__ float4 red[2][kRingThreads / 32];
+    __shared__ float4 red[2][kRingWarps];
     __shared__ float joined[2][8][4];
     starts_early();
     after_previous();
-    const int places = shape.places, cluster = shape.cluster;
+    const int places = shape.places, cluster = NV == 2 ? shape.cluster : 1;
     if (cluster > 1) cluster_sync();   // the others' shared memory is there
     const Place<NV> at(shape, a.cols);
     const Vectors<NV, FLOATS> vec{ring_bytes};
@@ -668,18 +692,23 @@ __global__ void __launch_bounds__(kRingThreads) residual_norm_backward_ring_kern
         // the row's words stay in registers, and their places take the rows ahead at once
         uint4 raw[NV][4];
         f32x2 s1 = 0, s2 = 0, s3 = 0;
-        const auto expand = [&](const uint4* w, int k, f32x2* xh, f32x2* tt, f32x2* u, f32x2* gr, f32x2* dy) {
-            pairs(w[0], dy);
-            pairs(w[1], tt);
-            pairs(w[2], xh);
-            pairs(w[3], u);
-            vec.read(at, 2, k, gr);
+        // half a chunk at a time: what is expanded takes fewer registers
+        const auto expand = [&](const uint4* w, const uint4* vw, int k, int h, f32x2* xh, f32x2* tt, f32x2* u, f32x2* gr, f32x2* dy, f32x2* kk) {
+            half_pairs(w[0], h, dy);
+            half_pairs(w[1], h, tt);
+            half_pairs(w[2], h, xh);
+            half_pairs(w[3], h, u);
+            f32x2 g2[2];
+            vec.half(at, 0, k, h, vw[0], kk);
+            vec.half(at, 1, k, h, vw[1], g2);
+            vec.half(at, 2, k, h, vw[2], gr);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 2; ++j) {
                 xh[j] = mul2(xh[j], rstd);
                 gr[j] = mul2(dy[j], gr[j]);
                 tt[j] = fma2(rstd, gr[j], tt[j]);
                 u[j] = mul2(u[j], post_rstd);
+                kk[j] = mul2(kk[j], g2[j]);
             }
         };
 #pragma unroll
@@ -688,17 +717,19 @@ __global__ void __launch_bounds__(kRingThreads) residual_norm_backward_ring_kern
             raw[k][1] = ring.read(at, a.dout, row, place, 1, k);
             raw[k][2] = ring.read(at, a.out, row, place, 2, k);
             raw[k][3] = ring.read(at, a.o, row, place, 3, k);
-            f32x2 xh[4], tt[4], u[4], gr[4], dy[4], p[4], w[4];
-            expand(raw[k], k, xh, tt, u, gr, dy);
-            vec.read(at, 0, k, p);
-            vec.read(at, 1, k, w);
+            const uint4 vw[3] = {vec.whole(at, 0, k), vec.whole(at, 1, k), vec.whole(at, 2, k)};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                dg[k][j] = fma2(dy[j], xh[j], dg[k][j]);
-                s1 = fma2(gr[j], xh[j], s1);
-                const f32x2 ku = mul2(mul2(p[j], w[j]), u[j]);
-                s2 = fma2(ku, tt[j], s2);
-                s3 = fma2(ku, xh[j], s3);
+            for (int h = 0; h < 2; ++h) {
+                f32x2 xh[2], tt[2], u[2], gr[2], dy[2], kk[2];
+                expand(raw[k], vw, k, h, xh, tt, u, gr, dy, kk);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    dg[k][2 * h + j] = fma2(dy[j], xh[j], dg[k][2 * h + j]);
+                    s1 = fma2(gr[j], xh[j], s1);
+                    const f32x2 ku = mul2(kk[j], u[j]);
+                    s2 = fma2(ku, tt[j], s2);
+                    s3 = fma2(ku, xh[j], s3);
+                }
             }
         }
         issue(row + places * stride, place);
@@ -711,19 +742,22 @@ __global__ void __launch_bounds__(kRingThreads) residual_norm_backward_ring_kern
         const f32x2 less1 = twice(-r1 * c1), less2 = twice(-c2), alpha = twice(a.alpha);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            f32x2 xh[4], tt[4], u[4], gr[4], dy[4], p[4], w[4];
-            expand(raw[k], k, xh, tt, u, gr, dy);
-            vec.read(at, 0, k, p);
-            vec.read(at, 1, k, w);
+            const uint4 vw[3] = {vec.whole(at, 0, k), vec.whole(at, 1, k), vec.whole(at, 2, k)};
+            f32x2 dh[4], db[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                tt[j] = fma2(less1, xh[j], tt[j]);
-                du[k][j] = fma2(tt[j], u[j], du[k][j]);
-                u[j] = mul2(post_rstd, fma2(u[j], less2, mul2(tt[j], mul2(p[j], w[j]))));
-                tt[j] = mul2(tt[j], alpha);
+            for (int h = 0; h < 2; ++h) {
+                f32x2 xh[2], tt[2], u[2], gr[2], dy[2], kk[2];
+                expand(raw[k], vw, k, h, xh, tt, u, gr, dy, kk);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    tt[j] = fma2(less1, xh[j], tt[j]);
+                    du[k][2 * h + j] = fma2(tt[j], u[j], du[k][2 * h + j]);
+                    db[2 * h + j] = mul2(post_rstd, fma2(u[j], less2, mul2(tt[j], kk[j])));
+                    dh[2 * h + j] = mul2(tt[j], alpha);
+                }
             }
-            put<NV, ANY>(at, a.dh, row, k, tt);
-            put<NV, ANY>(at, a.dblock, row, k, u);
+            put<NV, ANY>(at, a.dh, row, k, dh);
+            put<NV, ANY>(at, a.dblock, row, k, db);
         }
     }
     // the groups' column sums meet in shared memory: element j of chunk i at j * slots + i
@@ -752,16 +786,15 @@ __global__ void __launch_bounds__(kRingThreads) residual_norm_backward_ring_kern
         }
 }
 
-// The same for rows of 8200 to 12288 columns on 16-byte boundaries, a row to a block: the vectors lie
+// The same for rows of 4104 to 12288 columns on 16-byte boundaries, a row to a block: the vectors lie
 // in registers, as BF16, and two whole rows in the ring, from which both passes over a
-// row read.  (With the vectors in shared memory there is room for one row; and a thread's three
-// chunks, with their columns' sums, leave no registers to hold a row in between, 187 us at 4096 x 12288.)
-constexpr int kKeepChunks = 3;
-template <bool GATE>
-__global__ void __launch_bounds__(kRingThreads) residual_norm_backward_keep_kernel(const __grid_constant__ ResidualNormGrad a, const RingShape shape) {
-    constexpr int NV = kKeepChunks;
+// row read.  (With the vectors in shared memory there is room for one row of 12288; and a thread's three
+// chunks, with their columns' sums, leave no registers to hold a row in between, 187 us at 4096 x 12288;
+// two blocks to a row, 222: their barrier waits for the slower one's copies.)
+template <int NV, bool GATE>
+__global__ void __launch_bounds__(keep_threads) residual_norm_backward_keep_kernel(const __grid_constant__ ResidualNormGrad a, const RingShape shape) {
     extern __shared__ __align__(16) uint8_t ring_bytes[];
-    __shared__ float4 red[2][kRingThreads / 32];
+    __shared__ float4 red[2][kRingWarps];
     starts_early();
     after_previous();
     const Place<NV> at(shape, a.cols);
@@ -810,11 +843,6 @@ __global__ void __launch_bounds__(kRingThreads) residual_norm_backward_keep_kern
         copies_wait(1);
         const f32x2 rstd = twice(r1), post_rstd = twice(r2);
         // half a chunk at a time, which keeps what is expanded in the registers that are left
-        const auto words = [](uint4 w, int half, f32x2* v) {
-            const uint32_t x = half ? w.z : w.x, y = half ? w.w : w.y;
-            v[0] = pair(bf16_lo(x), bf16_hi(x));
-            v[1] = pair(bf16_lo(y), bf16_hi(y));
-        };
         const auto read = [&](int k, uint4* raw) {
             raw[0] = ring.read(at, a.dy, row, place, 0, k);
             raw[1] = ring.read(at, a.dout, row, place, 1, k);
@@ -822,14 +850,14 @@ __global__ void __launch_bounds__(kRingThreads) residual_norm_backward_keep_kern
             raw[3] = ring.read(at, a.o, row, place, 3, k);
         };
         const auto expand = [&](const uint4* raw, int k, int half, f32x2* xh, f32x2* tt, f32x2* u, f32x2* gr, f32x2* dy, f32x2* kk) {
-            words(raw[0], half, dy);
-            words(raw[1], half, tt);
-            words(raw[2], half, xh);
-            words(raw[3], half, u);
-            words(gammas[k], half, gr);
-            words(posts[k], half, kk);
+            half_pairs(raw[0], half, dy);
+            half_pairs(raw[1], half, tt);
+            half_pairs(raw[2], half, xh);
+            half_pairs(raw[3], half, u);
+            half_pairs(gammas[k], half, gr);
+            half_pairs(posts[k], half, kk);
             f32x2 w[2];
-            if (GATE) words(gates[k], half, w);
+            if (GATE) half_pairs(gates[k], half, w);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 xh[j] = mul2(xh[j], rstd);
@@ -978,16 +1006,17 @@ bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool aligned_or_none(const Mat& m) { return m.p == nullptr || rows_aligned(m); }
 
 // How the ring takes `matrices` rows of BF16: chunks to a thread (0: it does not), threads, groups,
-// clusters and places, with `most` chunks to a thread at most.
-int ring_shape(int64_t rows, int64_t cols, int matrices, bool floats, bool any, int most, int least_places, RingShape* s, int* bytes) {
+// clusters and places.  threads: of a block, by its chunks to a thread; `most` of these at most.
+int ring_shape(int64_t rows, int64_t cols, int matrices, bool floats, bool any, int (*threads)(int), int most, int least_places,
+               RingShape* s, int* bytes) {
     const int64_t chunks = (cols + 7) / 8;
     for (s->cluster = 1; s->cluster <= 8; s->cluster *= 2) {
         const int64_t share = (chunks + s->cluster - 1) / s->cluster;
-        const int nv = static_cast<int>((share + kRingThreads - 1) / kRingThreads);
-        if (nv > most) continue;
+        const int nv = s->cluster > 1 ? 2 : share <= threads(1) ? 1 : static_cast<int>((share + threads(2) - 1) / threads(2));
+        if (nv > most || share > static_cast<int64_t>(nv) * threads(nv)) continue;
         s->chunks = static_cast<int>(share);
         s->gt = round32((share + nv - 1) / nv);
-        s->groups = s->cluster > 1 ? 1 : static_cast<int>(std::min<int64_t>(std::min(kRingThreads / s->gt, 15), rows));
+        s->groups = s->cluster > 1 ? 1 : static_cast<int>(std::min<int64_t>(std::min(threads(nv) / s->gt, 15), rows));
         const int keep = 3 * nv * s->gt * (floats ? 32 : 16), row = matrices * nv * s->gt * (any ? 32 : 16);
         while (s->groups > 1 && keep + least_places * s->groups * row > kSharedMost) --s->groups;
         s->places = std::min(kMostPlaces, (kSharedMost - keep) / (row * s->groups));
@@ -1012,7 +1041,7 @@ cudaError_t launch_residual_norm_forward(const ResidualNorm& a, int sms, cudaStr
     const bool floats = !aligned || a.param_dtype == FSDP_DTYPE_F32;
     RingShape shape;
     int bytes = 0;
-    const int nv = half ? ring_shape(a.rows, a.cols, 2, floats, !aligned, 3, 2, &shape, &bytes) : 0;
+    const int nv = half ? ring_shape(a.rows, a.cols, 2, floats, !aligned, forward_threads, 3, 2, &shape, &bytes) : 0;
     if (nv != 0 && a.rows * shape.cluster >= 2 * static_cast<int64_t>(sms) * shape.groups) {   // rows enough for every group to walk two
         const unsigned clusters = static_cast<unsigned>(std::min<int64_t>((a.rows + shape.groups - 1) / shape.groups, sms / shape.cluster));
         const int threads = shape.gt * shape.groups;
@@ -1045,18 +1074,22 @@ cudaError_t launch_residual_norm_backward(const ResidualNormGrad& a, int sms, cu
     if (a.rows > 0) {
         RingShape shape;
         int bytes = 0;
-        const int nv = half ? ring_shape(a.rows, a.cols, 4, floats, !aligned, 2, 1, &shape, &bytes) : 0;
+        const int nv = half ? ring_shape(a.rows, a.cols, 4, floats, !aligned, backward_threads, 2, 1, &shape, &bytes) : 0;
         const Spread s = spread(a.cols);
         const int64_t chunks = a.cols / 8;
-        if (half && !floats && chunks > 2 * kRingThreads && chunks <= kKeepChunks * kRingThreads) {
+        if (half && !floats && chunks > backward_threads(1) && chunks <= 3 * keep_threads) {
+            const int keep = chunks <= 2 * keep_threads ? 2 : 3;
             shape.cluster = shape.groups = 1;
             shape.places = 2;
             shape.chunks = static_cast<int>(chunks);
-            shape.gt = round32((chunks + kKeepChunks - 1) / kKeepChunks);
+            shape.gt = round32((chunks + keep - 1) / keep);
             count = std::min<int64_t>(a.rows, sms);
-            bytes = 2 * 4 * kKeepChunks * shape.gt * 16;
-            e = a.gate != nullptr ? launch_shared<residual_norm_backward_keep_kernel<true>>(static_cast<unsigned>(count), shape.gt, bytes, st, a, shape)
-                                  : launch_shared<residual_norm_backward_keep_kernel<false>>(static_cast<unsigned>(count), shape.gt, bytes, st, a, shape);
+            bytes = 2 * 4 * keep * shape.gt * 16;
+            const unsigned blocks = static_cast<unsigned>(count);
+#define KEEP(nv_, g) launch_shared<residual_norm_backward_keep_kernel<nv_, g>>(blocks, shape.gt, bytes, st, a, shape)
+            if (a.gate != nullptr) e = keep == 2 ? KEEP(2, true) : KEEP(3, true);
+            else e = keep == 2 ? KEEP(2, false) : KEEP(3, false);
+#undef KEEP
         } else if (nv != 0) {
             count = std::min<int64_t>((a.rows + shape.groups - 1) / shape.groups, sms / shape.cluster);
             const unsigned blocks = static_cast<unsigned>(count * shape.cluster);
