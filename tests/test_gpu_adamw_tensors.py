@@ -56,6 +56,19 @@ def encode(x, signed, bits=None):
     return np.where(e == 255, 0, code).astype(np.uint8), exps.astype(np.uint8)
 
 
+def same_codes(got, x, signed, bits, what):
+    """encode()'s codes; where value and random bits add up to a code exactly, that or the one below."""
+    got, (want, exps) = got.cpu().numpy(), encode(x, signed, bits)
+    e = np.repeat(exps.astype(np.int64), 32)[:len(x)]
+    y = np.ldexp(np.where(e == 255, 0.0, np.abs(np.nan_to_num(x, nan=0, posinf=0, neginf=0))).astype(np.float64), 127 - np.minimum(e, 253))
+    k = np.ldexp(y, 3 - np.maximum(np.where(y > 0, np.frexp(y)[1] - 1, -30), -14 if signed else -30)) + bits / 65536
+    tie = (k == np.rint(k)) & (y > 0)
+    low, up = got.astype(np.int64) & (127 if signed else 255), want.astype(np.int64) & (127 if signed else 255)
+    assert len(x) < 1000 or tie.mean() <= 0.01, what
+    ok = (got == want) | (tie & (low == up - 1))
+    assert ok.all(), f"{what}: {np.flatnonzero(~ok)[:5]} of {ok.size}"
+
+
 def random_bits(n, number, seed, first=0):
     key = ((seed * 0x9E3779B97F4A7C15 + (number + 1) * 0xD1B54A32D192ED03) % 2 ** 64) >> 32
     i = np.arange(first, first + n, dtype=np.uint64)
@@ -151,10 +164,9 @@ def test_step(c, moments, grad, off):
             else:
                 rm, rv = random_bits(n, j, seed)
                 for got, x, signed, r in ((ms[j], m1, True, rm), (vs[j], v1, False, rv)):
-                    codes, exps = encode(x, signed, r)
-                    same(got.exps, exps, f"exponents {j} {signed}")
-                    same(got.codes, codes, f"codes {j} {signed}")
-                m1, v1 = decode(*encode(m1, True, rm), True).astype(f), decode(*encode(v1, False, rv), False).astype(f)
+                    same(got.exps, encode(x, signed, r)[1], f"exponents {j} {signed}")
+                    same_codes(got.codes, x, signed, r, f"codes {j} {signed}")
+                m1, v1 = (decode(s.codes.cpu().numpy(), s.exps.cpu().numpy(), s.signed).astype(f) for s in (ms[j], vs[j]))
             want[j] = (p1, g0, m1, v1)
     for t, buf in bufs:
         _untouched(t, buf, off)
@@ -199,8 +211,8 @@ def test_more_tensors_than_one_launch_takes(c):
         p1, m1, v1 = adamw(p0[j], host(gs[j]), np.zeros(sizes[j], f), np.zeros(sizes[j], f), 1)
         same(ps[j], p1, j)
         rm, rv = random_bits(sizes[j], j, 9)
-        same(ms[j].codes, encode(m1, True, rm)[0], j)
-        same(vs[j].codes, encode(v1, False, rv)[0], j)
+        same_codes(ms[j].codes, m1, True, rm, j)
+        same_codes(vs[j].codes, v1, False, rv, j)
 
 
 def test_skipped_and_empty(c):
@@ -309,12 +321,12 @@ def test_elements_beyond_32_bits(c):
     p1, m1, v1 = adamw(np.zeros(tail, f), host(g[first:]), np.zeros(tail, f), np.zeros(tail, f), 3)
     same(p[first:], p1, "param")
     rm, rv = random_bits(tail, 0, 1, first)
-    same(m.codes[first:], encode(m1, True, rm)[0], "m")
-    same(v.codes[first:], encode(v1, False, rv)[0], "v")
+    same_codes(m.codes[first:], m1, True, rm, "m")
+    same_codes(v.codes[first:], v1, False, rv, "v")
     assert not bool(m.codes[:first].any()) and not bool(p[:first].any())
     out = torch.empty(n, dtype=BF, device="cuda")
     c.state8_unpack(m, out)
-    same(host(out[first:]), decode(*encode(m1, True, rm), True).astype(f), "values")
+    same(host(out[first:]), decode(m.codes[first:].cpu().numpy(), m.exps[first // 32:].cpu().numpy(), True).astype(f), "values")
 
 
 def test_captured_and_on_another_stream(c):
