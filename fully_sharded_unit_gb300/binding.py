@@ -992,10 +992,12 @@ class AdamWTensors:
         lr_scale, decay_scale = ([1.0] * n if s is None else s for s in (lr_scale, decay_scale))
         if any(len(v) != n for v in (grads, exp_avg, exp_avg_sq, copies, lr_scale, decay_scale)):
             _refuse("the lists of an AdamW step are of one length")
-        self.count, self.device = n, params[0].get_device() if n else None
+        self.count, self.device = n, params[0].get_device() if n and isinstance(params[0], torch.Tensor) else None
         self.array = (AdamWTensor * max(1, n))()
         self.kept = (list(params), list(grads), list(exp_avg), list(exp_avg_sq), list(copies))
         for e, p, g, m, v, c, ls, ds in zip(self.array, params, grads, exp_avg, exp_avg_sq, copies, lr_scale, decay_scale):
+            if not (isinstance(p, torch.Tensor) and isinstance(g, torch.Tensor)):
+                _refuse("parameters and gradients are tensors")
             shape = p.shape
             e.numel = p.numel()
             e.param = _array(p, shape, torch.float32, self.device)

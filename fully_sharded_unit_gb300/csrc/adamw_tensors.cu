@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(256) state8_pack_kernel(const float* x, int64_
     }
 }
 
+// 708 M elements to BF16: 343 us, 6.3 TB/s.
 template <bool SIGNED>
 __global__ void __launch_bounds__(256) state8_unpack_kernel(const uint8_t* codes, const uint8_t* exps, int64_t n, void* out, int dtype,
                                                             bool vector) {
@@ -433,7 +434,11 @@ __device__ __forceinline__ void step1(const Tensor& t, const AdamWConsts& c, boo
     }
 }
 
-// EIGHT: moments in 8 bits.
+// EIGHT: moments in 8 bits.  A block takes tiles in turn.  236 M elements, 32 bits, with BF16 copies: 1.16 ms,
+// 6.1 TB/s.  708 M, 8 bits, BF16 gradients and copies: 2.6 ms, 4.4 TB/s, bound by issue: about
+// 100 instructions an element, a third of them the two divisions and the root, rounded as IEEE has
+// them so that fp32 moments give the unit's bits.  (Four blocks an SM: with three or five, and
+// 80 or 48 registers, 2.7 ms and more.)
 template <bool EIGHT, int MOST>
 __global__ void __launch_bounds__(256, 4) adamw_tensors_kernel(const __grid_constant__ Tensors<MOST> a) {
     starts_early();

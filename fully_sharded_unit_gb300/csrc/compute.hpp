@@ -1,6 +1,7 @@
 // Launchers of the block operators (layer norm, linear layer, 8-bit activation
-// checkpoints).  Every launcher enqueues on `st` only and returns the launch
-// status; arguments are checked by the C entry points in compute.cu.
+// checkpoints) and of those at a step's ends (log probabilities, residual norm, AdamW over
+// tensors).  Every launcher enqueues on `st` only and returns the launch
+// status; arguments are checked by the C entry points in compute.cu and compute_step.cu.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -257,6 +257,43 @@ def test_alternatives_that_one_list_holds(c, dtype, each):
     _check_forward(c, z, torch.zeros(1, dtype=torch.int64, device="cuda"), 1.0, 32)
 
 
+@pytest.mark.parametrize("dtype,vocab", [(BF, 1200000), (F32, 700001)])
+def test_rows_that_no_cluster_holds(c, dtype, vocab):
+    z, t = _logits(2, vocab, dtype, seed=6, std=1.0)
+    a = torch.tensor([1.0, -2.0], device="cuda")
+    lp, st, h = _check_forward(c, z, t, 1.0, 3)
+    want, tol = _wanted_grad(z, t, 1.0, a, a)
+    dz = torch.empty_like(z)
+    c.token_logprobs_loss(z, t, lp, dz, dlogprob=a, dentropy=a)
+    inside(dz, want, tol + U[dtype] * np.abs(want), "loss")
+    c.token_logprobs_backward(z, t, st, dz, dlogprob=a, entropy=h, dentropy=a)
+    inside(dz, want, tol + U[dtype] * np.abs(want), "backward")
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-3, 3e5, 1e7, 1e25, 1e30])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_scales(c, dtype, scale):
+    """From nearly uniform to one-hot; logits of either sign and size.  d may be off by 2^-23 of itself; as x e^-x and
+    x^2 e^-x are below 0.4 and 0.6, that is below 2^-22 of scale (|a| + |b| (1 + H)), H up to 7.2."""
+    z, t = _logits(6, 1283, dtype, seed=9)
+    z[1] -= 300.0
+    z[2] += 300.0
+    z[3] *= 1e-20
+    t[:] = z.float().argmax(dim=1)
+    lp, st, h = torch.empty(6, device="cuda"), torch.empty((6, 2), device="cuda"), torch.empty(6, device="cuda")
+    c.token_logprobs_forward(z, t, lp, entropy=h, stats=st, scale=scale)
+    _check_rows(_reference(z, t, scale), 1283, lp, st, h)
+    a = torch.ones(6, device="cuda")
+    dz = torch.empty_like(z)
+    want, tol = _wanted_grad(z, t, scale, a, a)
+    with np.errstate(over="ignore"):
+        want, tol = np.clip(want, -1e38, 1e38), tol + U[dtype] * np.abs(want)
+    for call in (lambda: c.token_logprobs_loss(z, t, lp, dz, dlogprob=a, dentropy=a, scale=scale),
+                 lambda: c.token_logprobs_backward(z, t, st, dz, dlogprob=a, entropy=h, dentropy=a, scale=scale)):
+        call()
+        inside(dz, want, tol + scale * 2.0 ** -18, "gradient")
+
+
 def test_no_rows_and_no_tokens(c):
     z, t = _logits(0, 100, BF)
     e = torch.empty(0, device="cuda")

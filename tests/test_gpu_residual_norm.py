@@ -149,7 +149,7 @@ def _check_backward(i, c, s, rstd, post_rstd, params, grads, out, pad, alpha=0.7
 
 
 SIZES = [(1, 1), (3, 7), (2, 8), (5, 40), (33, 72), (700, 128), (1, 1280), (9, 1283), (340, 1280), (6, 2560), (3, 5121), (320, 4096), (160, 12288), (2, 12288), (3, 12296), (2, 20488),
-         (2, 33001)]
+         (2, 33001), (2, 49992), (3, 70001)]
 
 
 @pytest.mark.parametrize("rows,cols", SIZES)

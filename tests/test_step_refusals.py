@@ -30,7 +30,7 @@ def test_host_tensors_are_refused():
                  lambda: B.fsdp_token_logprobs_loss(h, x, t, v, x, dlogprob=v), lambda: B.fsdp_residual_norm_forward(h, x, x),
                  lambda: B.fsdp_residual_norm_backward(h, x, x, x, x, x, x), lambda: B.State8(10, True, device="cpu"),
                  lambda: B.AdamWTensors([v], [v], [v], [v]), lambda: B.fsdp_state8_pack(h, v, v), lambda: B.fsdp_adamw_tensors(h, [v], HP, 1),
-                 lambda: B.AdamWTensors([v], [], [v], [v])):
+                 lambda: B.AdamWTensors([v], [], [v], [v]), lambda: B.AdamWTensors([v], [None], [v], [v]), lambda: B.AdamWTensors([None], [v], [v], [v])):
         _refused(call)
     _refused(lambda: B.fsdp_residual_norm_forward(h, None, x))
     _refused(lambda: B.fsdp_token_logprobs_forward(h, None, t, v))
