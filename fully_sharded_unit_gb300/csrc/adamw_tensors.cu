@@ -339,6 +339,17 @@ __device__ __forceinline__ void step8(const Tensor& t, const AdamWConsts& c, boo
     }
 #pragma unroll
     for (int j = 0; j < 8; j += 2) adamw_pair(p + j, g + j, m + j, v + j, c);
+    if (n == 8) {
+        store8(t.p, FSDP_DTYPE_F32, i, p);
+        if (t.copy != nullptr) store8(t.copy, FSDP_DTYPE_BF16, i, p);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j >= n) continue;
+            t.p[i + j] = p[j];
+            if (t.copy != nullptr) store1(t.copy, FSDP_DTYPE_BF16, i + j, p[j]);
+        }
+    }
     if (EIGHT) {
         if (n < 8) {   // what is not the tensor's stays out of the groups' largest
 #pragma unroll
@@ -371,8 +382,6 @@ __device__ __forceinline__ void step8(const Tensor& t, const AdamWConsts& c, boo
         }
     }
     if (n == 8) {
-        store8(t.p, FSDP_DTYPE_F32, i, p);
-        if (t.copy != nullptr) store8(t.copy, FSDP_DTYPE_BF16, i, p);
         if (EIGHT) {
             *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + i) = cm;
             *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i) = cv;
@@ -384,8 +393,6 @@ __device__ __forceinline__ void step8(const Tensor& t, const AdamWConsts& c, boo
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             if (j >= n) continue;
-            t.p[i + j] = p[j];
-            if (t.copy != nullptr) store1(t.copy, FSDP_DTYPE_BF16, i + j, p[j]);
             if (EIGHT) {
                 static_cast<uint8_t*>(t.m)[i + j] = static_cast<uint8_t>((j < 4 ? cm.x : cm.y) >> (8 * (j & 3)));
                 static_cast<uint8_t*>(t.v)[i + j] = static_cast<uint8_t>((j < 4 ? cv.x : cv.y) >> (8 * (j & 3)));
@@ -435,10 +442,10 @@ __device__ __forceinline__ void step1(const Tensor& t, const AdamWConsts& c, boo
 }
 
 // EIGHT: moments in 8 bits.  A block takes tiles in turn.  236 M elements, 32 bits, with BF16 copies: 1.16 ms,
-// 6.1 TB/s.  708 M, 8 bits, BF16 gradients and copies: 2.6 ms, 4.4 TB/s, bound by issue: about
+// 6.1 TB/s.  708 M, 8 bits, BF16 gradients and copies: 2.5 ms, 4.5 TB/s, bound by issue: about
 // 100 instructions an element, a third of them the two divisions and the root, rounded as IEEE has
 // them so that fp32 moments give the unit's bits.  (Four blocks an SM: with three or five, and
-// 80 or 48 registers, 2.7 ms and more.)
+// 80 or 48 registers, 2.8 ms and more.)
 template <bool EIGHT, int MOST>
 __global__ void __launch_bounds__(256, 4) adamw_tensors_kernel(const __grid_constant__ Tensors<MOST> a) {
     starts_early();
