@@ -674,7 +674,9 @@ FSDP_API int fsdp_act8_unpack(fsdp_compute* c, const fsdp_matrix* ckpt, int acti
  * is made of, with the logits' gradient; the norms before and after a block
  * with its gate and residual scale; AdamW over tensors that no unit shards, or that
  * want their moments in 8 bits.  Handles, streams and roundings are those of the
- * block operators; results do not depend on the order in which blocks run. */
+ * block operators; results do not depend on the order in which blocks run.  (In a call of
+ * another size a row may be split, and its sums rounded, otherwise.)  Only
+ * fsdp_residual_norm_backward needs workspace. */
 
 /* Log probabilities of given tokens.  logits: rows x vocab, BF16 or F32 (vocab <=
  * 2^30).  With z a row, d_i = scale (z_i - max z) and S = sum exp(d_i), in natural
