@@ -459,13 +459,13 @@ struct Vectors {
     uint8_t* base;
     static constexpr int kChunk = FLOATS ? 32 : 16;
     __device__ uint8_t* slot(const Place<NV>& at, int v, int k) const { return base + (v * NV + k) * at.gt * kChunk + at.t * 16; }
-    // From 16-byte boundaries, of the slots' type: asynchronous.
+    // From 16-byte boundaries, of the slots' type: asynchronous.  Places past the row's end are read too, and
+    // multiplied by the row's zeros there: they hold ones, for what a kernel before left may be NaN.
     __device__ void copy(const Place<NV>& at, const void* p, int v) const {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (at.in(k) == 0) continue;
             uint8_t* to = slot(at, v, k);
-            if (p != nullptr) {
+            if (p != nullptr && at.in(k) != 0) {
                 const uint8_t* from = static_cast<const uint8_t*>(p) + at.column(k) / 8 * kChunk;
                 copy16(shared_at(to), from);
                 if (FLOATS) copy16(shared_at(to + at.gt * 16), from + 16);
