@@ -105,15 +105,22 @@ struct Soft {
 
 __device__ __forceinline__ bool plain(float m, float c) { return fabsf(m * c) < 0x1p20f && c > 0x1p-79f && c < 0x1p20f; }
 
-// d of the old maximum under the new one; at kNone what is behind it vanishes.
+// By how much a term's d under the maximum m is below (z - m) c: what mc is off by, or nothing.
+__device__ __forceinline__ float anchor_gap(float m, float c) { return plain(m, c) ? fmaf(-m, c, __fmul_rn(m, c)) : 0.0f; }
+
+// d of the old maximum under the new one; at kNone what is behind it vanishes.  The two may stand on either
+// side of plain()'s limits, where one maximum's terms carry a gap and the other's do not.
 __device__ __forceinline__ float grown(float from, float to, float c) {
-    return fmaxf(plain(from, c) && plain(to, c) ? __fmul_rn(from, c) - __fmul_rn(to, c) : (from - to) * c, kNone);
+    if (plain(from, c) && plain(to, c)) return fmaxf(__fmul_rn(from, c) - __fmul_rn(to, c), kNone);
+    return fmaxf((from - to) * c + (anchor_gap(from, c) - anchor_gap(to, c)), kNone);
 }
 
 __device__ __forceinline__ void rescale(Soft& s, float to, float c) {
-    const float d = grown(s.m, to, c), f = exp2_fast(d);
-    s.Q = f * fmaf(d, s.S, s.Q);
-    s.S *= f;
+    if (s.m != -kInf) {   // else the sums are 0, or NaN
+        const float d = grown(s.m, to, c), f = exp2_fast(d);
+        s.Q = f * fmaf(d, s.S, s.Q);
+        s.S *= f;
+    }
     s.m = to;
 }
 
@@ -130,9 +137,6 @@ __device__ __forceinline__ Soft join_lanes(Soft s, float c) {
     }
     return s;
 }
-
-// What mc is off by, in natural logarithms.
-__device__ __forceinline__ float anchor_error(float m, float mc, float c) { return plain(m, c) ? kLn2 * fmaf(-m, c, mc) : 0.0f; }
 
 // Adds N words' elements to s, whose m is at least as large as they are.  Q's terms must not have
 // d = -inf: a bf16 logit is held at -2^100 first, two at a time, which is as good as masked
@@ -582,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) token_logprobs_kernel(const
         if (a.top > 0) top_lists(mine, tops);
         s = join_all<kThreads / 32>(s, c, softs, joined, rank, cluster);
         const bool bad = !(s.S == s.S);
-        const float ln = logf(s.S), ln_s = ln + anchor_error(s.m, __fmul_rn(s.m, c), c);
+        const float ln = logf(s.S), ln_s = ln + kLn2 * anchor_gap(s.m, c);
         const float h = s.S == 0.0f ? 0.0f : fmaf(-kLn2, s.Q / s.S, ln);
         if (t == 0 && rank == 0) row_results<ENTROPY>(a, row, s, ln_s, h, token, z_token);
         if (a.top > 0) {
@@ -667,7 +671,7 @@ __global__ void __launch_bounds__(T, 1024 / T) token_loss_kernel(const __grid_co
         }
         s = join_all<T / 32>(s, c, softs[flip], joined[flip], rank, cluster);
         flip ^= 1;
-        const float ln = logf(s.S), ln_s = ln + anchor_error(s.m, __fmul_rn(s.m, c), c);
+        const float ln = logf(s.S), ln_s = ln + kLn2 * anchor_gap(s.m, c);
         const float h = s.S == 0.0f ? 0.0f : fmaf(-kLn2, s.Q / s.S, ln);
         if (t == 0 && rank == 0) row_results<ENTROPY>(a, row, s, ln_s, h, given.token, z_token);
         const RowGrad g = row_grad(a, given, s.m, ln, 1.0f / s.S, h);
@@ -722,7 +726,7 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_backward_kernel(const
     const int part = blockIdx.x % parts;
     for (int64_t row = blockIdx.x / parts; row < a.rows; row += gridDim.x / parts) {
         const float m = a.stats[2 * row], ln_s = a.stats[2 * row + 1];
-        const float c = a.scale * kLog2e, ln = ln_s - anchor_error(m, __fmul_rn(m, c), c);
+        const float c = a.scale * kLog2e, ln = ln_s - kLn2 * anchor_gap(m, c);
         const RowGrad g = row_grad(a, RowGiven(a, row), m, ln, expf(-ln), a.entropy != nullptr ? a.entropy[row] : 0.0f);
         if (threadIdx.x == 0 && part == 0 && g.token >= a.vocab) atomicOr(a.status, FSDP_KSTATUS_BAD_TOKEN);
         const int chunks = grad_chunks(a, row);
