@@ -435,7 +435,7 @@ __device__ __forceinline__ RowGrad row_grad(const TokenLogprobs& x, const RowGiv
     g.a = g.token >= 0 ? given.a * x.scale : 0.0f;
     // a masked row's S is 0; a token that does not exist leaves nothing to say
     g.zero = (g.a == 0.0f && b == 0.0f) || ln == -kInf;
-    if (g.token >= x.vocab) {
+    if (given.token >= x.vocab) {   // with the entropy's gradient alone too
         g.a = __uint_as_float(0x7fc00000u);
         g.zero = false;
     }

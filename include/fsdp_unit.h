@@ -702,8 +702,9 @@ FSDP_API int fsdp_token_logprobs_forward(fsdp_compute* c, const fsdp_matrix* log
  * (floats, one a row; either may be NULL for zeros, not both):
  *     dlogits_i = scale (a ([i = t] - p_i) - b p_i (ln p_i + entropy)),  p_i = exp(d_i) / S
  * stats and, with dentropy, entropy as the forward wrote them.  tokens may be NULL
- * where dlogprob is.  dlogits: BF16 or F32, may be logits itself.  A row whose a and b
- * are 0 (a without a token counts as 0) gets zeros, whatever its logits. */
+ * where dlogprob is, and are not looked at there.  dlogits: BF16 or F32, may be logits itself.  A row whose a and b
+ * are 0 (a without a token counts as 0) gets zeros, whatever its logits, unless its token is
+ * one >= vocab. */
 FSDP_API int fsdp_token_logprobs_backward(fsdp_compute* c, const fsdp_matrix* logits, const int64_t* tokens, double scale,
                                           const float* stats, const float* entropy, const float* dlogprob,
                                           const float* dentropy, const fsdp_matrix* dlogits, void* stream);
