@@ -36,8 +36,15 @@ template <bool SIGNED>
 __device__ __forceinline__ uint32_t state8_code(float x, uint32_t byte, uint32_t random) {
     if (byte == 255u) return 0;
     const float away = __uint_as_float((254u - byte) << 23);   // 2^(127-B)
-    const uint32_t b = __float_as_uint(SIGNED ? fabsf(x) * away * kDown<SIGNED> : fmaxf(x, 0.0f) * away * kDown<SIGNED>);
-    const uint32_t r = random == kNearest ? 0x7ffffu + ((b >> 20) & 1u) : random;
+    const float y = (SIGNED ? fabsf(x) : fmaxf(x, 0.0f)) * away;
+    uint32_t b, r = random;
+    if (random == kNearest) {   // cut off, and what that lost moves a half up: one rounding in all
+        const float cut = __fmul_rz(y, kDown<SIGNED>);
+        b = __float_as_uint(cut);
+        r = 0x7ffffu + (((b >> 20) & 1u) | (cut * kUp<SIGNED> != y ? 1u : 0u));
+    } else {
+        b = __float_as_uint(y * kDown<SIGNED>);
+    }
     uint32_t code = min((b + r) >> 20, SIGNED ? 0x7fu : 0xffu);
     if (SIGNED) return code != 0 ? code | ((__float_as_uint(x) >> 24) & 0x80u) : 0u;
     return x > 0.0f ? max(code, 1u) : 0u;

@@ -1,4 +1,4 @@
-"""8-bit moments at values that a code stands for, and random bits of every kind."""
+"""8-bit moments at values that a code stands for, and next to those halfway between codes."""
 import numpy as np
 import pytest
 import torch
@@ -83,3 +83,21 @@ def test_codes_pack_to_themselves(c, signed):
     c.state8_pack(x, t)
     A.same(t.exps, exps, "exponents")
     A.same(t.codes, groups.reshape(-1), "codes")
+
+
+@pytest.mark.parametrize("signed", [True, False])
+def test_pack_next_to_halves(c, signed):
+    """The smallest codes are whole numbers of one step: the values a last place above, at and below each half between two of
+    them go up, to the even one and down."""
+    least, first = (-17, 1) if signed else (-33, 2)         # an unsigned element that is not 0 is at least the first code
+    k = np.arange(first if not signed else 0, 8) + 0.5
+    half = np.ldexp(k, least).astype(f)
+    x = np.concatenate([np.nextafter(half, f(0)), half, np.nextafter(half, f(4))])
+    want = np.concatenate([np.floor(k), np.rint(k), np.ceil(k)]).astype(np.uint8)
+    for top in (1.0, 2.0 ** -40, 2.0 ** 14, 2.0 ** 60):
+        group = np.zeros(32, f)
+        group[:len(x)] = x * f(top)
+        group[31] = top
+        s = B.State8(32, signed)
+        c.state8_pack(torch.from_numpy(group).cuda(), s)
+        A.same(s.codes[:len(x)], want, f"codes under {top}")
