@@ -905,6 +905,7 @@ def _vecs(named, n, device):
 
 def fsdp_residual_norm_forward(h, residual, out, block=None, post_gamma=None, gate=None, residual_scale=1.0, y=None, gamma=None,
                                eps=1e-6, rstd=None, post_rstd=None, stream=None) -> None:
+    """``out`` may be ``residual`` itself."""
     d = _device_of(h)
     hm = _shaped(residual, "residual", d)
     rows, cols = residual.shape

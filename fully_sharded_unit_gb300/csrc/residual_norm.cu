@@ -83,9 +83,9 @@ __global__ void __launch_bounds__(512) residual_norm_any_kernel(const ResidualNo
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (j < in) ss[0] = fmaf(s[j], s[j], ss[0]);
-            store_chunk_any(a.out.p, a.out.dtype, row * a.out.ld + c, in, s);
+            if (a.y.p == nullptr) store_chunk_any(a.out.p, a.out.dtype, row * a.out.ld + c, in, s);
         }
-        if (a.y.p != nullptr) {
+        if (a.y.p != nullptr) {   // out behind the sum: it may lie where the residual stream does, which is read again
             block_sums(ss, red[1]);
             const float rstd = 1.0f / sqrtf(ss[0] / n + a.eps);
             if (threadIdx.x == 0) a.rstd[row] = rstd;
@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(512) residual_norm_any_kernel(const ResidualNo
                 float s[8], g[8];
                 residual_chunk(a, row, c, in, post_rstd, s);
                 load_any(a.gamma, a.param_dtype, c, in, 1.0f, g);
+                store_chunk_any(a.out.p, a.out.dtype, row * a.out.ld + c, in, s);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) s[j] = s[j] * rstd * g[j];
                 store_chunk_any(a.y.p, a.y.dtype, row * a.y.ld + c, in, s);

@@ -727,7 +727,8 @@ FSDP_API int fsdp_token_logprobs_loss(fsdp_compute* c, const fsdp_matrix* logits
  * post_gamma and gate): out = residual_scale * h.  gamma NULL (with y and rstd): no norm
  * before the next block.  post_gamma, gate, gamma: cols elements of param_dtype (BF16
  * or F32).  residual, block, out, y: rows x cols, BF16 or F32 each.  rstd,
- * post_rstd: `rows` floats each, for the backward pass.  eps: finite, >= 0. */
+ * post_rstd: `rows` floats each, for the backward pass.  eps: finite, >= 0.  out may be
+ * residual itself. */
 FSDP_API int fsdp_residual_norm_forward(fsdp_compute* c, const fsdp_matrix* residual, const fsdp_matrix* block,
                                         const void* post_gamma, const void* gate, const void* gamma, int param_dtype,
                                         double residual_scale, double eps, const fsdp_matrix* out, const fsdp_matrix* y,
