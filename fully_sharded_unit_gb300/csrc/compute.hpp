@@ -13,6 +13,10 @@
 
 namespace fsdp {
 
+// Block counts are planned for this many SMs at most, so that the workspace
+// can be told without a device.
+constexpr int kSms = 152;
+
 // A matrix as the kernels see it: element (r, c) at p + (r*ld + c) elements.
 // ACT8: p is the int8 payload, e the exponent bytes, eld their row stride.
 struct Mat {

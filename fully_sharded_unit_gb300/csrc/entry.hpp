@@ -150,8 +150,4 @@ inline int check_workspace(const fsdp_compute* c, int64_t need) {
     return FSDP_OK;
 }
 
-// Block counts are planned for this many SMs at most, so that the workspace
-// can be told without a device.
-constexpr int kSms = 152;
-
 }  // namespace fsdp

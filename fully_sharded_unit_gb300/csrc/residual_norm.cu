@@ -992,8 +992,6 @@ __global__ void __launch_bounds__(256) residual_norm_sums_kernel(const ResidualN
     }
 }
 
-constexpr int kSms = 152;
-
 int round32(int64_t n) { return static_cast<int>((n + 31) / 32 * 32); }
 
 // How a chunk to a thread is laid out: 0 threads where eight blocks do not hold a row.
