@@ -37,8 +37,10 @@ inline int check_hp(const fsdp_adamw_hp* hp) {
     return FSDP_OK;
 }
 
+inline double adamw_bc1(const fsdp_adamw_hp& hp, int64_t t) { return 1.0 - std::pow(hp.beta1, static_cast<double>(t)); }
+
 inline AdamWConsts adamw_consts(const fsdp_adamw_hp* hp, int64_t t) {
-    const double bc1 = 1.0 - std::pow(hp->beta1, static_cast<double>(t));
+    const double bc1 = adamw_bc1(*hp, t);
     const double bc2 = 1.0 - std::pow(hp->beta2, static_cast<double>(t));
     AdamWConsts c;
     c.decay = static_cast<float>(1.0 - hp->lr * hp->weight_decay);
@@ -50,6 +52,16 @@ inline AdamWConsts adamw_consts(const fsdp_adamw_hp* hp, int64_t t) {
     c.step = static_cast<float>(hp->lr / bc1);
     c.eps = static_cast<float>(hp->eps);
     return c;
+}
+
+struct AdamWScaled {
+    float decay, step;
+};
+// decay and step of a tensor with scales of its own, as adamw_consts forms them.
+// bc1: 1 - beta1^t, the same for all of a call's tensors.
+inline AdamWScaled adamw_scaled(const fsdp_adamw_hp& hp, double bc1, double lr_scale, double decay_scale) {
+    const double lr = hp.lr * lr_scale;
+    return {static_cast<float>(1.0 - lr * (hp.weight_decay * decay_scale)), static_cast<float>(lr / bc1)};
 }
 
 #ifdef __CUDACC__

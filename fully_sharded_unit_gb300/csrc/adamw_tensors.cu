@@ -485,7 +485,7 @@ cudaError_t launch_tensors(const fsdp_adamw_tensor* tensors, int64_t count, cons
                            const float* grad_scale, const int32_t* skip, int sms, cudaStream_t st) {
     Tensors<MOST> a;
     a.c = adamw_consts(&hp, step);
-    const double bc1 = 1.0 - std::pow(hp.beta1, static_cast<double>(step));
+    const double bc1 = adamw_bc1(hp, step);
     a.grad_scale = grad_scale;
     a.skip = skip;
     for (const int moments : {FSDP_MOMENTS_F32, FSDP_MOMENTS_8BIT}) {   // a kernel for each kind
@@ -501,11 +501,10 @@ cudaError_t launch_tensors(const fsdp_adamw_tensor* tensors, int64_t count, cons
                 if (s.numel == 0 || s.moments != moments) continue;
                 const int64_t tiles = (s.numel + a.tile - 1) / a.tile;
                 if (a.tiles + tiles > 0x7fffffff) break;   // 2^40 elements are at most 2^29 tiles of the largest size
-                const double lr = hp.lr * s.lr_scale;      // decay and step as adamw_consts forms them
-                const float decay = static_cast<float>(1.0 - lr * (hp.weight_decay * s.decay_scale)), size = static_cast<float>(lr / bc1);
+                const AdamWScaled own = adamw_scaled(hp, bc1, s.lr_scale, s.decay_scale);
                 const uint64_t key = seed * 0x9E3779B97F4A7C15ull + (static_cast<uint64_t>(j) + 1) * 0xD1B54A32D192ED03ull;
                 a.t[a.count++] = Tensor{s.param, s.grad, s.exp_avg, s.exp_avg_sq, s.exp_avg_exps, s.exp_avg_sq_exps, s.copy_bf16, s.numel,
-                                        decay, size, static_cast<uint32_t>(key >> 32), a.tiles, s.grad_dtype, vector_accesses(s)};
+                                        own.decay, own.step, static_cast<uint32_t>(key >> 32), a.tiles, s.grad_dtype, vector_accesses(s)};
                 a.tiles += static_cast<uint32_t>(tiles);
             }
             if (a.count == 0) continue;

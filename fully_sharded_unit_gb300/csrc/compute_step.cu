@@ -96,14 +96,15 @@ int check_state8(int kind, int64_t numel, const uint8_t* codes, const uint8_t* e
     return FSDP_OK;
 }
 
-int check_tensor(const fsdp_adamw_tensor& t, const fsdp_adamw_hp& hp, int64_t number) {
+int check_tensor(const fsdp_adamw_tensor& t, const fsdp_adamw_hp& hp, double bc1, int64_t number) {
     const auto refuse = [&](int code, const char* why) { return fail(code, "tensor " + std::to_string(number) + ": " + why); };
     if (t.numel < 0 || t.numel > kMostElements) return refuse(FSDP_E_INVALID_ARG, "numel must be in [0, 2^40]");
     if (t.grad_dtype != FSDP_DTYPE_F32 && t.grad_dtype != FSDP_DTYPE_BF16) return refuse(FSDP_E_INVALID_ARG, "grad_dtype must be FSDP_DTYPE_F32 or FSDP_DTYPE_BF16");
     if (t.moments != FSDP_MOMENTS_F32 && t.moments != FSDP_MOMENTS_8BIT) return refuse(FSDP_E_INVALID_ARG, "unknown moments");
     if (!(t.lr_scale >= 0) || !(t.decay_scale >= 0) || !std::isfinite(t.lr_scale) || !std::isfinite(t.decay_scale))
         return refuse(FSDP_E_INVALID_ARG, "lr_scale and decay_scale must be finite and >= 0");
-    if (!std::isfinite(static_cast<float>(hp.lr * t.lr_scale)) || !std::isfinite(hp.lr * t.lr_scale * hp.weight_decay * t.decay_scale))
+    const AdamWScaled own = adamw_scaled(hp, bc1, t.lr_scale, t.decay_scale);
+    if (!std::isfinite(own.decay) || !std::isfinite(own.step))
         return refuse(FSDP_E_INVALID_ARG, "the scaled learning rate or weight decay is not finite");
     if (t.numel == 0) return FSDP_OK;
     const bool eight = t.moments == FSDP_MOMENTS_8BIT;
@@ -331,7 +332,8 @@ int fsdp_adamw_tensors(fsdp_compute* c, const fsdp_adamw_tensor* tensors, int64_
         if (count > 0 && tensors == nullptr) return fail(FSDP_E_INVALID_ARG, "tensors is null");
         TRY(check_hp(hp));
         if (step < 1) return fail(FSDP_E_INVALID_ARG, "step must be >= 1");
-        for (int64_t j = 0; j < count; ++j) TRY(check_tensor(tensors[j], *hp, j));
+        const double bc1 = adamw_bc1(*hp, step);
+        for (int64_t j = 0; j < count; ++j) TRY(check_tensor(tensors[j], *hp, bc1, j));
         if (grad_scale_dev != nullptr) TRY(take_floats(grad_scale_dev, "grad_scale_dev"));
         if (skip_dev != nullptr) TRY(take_array(skip_dev, "skip_dev", 3));
         OnDevice dev(c->device);
