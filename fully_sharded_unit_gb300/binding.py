@@ -844,7 +844,7 @@ def fsdp_token_logprobs_forward(h, logits, tokens, logprob, entropy=None, stats=
     rows = logits.shape[0]
     top = 0
     if top_tokens is not None or top_logprobs is not None:
-        if top_tokens is None or top_logprobs is None or top_tokens.dim() != 2:
+        if not isinstance(top_tokens, torch.Tensor) or top_logprobs is None or top_tokens.dim() != 2:
             _refuse("top_tokens and top_logprobs are two matrices of rows x k")
         top = top_tokens.shape[1]
         if top < 1:
@@ -1025,7 +1025,7 @@ def fsdp_adamw_tensors(h, tensors, hp, step, seed=0, grad_scale=None, skip=None,
     if tensors.__class__ is not AdamWTensors or (d is not None and tensors.count and tensors.device != d):
         _refuse("an AdamWTensors on the handle's device is expected")
     for t, dtype in ((grad_scale, torch.float32), (skip, torch.int32)):
-        if t is not None and (t.numel() != 1 or t.dtype != dtype or t.get_device() < 0 or (d is not None and t.get_device() != d)):
+        if t is not None and (not isinstance(t, torch.Tensor) or t.numel() != 1 or t.dtype != dtype or t.get_device() < 0 or (d is not None and t.get_device() != d)):
             _refuse(f"one {dtype} element on the handle's device is expected, not {_about(t)}")
     _check(lib().fsdp_adamw_tensors(h, tensors.array, tensors.count, ctypes.byref(_hp(hp)), int(step), int(seed) & (2 ** 64 - 1),
                                     None if grad_scale is None else grad_scale.data_ptr(), None if skip is None else skip.data_ptr(),
