@@ -813,8 +813,10 @@ typedef struct {
  *        key = high32(seed * 0x9E3779B97F4A7C15 + (j + 1) * 0xD1B54A32D192ED03 mod 2^64)
  *        x ^= x >> 16; x *= 0xD36F86A9; x ^= x >> 15; x *= 0xC242E759; x ^= x >> 16
  *    r = the low half of x for exp_avg, the high half for exp_avg_sq; the magnitude is rounded
- *    to 20 bits below the code's last (to nearest) and goes up if those plus 16 r reach 2^20.  So
- *    a value that a code stands for is kept as it is.
+ *    to 20 bits below the code's last (to nearest) and goes up if those plus 16 r pass 2^20.  Where
+ *    they reach it exactly, and where r = 0 and a code stands for the value (together one element in 2^20),
+ *    the sum in 64 bits decides, |x| pow(2, 127-B) in codes' steps and r / 2^16 cut off: that code, or the
+ *    one below where CUDA's pow is low in its last place.  A host that repeats the rule may find either.
  * The constants are formed from hp and `step` at the call: a captured call replays them.  No
  * two tensors share what is written. */
 FSDP_API int fsdp_adamw_tensors(fsdp_compute* c, const fsdp_adamw_tensor* tensors, int64_t count, const fsdp_adamw_hp* hp,

@@ -20,35 +20,8 @@ def c():
 
 
 @pytest.mark.parametrize("off", [0, 1])
-def test_moments_that_a_code_stands_for_stay(c, off):
-    """With betas of 0 the moments are g and g^2.  For g = 1 or 1.5 times a power of two both are codes' values, and are kept as they
-    are whatever the random bits: of 2^22 elements' 2^16 values about 64 are 0.  Exponent bytes from 7 to 194; a group's
-    elements are up to 2^4 apart."""
-    n = 2 ** 22
-    rng = np.random.default_rng(1)
-    e = np.repeat(rng.integers(-60, 30, n // 32), 32) + rng.integers(0, 4, n)
-    g = (np.ldexp(np.where(rng.random(n) < 0.5, 1.0, 1.5), e) * rng.choice([-1, 1], n)).astype(f)
-    for m in (np.abs(g), g * g):
-        assert np.array_equal(A.decode(*A.encode(m, False), False).astype(f), m)
-    p, gt = (torch.zeros(n + off, device="cuda")[off:] for _ in range(2))
-    gt.copy_(torch.from_numpy(g))
-    codes = [torch.zeros(n + off, dtype=torch.uint8, device="cuda")[off:] for _ in range(2)]
-    exps = [torch.zeros(n // 32, dtype=torch.uint8, device="cuda") for _ in range(2)]
-    m, v = B.State8(n, True, codes[0], exps[0]), B.State8(n, False, codes[1], exps[1])
-    hp = dict(A.HP, lr=0.0, beta1=0.0, beta2=0.0)
-    for seed in (1, 2):
-        assert (A.random_bits(n, 0, seed)[0] == 0).any() and (A.random_bits(n, 0, seed)[1] == 0).any()
-        c.adamw_tensors(B.AdamWTensors([p], [gt], [m], [v]), hp, 1, seed=seed)
-        for state, want, name in ((m, g, "exp_avg"), (v, g * g, "exp_avg_sq")):
-            out = torch.empty(n, device="cuda")
-            c.state8_unpack(state, out)
-            A.same(out, want, name)
-            A.same(state.exps, A.encode(want, state.signed)[1], name + " exponents")
-
-
-@pytest.mark.parametrize("off", [0, 1])
 def test_every_code_is_the_rules(c, off):
-    """Any values: one code for each, where value and random bits add up to a code exactly as elsewhere."""
+    """Any values: one code for each, or one of two where value and random bits add up to a code exactly."""
     n = 2 ** 21 + 13
     rng = np.random.default_rng(2)
     with np.errstate(over="ignore"):   # few bits, so that many sums are a code exactly, and a few infinities
@@ -59,9 +32,8 @@ def test_every_code_is_the_rules(c, off):
     c.adamw_tensors(B.AdamWTensors([p], [gt], [m], [v]), dict(A.HP, lr=0.0, beta1=0.0, beta2=0.0), 1, seed=5)
     rm, rv = A.random_bits(n, 0, 5)
     for state, x, r in ((m, g, rm), (v, g * g, rv)):
-        codes, exps = A.encode(x, state.signed, r)
-        A.same(state.exps, exps, "exponents")
-        A.same(state.codes, codes, "codes")
+        A.same(state.exps, A.encode(x, state.signed, r)[1], "exponents")
+        A.same_codes(state.codes, x, state.signed, r, "codes")
 
 
 @pytest.mark.parametrize("signed", [True, False])
