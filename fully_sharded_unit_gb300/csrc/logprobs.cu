@@ -509,10 +509,11 @@ __device__ __forceinline__ float token_logit(const TokenLogprobs& a, int64_t row
 // Rows to blocks, or to clusters of blocks.  A thread copies the words that it will look at itself,
 // in groups and row after row, into its own places in shared memory (cp.async), so
 // that while the block joins a row's sums and looks for its alternatives the next row's
-// words are under way.  8192 x 50257 bf16 with entropy and five alternatives: 174 us, 4.7 TB/s;
-// bound by instructions, 9 a logit and a quarter more for the row's sums and alternatives
-// (a row to 256 threads, whose joint work weighs more, 286 us before that was cut down;
-// words ahead in registers, 229).
+// words are under way.  8192 x 50257 bf16: 134 us, 6.1 TB/s; with entropy 137; with entropy and five
+// alternatives 176, 4.7 TB/s.  2048 x 50257 fp32: 76 us, 5.4 TB/s, and 92.  What the alternatives
+// add is steps that a block takes together, with five blocks to an SM: neither DRAM (55 % by the counters) nor the issue
+// slots (10 instructions a logit, 2.4 of 4 a cycle) are at their limit.  (A row to 256 threads, whose
+// joint work weighs more, 286 us before that was cut down; words ahead in registers, 229.)
 template <bool BF16, bool ENTROPY, bool GRAD>
 __global__ void __launch_bounds__(kThreads, kBlocks) token_logprobs_kernel(const __grid_constant__ TokenLogprobs a, int cluster) {
     constexpr int threads = kThreads;
@@ -621,8 +622,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) token_logprobs_kernel(const
 // Forward and backward with the row's words held in shared memory in between: kMostSlots words
 // to a thread, copied by itself.  Where a word has given its gradient, the next row's
 // takes its place, so a block's loads run on under its second pass.  dz lies on its words as z does.
-// 8192 x 50257 bf16: 297 us, 5.5 TB/s of reads and writes (the second pass from L2: 458), with the SMs
-// issuing in 70 % of their cycles.
+// 8192 x 50257 bf16: 299 us, 5.5 TB/s of reads and writes (the second pass from L2: 458), with entropy 330; the SMs
+// issue 2.7 of 4 a cycle.  2048 x 50257 fp32 (1024 threads, one block on an SM) 164 us, 2048 x 128256 bf16 (two such
+// blocks to a row) 246.  Where dz does not lie on its words as z does, token_logprobs_kernel gives the gradient too, from
+// L2: 2048 x 50257 bf16 to fp32 215 us, fp32 to bf16 244, bf16 off by an element 186.
 constexpr int kMostSlots = 13;      // of 512 threads: 104 KB, two blocks on an SM
 
 template <bool BF16, bool ENTROPY, int T>
@@ -718,7 +721,7 @@ __global__ void __launch_bounds__(T, 1024 / T) token_loss_kernel(const __grid_co
 }
 
 // `parts` blocks to a row, which have a run of its chunks each.  One read, one write and an
-// exponential a logit: 2048 x 50257 fp32 125 us, 6.6 TB/s.
+// exponential a logit: 2048 x 50257 fp32 126 us, 6.5 TB/s; 8192 x 50257 bf16 250, 6.6 TB/s.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) token_logprobs_backward_kernel(const TokenLogprobs a, int parts) {
     starts_early();

@@ -182,7 +182,9 @@ __global__ void __launch_bounds__(512) residual_norm_any_backward_kernel(const R
 //
 // Rows of any type and alignment in registers: a row to a block, or to a cluster of blocks
 // that join their sums through one another's shared memory.  Bound by a row's latency, one
-// row of up to 6144 columns at a time to an SM in the backward pass: 1031 x 5121 52 us (1.2 TB/s).
+// row of up to 6144 columns at a time to an SM in the backward pass, with nothing of the next row under way: 1031 x 5121
+// 52 us (1.2 TB/s).  What the ring does not take comes here.  At 4096 x 1280 and 4096 x 12288: F32 forward 25 and 324 us,
+// backward 46 and 351; BF16 without a block (a model's first norm) 16 and 206, 38 and 281; without dout (its last) 42 and 315.
 
 constexpr int kMostThreads = 768;   // of a block, which leaves a thread the 80 registers that the backward pass takes
 
@@ -347,9 +349,9 @@ __global__ void __launch_bounds__(kMostThreads) residual_norm_backward_kernel(co
 // columns t + k GT, k < NV, and copies the ones of the rows ahead into a ring of shared
 // memory (cp.async), so that it waits for its own copies alone.  ANY: rows start anywhere;
 // a chunk is then the two 16-byte words that hold it, moved together when it is read.
-// Forward, 4096 x 12288: 66 us, 6.1 TB/s.  Backward, 4096 x 1280: 22 us with 4 us for the sums
-// over the blocks, bound by a row's latency at three rows to an SM; 1031 x 5121 (ANY): 35 us,
-// seven rows to an SM behind one another.
+// Forward, 4096 x 12288: 66 us, 6.1 TB/s; 4096 x 1280 15 us; 4096 x 5121 (ANY) 91.  Backward, 4096 x 1280: 22 us with 4 us
+// for the sums over the blocks, bound by a row's latency at three rows to an SM; 1031 x 5121 (ANY): 35 us,
+// seven rows to an SM behind one another; 4096 x 5121 107.
 
 constexpr int kMostPlaces = 4;      // rows of a group in the ring
 // Threads of a block by the chunks of one.  The backward pass holds a row's words and its columns' sums:
@@ -798,7 +800,8 @@ __global__ void __launch_bounds__(backward_threads(NV)) residual_norm_backward_r
 // row read.  (With the vectors in shared memory there is room for one row of 12288; and a thread's three
 // chunks, with their columns' sums, leave no registers to hold a row in between, 187 us at 4096 x 12288;
 // two blocks to a row, 222: their barrier waits for the slower one's copies.)  4096 x 12288: 116 us, 5.2
-// TB/s; the two passes over shared memory and a row's one barrier take as long as its copies.
+// TB/s; the two passes over shared memory and a row's one barrier take as long as its copies.  With a gate, whose
+// vector takes registers that are not left, three chunks to a thread spill 200 bytes: 174 us; 4096 x 5120 68.
 template <int NV, bool GATE>
 __global__ void __launch_bounds__(keep_threads) residual_norm_backward_keep_kernel(const __grid_constant__ ResidualNormGrad a, const RingShape shape) {
     extern __shared__ __align__(16) uint8_t ring_bytes[];

@@ -588,8 +588,9 @@ FSDP_API int fsdp_linear_workspace_bytes(int64_t tokens, int64_t in_features, in
 /* Like fsdp_kernel_status, for the handle's kernels (the linear layer's
  * products wait, with a bound, on their own copies and matrix instructions):
  * synchronises `stream`, stores the FSDP_KSTATUS_* bits raised since the last
- * call in *flags and clears them.  After a raised bit the outputs of the calls
- * enqueued since the last read are incomplete; after
+ * call in *flags and clears them.  After FSDP_KSTATUS_WAIT_TIMEOUT or _DRAIN_TIMEOUT the
+ * outputs of the calls enqueued since the last read are incomplete (FSDP_KSTATUS_BAD_TOKEN
+ * concerns its rows alone); after
  * FSDP_KSTATUS_DRAIN_TIMEOUT every later call but this one and destroy returns
  * FSDP_E_STATE. */
 FSDP_API int fsdp_compute_status(fsdp_compute* c, int32_t* flags, void* stream);
@@ -687,7 +688,7 @@ FSDP_API int fsdp_act8_unpack(fsdp_compute* c, const fsdp_matrix* ckpt, int acti
  *     top_tokens, top_logprobs [row*top + j]: the j-th largest logit's index and
  *     log probability, the lowest index first among equal logits
  * tokens, logprob: both or neither; the other outputs may be NULL (both top_*
- * with top = 0).  top: 0 .. 32, at most vocab.  scale (1 / temperature): finite, > 0.
+ * with top = 0).  top: 0 .. 32, at most vocab.  scale (1 / temperature): 1e-30 .. 1e30.
  *  - tokens[row] < 0 gives none: logprob 0, and no gradient through it.
  *  - tokens[row] >= vocab: logprob (and in the gradient's calls the whole row of
  *    dlogits) is NaN and FSDP_KSTATUS_BAD_TOKEN is raised; nothing is read there.
@@ -702,16 +703,16 @@ FSDP_API int fsdp_token_logprobs_forward(fsdp_compute* c, const fsdp_matrix* log
  * (floats, one a row; either may be NULL for zeros, not both):
  *     dlogits_i = scale (a ([i = t] - p_i) - b p_i (ln p_i + entropy)),  p_i = exp(d_i) / S
  * stats and, with dentropy, entropy as the forward wrote them.  tokens may be NULL
- * where dlogprob is, and are not looked at there.  dlogits: BF16 or F32, may be logits itself.  A row whose a and b
- * are 0 (a without a token counts as 0) gets zeros, whatever its logits, unless its token is
- * one >= vocab. */
+ * where dlogprob is, and are not looked at there.  dlogits: BF16 or F32, may be logits
+ * itself.  A row whose a and b are 0 (a without a token counts as 0) gets zeros, whatever
+ * its logits, unless its token is one >= vocab. */
 FSDP_API int fsdp_token_logprobs_backward(fsdp_compute* c, const fsdp_matrix* logits, const int64_t* tokens, double scale,
                                           const float* stats, const float* entropy, const float* dlogprob,
                                           const float* dentropy, const fsdp_matrix* dlogits, void* stream);
 
 /* Both in one call, where a and b are known before the log probabilities (a loss that is
  * a weighted sum of them): the logits are read from memory once.  logprob is
- * required; entropy and stats may be NULL. */
+ * required; entropy and stats may be NULL.  dlogits may be logits itself. */
 FSDP_API int fsdp_token_logprobs_loss(fsdp_compute* c, const fsdp_matrix* logits, const int64_t* tokens, double scale,
                                       const float* dlogprob, const float* dentropy, float* logprob, float* entropy,
                                       float* stats, const fsdp_matrix* dlogits, void* stream);
@@ -764,7 +765,8 @@ FSDP_API int fsdp_residual_norm_workspace_bytes(int64_t rows, int64_t cols, int6
  * byte B stands for f * 2^(B-127), 1 <= B <= 253, where f < 2 is a small float:
  *   SIGNED (exp_avg):      sign, 4 bits of exponent e, 3 of mantissa k: (8 + k) * 2^(e-18), k * 2^-17 for e = 0
  *   UNSIGNED (exp_avg_sq):       5 bits of exponent e, 3 of mantissa k: (8 + k) * 2^(e-34), k * 2^-33 for e = 0
- * B is the smallest for which every magnitude is at most 1.875 * 2^(B-127).  A group with
+ * B is the smallest for which every magnitude is at most 1.875 * 2^(B-127), and 253 where none
+ * is: larger magnitudes are cut to 1.875 * 2^126.  A group with
  * an infinity or a NaN gets byte 255 and stands for NaN.  Bytes of zeros stand for
  * zeros.  An UNSIGNED element that is not 0 is not rounded to 0 (the update divides by
  * its root); a negative one counts as 0. */
