@@ -27,7 +27,7 @@ VECTORS = [(BF, True, True), (BF, True, False), (F32, True, True), (BF, False, T
 
 # forward: one, two and three chunks to a thread, 1 to 15 groups to a block, clusters of two to eight.  Backward: groups up to
 # 4096 columns, rows held from 4104 to 12288 (two and three chunks; BF16 vectors), clusters beyond and where vectors are floats
-@pytest.mark.parametrize("rows,cols", [(1, 8), (5, 40), (5000, 128), (1300, 1280), (700, 2048), (320, 4096), (160, 4104), (160, 5120), (320, 6144), (320, 7168), (160, 8192),
+@pytest.mark.parametrize("rows,cols", [(1, 8), (5, 40), (1, 5120), (3, 9000), (2, 12288), (2, 12304), (5000, 128), (1300, 1280), (700, 2048), (320, 4096), (160, 4104), (160, 5120), (320, 6144), (320, 7168), (160, 8192),
                                        (160, 8200), (320, 12288), (160, 12304), (160, 20480), (80, 33008), (40, 49152)])
 @pytest.mark.parametrize("params,post,gate", VECTORS)
 def test_rows_on_boundaries(monkeypatch, rows, cols, params, post, gate):
