@@ -694,7 +694,10 @@ FSDP_API int fsdp_act8_unpack(fsdp_compute* c, const fsdp_matrix* ckpt, int acti
  *    dlogits) is NaN and FSDP_KSTATUS_BAD_TOKEN is raised; nothing is read there.
  *  - A logit of -inf is masked: probability 0, gradient 0.  A row of nothing else
  *    has log probabilities of -inf, entropy 0 and gradient 0.
- *  - A row that holds +inf or NaN has NaN results, and top_tokens of -1. */
+ *  - A row that holds +inf or NaN has NaN results, and top_tokens of -1.
+ * The sums are fp32: what comes of them is off by a few units of 2^-23 of 1 + ln S and of itself
+ * (measured at up to 131072 logits: 1.5e-6), near 0 too, where a log probability has no more
+ * than that of its own. */
 FSDP_API int fsdp_token_logprobs_forward(fsdp_compute* c, const fsdp_matrix* logits, const int64_t* tokens, double scale,
                                          float* logprob, float* entropy, float* stats, int top, int64_t* top_tokens,
                                          float* top_logprobs, void* stream);
